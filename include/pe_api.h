@@ -1,7 +1,9 @@
 /*
  * pe_api.h -- C ABI of libpe.so: the per-step data path of P-EAGLE parallel
  * drafting on one GB300 (sm_103a): greedy verification, the fused
- * draft-batch rebuild and the drafter input assembly.
+ * draft-batch rebuild and the drafter input assembly; and, for the drafter's
+ * layers that follow, the rotated append to a 4-bit paged KV cache and the
+ * attention over that cache and over whole prompts.
  *
  * Sources (page title -- section):
  *  [P1] "P-EAGLE: Faster LLM Inference with Parallel Speculative Decoding in
@@ -100,6 +102,9 @@ typedef enum pe_dtype { PE_F32 = 0, PE_BF16 = 1 } pe_dtype;
                                  its next use.  Detection is by range: a
                                  corruption that keeps every value inside
                                  its legal range goes unseen.              */
+
+#define PE_ERR_POS_RANGE 1024u /* position outside the rotation table: row
+                                 taken as not rotated                       */
 
 /* Limits checked on the host. */
 #define PE_MAX_KP 255 /* previous draft depth K'  */
@@ -393,6 +398,127 @@ int pe_set_tuning(const pe_tuning* in /* host */);
  * one round trip to global memory. */
 int pe_latency_floor(int32_t ctas, int32_t hops, const int32_t* chain, int32_t n,
                      int32_t* out, void* stream);
+
+/* ------------------------------------------------------------------------
+ * The drafter layer's attention.  Rows are the draft batch that pe_step
+ * builds: T rows packed request after request, each with a position, a paged
+ * slot (-1 for a rejected row) and a rejected flag.  Activations are PE_BF16.
+ * The pages have no counterpart: they leave the drafter's layers to the
+ * engine [P2 KV Cache and CUDA Graphs].
+ *
+ * The KV cache.  One byte tensor [num_blocks, Hkv, block_size/16, 18*D]:
+ * each (block, head) holds block_size/16 records of 16 tokens.  A record is
+ *   key codes    [16][D/2]   byte i of a token: elements 2i (low half), 2i+1
+ *   value codes  [16][D/2]
+ *   key scales   [16][D/16]
+ *   value scales [16][D/16]
+ * Element x of a group of 16 consecutive elements is held as the e2m1 number
+ * nearest to x / s, s = e4m3(min(max|x| / 6, 448)) of its group (both to
+ * nearest, ties to even, saturating; s = 0 holds zeros), and stands for code
+ * times s.  D is 64 or 128, block_size a multiple of 16, slot =
+ * block * block_size + offset as in slot_mapping.  A group with an infinity
+ * saturates; the codes of a group with a NaN are unspecified (finite). */
+
+/* Rotate queries and keys by position and write keys and values to the cache.
+ * For row t, head h, pairs (x0, x1) of the first rot_dim elements are turned:
+ *   (x0 c - x1 s, x1 c + x0 s), c = rope[p][i], s = rope[p][rot_dim/2 + i]
+ * with p = positions[t] and pair i = elements (i, i + rot_dim/2), or
+ * (2i, 2i+1) when interleaved; elements from rot_dim on are kept.
+ *   q_out[t]   the rotated query, rounded to bf16 (from fp32)
+ *   k_out[t]   the rotated key, rounded to bf16 (correctly: from the exact
+ *              value); optional
+ *   cache      the key as k_out has it and the value, at slots[t]; nothing
+ *              for slot -1.  Slots must not repeat among the rows.
+ * A position outside [0, max_pos) turns nothing (PE_ERR_POS_RANGE); a slot
+ * below -1 or past the cache is skipped (PE_ERR_BLOCK_RANGE).
+ *  q [T,Hq,D], k, v [T,Hkv,D] with row and head strides in elements (multiples
+ *  of 8), q_out [T,Hq,D] and k_out [T,Hkv,D] dense; q_out may be q and k_out
+ *  may be k where those are dense.  rope [max_pos, rot_dim] fp32;
+ *  rot_dim a multiple of 32, at most D.  T == 0 enqueues nothing. */
+typedef struct pe_kv_append_args {
+  int32_t T, Hq, Hkv, D, block_size, rot_dim, interleaved, max_pos;
+  int64_t num_blocks;
+  int64_t q_row, q_head, k_row, k_head, v_row, v_head; /* strides */
+  const void* q;
+  const void* k;
+  const void* v;
+  const int32_t* positions; /* [T] */
+  const int64_t* slots;     /* [T] */
+  const float* rope;
+  void* cache;
+  void* q_out;
+  void* k_out; /* or NULL */
+  uint32_t* err;
+} pe_kv_append_args;
+int pe_kv_append(const pe_kv_append_args* args /* host */, void* stream);
+
+/* Read cached rows back: k_out[t], v_out[t] [n,Hkv,D] bf16 = the values that
+ * the cache holds at slots[t] (exact in bf16); zeros for slot -1, and for a
+ * slot outside the cache (PE_ERR_BLOCK_RANGE).  Either output may be NULL.
+ * n == 0 enqueues nothing. */
+int pe_kv_read(const void* cache, int64_t num_blocks, int32_t block_size,
+               int32_t Hkv, int32_t D, const int64_t* slots, int32_t n,
+               void* k_out, void* v_out, uint32_t* err, void* stream);
+
+/* Bytes of scratch that pe_attn_cached and pe_attn_prompt need for head size
+ * D (0 when D is neither 64 nor 128).  Allocated once, zero-filled; every call
+ * leaves its counters zero again (unless it raised PE_ERR_TIMEOUT or
+ * PE_ERR_WORKSPACE), so it serves every later call of either, of any batch,
+ * with that D or a smaller one.  Calls that may run concurrently need separate
+ * workspaces. */
+size_t pe_workspace_bytes_attn(int32_t D);
+
+#define PE_MAX_ATTN_B 4096  /* requests of one attention call                */
+#define PE_MAX_ATTN_G 128   /* query heads per key head                      */
+
+/* Attention over the cache.  Row t of request b sees the keys 0..limit-1 of
+ * the request's pages, limit = positions[t] + 1, or 0 when rejected:
+ *   out[t,h] = sum_j softmax_j(scale * q[t,h] . K[j,h/G]) V[j,h/G],  G = Hq/Hkv
+ * and zeros when limit is 0.  Key j lies in page block_table[b][j/block_size].
+ * The keys of the rows themselves have to be in the cache (pe_kv_append).
+ *  q, out [T,Hq,D] bf16, dense.  offsets [B+1] int32: the segments, as
+ *  out_offsets; NULL: T/B rows each.  is_rejected [T] or NULL: none.
+ *  scale: finite.  Sums and softmax statistics are fp32.
+ *  err: PE_ERR_OFFSETS (offsets no partition of T: nothing is written);
+ *  PE_ERR_BLOCK_RANGE (a position below 0 sees nothing, one past the table
+ *  sees the table's keys; the keys of a page outside the cache are left out);
+ *  PE_ERR_WORKSPACE, PE_ERR_TIMEOUT as above.
+ * T == 0 enqueues nothing. */
+typedef struct pe_attn_cached_args {
+  int32_t T, B, Hq, Hkv, D, block_size, bt_width;
+  float scale;
+  int64_t num_blocks;
+  const void* q;
+  const void* cache;
+  const int32_t* block_table; /* [B, bt_width] */
+  const int32_t* offsets;     /* [B+1] or NULL */
+  const int32_t* positions;   /* [T] */
+  const uint8_t* is_rejected; /* [T] or NULL */
+  void* out;
+  void* workspace;
+  uint32_t* err;
+} pe_attn_cached_args;
+int pe_attn_cached(const pe_attn_cached_args* args /* host */, void* stream);
+
+/* Causal attention over whole packed prompts: row i of a segment sees the
+ * keys 0..i of the same segment.
+ *  q [T,Hq,D], k, v [T,Hkv,D] bf16 with row and head strides in elements
+ *  (multiples of 8; below 2^31); out [T,Hq,D] dense; offsets [B+1] int32 or
+ *  NULL as above (empty segments are allowed).  err as above.
+ * T == 0 enqueues nothing. */
+typedef struct pe_attn_prompt_args {
+  int32_t T, B, Hq, Hkv, D;
+  float scale;
+  int64_t q_row, q_head, k_row, k_head, v_row, v_head; /* strides */
+  const void* q;
+  const void* k;
+  const void* v;
+  const int32_t* offsets; /* [B+1] or NULL */
+  void* out;
+  void* workspace;
+  uint32_t* err;
+} pe_attn_prompt_args;
+int pe_attn_prompt(const pe_attn_prompt_args* args /* host */, void* stream);
 
 /* Human-readable name of a pe_status value. */
 const char* pe_status_str(int status);

@@ -32,6 +32,7 @@ ERR_ROW_RANGE = 64
 ERR_NAN = 128
 ERR_INTERNAL = 256
 ERR_WORKSPACE = 512
+ERR_POS_RANGE = 1024
 MAX_KP, MAX_K = 255, 256
 
 # every function the C header declares
@@ -40,7 +41,9 @@ EXPORTS = ("pe_workspace_bytes", "pe_verify_greedy", "pe_draft_readout",
            "pe_build_draft_batch",
            "pe_assemble_draft_inputs", "pe_step", "pe_step_early_exit", "pe_step_noalloc",
            "pe_get_tuning",
-           "pe_set_tuning", "pe_latency_floor", "pe_status_str")
+           "pe_set_tuning", "pe_latency_floor", "pe_status_str",
+           "pe_kv_append", "pe_kv_read", "pe_workspace_bytes_attn", "pe_attn_cached",
+           "pe_attn_prompt")
 
 
 class PEError(RuntimeError):
@@ -74,6 +77,31 @@ class Tuning(ctypes.Structure):
     _fields_ = [("ctas_per_sm", i32), ("chunk_batches", i32), ("rows_per_unit", i32),
                 ("variant", i32), ("queue_order", i32), ("early_full_read_mb", i32),
                 ("single_pass", i32)]
+
+
+class KvAppendArgs(ctypes.Structure):
+    """Mirror of pe_kv_append_args."""
+    _fields_ = ([(n, i32) for n in ("T", "Hq", "Hkv", "D", "block_size", "rot_dim", "interleaved",
+                                    "max_pos")] +
+                [(n, i64) for n in ("num_blocks", "q_row", "q_head", "k_row", "k_head", "v_row",
+                                    "v_head")] +
+                [(n, P) for n in ("q", "k", "v", "positions", "slots", "rope", "cache", "q_out",
+                                  "k_out", "err")])
+
+
+class AttnCachedArgs(ctypes.Structure):
+    """Mirror of pe_attn_cached_args."""
+    _fields_ = ([(n, i32) for n in ("T", "B", "Hq", "Hkv", "D", "block_size", "bt_width")] +
+                [("scale", ctypes.c_float), ("num_blocks", i64)] +
+                [(n, P) for n in ("q", "cache", "block_table", "offsets", "positions",
+                                  "is_rejected", "out", "workspace", "err")])
+
+
+class AttnPromptArgs(ctypes.Structure):
+    """Mirror of pe_attn_prompt_args."""
+    _fields_ = ([(n, i32) for n in ("T", "B", "Hq", "Hkv", "D")] + [("scale", ctypes.c_float)] +
+                [(n, i64) for n in ("q_row", "q_head", "k_row", "k_head", "v_row", "v_head")] +
+                [(n, P) for n in ("q", "k", "v", "offsets", "out", "workspace", "err")])
 
 
 _lock = threading.Lock()
@@ -134,6 +162,14 @@ def _open(path: str):
     lib.pe_set_tuning.argtypes = [ctypes.POINTER(Tuning)]
     lib.pe_latency_floor.argtypes = [i32, i32, P, i32, P, P]
     lib.pe_latency_floor.restype = ctypes.c_int
+    lib.pe_kv_append.argtypes = [ctypes.POINTER(KvAppendArgs), P]
+    lib.pe_kv_read.argtypes = [P, i64, i32, i32, i32, P, i32, P, P, P, P]
+    lib.pe_workspace_bytes_attn.argtypes = [i32]
+    lib.pe_workspace_bytes_attn.restype = ctypes.c_size_t
+    lib.pe_attn_cached.argtypes = [ctypes.POINTER(AttnCachedArgs), P]
+    lib.pe_attn_prompt.argtypes = [ctypes.POINTER(AttnPromptArgs), P]
+    for f in ("pe_kv_append", "pe_kv_read", "pe_attn_cached", "pe_attn_prompt"):
+        getattr(lib, f).restype = ctypes.c_int
     lib.pe_status_str.argtypes = [ctypes.c_int]
     lib.pe_status_str.restype = ctypes.c_char_p
     for f in ("pe_verify_greedy", "pe_build_draft_batch", "pe_assemble_draft_inputs",
@@ -421,6 +457,166 @@ def latency_floor(ctas: int, hops: int = 0, chain=None, out=None, stream=None):
     rc = lib.pe_latency_floor(ctas, hops, _dev(chain, "chain", torch.int32), n,
                               _dev(out, "out", torch.int32, 1), _stream(stream))
     _check(lib, rc, "pe_latency_floor")
+
+
+# ------------------------------------------------ the drafter layer's attention
+
+def _rows(t: torch.Tensor, name: str, T=None, H=None, D=None):
+    """Pointer and strides of [T, heads, D] bf16 rows with dense elements."""
+    if not t.is_cuda or t.dim() != 3:
+        raise ValueError("%s must be a CUDA tensor [T, heads, D]" % name)
+    if t.dtype != torch.bfloat16:
+        raise TypeError("%s must be bfloat16, got %s" % (name, t.dtype))
+    if t.shape[2] > 1 and t.stride(2) != 1:
+        raise ValueError("%s must have unit element stride" % name)
+    for axis, n in ((0, T), (1, H), (2, D)):
+        if n is not None and t.shape[axis] != n:
+            raise ValueError("%s must be %s, got %s" % (name, [T, H, D], list(t.shape)))
+    # the stride of an axis of one element is never used
+    return (ctypes.c_void_p(t.data_ptr()), t.stride(0) if t.shape[0] > 1 else 0,
+            t.stride(1) if t.shape[1] > 1 else 0)
+
+
+def _dense(t: torch.Tensor | None, name: str, *shape):
+    if t is None:
+        return None
+    p = _rows(t, name, *shape)[0]
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return p
+
+
+def _cache(t: torch.Tensor, Hkv=None, D=None):
+    """Pointer, blocks, block size, heads and head size of a 4-bit cache."""
+    if not t.is_cuda or t.dim() != 4 or t.dtype != torch.uint8 or not t.is_contiguous():
+        raise ValueError("cache must be a contiguous uint8 CUDA tensor "
+                         "[num_blocks, Hkv, block_size/16, 18*D]")
+    if t.shape[3] % 18 or (Hkv is not None and t.shape[1] != Hkv) or \
+            (D is not None and t.shape[3] != 18 * D):
+        raise ValueError("cache of shape %s does not hold Hkv=%s, D=%s"
+                         % (list(t.shape), Hkv, D))
+    return (ctypes.c_void_p(t.data_ptr()), t.shape[0], 16 * t.shape[2], t.shape[1],
+            t.shape[3] // 18)
+
+
+def _exactly(t: torch.Tensor | None, name: str, dtype, n: int):
+    p = _dev(t, name, dtype, n)
+    if t is not None and t.numel() != n:
+        raise ValueError("%s holds %d elements, needs %d" % (name, t.numel(), n))
+    return p
+
+
+def new_kv_cache(num_blocks: int, block_size: int, Hkv: int, D: int, device="cuda") -> torch.Tensor:
+    """A zeroed 4-bit paged KV cache (see include/pe_api.h for the layout):
+    1.125 bytes per element pair of key and value."""
+    if num_blocks < 1 or Hkv < 1 or D not in (64, 128) or block_size < 16 or block_size % 16:
+        raise ValueError("need num_blocks >= 1, Hkv >= 1, D 64 or 128, block_size a multiple of 16")
+    return torch.zeros(num_blocks, Hkv, block_size // 16, 18 * D, dtype=torch.uint8, device=device)
+
+
+def rope_table(max_pos: int, rot_dim: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
+    """fp32 [max_pos, rot_dim]: cos then sin of pos * base^(-2i/rot_dim), the
+    angles in fp64 so that far positions keep their digits."""
+    inv = base ** (-torch.arange(0, rot_dim, 2, dtype=torch.float64, device=device) / rot_dim)
+    a = torch.arange(max_pos, dtype=torch.float64, device=device)[:, None] * inv
+    return torch.cat((a.cos(), a.sin()), 1).float()
+
+
+def kv_append(q, k, v, positions, slots, rope, cache, q_out, err, k_out=None, interleaved=False,
+              stream=None):
+    """Rotate q and k by position; write k and v into ``cache`` at ``slots``
+    (slot_mapping of the draft batch: -1 writes nothing); q_out (and k_out)
+    take the rotated rows."""
+    lib = load()
+    a = KvAppendArgs()
+    a.cache, a.num_blocks, a.block_size, a.Hkv, a.D = _cache(cache)
+    a.T, a.Hq = q.shape[0], q.shape[1] if q.dim() == 3 else 0
+    a.q, a.q_row, a.q_head = _rows(q, "q", a.T, a.Hq, a.D)
+    a.k, a.k_row, a.k_head = _rows(k, "k", a.T, a.Hkv, a.D)
+    a.v, a.v_row, a.v_head = _rows(v, "v", a.T, a.Hkv, a.D)
+    if rope.dim() != 2:
+        raise ValueError("rope must be [max_pos, rot_dim]")
+    a.max_pos, a.rot_dim = rope.shape
+    a.rope = _dev(rope, "rope", torch.float32)
+    a.interleaved = int(bool(interleaved))
+    a.positions = _exactly(positions, "positions", torch.int32, a.T)
+    a.slots = _exactly(slots, "slots", torch.int64, a.T)
+    a.q_out = _dense(q_out, "q_out", a.T, a.Hq, a.D)
+    a.k_out = _dense(k_out, "k_out", a.T, a.Hkv, a.D)
+    a.err = _dev(err, "err", torch.int32, 1)
+    _check(lib, lib.pe_kv_append(ctypes.byref(a), _stream(stream)), "pe_kv_append")
+
+
+def kv_read(cache, slots, k_out, v_out, err, stream=None):
+    """The values that ``cache`` holds at ``slots``, as bf16 rows [n, Hkv, D]
+    (zeros for slot -1); either output may be None."""
+    lib = load()
+    cp, nb, bs, Hkv, D = _cache(cache)
+    n = slots.numel()
+    rc = lib.pe_kv_read(cp, nb, bs, Hkv, D, _dev(slots, "slots", torch.int64), n,
+                        _dense(k_out, "k_out", n, Hkv, D), _dense(v_out, "v_out", n, Hkv, D),
+                        _dev(err, "err", torch.int32, 1), _stream(stream))
+    _check(lib, rc, "pe_kv_read")
+
+
+def workspace_bytes_attn(D: int) -> int:
+    return int(load().pe_workspace_bytes_attn(D))
+
+
+def new_attn_workspace(D: int, device="cuda") -> torch.Tensor:
+    """Zero-filled scratch for attn_cached / attn_prompt (reusable)."""
+    return torch.zeros(workspace_bytes_attn(D), dtype=torch.uint8, device=device)
+
+
+def _default_scale(scale, D):
+    return float(scale) if scale is not None else D ** -0.5
+
+
+def attn_cached(q, cache, block_table, offsets, positions, is_rejected, out, workspace, err,
+                scale=None, stream=None):
+    """Attention of the packed rows over their requests' cached keys
+    (0..positions[t]; rejected rows give zeros).  offsets [B+1], or None for
+    equal segments; scale defaults to D**-0.5."""
+    lib = load()
+    a = AttnCachedArgs()
+    a.cache, a.num_blocks, a.block_size, a.Hkv, a.D = _cache(cache)
+    a.T, a.Hq = q.shape[0], q.shape[1] if q.dim() == 3 else 0
+    a.q = _dense(q, "q", a.T, a.Hq, a.D)
+    a.out = _dense(out, "out", a.T, a.Hq, a.D)
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B, width]")
+    a.B, a.bt_width = block_table.shape
+    a.block_table = _dev(block_table, "block_table", torch.int32)
+    a.offsets = _exactly(offsets, "offsets", torch.int32, a.B + 1)
+    a.positions = _exactly(positions, "positions", torch.int32, a.T)
+    a.is_rejected = _exactly(is_rejected, "is_rejected", torch.uint8, a.T)
+    a.scale = _default_scale(scale, a.D)
+    a.workspace = _dev(workspace, "workspace", torch.uint8, workspace_bytes_attn(a.D))
+    a.err = _dev(err, "err", torch.int32, 1)
+    _check(lib, lib.pe_attn_cached(ctypes.byref(a), _stream(stream)), "pe_attn_cached")
+
+
+def attn_prompt(q, k, v, offsets, out, workspace, err, scale=None, B=None, stream=None):
+    """Causal attention over packed prompts.  offsets [B+1], or None for B
+    equal segments; scale defaults to D**-0.5."""
+    lib = load()
+    a = AttnPromptArgs()
+    if q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q and k must be [T, heads, D]")
+    a.T, a.Hq, a.D = q.shape
+    a.Hkv = k.shape[1]
+    a.q, a.q_row, a.q_head = _rows(q, "q")
+    a.k, a.k_row, a.k_head = _rows(k, "k", a.T, a.Hkv, a.D)
+    a.v, a.v_row, a.v_head = _rows(v, "v", a.T, a.Hkv, a.D)
+    a.out = _dense(out, "out", a.T, a.Hq, a.D)
+    if offsets is None and B is None:
+        raise ValueError("offsets or B is needed")
+    a.B = offsets.numel() - 1 if offsets is not None else B
+    a.offsets = _exactly(offsets, "offsets", torch.int32, a.B + 1)
+    a.scale = _default_scale(scale, a.D)
+    a.workspace = _dev(workspace, "workspace", torch.uint8, workspace_bytes_attn(a.D))
+    a.err = _dev(err, "err", torch.int32, 1)
+    _check(lib, lib.pe_attn_prompt(ctypes.byref(a), _stream(stream)), "pe_attn_prompt")
 
 
 def get_tuning() -> dict:

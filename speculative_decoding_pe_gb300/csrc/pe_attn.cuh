@@ -1,0 +1,68 @@
+// What the attention kernels share: segments, workspace, argument checks.
+#pragma once
+
+#include <math.h>
+
+#include "pe_internal.cuh"
+#include "pe_kv.cuh"
+
+namespace pe {
+
+// Segment b of the packed rows: offsets[b..b+1], or T/B rows each.
+struct Segments {
+  const int32_t* offsets;
+  int T, B;
+  __device__ int begin(int b) const { return offsets ? __ldg(offsets + b) : b * (T / B); }
+  __device__ int end(int b) const { return offsets ? __ldg(offsets + b + 1) : (b + 1) * (T / B); }
+  // The request that row t belongs to (offsets valid).
+  __device__ int request(int t) const {
+    if (!offsets) return t / (T / B);
+    int lo = 0, hi = B - 1;  // the last b with begin(b) <= t
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (__ldg(offsets + mid) <= t) lo = mid; else hi = mid - 1;
+    }
+    return lo;
+  }
+};
+
+// Keys that a row of the cached attention sees.
+__device__ __forceinline__ int row_limit(const int32_t* positions, const uint8_t* is_rejected,
+                                         int t, int table_keys, bool& bad) {
+  if (is_rejected && __ldg(is_rejected + t)) return 0;
+  const int pos = __ldg(positions + t);
+  if (pos < 0) {
+    bad = true;
+    return 0;
+  }
+  if (pos >= table_keys) {
+    bad = true;
+    return table_keys;
+  }
+  return pos + 1;
+}
+
+// Scratch: one counter per CTA that begins a split item, then two partial
+// results per CTA of up to 256 rows (fp32 sums, maximum and total of a row).
+constexpr int kAttnCtas = 304;
+struct AttnWorkspace {
+  static constexpr size_t kPartials = 4096;  // byte offset; counters before it
+  static constexpr size_t partial_bytes(int D) { return (size_t)256 * (D + 2) * 4; }
+  static constexpr size_t bytes(int D) { return kPartials + 2 * kAttnCtas * partial_bytes(D); }
+};
+
+}  // namespace pe
+
+namespace pe_host {
+
+// The checks that both attention calls share (sizes only).
+inline int attn_sizes(int T, int B, int Hq, int Hkv, int D, const void* offsets, float scale) {
+  if (T < 0 || B < 1 || B > PE_MAX_ATTN_B || Hq < 1 || Hkv < 1 || Hq % Hkv ||
+      Hq / Hkv > PE_MAX_ATTN_G || (D != 64 && D != 128) || !isfinite(scale))
+    return PE_EINVAL;
+  if (!offsets && T % B) return PE_EINVAL;
+  if ((int64_t)T * Hq * D > ((int64_t)1 << 40)) return PE_EINVAL;
+  return PE_OK;
+}
+
+}  // namespace pe_host
