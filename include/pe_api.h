@@ -468,7 +468,7 @@ int pe_kv_read(const void* cache, int64_t num_blocks, int32_t block_size,
  * workspaces. */
 size_t pe_workspace_bytes_attn(int32_t D);
 
-#define PE_MAX_ATTN_B 4096  /* requests of one attention call                */
+#define PE_MAX_ATTN_B 2048  /* requests of one attention call                */
 #define PE_MAX_ATTN_G 128   /* query heads per key head                      */
 
 /* Attention over the cache.  Row t of request b sees the keys 0..limit-1 of

@@ -42,13 +42,13 @@ __device__ __forceinline__ int row_limit(const int32_t* positions, const uint8_t
   return pos + 1;
 }
 
-// Scratch: one counter per CTA that begins a split item, then two partial
+// Scratch: one counter per CTA that begins a split item, then three partial
 // results per CTA of up to 256 rows (fp32 sums, maximum and total of a row).
-constexpr int kAttnCtas = 304;
+constexpr int kAttnCtas = 152;
 struct AttnWorkspace {
   static constexpr size_t kPartials = 4096;  // byte offset; counters before it
-  static constexpr size_t partial_bytes(int D) { return (size_t)256 * (D + 2) * 4; }
-  static constexpr size_t bytes(int D) { return kPartials + 2 * kAttnCtas * partial_bytes(D); }
+  __host__ __device__ static constexpr size_t partial_bytes(int D) { return (size_t)256 * (D + 2) * 4; }
+  __host__ __device__ static constexpr size_t bytes(int D) { return kPartials + 3 * kAttnCtas * partial_bytes(D); }
 };
 
 }  // namespace pe

@@ -2,23 +2,9 @@
 //
 // One warp per row and query head, one pass over the keys with the running
 // maximum and sum of the softmax; a lane holds D/32 elements.
-#include "pe_attn.cuh"
+#include "pe_attn_few.cuh"
 
 namespace pe {
-
-struct CachedParams {
-  Segments seg;
-  int Hq, Hkv, block_size, bt_width, table_keys;
-  long long num_blocks;
-  float scale_log2;
-  const uint16_t* q;
-  const uint8_t* cache;
-  const int32_t* block_table;
-  const int32_t* positions;
-  const uint8_t* is_rejected;
-  uint16_t* out;
-  uint32_t* err;
-};
 
 template <int D>
 __global__ void __launch_bounds__(kThreads) attn_cached_kernel(const CachedParams p) {
@@ -84,6 +70,21 @@ __global__ void __launch_bounds__(kThreads) attn_cached_kernel(const CachedParam
 
 }  // namespace pe
 
+namespace {
+
+template <int D, int NB>
+int launch_few(const pe::CachedParams& p, int sms, cudaStream_t s) {
+  static std::atomic<unsigned long long> allowed{0};
+  const int most = pe::FewShape<D>::kBytes + 12 * (PE_MAX_ATTN_B + 1);
+  if (!pe_host::allow_smem(pe::attn_few_kernel<D, NB>, most, allowed)) return PE_ECUDA;
+  const int bytes = pe::FewShape<D>::kBytes + 12 * (p.seg.B + 1);
+  const int grid = 2 * (sms < pe::kAttnCtas ? sms : pe::kAttnCtas);
+  pe::attn_few_kernel<D, NB><<<grid, 256, bytes, s>>>(p);
+  return pe_host::launch_status();
+}
+
+}  // namespace
+
 extern "C" size_t pe_workspace_bytes_attn(int32_t D) {
   return D == 64 || D == 128 ? pe::AttnWorkspace::bytes(D) : 0;
 }
@@ -116,8 +117,12 @@ extern "C" int pe_attn_cached(const pe_attn_cached_args* a, void* stream) {
   p.is_rejected = a->is_rejected;
   p.out = static_cast<uint16_t*>(a->out);
   p.err = a->err;
+  p.ws = static_cast<uint8_t*>(a->workspace);
   const int grid = dev.sm_count * 8;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int64_t rows = a->offsets ? INT64_MAX : (int64_t)(a->T / a->B) * (a->Hq / a->Hkv);
+  if (rows <= 8) return a->D == 64 ? launch_few<64, 1>(p, dev.sm_count, s) : launch_few<128, 1>(p, dev.sm_count, s);
+  if (rows <= 16) return a->D == 64 ? launch_few<64, 2>(p, dev.sm_count, s) : launch_few<128, 2>(p, dev.sm_count, s);
   if (a->D == 64)
     pe::attn_cached_kernel<64><<<grid, pe::kThreads, 0, s>>>(p);
   else

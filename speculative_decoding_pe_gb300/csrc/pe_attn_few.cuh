@@ -1,0 +1,480 @@
+// Attention over the 4-bit cache for few rows: at most 16 rows (tokens times
+// query heads per key head) of a request, as a step without drafts has them.
+//
+// Bound by the bytes of the cache (a row of 64 keeps 8 heads: 8 products per
+// code), then by the instructions that turn codes into numbers, so the layout
+// serves the conversion: S^T = K Q^T and O^T = V^T P^T on m16n8k16 products, in
+// which the 16-row operand is what was just converted in registers (no trip
+// through shared memory as the tcgen05 operands would take) and the 8 columns
+// are the rows: 8 rows fill it, where a product with the rows as M would leave
+// half of it empty.  The order of elements within a product is free as long as
+// both operands agree, so a lane takes 8 or 16 consecutive bytes of a token's
+// keys, and 4 or 8 of its values.
+//
+// Weights.  P is f16 and codes times scales are exact in f16 (6 bits), so V is
+// exact and P keeps 11 bits.  Queries become f16 too after a power of two is
+// taken out of each row (its largest element lies in [1, 2)): elements down to
+// 2^-14 of it keep their 8 bits, and what a smaller one loses is below 2^-25 of
+// the largest.
+//
+// Work.  A part of the line is a run of records (16 keys); its CTA's 8 warps
+// share a segment's records and meet at its end.  Each warp brings its records
+// by bulk copies, a step ahead, through segments.
+#pragma once
+
+#include "pe_attn_line.cuh"
+#include "pe_tma.cuh"
+#include "pe_umma.cuh"
+
+namespace pe {
+
+struct CachedParams {
+  Segments seg;
+  int Hq, Hkv, block_size, bt_width, table_keys;
+  long long num_blocks;
+  float scale_log2;
+  const uint16_t* q;
+  const uint8_t* cache;
+  const int32_t* block_table;
+  const int32_t* positions;
+  const uint8_t* is_rejected;
+  uint16_t* out;
+  uint8_t* ws;
+  uint32_t* err;
+};
+
+template <int D>
+struct FewShape {
+  static constexpr int kWarps = 8;
+  static constexpr int kStages = 2;
+  static constexpr int kRecords = 256 / D;                        // of a step
+  static constexpr int kStep = kRecords * Record<D>::kBytes;      // 4608 bytes
+  static constexpr int kRing = kWarps * kStages * kStep;
+  static constexpr int kMeet = kWarps * 8 * 64 * 4;               // 64 sums of 8 rows per warp
+  static constexpr int kBytes = kRing + kMeet;                    // then prefix and keys
+  static constexpr int kMinRecords = 16;                          // of a part
+};
+
+struct FewControl {
+  uint64_t full[8][2];
+  Walk start;
+  long long total, parts;
+  int dead, last;
+  float m[8][16], l[8][16];
+};
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                        uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t lo_halves(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x5410); }
+__device__ __forceinline__ uint32_t hi_halves(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x7632); }
+
+// The power of two to take out of a row whose largest magnitude is `most`, as
+// (factor, its inverse); the exponents stay those of normal numbers.
+__device__ __forceinline__ float2 row_factor(float most) {
+  uint32_t e = __float_as_uint(most) >> 23;
+  if (most == 0.0f || e >= 255) return make_float2(1.0f, 1.0f);
+  e = min(max(e, 1u), 252u);
+  return make_float2(__uint_as_float((254 - e) << 23), __uint_as_float(e << 23));
+}
+
+template <int D, int NB>
+__global__ void __launch_bounds__(256, 2) attn_few_kernel(const CachedParams p) {
+  using R = Record<D>;
+  using F = FewShape<D>;
+  constexpr int kGroups = D / 64;       // key groups of 16 elements per lane and token
+  constexpr int kSteps = D / 16;        // products of a record's scores
+  constexpr int kRec = F::kRecords;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ FewControl c;
+  __shared__ long long sums[256];
+  long long* prefix = reinterpret_cast<long long*>(smem + F::kBytes);
+  int* keys = reinterpret_cast<int*>(prefix + p.seg.B + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, cc = lane & 3;
+  if (lane < F::kStages) mbar_init(&c.full[warp][lane], 1);
+  if (threadIdx.x == 0) c.dead = 0;
+  mbar_init_fence();
+  Line<true, 16> line{p.seg, p.Hkv, p.Hq / p.Hkv, kTile / (p.Hq / p.Hkv), nullptr, nullptr};
+  if (!plan(line, F::kMinRecords, c, prefix, keys, sums, p.positions, p.is_rejected, p.table_keys, p.err))
+    return;
+  if (c.start.u >= c.start.end) return;
+
+  uint8_t* ring = smem + warp * F::kStages * F::kStep;
+  float* meet = reinterpret_cast<float*>(smem + F::kRing);
+  const int per_page = p.block_size >> 4;
+  // the token of a record that row r of a 16-row operand holds (and r + 8: 8
+  // more), so that the lanes of one load reach different banks
+  constexpr uint32_t kOrder = D == 64 ? 0x57463120u : 0x67542310u;
+  auto order = [&](int i) { return (int)(kOrder >> (4 * i)) & 15; };
+  const int key_tok = order(r), val_a = order(2 * cc), val_b = order(2 * cc + 1);
+
+  // ---- the loader: pages one step ahead of the copies, copies kStages ahead
+  Walk lw = c.start;
+  int lpos = 0, lend = 0, page = -1, ln = 0, lrec = 0, lh = 0;
+  bool more = true;
+  uint32_t issued = 0, taken = 0, ok_bits = 0;
+  auto next_pages = [&]() {  // the step after the one just issued: its pages' ids
+    while (more && lpos >= lend) {
+      more = walk_next(line, lw);
+      if (!more) break;
+      const int n = lw.t1 - lw.t0;
+      lpos = lw.t0 + (int)((long long)n * warp / F::kWarps);
+      lend = lw.t0 + (int)((long long)n * (warp + 1) / F::kWarps);
+    }
+    ln = 0;
+    if (!more) return;
+    ln = min(kRec, lend - lpos);
+    lrec = lpos, lh = lw.h;
+    page = -1;
+    if (lane < ln && (lrec + lane) * 16 < max(1, keys[lw.b]))
+      page = __ldg(p.block_table + (long long)lw.b * p.bt_width + (lrec + lane) / per_page);
+    lpos += ln;
+  };
+  auto issue = [&]() {
+    if (!ln) return;
+    const uint32_t st = issued % F::kStages;
+    const bool ok = lane < ln && page >= 0 && page < p.num_blocks;
+    const uint32_t bits = __ballot_sync(0xffffffffu, ok);
+    ok_bits = (ok_bits & ~(0xffu << (8 * st))) | bits << (8 * st);
+    if (lane == 0) mbar_arrive_expect_tx(&c.full[warp][st], __popc(bits) * R::kBytes);
+    __syncwarp();
+    if (ok)
+      bulk_load(ring + st * F::kStep + lane * R::kBytes,
+                p.cache + (((long long)page * p.Hkv + lh) * per_page + (lrec + lane) % per_page) * R::kBytes,
+                R::kBytes, &c.full[warp][st]);
+    ++issued;
+    next_pages();
+  };
+  next_pages();
+#pragma unroll
+  for (int i = 0; i < F::kStages; ++i) issue();
+
+  Walk w = c.start;
+  while (walk_next(line, w)) {
+    const int G = line.G, L = keys[w.b];
+    const int nrows = w.rows * G;
+    // ---- queries: this lane's elements of row r (and r + 8)
+    uint32_t q[NB][kSteps][2];
+    float sc[NB][2];        // of rows 2 cc, 2 cc + 1
+    int limit[NB][2], least = INT32_MAX;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const int row = 8 * b + r;
+      const bool in = row < nrows;
+      uint32_t raw[2 * kSteps] = {};
+      float most = 0.0f;
+      if (in) {
+        const uint4* src = reinterpret_cast<const uint4*>(
+            p.q + ((long long)(w.first + row / G) * p.Hq + w.h * G + row % G) * D + 16 * kGroups * cc);
+#pragma unroll
+        for (int i = 0; i < kSteps / 2; ++i) {
+          const uint4 x = __ldg(src + i);
+          raw[4 * i] = x.x, raw[4 * i + 1] = x.y, raw[4 * i + 2] = x.z, raw[4 * i + 3] = x.w;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 2 * kSteps; ++i) most = fmaxf(most, fmaxf(fabsf(bf16_lo(raw[i])), fabsf(bf16_hi(raw[i]))));
+      most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+      most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+      const float2 f = row_factor(most);
+#pragma unroll
+      for (int i = 0; i < 2 * kSteps; ++i) q[b][i / 2][i % 2] = pack_f16(bf16_lo(raw[i]) * f.x, bf16_hi(raw[i]) * f.x);
+      bool bad = false;  // reported by the plan
+      const int mine = in ? row_limit(p.positions, p.is_rejected, w.first + row / G, p.table_keys, bad) : 0;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        sc[b][e] = p.scale_log2 * __shfl_sync(0xffffffffu, f.y, 4 * (2 * cc + e));
+        limit[b][e] = __shfl_sync(0xffffffffu, mine, 4 * (2 * cc + e));
+        // a row that sees nothing computes what it likes and is thrown away
+        if (limit[b][e] > 0) least = min(least, limit[b][e]);
+      }
+    }
+    least = min(least, __shfl_xor_sync(0xffffffffu, least, 1));
+    least = min(least, __shfl_xor_sync(0xffffffffu, least, 2));
+    float m[NB][2], l[NB][2], o[NB][D / 16][4];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) m[b][e] = -INFINITY, l[b][e] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[b][j][e] = 0.0f;
+    }
+
+    // ---- this warp's records
+    const int n = w.t1 - w.t0;
+    int pos = w.t0 + (int)((long long)n * warp / F::kWarps);
+    const int end = w.t0 + (int)((long long)n * (warp + 1) / F::kWarps);
+    while (pos < end) {
+      const int cnt = min(kRec, end - pos);
+      const uint32_t st = taken % F::kStages;
+      wait_warp(&c.full[warp][st], (taken / F::kStages) & 1, &c.dead);
+      ++taken;
+      const uint32_t ok = (ok_bits >> (8 * st)) & 0xffu;
+      const uint8_t* step = ring + st * F::kStep;
+      const bool masked = cnt < kRec || ok != (1u << kRec) - 1 || (pos + kRec) * 16 > least;
+      float s[NB][kRec][4];
+#pragma unroll
+      for (int x = 0; x < kRec; ++x) {
+        const uint8_t* rec = step + x * R::kBytes;
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[b][x][e] = 0.0f;
+        uint32_t kw[2][2 * kGroups], ks[2][kGroups];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int tok = key_tok + 8 * e;
+          if (kGroups == 1) {
+            const uint2 y = *reinterpret_cast<const uint2*>(rec + R::kK + tok * R::kRow + 8 * cc);
+            kw[e][0] = y.x, kw[e][1] = y.y;
+            ks[e][0] = e4m3_f16x2(rec[R::kKs + tok * R::kScaleRow + cc]);
+          } else {
+            const uint4 y = *reinterpret_cast<const uint4*>(rec + R::kK + tok * R::kRow + 16 * cc);
+            kw[e][0] = y.x, kw[e][1] = y.y, kw[e][2 * kGroups - 2] = y.z, kw[e][2 * kGroups - 1] = y.w;
+            const uint16_t two = *reinterpret_cast<const uint16_t*>(rec + R::kKs + tok * R::kScaleRow + 2 * cc);
+            uint32_t both;
+            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(both) : "h"(two));
+            ks[e][0] = __byte_perm(both, both, 0x1010);
+            ks[e][kGroups - 1] = __byte_perm(both, both, 0x3232);
+          }
+        }
+#pragma unroll
+        for (int g = 0; g < 2 * kGroups; ++g) {  // 8 codes of both tokens: two products
+          uint32_t a[4], b8[4];
+          e2m1x8_f16(kw[0][g], a);
+          e2m1x8_f16(kw[1][g], b8);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) a[e] = hmul2(a[e], ks[0][g / 2]), b8[e] = hmul2(b8[e], ks[1][g / 2]);
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            mma_f16(s[b][x], a[0], b8[0], a[1], b8[1], q[b][2 * g][0], q[b][2 * g][1]);
+            mma_f16(s[b][x], a[2], b8[2], a[3], b8[3], q[b][2 * g + 1][0], q[b][2 * g + 1][1]);
+          }
+        }
+      }
+      if (masked) {
+#pragma unroll
+        for (int x = 0; x < kRec; ++x)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int key = (pos + x) * 16 + key_tok + 8 * (e >> 1);
+            const bool there = x < cnt && (ok >> x & 1);
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+              if (!there || key >= limit[b][e & 1]) s[b][x][e] = -INFINITY;
+          }
+      }
+      // ---- maxima: a row's are shared by the 8 lanes of its column
+      bool grew = false;
+      float top[NB][2];
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float t = -INFINITY;
+#pragma unroll
+          for (int x = 0; x < kRec; ++x) t = max3(t, s[b][x][e], s[b][x][e + 2]);
+          top[b][e] = t * sc[b][e];
+          grew |= top[b][e] > m[b][e] + 8.0f;
+        }
+      if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float t = top[b][e];
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, d));
+            const bool g = t > m[b][e] + 8.0f;
+            const float f = g ? exp2_approx(m[b][e] - t) : 1.0f;
+            if (g) m[b][e] = t;
+            l[b][e] *= f;
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) o[b][j][e] *= f, o[b][j][e + 2] *= f;
+          }
+      }
+      // ---- weights; the maximum is held at 2^7, so that an f16 weight keeps
+      // every bit down to 2^-21 of it (before a rescale it reaches 2^15 at most)
+#pragma unroll
+      for (int x = 0; x < kRec; ++x) {
+        if (x >= cnt) break;
+        const uint8_t* rec = step + x * R::kBytes;
+        uint32_t pt[NB][2];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          float e[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float shift = (m[b][i & 1] == -INFINITY ? 0.0f : -m[b][i & 1]) + 7.0f;
+            e[i] = exp2_approx(fmaf(s[b][x][i], sc[b][i & 1], shift));
+            l[b][i & 1] += e[i];
+          }
+          pt[b][0] = transpose8x8(pack_f16(e[0], e[1]));
+          pt[b][1] = transpose8x8(pack_f16(e[2], e[3]));
+        }
+        uint32_t vw[4][kGroups], vs[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int tok = (i & 1 ? val_b : val_a) + 8 * (i >> 1);
+          const uint8_t* src = rec + R::kV + tok * R::kRow + 4 * kGroups * r;
+          if (kGroups == 1) {
+            vw[i][0] = *reinterpret_cast<const uint32_t*>(src);
+          } else {
+            const uint2 y = *reinterpret_cast<const uint2*>(src);
+            vw[i][0] = y.x, vw[i][kGroups - 1] = y.y;
+          }
+          uint32_t scale = rec[R::kVs + tok * R::kScaleRow + (kGroups == 1 ? r >> 1 : r)];
+          // what lies past the request's keys may be anything, a NaN too
+          if (masked && ((pos + x) * 16 + tok >= L || !(ok >> x & 1))) scale = 0;
+          vs[i] = e4m3_f16x2(scale);
+        }
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) {
+          uint32_t v[4][4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            e2m1x8_f16(vw[i][g], v[i]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[i][e] = hmul2(v[i][e], vs[i]);
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+              mma_f16(o[b][4 * g + e], lo_halves(v[0][e], v[1][e]), hi_halves(v[0][e], v[1][e]),
+                      lo_halves(v[2][e], v[3][e]), hi_halves(v[2][e], v[3][e]), pt[b][0], pt[b][1]);
+        }
+      }
+      if (ok != (1u << cnt) - 1 && lane == 0 && pos * 16 < L) atomicOr(p.err, PE_ERR_BLOCK_RANGE);
+      pos += cnt;
+      __syncwarp();  // the step is read: its place takes the next copies
+      issue();
+    }
+
+    // ---- the 8 warps meet
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) l[b][e] += __shfl_xor_sync(0xffffffffu, l[b][e], d);
+        if (r == 0) c.m[warp][8 * b + 2 * cc + e] = m[b][e], c.l[warp][8 * b + 2 * cc + e] = l[b][e];
+      }
+    __syncthreads();
+    const bool whole = w.t0 == 0 && w.t1 == w.tiles;
+    Reach at{0, 0};
+    if (!whole) at = reach(w, c.parts, c.total);
+    // partial results: [slot][row][D] sums, then (maximum, total) [row]
+    auto slot = [&](int part, int i) {
+      return reinterpret_cast<float*>(p.ws + AttnWorkspace::kPartials) + (2LL * part + i) * (16 * (D + 2));
+    };
+    float* mine = slot(blockIdx.x, (int)blockIdx.x == at.first);
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float top = -INFINITY;
+        for (int i = 0; i < F::kWarps; ++i) top = fmaxf(top, c.m[i][8 * b + 2 * cc + e]);
+        const float f = m[b][e] == -INFINITY ? 0.0f : exp2_approx(m[b][e] - top);
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) o[b][j][e] *= f, o[b][j][e + 2] *= f;
+      }
+#pragma unroll
+      for (int half = 0; half < kGroups; ++half) {
+        // 64 elements of 8 rows: [warp][row][64]; lane r holds elements 8 kGroups r + ...
+        float* to = meet + warp * 512;
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            *reinterpret_cast<float2*>(to + (2 * cc + e) * 64 + 8 * r + 2 * j) =
+                make_float2(o[b][4 * half + j][e], o[b][4 * half + j][e + 2]);
+        __syncthreads();
+        {
+          const int row = 8 * b + warp, pair = lane;
+          // element pair of the lane that held it
+          const int d = (pair / 4) * 8 * kGroups + 8 * half + 2 * (pair % 4);
+          float top = -INFINITY, total = 0.0f;
+          float2 sum = make_float2(0.0f, 0.0f);
+          for (int k = 0; k < F::kWarps; ++k) top = fmaxf(top, c.m[k][row]);
+          for (int k = 0; k < F::kWarps; ++k) {
+            if (c.m[k][row] == -INFINITY) continue;
+            total += c.l[k][row] * exp2_approx(c.m[k][row] - top);
+            const float2 y = *reinterpret_cast<const float2*>(meet + k * 512 + (row & 7) * 64 + 2 * pair);
+            sum.x += y.x, sum.y += y.y;
+          }
+          if (row < nrows) {
+            bool bad = false;
+            const bool live =
+                row_limit(p.positions, p.is_rejected, w.first + row / G, p.table_keys, bad) > 0;
+            if (whole) {
+              const float inv = total > 0.0f ? 1.0f / total : (total == total ? 0.0f : total);
+              *reinterpret_cast<uint32_t*>(
+                  p.out + ((long long)(w.first + row / G) * p.Hq + w.h * G + row % G) * D + d) =
+                  live ? pack_bf16(sum.x * inv, sum.y * inv) : 0u;
+            } else {
+              *reinterpret_cast<float2*>(mine + row * D + d) = sum;
+              if (d == 0)
+                *reinterpret_cast<float2*>(mine + 16 * D + 2 * row) =
+                    live ? make_float2(top, total) : make_float2(-INFINITY, 0.0f);
+            }
+          }
+        }
+        __syncthreads();
+      }
+    }
+    if (!whole) {
+      if (threadIdx.x == 0) {
+        unsigned* count = reinterpret_cast<unsigned*>(p.ws) + at.first;
+        const unsigned old = atom_add_acq_rel_u32(count, 1), want = at.last - at.first;
+        if (old > want) atomicOr(p.err, PE_ERR_WORKSPACE);
+        c.last = old == want;
+        if (c.last) *count = 0;
+      }
+      __syncthreads();
+      if (c.last) {
+        for (int i = threadIdx.x; i < nrows * (D / 2); i += 256) {
+          const int row = i / (D / 2), d = 2 * (i % (D / 2));
+          float top = -INFINITY, total = 0.0f;
+          float2 sum = make_float2(0.0f, 0.0f);
+          for (int part = at.first; part <= at.last; ++part) {
+            const float* from = slot(part, part == at.first);
+            const float2 ml = __ldcg(reinterpret_cast<const float2*>(from + 16 * D + 2 * row));
+            const float2 y = __ldcg(reinterpret_cast<const float2*>(from + row * D + d));
+            if (ml.x == -INFINITY) continue;
+            const float t = fmaxf(top, ml.x);
+            const float f = top == -INFINITY ? 0.0f : exp2_approx(top - t), g = exp2_approx(ml.x - t);
+            total = total * f + ml.y * g;
+            sum.x = sum.x * f + y.x * g, sum.y = sum.y * f + y.y * g;
+            top = t;
+          }
+          const float inv = total > 0.0f ? 1.0f / total : (total == total ? 0.0f : total);
+          *reinterpret_cast<uint32_t*>(
+              p.out + ((long long)(w.first + row / G) * p.Hq + w.h * G + row % G) * D + d) =
+              pack_bf16(sum.x * inv, sum.y * inv);
+        }
+      }
+      __syncthreads();
+    }
+  }
+  if (c.dead && threadIdx.x == 0) {  // what is still on its way arrives before the CTA leaves
+    atomicOr(p.err, PE_ERR_TIMEOUT);
+    const unsigned long long t0 = global_ns();
+    while (global_ns() - t0 < kWaitLimitNs) {
+    }
+  }
+}
+
+}  // namespace pe

@@ -1,0 +1,211 @@
+// How an attention call is cut among the CTAs.
+//
+// An item is (request, key head, a block of rows); its units are blocks of
+// kUnit keys.  The units of all items form one line, request after request,
+// and part c of n is units [c U / n, (c + 1) U / n): equal parts whatever the
+// lengths are.  No plan is made on the host, which does not know the lengths:
+// every CTA sums them up for itself.
+#pragma once
+
+#include "pe_attn.cuh"
+
+namespace pe {
+
+constexpr int kTile = 128;        // rows of a stream; keys of a tile
+
+// sum_{i=1..k} ceil(i w / 128)
+__device__ __forceinline__ long long sum_tiles(long long k, long long w) {
+  // sum_{i=0..k-1} floor((a i + b) / m), with ceil(x / 128) = floor((x + 127) / 128)
+  long long n = k, m = kTile, a = w, b = w + kTile - 1, sum = 0;
+  for (;;) {
+    if (a >= m) {
+      sum += (n - 1) * n / 2 * (a / m);
+      a %= m;
+    }
+    if (b >= m) {
+      sum += n * (b / m);
+      b %= m;
+    }
+    const long long y = a * n + b;
+    if (y < m) return sum;
+    n = y / m;
+    b = y % m;
+    const long long t = m;
+    m = a;
+    a = t;
+  }
+}
+
+// How the items of a call are laid on the line of units.  `prefix` and `keys`
+// lie in shared memory.
+template <bool kCached, int kUnit = kTile>
+struct Line {
+  Segments seg;
+  int Hkv, G, span;         // span: tokens of a stream (128 / G)
+  const long long* prefix;  // units before request b; [B] is the total
+  const int* keys;          // kCached: keys of request b
+
+  __device__ bool halves(int rows) const { return kCached && rows <= span; }  // both streams on the same rows
+  __device__ int tokens(int rows) const { return halves(rows) ? span : 2 * span; }  // of an item
+  // units of items 0..k-1 of one (request, head)
+  __device__ long long before(long long k, int rows, int nkeys) const {
+    const int w = tokens(rows);
+    if (kCached) return k * max(1, (nkeys + kUnit - 1) / kUnit);
+    if (k * w <= rows) return sum_tiles(k, w);
+    return (k > 1 ? sum_tiles(k - 1, w) : 0) + (rows + kUnit - 1) / kUnit;
+  }
+  __device__ int items(int rows) const { return (rows + tokens(rows) - 1) / tokens(rows); }
+  __device__ int tiles(int mt, int rows, int nkeys) const {
+    const long long n = kCached ? nkeys : min((long long)rows, (mt + 1LL) * tokens(rows));
+    return (int)max(1LL, (n + kUnit - 1) / kUnit);
+  }
+};
+
+// One CTA's walk over its part of the line.
+struct Walk {
+  int b, h, mt;          // item
+  int t0, t1, tiles;     // its units [t0, t1) of `tiles`
+  int rows, first;       // the request's rows and its first row
+  long long u, end;      // next unit, end of the part
+};
+
+template <bool kCached, int kUnit>
+__device__ __forceinline__ bool walk_next(const Line<kCached, kUnit>& line, Walk& w) {
+  if (w.u >= w.end) return false;
+  w.t0 += w.t1 - w.t0;  // the tile after the last one
+  if (w.t1 >= w.tiles) {
+    w.t0 = 0;
+    if (++w.mt >= line.items(w.rows)) {
+      w.mt = 0;
+      if (++w.h >= line.Hkv) {
+        w.h = 0;
+        do ++w.b;
+        while (line.prefix[w.b + 1] == line.prefix[w.b]);  // u < end: there is one
+        w.first = line.seg.begin(w.b);
+        w.rows = line.seg.end(w.b) - w.first;
+      }
+    }
+    w.tiles = line.tiles(w.mt, w.rows, kCached ? line.keys[w.b] : 0);
+  }
+  w.t1 = (int)min((long long)w.tiles, w.t0 + (w.end - w.u));
+  w.u += w.t1 - w.t0;
+  return true;
+}
+
+// The walk's state before its first segment.
+template <bool kCached, int kUnit>
+__device__ Walk walk_begin(const Line<kCached, kUnit>& line, long long u, long long end) {
+  Walk w;
+  w.u = u, w.end = end;
+  w.b = w.h = w.mt = w.t0 = w.t1 = w.tiles = w.rows = w.first = 0;
+  if (u >= end) return w;
+  int lo = 0, hi = line.seg.B - 1;  // the last b with prefix[b] <= u
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (line.prefix[mid] <= u) lo = mid; else hi = mid - 1;
+  }
+  w.b = lo;  // empty requests share their prefix with the next one, and that one is later
+  w.first = line.seg.begin(w.b);
+  w.rows = line.seg.end(w.b) - w.first;
+  const int nkeys = kCached ? line.keys[w.b] : 0;
+  const long long per_head = (line.prefix[w.b + 1] - line.prefix[w.b]) / line.Hkv;
+  long long r = u - line.prefix[w.b];
+  w.h = (int)(r / per_head);
+  r -= w.h * per_head;
+  lo = 0, hi = line.items(w.rows) - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (line.before(mid, w.rows, nkeys) <= r) lo = mid; else hi = mid - 1;
+  }
+  w.mt = lo;
+  w.tiles = line.tiles(w.mt, w.rows, nkeys);
+  w.t0 = w.t1 = (int)(r - line.before(w.mt, w.rows, nkeys));
+  return w;
+}
+
+// ------------------------------------------------------------------- the plan
+// Every CTA lays the line out for itself (a few loads per request) and finds
+// its part.  False when the offsets are no partition of the rows.
+template <bool kCached, int kUnit, class Control>
+__device__ bool plan(Line<kCached, kUnit>& line, long long min_units, Control& c, long long* prefix, int* keys, long long* sums,
+                     const int32_t* positions, const uint8_t* is_rejected, int table_keys,
+                     uint32_t* err) {
+  const int tid = threadIdx.x, n = blockDim.x, B = line.seg.B;
+  if (line.seg.offsets && !offsets_valid(line.seg.offsets, B, line.seg.T, 0)) {
+    if (tid == 0 && blockIdx.x == 0) atomicOr(err, PE_ERR_OFFSETS);
+    return false;
+  }
+  if (kCached) {  // keys of a request: the most that one of its rows sees
+    int lanes = 1;
+    while (lanes < 32 && 2 * lanes * B <= n) lanes *= 2;
+    const int groups = n / lanes, lane = tid % lanes;
+    for (int b0 = 0; b0 < B; b0 += groups) {
+      const int b = b0 + tid / lanes;
+      int most = 0;
+      bool bad = false;
+      if (b < B) {
+        const int end = line.seg.end(b);
+        for (int t = line.seg.begin(b) + lane; t < end; t += lanes)
+          most = max(most, row_limit(positions, is_rejected, t, table_keys, bad));
+      }
+      for (int d = lanes >> 1; d; d >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, d));
+      if (b < B && lane == 0) keys[b] = most;
+      if (bad && blockIdx.x == 0) atomicOr(err, PE_ERR_BLOCK_RANGE);
+    }
+    __syncthreads();
+  }
+  // inclusive sums: a run of requests per thread, then over the threads
+  const int per = (B + n - 1) / n, b0 = tid * per, b1 = min(B, b0 + per);
+  long long mine = 0;
+  for (int b = b0; b < b1; ++b) {
+    const int rows = line.seg.end(b) - line.seg.begin(b);
+    mine += rows ? line.Hkv * line.before(line.items(rows), rows, kCached ? keys[b] : 0) : 0;
+    prefix[b + 1] = mine;
+  }
+  sums[tid] = mine;
+  __syncthreads();
+  if (tid < 32) {
+    long long run = 0;
+    for (int i0 = 0; i0 < n; i0 += 32) {
+      const long long x = sums[i0 + tid];
+      long long y = x;
+      for (int d = 1; d < 32; d <<= 1) {
+        const long long z = __shfl_up_sync(0xffffffffu, y, d);
+        if (tid >= d) y += z;
+      }
+      sums[i0 + tid] = run + y - x;
+      run += __shfl_sync(0xffffffffu, y, 31);
+    }
+    if (tid == 0) {
+      prefix[0] = 0;
+      c.total = run;
+    }
+  }
+  __syncthreads();
+  for (int b = b0; b < b1; ++b) prefix[b + 1] += sums[tid];
+  __syncthreads();
+  line.prefix = prefix;
+  line.keys = keys;
+  if (tid == 0) {
+    // a part below min_units would spend its time on partial results
+    c.parts = max(1LL, min((long long)gridDim.x, c.total / min_units));
+    const long long part = blockIdx.x;
+    if (part < c.parts)
+      c.start = walk_begin(line, part * c.total / c.parts, (part + 1) * c.total / c.parts);
+    else
+      c.start.u = c.start.end = 0;
+  }
+  __syncthreads();
+  return true;
+}
+
+// The parts that an item reaches over, from the walk after its segment.
+struct Reach {
+  int first, last;
+};
+__device__ __forceinline__ Reach reach(const Walk& w, long long parts, long long total) {
+  const long long u0 = w.u - w.t1, u1 = u0 + w.tiles;  // w.u: the unit after t1
+  return {(int)(((u0 + 1) * parts - 1) / total), (int)((u1 * parts - 1) / total)};
+}
+
+}  // namespace pe

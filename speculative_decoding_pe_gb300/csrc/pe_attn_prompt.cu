@@ -1,98 +1,223 @@
-// Causal attention over whole packed prompts (pe_attn_prompt).
+// Causal attention over whole packed prompts (pe_attn_prompt): the tensor-core
+// attention of pe_attn_mma.cuh with queries, keys and values brought by TMA.
 //
-// One warp per row and query head, one pass over the keys with the running
-// maximum and sum of the softmax; a lane holds D/32 elements.
-#include "pe_attn.cuh"
+// A query tile is the G heads of a key head times 128/G tokens, one 3-axis box;
+// a key tile 128 tokens of one head.  Tiles may reach past a prompt's end into
+// the next prompt, or past the last row (filled with zeros): their scores are
+// masked, and their values must not meet even a weight of zero, because zero
+// times an infinity is a NaN.  So two warps look over the value tiles that any
+// row masks: rows past the prompt are cleared, and elements that are not finite
+// are taken out and given back at the end to the rows that see them.
+#include "pe_attn_mma.cuh"
 
 namespace pe {
 
 struct PromptParams {
   Segments seg;
-  int Hq, Hkv;
-  long long q_row, q_head, k_row, k_head, v_row, v_head;
-  float scale_log2;
-  const uint16_t *q, *k, *v;
-  uint16_t* out;
-  uint32_t* err;
+  int Hkv, G;
+  SoftmaxArgs softmax;
 };
 
-template <int D>
-__global__ void __launch_bounds__(kThreads) attn_prompt_kernel(const PromptParams p) {
-  constexpr int E = D / 32;
-  if (p.seg.offsets && !offsets_valid(p.seg.offsets, p.seg.B, p.seg.T, 0)) {
-    if (threadIdx.x == 0) atomicOr(p.err, PE_ERR_OFFSETS);
-    return;
-  }
-  const int lane = threadIdx.x & 31, G = p.Hq / p.Hkv;
-  const long long nwarps = ((long long)gridDim.x * kThreads) >> 5;
-  for (long long it = ((long long)blockIdx.x * kThreads + threadIdx.x) >> 5;
-       it < (long long)p.seg.T * p.Hq; it += nwarps) {
-    const int t = (int)(it / p.Hq), h = (int)(it - (long long)t * p.Hq), hk = h / G;
-    const int first = p.seg.begin(p.seg.request(t));
-    float q[E], o[E], m = -INFINITY, l = 0.0f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      q[e] = __uint_as_float((uint32_t)p.q[t * p.q_row + h * p.q_head + lane * E + e] << 16) *
-             p.scale_log2;
-      o[e] = 0.0f;
+constexpr int kPromptThreads = 12 * 32;
+constexpr int kGuards = 2;  // warps that look over values
+
+// Query, key and value tiles into shared memory; one thread.
+template <int D, class Control>
+__device__ void bring_tiles(const Line<false>& line, Control& c, uint8_t* smem, const CUtensorMap* qm,
+                            const CUtensorMap* km, const CUtensorMap* vm) {
+  using S = AttnShape<D, false>;
+  volatile int* dead = &c.dead;
+  Walk w = c.start;
+  uint32_t k = 0, nq[2] = {0, 0};
+  const uint32_t q_bytes = line.G * line.span * D * 2;
+  while (walk_next(line, w)) {
+    for (int s = 0; s < 2; ++s) {
+      if (!visits(line, w, s).count) continue;
+      if (!wait_or_dead(&c.q_empty[s], (nq[s]++ & 1) ^ 1, dead)) return;
+      mbar_arrive_expect_tx(&c.q_full[s], q_bytes);
+      for (int x = 0; x < D / 64; ++x)
+        tma_load_3d(smem + S::kQ + s * S::kOperand + x * kTile * 128, qm, 64 * x, w.h * line.G,
+                    w.first + (2 * w.mt + s) * line.span, &c.q_full[s]);
     }
-    for (int j = first; j <= t; ++j) {
-      const uint32_t* k = reinterpret_cast<const uint32_t*>(p.k + j * p.k_row + hk * p.k_head + lane * E);
-      const uint32_t* v = reinterpret_cast<const uint32_t*>(p.v + j * p.v_row + hk * p.v_head + lane * E);
-      float s = 0.0f;
+    for (int j = w.t0; j < w.t1; ++j, ++k) {
+      const uint32_t st = k % S::kStages, phase = (k / S::kStages) & 1;
+      const int row = w.first + j * kTile;
+      if (!wait_or_dead(&c.k_empty[st], phase ^ 1, dead)) return;
+      mbar_arrive_expect_tx(&c.k_full[st], S::kOperand);
+      for (int x = 0; x < D / 64; ++x)
+        tma_load_3d(smem + S::kK + st * S::kOperand + x * kTile * 128, km, 64 * x, w.h, row, &c.k_full[st]);
+      if (!wait_or_dead(&c.v_empty[st], phase ^ 1, dead)) return;
+      mbar_arrive_expect_tx(&c.v_full[st], S::kOperand);
+      for (int x = 0; x < D / 64; ++x)
+        tma_load_3d(smem + S::kV + st * S::kOperand + x * kTile * 128, vm, 64 * x, w.h, row, &c.v_full[st]);
+    }
+  }
+}
+
+// Values on their way to the tensor core; warp `guard` of kGuards.
+template <int D, class Control>
+__device__ void look_over_values(const Line<false>& line, Control& c, uint8_t* smem, int guard) {
+  using S = AttnShape<D, false>;
+  volatile int* dead = &c.dead;
+  const int lane = threadIdx.x & 31;
+  Walk w = c.start;
+  uint32_t k = 0;
+  for (int segment = 0; walk_next(line, w); ++segment) {
+    const int least = 2 * w.mt * line.span + 1;  // keys that the item's first row sees
+    for (int j = w.t0; j < w.t1; ++j, ++k) {
+      const uint32_t st = k % S::kStages;
+      if (!wait_warp(&c.v_full[st], (k / S::kStages) & 1, dead)) return;
+      if ((j + 1) * kTile > least) {
+        uint8_t* tile = smem + S::kV + st * S::kOperand;
+        for (int half = 0; half < 2; ++half) {
+          const int row = (half * kGuards + guard) * 32 + lane, key = j * kTile + row;
+          bool found = false;
+          if (key >= least) {
+            for (int x = 0; x < D / 64; ++x)
 #pragma unroll
-      for (int e = 0; e < E / 2; ++e) s += q[2 * e] * bf16_lo(k[e]) + q[2 * e + 1] * bf16_hi(k[e]);
+              for (int i = 0; i < 8; ++i) {
+                // the lanes take the row's pieces in different orders (banks)
+                uint4* at = reinterpret_cast<uint4*>(tile + x * kTile * 128 + row * 128) + ((i + lane) & 7);
+                if (key >= w.rows) {
+                  *at = make_uint4(0, 0, 0, 0);
+                  continue;
+                }
+                uint4 y = *at;
+                uint32_t* yw = reinterpret_cast<uint32_t*>(&y);
+                bool any = false;
 #pragma unroll
-      for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-      const float mn = fmaxf(m, s), f = exp2f(m - mn), w = exp2f(s - mn);
-      l = l * f + w;
-#pragma unroll
-      for (int e = 0; e < E / 2; ++e) {
-        o[2 * e] = o[2 * e] * f + w * bf16_lo(v[e]);
-        o[2 * e + 1] = o[2 * e + 1] * f + w * bf16_hi(v[e]);
+                for (int e = 0; e < 4; ++e) {
+                  if ((yw[e] & 0x7f80u) == 0x7f80u) yw[e] &= 0xffff0000u, any = true;
+                  if ((yw[e] & 0x7f800000u) == 0x7f800000u) yw[e] &= 0xffffu, any = true;
+                }
+                if (any) *at = y, found = true;
+              }
+          }
+          const uint32_t bits = __ballot_sync(0xffffffffu, found);
+          if (lane == 0)
+            c.not_finite[segment & 7][(j - least / kTile) * 4 + half * kGuards + guard] = bits;
+        }
+        fence_async_shared();
       }
-      m = mn;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&c.v_ready[st]);
     }
-    const float r = 1.0f / l;
-#pragma unroll
-    for (int e = 0; e < E; e += 2)
-      *reinterpret_cast<uint32_t*>(p.out + it * D + lane * E + e) = pack_bf16(o[e] * r, o[e + 1] * r);
   }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kPromptThreads, 1)
+    attn_prompt_kernel(const PromptParams p, const __grid_constant__ CUtensorMap qm,
+                       const __grid_constant__ CUtensorMap km, const __grid_constant__ CUtensorMap vm) {
+  using S = AttnShape<D, false>;
+  extern __shared__ uint8_t raw[];
+  __shared__ AttnControl<S::kStages> c;
+  __shared__ long long sums[kPromptThreads];
+  uint8_t* smem = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
+  long long* prefix = reinterpret_cast<long long*>(smem + S::kData);
+  const int warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) c.init(1, kGuards, 1);
+  Line<false> line{p.seg, p.Hkv, p.G, kTile / p.G, nullptr, nullptr};
+  if (!plan(line, 2, c, prefix, nullptr, sums, nullptr, nullptr, 0, p.softmax.err)) return;
+  if (c.start.u >= c.start.end) return;  // fewer parts than CTAs
+  if (warp == 8) tmem_alloc(&c.tmem, S::kColumns);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp < 8) {
+    softmax_rows<D, false>(line, c, p.softmax, warp >> 2);
+  } else if (warp == 8) {
+    if ((threadIdx.x & 31) == 0) issue_products<D, false>(line, c, smem_addr(smem));
+  } else if (warp == 9) {
+    if ((threadIdx.x & 31) == 0) bring_tiles<D>(line, c, smem, &qm, &km, &vm);
+  } else {
+    look_over_values<D>(line, c, smem, warp - 10);
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (c.dead) leave_after_timeout<D, false>(c, p.softmax.err);
+  if (warp == 8) tmem_dealloc(c.tmem, S::kColumns);
 }
 
 }  // namespace pe
 
+namespace {
+
+// Rows [T, heads, D] as a 3-axis map with boxes of 64 elements x heads x tokens.
+bool encode_rows(CUtensorMap* map, const void* base, int D, int heads, int T, int64_t head, int64_t row,
+                 int box_heads, int box_rows) {
+  using Encode = decltype(&cuTensorMapEncodeTiled);
+  static std::atomic<Encode> cached{nullptr};
+  Encode encode = cached.load(std::memory_order_relaxed);
+  if (!encode) {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) !=
+            cudaSuccess ||
+        found != cudaDriverEntryPointSuccess)
+      return false;
+    encode = reinterpret_cast<Encode>(f);
+    cached.store(encode, std::memory_order_relaxed);
+  }
+  const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)T};
+  // the stride of an axis of one element is never used
+  const cuuint64_t strides[2] = {(cuuint64_t)(heads > 1 ? head : D) * 2, (cuuint64_t)(T > 1 ? row : D) * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_rows};
+  const cuuint32_t steps[3] = {1, 1, 1};
+  return encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, steps,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D>
+int launch(const pe_attn_prompt_args* a, const pe::PromptParams& p, int sms, cudaStream_t s) {
+  CUtensorMap q, k, v;
+  if (!encode_rows(&q, a->q, D, a->Hq, a->T, a->q_head, a->q_row, p.G, pe::kTile / p.G) ||
+      !encode_rows(&k, a->k, D, a->Hkv, a->T, a->k_head, a->k_row, 1, pe::kTile) ||
+      !encode_rows(&v, a->v, D, a->Hkv, a->T, a->v_head, a->v_row, 1, pe::kTile))
+    return PE_ECUDA;
+  static std::atomic<unsigned long long> allowed{0};
+  const int most = pe::AttnShape<D, false>::kData + 1024 + 8 * (PE_MAX_ATTN_B + 1);
+  if (!pe_host::allow_smem(pe::attn_prompt_kernel<D>, most, allowed)) return PE_ECUDA;
+  const int bytes = pe::AttnShape<D, false>::kData + 1024 + 8 * (a->B + 1);
+  const int grid = sms < pe::kAttnCtas ? sms : pe::kAttnCtas;
+  pe::attn_prompt_kernel<D><<<grid, pe::kPromptThreads, bytes, s>>>(p, q, k, v);
+  return pe_host::launch_status();
+}
+
+}  // namespace
+
 extern "C" int pe_attn_prompt(const pe_attn_prompt_args* a, void* stream) {
   if (!a) return PE_EINVAL;
   if (int rc = pe_host::attn_sizes(a->T, a->B, a->Hq, a->Hkv, a->D, a->offsets, a->scale)) return rc;
-  const int64_t strides[] = {a->q_row, a->q_head, a->k_row, a->k_head, a->v_row, a->v_head};
-  for (int64_t s : strides)
-    if (s < 0 || s > INT32_MAX) return PE_EINVAL;
+  const int64_t strides[][2] = {{a->q_row, a->T}, {a->q_head, a->Hq}, {a->k_row, a->T},
+                                {a->k_head, a->Hkv}, {a->v_row, a->T}, {a->v_head, a->Hkv}};
+  for (auto& s : strides)
+    if (s[0] < 0 || s[0] > INT32_MAX || (s[0] == 0 && s[1] > 1)) return PE_EINVAL;
   if (a->T == 0) return PE_OK;
   if (!a->q || !a->k || !a->v || !a->out || !a->workspace || !a->err) return PE_EINVAL;
   if (!pe_host::aligned16(a->q) || !pe_host::aligned16(a->k) || !pe_host::aligned16(a->v) ||
       !pe_host::aligned16(a->out) || !pe_host::aligned16(a->workspace))
     return PE_EALIGN;
-  for (int64_t s : strides)
-    if (s % 8) return PE_EALIGN;
+  for (auto& s : strides)
+    if (s[0] % 8) return PE_EALIGN;
   pe_host::DeviceInfo dev;
   if (pe_host::device_info(&dev) != PE_OK) return PE_ECUDA;
   pe::PromptParams p;
   p.seg = {a->offsets, a->T, a->B};
-  p.Hq = a->Hq, p.Hkv = a->Hkv;
-  p.q_row = a->q_row, p.q_head = a->q_head, p.k_row = a->k_row, p.k_head = a->k_head;
-  p.v_row = a->v_row, p.v_head = a->v_head;
-  p.scale_log2 = a->scale * 1.4426950408889634f;
-  p.q = static_cast<const uint16_t*>(a->q);
-  p.k = static_cast<const uint16_t*>(a->k);
-  p.v = static_cast<const uint16_t*>(a->v);
-  p.out = static_cast<uint16_t*>(a->out);
-  p.err = a->err;
-  const int grid = dev.sm_count * 8;
+  p.Hkv = a->Hkv, p.G = a->Hq / a->Hkv;
+  p.softmax.Hq = a->Hq;
+  p.softmax.table_keys = 0;
+  p.softmax.scale_log2 = a->scale * 1.4426950408889634f;
+  p.softmax.positions = nullptr;
+  p.softmax.is_rejected = nullptr;
+  p.softmax.v = static_cast<const uint16_t*>(a->v);
+  p.softmax.v_row = a->v_row, p.softmax.v_head = a->v_head;
+  p.softmax.out = static_cast<uint16_t*>(a->out);
+  p.softmax.ws = static_cast<uint8_t*>(a->workspace);
+  p.softmax.err = a->err;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (a->D == 64)
-    pe::attn_prompt_kernel<64><<<grid, pe::kThreads, 0, s>>>(p);
-  else
-    pe::attn_prompt_kernel<128><<<grid, pe::kThreads, 0, s>>>(p);
-  return pe_host::launch_status();
+  return a->D == 64 ? launch<64>(a, p, dev.sm_count, s) : launch<128>(a, p, dev.sm_count, s);
 }

@@ -71,7 +71,7 @@ def test_read_refusals(lib, over, rc):
 
 
 COMMON = [
-    (dict(T=-1), EINVAL), (dict(B=0), EINVAL), (dict(B=4097), EINVAL), (dict(Hq=65), EINVAL),
+    (dict(T=-1), EINVAL), (dict(B=0), EINVAL), (dict(B=2049), EINVAL), (dict(Hq=65), EINVAL),
     (dict(Hq=129, Hkv=1), EINVAL), (dict(D=80), EINVAL), (dict(scale=float("nan")), EINVAL),
     (dict(scale=float("inf")), EINVAL), (dict(T=15, B=2, offsets=None), EINVAL),
     (dict(q=None), EINVAL), (dict(out=None), EINVAL), (dict(workspace=None), EINVAL),
