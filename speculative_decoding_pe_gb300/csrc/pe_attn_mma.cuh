@@ -6,8 +6,9 @@
 // once for all of them) and 128 keys at a time:
 //   S = Q K^T (fp32);  m' = max(m, max S);  P = 2^(S scale log2 e - m');
 //   l = l 2^(m - m') + sum P;  O = O 2^(m - m') + P V;  out = O / l.
-// O is rescaled only when the maximum grew by more than 2^8 (any m' within that
-// of the true maximum gives the same quotient; P stays in range).  S, O, m and
+// m need not be the maximum: any m gives the same quotient as long as P stays in
+// range, so it is taken from an item's first tile and then only when a score
+// passes it by more than the type of P holds; O is rarely rescaled.  S, O, m and
 // l are fp32.  P is rounded to the type of V for the product: 2^-9 of each
 // weight on average nothing, at most as much as the rounding of the output.
 //
@@ -21,16 +22,14 @@
 // CTA.  Two streams of 128 rows, one per softmax warpgroup, alternate on the
 // tensor core: while one takes its exponentials, the other's products run.
 // Warps 0-3 and 4-7 hold one row per thread (S and O arrive from TMEM without
-// any exchange between threads), one warp issues the products, the others
-// bring keys and values.
+// any exchange between threads), one warp per stream issues its products, the
+// others bring keys and values.
 #pragma once
 
 #include "pe_attn_line.cuh"
 #include "pe_umma.cuh"
 
 namespace pe {
-
-constexpr float kRescale = 8.0f;  // log2 of how far P may exceed 1
 
 // What one stream does in a segment: its visits, in order.
 struct Visits {
@@ -76,16 +75,25 @@ struct AttnShape {
   static constexpr int kK = 2 * kOperand;
   static constexpr int kV = kK + kStages * kOperand;
   static constexpr int kData = kV + kStages * kOperand;  // bytes, 1024-byte aligned parts
-  // tensor memory: S (P takes its first half) of both streams, then O
+  // Tensor memory: S of both streams, O, and P where there is room (D = 64).
+  // With its own P, S outlives the weights, so the maximum is looked for only when
+  // they turn out too large (D = 64 has as many exponentials as products, and
+  // the softmax is what bounds it), and the next S comes before the products of
+  // P.  For D = 128 P takes the first half of S: the next S comes after the
+  // products of P, which begin with P's first half.
   static constexpr int kColumns = 512;
+  static constexpr bool kOwnP = D == 64;
   __host__ __device__ static constexpr uint32_t s_col(int s) { return s * kTile; }
   __host__ __device__ static constexpr uint32_t o_col(int s) { return 2 * kTile + s * D; }
+  __host__ __device__ static constexpr uint32_t p_col(int s) {
+    return kOwnP ? 2 * kTile + 2 * D + s * (kTile / 2) : s_col(s);
+  }
 };
 
 template <int kStages>
 struct AttnControl {
   uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_ready[kStages], v_empty[kStages];
-  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], pair;
+  uint64_t q_full[2], q_empty[2], s_full[2], p_half[2], p_full[2], o_full[2], pair;
   Walk start;
   long long total, parts;
   uint32_t tmem;
@@ -100,13 +108,14 @@ struct AttnControl {
       mbar_init(&k_full[i], k_count);
       mbar_init(&v_full[i], 1);
       mbar_init(&v_ready[i], v_count);
-      mbar_init(&k_empty[i], 1);
-      mbar_init(&v_empty[i], 1);
+      mbar_init(&k_empty[i], 2);  // both streams
+      mbar_init(&v_empty[i], 2);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&q_full[s], q_count);
       mbar_init(&q_empty[s], 1);
       mbar_init(&s_full[s], 1);
+      mbar_init(&p_half[s], 4);
       mbar_init(&p_full[s], 4);
       mbar_init(&o_full[s], 1);
     }
@@ -117,58 +126,91 @@ struct AttnControl {
 };
 
 // ------------------------------------------------------------------- products
-// The one thread that issues the tensor-core products.
+// The products of stream s: one elected lane of a warp of its own.  (One warp
+// for both streams took 1500 cycles for a visit of each, most of it waiting for
+// its own instructions, and bounded the kernel.)
 template <int D, bool kCached, class Control>
-__device__ void issue_products(const Line<kCached>& line, Control& c, uint32_t smem) {
+__device__ void issue_products(const Line<kCached>& line, Control& c, uint32_t smem, int s) {
   using S = AttnShape<D, kCached>;
   constexpr uint32_t kIdescS = umma_idesc(!kCached, kTile, false);
   constexpr uint32_t kIdescO = umma_idesc(!kCached, D, true);
+  constexpr uint32_t kStep = S::kOperand >> 4;  // of a descriptor's address
   volatile int* dead = &c.dead;
-  const uint32_t tmem = c.tmem;
+  const uint32_t s_tmem = c.tmem + S::s_col(s), o_tmem = c.tmem + S::o_col(s), p_tmem = c.tmem + S::p_col(s);
+  const uint64_t q_desc = umma_desc(smem + S::kQ + s * S::kOperand, 16), k_desc = umma_desc(smem + S::kK, 16);
+  const uint64_t v_desc = umma_desc(smem + S::kV, kTile * 128);
   Walk w = c.start;
-  uint32_t kv0 = 0, np[2] = {0, 0}, nq[2] = {0, 0};
+  uint32_t kv0 = 0, p_phase = 0, q_phase = 0;
   while (walk_next(line, w)) {
-    Visits v[2] = {visits(line, w, 0), visits(line, w, 1)};
-    const bool alone = line.halves(w.rows) || !v[1].count;  // a tile has one user
-
-    auto scores = [&](int s, int i) {
-      const uint32_t k = kv0 + v[s].tile(i) - w.t0, st = k % S::kStages;
-      if (!wait_or_dead(&c.k_full[st], (k / S::kStages) & 1, dead)) return false;
-      tc_fence_after();
-      const uint32_t qa = smem + S::kQ + s * S::kOperand, ka = smem + S::kK + st * S::kOperand;
+    const Visits v = visits(line, w, s);
+    const int tiles = w.t1 - w.t0;
+    uint32_t k = kv0 + v.tile0 - w.t0;  // the visit's tile, of all that the CTA reads
+    // S of the tile k
+    auto scores = [&](uint32_t k, bool last) {
+      const uint32_t st = k % S::kStages;
+      const uint64_t ka = k_desc + st * kStep;
 #pragma unroll
       for (int x = 0; x < D / 16; ++x) {
-        const uint32_t off = (x / 4) * (kTile * 128) + (x % 4) * 32;
-        umma_ss(tmem + S::s_col(s), umma_desc(qa + off, 16), umma_desc(ka + off, 16), kIdescS, x > 0);
+        const uint32_t off = ((x / 4) * (kTile * 128) + (x % 4) * 32) >> 4;
+        umma_ss(s_tmem, q_desc + off, ka + off, kIdescS, x > 0);
       }
       tc_commit(&c.s_full[s]);
-      if (alone || s == 1) tc_commit(&c.k_empty[st]);
-      if (i == v[s].count - 1) tc_commit(&c.q_empty[s]);
+      tc_commit(&c.k_empty[st]);
+      if (last) tc_commit(&c.q_empty[s]);
+    };
+    // O += P V, keys [16 from, 16 to) of the tile k
+    auto values = [&](uint32_t k, int from, int to, bool add) {
+      const uint64_t va = v_desc + (k % S::kStages) * kStep;
+#pragma unroll
+      for (int y = from; y < to; ++y)
+        umma_ts(o_tmem, p_tmem + y * 8, va + (y * 16 * 128 >> 4), kIdescO, add || y > 0);
+    };
+    auto keys_there = [&](uint32_t k) { return wait_or_dead(&c.k_full[k % S::kStages], (k / S::kStages) & 1, dead); };
+    auto values_there = [&](uint32_t k) { return wait_or_dead(&c.v_ready[k % S::kStages], (k / S::kStages) & 1, dead); };
+    // a tile that this stream does not visit (the other one does)
+    auto pass = [&](uint32_t k) {
+      if (!keys_there(k) || !values_there(k)) return false;
+      mbar_arrive(&c.k_empty[k % S::kStages]);
+      mbar_arrive(&c.v_empty[k % S::kStages]);
       return true;
     };
 
-    for (int s = 0; s < 2; ++s)
-      if (v[s].count) {
-        if (!wait_or_dead(&c.q_full[s], nq[s]++ & 1, dead) || !scores(s, 0)) return;
-      }
-    const int n = max(v[0].count, v[1].count);
-    for (int i = 0; i < n; ++i)
-      for (int s = 0; s < 2; ++s) {
-        if (i >= v[s].count) continue;
-        const uint32_t k = kv0 + v[s].tile(i) - w.t0, st = k % S::kStages;
-        if (!wait_or_dead(&c.v_ready[st], (k / S::kStages) & 1, dead)) return;
-        if (!wait_or_dead(&c.p_full[s], np[s]++ & 1, dead)) return;
+    if (v.count) {
+      if (!wait_or_dead(&c.q_full[s], q_phase, dead) || !keys_there(k)) return;
+      q_phase ^= 1;
+      tc_fence_after();
+      scores(k, v.count == 1);
+    }
+#pragma unroll 1
+    for (int i = 0; i < v.count; ++i, k += v.step) {
+      const bool next = i + 1 < v.count;
+      if (next && !keys_there(k + v.step)) return;
+      if (!values_there(k)) return;
+      if (!S::kOwnP) {
+        if (!wait_or_dead(&c.p_half[s], p_phase, dead)) return;
         tc_fence_after();
-        const uint32_t va = smem + S::kV + st * S::kOperand;
-#pragma unroll
-        for (int x = 0; x < kTile / 16; ++x)
-          umma_ts(tmem + S::o_col(s), tmem + S::s_col(s) + x * 8,
-                  umma_desc(va + x * 16 * 128, kTile * 128), kIdescO, i > 0 || x > 0);
-        tc_commit(&c.o_full[s]);
-        if (alone || s == 1) tc_commit(&c.v_empty[st]);
-        if (i + 1 < v[s].count && !scores(s, i + 1)) return;
+        values(k, 0, kTile / 32, i > 0);
       }
-    kv0 += w.t1 - w.t0;
+      if (!wait_or_dead(&c.p_full[s], p_phase, dead)) return;
+      p_phase ^= 1;
+      tc_fence_after();
+      if (S::kOwnP && next) scores(k + v.step, i + 2 == v.count);
+      values(k, S::kOwnP ? 0 : kTile / 32, kTile / 16, i > 0 || !S::kOwnP);
+      tc_commit(&c.o_full[s]);
+      tc_commit(&c.v_empty[k % S::kStages]);
+      if (!S::kOwnP && next) scores(k + v.step, i + 2 == v.count);
+      if (v.step == 2) {  // the other stream's tile of this pair
+        const uint32_t other = s ? k - 1 : k + 1;
+        if (other - kv0 < (uint32_t)tiles && !pass(other)) return;
+      }
+    }
+    if (v.step == 2) {
+      if (s == 1 && (tiles & 1) && !pass(kv0 + tiles - 1)) return;  // stream 0's last
+    } else {
+      for (int j = v.count; j < tiles; ++j)
+        if (!pass(kv0 + j)) return;
+    }
+    kv0 += tiles;
   }
 }
 
@@ -193,31 +235,23 @@ __device__ __forceinline__ float4* partial(uint8_t* ws, int cta, int slot) {
   return reinterpret_cast<float4*>(ws + AttnWorkspace::kPartials +
                                    (3LL * cta + slot) * AttnWorkspace::partial_bytes(D));
 }
+// Of a partial result: a row's (maximum, total).
 template <int D>
-__device__ __forceinline__ void put_partial(float4* to, int row, const float (&o)[D], float m, float l) {
-#pragma unroll
-  for (int d = 0; d < D / 4; ++d)
-    to[d * 256 + row] = make_float4(o[4 * d], o[4 * d + 1], o[4 * d + 2], o[4 * d + 3]);
-  reinterpret_cast<float2*>(to + D / 4 * 256)[row] = make_float2(m, l);
+__device__ __forceinline__ float2* partial_ml(float4* of, int row) {
+  return reinterpret_cast<float2*>(of + D / 4 * 256) + row;
 }
-// (o, m, l) += the partial result.
-template <int D>
-__device__ __forceinline__ void add_partial(const float4* from, int row, float (&o)[D], float& m, float& l) {
-  const float2 ml = __ldcg(reinterpret_cast<const float2*>(from + D / 4 * 256) + row);
-  if (ml.x == -INFINITY) return;  // saw no key
-  const float mn = fmaxf(m, ml.x);
-  const float f = m == -INFINITY ? 0.0f : exp2_approx(m - mn), g = exp2_approx(ml.x - mn);
-  const bool had = m != -INFINITY;
-  l = (had ? l * f : 0.0f) + ml.y * g;
+// The factors by which two results join: of the first, of the second.
+__device__ __forceinline__ float2 join(float& m, float& l, float2 other) {
+  const float mn = fmaxf(m, other.x);  // -infinity: saw no key
+  const float f = m == -INFINITY ? 0.0f : exp2_approx(m - mn);
+  const float g = other.x == -INFINITY ? 0.0f : exp2_approx(other.x - mn);
+  l = (f > 0.0f ? l * f : 0.0f) + (g > 0.0f ? other.y * g : 0.0f);
   m = mn;
-#pragma unroll
-  for (int d = 0; d < D / 4; ++d) {
-    const float4 x = __ldcg(from + d * 256 + row);
-    o[4 * d] = (had ? o[4 * d] * f : 0.0f) + x.x * g;
-    o[4 * d + 1] = (had ? o[4 * d + 1] * f : 0.0f) + x.y * g;
-    o[4 * d + 2] = (had ? o[4 * d + 2] * f : 0.0f) + x.z * g;
-    o[4 * d + 3] = (had ? o[4 * d + 3] * f : 0.0f) + x.w * g;
-  }
+  return make_float2(f, g);
+}
+// x f + y g, where a factor of zero takes its term out whatever it is.
+__device__ __forceinline__ float mix(float x, float f, float y, float g) {
+  return (f > 0.0f ? x * f : 0.0f) + (g > 0.0f ? y * g : 0.0f);
 }
 
 // Both streams' warps; orders their writes.  False: given up.
@@ -232,13 +266,20 @@ __device__ __forceinline__ bool join_streams(Control& c, uint32_t& joins) {
 template <int D, bool kCached, class Control>
 __device__ void softmax_rows(const Line<kCached>& line, Control& c, const SoftmaxArgs& p, int s) {
   using Sh = AttnShape<D, kCached>;
-  // an f16 weight loses its low end below 2^-14: the maximum is held at 2^7 (at
-  // most 2^15 before a rescale), so weights down to 2^-21 of it keep every bit
+  // an f16 weight loses its low end below 2^-14: the maximum is held at 2^7, so
+  // weights down to 2^-21 of it keep every bit
   constexpr float kLift = kCached ? 7.0f : 0.0f;
+  // How far (log2) a score may pass the maximum that is held before the row takes
+  // the new one and O is rescaled: an f16 weight must stay below 65504; bf16
+  // ones, and the sums, have fp32's range.
+  constexpr float kSlack = kCached ? 8.0f : 30.0f;
+  // the same for a tile's weights together
+  constexpr float kMostWeight = kCached ? 32768.0f : 1073741824.0f;
   volatile int* dead = &c.dead;
   const int row = threadIdx.x & (kTile - 1);
   const uint32_t lane_base = c.tmem + ((uint32_t)(row & ~31) << 16);
   const uint32_t s_addr = lane_base + Sh::s_col(s), o_addr = lane_base + Sh::o_col(s);
+  const uint32_t p_addr = lane_base + Sh::p_col(s);
   const int tok = row / line.G, g = row - tok * line.G;
   uint32_t visit = 0, filled = 0, joins = 0;  // visits, segments with visits, joins so far
   int segment = 0;
@@ -249,7 +290,8 @@ __device__ void softmax_rows(const Line<kCached>& line, Control& c, const Softma
     const int from = halves ? 0 : (2 * w.mt + s) * line.span;
     const bool valid = tok < line.span && from + tok < w.rows;
     const int t = w.first + from + tok;
-    // a row that sees nothing computes what it likes and is thrown away
+    // a row that sees nothing computes what it likes and is thrown away;
+    // its weights may overflow, and stay in its own row
     int limit = INT32_MAX;
     bool live = valid;
     if (valid) {
@@ -262,156 +304,241 @@ __device__ void softmax_rows(const Line<kCached>& line, Control& c, const Softma
         limit = from + tok + 1;
       }
     }
-    float m = -INFINITY, l = 0.0f, scale = p.scale_log2;
+    const int least = __reduce_min_sync(0xffffffffu, limit);
+    float m = live ? -INFINITY : 0.0f, l = 0.0f, scale = p.scale_log2;
     for (int i = 0; i < v.count; ++i, ++visit) {
       if (!wait_warp(&c.s_full[s], visit & 1, dead)) return;
       tc_fence_after();
       if (kCached && i == 0) scale = p.scale_log2 * c.row_scale[filled++ & 1][s][row];
       const int key0 = v.tile(i) * kTile;
-      uint32_t x[kTile];
+      // A row takes a maximum in its first tile, and when the weights by the one it
+      // holds grow too large (each row for itself: what it gets does not depend
+      // on its neighbours).  Where P lies on S that has to be known before.
+      bool ask = i == 0 || m == -INFINITY;
+      bool look = !Sh::kOwnP || __any_sync(0xffffffffu, ask);
+      float2 sum[2];
+#pragma unroll 1
+      for (int pass = 0; pass < 2; ++pass) {
+        uint32_t x[kTile];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) tmem_ld32(s_addr + 32 * q, x + 32 * q);
-      tc_wait_ld();
-      if (__any_sync(0xffffffffu, limit < key0 + kTile)) {
-        const int seen = limit - key0;
+        for (int q = 0; q < kTile; q += 32) tmem_ld32(s_addr + q, x + q);
+        tc_wait_ld();
+        if (least < key0 + kTile) {
+          // scores that a row does not see become -infinity, whatever they were
 #pragma unroll
-        for (int q = 0; q < kTile; ++q)
-          if (q >= seen) x[q] = 0xff800000u;  // whatever it was: -infinity
-      }
-      float mx[4];
+          for (int q = 0; q < kTile; q += 32)
+            if (least < key0 + q + 32) {
+              const int seen = limit - key0 - q;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) mx[q] = __uint_as_float(x[q]);
+              for (int r = 0; r < 32; ++r)
+                if (r >= seen) x[q + r] = 0xff800000u;
+            }
+        }
+        if (look) {
+          float mx[8];
 #pragma unroll
-      for (int q = 4; q < kTile - 4; q += 8)
+          for (int r = 0; r < 8; ++r)
+            mx[r] = max3(__uint_as_float(x[r]), __uint_as_float(x[r + 8]), __uint_as_float(x[r + 16]));
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          mx[r] = max3(mx[r], __uint_as_float(x[q + r]), __uint_as_float(x[q + 4 + r]));
+          for (int q = 24; q < kTile - 8; q += 16)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) mx[r] = fmaxf(mx[r], __uint_as_float(x[kTile - 4 + r]));
-      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
-      const bool grew = top > m + kRescale;
-      if (__any_sync(0xffffffffu, grew)) {
-        const float f = grew ? exp2_approx(m - top) : 1.0f;
-        if (grew) m = top;
-        l *= f;
-        if (i > 0) {  // O of the visits before
-          if (!wait_warp(&c.o_full[s], (visit - 1) & 1, dead)) return;
-          tc_fence_after();
+            for (int r = 0; r < 8; ++r)
+              mx[r] = max3(mx[r], __uint_as_float(x[q + r]), __uint_as_float(x[q + 8 + r]));
 #pragma unroll
-          for (int q = 0; q < D; q += 32) {
-            uint32_t o[32];
-            tmem_ld32(o_addr + q, o);
-            tc_wait_ld();
+          for (int r = 0; r < 8; ++r) mx[r] = fmaxf(mx[r], __uint_as_float(x[kTile - 8 + r]));
+          const float top =
+              fmaxf(max3(mx[0], mx[1], mx[2]), max3(max3(mx[3], mx[4], mx[5]), mx[6], mx[7])) * scale;
+          const bool grew = live && top > m + (Sh::kOwnP && ask ? 0.0f : kSlack);
+          if (__any_sync(0xffffffffu, grew)) {
+            const float f = grew ? exp2_approx(m - top) : 1.0f;
+            if (grew) m = top;
+            l *= f;
+            if (i > 0) {  // O of the visits before
+              if (!wait_warp(&c.o_full[s], (visit - 1) & 1, dead)) return;
+              tc_fence_after();
+#pragma unroll 1
+              for (int q = 0; q < D; q += 16) {
+                uint32_t o[16];
+                tmem_ld16(o_addr + q, o);
+                tc_wait_ld();
 #pragma unroll
-            for (int r = 0; r < 32; ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) * f);
-            tmem_st32(o_addr + q, o);
+                for (int r = 0; r < 16; ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) * f);
+                tmem_st16(o_addr + q, o);
+              }
+            }
           }
         }
-      }
-      const float shift = (m == -INFINITY ? 0.0f : -m) + kLift;
-      float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+        const float shift = (m == -INFINITY ? 0.0f : -m) + kLift;
+        sum[0] = sum[1] = make_float2(0.0f, 0.0f);
 #pragma unroll
-      for (int q = 0; q < kTile; q += 32) {
-        uint32_t pk[16];
+        for (int half = 0; half < kTile; half += kTile / 2) {
+          uint32_t pk[32];
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          float2 e = fma2(make_float2(__uint_as_float(x[q + 2 * r]), __uint_as_float(x[q + 2 * r + 1])),
-                          make_float2(scale, scale), make_float2(shift, shift));
-          e.x = exp2_approx(e.x);
-          e.y = exp2_approx(e.y);
-          sum[r & 1] = add2(sum[r & 1], e);
-          pk[r] = kCached ? pack_f16(e.x, e.y) : pack_bf16(e.x, e.y);
+          for (int r = 0; r < 32; ++r) {
+            float2 e = fma2(make_float2(__uint_as_float(x[half + 2 * r]), __uint_as_float(x[half + 2 * r + 1])),
+                            make_float2(scale, scale), make_float2(shift, shift));
+            e.x = exp2_approx(e.x);
+            e.y = exp2_approx(e.y);
+            sum[r & 1] = add2(sum[r & 1], e);
+            pk[r] = kCached ? pack_f16(e.x, e.y) : pack_bf16(e.x, e.y);
+          }
+          if (Sh::kOwnP && half == 0 && i > 0) {  // the products that read the last P
+            if (!wait_warp(&c.o_full[s], (visit - 1) & 1, dead)) return;
+            tc_fence_after();
+          }
+          tmem_st16(p_addr + half / 2, pk);
+          tmem_st16(p_addr + half / 2 + 16, pk + 16);
+          if (!Sh::kOwnP && half == 0) {  // the first half's products may begin
+            tc_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if ((threadIdx.x & 31) == 0) mbar_arrive(&c.p_half[s]);
+          }
         }
-        tmem_st16(s_addr + q / 2, pk);
+        sum[0] = add2(sum[0], sum[1]);
+        if (look) break;
+        ask = live && sum[0].x + sum[0].y > kMostWeight;
+        look = __any_sync(0xffffffffu, ask);
+        if (!look) break;
       }
+      l += sum[0].x + sum[0].y;
       tc_wait_st();
       tc_fence_before();
       __syncwarp();
       if ((threadIdx.x & 31) == 0) mbar_arrive(&c.p_full[s]);
-      l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
     }
-    // ---- the segment's result
-    float o[D];
+    // ---- the segment's result, 32 columns at a time
     if (v.count) {
       if (!wait_warp(&c.o_full[s], (visit - 1) & 1, dead)) return;
       tc_fence_after();
-#pragma unroll
-      for (int q = 0; q < D; q += 32) tmem_ld32(o_addr + q, reinterpret_cast<uint32_t*>(o) + q);
-      tc_wait_ld();
-      tc_fence_before();
-    } else {
-#pragma unroll
-      for (int q = 0; q < D; ++q) o[q] = 0.0f;
     }
     if (!live) m = -INFINITY, l = 0.0f;
-    if (!kCached) {
-      // values that are not finite were taken out of masked tiles (bring_values):
-      // the rows that see them get them back
-      const int first_masked = (2 * w.mt * line.span + 1) / kTile;
-      for (int j = max(w.t0, first_masked); j < w.t0 + v.count; ++j)
-        for (int word = 0; word < 4; ++word) {
-          uint32_t bits = c.not_finite[segment & 7][(j - first_masked) * 4 + word];
-          for (; bits; bits &= bits - 1) {
-            const int key = j * kTile + word * 32 + __ffs(bits) - 1;
-            if (!live || key >= limit) continue;
-            const uint16_t* src = p.v + (w.first + key) * p.v_row + w.h * p.v_head;
+    const bool whole = w.t0 == 0 && w.t1 == w.tiles;
+    const int slot_row = halves ? row : s * kTile + row;
+    auto sums = [&](int q, float(&o)[32]) {
+      if (v.count) {
+        tmem_ld32(o_addr + q, reinterpret_cast<uint32_t*>(o));
+        tc_wait_ld();
+      } else {
 #pragma unroll
-            for (int d = 0; d < D; ++d) {
-              const uint32_t b = src[d];
-              if ((b & 0x7f80u) == 0x7f80u) o[d] += __uint_as_float(b << 16);
+        for (int r = 0; r < 32; ++r) o[r] = 0.0f;
+      }
+      if (!kCached) {
+        // values that are not finite were taken out of masked tiles
+        // (look_over_values): the rows that see them get them back
+        const int first_masked = (2 * w.mt * line.span + 1) / kTile;
+        for (int j = max(w.t0, first_masked); j < w.t0 + v.count; ++j)
+          for (int word = 0; word < 4; ++word) {
+            uint32_t bits = c.not_finite[segment & 7][(j - first_masked) * 4 + word];
+            for (; bits; bits &= bits - 1) {
+              const int key = j * kTile + word * 32 + __ffs(bits) - 1;
+              if (!live || key >= limit) continue;
+              const uint16_t* src = p.v + (w.first + key) * p.v_row + w.h * p.v_head + q;
+#pragma unroll
+              for (int r = 0; r < 32; ++r) {
+                const uint32_t b = src[r];
+                if ((b & 0x7f80u) == 0x7f80u) o[r] += __uint_as_float(b << 16);
+              }
             }
           }
-        }
-    }
-    const bool whole = w.t0 == 0 && w.t1 == w.tiles;
-    bool finish = whole;
-    const int slot_row = halves ? row : s * kTile + row;
-    if (halves) {  // stream 1 hands its half to stream 0
-      float4* x = partial<D>(p.ws, blockIdx.x, 2);
-      const int xr = (segment & 1) * kTile + row;
-      if (s == 1) {
-        put_partial<D>(x, xr, o, m, l);
-        if (!join_streams(c, joins)) return;
-      } else {
-        if (!join_streams(c, joins)) return;
-        add_partial<D>(x, xr, o, m, l);
       }
-    }
-    if (!whole) {
-      const Reach at = reach(w, c.parts, c.total);  // the first part's counter counts
-      const int c0 = at.first, c1 = at.last;
-      if (!halves || s == 0)
-        put_partial<D>(partial<D>(p.ws, blockIdx.x, (int)blockIdx.x == c0), slot_row, o, m, l);
-      if (!join_streams(c, joins)) return;
-      if (threadIdx.x == 0) {
-        unsigned* count = reinterpret_cast<unsigned*>(p.ws) + c0;
-        const unsigned old = atom_add_acq_rel_u32(count, 1);
-        if (old > (unsigned)(c1 - c0)) atomicOr(p.err, PE_ERR_WORKSPACE);
-        c.last[segment & 1] = old == (unsigned)(c1 - c0);
-        if (c.last[segment & 1]) *count = 0;
-      }
-      if (!join_streams(c, joins)) return;
-      finish = c.last[segment & 1] && (!halves || s == 0);
-      if (finish) {
-        m = -INFINITY, l = 0.0f;
+    };
+    auto finish = [&](int q, const float(&o)[32], float inv) {
+      uint4* out = reinterpret_cast<uint4*>(p.out + ((long long)t * p.Hq + w.h * line.G + g) * D + q);
 #pragma unroll
-        for (int q = 0; q < D; ++q) o[q] = 0.0f;
-        for (int part = c0; part <= c1; ++part)
-          add_partial<D>(partial<D>(p.ws, part, part == c0), slot_row, o, m, l);
-      }
-    }
-    if (finish && valid && (!halves || s == 0)) {
-      const float r = l > 0.0f ? 1.0f / l : (l == l ? 0.0f : l);  // no key: zeros; a NaN stays
-      uint4* out = reinterpret_cast<uint4*>(p.out + ((long long)t * p.Hq + w.h * line.G + g) * D);
-#pragma unroll
-      for (int d = 0; d < D / 8; ++d) {
+      for (int d = 0; d < 4; ++d) {
         uint4 y;
         uint32_t* yw = reinterpret_cast<uint32_t*>(&y);
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          yw[e] = live ? pack_bf16(o[8 * d + 2 * e] * r, o[8 * d + 2 * e + 1] * r) : 0u;
+          yw[e] = live ? pack_bf16(o[8 * d + 2 * e] * inv, o[8 * d + 2 * e + 1] * inv) : 0u;
         out[d] = y;
       }
+    };
+    auto inverse = [](float l) { return l > 0.0f ? 1.0f / l : (l == l ? 0.0f : l); };  // no key: zeros
+    float4* half = partial<D>(p.ws, blockIdx.x, 2);
+    const int half_row = (segment & 1) * kTile + row;
+    if (halves && s == 1) {  // stream 1 hands its half to stream 0
+#pragma unroll 1
+      for (int q = 0; q < D; q += 32) {
+        float o[32];
+        sums(q, o);
+#pragma unroll
+        for (int d = 0; d < 8; ++d)
+          half[(q / 4 + d) * 256 + half_row] = make_float4(o[4 * d], o[4 * d + 1], o[4 * d + 2], o[4 * d + 3]);
+      }
+      *partial_ml<D>(half, half_row) = make_float2(m, l);
+      if (!join_streams(c, joins)) return;
+    } else {
+      float2 fg = make_float2(1.0f, 0.0f);
+      if (halves) {
+        if (!join_streams(c, joins)) return;
+        fg = join(m, l, __ldcg(partial_ml<D>(half, half_row)));
+      }
+      const float inv = inverse(l);
+      float4* mine = whole ? nullptr : partial<D>(p.ws, blockIdx.x, (int)blockIdx.x == reach(w, c.parts, c.total).first);
+#pragma unroll 1
+      for (int q = 0; q < D; q += 32) {
+        float o[32];
+        sums(q, o);
+        if (halves) {
+#pragma unroll
+          for (int d = 0; d < 8; ++d) {
+            const float4 x = __ldcg(half + (q / 4 + d) * 256 + half_row);
+            o[4 * d] = mix(o[4 * d], fg.x, x.x, fg.y);
+            o[4 * d + 1] = mix(o[4 * d + 1], fg.x, x.y, fg.y);
+            o[4 * d + 2] = mix(o[4 * d + 2], fg.x, x.z, fg.y);
+            o[4 * d + 3] = mix(o[4 * d + 3], fg.x, x.w, fg.y);
+          }
+        }
+        if (whole) {
+          if (valid) finish(q, o, inv);
+        } else {
+#pragma unroll
+          for (int d = 0; d < 8; ++d)
+            mine[(q / 4 + d) * 256 + slot_row] = make_float4(o[4 * d], o[4 * d + 1], o[4 * d + 2], o[4 * d + 3]);
+        }
+      }
+      if (!whole) *partial_ml<D>(mine, slot_row) = make_float2(m, l);
+    }
+    tc_fence_before();
+    if (whole) continue;
+    // ---- the item is cut: the CTA that comes last adds the parts, in order
+    const Reach at = reach(w, c.parts, c.total);  // the first part's counter counts
+    if (!join_streams(c, joins)) return;
+    if (threadIdx.x == 0) {
+      unsigned* count = reinterpret_cast<unsigned*>(p.ws) + at.first;
+      const unsigned old = atom_add_acq_rel_u32(count, 1), want = at.last - at.first;
+      if (old > want) atomicOr(p.err, PE_ERR_WORKSPACE);
+      c.last[segment & 1] = old == want;
+      if (old == want) *count = 0;
+    }
+    if (!join_streams(c, joins)) return;
+    if (!c.last[segment & 1] || !valid || (halves && s == 1)) continue;
+    m = -INFINITY, l = 0.0f;
+    for (int part = at.first; part <= at.last; ++part)
+      join(m, l, __ldcg(partial_ml<D>(partial<D>(p.ws, part, part == at.first), slot_row)));
+    const float inv = inverse(l);
+#pragma unroll 1
+    for (int q = 0; q < D; q += 32) {
+      float o[32];
+#pragma unroll
+      for (int r = 0; r < 32; ++r) o[r] = 0.0f;
+#pragma unroll 1
+      for (int part = at.first; part <= at.last; ++part) {
+        float4* from = partial<D>(p.ws, part, part == at.first);
+        const float mp = __ldcg(partial_ml<D>(from, slot_row)).x;
+        const float f = mp == -INFINITY ? 0.0f : exp2_approx(mp - m);
+#pragma unroll
+        for (int d = 0; d < 8; ++d) {
+          const float4 x = __ldcg(from + (q / 4 + d) * 256 + slot_row);
+          if (f > 0.0f) {
+            o[4 * d] += x.x * f, o[4 * d + 1] += x.y * f;
+            o[4 * d + 2] += x.z * f, o[4 * d + 3] += x.w * f;
+          }
+        }
+      }
+      finish(q, o, inv);
     }
   }
 }

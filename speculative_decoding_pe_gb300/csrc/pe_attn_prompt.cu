@@ -5,7 +5,7 @@
 // a key tile 128 tokens of one head.  Tiles may reach past a prompt's end into
 // the next prompt, or past the last row (filled with zeros): their scores are
 // masked, and their values must not meet even a weight of zero, because zero
-// times an infinity is a NaN.  So two warps look over the value tiles that any
+// times an infinity is a NaN.  So a warp looks over the value tiles that any
 // row masks: rows past the prompt are cleared, and elements that are not finite
 // are taken out and given back at the end to the rows that see them.
 #include "pe_attn_mma.cuh"
@@ -19,7 +19,6 @@ struct PromptParams {
 };
 
 constexpr int kPromptThreads = 12 * 32;
-constexpr int kGuards = 2;  // warps that look over values
 
 // Query, key and value tiles into shared memory; one thread.
 template <int D, class Control>
@@ -54,9 +53,16 @@ __device__ void bring_tiles(const Line<false>& line, Control& c, uint8_t* smem, 
   }
 }
 
-// Values on their way to the tensor core; warp `guard` of kGuards.
+// 0 x + sum for two bf16.
+__device__ __forceinline__ uint32_t zero_times(uint32_t x, uint32_t sum) {
+  uint32_t d;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(x), "r"(0u), "r"(sum));
+  return d;
+}
+
+// Values on their way to the tensor core; one warp.
 template <int D, class Control>
-__device__ void look_over_values(const Line<false>& line, Control& c, uint8_t* smem, int guard) {
+__device__ void look_over_values(const Line<false>& line, Control& c, uint8_t* smem) {
   using S = AttnShape<D, false>;
   volatile int* dead = &c.dead;
   const int lane = threadIdx.x & 31;
@@ -69,33 +75,42 @@ __device__ void look_over_values(const Line<false>& line, Control& c, uint8_t* s
       if (!wait_warp(&c.v_full[st], (k / S::kStages) & 1, dead)) return;
       if ((j + 1) * kTile > least) {
         uint8_t* tile = smem + S::kV + st * S::kOperand;
-        for (int half = 0; half < 2; ++half) {
-          const int row = (half * kGuards + guard) * 32 + lane, key = j * kTile + row;
+#pragma unroll 1
+        for (int word = 0; word < 4; ++word) {
+          const int row = word * 32 + lane, key = j * kTile + row;
+          // the lanes take a row's pieces in different orders (banks)
+          auto piece = [&](int x, int i) {
+            return reinterpret_cast<uint4*>(tile + x * kTile * 128 + row * 128) + ((i + lane) & 7);
+          };
           bool found = false;
-          if (key >= least) {
+          if (key >= w.rows) {
+#pragma unroll
+            for (int x = 0; x < D / 64; ++x)
+#pragma unroll
+              for (int i = 0; i < 8; ++i) *piece(x, i) = make_uint4(0, 0, 0, 0);
+          } else if (key >= least) {
+            uint32_t sum[4] = {0, 0, 0, 0};  // zero times the elements: a NaN if one is not finite
+#pragma unroll
             for (int x = 0; x < D / 64; ++x)
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
-                // the lanes take the row's pieces in different orders (banks)
-                uint4* at = reinterpret_cast<uint4*>(tile + x * kTile * 128 + row * 128) + ((i + lane) & 7);
-                if (key >= w.rows) {
-                  *at = make_uint4(0, 0, 0, 0);
-                  continue;
-                }
-                uint4 y = *at;
-                uint32_t* yw = reinterpret_cast<uint32_t*>(&y);
-                bool any = false;
-#pragma unroll
+                const uint4 y = *piece(x, i);
+                sum[0] = zero_times(y.x, sum[0]), sum[1] = zero_times(y.y, sum[1]);
+                sum[2] = zero_times(y.z, sum[2]), sum[3] = zero_times(y.w, sum[3]);
+              }
+            found = ((sum[0] | sum[1] | sum[2] | sum[3]) & 0x7fff7fffu) != 0;
+            if (found)
+#pragma unroll 1
+              for (int i = 0; i < D / 8; ++i) {
+                uint32_t* y = reinterpret_cast<uint32_t*>(piece(i / 8, i % 8));
                 for (int e = 0; e < 4; ++e) {
-                  if ((yw[e] & 0x7f80u) == 0x7f80u) yw[e] &= 0xffff0000u, any = true;
-                  if ((yw[e] & 0x7f800000u) == 0x7f800000u) yw[e] &= 0xffffu, any = true;
+                  if ((y[e] & 0x7f80u) == 0x7f80u) y[e] &= 0xffff0000u;
+                  if ((y[e] & 0x7f800000u) == 0x7f800000u) y[e] &= 0xffffu;
                 }
-                if (any) *at = y, found = true;
               }
           }
           const uint32_t bits = __ballot_sync(0xffffffffu, found);
-          if (lane == 0)
-            c.not_finite[segment & 7][(j - least / kTile) * 4 + half * kGuards + guard] = bits;
+          if (lane == 0) c.not_finite[segment & 7][(j - least / kTile) * 4 + word] = bits;
         }
         fence_async_shared();
       }
@@ -116,7 +131,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   uint8_t* smem = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
   long long* prefix = reinterpret_cast<long long*>(smem + S::kData);
   const int warp = threadIdx.x >> 5;
-  if (threadIdx.x == 0) c.init(1, kGuards, 1);
+  if (threadIdx.x == 0) c.init(1, 1, 1);
   Line<false> line{p.seg, p.Hkv, p.G, kTile / p.G, nullptr, nullptr};
   if (!plan(line, 2, c, prefix, nullptr, sums, nullptr, nullptr, 0, p.softmax.err)) return;
   if (c.start.u >= c.start.end) return;  // fewer parts than CTAs
@@ -124,14 +139,19 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  // 12 warps of 168 registers: 200 for the softmax's rows, 104 for the others
+  if (warp < 8)
+    take_registers<200>();
+  else
+    give_registers<104>();
   if (warp < 8) {
     softmax_rows<D, false>(line, c, p.softmax, warp >> 2);
-  } else if (warp == 8) {
-    if ((threadIdx.x & 31) == 0) issue_products<D, false>(line, c, smem_addr(smem));
-  } else if (warp == 9) {
-    if ((threadIdx.x & 31) == 0) bring_tiles<D>(line, c, smem, &qm, &km, &vm);
+  } else if (warp < 10) {
+    if (elect_one()) issue_products<D, false>(line, c, smem_addr(smem), warp - 8);
+  } else if (warp == 10) {
+    if (elect_one()) bring_tiles<D>(line, c, smem, &qm, &km, &vm);
   } else {
-    look_over_values<D>(line, c, smem, warp - 10);
+    look_over_values<D>(line, c, smem);
   }
   __syncwarp();
   tc_fence_before();

@@ -12,24 +12,29 @@ namespace pe {
 // Wait for a phase of `bar`; false when it does not come (kWaitLimitNs), or
 // when another wait of this CTA has given up before (*dead): every role then
 // leaves its loop.
-__device__ __forceinline__ bool wait_or_dead(uint64_t* bar, uint32_t parity, volatile int* dead) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const unsigned long long t0 = global_ns();
+__device__ __forceinline__ bool wait_slowly(uint64_t* bar, uint32_t parity, volatile int* dead) {
+  unsigned long long t0 = 0;
   for (;;) {
 #pragma unroll 1
-    for (int i = 0; i < 16; ++i)
+    for (int i = 0; i < 64; ++i)  // the clock is slow to read
       if (mbar_try_wait(bar, parity)) return true;
     if (*dead) return false;
-    if (global_ns() - t0 > kWaitLimitNs) {
+    const unsigned long long t = global_ns();
+    if (t0 == 0) t0 = t;
+    if (t - t0 > kWaitLimitNs) {
       *dead = 1;
       return false;
     }
   }
 }
+__device__ __forceinline__ bool wait_or_dead(uint64_t* bar, uint32_t parity, volatile int* dead) {
+  return mbar_try_wait(bar, parity) || wait_slowly(bar, parity, dead);
+}
 
 // The same for a whole warp, with one answer.
 __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* dead) {
-  return __all_sync(0xffffffffu, wait_or_dead(bar, parity, dead));
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return __all_sync(0xffffffffu, wait_slowly(bar, parity, dead));
 }
 
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
@@ -39,6 +44,17 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
 // Writes of this thread to shared memory become visible to the tensor core and TMA.
 __device__ __forceinline__ void fence_async_shared() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// Registers of this warp's warpgroup, out of those that the CTA was launched
+// with; all four warps call it.
+template <int kRegs>
+__device__ __forceinline__ void give_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void take_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
 
 // --------------------------------------------------------------------- TMA
@@ -91,6 +107,15 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t* r) {
         "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(addr));
 }
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(addr));
+}
 __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
@@ -99,11 +124,6 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
       "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t* r) {
-  tmem_st16(addr, r);
-  tmem_st16(addr + 16, r + 16);
-}
-
 // ------------------------------------------------------------------------ MMA
 // Shared-memory operand: rows of 128 bytes in the 128-byte swizzle, groups of
 // 8 rows 1024 bytes apart.  `lead` is the distance of the next 64 elements
@@ -118,20 +138,29 @@ __host__ __device__ constexpr uint32_t umma_idesc(bool bf16, int n, bool b_along
   return 1u << 4 | (bf16 ? 1u << 7 | 1u << 10 : 0u) | (b_along_n ? 1u << 16 : 0u) |
          (uint32_t)(n / 8) << 17 | (128u / 16) << 24;
 }
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t yes;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(yes));
+  return yes != 0;
+}
+// The value of lane 0, known to the compiler as one value for the warp.
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+
 // D[tmem] (+)= A[smem] B[smem]; 16 elements of K.  One thread.
-__device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      "l"(a), "l"(b), "r"(idesc), "r"(add)
       : "memory");
 }
 // D[tmem] (+)= A[tmem] B[smem].
-__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t add) {
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      "r"(a), "l"(b), "r"(idesc), "r"(add)
       : "memory");
 }
 
