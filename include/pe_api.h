@@ -478,7 +478,7 @@ size_t pe_workspace_bytes_attn(int32_t D);
  * The keys of the rows themselves have to be in the cache (pe_kv_append).
  *  q, out [T,Hq,D] bf16, dense.  offsets [B+1] int32: the segments, as
  *  out_offsets; NULL: T/B rows each.  is_rejected [T] or NULL: none.
- *  scale: finite.  Sums and softmax statistics are fp32.
+ *  scale: finite, above 0.  Sums and softmax statistics are fp32.
  *  err: PE_ERR_OFFSETS (offsets no partition of T: nothing is written);
  *  PE_ERR_BLOCK_RANGE (a position below 0 sees nothing, one past the table
  *  sees the table's keys; the keys of a page outside the cache are left out);

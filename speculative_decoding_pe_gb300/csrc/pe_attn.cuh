@@ -58,7 +58,7 @@ namespace pe_host {
 // The checks that both attention calls share (sizes only).
 inline int attn_sizes(int T, int B, int Hq, int Hkv, int D, const void* offsets, float scale) {
   if (T < 0 || B < 1 || B > PE_MAX_ATTN_B || Hq < 1 || Hkv < 1 || Hq % Hkv ||
-      Hq / Hkv > PE_MAX_ATTN_G || (D != 64 && D != 128) || !isfinite(scale))
+      Hq / Hkv > PE_MAX_ATTN_G || (D != 64 && D != 128) || !isfinite(scale) || !(scale > 0.0f))
     return PE_EINVAL;
   if (!offsets && T % B) return PE_EINVAL;
   if ((int64_t)T * Hq * D > ((int64_t)1 << 40)) return PE_EINVAL;

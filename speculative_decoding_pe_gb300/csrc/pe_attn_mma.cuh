@@ -99,6 +99,7 @@ struct AttnControl {
   uint32_t tmem;
   int dead, last[2];
   uint32_t not_finite[8][12];  // values of a masked tile: tokens that hold an infinity or NaN
+  int any_not_finite[8];       // of a segment
   float row_scale[2][2][kTile];  // kCached, [segment parity]: the power of two taken out of a query row
 
   // Barriers before their first use; one thread.  The counts: arrivals on
@@ -323,7 +324,7 @@ __device__ void softmax_rows(const Line<kCached>& line, Control& c, const Softma
 #pragma unroll
         for (int q = 0; q < kTile; q += 32) tmem_ld32(s_addr + q, x + q);
         tc_wait_ld();
-        if (least < key0 + kTile) {
+        if (__builtin_expect(least < key0 + kTile, 0)) {
           // scores that a row does not see become -infinity, whatever they were
 #pragma unroll
           for (int q = 0; q < kTile; q += 32)
@@ -334,7 +335,7 @@ __device__ void softmax_rows(const Line<kCached>& line, Control& c, const Softma
                 if (r >= seen) x[q + r] = 0xff800000u;
             }
         }
-        if (look) {
+        if (Sh::kOwnP ? __builtin_expect(look, 0) : true) {
           float mx[8];
 #pragma unroll
           for (int r = 0; r < 8; ++r)
@@ -423,7 +424,7 @@ __device__ void softmax_rows(const Line<kCached>& line, Control& c, const Softma
 #pragma unroll
         for (int r = 0; r < 32; ++r) o[r] = 0.0f;
       }
-      if (!kCached) {
+      if (!kCached && __builtin_expect(c.any_not_finite[segment & 7], 0)) {
         // values that are not finite were taken out of masked tiles
         // (look_over_values): the rows that see them get them back
         const int first_masked = (2 * w.mt * line.span + 1) / kTile;

@@ -70,6 +70,8 @@ __device__ void look_over_values(const Line<false>& line, Control& c, uint8_t* s
   uint32_t k = 0;
   for (int segment = 0; walk_next(line, w); ++segment) {
     const int least = 2 * w.mt * line.span + 1;  // keys that the item's first row sees
+    uint32_t any = 0;
+    if (lane == 0) c.any_not_finite[segment & 7] = 0;
     for (int j = w.t0; j < w.t1; ++j, ++k) {
       const uint32_t st = k % S::kStages;
       if (!wait_warp(&c.v_full[st], (k / S::kStages) & 1, dead)) return;
@@ -110,7 +112,11 @@ __device__ void look_over_values(const Line<false>& line, Control& c, uint8_t* s
               }
           }
           const uint32_t bits = __ballot_sync(0xffffffffu, found);
-          if (lane == 0) c.not_finite[segment & 7][(j - least / kTile) * 4 + word] = bits;
+          any |= bits;
+          if (lane == 0) {
+            c.not_finite[segment & 7][(j - least / kTile) * 4 + word] = bits;
+            c.any_not_finite[segment & 7] = any != 0;
+          }
         }
         fence_async_shared();
       }

@@ -73,7 +73,8 @@ def test_read_refusals(lib, over, rc):
 COMMON = [
     (dict(T=-1), EINVAL), (dict(B=0), EINVAL), (dict(B=2049), EINVAL), (dict(Hq=65), EINVAL),
     (dict(Hq=129, Hkv=1), EINVAL), (dict(D=80), EINVAL), (dict(scale=float("nan")), EINVAL),
-    (dict(scale=float("inf")), EINVAL), (dict(T=15, B=2, offsets=None), EINVAL),
+    (dict(scale=float("inf")), EINVAL), (dict(scale=0.0), EINVAL), (dict(scale=-0.125), EINVAL),
+    (dict(T=15, B=2, offsets=None), EINVAL),
     (dict(q=None), EINVAL), (dict(out=None), EINVAL), (dict(workspace=None), EINVAL),
     (dict(err=None), EINVAL), (dict(q=MIS), EALIGN), (dict(out=MIS), EALIGN),
     (dict(workspace=MIS), EALIGN), (dict(T=0, q=None), 0)]
