@@ -42,6 +42,31 @@ __device__ __forceinline__ int row_limit(const int32_t* positions, const uint8_t
   return pos + 1;
 }
 
+// The call over the cache.
+struct CachedParams {
+  Segments seg;
+  int Hq, Hkv, block_size, bt_width, table_keys;
+  long long num_blocks;
+  float scale_log2;
+  const uint16_t* q;
+  const uint8_t* cache;
+  const int32_t* block_table;
+  const int32_t* positions;
+  const uint8_t* is_rejected;
+  uint16_t* out;
+  uint8_t* ws;
+  uint32_t* err;
+};
+
+// The power of two to take out of a row whose largest magnitude is `most`, as
+// (factor, its inverse); the exponents stay those of normal numbers.
+__device__ __forceinline__ float2 row_factor(float most) {
+  uint32_t e = __float_as_uint(most) >> 23;
+  if (most == 0.0f || e >= 255) return make_float2(1.0f, 1.0f);
+  e = min(max(e, 1u), 252u);
+  return make_float2(__uint_as_float((254 - e) << 23), __uint_as_float(e << 23));
+}
+
 // Scratch: one counter per CTA that begins a split item, then three partial
 // results per CTA of up to 256 rows (fp32 sums, maximum and total of a row).
 constexpr int kAttnCtas = 152;

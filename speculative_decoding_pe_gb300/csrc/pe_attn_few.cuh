@@ -28,21 +28,6 @@
 
 namespace pe {
 
-struct CachedParams {
-  Segments seg;
-  int Hq, Hkv, block_size, bt_width, table_keys;
-  long long num_blocks;
-  float scale_log2;
-  const uint16_t* q;
-  const uint8_t* cache;
-  const int32_t* block_table;
-  const int32_t* positions;
-  const uint8_t* is_rejected;
-  uint16_t* out;
-  uint8_t* ws;
-  uint32_t* err;
-};
-
 template <int D>
 struct FewShape {
   static constexpr int kWarps = 8;
@@ -79,15 +64,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 __device__ __forceinline__ uint32_t lo_halves(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x5410); }
 __device__ __forceinline__ uint32_t hi_halves(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x7632); }
 
-// The power of two to take out of a row whose largest magnitude is `most`, as
-// (factor, its inverse); the exponents stay those of normal numbers.
-__device__ __forceinline__ float2 row_factor(float most) {
-  uint32_t e = __float_as_uint(most) >> 23;
-  if (most == 0.0f || e >= 255) return make_float2(1.0f, 1.0f);
-  e = min(max(e, 1u), 252u);
-  return make_float2(__uint_as_float((254 - e) << 23), __uint_as_float(e << 23));
-}
-
 template <int D, int NB>
 __global__ void __launch_bounds__(256, 2) attn_few_kernel(const CachedParams p) {
   using R = Record<D>;
@@ -97,7 +73,6 @@ __global__ void __launch_bounds__(256, 2) attn_few_kernel(const CachedParams p) 
   constexpr int kRec = F::kRecords;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ FewControl c;
-  __shared__ long long sums[256];
   long long* prefix = reinterpret_cast<long long*>(smem + F::kBytes);
   int* keys = reinterpret_cast<int*>(prefix + p.seg.B + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, cc = lane & 3;
@@ -105,7 +80,7 @@ __global__ void __launch_bounds__(256, 2) attn_few_kernel(const CachedParams p) 
   if (threadIdx.x == 0) c.dead = 0;
   mbar_init_fence();
   Line<true, 16> line{p.seg, p.Hkv, p.Hq / p.Hkv, kTile / (p.Hq / p.Hkv), nullptr, nullptr};
-  if (!plan(line, F::kMinRecords, c, prefix, keys, sums, p.positions, p.is_rejected, p.table_keys, p.err))
+  if (!plan(line, F::kMinRecords, c, prefix, keys, reinterpret_cast<long long*>(smem), p.positions, p.is_rejected, p.table_keys, p.err))
     return;
   if (c.start.u >= c.start.end) return;
 

@@ -45,18 +45,19 @@ struct Line {
   const long long* prefix;  // units before request b; [B] is the total
   const int* keys;          // kCached: keys of request b
 
-  __device__ bool halves(int rows) const { return kCached && rows <= span; }  // both streams on the same rows
-  __device__ int tokens(int rows) const { return halves(rows) ? span : 2 * span; }  // of an item
+  // Over the cache an item is one stream's rows, and both streams take it, every
+  // other unit each: a batch of drafts has no more rows.  A prompt's item is two.
+  __device__ int tokens() const { return kCached ? span : 2 * span; }
   // units of items 0..k-1 of one (request, head)
   __device__ long long before(long long k, int rows, int nkeys) const {
-    const int w = tokens(rows);
+    const int w = tokens();
     if (kCached) return k * max(1, (nkeys + kUnit - 1) / kUnit);
     if (k * w <= rows) return sum_tiles(k, w);
     return (k > 1 ? sum_tiles(k - 1, w) : 0) + (rows + kUnit - 1) / kUnit;
   }
-  __device__ int items(int rows) const { return (rows + tokens(rows) - 1) / tokens(rows); }
+  __device__ int items(int rows) const { return (rows + tokens() - 1) / tokens(); }
   __device__ int tiles(int mt, int rows, int nkeys) const {
-    const long long n = kCached ? nkeys : min((long long)rows, (mt + 1LL) * tokens(rows));
+    const long long n = kCached ? nkeys : min((long long)rows, (mt + 1LL) * tokens());
     return (int)max(1LL, (n + kUnit - 1) / kUnit);
   }
 };

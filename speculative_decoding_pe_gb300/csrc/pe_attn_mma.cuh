@@ -9,8 +9,9 @@
 // m need not be the maximum: any m gives the same quotient as long as P stays in
 // range, so it is taken from an item's first tile and then only when a score
 // passes it by more than the type of P holds; O is rarely rescaled.  S, O, m and
-// l are fp32.  P is rounded to the type of V for the product: 2^-9 of each
-// weight on average nothing, at most as much as the rounding of the output.
+// l are fp32.  P is rounded to bf16 for the product, each weight by at most 2^-8
+// of itself however small it is (an f16 would lose the small ones), which is
+// what the output is rounded by.
 //
 // Work.  An item is (request, key head, up to 256 rows); its unit is a tile of
 // 128 keys.  All units of the call are one line that the CTAs cut into equal
@@ -38,7 +39,7 @@ struct Visits {
 };
 template <bool kCached>
 __device__ __forceinline__ Visits visits(const Line<kCached>& line, const Walk& w, int s) {
-  if (line.halves(w.rows)) {  // every other tile
+  if (kCached) {  // every other tile
     const int n = w.t1 - w.t0 - s;
     return {n > 0 ? (n + 1) / 2 : 0, w.t0 + s, 2};
   }
@@ -71,10 +72,12 @@ template <int D, bool kCached>
 struct AttnShape {
   static constexpr int kStages = D == 64 ? 4 : 2;
   static constexpr int kOperand = kTile * D * 2;  // bytes of 128 rows
-  static constexpr int kQ = 0;
-  static constexpr int kK = 2 * kOperand;
+  static constexpr int kQ = 0;                    // (over the cache, of both streams)
+  static constexpr int kK = (kCached ? 1 : 2) * kOperand;
   static constexpr int kV = kK + kStages * kOperand;
-  static constexpr int kData = kV + kStages * kOperand;  // bytes, 1024-byte aligned parts
+  static constexpr int kRaw = kV + kStages * kOperand;  // records as they lie in the cache
+  static constexpr int kRawStages = !kCached ? 0 : D == 64 ? 4 : 2;
+  static constexpr int kData = kRaw + kRawStages * (kTile / 16) * Record<D>::kBytes;
   // Tensor memory: S of both streams, O, and P where there is room (D = 64).
   // With its own P, S outlives the weights, so the maximum is looked for only when
   // they turn out too large (D = 64 has as many exponentials as products, and
@@ -100,17 +103,18 @@ struct AttnControl {
   int dead, last[2];
   uint32_t not_finite[8][12];  // values of a masked tile: tokens that hold an infinity or NaN
   int any_not_finite[8];       // of a segment
-  float row_scale[2][2][kTile];  // kCached, [segment parity]: the power of two taken out of a query row
+  float row_scale[4][kTile];   // kCached, by segment: the power of two taken out of a query row
+  uint32_t tile_ok[16];        // kCached: records of a tile that lie in the cache
 
   // Barriers before their first use; one thread.  The counts: arrivals on
-  // k_full, v_ready and q_full.
-  __device__ void init(int k_count, int v_count, int q_count) {
+  // k_full, v_ready and q_full, and streams that use a tile.
+  __device__ void init(int k_count, int v_count, int q_count, int users) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&k_full[i], k_count);
       mbar_init(&v_full[i], 1);
       mbar_init(&v_ready[i], v_count);
-      mbar_init(&k_empty[i], 2);  // both streams
-      mbar_init(&v_empty[i], 2);
+      mbar_init(&k_empty[i], users);
+      mbar_init(&v_empty[i], users);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&q_full[s], q_count);
@@ -134,11 +138,11 @@ template <int D, bool kCached, class Control>
 __device__ void issue_products(const Line<kCached>& line, Control& c, uint32_t smem, int s) {
   using S = AttnShape<D, kCached>;
   constexpr uint32_t kIdescS = umma_idesc(!kCached, kTile, false);
-  constexpr uint32_t kIdescO = umma_idesc(!kCached, D, true);
+  constexpr uint32_t kIdescO = umma_idesc(true, D, true);
   constexpr uint32_t kStep = S::kOperand >> 4;  // of a descriptor's address
   volatile int* dead = &c.dead;
   const uint32_t s_tmem = c.tmem + S::s_col(s), o_tmem = c.tmem + S::o_col(s), p_tmem = c.tmem + S::p_col(s);
-  const uint64_t q_desc = umma_desc(smem + S::kQ + s * S::kOperand, 16), k_desc = umma_desc(smem + S::kK, 16);
+  const uint64_t q_desc = umma_desc(smem + S::kQ + (kCached ? 0 : s) * S::kOperand, 16), k_desc = umma_desc(smem + S::kK, 16);
   const uint64_t v_desc = umma_desc(smem + S::kV, kTile * 128);
   Walk w = c.start;
   uint32_t kv0 = 0, p_phase = 0, q_phase = 0;
@@ -185,7 +189,6 @@ __device__ void issue_products(const Line<kCached>& line, Control& c, uint32_t s
 #pragma unroll 1
     for (int i = 0; i < v.count; ++i, k += v.step) {
       const bool next = i + 1 < v.count;
-      if (next && !keys_there(k + v.step)) return;
       if (!values_there(k)) return;
       if (!S::kOwnP) {
         if (!wait_or_dead(&c.p_half[s], p_phase, dead)) return;
@@ -195,22 +198,21 @@ __device__ void issue_products(const Line<kCached>& line, Control& c, uint32_t s
       if (!wait_or_dead(&c.p_full[s], p_phase, dead)) return;
       p_phase ^= 1;
       tc_fence_after();
-      if (S::kOwnP && next) scores(k + v.step, i + 2 == v.count);
+      if (S::kOwnP && next) {
+        if (!keys_there(k + v.step)) return;
+        scores(k + v.step, i + 2 == v.count);
+      }
       values(k, S::kOwnP ? 0 : kTile / 32, kTile / 16, i > 0 || !S::kOwnP);
       tc_commit(&c.o_full[s]);
       tc_commit(&c.v_empty[k % S::kStages]);
-      if (!S::kOwnP && next) scores(k + v.step, i + 2 == v.count);
-      if (v.step == 2) {  // the other stream's tile of this pair
-        const uint32_t other = s ? k - 1 : k + 1;
-        if (other - kv0 < (uint32_t)tiles && !pass(other)) return;
+      if (!S::kOwnP && next) {
+        if (!keys_there(k + v.step)) return;
+        scores(k + v.step, i + 2 == v.count);
       }
     }
-    if (v.step == 2) {
-      if (s == 1 && (tiles & 1) && !pass(kv0 + tiles - 1)) return;  // stream 0's last
-    } else {
+    if (!kCached)
       for (int j = v.count; j < tiles; ++j)
         if (!pass(kv0 + j)) return;
-    }
     kv0 += tiles;
   }
 }
@@ -267,28 +269,24 @@ __device__ __forceinline__ bool join_streams(Control& c, uint32_t& joins) {
 template <int D, bool kCached, class Control>
 __device__ void softmax_rows(const Line<kCached>& line, Control& c, const SoftmaxArgs& p, int s) {
   using Sh = AttnShape<D, kCached>;
-  // an f16 weight loses its low end below 2^-14: the maximum is held at 2^7, so
-  // weights down to 2^-21 of it keep every bit
-  constexpr float kLift = kCached ? 7.0f : 0.0f;
   // How far (log2) a score may pass the maximum that is held before the row takes
-  // the new one and O is rescaled: an f16 weight must stay below 65504; bf16
-  // ones, and the sums, have fp32's range.
-  constexpr float kSlack = kCached ? 8.0f : 30.0f;
-  // the same for a tile's weights together
-  constexpr float kMostWeight = kCached ? 32768.0f : 1073741824.0f;
+  // the new one and O is rescaled: weights and sums have fp32's range.
+  constexpr float kSlack = 30.0f;
+  constexpr float kMostWeight = 1073741824.0f;  // the same for a tile's weights together
   volatile int* dead = &c.dead;
   const int row = threadIdx.x & (kTile - 1);
   const uint32_t lane_base = c.tmem + ((uint32_t)(row & ~31) << 16);
   const uint32_t s_addr = lane_base + Sh::s_col(s), o_addr = lane_base + Sh::o_col(s);
   const uint32_t p_addr = lane_base + Sh::p_col(s);
   const int tok = row / line.G, g = row - tok * line.G;
-  uint32_t visit = 0, filled = 0, joins = 0;  // visits, segments with visits, joins so far
+  uint32_t visit = 0, joins = 0;  // visits, joins so far
   int segment = 0;
   Walk w = c.start;
-  for (; walk_next(line, w); ++segment) {
+  uint32_t kv0 = 0;  // tiles before the segment
+  for (; walk_next(line, w); kv0 += w.t1 - w.t0, ++segment) {
     const Visits v = visits(line, w, s);
-    const bool halves = line.halves(w.rows);
-    const int from = halves ? 0 : (2 * w.mt + s) * line.span;
+    constexpr bool halves = kCached;  // both streams have the same rows
+    const int from = (halves ? w.mt : 2 * w.mt + s) * line.span;
     const bool valid = tok < line.span && from + tok < w.rows;
     const int t = w.first + from + tok;
     // a row that sees nothing computes what it likes and is thrown away;
@@ -306,12 +304,23 @@ __device__ void softmax_rows(const Line<kCached>& line, Control& c, const Softma
       }
     }
     const int least = __reduce_min_sync(0xffffffffu, limit);
+    const bool idle = kCached && !__any_sync(0xffffffffu, live);
     float m = live ? -INFINITY : 0.0f, l = 0.0f, scale = p.scale_log2;
     for (int i = 0; i < v.count; ++i, ++visit) {
       if (!wait_warp(&c.s_full[s], visit & 1, dead)) return;
       tc_fence_after();
-      if (kCached && i == 0) scale = p.scale_log2 * c.row_scale[filled++ & 1][s][row];
+      if (kCached && i == 0) scale = p.scale_log2 * c.row_scale[segment & 3][row];
+      if (kCached && idle) {  // every row of the warp is thrown away: P may be anything
+        tc_fence_before();
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) {
+          if (!Sh::kOwnP) mbar_arrive(&c.p_half[s]);
+          mbar_arrive(&c.p_full[s]);
+        }
+        continue;
+      }
       const int key0 = v.tile(i) * kTile;
+      const uint32_t ok = kCached ? c.tile_ok[(kv0 + v.tile(i) - w.t0) & 15] : 0xffu;
       // A row takes a maximum in its first tile, and when the weights by the one it
       // holds grow too large (each row for itself: what it gets does not depend
       // on its neighbours).  Where P lies on S that has to be known before.
@@ -324,15 +333,15 @@ __device__ void softmax_rows(const Line<kCached>& line, Control& c, const Softma
 #pragma unroll
         for (int q = 0; q < kTile; q += 32) tmem_ld32(s_addr + q, x + q);
         tc_wait_ld();
-        if (__builtin_expect(least < key0 + kTile, 0)) {
+        if (__builtin_expect(least < key0 + kTile || ok != 0xffu, 0)) {
           // scores that a row does not see become -infinity, whatever they were
 #pragma unroll
           for (int q = 0; q < kTile; q += 32)
-            if (least < key0 + q + 32) {
+            if (least < key0 + q + 32 || ok != 0xffu) {
               const int seen = limit - key0 - q;
 #pragma unroll
               for (int r = 0; r < 32; ++r)
-                if (r >= seen) x[q + r] = 0xff800000u;
+                if (r >= seen || !(ok >> ((q + r) / 16) & 1)) x[q + r] = 0xff800000u;
             }
         }
         if (Sh::kOwnP ? __builtin_expect(look, 0) : true) {
@@ -369,7 +378,7 @@ __device__ void softmax_rows(const Line<kCached>& line, Control& c, const Softma
             }
           }
         }
-        const float shift = (m == -INFINITY ? 0.0f : -m) + kLift;
+        const float shift = m == -INFINITY ? 0.0f : -m;
         sum[0] = sum[1] = make_float2(0.0f, 0.0f);
 #pragma unroll
         for (int half = 0; half < kTile; half += kTile / 2) {
@@ -381,7 +390,7 @@ __device__ void softmax_rows(const Line<kCached>& line, Control& c, const Softma
             e.x = exp2_approx(e.x);
             e.y = exp2_approx(e.y);
             sum[r & 1] = add2(sum[r & 1], e);
-            pk[r] = kCached ? pack_f16(e.x, e.y) : pack_bf16(e.x, e.y);
+            pk[r] = pack_bf16(e.x, e.y);
           }
           if (Sh::kOwnP && half == 0 && i > 0) {  // the products that read the last P
             if (!wait_warp(&c.o_full[s], (visit - 1) & 1, dead)) return;

@@ -133,13 +133,12 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   using S = AttnShape<D, false>;
   extern __shared__ uint8_t raw[];
   __shared__ AttnControl<S::kStages> c;
-  __shared__ long long sums[kPromptThreads];
   uint8_t* smem = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
   long long* prefix = reinterpret_cast<long long*>(smem + S::kData);
   const int warp = threadIdx.x >> 5;
-  if (threadIdx.x == 0) c.init(1, 1, 1);
+  if (threadIdx.x == 0) c.init(1, 1, 1, 2);
   Line<false> line{p.seg, p.Hkv, p.G, kTile / p.G, nullptr, nullptr};
-  if (!plan(line, 2, c, prefix, nullptr, sums, nullptr, nullptr, 0, p.softmax.err)) return;
+  if (!plan(line, 2, c, prefix, nullptr, reinterpret_cast<long long*>(smem), nullptr, nullptr, 0, p.softmax.err)) return;
   if (c.start.u >= c.start.end) return;  // fewer parts than CTAs
   if (warp == 8) tmem_alloc(&c.tmem, S::kColumns);
   tc_fence_before();
