@@ -3,7 +3,7 @@
 //
 // One warp brings the records of a key tile as they lie in the cache (one bulk
 // copy per record, ahead of their use by the ring of raw tiles), four warps turn
-// codes into operands, one token per thread: code times scale has 6 bits and is
+// key codes into operands and four value codes, one token per thread: code times scale has 6 bits and is
 // exact in f16 and in bf16.  Keys and values have the same layout (128-byte rows of 64 elements,
 // swizzled); the products read values with their contiguous axis along N.
 // Queries become f16 after a power of two is taken out of each row, which the
@@ -14,8 +14,8 @@
 
 namespace pe {
 
-constexpr int kManyThreads = 16 * 32;
-constexpr int kConverters = 4;  // warps
+constexpr int kManyThreads = 20 * 32;
+constexpr int kConverters = 4;  // warps for keys, and as many for values
 
 template <int kRawStages>
 struct RawControl {
@@ -23,78 +23,89 @@ struct RawControl {
   uint32_t ok[kRawStages];  // records that came
 };
 
-// Records into the ring of raw tiles; one warp, a lane per record.
+// Records into the ring of raw tiles; one warp.  A lane looks up the page of one
+// record of the next four tiles while the copies of these four are issued.
 template <int D, class Control, class Raw>
 __device__ void bring_records(const Line<true>& line, Control& c, Raw& raw, const CachedParams& p, uint8_t* smem) {
   using S = AttnShape<D, true>;
   using R = Record<D>;
-  constexpr int kRecords = kTile / 16;
+  constexpr int kRecords = kTile / 16, kAhead = 32 / kRecords;
   volatile int* dead = &c.dead;
   const int lane = threadIdx.x & 31, per_page = p.block_size >> 4;
   Walk w = c.start;
   bool more = walk_next(line, w);
-  int j = w.t0;
-  // the page of this lane's record of the tile ahead
+  int j = w.t0;  // first of the tiles ahead
+  // the page of this lane's record of the tiles ahead
   auto look_up = [&]() {
     const int rec = j * kRecords + lane;
-    if (!more || lane >= kRecords || rec * 16 >= line.keys[w.b]) return -1;
+    if (!more || j + lane / kRecords >= w.t1 || rec * 16 >= line.keys[w.b]) return -1;
     return __ldg(p.block_table + (long long)w.b * p.bt_width + rec / per_page);
   };
-  int page = look_up();
-  for (uint32_t k = 0; more; ++k) {
-    const uint32_t st = k % S::kRawStages;
-    const int rec = j * kRecords + lane, keys = line.keys[w.b], h = w.h;
-    const bool wanted = lane < kRecords && rec * 16 < keys;
-    const bool ok = wanted && page >= 0 && page < p.num_blocks;
-    const int mine = page;
-    if (++j >= w.t1) {
+  int ahead = look_up();
+  for (uint32_t k = 0; more;) {
+    const int page = ahead, rec = j * kRecords + lane, tiles = min(kAhead, w.t1 - j);
+    const bool wanted = lane < tiles * kRecords && rec * 16 < line.keys[w.b];
+    const uint8_t* base = p.cache + ((long long)w.h * per_page + rec % per_page) * R::kBytes;
+    j += tiles;
+    if (j >= w.t1) {
       more = walk_next(line, w);
       j = w.t0;
     }
-    page = look_up();
-    if (!wait_warp(&raw.empty[st], ((k / S::kRawStages) & 1) ^ 1, dead)) return;
-    const uint32_t bits = __ballot_sync(0xffffffffu, ok);
+    ahead = look_up();
+    const bool ok = wanted && page >= 0 && page < p.num_blocks;
     if (wanted && !ok) atomicOr(p.err, PE_ERR_BLOCK_RANGE);
-    if (lane == 0) {
-      raw.ok[st] = bits;
-      mbar_arrive_expect_tx(&raw.full[st], __popc(bits) * R::kBytes);
+    const uint32_t all = __ballot_sync(0xffffffffu, ok);
+    const uint8_t* src = base + (long long)page * p.Hkv * per_page * R::kBytes;
+#pragma unroll 1
+    for (int q = 0; q < tiles; ++q, ++k) {
+      const uint32_t st = k % S::kRawStages;
+      if (!wait_warp(&raw.empty[st], ((k / S::kRawStages) & 1) ^ 1, dead)) return;
+      if (lane == 0) {
+        raw.ok[st] = (all >> (q * kRecords)) & 0xffu;
+        mbar_arrive_expect_tx(&raw.full[st], __popc(raw.ok[st]) * R::kBytes);
+      }
+      __syncwarp();
+      if (ok && lane / kRecords == q)
+        bulk_load(smem + S::kRaw + (st * kRecords + lane % kRecords) * R::kBytes, src, R::kBytes, &raw.full[st]);
     }
-    __syncwarp();
-    if (ok)
-      bulk_load(smem + S::kRaw + (st * kRecords + lane) * R::kBytes,
-                p.cache + (((long long)mine * p.Hkv + h) * per_page + rec % per_page) * R::kBytes, R::kBytes,
-                &raw.full[st]);
   }
 }
 
 // Codes of one token, D elements, into row `row` of an operand tile: as f16 (the
 // keys, next to f16 queries) or as bf16 (the values, next to bf16 weights).
-// Both are exact.  An f16 number becomes bf16 by moving its exponent and mantissa
-// down three bits, which takes 2^112 out of it; the scale puts that back.
+// Both are exact.  Rolled: the roles of this kernel share an instruction cache.
 template <int D, bool kBf16>
-__device__ __forceinline__ void put_codes(uint8_t* tile, int row, const uint32_t (&codes)[D / 8],
-                                          const uint32_t (&scales)[D / 64]) {
+__device__ __forceinline__ void put_codes(uint8_t* tile, int row, const uint8_t* codes, const uint8_t* scales,
+                                          bool valid) {
+#pragma unroll 1
+  for (int i = 0; i < D / 32; ++i) {
+    const uint4 y = reinterpret_cast<const uint4*>(codes)[i];
+    // past the request's keys lies anything, a NaN too (codes are finite)
+    const uint32_t two = valid ? reinterpret_cast<const uint16_t*>(scales)[i] : 0u;
+    const uint32_t s[2] = {e4m3_f16x2(two & 0xffu), e4m3_f16x2(two >> 8)};
+    const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+    uint8_t* to = tile + (i / 2) * kTile * 128 + row * 128;
 #pragma unroll
-  for (int i = 0; i < D / 8; ++i) {  // 8 elements: 16 bytes
-    uint32_t s = e4m3_f16x2((scales[i / 8] >> (8 * (i / 2 % 4))) & 0xffu);
-    if (kBf16) {
-      float lo, hi;
-      f16x2_to_f32(s, lo, hi);
-      lo *= 5192296858534827628530496329220096.0f;  // 2^112
-      s = pack_bf16(lo, lo);
+    for (int q = 0; q < 4; ++q) {  // 8 elements: 16 bytes
+      uint32_t x[4];
+      e2m1x8_f16(w[q], x);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        x[e] = hmul2(x[e], s[q / 2]);
+        if (kBf16) {
+          float lo, hi;
+          f16x2_to_f32(x[e], lo, hi);
+          x[e] = pack_bf16(lo, hi);
+        }
+      }
+      *reinterpret_cast<uint4*>(to + ((((i & 1) * 4 + q) ^ (row & 7)) * 16)) = make_uint4(x[0], x[1], x[2], x[3]);
     }
-    uint32_t x[4];
-    e2m1x8_f16(codes[i], x);
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      x[e] = kBf16 ? mul_bf16x2((x[e] & 0x80008000u) | ((x[e] >> 3) & 0x0fff0fffu), s) : hmul2(x[e], s);
-    *reinterpret_cast<uint4*>(tile + (i / 8) * kTile * 128 + row * 128 + ((i % 8) ^ (row & 7)) * 16) =
-        make_uint4(x[0], x[1], x[2], x[3]);
   }
 }
 
-// Operands from codes and queries; `row`: this thread's row of a tile.
-template <int D, class Control, class Raw>
+// The values of every tile, or its keys and (kKeys) the queries; `row`: this
+// thread's row of a tile.
+template <int D, bool kKeys, class Control, class Raw>
 __device__ void convert_tiles(const Line<true>& line, Control& c, Raw& raw, const CachedParams& p, uint8_t* smem,
                               int row) {
   using S = AttnShape<D, true>;
@@ -102,17 +113,12 @@ __device__ void convert_tiles(const Line<true>& line, Control& c, Raw& raw, cons
   volatile int* dead = &c.dead;
   const int tok = row / line.G, g = row - tok * line.G;
   const bool first_lane = (threadIdx.x & 31) == 0;
-  auto arrive = [&](uint64_t* bar) {
-    fence_async_shared();
-    __syncwarp();
-    if (first_lane) mbar_arrive(bar);
-  };
   Walk w = c.start;
   uint32_t k = 0, used[2] = {0, 0};  // tiles; segments that each stream visited
   bool busy[2] = {false, false};     // it may still read the queries there
   for (int segment = 0; walk_next(line, w); ++segment) {
-    {
-      // ---- queries: this row, its largest element brought to [1, 2)
+    if (kKeys) {
+      // this row's query, its largest element brought to [1, 2)
       const int t = w.mt * line.span + tok;
       const bool valid = tok < line.span && t < w.rows;
       const uint4* src = reinterpret_cast<const uint4*>(
@@ -155,35 +161,20 @@ __device__ void convert_tiles(const Line<true>& line, Control& c, Raw& raw, cons
       const uint32_t st = k % S::kStages, phase = (k / S::kStages) & 1, rst = k % S::kRawStages;
       if (!wait_warp(&raw.full[rst], (k / S::kRawStages) & 1, dead)) return;
       const uint8_t* rec = smem + S::kRaw + (rst * (kTile / 16) + row / 16) * R::kBytes;
-      uint32_t kc[D / 8], vc[D / 8], ks[D / 64], vs[D / 64];
       const int r = row & 15;
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        const uint4 a = reinterpret_cast<const uint4*>(rec + R::kK + r * R::kRow)[i];
-        const uint4 b = reinterpret_cast<const uint4*>(rec + R::kV + r * R::kRow)[i];
-        kc[4 * i] = a.x, kc[4 * i + 1] = a.y, kc[4 * i + 2] = a.z, kc[4 * i + 3] = a.w;
-        vc[4 * i] = b.x, vc[4 * i + 1] = b.y, vc[4 * i + 2] = b.z, vc[4 * i + 3] = b.w;
-      }
-#pragma unroll
-      for (int i = 0; i < D / 64; ++i) {
-        ks[i] = reinterpret_cast<const uint32_t*>(rec + R::kKs + r * R::kScaleRow)[i];
-        vs[i] = reinterpret_cast<const uint32_t*>(rec + R::kVs + r * R::kScaleRow)[i];
-      }
       const uint32_t ok = raw.ok[rst];
-      if (j * kTile + row >= keys || !(ok >> (row / 16) & 1)) {
-        // past the request's keys lies anything, a NaN too; codes are finite
-#pragma unroll
-        for (int i = 0; i < D / 64; ++i) ks[i] = vs[i] = 0;
-      }
+      if (!wait_warp(kKeys ? &c.k_empty[st] : &c.v_empty[st], phase ^ 1, dead)) return;
+      if (kKeys && row == 0)
+        c.tile_ok[k & 15] = ok | ~((1u << min(kTile / 16, (keys - j * kTile + 15) / 16)) - 1) & 0xffu;
+      put_codes<D, !kKeys>(smem + (kKeys ? S::kK : S::kV) + st * S::kOperand, row,
+                           rec + (kKeys ? R::kK : R::kV) + r * R::kRow, rec + (kKeys ? R::kKs : R::kVs) + r * R::kScaleRow,
+                           j * kTile + row < keys && (ok >> (row / 16) & 1));
+      fence_async_shared();
       __syncwarp();
-      if (first_lane) mbar_arrive(&raw.empty[rst]);
-      if (!wait_warp(&c.k_empty[st], phase ^ 1, dead)) return;
-      if (row == 0) c.tile_ok[k & 15] = ok | ~((1u << min(kTile / 16, (keys - j * kTile + 15) / 16)) - 1) & 0xffu;
-      put_codes<D, false>(smem + S::kK + st * S::kOperand, row, kc, ks);
-      arrive(&c.k_full[st]);
-      if (!wait_warp(&c.v_empty[st], phase ^ 1, dead)) return;
-      put_codes<D, true>(smem + S::kV + st * S::kOperand, row, vc, vs);
-      arrive(&c.v_ready[st]);
+      if (first_lane) {
+        mbar_arrive(kKeys ? &c.k_full[st] : &c.v_ready[st]);
+        mbar_arrive(&raw.empty[rst]);
+      }
     }
   }
 }
@@ -201,7 +192,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) attn_many_kernel(const Cached
   if (threadIdx.x == 0) {
     for (int i = 0; i < S::kRawStages; ++i) {
       mbar_init(&raw.full[i], 1);
-      mbar_init(&raw.empty[i], kConverters);
+      mbar_init(&raw.empty[i], 2 * kConverters);
     }
     c.init(kConverters, kConverters, kConverters, 1);
   }
@@ -215,13 +206,14 @@ __global__ void __launch_bounds__(kManyThreads, 1) attn_many_kernel(const Cached
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  // 16 warps of 128 registers: 176 for the softmax's rows, 64 for the products and the loads, 96 for the converters
+  // 20 warps of 96 registers: 112 for the softmax's rows, 80 for the products and
+  // the loads, 88 for the converters
   if (warp < 8)
-    take_registers<176>();
+    take_registers<112>();
   else if (warp < 12)
-    give_registers<64>();
+    give_registers<80>();
   else
-    give_registers<96>();
+    give_registers<88>();
   if (warp < 8) {
     SoftmaxArgs a;
     a.Hq = p.Hq, a.table_keys = p.table_keys, a.scale_log2 = p.scale_log2;
@@ -233,8 +225,10 @@ __global__ void __launch_bounds__(kManyThreads, 1) attn_many_kernel(const Cached
     if (elect_one()) issue_products<D, true>(line, c, smem_addr(smem), warp - 8);
   } else if (warp == 10) {
     bring_records<D>(line, c, raw, p, smem);
+  } else if (warp >= 12 + kConverters) {
+    convert_tiles<D, false>(line, c, raw, p, smem, threadIdx.x - (12 + kConverters) * 32);
   } else if (warp >= 12) {
-    convert_tiles<D>(line, c, raw, p, smem, threadIdx.x - 12 * 32);
+    convert_tiles<D, true>(line, c, raw, p, smem, threadIdx.x - 12 * 32);
   }
   __syncwarp();
   tc_fence_before();

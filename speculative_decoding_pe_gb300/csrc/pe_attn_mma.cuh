@@ -181,34 +181,40 @@ __device__ void issue_products(const Line<kCached>& line, Control& c, uint32_t s
     };
 
     if (v.count) {
-      if (!wait_or_dead(&c.q_full[s], q_phase, dead) || !keys_there(k)) return;
+      if (!wait_or_dead(&c.q_full[s], q_phase, dead)) return;
       q_phase ^= 1;
-      tc_fence_after();
-      scores(k, v.count == 1);
     }
 #pragma unroll 1
-    for (int i = 0; i < v.count; ++i, k += v.step) {
+    for (int i = -1; i < v.count; ++i) {  // P V of visit i, Q K of the next one
       const bool next = i + 1 < v.count;
-      if (!values_there(k)) return;
-      if (!S::kOwnP) {
-        if (!wait_or_dead(&c.p_half[s], p_phase, dead)) return;
+      const uint32_t kn = i < 0 ? k : k + v.step;
+      if (i >= 0) {
+        if (!values_there(k)) return;
+        if (!S::kOwnP) {
+          if (!wait_or_dead(&c.p_half[s], p_phase, dead)) return;
+          tc_fence_after();
+          values(k, 0, kTile / 32, i > 0);
+        }
+        if (!wait_or_dead(&c.p_full[s], p_phase, dead)) return;
+        p_phase ^= 1;
         tc_fence_after();
-        values(k, 0, kTile / 32, i > 0);
       }
-      if (!wait_or_dead(&c.p_full[s], p_phase, dead)) return;
-      p_phase ^= 1;
-      tc_fence_after();
       if (S::kOwnP && next) {
-        if (!keys_there(k + v.step)) return;
-        scores(k + v.step, i + 2 == v.count);
+        if (!keys_there(kn)) return;
+        tc_fence_after();
+        scores(kn, i + 2 == v.count);
       }
-      values(k, S::kOwnP ? 0 : kTile / 32, kTile / 16, i > 0 || !S::kOwnP);
-      tc_commit(&c.o_full[s]);
-      tc_commit(&c.v_empty[k % S::kStages]);
+      if (i >= 0) {
+        values(k, S::kOwnP ? 0 : kTile / 32, kTile / 16, i > 0 || !S::kOwnP);
+        tc_commit(&c.o_full[s]);
+        tc_commit(&c.v_empty[k % S::kStages]);
+      }
       if (!S::kOwnP && next) {
-        if (!keys_there(k + v.step)) return;
-        scores(k + v.step, i + 2 == v.count);
+        if (!keys_there(kn)) return;
+        tc_fence_after();
+        scores(kn, i + 2 == v.count);
       }
+      k = kn;
     }
     if (!kCached)
       for (int j = v.count; j < tiles; ++j)
@@ -272,6 +278,11 @@ __device__ void softmax_rows(const Line<kCached>& line, Control& c, const Softma
   // How far (log2) a score may pass the maximum that is held before the row takes
   // the new one and O is rescaled: weights and sums have fp32's range.
   constexpr float kSlack = 30.0f;
+  // Columns of S in registers at a time.  Over the cache eight warps that convert
+  // codes share the instruction cache with the softmax, and its shorter code is
+  // worth more than fewer loads (b64 drafts: 727 us against 468); a prompt's
+  // softmax is faster unrolled (b8: 2.19 ms against 2.54).
+  constexpr int kCols = kCached ? 64 : kTile;
   constexpr float kMostWeight = 1073741824.0f;  // the same for a tile's weights together
   volatile int* dead = &c.dead;
   const int row = threadIdx.x & (kTile - 1);
@@ -327,35 +338,35 @@ __device__ void softmax_rows(const Line<kCached>& line, Control& c, const Softma
       bool ask = i == 0 || m == -INFINITY;
       bool look = !Sh::kOwnP || __any_sync(0xffffffffu, ask);
       float2 sum[2];
+      // kCols columns of S from q on; scores that a row does not see become
+      // -infinity, whatever they were.
+      auto load = [&](int q, uint32_t(&y)[kCols]) {
+#pragma unroll
+        for (int r = 0; r < kCols; r += 32) tmem_ld32(s_addr + q + r, y + r);
+        tc_wait_ld();
+        if (__builtin_expect(least < key0 + q + kCols || ok != 0xffu, 0)) {
+          const int seen = limit - key0 - q;
+          const uint32_t there = ok >> (q / 16);
+#pragma unroll
+          for (int r = 0; r < kCols; ++r)
+            if (r >= seen || (kCached && !(there >> (r / 16) & 1))) y[r] = 0xff800000u;
+        }
+      };
 #pragma unroll 1
       for (int pass = 0; pass < 2; ++pass) {
-        uint32_t x[kTile];
-#pragma unroll
-        for (int q = 0; q < kTile; q += 32) tmem_ld32(s_addr + q, x + q);
-        tc_wait_ld();
-        if (__builtin_expect(least < key0 + kTile || ok != 0xffu, 0)) {
-          // scores that a row does not see become -infinity, whatever they were
-#pragma unroll
-          for (int q = 0; q < kTile; q += 32)
-            if (least < key0 + q + 32 || ok != 0xffu) {
-              const int seen = limit - key0 - q;
-#pragma unroll
-              for (int r = 0; r < 32; ++r)
-                if (r >= seen || !(ok >> ((q + r) / 16) & 1)) x[q + r] = 0xff800000u;
-            }
-        }
+        uint32_t y[kCols];
+        load(0, y);
         if (Sh::kOwnP ? __builtin_expect(look, 0) : true) {
           float mx[8];
 #pragma unroll
-          for (int r = 0; r < 8; ++r)
-            mx[r] = max3(__uint_as_float(x[r]), __uint_as_float(x[r + 8]), __uint_as_float(x[r + 16]));
+          for (int r = 0; r < 8; ++r) mx[r] = -INFINITY;
+#pragma unroll 1
+          for (int q = 0; q < kTile; q += kCols) {
+            if (q > 0) load(q, y);
 #pragma unroll
-          for (int q = 24; q < kTile - 8; q += 16)
-#pragma unroll
-            for (int r = 0; r < 8; ++r)
-              mx[r] = max3(mx[r], __uint_as_float(x[q + r]), __uint_as_float(x[q + 8 + r]));
-#pragma unroll
-          for (int r = 0; r < 8; ++r) mx[r] = fmaxf(mx[r], __uint_as_float(x[kTile - 8 + r]));
+            for (int r = 0; r < kCols / 2; ++r)
+              mx[r & 7] = max3(mx[r & 7], __uint_as_float(y[r]), __uint_as_float(y[r + kCols / 2]));
+          }
           const float top =
               fmaxf(max3(mx[0], mx[1], mx[2]), max3(max3(mx[3], mx[4], mx[5]), mx[6], mx[7])) * scale;
           const bool grew = live && top > m + (Sh::kOwnP && ask ? 0.0f : kSlack);
@@ -380,29 +391,35 @@ __device__ void softmax_rows(const Line<kCached>& line, Control& c, const Softma
         }
         const float shift = m == -INFINITY ? 0.0f : -m;
         sum[0] = sum[1] = make_float2(0.0f, 0.0f);
+        // the products that read the last P
+        auto p_free = [&]() { return !Sh::kOwnP || i == 0 || wait_warp(&c.o_full[s], (visit - 1) & 1, dead); };
+        if (kCached && !p_free()) return;
+        if (kCols < kTile && look) load(0, y);  // the maximum took it as far as the last columns
+#pragma unroll 1
+        for (int q = 0; q < kTile; q += kCols) {
+          if (q > 0) load(q, y);
 #pragma unroll
-        for (int half = 0; half < kTile; half += kTile / 2) {
-          uint32_t pk[32];
+          for (int half = 0; half < kCols; half += 64) {
+            uint32_t pk[32];
 #pragma unroll
-          for (int r = 0; r < 32; ++r) {
-            float2 e = fma2(make_float2(__uint_as_float(x[half + 2 * r]), __uint_as_float(x[half + 2 * r + 1])),
-                            make_float2(scale, scale), make_float2(shift, shift));
-            e.x = exp2_approx(e.x);
-            e.y = exp2_approx(e.y);
-            sum[r & 1] = add2(sum[r & 1], e);
-            pk[r] = pack_bf16(e.x, e.y);
-          }
-          if (Sh::kOwnP && half == 0 && i > 0) {  // the products that read the last P
-            if (!wait_warp(&c.o_full[s], (visit - 1) & 1, dead)) return;
+            for (int r = 0; r < 32; ++r) {
+              float2 e = fma2(make_float2(__uint_as_float(y[half + 2 * r]), __uint_as_float(y[half + 2 * r + 1])),
+                              make_float2(scale, scale), make_float2(shift, shift));
+              e.x = exp2_approx(e.x);
+              e.y = exp2_approx(e.y);
+              sum[r & 1] = add2(sum[r & 1], e);
+              pk[r] = pack_bf16(e.x, e.y);
+            }
+            if (!kCached && q + half == 0 && !p_free()) return;
             tc_fence_after();
-          }
-          tmem_st16(p_addr + half / 2, pk);
-          tmem_st16(p_addr + half / 2 + 16, pk + 16);
-          if (!Sh::kOwnP && half == 0) {  // the first half's products may begin
-            tc_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if ((threadIdx.x & 31) == 0) mbar_arrive(&c.p_half[s]);
+            tmem_st16(p_addr + (q + half) / 2, pk);
+            tmem_st16(p_addr + (q + half) / 2 + 16, pk + 16);
+            if (!Sh::kOwnP && q + half == 0) {  // the first half's products may begin
+              tc_wait_st();
+              tc_fence_before();
+              __syncwarp();
+              if ((threadIdx.x & 31) == 0) mbar_arrive(&c.p_half[s]);
+            }
           }
         }
         sum[0] = add2(sum[0], sum[1]);
