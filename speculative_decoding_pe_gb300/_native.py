@@ -461,49 +461,77 @@ def latency_floor(ctas: int, hops: int = 0, chain=None, out=None, stream=None):
 
 # ------------------------------------------------ the drafter layer's attention
 
-def _rows(t: torch.Tensor, name: str, T=None, H=None, D=None):
-    """Pointer and strides of [T, heads, D] bf16 rows with dense elements."""
-    if not t.is_cuda or t.dim() != 3:
-        raise ValueError("%s must be a CUDA tensor [T, heads, D]" % name)
-    if t.dtype != torch.bfloat16:
+# These calls are short next to what Python spends on checking their arguments,
+# so each check reads a tensor's properties once.
+
+_BF16 = torch.bfloat16
+
+
+def _raw_stream(stream, t: torch.Tensor) -> int:
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(t.device.index)
+
+
+def _rows(t: torch.Tensor, name: str, shape):
+    """Pointer and strides of bf16 rows [T, heads, D] with dense elements."""
+    if t.shape != shape:
+        raise ValueError("%s must be %s, got %s" % (name, list(shape), list(t.shape)))
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if t.dtype is not _BF16:
         raise TypeError("%s must be bfloat16, got %s" % (name, t.dtype))
-    if t.shape[2] > 1 and t.stride(2) != 1:
+    row, head, elt = t.stride()
+    if elt != 1 and shape[2] > 1:
         raise ValueError("%s must have unit element stride" % name)
-    for axis, n in ((0, T), (1, H), (2, D)):
-        if n is not None and t.shape[axis] != n:
-            raise ValueError("%s must be %s, got %s" % (name, [T, H, D], list(t.shape)))
     # the stride of an axis of one element is never used
-    return (ctypes.c_void_p(t.data_ptr()), t.stride(0) if t.shape[0] > 1 else 0,
-            t.stride(1) if t.shape[1] > 1 else 0)
+    return t.data_ptr(), row if shape[0] > 1 else 0, head if shape[1] > 1 else 0
 
 
-def _dense(t: torch.Tensor | None, name: str, *shape):
+def _heads(t: torch.Tensor, name: str):
+    if t.dim() != 3:
+        raise ValueError("%s must be [T, heads, D]" % name)
+    return t.shape
+
+
+def _dense(t: torch.Tensor | None, name: str, shape):
+    """Pointer of a contiguous bf16 tensor of the given shape."""
     if t is None:
         return None
-    p = _rows(t, name, *shape)[0]
-    if not t.is_contiguous():
-        raise ValueError("%s must be contiguous" % name)
-    return p
+    if t.shape != shape or not t.is_cuda or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous CUDA tensor %s" % (name, list(shape)))
+    if t.dtype is not _BF16:
+        raise TypeError("%s must be bfloat16, got %s" % (name, t.dtype))
+    return t.data_ptr()
 
 
-def _cache(t: torch.Tensor, Hkv=None, D=None):
+def _cache(t: torch.Tensor):
     """Pointer, blocks, block size, heads and head size of a 4-bit cache."""
-    if not t.is_cuda or t.dim() != 4 or t.dtype != torch.uint8 or not t.is_contiguous():
+    if not t.is_cuda or t.dim() != 4 or t.dtype is not torch.uint8 or not t.is_contiguous():
         raise ValueError("cache must be a contiguous uint8 CUDA tensor "
                          "[num_blocks, Hkv, block_size/16, 18*D]")
-    if t.shape[3] % 18 or (Hkv is not None and t.shape[1] != Hkv) or \
-            (D is not None and t.shape[3] != 18 * D):
-        raise ValueError("cache of shape %s does not hold Hkv=%s, D=%s"
-                         % (list(t.shape), Hkv, D))
-    return (ctypes.c_void_p(t.data_ptr()), t.shape[0], 16 * t.shape[2], t.shape[1],
-            t.shape[3] // 18)
+    blocks, Hkv, sub, rec = t.shape
+    if rec % 18:
+        raise ValueError("cache of shape %s does not hold records of 18*D bytes" % list(t.shape))
+    return t.data_ptr(), blocks, 16 * sub, Hkv, rec // 18
 
 
-def _exactly(t: torch.Tensor | None, name: str, dtype, n: int):
-    p = _dev(t, name, dtype, n)
-    if t is not None and t.numel() != n:
-        raise ValueError("%s holds %d elements, needs %d" % (name, t.numel(), n))
-    return p
+def _vector(t: torch.Tensor | None, name: str, dtype, n: int):
+    """Pointer of a contiguous tensor of exactly n elements."""
+    if t is None:
+        return None
+    if t.dtype is not dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if not t.is_cuda or t.numel() != n or not t.is_contiguous():
+        raise ValueError("%s must be a contiguous CUDA tensor of %d elements" % (name, n))
+    return t.data_ptr()
+
+
+def _scratch(workspace, err, D: int):
+    if not workspace.is_cuda or workspace.dtype is not torch.uint8 or \
+            not workspace.is_contiguous() or workspace.numel() < workspace_bytes_attn(D):
+        raise ValueError("workspace must be what new_attn_workspace(%d) gives" % D)
+    return workspace.data_ptr(), _vector(err, "err", torch.int32, 1)
 
 
 def new_kv_cache(num_blocks: int, block_size: int, Hkv: int, D: int, device="cuda") -> torch.Tensor:
@@ -527,40 +555,45 @@ def kv_append(q, k, v, positions, slots, rope, cache, q_out, err, k_out=None, in
     """Rotate q and k by position; write k and v into ``cache`` at ``slots``
     (slot_mapping of the draft batch: -1 writes nothing); q_out (and k_out)
     take the rotated rows."""
-    lib = load()
-    a = KvAppendArgs()
-    a.cache, a.num_blocks, a.block_size, a.Hkv, a.D = _cache(cache)
-    a.T, a.Hq = q.shape[0], q.shape[1] if q.dim() == 3 else 0
-    a.q, a.q_row, a.q_head = _rows(q, "q", a.T, a.Hq, a.D)
-    a.k, a.k_row, a.k_head = _rows(k, "k", a.T, a.Hkv, a.D)
-    a.v, a.v_row, a.v_head = _rows(v, "v", a.T, a.Hkv, a.D)
+    lib = _lib or load()
+    cp, blocks, bs, Hkv, D = _cache(cache)
+    T, Hq, _ = _heads(q, "q")
+    qs, ks = (T, Hq, D), (T, Hkv, D)
+    qp, q_row, q_head = _rows(q, "q", qs)
+    kp, k_row, k_head = _rows(k, "k", ks)
+    vp, v_row, v_head = _rows(v, "v", ks)
     if rope.dim() != 2:
         raise ValueError("rope must be [max_pos, rot_dim]")
-    a.max_pos, a.rot_dim = rope.shape
-    a.rope = _dev(rope, "rope", torch.float32)
-    a.interleaved = int(bool(interleaved))
-    a.positions = _exactly(positions, "positions", torch.int32, a.T)
-    a.slots = _exactly(slots, "slots", torch.int64, a.T)
-    a.q_out = _dense(q_out, "q_out", a.T, a.Hq, a.D)
-    a.k_out = _dense(k_out, "k_out", a.T, a.Hkv, a.D)
-    a.err = _dev(err, "err", torch.int32, 1)
-    _check(lib, lib.pe_kv_append(ctypes.byref(a), _stream(stream)), "pe_kv_append")
+    max_pos, rot = rope.shape
+    a = KvAppendArgs(T, Hq, Hkv, D, bs, rot, 1 if interleaved else 0, max_pos, blocks, q_row, q_head,
+                     k_row, k_head, v_row, v_head, qp, kp, vp,
+                     _vector(positions, "positions", torch.int32, T),
+                     _vector(slots, "slots", torch.int64, T),
+                     _vector(rope, "rope", torch.float32, max_pos * rot), cp,
+                     _dense(q_out, "q_out", qs), _dense(k_out, "k_out", ks),
+                     _vector(err, "err", torch.int32, 1))
+    _check(lib, lib.pe_kv_append(ctypes.byref(a), _raw_stream(stream, q)), "pe_kv_append")
 
 
 def kv_read(cache, slots, k_out, v_out, err, stream=None):
     """The values that ``cache`` holds at ``slots``, as bf16 rows [n, Hkv, D]
     (zeros for slot -1); either output may be None."""
-    lib = load()
+    lib = _lib or load()
     cp, nb, bs, Hkv, D = _cache(cache)
     n = slots.numel()
-    rc = lib.pe_kv_read(cp, nb, bs, Hkv, D, _dev(slots, "slots", torch.int64), n,
-                        _dense(k_out, "k_out", n, Hkv, D), _dense(v_out, "v_out", n, Hkv, D),
-                        _dev(err, "err", torch.int32, 1), _stream(stream))
+    rc = lib.pe_kv_read(cp, nb, bs, Hkv, D, _vector(slots, "slots", torch.int64, n), n,
+                        _dense(k_out, "k_out", (n, Hkv, D)), _dense(v_out, "v_out", (n, Hkv, D)),
+                        _vector(err, "err", torch.int32, 1), _raw_stream(stream, cache))
     _check(lib, rc, "pe_kv_read")
 
 
+_attn_bytes = {}  # by head size: constants of the library
+
+
 def workspace_bytes_attn(D: int) -> int:
-    return int(load().pe_workspace_bytes_attn(D))
+    if D not in _attn_bytes:
+        _attn_bytes[D] = int(load().pe_workspace_bytes_attn(D))
+    return _attn_bytes[D]
 
 
 def new_attn_workspace(D: int, device="cuda") -> torch.Tensor:
@@ -568,55 +601,49 @@ def new_attn_workspace(D: int, device="cuda") -> torch.Tensor:
     return torch.zeros(workspace_bytes_attn(D), dtype=torch.uint8, device=device)
 
 
-def _default_scale(scale, D):
-    return float(scale) if scale is not None else D ** -0.5
-
-
 def attn_cached(q, cache, block_table, offsets, positions, is_rejected, out, workspace, err,
                 scale=None, stream=None):
     """Attention of the packed rows over their requests' cached keys
     (0..positions[t]; rejected rows give zeros).  offsets [B+1], or None for
     equal segments; scale defaults to D**-0.5."""
-    lib = load()
-    a = AttnCachedArgs()
-    a.cache, a.num_blocks, a.block_size, a.Hkv, a.D = _cache(cache)
-    a.T, a.Hq = q.shape[0], q.shape[1] if q.dim() == 3 else 0
-    a.q = _dense(q, "q", a.T, a.Hq, a.D)
-    a.out = _dense(out, "out", a.T, a.Hq, a.D)
+    lib = _lib or load()
+    cp, blocks, bs, Hkv, D = _cache(cache)
+    T, Hq, _ = _heads(q, "q")
+    shape = (T, Hq, D)
     if block_table.dim() != 2:
         raise ValueError("block_table must be [B, width]")
-    a.B, a.bt_width = block_table.shape
-    a.block_table = _dev(block_table, "block_table", torch.int32)
-    a.offsets = _exactly(offsets, "offsets", torch.int32, a.B + 1)
-    a.positions = _exactly(positions, "positions", torch.int32, a.T)
-    a.is_rejected = _exactly(is_rejected, "is_rejected", torch.uint8, a.T)
-    a.scale = _default_scale(scale, a.D)
-    a.workspace = _dev(workspace, "workspace", torch.uint8, workspace_bytes_attn(a.D))
-    a.err = _dev(err, "err", torch.int32, 1)
-    _check(lib, lib.pe_attn_cached(ctypes.byref(a), _stream(stream)), "pe_attn_cached")
+    B, width = block_table.shape
+    ws, ep = _scratch(workspace, err, D)
+    a = AttnCachedArgs(T, B, Hq, Hkv, D, bs, width, D ** -0.5 if scale is None else scale, blocks,
+                       _dense(q, "q", shape), cp,
+                       _vector(block_table, "block_table", torch.int32, B * width),
+                       _vector(offsets, "offsets", torch.int32, B + 1),
+                       _vector(positions, "positions", torch.int32, T),
+                       _vector(is_rejected, "is_rejected", torch.uint8, T),
+                       _dense(out, "out", shape), ws, ep)
+    _check(lib, lib.pe_attn_cached(ctypes.byref(a), _raw_stream(stream, q)), "pe_attn_cached")
 
 
 def attn_prompt(q, k, v, offsets, out, workspace, err, scale=None, B=None, stream=None):
     """Causal attention over packed prompts.  offsets [B+1], or None for B
     equal segments; scale defaults to D**-0.5."""
-    lib = load()
-    a = AttnPromptArgs()
-    if q.dim() != 3 or k.dim() != 3:
-        raise ValueError("q and k must be [T, heads, D]")
-    a.T, a.Hq, a.D = q.shape
-    a.Hkv = k.shape[1]
-    a.q, a.q_row, a.q_head = _rows(q, "q")
-    a.k, a.k_row, a.k_head = _rows(k, "k", a.T, a.Hkv, a.D)
-    a.v, a.v_row, a.v_head = _rows(v, "v", a.T, a.Hkv, a.D)
-    a.out = _dense(out, "out", a.T, a.Hq, a.D)
-    if offsets is None and B is None:
+    lib = _lib or load()
+    shape = _heads(q, "q")
+    T, Hq, D = shape
+    Hkv = _heads(k, "k")[1]
+    qp, q_row, q_head = _rows(q, "q", shape)
+    kp, k_row, k_head = _rows(k, "k", (T, Hkv, D))
+    vp, v_row, v_head = _rows(v, "v", (T, Hkv, D))
+    if offsets is not None:
+        B = offsets.numel() - 1
+    elif B is None:
         raise ValueError("offsets or B is needed")
-    a.B = offsets.numel() - 1 if offsets is not None else B
-    a.offsets = _exactly(offsets, "offsets", torch.int32, a.B + 1)
-    a.scale = _default_scale(scale, a.D)
-    a.workspace = _dev(workspace, "workspace", torch.uint8, workspace_bytes_attn(a.D))
-    a.err = _dev(err, "err", torch.int32, 1)
-    _check(lib, lib.pe_attn_prompt(ctypes.byref(a), _stream(stream)), "pe_attn_prompt")
+    ws, ep = _scratch(workspace, err, D)
+    a = AttnPromptArgs(T, B, Hq, Hkv, D, D ** -0.5 if scale is None else scale, q_row, q_head,
+                       k_row, k_head, v_row, v_head, qp, kp, vp,
+                       _vector(offsets, "offsets", torch.int32, B + 1),
+                       _dense(out, "out", shape), ws, ep)
+    _check(lib, lib.pe_attn_prompt(ctypes.byref(a), _raw_stream(stream, q)), "pe_attn_prompt")
 
 
 def get_tuning() -> dict:

@@ -422,18 +422,22 @@ __global__ void __launch_bounds__(256, 2) attn_few_kernel(const CachedParams p) 
       if (c.last) {
         for (int i = threadIdx.x; i < nrows * (D / 2); i += 256) {
           const int row = i / (D / 2), d = 2 * (i % (D / 2));
+          // first the maximum, then the sums: the loads of eight parts at a time
           float top = -INFINITY, total = 0.0f;
           float2 sum = make_float2(0.0f, 0.0f);
+          auto ml_of = [&](int part) {
+            return __ldcg(reinterpret_cast<const float2*>(slot(part, part == at.first) + 16 * D + 2 * row));
+          };
+#pragma unroll 8
+          for (int part = at.first; part <= at.last; ++part) top = fmaxf(top, ml_of(part).x);
+#pragma unroll 8
           for (int part = at.first; part <= at.last; ++part) {
-            const float* from = slot(part, part == at.first);
-            const float2 ml = __ldcg(reinterpret_cast<const float2*>(from + 16 * D + 2 * row));
-            const float2 y = __ldcg(reinterpret_cast<const float2*>(from + row * D + d));
-            if (ml.x == -INFINITY) continue;
-            const float t = fmaxf(top, ml.x);
-            const float f = top == -INFINITY ? 0.0f : exp2_approx(top - t), g = exp2_approx(ml.x - t);
-            total = total * f + ml.y * g;
-            sum.x = sum.x * f + y.x * g, sum.y = sum.y * f + y.y * g;
-            top = t;
+            const float2 ml = ml_of(part);
+            const float2 y = __ldcg(reinterpret_cast<const float2*>(slot(part, part == at.first) + row * D + d));
+            const bool any = ml.x != -INFINITY;  // the others hold what they like
+            const float f = any ? exp2_approx(ml.x - top) : 0.0f;
+            total += any ? ml.y * f : 0.0f;
+            sum.x += any ? y.x * f : 0.0f, sum.y += any ? y.y * f : 0.0f;
           }
           const float inv = total > 0.0f ? 1.0f / total : (total == total ? 0.0f : total);
           *reinterpret_cast<uint32_t*>(

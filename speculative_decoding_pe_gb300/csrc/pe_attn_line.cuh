@@ -62,6 +62,11 @@ struct Line {
   }
 };
 
+// a / b, in 32 bits where they do (a 64-bit division takes some 500 cycles).
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 // One CTA's walk over its part of the line.
 struct Walk {
   int b, h, mt;          // item
@@ -109,9 +114,9 @@ __device__ Walk walk_begin(const Line<kCached, kUnit>& line, long long u, long l
   w.first = line.seg.begin(w.b);
   w.rows = line.seg.end(w.b) - w.first;
   const int nkeys = kCached ? line.keys[w.b] : 0;
-  const long long per_head = (line.prefix[w.b + 1] - line.prefix[w.b]) / line.Hkv;
+  const long long per_head = quotient(line.prefix[w.b + 1] - line.prefix[w.b], line.Hkv);
   long long r = u - line.prefix[w.b];
-  w.h = (int)(r / per_head);
+  w.h = (int)quotient(r, per_head);
   r -= w.h * per_head;
   lo = 0, hi = line.items(w.rows) - 1;
   while (lo < hi) {
@@ -155,26 +160,35 @@ __device__ bool plan(Line<kCached, kUnit>& line, long long min_units, Control& c
     }
     __syncthreads();
   }
-  // inclusive sums: a run of requests per thread, then over the threads
-  const int per = (B + n - 1) / n, b0 = tid * per, b1 = min(B, b0 + per);
-  long long mine = 0;
-  for (int b = b0; b < b1; ++b) {
+  line.prefix = prefix;
+  line.keys = keys;
+  auto units = [&](int b) {
     const int rows = line.seg.end(b) - line.seg.begin(b);
-    mine += rows ? line.Hkv * line.before(line.items(rows), rows, kCached ? keys[b] : 0) : 0;
-    prefix[b + 1] = mine;
+    return rows ? line.Hkv * line.before(line.items(rows), rows, kCached ? keys[b] : 0) : 0LL;
+  };
+  // sums over the requests: a run of them per thread (per lane of one warp while
+  // there are few), then over the threads
+  const int per = (B + n - 1) / n, used = (B + per - 1) / per;
+  const int b0 = tid * per, b1 = min(B, b0 + per);
+  long long mine = 0;
+  if (used > 32) {
+    for (int b = b0; b < b1; ++b) prefix[b + 1] = mine += units(b);
+    sums[tid] = mine;
+    __syncthreads();
   }
-  sums[tid] = mine;
-  __syncthreads();
   if (tid < 32) {
     long long run = 0;
-    for (int i0 = 0; i0 < n; i0 += 32) {
-      const long long x = sums[i0 + tid];
+    for (int i0 = 0; i0 < used; i0 += 32) {
+      const long long x = used > 32 ? sums[i0 + tid] : b0 < B ? units(b0) : 0;
       long long y = x;
       for (int d = 1; d < 32; d <<= 1) {
         const long long z = __shfl_up_sync(0xffffffffu, y, d);
         if (tid >= d) y += z;
       }
-      sums[i0 + tid] = run + y - x;
+      if (used > 32)
+        sums[i0 + tid] = run + y - x;
+      else if (b0 < B)
+        prefix[b0 + 1] = y;
       run += __shfl_sync(0xffffffffu, y, 31);
     }
     if (tid == 0) {
@@ -182,17 +196,18 @@ __device__ bool plan(Line<kCached, kUnit>& line, long long min_units, Control& c
       c.total = run;
     }
   }
-  __syncthreads();
-  for (int b = b0; b < b1; ++b) prefix[b + 1] += sums[tid];
-  __syncthreads();
-  line.prefix = prefix;
-  line.keys = keys;
+  if (used > 32) {
+    __syncthreads();
+    for (int b = b0; b < b1; ++b) prefix[b + 1] += sums[tid];
+    __syncthreads();
+  }
+  __syncwarp();
   if (tid == 0) {
     // a part below min_units would spend its time on partial results
-    c.parts = max(1LL, min((long long)gridDim.x, c.total / min_units));
+    c.parts = max(1LL, min((long long)gridDim.x, quotient(c.total, min_units)));
     const long long part = blockIdx.x;
     if (part < c.parts)
-      c.start = walk_begin(line, part * c.total / c.parts, (part + 1) * c.total / c.parts);
+      c.start = walk_begin(line, quotient(part * c.total, c.parts), quotient((part + 1) * c.total, c.parts));
     else
       c.start.u = c.start.end = 0;
   }
@@ -206,7 +221,7 @@ struct Reach {
 };
 __device__ __forceinline__ Reach reach(const Walk& w, long long parts, long long total) {
   const long long u0 = w.u - w.t1, u1 = u0 + w.tiles;  // w.u: the unit after t1
-  return {(int)(((u0 + 1) * parts - 1) / total), (int)((u1 * parts - 1) / total)};
+  return {(int)quotient((u0 + 1) * parts - 1, total), (int)quotient(u1 * parts - 1, total)};
 }
 
 }  // namespace pe

@@ -541,31 +541,38 @@ __device__ void softmax_rows(const Line<kCached>& line, Control& c, const Softma
       if (old == want) *count = 0;
     }
     if (!join_streams(c, joins)) return;
-    if (!c.last[segment & 1] || !valid || (halves && s == 1)) continue;
-    m = -INFINITY, l = 0.0f;
+    if (!c.last[segment & 1] || !valid) continue;
+    // All threads of both streams add; where these have the same rows, each takes
+    // half of the columns.  The loads of a part's 32 columns go together, and those
+    // of the next part with them.
+    m = -INFINITY;
+#pragma unroll 4
     for (int part = at.first; part <= at.last; ++part)
-      join(m, l, __ldcg(partial_ml<D>(partial<D>(p.ws, part, part == at.first), slot_row)));
-    const float inv = inverse(l);
+      m = fmaxf(m, __ldcg(partial_ml<D>(partial<D>(p.ws, part, part == at.first), slot_row)).x);
+    const int q0 = halves ? s * (D / 2) : 0;
 #pragma unroll 1
-    for (int q = 0; q < D; q += 32) {
+    for (int q = q0; q < q0 + (halves ? D / 2 : D); q += 32) {
       float o[32];
 #pragma unroll
       for (int r = 0; r < 32; ++r) o[r] = 0.0f;
-#pragma unroll 1
+      l = 0.0f;
+#pragma unroll 2
       for (int part = at.first; part <= at.last; ++part) {
         float4* from = partial<D>(p.ws, part, part == at.first);
-        const float mp = __ldcg(partial_ml<D>(from, slot_row)).x;
-        const float f = mp == -INFINITY ? 0.0f : exp2_approx(mp - m);
+        const float2 ml = __ldcg(partial_ml<D>(from, slot_row));
+        float4 x[8];
+#pragma unroll
+        for (int d = 0; d < 8; ++d) x[d] = __ldcg(from + (q / 4 + d) * 256 + slot_row);
+        const bool any = ml.x != -INFINITY;  // the others hold what they like
+        const float f = any ? exp2_approx(ml.x - m) : 0.0f;
+        l += any ? ml.y * f : 0.0f;
 #pragma unroll
         for (int d = 0; d < 8; ++d) {
-          const float4 x = __ldcg(from + (q / 4 + d) * 256 + slot_row);
-          if (f > 0.0f) {
-            o[4 * d] += x.x * f, o[4 * d + 1] += x.y * f;
-            o[4 * d + 2] += x.z * f, o[4 * d + 3] += x.w * f;
-          }
+          o[4 * d] += any ? x[d].x * f : 0.0f, o[4 * d + 1] += any ? x[d].y * f : 0.0f;
+          o[4 * d + 2] += any ? x[d].z * f : 0.0f, o[4 * d + 3] += any ? x[d].w * f : 0.0f;
         }
       }
-      finish(q, o, inv);
+      finish(q, o, inverse(l));
     }
   }
 }
