@@ -31,7 +31,7 @@ namespace pe {
 template <int D>
 struct FewShape {
   static constexpr int kWarps = 8;
-  static constexpr int kStages = 2;
+  static constexpr int kStages = 2;  // (8 bits of ok_bits each)
   static constexpr int kRecords = 256 / D;                        // of a step
   static constexpr int kStep = kRecords * Record<D>::kBytes;      // 4608 bytes
   static constexpr int kRing = kWarps * kStages * kStep;
@@ -40,12 +40,13 @@ struct FewShape {
   static constexpr int kMinRecords = 16;                          // of a part
 };
 
+template <int kWarps, int kStages>
 struct FewControl {
-  uint64_t full[8][2];
+  uint64_t full[kWarps][kStages];
   Walk start;
   long long total, parts;
   int dead, last;
-  float m[8][16], l[8][16];
+  float m[kWarps][16], l[kWarps][16];
 };
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -61,9 +62,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
-__device__ __forceinline__ uint32_t lo_halves(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x5410); }
-__device__ __forceinline__ uint32_t hi_halves(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x7632); }
-
 template <int D, int NB>
 __global__ void __launch_bounds__(256, 2) attn_few_kernel(const CachedParams p) {
   using R = Record<D>;
@@ -72,7 +70,7 @@ __global__ void __launch_bounds__(256, 2) attn_few_kernel(const CachedParams p) 
   constexpr int kSteps = D / 16;        // products of a record's scores
   constexpr int kRec = F::kRecords;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ FewControl c;
+  __shared__ FewControl<F::kWarps, F::kStages> c;
   long long* prefix = reinterpret_cast<long long*>(smem + F::kBytes);
   int* keys = reinterpret_cast<int*>(prefix + p.seg.B + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, cc = lane & 3;
@@ -93,45 +91,52 @@ __global__ void __launch_bounds__(256, 2) attn_few_kernel(const CachedParams p) 
   auto order = [&](int i) { return (int)(kOrder >> (4 * i)) & 15; };
   const int key_tok = order(r), val_a = order(2 * cc), val_b = order(2 * cc + 1);
 
-  // ---- the loader: pages one step ahead of the copies, copies kStages ahead
+  // ---- the loader: this warp's records in batches of 32, a lane for each; the
+  // pages of the next batch are looked up while this one's copies are issued
   Walk lw = c.start;
-  int lpos = 0, lend = 0, page = -1, ln = 0, lrec = 0, lh = 0;
-  bool more = true;
+  int lpos = 0, lend = 0;                       // what is left of the warp's share of lw
+  int next_n = 0, next_rec = 0, page = -1;      // the next batch; page: this lane's
+  int cur = 0, batch = 0;                       // the batch at hand: issued, in all
+  uint32_t batch_ok = 0;
+  const uint8_t* src = nullptr;                 // this lane's record
   uint32_t issued = 0, taken = 0, ok_bits = 0;
-  auto next_pages = [&]() {  // the step after the one just issued: its pages' ids
-    while (more && lpos >= lend) {
-      more = walk_next(line, lw);
-      if (!more) break;
+  auto look_up = [&]() {
+    next_n = 0;
+    while (lpos >= lend) {
+      if (!walk_next(line, lw)) return;
       const int n = lw.t1 - lw.t0;
-      lpos = lw.t0 + (int)((long long)n * warp / F::kWarps);
-      lend = lw.t0 + (int)((long long)n * (warp + 1) / F::kWarps);
+      lpos = lw.t0 + n * warp / F::kWarps;
+      lend = lw.t0 + n * (warp + 1) / F::kWarps;
     }
-    ln = 0;
-    if (!more) return;
-    ln = min(kRec, lend - lpos);
-    lrec = lpos, lh = lw.h;
+    next_n = min(32, lend - lpos);
+    next_rec = lpos + lane;
     page = -1;
-    if (lane < ln && (lrec + lane) * 16 < max(1, keys[lw.b]))
-      page = __ldg(p.block_table + (long long)lw.b * p.bt_width + (lrec + lane) / per_page);
-    lpos += ln;
+    if (lane < next_n && next_rec * 16 < keys[lw.b])
+      page = __ldg(p.block_table + (long long)lw.b * p.bt_width + next_rec / per_page);
+    lpos += next_n;
   };
-  auto issue = [&]() {
-    if (!ln) return;
+  auto issue = [&]() {  // the copies of one step
+    if (cur >= batch) {
+      if (!next_n) return;
+      const bool ok = page >= 0 && page < p.num_blocks;
+      if (!ok && lane < next_n && next_rec * 16 < keys[lw.b]) atomicOr(p.err, PE_ERR_BLOCK_RANGE);
+      batch_ok = __ballot_sync(0xffffffffu, ok && lane < next_n);
+      src = p.cache + (((long long)page * p.Hkv + lw.h) * per_page + next_rec % per_page) * R::kBytes;
+      cur = 0, batch = next_n;
+      look_up();
+    }
     const uint32_t st = issued % F::kStages;
-    const bool ok = lane < ln && page >= 0 && page < p.num_blocks;
-    const uint32_t bits = __ballot_sync(0xffffffffu, ok);
+    const uint32_t bits = (batch_ok >> cur) & ((1u << kRec) - 1);
     ok_bits = (ok_bits & ~(0xffu << (8 * st))) | bits << (8 * st);
     if (lane == 0) mbar_arrive_expect_tx(&c.full[warp][st], __popc(bits) * R::kBytes);
     __syncwarp();
-    if (ok)
-      bulk_load(ring + st * F::kStep + lane * R::kBytes,
-                p.cache + (((long long)page * p.Hkv + lh) * per_page + (lrec + lane) % per_page) * R::kBytes,
-                R::kBytes, &c.full[warp][st]);
+    if (lane >= cur && lane < cur + kRec && (batch_ok >> lane & 1))
+      bulk_load(ring + st * F::kStep + (lane - cur) * R::kBytes, src, R::kBytes, &c.full[warp][st]);
+    cur += kRec;
     ++issued;
-    next_pages();
   };
-  next_pages();
-#pragma unroll
+  look_up();
+#pragma unroll 1
   for (int i = 0; i < F::kStages; ++i) issue();
 
   Walk w = c.start;
@@ -189,8 +194,8 @@ __global__ void __launch_bounds__(256, 2) attn_few_kernel(const CachedParams p) 
 
     // ---- this warp's records
     const int n = w.t1 - w.t0;
-    int pos = w.t0 + (int)((long long)n * warp / F::kWarps);
-    const int end = w.t0 + (int)((long long)n * (warp + 1) / F::kWarps);
+    int pos = w.t0 + n * warp / F::kWarps;
+    const int end = w.t0 + n * (warp + 1) / F::kWarps;
     while (pos < end) {
       const int cnt = min(kRec, end - pos);
       const uint32_t st = taken % F::kStages;
@@ -218,9 +223,8 @@ __global__ void __launch_bounds__(256, 2) attn_few_kernel(const CachedParams p) 
           } else {
             const uint4 y = *reinterpret_cast<const uint4*>(rec + R::kK + tok * R::kRow + 16 * cc);
             kw[e][0] = y.x, kw[e][1] = y.y, kw[e][2 * kGroups - 2] = y.z, kw[e][2 * kGroups - 1] = y.w;
-            const uint16_t two = *reinterpret_cast<const uint16_t*>(rec + R::kKs + tok * R::kScaleRow + 2 * cc);
-            uint32_t both;
-            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(both) : "h"(two));
+            const uint32_t both =
+                e4m3x2_f16x2(*reinterpret_cast<const uint16_t*>(rec + R::kKs + tok * R::kScaleRow + 2 * cc));
             ks[e][0] = __byte_perm(both, both, 0x1010);
             ks[e][kGroups - 1] = __byte_perm(both, both, 0x3232);
           }
@@ -280,6 +284,11 @@ __global__ void __launch_bounds__(256, 2) attn_few_kernel(const CachedParams p) 
             for (int j = 0; j < D / 16; ++j) o[b][j][e] *= f, o[b][j][e + 2] *= f;
           }
       }
+      float shift[NB][2];
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) shift[b][e] = (m[b][e] == -INFINITY ? 0.0f : -m[b][e]) + 7.0f;
       // ---- weights; the maximum is held at 2^7, so that an f16 weight keeps
       // every bit down to 2^-21 of it (before a rescale it reaches 2^15 at most)
 #pragma unroll
@@ -292,8 +301,7 @@ __global__ void __launch_bounds__(256, 2) attn_few_kernel(const CachedParams p) 
           float e[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float shift = (m[b][i & 1] == -INFINITY ? 0.0f : -m[b][i & 1]) + 7.0f;
-            e[i] = exp2_approx(fmaf(s[b][x][i], sc[b][i & 1], shift));
+            e[i] = exp2_approx(fmaf(s[b][x][i], sc[b][i & 1], shift[b][i & 1]));
             l[b][i & 1] += e[i];
           }
           pt[b][0] = transpose8x8(pack_f16(e[0], e[1]));
@@ -303,36 +311,41 @@ __global__ void __launch_bounds__(256, 2) attn_few_kernel(const CachedParams p) 
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int tok = (i & 1 ? val_b : val_a) + 8 * (i >> 1);
-          const uint8_t* src = rec + R::kV + tok * R::kRow + 4 * kGroups * r;
+          const uint8_t* at = rec + R::kV + tok * R::kRow + 4 * kGroups * r;
           if (kGroups == 1) {
-            vw[i][0] = *reinterpret_cast<const uint32_t*>(src);
+            vw[i][0] = *reinterpret_cast<const uint32_t*>(at);
           } else {
-            const uint2 y = *reinterpret_cast<const uint2*>(src);
+            const uint2 y = *reinterpret_cast<const uint2*>(at);
             vw[i][0] = y.x, vw[i][kGroups - 1] = y.y;
           }
-          uint32_t scale = rec[R::kVs + tok * R::kScaleRow + (kGroups == 1 ? r >> 1 : r)];
+          vs[i] = rec[R::kVs + tok * R::kScaleRow + (kGroups == 1 ? r >> 1 : r)];
           // what lies past the request's keys may be anything, a NaN too
-          if (masked && ((pos + x) * 16 + tok >= L || !(ok >> x & 1))) scale = 0;
-          vs[i] = e4m3_f16x2(scale);
+          if (masked && ((pos + x) * 16 + tok >= L || !(ok >> x & 1))) vs[i] = 0;
         }
+        // A product wants two tokens' values of one element together, so the codes
+        // of two tokens are interleaved before they are converted.
+        const uint32_t s01 = e4m3x2_f16x2(vs[0] | vs[1] << 8), s23 = e4m3x2_f16x2(vs[2] | vs[3] << 8);
 #pragma unroll
         for (int g = 0; g < kGroups; ++g) {
-          uint32_t v[4][4];
+          uint32_t even[2][4], odd[2][4];  // [tokens][pair of elements]
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            e2m1x8_f16(vw[i][g], v[i]);
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t a = vw[2 * i][g], b8 = vw[2 * i + 1][g];
+            e2m1x8_f16((a & 0x0f0f0f0fu) | ((b8 << 4) & 0xf0f0f0f0u), even[i]);
+            e2m1x8_f16(((a >> 4) & 0x0f0f0f0fu) | (b8 & 0xf0f0f0f0u), odd[i]);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[i][e] = hmul2(v[i][e], vs[i]);
+            for (int e = 0; e < 4; ++e) {
+              even[i][e] = hmul2(even[i][e], i ? s23 : s01);
+              odd[i][e] = hmul2(odd[i][e], i ? s23 : s01);
+            }
           }
 #pragma unroll
           for (int e = 0; e < 4; ++e)
 #pragma unroll
             for (int b = 0; b < NB; ++b)
-              mma_f16(o[b][4 * g + e], lo_halves(v[0][e], v[1][e]), hi_halves(v[0][e], v[1][e]),
-                      lo_halves(v[2][e], v[3][e]), hi_halves(v[2][e], v[3][e]), pt[b][0], pt[b][1]);
+              mma_f16(o[b][4 * g + e], even[0][e], odd[0][e], even[1][e], odd[1][e], pt[b][0], pt[b][1]);
         }
       }
-      if (ok != (1u << cnt) - 1 && lane == 0 && pos * 16 < L) atomicOr(p.err, PE_ERR_BLOCK_RANGE);
       pos += cnt;
       __syncwarp();  // the step is read: its place takes the next copies
       issue();

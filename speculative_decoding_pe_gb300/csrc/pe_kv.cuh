@@ -46,13 +46,14 @@ __device__ __forceinline__ uint32_t to_e4m3(float x) {
   return d & 0xffu;
 }
 
-// The scale byte `b` in both halves, as f16 (exact).
-__device__ __forceinline__ uint32_t e4m3_f16x2(uint32_t b) {
+// Two scale bytes as f16 (exact).
+__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t two) {
   uint32_t d;
-  const uint16_t two = (uint16_t)(b | (b << 8));
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"(two));
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"((uint16_t)two));
   return d;
 }
+// The scale byte `b` in both halves, as f16.
+__device__ __forceinline__ uint32_t e4m3_f16x2(uint32_t b) { return e4m3x2_f16x2(b | (b << 8)); }
 
 // Four bytes of codes as eight f16 numbers (exact): d[i] holds elements 2i, 2i+1.
 __device__ __forceinline__ void e2m1x8_f16(uint32_t w, uint32_t (&d)[4]) {
