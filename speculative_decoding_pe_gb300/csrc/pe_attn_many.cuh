@@ -123,13 +123,16 @@ __device__ void convert_tiles(const Line<true>& line, Control& c, Raw& raw, cons
       const bool valid = tok < line.span && t < w.rows;
       const uint4* src = reinterpret_cast<const uint4*>(
           p.q + ((long long)(w.first + t) * p.Hq + w.h * line.G + g) * D);
-      float most = 0.0f;
+      float most = 0.0f, all = 0.0f;
 #pragma unroll 4
       for (int i = 0; i < D / 8; ++i) {
         const uint4 q = valid ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
         const uint32_t y[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) most = fmaxf(most, fmaxf(fabsf(bf16_lo(y[e])), fabsf(bf16_hi(y[e]))));
+        for (int e = 0; e < 4; ++e) {
+          most = fmaxf(most, fmaxf(fabsf(bf16_lo(y[e])), fabsf(bf16_hi(y[e]))));
+          all += fabsf(bf16_lo(y[e])) + fabsf(bf16_hi(y[e]));
+        }
       }
       const float2 f = row_factor(most);
 #pragma unroll
@@ -141,6 +144,7 @@ __device__ void convert_tiles(const Line<true>& line, Control& c, Raw& raw, cons
         used[s] += busy[s];
       }
       c.row_scale[segment & 3][row] = f.y;
+      c.row_sum[segment & 3][row] = all * 1.001f;  // (a bound: its own roundings)
 #pragma unroll 4
       for (int i = 0; i < D / 8; ++i) {
         const uint4 q = valid ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
@@ -163,12 +167,21 @@ __device__ void convert_tiles(const Line<true>& line, Control& c, Raw& raw, cons
       const uint8_t* rec = smem + S::kRaw + (rst * (kTile / 16) + row / 16) * R::kBytes;
       const int r = row & 15;
       const uint32_t ok = raw.ok[rst];
+      const bool valid = j * kTile + row < keys && (ok >> (row / 16) & 1);
+      const uint8_t* scales = rec + (kKeys ? R::kKs : R::kVs) + r * R::kScaleRow;
+      uint32_t most = 0;  // the largest scale of the warp's keys (the bytes of magnitudes are in order)
+      if (kKeys) {
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) most = __vmaxu4(most, reinterpret_cast<const uint32_t*>(scales)[i] & 0x7f7f7f7fu);
+        most = __vmaxu4(most, most >> 16);
+        most = __reduce_max_sync(0xffffffffu, valid ? __vmaxu4(most, most >> 8) & 0xffu : 0u);
+      }
       if (!wait_warp(kKeys ? &c.k_empty[st] : &c.v_empty[st], phase ^ 1, dead)) return;
+      if (kKeys && first_lane) c.tile_scale[k & 15][row / 32] = (uint8_t)most;
       if (kKeys && row == 0)
         c.tile_ok[k & 15] = ok | ~((1u << min(kTile / 16, (keys - j * kTile + 15) / 16)) - 1) & 0xffu;
       put_codes<D, !kKeys>(smem + (kKeys ? S::kK : S::kV) + st * S::kOperand, row,
-                           rec + (kKeys ? R::kK : R::kV) + r * R::kRow, rec + (kKeys ? R::kKs : R::kVs) + r * R::kScaleRow,
-                           j * kTile + row < keys && (ok >> (row / 16) & 1));
+                           rec + (kKeys ? R::kK : R::kV) + r * R::kRow, scales, valid);
       fence_async_shared();
       __syncwarp();
       if (first_lane) {
@@ -194,7 +207,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) attn_many_kernel(const Cached
       mbar_init(&raw.full[i], 1);
       mbar_init(&raw.empty[i], 2 * kConverters);
     }
-    c.init(kConverters, kConverters, kConverters, 1);
+    c.init(kConverters, kConverters, kConverters);
   }
   const int G = p.Hq / p.Hkv;
   Line<true> line{p.seg, p.Hkv, G, kTile / G, nullptr, nullptr};
@@ -221,9 +234,9 @@ __global__ void __launch_bounds__(kManyThreads, 1) attn_many_kernel(const Cached
     a.v = nullptr, a.v_row = a.v_head = 0;
     a.out = p.out, a.ws = p.ws, a.err = p.err;
     softmax_rows<D, true>(line, c, a, warp >> 2);
-  } else if (warp < 10) {
-    if (elect_one()) issue_products<D, true>(line, c, smem_addr(smem), warp - 8);
-  } else if (warp == 10) {
+  } else if (warp == 8) {
+    if (elect_one()) issue_products<D, true>(line, c, smem_addr(smem));
+  } else if (warp == 9) {
     bring_records<D>(line, c, raw, p, smem);
   } else if (warp >= 12 + kConverters) {
     convert_tiles<D, false>(line, c, raw, p, smem, threadIdx.x - (12 + kConverters) * 32);

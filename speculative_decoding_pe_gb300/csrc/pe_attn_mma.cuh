@@ -8,7 +8,7 @@
 //   l = l 2^(m - m') + sum P;  O = O 2^(m - m') + P V;  out = O / l.
 // m need not be the maximum: any m gives the same quotient as long as P stays in
 // range, so it is taken from an item's first tile and then only when a score
-// passes it by more than the type of P holds; O is rarely rescaled.  S, O, m and
+// passes it by kSlack; O is rarely rescaled.  S, O, m and
 // l are fp32.  P is rounded to bf16 for the product, each weight by at most 2^-8
 // of itself however small it is (an f16 would lose the small ones), which is
 // what the output is rounded by.
@@ -23,8 +23,8 @@
 // CTA.  Two streams of 128 rows, one per softmax warpgroup, alternate on the
 // tensor core: while one takes its exponentials, the other's products run.
 // Warps 0-3 and 4-7 hold one row per thread (S and O arrive from TMEM without
-// any exchange between threads), one warp per stream issues its products, the
-// others bring keys and values.
+// any exchange between threads), one warp issues the products, the others bring
+// keys and values.
 #pragma once
 
 #include "pe_attn_line.cuh"
@@ -49,6 +49,16 @@ __device__ __forceinline__ Visits visits(const Line<kCached>& line, const Walk& 
   if (!kCached) last = min(last, (min(w.rows, from + line.span) + kTile - 1) / kTile);
   return {max(0, last - w.t0), w.t0, 1};
 }
+
+// The visits of both streams take turns until one has no more; the x-th of all.
+struct Order {
+  int count[2], both, total;
+  __device__ Order(const Visits& a, const Visits& b)
+      : count{a.count, b.count}, both(min(a.count, b.count)), total(a.count + b.count) {}
+  __device__ int stream(int x) const { return x < 2 * both ? x & 1 : count[1] > count[0]; }
+  __device__ int visit(int x) const { return x < 2 * both ? x >> 1 : x - both; }
+  __device__ int index(int s, int i) const { return i < both ? 2 * i + s : i + both; }
+};
 
 // ------------------------------------------------------------ packed fp32 pairs
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
@@ -78,25 +88,24 @@ struct AttnShape {
   static constexpr int kRaw = kV + kStages * kOperand;  // records as they lie in the cache
   static constexpr int kRawStages = !kCached ? 0 : D == 64 ? 4 : 2;
   static constexpr int kData = kRaw + kRawStages * (kTile / 16) * Record<D>::kBytes;
-  // Tensor memory: S of both streams, O, and P where there is room (D = 64).
-  // With its own P, S outlives the weights, so the maximum is looked for only when
-  // they turn out too large (D = 64 has as many exponentials as products, and
-  // the softmax is what bounds it), and the next S comes before the products of
-  // P.  For D = 128 P takes the first half of S: the next S comes after the
-  // products of P, which begin with P's first half.
+  // Tensor memory: S in as many buffers as fit beside O of both streams.  The
+  // visits take them in turn, P takes the first half of its S, and a buffer's next
+  // S follows the products of its P.  With three of them (D = 64, which has as many
+  // exponentials as products) the softmax finds its next S ready.
   static constexpr int kColumns = 512;
-  static constexpr bool kOwnP = D == 64;
-  __host__ __device__ static constexpr uint32_t s_col(int s) { return s * kTile; }
-  __host__ __device__ static constexpr uint32_t o_col(int s) { return 2 * kTile + s * D; }
-  __host__ __device__ static constexpr uint32_t p_col(int s) {
-    return kOwnP ? 2 * kTile + 2 * D + s * (kTile / 2) : s_col(s);
-  }
+  static constexpr int kBuffers = D == 64 ? 3 : 2;
+  static constexpr bool kHalves = D == 128;  // P's first half is announced
+  __host__ __device__ static constexpr uint32_t s_col(int buffer) { return buffer * kTile; }
+  __host__ __device__ static constexpr uint32_t o_col(int s) { return kBuffers * kTile + s * D; }
 };
 
 template <int kStages>
 struct AttnControl {
   uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_ready[kStages], v_empty[kStages];
-  uint64_t q_full[2], q_empty[2], s_full[2], p_half[2], p_full[2], o_full[2], pair;
+  uint64_t q_full[2], q_empty[2], pair;
+  // by visit of the stream: S runs up to three ahead of the products of P, and so
+  // may one warp of the others; a phase two away would look like the awaited one
+  uint64_t s_full[2][4], p_half[2][4], p_full[2][4], o_full[2][4];
   Walk start;
   long long total, parts;
   uint32_t tmem;
@@ -104,25 +113,29 @@ struct AttnControl {
   uint32_t not_finite[8][12];  // values of a masked tile: tokens that hold an infinity or NaN
   int any_not_finite[8];       // of a segment
   float row_scale[4][kTile];   // kCached, by segment: the power of two taken out of a query row
+  float row_sum[4][kTile];     // kCached, by segment: the sum of a query's magnitudes
   uint32_t tile_ok[16];        // kCached: records of a tile that lie in the cache
+  uint8_t tile_scale[16][4];   // kCached: the largest key scale of a tile's quarters
 
   // Barriers before their first use; one thread.  The counts: arrivals on
-  // k_full, v_ready and q_full, and streams that use a tile.
-  __device__ void init(int k_count, int v_count, int q_count, int users) {
+  // k_full, v_ready and q_full.
+  __device__ void init(int k_count, int v_count, int q_count) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&k_full[i], k_count);
       mbar_init(&v_full[i], 1);
       mbar_init(&v_ready[i], v_count);
-      mbar_init(&k_empty[i], users);
-      mbar_init(&v_empty[i], users);
+      mbar_init(&k_empty[i], 1);
+      mbar_init(&v_empty[i], 1);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&q_full[s], q_count);
       mbar_init(&q_empty[s], 1);
-      mbar_init(&s_full[s], 1);
-      mbar_init(&p_half[s], 4);
-      mbar_init(&p_full[s], 4);
-      mbar_init(&o_full[s], 1);
+      for (int i = 0; i < 4; ++i) {
+        mbar_init(&s_full[s][i], 1);
+        mbar_init(&o_full[s][i], 1);
+        mbar_init(&p_half[s][i], 4);
+        mbar_init(&p_full[s][i], 4);
+      }
     }
     mbar_init(&pair, 8);
     dead = 0;
@@ -131,95 +144,76 @@ struct AttnControl {
 };
 
 // ------------------------------------------------------------------- products
-// The products of stream s: one elected lane of a warp of its own.  (One warp
-// for both streams took 1500 cycles for a visit of each, most of it waiting for
-// its own instructions, and bounded the kernel.)
+// The products: one elected lane.
 template <int D, bool kCached, class Control>
-__device__ void issue_products(const Line<kCached>& line, Control& c, uint32_t smem, int s) {
+__device__ void issue_products(const Line<kCached>& line, Control& c, uint32_t smem) {
   using S = AttnShape<D, kCached>;
   constexpr uint32_t kIdescS = umma_idesc(!kCached, kTile, false);
   constexpr uint32_t kIdescO = umma_idesc(true, D, true);
   constexpr uint32_t kStep = S::kOperand >> 4;  // of a descriptor's address
   volatile int* dead = &c.dead;
-  const uint32_t s_tmem = c.tmem + S::s_col(s), o_tmem = c.tmem + S::o_col(s), p_tmem = c.tmem + S::p_col(s);
-  const uint64_t q_desc = umma_desc(smem + S::kQ + (kCached ? 0 : s) * S::kOperand, 16), k_desc = umma_desc(smem + S::kK, 16);
+  const uint32_t tmem = c.tmem;
+  const uint64_t q_desc = umma_desc(smem + S::kQ, 16), k_desc = umma_desc(smem + S::kK, 16);
   const uint64_t v_desc = umma_desc(smem + S::kV, kTile * 128);
   Walk w = c.start;
-  uint32_t kv0 = 0, p_phase = 0, q_phase = 0;
+  uint32_t kv0 = 0, u0 = 0, q_phase = 0;  // tiles and visits before the segment
+  uint32_t done[2] = {0, 0};                           // visits of each stream
   while (walk_next(line, w)) {
-    const Visits v = visits(line, w, s);
-    const int tiles = w.t1 - w.t0;
-    uint32_t k = kv0 + v.tile0 - w.t0;  // the visit's tile, of all that the CTA reads
-    // S of the tile k
-    auto scores = [&](uint32_t k, bool last) {
-      const uint32_t st = k % S::kStages;
-      const uint64_t ka = k_desc + st * kStep;
-#pragma unroll
-      for (int x = 0; x < D / 16; ++x) {
-        const uint32_t off = ((x / 4) * (kTile * 128) + (x % 4) * 32) >> 4;
-        umma_ss(s_tmem, q_desc + off, ka + off, kIdescS, x > 0);
-      }
-      tc_commit(&c.s_full[s]);
-      tc_commit(&c.k_empty[st]);
-      if (last) tc_commit(&c.q_empty[s]);
-    };
-    // O += P V, keys [16 from, 16 to) of the tile k
-    auto values = [&](uint32_t k, int from, int to, bool add) {
-      const uint64_t va = v_desc + (k % S::kStages) * kStep;
-#pragma unroll
-      for (int y = from; y < to; ++y)
-        umma_ts(o_tmem, p_tmem + y * 8, va + (y * 16 * 128 >> 4), kIdescO, add || y > 0);
-    };
-    auto keys_there = [&](uint32_t k) { return wait_or_dead(&c.k_full[k % S::kStages], (k / S::kStages) & 1, dead); };
-    auto values_there = [&](uint32_t k) { return wait_or_dead(&c.v_ready[k % S::kStages], (k / S::kStages) & 1, dead); };
-    // a tile that this stream does not visit (the other one does)
-    auto pass = [&](uint32_t k) {
-      if (!keys_there(k) || !values_there(k)) return false;
-      mbar_arrive(&c.k_empty[k % S::kStages]);
-      mbar_arrive(&c.v_empty[k % S::kStages]);
-      return true;
-    };
-
-    if (v.count) {
-      if (!wait_or_dead(&c.q_full[s], q_phase, dead)) return;
-      q_phase ^= 1;
-    }
+    const Visits v[2] = {visits(line, w, 0), visits(line, w, 1)};
+    const Order order(v[0], v[1]);
+    const bool alone = kCached || !v[1].count;  // a tile has one user
 #pragma unroll 1
-    for (int i = -1; i < v.count; ++i) {  // P V of visit i, Q K of the next one
-      const bool next = i + 1 < v.count;
-      const uint32_t kn = i < 0 ? k : k + v.step;
-      if (i >= 0) {
-        if (!values_there(k)) return;
-        if (!S::kOwnP) {
-          if (!wait_or_dead(&c.p_half[s], p_phase, dead)) return;
+    for (int s = 0; s < 2; ++s)
+      if (order.count[s]) {
+        if (!wait_or_dead(&c.q_full[s], (q_phase >> s) & 1, dead)) return;
+        q_phase ^= 1u << s;
+      }
+    // P V of the x-th visit, then Q K of the one that takes its buffer next
+#pragma unroll 1
+    for (int x = -S::kBuffers; x < order.total; ++x) {
+      if (x >= 0) {
+        const int s = order.stream(x), i = order.visit(x);
+        const uint32_t n = (s ? done[1] : done[0]) + i;  // of the stream's visits
+        const uint32_t k = kv0 + v[0].step * i + (s ? v[1].tile0 : v[0].tile0) - w.t0, st = k % S::kStages;
+        const uint32_t o = tmem + S::o_col(s), p = tmem + S::s_col((u0 + x) % S::kBuffers);
+        const uint64_t va = v_desc + st * kStep;
+        if (!wait_or_dead(&c.v_ready[st], (k / S::kStages) & 1, dead)) return;
+        if (S::kHalves) {
+          if (!wait_or_dead(&c.p_half[s][n & 3], (n >> 2) & 1, dead)) return;
           tc_fence_after();
-          values(k, 0, kTile / 32, i > 0);
+#pragma unroll
+          for (int y = 0; y < kTile / 32; ++y)
+            umma_ts(o, p + y * 8, va + (y * 16 * 128 >> 4), kIdescO, i > 0 || y > 0);
         }
-        if (!wait_or_dead(&c.p_full[s], p_phase, dead)) return;
-        p_phase ^= 1;
+        if (!wait_or_dead(&c.p_full[s][n & 3], (n >> 2) & 1, dead)) return;
         tc_fence_after();
+#pragma unroll
+        for (int y = S::kHalves ? kTile / 32 : 0; y < kTile / 16; ++y)
+          umma_ts(o, p + y * 8, va + (y * 16 * 128 >> 4), kIdescO, i > 0 || y > 0);
+        tc_commit(&c.o_full[s][n & 3]);
+        if (alone || s == 1) tc_commit(&c.v_empty[st]);
       }
-      if (S::kOwnP && next) {
-        if (!keys_there(kn)) return;
+      const int next = x + S::kBuffers;
+      if (next < order.total) {
+        const int s = order.stream(next), i = order.visit(next);
+        const uint32_t k = kv0 + v[0].step * i + (s ? v[1].tile0 : v[0].tile0) - w.t0, st = k % S::kStages;
+        const int buffer = (u0 + next) % S::kBuffers;
+        const uint64_t qa = q_desc + (kCached ? 0 : s) * kStep, ka = k_desc + st * kStep;
+        if (!wait_or_dead(&c.k_full[st], (k / S::kStages) & 1, dead)) return;
         tc_fence_after();
-        scores(kn, i + 2 == v.count);
+#pragma unroll
+        for (int y = 0; y < D / 16; ++y) {
+          const uint32_t off = ((y / 4) * (kTile * 128) + (y % 4) * 32) >> 4;
+          umma_ss(tmem + S::s_col(buffer), qa + off, ka + off, kIdescS, y > 0);
+        }
+        tc_commit(&c.s_full[s][(s ? done[1] : done[0]) + i & 3]);
+        if (alone || s == 1) tc_commit(&c.k_empty[st]);
+        if (i == order.count[s] - 1) tc_commit(&c.q_empty[s]);
       }
-      if (i >= 0) {
-        values(k, S::kOwnP ? 0 : kTile / 32, kTile / 16, i > 0 || !S::kOwnP);
-        tc_commit(&c.o_full[s]);
-        tc_commit(&c.v_empty[k % S::kStages]);
-      }
-      if (!S::kOwnP && next) {
-        if (!keys_there(kn)) return;
-        tc_fence_after();
-        scores(kn, i + 2 == v.count);
-      }
-      k = kn;
     }
-    if (!kCached)
-      for (int j = v.count; j < tiles; ++j)
-        if (!pass(kv0 + j)) return;
-    kv0 += tiles;
+    kv0 += w.t1 - w.t0;
+    u0 += order.total;
+    done[0] += order.count[0], done[1] += order.count[1];
   }
 }
 
@@ -277,25 +271,26 @@ __device__ void softmax_rows(const Line<kCached>& line, Control& c, const Softma
   using Sh = AttnShape<D, kCached>;
   // How far (log2) a score may pass the maximum that is held before the row takes
   // the new one and O is rescaled: weights and sums have fp32's range.
-  constexpr float kSlack = 30.0f;
+  constexpr float kSlack = 100.0f;
   // Columns of S in registers at a time.  Over the cache eight warps that convert
   // codes share the instruction cache with the softmax, and its shorter code is
   // worth more than fewer loads (b64 drafts: 727 us against 468); a prompt's
   // softmax is faster unrolled (b8: 2.19 ms against 2.54).
   constexpr int kCols = kCached ? 64 : kTile;
-  constexpr float kMostWeight = 1073741824.0f;  // the same for a tile's weights together
   volatile int* dead = &c.dead;
   const int row = threadIdx.x & (kTile - 1);
   const uint32_t lane_base = c.tmem + ((uint32_t)(row & ~31) << 16);
-  const uint32_t s_addr = lane_base + Sh::s_col(s), o_addr = lane_base + Sh::o_col(s);
-  const uint32_t p_addr = lane_base + Sh::p_col(s);
+  const uint32_t o_addr = lane_base + Sh::o_col(s);
   const int tok = row / line.G, g = row - tok * line.G;
   uint32_t visit = 0, joins = 0;  // visits, joins so far
   int segment = 0;
   Walk w = c.start;
-  uint32_t kv0 = 0;  // tiles before the segment
+  uint32_t kv0 = 0, u0 = 0;  // tiles and visits before the segment
   for (; walk_next(line, w); kv0 += w.t1 - w.t0, ++segment) {
     const Visits v = visits(line, w, s);
+    const Order order(s ? visits(line, w, 0) : v, s ? v : visits(line, w, 1));
+    const uint32_t base = u0;
+    u0 += order.total;
     constexpr bool halves = kCached;  // both streams have the same rows
     const int from = (halves ? w.mt : 2 * w.mt + s) * line.span;
     const bool valid = tok < line.span && from + tok < w.rows;
@@ -316,28 +311,32 @@ __device__ void softmax_rows(const Line<kCached>& line, Control& c, const Softma
     }
     const int least = __reduce_min_sync(0xffffffffu, limit);
     const bool idle = kCached && !__any_sync(0xffffffffu, live);
-    float m = live ? -INFINITY : 0.0f, l = 0.0f, scale = p.scale_log2;
+    float m = live ? -INFINITY : 0.0f, l = 0.0f, scale = p.scale_log2, row_sum = 0.0f;
     for (int i = 0; i < v.count; ++i, ++visit) {
-      if (!wait_warp(&c.s_full[s], visit & 1, dead)) return;
+      const uint32_t u = base + order.index(s, i);
+      const int buffer = u % Sh::kBuffers;
+      const uint32_t s_addr = lane_base + Sh::s_col(buffer);  // and of P
+      // (a ring of a stream's own: S is at most three visits ahead)
+      if (!wait_warp(&c.s_full[s][visit & 3], (visit >> 2) & 1, dead)) return;
       tc_fence_after();
-      if (kCached && i == 0) scale = p.scale_log2 * c.row_scale[segment & 3][row];
-      if (kCached && idle) {  // every row of the warp is thrown away: P may be anything
+      auto announce = [&](uint64_t* bar) {  // P, as far as it is written
+        tc_wait_st();
         tc_fence_before();
         __syncwarp();
-        if ((threadIdx.x & 31) == 0) {
-          if (!Sh::kOwnP) mbar_arrive(&c.p_half[s]);
-          mbar_arrive(&c.p_full[s]);
-        }
+        if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
+      };
+      if (kCached && idle) {  // every row of the warp is thrown away: P may be anything
+        if (Sh::kHalves) announce(&c.p_half[s][visit & 3]);
+        announce(&c.p_full[s][visit & 3]);
         continue;
       }
       const int key0 = v.tile(i) * kTile;
-      const uint32_t ok = kCached ? c.tile_ok[(kv0 + v.tile(i) - w.t0) & 15] : 0xffu;
-      // A row takes a maximum in its first tile, and when the weights by the one it
-      // holds grow too large (each row for itself: what it gets does not depend
-      // on its neighbours).  Where P lies on S that has to be known before.
-      bool ask = i == 0 || m == -INFINITY;
-      bool look = !Sh::kOwnP || __any_sync(0xffffffffu, ask);
-      float2 sum[2];
+      const uint32_t kv = (kv0 + v.tile(i) - w.t0) & 15;
+      const uint32_t ok = kCached ? c.tile_ok[kv] : 0xffu;
+      if (kCached && i == 0) {
+        scale = p.scale_log2 * c.row_scale[segment & 3][row];
+        row_sum = p.scale_log2 * c.row_sum[segment & 3][row];
+      }
       // kCols columns of S from q on; scores that a row does not see become
       // -infinity, whatever they were.
       auto load = [&](int q, uint32_t(&y)[kCols]) {
@@ -352,91 +351,81 @@ __device__ void softmax_rows(const Line<kCached>& line, Control& c, const Softma
             if (r >= seen || (kCached && !(there >> (r / 16) & 1))) y[r] = 0xff800000u;
         }
       };
-#pragma unroll 1
-      for (int pass = 0; pass < 2; ++pass) {
-        uint32_t y[kCols];
-        load(0, y);
-        if (Sh::kOwnP ? __builtin_expect(look, 0) : true) {
-          float mx[8];
+      uint32_t y[kCols];
+      load(0, y);
+      // Over the cache the largest key scale s of the tile tells in advance that no
+      // score can pass the maximum by too much: |q k| <= sum |q| * 6 s.  (What a row
+      // takes depends on its own scores alone.)
+      bool look = true;
+      if (kCached) {
+        const uint32_t four = *reinterpret_cast<const uint32_t*>(c.tile_scale[kv]);
+        const uint32_t two = __vmaxu4(four, four >> 16), one = __vmaxu4(two, two >> 8) & 0xffu;
+        float most, unused;
+        f16x2_to_f32(e4m3_f16x2(one), most, unused);
+        look = __any_sync(0xffffffffu, live && !(row_sum * (6.0f * most) <= m + kSlack));
+      }
+      if (look) {
+        float mx[8];
 #pragma unroll
-          for (int r = 0; r < 8; ++r) mx[r] = -INFINITY;
-#pragma unroll 1
-          for (int q = 0; q < kTile; q += kCols) {
-            if (q > 0) load(q, y);
-#pragma unroll
-            for (int r = 0; r < kCols / 2; ++r)
-              mx[r & 7] = max3(mx[r & 7], __uint_as_float(y[r]), __uint_as_float(y[r + kCols / 2]));
-          }
-          const float top =
-              fmaxf(max3(mx[0], mx[1], mx[2]), max3(max3(mx[3], mx[4], mx[5]), mx[6], mx[7])) * scale;
-          const bool grew = live && top > m + (Sh::kOwnP && ask ? 0.0f : kSlack);
-          if (__any_sync(0xffffffffu, grew)) {
-            const float f = grew ? exp2_approx(m - top) : 1.0f;
-            if (grew) m = top;
-            l *= f;
-            if (i > 0) {  // O of the visits before
-              if (!wait_warp(&c.o_full[s], (visit - 1) & 1, dead)) return;
-              tc_fence_after();
-#pragma unroll 1
-              for (int q = 0; q < D; q += 16) {
-                uint32_t o[16];
-                tmem_ld16(o_addr + q, o);
-                tc_wait_ld();
-#pragma unroll
-                for (int r = 0; r < 16; ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) * f);
-                tmem_st16(o_addr + q, o);
-              }
-            }
-          }
-        }
-        const float shift = m == -INFINITY ? 0.0f : -m;
-        sum[0] = sum[1] = make_float2(0.0f, 0.0f);
-        // the products that read the last P
-        auto p_free = [&]() { return !Sh::kOwnP || i == 0 || wait_warp(&c.o_full[s], (visit - 1) & 1, dead); };
-        if (kCached && !p_free()) return;
-        if (kCols < kTile && look) load(0, y);  // the maximum took it as far as the last columns
+        for (int r = 0; r < 8; ++r) mx[r] = -INFINITY;
 #pragma unroll 1
         for (int q = 0; q < kTile; q += kCols) {
           if (q > 0) load(q, y);
 #pragma unroll
-          for (int half = 0; half < kCols; half += 64) {
-            uint32_t pk[32];
-#pragma unroll
-            for (int r = 0; r < 32; ++r) {
-              float2 e = fma2(make_float2(__uint_as_float(y[half + 2 * r]), __uint_as_float(y[half + 2 * r + 1])),
-                              make_float2(scale, scale), make_float2(shift, shift));
-              e.x = exp2_approx(e.x);
-              e.y = exp2_approx(e.y);
-              sum[r & 1] = add2(sum[r & 1], e);
-              pk[r] = pack_bf16(e.x, e.y);
-            }
-            if (!kCached && q + half == 0 && !p_free()) return;
+          for (int r = 0; r < kCols / 2; ++r)
+            mx[r & 7] = max3(mx[r & 7], __uint_as_float(y[r]), __uint_as_float(y[r + kCols / 2]));
+        }
+        const float top =
+            fmaxf(max3(mx[0], mx[1], mx[2]), max3(max3(mx[3], mx[4], mx[5]), mx[6], mx[7])) * scale;
+        const bool grew = live && top > m + kSlack;
+        if (__any_sync(0xffffffffu, grew)) {
+          const float f = grew ? exp2_approx(m - top) : 1.0f;
+          if (grew) m = top;
+          l *= f;
+          if (i > 0) {  // O of the visits before
+            if (!wait_warp(&c.o_full[s][(visit - 1) & 3], ((visit - 1) >> 2) & 1, dead)) return;
             tc_fence_after();
-            tmem_st16(p_addr + (q + half) / 2, pk);
-            tmem_st16(p_addr + (q + half) / 2 + 16, pk + 16);
-            if (!Sh::kOwnP && q + half == 0) {  // the first half's products may begin
-              tc_wait_st();
-              tc_fence_before();
-              __syncwarp();
-              if ((threadIdx.x & 31) == 0) mbar_arrive(&c.p_half[s]);
+#pragma unroll 1
+            for (int q = 0; q < D; q += 16) {
+              uint32_t o[16];
+              tmem_ld16(o_addr + q, o);
+              tc_wait_ld();
+#pragma unroll
+              for (int r = 0; r < 16; ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) * f);
+              tmem_st16(o_addr + q, o);
             }
           }
         }
-        sum[0] = add2(sum[0], sum[1]);
-        if (look) break;
-        ask = live && sum[0].x + sum[0].y > kMostWeight;
-        look = __any_sync(0xffffffffu, ask);
-        if (!look) break;
+        if (kCols < kTile) load(0, y);
       }
-      l += sum[0].x + sum[0].y;
-      tc_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if ((threadIdx.x & 31) == 0) mbar_arrive(&c.p_full[s]);
+      const float shift = m == -INFINITY ? 0.0f : -m;
+      float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll 1
+      for (int q = 0; q < kTile; q += kCols) {
+        if (q > 0) load(q, y);
+#pragma unroll
+        for (int half = 0; half < kCols; half += 64) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int r = 0; r < 32; ++r) {
+            float2 e = fma2(make_float2(__uint_as_float(y[half + 2 * r]), __uint_as_float(y[half + 2 * r + 1])),
+                            make_float2(scale, scale), make_float2(shift, shift));
+            e.x = exp2_approx(e.x);
+            e.y = exp2_approx(e.y);
+            sum[r & 1] = add2(sum[r & 1], e);
+            pk[r] = pack_bf16(e.x, e.y);
+          }
+          tmem_st16(s_addr + (q + half) / 2, pk);
+          tmem_st16(s_addr + (q + half) / 2 + 16, pk + 16);
+          if (Sh::kHalves && q + half == 0) announce(&c.p_half[s][visit & 3]);
+        }
+      }
+      announce(&c.p_full[s][visit & 3]);
+      l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
     }
     // ---- the segment's result, 32 columns at a time
     if (v.count) {
-      if (!wait_warp(&c.o_full[s], (visit - 1) & 1, dead)) return;
+      if (!wait_warp(&c.o_full[s][(visit - 1) & 3], ((visit - 1) >> 2) & 1, dead)) return;
       tc_fence_after();
     }
     if (!live) m = -INFINITY, l = 0.0f;

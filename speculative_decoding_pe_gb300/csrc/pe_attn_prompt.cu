@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   uint8_t* smem = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
   long long* prefix = reinterpret_cast<long long*>(smem + S::kData);
   const int warp = threadIdx.x >> 5;
-  if (threadIdx.x == 0) c.init(1, 1, 1, 2);
+  if (threadIdx.x == 0) c.init(1, 1, 1);
   Line<false> line{p.seg, p.Hkv, p.G, kTile / p.G, nullptr, nullptr};
   if (!plan(line, 2, c, prefix, nullptr, reinterpret_cast<long long*>(smem), nullptr, nullptr, 0, p.softmax.err)) return;
   if (c.start.u >= c.start.end) return;  // fewer parts than CTAs
@@ -151,11 +151,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
     give_registers<104>();
   if (warp < 8) {
     softmax_rows<D, false>(line, c, p.softmax, warp >> 2);
-  } else if (warp < 10) {
-    if (elect_one()) issue_products<D, false>(line, c, smem_addr(smem), warp - 8);
-  } else if (warp == 10) {
+  } else if (warp == 8) {
+    if (elect_one()) issue_products<D, false>(line, c, smem_addr(smem));
+  } else if (warp == 9) {
     if (elect_one()) bring_tiles<D>(line, c, smem, &qm, &km, &vm);
-  } else {
+  } else if (warp == 10) {
     look_over_values<D>(line, c, smem);
   }
   __syncwarp();
