@@ -219,14 +219,14 @@ __global__ void __launch_bounds__(kManyThreads, 1) attn_many_kernel(const Cached
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  // 20 warps of 96 registers: 112 for the softmax's rows, 80 for the products and
-  // the loads, 88 for the converters
+  // 20 warps of 96 registers: 128 for the softmax's rows, 72 for the products,
+  // the loads and the converters
   if (warp < 8)
-    take_registers<112>();
+    take_registers<128>();
   else if (warp < 12)
-    give_registers<80>();
+    give_registers<72>();
   else
-    give_registers<88>();
+    give_registers<72>();
   if (warp < 8) {
     SoftmaxArgs a;
     a.Hq = p.Hq, a.table_keys = p.table_keys, a.scale_log2 = p.scale_log2;
