@@ -27,7 +27,9 @@ struct Record {
 // Byte offset of the record of token `slot` (a slot of the whole cache) and head h.
 __device__ __forceinline__ long long record_offset(long long slot, int block_size, int Hkv,
                                                    int h, int rec_bytes) {
-  const long long block = slot / block_size;
+  // (a 64-bit division takes some hundred instructions)
+  const long long block =
+      (slot >> 32) == 0 ? (long long)((uint32_t)slot / (uint32_t)block_size) : slot / block_size;
   const int sub = (int)(slot - block * block_size) >> 4;
   return ((block * Hkv + h) * (block_size >> 4) + sub) * rec_bytes;
 }

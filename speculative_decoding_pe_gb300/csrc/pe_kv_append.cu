@@ -9,16 +9,18 @@
 // exact value would.  So a key next to a border of its code falls on the right
 // side, whatever order a checker adds in.  Queries take plain fp32.
 //
-// Work.  A warp takes one row; its lanes are D/32 units of 32 elements times
-// 1024/D heads, so a lane keeps the 32 table entries of its unit for every
-// head that it visits.  Queries, keys and values are one list of heads.  Bound
-// by memory: every element is read and written once.
+// Work.  A lane takes 32 elements of a head (two groups that hold both halves of
+// its pairs), a warp 1024/D heads of keys and values or twice as many of queries,
+// whose lanes use each table entry for two heads.  The warps go through all keys
+// and values first, then through all queries: with both at once the two codes
+// drove each other out of the instruction cache.  Bound by memory: every element
+// is read and written once.
 #include "pe_kv.cuh"
 
 namespace pe {
 
 struct AppendParams {
-  int T, Hq, Hkv, block_size, half, interleaved, max_pos, chunks;
+  int T, Hq, Hkv, block_size, half, max_pos, kv_chunks, q_chunks;
   long long slots_end;
   long long q_row, q_head, k_row, k_head, v_row, v_head;
   const uint16_t *q, *k, *v;
@@ -47,8 +49,9 @@ __device__ __forceinline__ float diff_of_products_odd(float a, float c, float b,
   return lo == lo ? __uint_as_float(u) : hi;  // an infinity or NaN leaves no remainder
 }
 
-// 16 bf16 elements (8 words) as codes and scale of one group.
-__device__ __forceinline__ void encode_group(const uint32_t (&w)[8], uint2& codes, uint32_t& scale) {
+// 16 bf16 elements as codes (x, y) and scale (z) of one group.
+__device__ __forceinline__ uint4 encode_group(uint4 a, uint4 b) {
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
   float x[16], m = 0.0f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -58,7 +61,7 @@ __device__ __forceinline__ void encode_group(const uint32_t (&w)[8], uint2& code
   }
   // max / 6 lies on a border of e4m3 only when it is exact in fp32 (a border
   // has 5 significant bits, six times it 7, a bf16 has 8)
-  scale = to_e4m3(fminf(__fdiv_rn(m, 6.0f), 448.0f));
+  const uint32_t scale = to_e4m3(fminf(__fdiv_rn(m, 6.0f), 448.0f));
   float s, unused;
   f16x2_to_f32(e4m3_f16x2(scale), s, unused);
   const float r = s > 0.0f ? __frcp_rn(s) : 0.0f;
@@ -68,121 +71,131 @@ __device__ __forceinline__ void encode_group(const uint32_t (&w)[8], uint2& code
 #pragma unroll
   for (int i = 0; i < 16; ++i)
     x[i] = __uint_as_float((__float_as_uint(__fmul_rn(x[i], r)) + 0x80u) & 0xffffff00u);
-  codes.x = to_e2m1x8(x);
-  codes.y = to_e2m1x8(x + 8);
+  return make_uint4(to_e2m1x8(x), to_e2m1x8(x + 8), scale, 0);
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThreads) kv_append_kernel(const AppendParams p) {
+// 32 elements of a head in two groups of 16.
+struct Unit {
+  uint32_t w[2][8];
+  __device__ __forceinline__ void load(const uint16_t* head, int e0, int e1) {
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      const uint4* v = reinterpret_cast<const uint4*>(head + (g ? e1 : e0));
+      const uint4 a = v[0], b = v[1];
+      w[g][0] = a.x, w[g][1] = a.y, w[g][2] = a.z, w[g][3] = a.w;
+      w[g][4] = b.x, w[g][5] = b.y, w[g][6] = b.z, w[g][7] = b.w;
+    }
+  }
+  __device__ __forceinline__ void store(uint16_t* head, int e0, int e1) const {
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      uint4* v = reinterpret_cast<uint4*>(head + (g ? e1 : e0));
+      v[0] = make_uint4(w[g][0], w[g][1], w[g][2], w[g][3]);
+      v[1] = make_uint4(w[g][4], w[g][5], w[g][6], w[g][7]);
+    }
+  }
+  // Turn pairs 4x .. 4x + 3 of the unit.
+  template <bool kInterleaved, bool kExact>
+  __device__ __forceinline__ void turn(int x, const float4& ca, const float4& sa) {
+    const float c[4] = {ca.x, ca.y, ca.z, ca.w}, s[4] = {sa.x, sa.y, sa.z, sa.w};
+    auto first = [](float a, float c, float b, float s) {
+      return kExact ? diff_of_products_odd(a, c, b, s) : a * c - b * s;
+    };
+    if (kInterleaved) {
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        uint32_t& word = w[x / 2][4 * (x % 2) + y];
+        const float x0 = bf16_lo(word), x1 = bf16_hi(word);
+        word = pack_bf16(first(x0, c[y], x1, s[y]), first(x1, c[y], x0, -s[y]));
+      }
+    } else {
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        uint32_t &wa = w[0][2 * x + y], &wb = w[1][2 * x + y];
+        const float a0 = bf16_lo(wa), a1 = bf16_hi(wa), b0 = bf16_lo(wb), b1 = bf16_hi(wb);
+        const float c0 = c[2 * y], c1 = c[2 * y + 1], s0 = s[2 * y], s1 = s[2 * y + 1];
+        wa = pack_bf16(first(a0, c0, b0, s0), first(a1, c1, b1, s1));
+        wb = pack_bf16(first(b0, c0, a0, -s0), first(b1, c1, a1, -s1));
+      }
+    }
+  }
+};
+
+template <int D, bool kInterleaved>
+__global__ void __launch_bounds__(kThreads, 3) kv_append_kernel(const AppendParams p) {
   using R = Record<D>;
   constexpr int kUnits = D / 32, kHeads = 32 / kUnits;
   const int lane = threadIdx.x & 31;
   const int unit = lane % kUnits, head0 = lane / kUnits;
-  const long long nwarps = ((long long)gridDim.x * kThreads) >> 5;
-  const int heads = p.Hq + 2 * p.Hkv;
-  const int per_chunk = (heads + p.chunks - 1) / p.chunks;
-  const int rot_units = p.half / 16;
+  const uint32_t nwarps = gridDim.x * (kThreads / 32);
+  const uint32_t kv_items = (uint32_t)p.T * p.kv_chunks, items = kv_items + (uint32_t)p.T * p.q_chunks;
   // elements of the unit's two groups
-  const bool turned = unit < rot_units;
-  const int e0 = !turned ? 32 * unit : p.interleaved ? 32 * unit : 16 * unit;
-  const int e1 = !turned || p.interleaved ? e0 + 16 : e0 + p.half;
-  for (long long it = ((long long)blockIdx.x * kThreads + threadIdx.x) >> 5;
-       it < (long long)p.T * p.chunks; it += nwarps) {
-    const int t = (int)(it / p.chunks), chunk = (int)(it - (long long)t * p.chunks);
-    const int pos = __ldg(p.positions + t);
-    const long long slot = __ldg(p.slots + t);
-    const bool pos_ok = pos >= 0 && pos < p.max_pos;
-    const bool live = slot >= 0 && slot < p.slots_end;
-    if (lane == 0 && chunk == 0) {
-      if (!pos_ok) atomicOr(p.err, PE_ERR_POS_RANGE);
-      if (!live && slot != -1) atomicOr(p.err, PE_ERR_BLOCK_RANGE);
-    }
-    const bool turn = turned && pos_ok;
-    float c[16], s[16];
-    if (turn) {
-      const float4* row = reinterpret_cast<const float4*>(p.rope + (long long)pos * 2 * p.half +
-                                                          16 * unit);
-      const float4* sin_row = row + p.half / 4;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float4 a = __ldg(row + i), b = __ldg(sin_row + i);
-        c[4 * i] = a.x, c[4 * i + 1] = a.y, c[4 * i + 2] = a.z, c[4 * i + 3] = a.w;
-        s[4 * i] = b.x, s[4 * i + 1] = b.y, s[4 * i + 2] = b.z, s[4 * i + 3] = b.w;
+  const bool turned = unit < p.half / 16;
+  const int e0 = !turned ? 32 * unit : kInterleaved ? 32 * unit : 16 * unit;
+  const int e1 = !turned || kInterleaved ? e0 + 16 : e0 + p.half;
+  for (uint32_t it = (blockIdx.x * kThreads + threadIdx.x) >> 5; it < items; it += nwarps) {
+    if (it < kv_items) {  // keys and values
+      const int t = (int)(it / (uint32_t)p.kv_chunks), chunk = (int)(it - (uint32_t)t * p.kv_chunks);
+      const int hh = chunk * kHeads + head0;
+      const bool value = hh >= p.Hkv;
+      const int h = value ? hh - p.Hkv : hh;
+      const int pos = __ldg(p.positions + t);
+      const long long slot = __ldg(p.slots + t);
+      Unit u;
+      if (hh < 2 * p.Hkv)
+        u.load(value ? p.v + t * p.v_row + h * p.v_head : p.k + t * p.k_row + h * p.k_head, e0, e1);
+      const bool pos_ok = pos >= 0 && pos < p.max_pos;
+      const bool live = slot >= 0 && slot < p.slots_end;
+      if (lane == 0 && chunk == 0) {
+        if (!pos_ok) atomicOr(p.err, PE_ERR_POS_RANGE);
+        if (!live && slot != -1) atomicOr(p.err, PE_ERR_BLOCK_RANGE);
       }
-    }
-    const int end = min(heads, (chunk + 1) * per_chunk);
-    for (int hh = chunk * per_chunk + head0; hh < end; hh += kHeads) {
-      const int kind = hh < p.Hq ? 0 : hh < p.Hq + p.Hkv ? 1 : 2;
-      const int h = kind == 0 ? hh : hh - p.Hq - (kind == 2 ? p.Hkv : 0);
-      const uint16_t* src = kind == 0   ? p.q + t * p.q_row + h * p.q_head
-                            : kind == 1 ? p.k + t * p.k_row + h * p.k_head
-                                        : p.v + t * p.v_row + h * p.v_head;
-      uint32_t w[2][8];
+      if (hh >= 2 * p.Hkv) continue;
+      if (!value) {
+        if (turned && pos_ok) {
+          const float4* cos_row =
+              reinterpret_cast<const float4*>(p.rope + (long long)pos * 2 * p.half + 16 * unit);
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            u.turn<kInterleaved, true>(x, __ldg(cos_row + x), __ldg(cos_row + p.half / 4 + x));
+        }
+        if (p.k_out) u.store(p.k_out + ((long long)t * p.Hkv + h) * D, e0, e1);
+      }
+      if (!live) continue;
+      uint8_t* rec = p.cache + record_offset(slot, p.block_size, p.Hkv, h, R::kBytes);
+      const int row = (int)(slot & 15);
+      uint8_t* codes = rec + (value ? R::kV : R::kK) + row * R::kRow;
+      uint8_t* scales = rec + (value ? R::kVs : R::kKs) + row * R::kScaleRow;
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
-        const uint4* v = reinterpret_cast<const uint4*>(src + (g ? e1 : e0));
-        const uint4 a = v[0], b = v[1];
-        w[g][0] = a.x, w[g][1] = a.y, w[g][2] = a.z, w[g][3] = a.w;
-        w[g][4] = b.x, w[g][5] = b.y, w[g][6] = b.z, w[g][7] = b.w;
+        const uint4 c = encode_group(make_uint4(u.w[g][0], u.w[g][1], u.w[g][2], u.w[g][3]),
+                                     make_uint4(u.w[g][4], u.w[g][5], u.w[g][6], u.w[g][7]));
+        const int e = g ? e1 : e0;
+        *reinterpret_cast<uint2*>(codes + e / 2) = make_uint2(c.x, c.y);
+        scales[e / 16] = (uint8_t)c.z;
       }
-      if (kind < 2) {
-        if (turn) {
-          if (p.interleaved) {
+    } else {  // queries, two heads per lane
+      const uint32_t rest = it - kv_items;
+      const int t = (int)(rest / (uint32_t)p.q_chunks), chunk = (int)(rest - (uint32_t)t * p.q_chunks);
+      const int h = chunk * 2 * kHeads + head0;
+      const int pos = __ldg(p.positions + t);
+      Unit u[2];
 #pragma unroll
-            for (int g = 0; g < 2; ++g)
+      for (int i = 0; i < 2; ++i)
+        if (h + i * kHeads < p.Hq) u[i].load(p.q + t * p.q_row + (h + i * kHeads) * p.q_head, e0, e1);
+      if (turned && pos >= 0 && pos < p.max_pos) {
+        const float4* cos_row =
+            reinterpret_cast<const float4*>(p.rope + (long long)pos * 2 * p.half + 16 * unit);
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const float x0 = bf16_lo(w[g][i]), x1 = bf16_hi(w[g][i]);
-                const float ci = c[8 * g + i], si = s[8 * g + i];
-                w[g][i] = kind == 0 ? pack_bf16(x0 * ci - x1 * si, x1 * ci + x0 * si)
-                                    : pack_bf16(diff_of_products_odd(x0, ci, x1, si),
-                                                diff_of_products_odd(x1, ci, x0, -si));
-              }
-          } else {
+        for (int x = 0; x < 4; ++x) {
+          const float4 c = __ldg(cos_row + x), s = __ldg(cos_row + p.half / 4 + x);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float a0 = bf16_lo(w[0][i]), a1 = bf16_hi(w[0][i]);
-              const float b0 = bf16_lo(w[1][i]), b1 = bf16_hi(w[1][i]);
-              const float c0 = c[2 * i], c1 = c[2 * i + 1], s0 = s[2 * i], s1 = s[2 * i + 1];
-              if (kind == 0) {
-                w[0][i] = pack_bf16(a0 * c0 - b0 * s0, a1 * c1 - b1 * s1);
-                w[1][i] = pack_bf16(b0 * c0 + a0 * s0, b1 * c1 + a1 * s1);
-              } else {
-                w[0][i] = pack_bf16(diff_of_products_odd(a0, c0, b0, s0),
-                                    diff_of_products_odd(a1, c1, b1, s1));
-                w[1][i] = pack_bf16(diff_of_products_odd(b0, c0, a0, -s0),
-                                    diff_of_products_odd(b1, c1, a1, -s1));
-              }
-            }
-          }
-        }
-        uint16_t* out = kind == 0 ? p.q_out + ((long long)t * p.Hq + h) * D
-                        : p.k_out ? p.k_out + ((long long)t * p.Hkv + h) * D
-                                  : nullptr;
-        if (out) {
-#pragma unroll
-          for (int g = 0; g < 2; ++g) {
-            uint4* v = reinterpret_cast<uint4*>(out + (g ? e1 : e0));
-            v[0] = make_uint4(w[g][0], w[g][1], w[g][2], w[g][3]);
-            v[1] = make_uint4(w[g][4], w[g][5], w[g][6], w[g][7]);
-          }
+          for (int i = 0; i < 2; ++i) u[i].turn<kInterleaved, false>(x, c, s);
         }
       }
-      if (kind > 0 && live) {
-        uint8_t* rec = p.cache + record_offset(slot, p.block_size, p.Hkv, h, R::kBytes);
-        const int row = (int)(slot & 15);
-        uint8_t* codes = rec + (kind == 1 ? R::kK : R::kV) + row * R::kRow;
-        uint8_t* scales = rec + (kind == 1 ? R::kKs : R::kVs) + row * R::kScaleRow;
 #pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          uint2 cd;
-          uint32_t sc;
-          encode_group(w[g], cd, sc);
-          const int e = g ? e1 : e0;
-          *reinterpret_cast<uint2*>(codes + e / 2) = cd;
-          scales[e / 16] = (uint8_t)sc;
-        }
-      }
+      for (int i = 0; i < 2; ++i)
+        if (h + i * kHeads < p.Hq) u[i].store(p.q_out + ((long long)t * p.Hq + h + i * kHeads) * D, e0, e1);
     }
   }
 }
@@ -193,14 +206,13 @@ __global__ void __launch_bounds__(kThreads)
     kv_read_kernel(const uint8_t* cache, long long slots_end, int block_size, int Hkv,
                    const long long* slots, int n, uint16_t* k_out, uint16_t* v_out, uint32_t* err) {
   using R = Record<D>;
-  const long long total = (long long)n * Hkv * 2 * (D / 16);
-  for (long long i = (long long)blockIdx.x * kThreads + threadIdx.x; i < total;
-       i += (long long)gridDim.x * kThreads) {
+  const uint32_t total = (uint32_t)n * Hkv * (D / 8);  // the host keeps it below 2^32
+  for (uint32_t i = blockIdx.x * kThreads + threadIdx.x; i < total; i += gridDim.x * kThreads) {
     const int g = (int)(i % (D / 16));
-    const long long rest = i / (D / 16);
+    const uint32_t rest = i / (D / 16);
     const int kind = (int)(rest & 1);
-    const long long row = rest >> 1;  // t * Hkv + h
-    const int t = (int)(row / Hkv), h = (int)(row - (long long)t * Hkv);
+    const uint32_t row = rest >> 1;  // t * Hkv + h
+    const int t = (int)(row / (uint32_t)Hkv), h = (int)(row - (uint32_t)t * Hkv);
     uint16_t* out = kind ? v_out : k_out;
     const long long slot = __ldg(slots + t);
     const bool live = slot >= 0 && slot < slots_end;
@@ -223,7 +235,7 @@ __global__ void __launch_bounds__(kThreads)
         w[j] = pack_bf16(lo, hi);
       }
     }
-    uint4* v = reinterpret_cast<uint4*>(out + row * D + 16 * g);
+    uint4* v = reinterpret_cast<uint4*>(out + (long long)row * D + 16 * g);
     v[0] = make_uint4(w[0], w[1], w[2], w[3]);
     v[1] = make_uint4(w[4], w[5], w[6], w[7]);
   }
@@ -244,6 +256,7 @@ extern "C" int pe_kv_append(const pe_kv_append_args* a, void* stream) {
   if (a->block_size < 16 || a->block_size % 16 || a->num_blocks < 1 ||
       a->num_blocks > (INT64_MAX >> 8) / ((int64_t)a->Hkv * a->block_size * a->D))
     return PE_EINVAL;
+  if ((int64_t)a->T * ((int64_t)a->Hq + 2 * a->Hkv) > INT32_MAX / 16) return PE_EINVAL;
   if (a->rot_dim < 32 || a->rot_dim > a->D || a->rot_dim % 32 || a->max_pos < 1) return PE_EINVAL;
   if (a->T == 0) return PE_OK;
   if (!a->q || !a->k || !a->v || !a->positions || !a->slots || !a->rope || !a->cache || !a->q_out ||
@@ -259,7 +272,7 @@ extern "C" int pe_kv_append(const pe_kv_append_args* a, void* stream) {
   if (pe_host::device_info(&dev) != PE_OK) return PE_ECUDA;
   pe::AppendParams p;
   p.T = a->T, p.Hq = a->Hq, p.Hkv = a->Hkv, p.block_size = a->block_size;
-  p.half = a->rot_dim / 2, p.interleaved = a->interleaved != 0, p.max_pos = a->max_pos;
+  p.half = a->rot_dim / 2, p.max_pos = a->max_pos;
   p.slots_end = a->num_blocks * a->block_size;
   p.q_row = a->q_row, p.q_head = a->q_head, p.k_row = a->k_row, p.k_head = a->k_head;
   p.v_row = a->v_row, p.v_head = a->v_head;
@@ -273,17 +286,17 @@ extern "C" int pe_kv_append(const pe_kv_append_args* a, void* stream) {
   p.q_out = static_cast<uint16_t*>(a->q_out);
   p.k_out = static_cast<uint16_t*>(a->k_out);
   p.err = a->err;
-  const int heads = a->Hq + 2 * a->Hkv, per_warp = 1024 / a->D;
-  p.chunks = (heads + per_warp - 1) / per_warp;
-  const long long warps = (long long)a->T * p.chunks;
+  const int per_warp = 1024 / a->D;
+  p.kv_chunks = (2 * a->Hkv + per_warp - 1) / per_warp;
+  p.q_chunks = (a->Hq + 2 * per_warp - 1) / (2 * per_warp);
+  const long long warps = (long long)a->T * (p.kv_chunks + p.q_chunks);
   const long long want = (warps + pe::kWarps - 1) / pe::kWarps;
   const long long most = (long long)dev.sm_count * 8;
   const int grid = (int)(want < most ? want : most);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (a->D == 64)
-    pe::kv_append_kernel<64><<<grid, pe::kThreads, 0, s>>>(p);
-  else
-    pe::kv_append_kernel<128><<<grid, pe::kThreads, 0, s>>>(p);
+  auto kernel = a->D == 64 ? (a->interleaved ? pe::kv_append_kernel<64, true> : pe::kv_append_kernel<64, false>)
+                           : (a->interleaved ? pe::kv_append_kernel<128, true> : pe::kv_append_kernel<128, false>);
+  kernel<<<grid, pe::kThreads, 0, s>>>(p);
   return pe_host::launch_status();
 }
 
@@ -291,7 +304,8 @@ extern "C" int pe_kv_read(const void* cache, int64_t num_blocks, int32_t block_s
                           int32_t D, const int64_t* slots, int32_t n, void* k_out, void* v_out,
                           uint32_t* err, void* stream) {
   if (n < 0 || Hkv < 1 || (D != 64 && D != 128) || block_size < 16 || block_size % 16 ||
-      num_blocks < 1 || num_blocks > (INT64_MAX >> 8) / ((int64_t)Hkv * block_size * D))
+      num_blocks < 1 || num_blocks > (INT64_MAX >> 8) / ((int64_t)Hkv * block_size * D) ||
+      (int64_t)n * Hkv > INT32_MAX / 32)
     return PE_EINVAL;
   if (n == 0) return PE_OK;
   if (!cache || !slots || !err) return PE_EINVAL;
