@@ -122,7 +122,7 @@ struct Unit {
 };
 
 template <int D, bool kInterleaved>
-__global__ void __launch_bounds__(kThreads, 3) kv_append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(kThreads, 2) kv_append_kernel(const AppendParams p) {
   using R = Record<D>;
   constexpr int kUnits = D / 32, kHeads = 32 / kUnits;
   const int lane = threadIdx.x & 31;
