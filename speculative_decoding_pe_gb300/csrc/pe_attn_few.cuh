@@ -358,6 +358,7 @@ __global__ void __launch_bounds__(256, 2) attn_few_kernel(const CachedParams p) 
       for (int e = 0; e < 2; ++e) {
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) l[b][e] += __shfl_xor_sync(0xffffffffu, l[b][e], d);
+        if (l[b][e] != l[b][e] && m[b][e] == -INFINITY) m[b][e] = 0.0f;  // a NaN is not a row that saw no key
         if (r == 0) c.m[warp][8 * b + 2 * cc + e] = m[b][e], c.l[warp][8 * b + 2 * cc + e] = l[b][e];
       }
     __syncthreads();

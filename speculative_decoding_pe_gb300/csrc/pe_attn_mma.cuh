@@ -8,10 +8,9 @@
 //   l = l 2^(m - m') + sum P;  O = O 2^(m - m') + P V;  out = O / l.
 // m need not be the maximum: any m gives the same quotient as long as P stays in
 // range, so it is taken from an item's first tile and then only when a score
-// passes it by kSlack; O is rarely rescaled.  S, O, m and
-// l are fp32.  P is rounded to bf16 for the product, each weight by at most 2^-8
-// of itself however small it is (an f16 would lose the small ones), which is
-// what the output is rounded by.
+// passes it by kSlack; O is rarely rescaled.  S, O, m and l are fp32.  P is
+// rounded to bf16 for the product, each weight by at most 2^-8 of itself however
+// small it is (an f16 would lose the small ones), as the output is.
 //
 // Work.  An item is (request, key head, up to 256 rows); its unit is a tile of
 // 128 keys.  All units of the call are one line that the CTAs cut into equal
@@ -428,6 +427,7 @@ __device__ void softmax_rows(const Line<kCached>& line, Control& c, const Softma
       if (!wait_warp(&c.o_full[s][(visit - 1) & 3], ((visit - 1) >> 2) & 1, dead)) return;
       tc_fence_after();
     }
+    if (l != l && m == -INFINITY) m = 0.0f;  // a NaN is not a row that saw no key
     if (!live) m = -INFINITY, l = 0.0f;
     const bool whole = w.t0 == 0 && w.t1 == w.tiles;
     const int slot_row = halves ? row : s * kTile + row;

@@ -320,6 +320,25 @@ def test_values_that_are_not_finite_reach_the_rows_that_see_them():
         assert bool(got.isfinite().all())
 
 
+@pytest.mark.parametrize("what", [float("nan"), float("inf")])
+@pytest.mark.parametrize("kind", ["token", "draft", "prompt"])
+def test_a_query_that_is_not_finite_keeps_to_its_row(kind, what):
+    """Its row is NaN, whole or put together from parts of a long context; the others are as they were."""
+    make = lambda: (Prompt([3000, 40], 8, 2, 64, 7) if kind == "prompt" else  # noqa: E731
+                    Cached([[9000], [33]] if kind == "token" else [draft(9000, 3), draft(33, 7)], 8, 2, 64, seed=7, uniform=True))
+    want = make().run().clone()
+    c = make()
+    rows = (2990, 3000) if kind == "prompt" else (0, 1) if kind == "token" else (1, 15)
+    for t in rows:
+        c.q[t, 5, 7] = what
+    got = c.run()
+    torch.cuda.synchronize()
+    for t in rows:
+        assert bool(got[t, 5].isnan().all())
+        got[t, 5] = want[t, 5]
+    assert torch.equal(got.view(torch.int16), want.view(torch.int16))
+
+
 @pytest.mark.parametrize("kind", ["token", "draft", "prompt"])
 def test_streams_graphs_and_a_reused_workspace(kind):
     """One workspace through calls of changing size, on another stream, and in
