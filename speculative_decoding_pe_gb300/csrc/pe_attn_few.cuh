@@ -44,7 +44,7 @@ template <int kWarps, int kStages>
 struct FewControl {
   uint64_t full[kWarps][kStages];
   Walk start;
-  long long total, parts;
+  long long total, parts, snap;
   int dead, last;
   float m[kWarps][16], l[kWarps][16];
 };
@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(256, 2) attn_few_kernel(const CachedParams p) 
   if (threadIdx.x == 0) c.dead = 0;
   mbar_init_fence();
   Line<true, 16> line{p.seg, p.Hkv, p.Hq / p.Hkv, kTile / (p.Hq / p.Hkv), nullptr, nullptr};
-  if (!plan(line, F::kMinRecords, c, prefix, keys, reinterpret_cast<long long*>(smem), p.positions, p.is_rejected, p.table_keys, p.err))
+  if (!plan(line, F::kMinRecords, F::kMinRecords / 2, c, prefix, keys, reinterpret_cast<long long*>(smem), p.positions, p.is_rejected, p.table_keys, p.err))
     return;
   if (c.start.u >= c.start.end) return;
 
@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(256, 2) attn_few_kernel(const CachedParams p) 
     __syncthreads();
     const bool whole = w.t0 == 0 && w.t1 == w.tiles;
     Reach at{0, 0};
-    if (!whole) at = reach(w, c.parts, c.total);
+    if (!whole) at = reach(w, c);
     // partial results: [slot][row][D] sums, then (maximum, total) [row]
     auto slot = [&](int part, int i) {
       return reinterpret_cast<float*>(p.ws + AttnWorkspace::kPartials) + (2LL * part + i) * (16 * (D + 2));

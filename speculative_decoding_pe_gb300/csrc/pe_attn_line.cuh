@@ -3,7 +3,9 @@
 // An item is (request, key head, a block of rows); its units are blocks of
 // kUnit keys.  The units of all items form one line, request after request,
 // and part c of n is units [c U / n, (c + 1) U / n): equal parts whatever the
-// lengths are.  No plan is made on the host, which does not know the lengths:
+// lengths are, but that an end less than `snap` units from an item's end moves
+// there, because a piece of an item costs a CTA as much as some units do (one
+// token over 4000 keys: 16.4 us against 13.2).  No plan is made on the host, which does not know the lengths:
 // every CTA sums them up for itself.
 #pragma once
 
@@ -13,23 +15,30 @@ namespace pe {
 
 constexpr int kTile = 128;        // rows of a stream; keys of a tile
 
+// a / b, in 32 bits where they do (a 64-bit division takes some 500 cycles).
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 // sum_{i=1..k} ceil(i w / 128)
 __device__ __forceinline__ long long sum_tiles(long long k, long long w) {
   // sum_{i=0..k-1} floor((a i + b) / m), with ceil(x / 128) = floor((x + 127) / 128)
   long long n = k, m = kTile, a = w, b = w + kTile - 1, sum = 0;
   for (;;) {
     if (a >= m) {
-      sum += (n - 1) * n / 2 * (a / m);
-      a %= m;
+      const long long c = quotient(a, m);
+      sum += (n - 1) * n / 2 * c;
+      a -= c * m;
     }
     if (b >= m) {
-      sum += n * (b / m);
-      b %= m;
+      const long long c = quotient(b, m);
+      sum += n * c;
+      b -= c * m;
     }
     const long long y = a * n + b;
     if (y < m) return sum;
-    n = y / m;
-    b = y % m;
+    n = quotient(y, m);
+    b = y - n * m;
     const long long t = m;
     m = a;
     a = t;
@@ -61,11 +70,6 @@ struct Line {
     return (int)max(1LL, (n + kUnit - 1) / kUnit);
   }
 };
-
-// a / b, in 32 bits where they do (a 64-bit division takes some 500 cycles).
-__device__ __forceinline__ long long quotient(long long a, long long b) {
-  return ((a | b) >> 32) == 0 ? (long long)((uint32_t)a / (uint32_t)b) : a / b;
-}
 
 // One CTA's walk over its part of the line.
 struct Walk {
@@ -133,7 +137,7 @@ __device__ Walk walk_begin(const Line<kCached, kUnit>& line, long long u, long l
 // Every CTA lays the line out for itself (a few loads per request) and finds
 // its part.  False when the offsets are no partition of the rows.
 template <bool kCached, int kUnit, class Control>
-__device__ bool plan(Line<kCached, kUnit>& line, long long min_units, Control& c, long long* prefix, int* keys, long long* sums,
+__device__ bool plan(Line<kCached, kUnit>& line, int min_units, int most_snap, Control& c, long long* prefix, int* keys, long long* sums,
                      const int32_t* positions, const uint8_t* is_rejected, int table_keys,
                      uint32_t* err) {
   const int tid = threadIdx.x, n = blockDim.x, B = line.seg.B;
@@ -202,26 +206,47 @@ __device__ bool plan(Line<kCached, kUnit>& line, long long min_units, Control& c
     __syncthreads();
   }
   __syncwarp();
-  if (tid == 0) {
+  __syncwarp();
+  if (tid < 2) {  // the part's begin and end
+    const long long total = c.total;
     // a part below min_units would spend its time on partial results
-    c.parts = max(1LL, min((long long)gridDim.x, quotient(c.total, min_units)));
-    const long long part = blockIdx.x;
-    if (part < c.parts)
-      c.start = walk_begin(line, quotient(part * c.total, c.parts), quotient((part + 1) * c.total, c.parts));
-    else
-      c.start.u = c.start.end = 0;
+    const long long parts = max(1LL, min((long long)gridDim.x, quotient(total, min_units)));
+    const long long snap = min(quotient(total, 2 * parts), (long long)most_snap);
+    long long u = min(parts, (long long)blockIdx.x + tid);
+    u = quotient(u * total, parts);
+    Walk w = walk_begin(line, u, total);
+    if (u < total) {
+      const int r = w.t0, rest = w.tiles - w.t0;
+      if (r <= snap && r < rest) {
+        u -= r;
+        w.t0 = w.t1 = 0;
+      } else if (rest <= snap) {
+        u += rest;
+        w.t0 = w.t1 = w.tiles;
+      }
+    }
+    const long long end = __shfl_sync(3u, u, 1);
+    if (tid == 0) {
+      w.u = u, w.end = end;
+      c.start = w;
+      c.parts = parts;
+      c.snap = snap;
+    }
   }
   __syncthreads();
   return true;
 }
 
-// The parts that an item reaches over, from the walk after its segment.
+// The parts that a cut item reaches over, from the walk after its segment: those
+// around the ends c U / parts that lie more than `snap` units inside it.
 struct Reach {
   int first, last;
 };
-__device__ __forceinline__ Reach reach(const Walk& w, long long parts, long long total) {
+template <class Control>
+__device__ __forceinline__ Reach reach(const Walk& w, const Control& c) {
   const long long u0 = w.u - w.t1, u1 = u0 + w.tiles;  // w.u: the unit after t1
-  return {(int)quotient((u0 + 1) * parts - 1, total), (int)quotient(u1 * parts - 1, total)};
+  return {(int)quotient((u0 + c.snap + 1) * c.parts + c.total - 1, c.total) - 1,
+          (int)quotient((u1 - c.snap) * c.parts - 1, c.total)};
 }
 
 }  // namespace pe

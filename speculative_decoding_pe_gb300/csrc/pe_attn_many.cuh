@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) attn_many_kernel(const Cached
   }
   const int G = p.Hq / p.Hkv;
   Line<true> line{p.seg, p.Hkv, G, kTile / G, nullptr, nullptr};
-  if (!plan(line, 2, c, prefix, keys, reinterpret_cast<long long*>(smem), p.positions, p.is_rejected, p.table_keys,
+  if (!plan(line, 2, 2, c, prefix, keys, reinterpret_cast<long long*>(smem), p.positions, p.is_rejected, p.table_keys,
             p.err))
     return;
   if (c.start.u >= c.start.end) return;  // fewer parts than CTAs

@@ -106,7 +106,7 @@ struct AttnControl {
   // may one warp of the others; a phase two away would look like the awaited one
   uint64_t s_full[2][4], p_half[2][4], p_full[2][4], o_full[2][4];
   Walk start;
-  long long total, parts;
+  long long total, parts, snap;
   uint32_t tmem;
   int dead, last[2];
   uint32_t not_finite[8][12];  // values of a masked tile: tokens that hold an infinity or NaN
@@ -247,13 +247,13 @@ __device__ __forceinline__ float2 join(float& m, float& l, float2 other) {
   const float mn = fmaxf(m, other.x);  // -infinity: saw no key
   const float f = m == -INFINITY ? 0.0f : exp2_approx(m - mn);
   const float g = other.x == -INFINITY ? 0.0f : exp2_approx(other.x - mn);
-  l = (f > 0.0f ? l * f : 0.0f) + (g > 0.0f ? other.y * g : 0.0f);
+  l = (f != 0.0f ? l * f : 0.0f) + (g != 0.0f ? other.y * g : 0.0f);
   m = mn;
   return make_float2(f, g);
 }
 // x f + y g, where a factor of zero takes its term out whatever it is.
 __device__ __forceinline__ float mix(float x, float f, float y, float g) {
-  return (f > 0.0f ? x * f : 0.0f) + (g > 0.0f ? y * g : 0.0f);
+  return (f != 0.0f ? x * f : 0.0f) + (g != 0.0f ? y * g : 0.0f);
 }
 
 // Both streams' warps; orders their writes.  False: given up.
@@ -492,7 +492,7 @@ __device__ void softmax_rows(const Line<kCached>& line, Control& c, const Softma
         fg = join(m, l, __ldcg(partial_ml<D>(half, half_row)));
       }
       const float inv = inverse(l);
-      float4* mine = whole ? nullptr : partial<D>(p.ws, blockIdx.x, (int)blockIdx.x == reach(w, c.parts, c.total).first);
+      float4* mine = whole ? nullptr : partial<D>(p.ws, blockIdx.x, (int)blockIdx.x == reach(w, c).first);
 #pragma unroll 1
       for (int q = 0; q < D; q += 32) {
         float o[32];
@@ -520,7 +520,7 @@ __device__ void softmax_rows(const Line<kCached>& line, Control& c, const Softma
     tc_fence_before();
     if (whole) continue;
     // ---- the item is cut: the CTA that comes last adds the parts, in order
-    const Reach at = reach(w, c.parts, c.total);  // the first part's counter counts
+    const Reach at = reach(w, c);  // the first part's counter counts
     if (!join_streams(c, joins)) return;
     if (threadIdx.x == 0) {
       unsigned* count = reinterpret_cast<unsigned*>(p.ws) + at.first;

@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1)
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) c.init(1, 1, 1);
   Line<false> line{p.seg, p.Hkv, p.G, kTile / p.G, nullptr, nullptr};
-  if (!plan(line, 2, c, prefix, nullptr, reinterpret_cast<long long*>(smem), nullptr, nullptr, 0, p.softmax.err)) return;
+  if (!plan(line, 2, 2, c, prefix, nullptr, reinterpret_cast<long long*>(smem), nullptr, nullptr, 0, p.softmax.err)) return;
   if (c.start.u >= c.start.end) return;  // fewer parts than CTAs
   if (warp == 8) tmem_alloc(&c.tmem, S::kColumns);
   tc_fence_before();
