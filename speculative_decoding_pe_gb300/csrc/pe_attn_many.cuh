@@ -15,6 +15,11 @@
 namespace pe {
 
 constexpr int kManyThreads = 20 * 32;
+__device__ __forceinline__ void store_shared(uint32_t at, const uint32_t (&x)[4]) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3])
+               : "memory");
+}
+
 constexpr int kConverters = 4;  // warps for keys, and as many for values
 
 template <int kRawStages>
@@ -73,33 +78,40 @@ __device__ void bring_records(const Line<true>& line, Control& c, Raw& raw, cons
 
 // Codes of one token, D elements, into row `row` of an operand tile: as f16 (the
 // keys, next to f16 queries) or as bf16 (the values, next to bf16 weights).
-// Both are exact.  Rolled: the roles of this kernel share an instruction cache.
-template <int D, bool kBf16>
+// Both are exact.  Values rolled, keys two steps at a time: the roles of this
+// kernel share an instruction cache (b64 drafts 391 us; values unrolled too, 401;
+// keys rolled too, 401).
+template <int D, bool kBf16, int kUnroll = kBf16 ? 1 : 2>
 __device__ __forceinline__ void put_codes(uint8_t* tile, int row, const uint8_t* codes, const uint8_t* scales,
                                           bool valid) {
-#pragma unroll 1
+  // chunk c (8 elements) of a row lies at c ^ (row & 7)
+  uint32_t at = smem_addr(tile) + row * 128 + (row & 7) * 16;
+  uint32_t chunk = 0;
+#pragma unroll kUnroll
   for (int i = 0; i < D / 32; ++i) {
     const uint4 y = reinterpret_cast<const uint4*>(codes)[i];
     // past the request's keys lies anything, a NaN too (codes are finite)
     const uint32_t two = valid ? reinterpret_cast<const uint16_t*>(scales)[i] : 0u;
     const uint32_t s[2] = {e4m3_f16x2(two & 0xffu), e4m3_f16x2(two >> 8)};
     const uint32_t w[4] = {y.x, y.y, y.z, y.w};
-    uint8_t* to = tile + (i / 2) * kTile * 128 + row * 128;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {  // 8 elements: 16 bytes
       uint32_t x[4];
       e2m1x8_f16(w[q], x);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        x[e] = hmul2(x[e], s[q / 2]);
         if (kBf16) {
           float lo, hi;
-          f16x2_to_f32(x[e], lo, hi);
+          mul_f16x2_f32(x[e], s[q / 2], lo, hi);
           x[e] = pack_bf16(lo, hi);
+        } else {
+          x[e] = hmul2(x[e], s[q / 2]);
         }
       }
-      *reinterpret_cast<uint4*>(to + ((((i & 1) * 4 + q) ^ (row & 7)) * 16)) = make_uint4(x[0], x[1], x[2], x[3]);
+      store_shared(at ^ (chunk + q * 16), x);
     }
+    chunk ^= 64;
+    if (i & 1) at += kTile * 128;
   }
 }
 

@@ -95,6 +95,14 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
   return d;
 }
 
+// Products of two f16 pairs as fp32 (exact).
+__device__ __forceinline__ void mul_f16x2_f32(uint32_t x, uint32_t y, float& lo, float& hi) {
+  asm("{\n\t.reg .f16 a, b, c, d;\n\tmov.b32 {a, b}, %2;\n\tmov.b32 {c, d}, %3;\n\t"
+      "fma.rn.f32.f16 %0, a, c, %4;\n\tfma.rn.f32.f16 %1, b, d, %4;\n\t}"
+      : "=f"(lo), "=f"(hi)
+      : "r"(x), "r"(y), "f"(0.0f));
+}
+
 __device__ __forceinline__ void f16x2_to_f32(uint32_t w, float& lo, float& hi) {
   asm("{\n\t.reg .f16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
       : "=f"(lo), "=f"(hi)
