@@ -14,23 +14,13 @@ struct Segments {
   int T, B;
   __device__ int begin(int b) const { return offsets ? __ldg(offsets + b) : b * (T / B); }
   __device__ int end(int b) const { return offsets ? __ldg(offsets + b + 1) : (b + 1) * (T / B); }
-  // The request that row t belongs to (offsets valid).
-  __device__ int request(int t) const {
-    if (!offsets) return t / (T / B);
-    int lo = 0, hi = B - 1;  // the last b with begin(b) <= t
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (__ldg(offsets + mid) <= t) lo = mid; else hi = mid - 1;
-    }
-    return lo;
-  }
 };
 
 // Keys that a row of the cached attention sees.
 __device__ __forceinline__ int row_limit(const int32_t* positions, const uint8_t* is_rejected,
                                          int t, int table_keys, bool& bad) {
-  if (is_rejected && __ldg(is_rejected + t)) return 0;
-  const int pos = __ldg(positions + t);
+  const int gone = is_rejected ? __ldg(is_rejected + t) : 0, pos = __ldg(positions + t);  // (both loads at once)
+  if (gone) return 0;
   if (pos < 0) {
     bad = true;
     return 0;
@@ -56,6 +46,7 @@ struct CachedParams {
   uint16_t* out;
   uint8_t* ws;
   uint32_t* err;
+  int together;  // the CTAs run at once and add up cut items together
 };
 
 // The power of two to take out of a row whose largest magnitude is `most`, as

@@ -4,6 +4,36 @@
 
 namespace {
 
+// Are most items cut into several parts?  (Items: at most those of B requests that
+// fill their last one by a token.)
+bool cut_often(const pe::CachedParams& p, int grid) {
+  const int64_t span = pe::kTile / (p.Hq / p.Hkv);
+  return 2 * p.Hkv * (p.seg.B + p.seg.T / span) <= grid;
+}
+
+// Together: cooperative, so that every CTA runs at once.  A refusal (other work
+// holds part of the GPU) leaves no error behind.
+template <class Kernel>
+int launch(Kernel* kernel, int grid, int threads, int bytes, pe::CachedParams p, cudaStream_t s) {
+  p.together = cut_often(p, grid);
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeCooperative;
+  attr.val.cooperative = 1;
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = p.together ? 1 : 0;
+  if (p.together && cudaLaunchKernelEx(&cfg, kernel, p) != cudaSuccess) {
+    (void)cudaGetLastError();
+    p.together = cfg.numAttrs = 0;
+  }
+  if (!p.together) (void)cudaLaunchKernelEx(&cfg, kernel, p);
+  return pe_host::launch_status();
+}
+
 template <int D, int NB>
 int launch_few(const pe::CachedParams& p, int sms, cudaStream_t s) {
   static std::atomic<unsigned long long> allowed{0};
@@ -11,8 +41,7 @@ int launch_few(const pe::CachedParams& p, int sms, cudaStream_t s) {
   if (!pe_host::allow_smem(pe::attn_few_kernel<D, NB>, most, allowed)) return PE_ECUDA;
   const int bytes = pe::FewShape<D>::kBytes + 12 * (p.seg.B + 1);
   const int grid = 2 * (sms < pe::kAttnCtas ? sms : pe::kAttnCtas);
-  pe::attn_few_kernel<D, NB><<<grid, 256, bytes, s>>>(p);
-  return pe_host::launch_status();
+  return launch(pe::attn_few_kernel<D, NB>, grid, 256, bytes, p, s);
 }
 
 template <int D>
@@ -21,8 +50,7 @@ int launch_many(const pe::CachedParams& p, int sms, cudaStream_t s) {
   constexpr int kData = pe::AttnShape<D, true>::kData + 1024;
   if (!pe_host::allow_smem(pe::attn_many_kernel<D>, kData + 12 * (PE_MAX_ATTN_B + 1), allowed)) return PE_ECUDA;
   const int grid = sms < pe::kAttnCtas ? sms : pe::kAttnCtas;
-  pe::attn_many_kernel<D><<<grid, pe::kManyThreads, kData + 12 * (p.seg.B + 1), s>>>(p);
-  return pe_host::launch_status();
+  return launch(pe::attn_many_kernel<D>, grid, pe::kManyThreads, kData + 12 * (p.seg.B + 1), p, s);
 }
 
 }  // namespace

@@ -45,7 +45,8 @@ struct FewControl {
   uint64_t full[kWarps][kStages];
   Walk start;
   long long total, parts, snap;
-  int dead, last;
+  int dead, last, cuts;
+  Cut cut[2];
   float m[kWarps][16], l[kWarps][16];
 };
 
@@ -75,7 +76,7 @@ __global__ void __launch_bounds__(256, 2) attn_few_kernel(const CachedParams p) 
   int* keys = reinterpret_cast<int*>(prefix + p.seg.B + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, cc = lane & 3;
   if (lane < F::kStages) mbar_init(&c.full[warp][lane], 1);
-  if (threadIdx.x == 0) c.dead = 0;
+  if (threadIdx.x == 0) c.dead = c.cuts = 0;
   mbar_init_fence();
   Line<true, 16> line{p.seg, p.Hkv, p.Hq / p.Hkv, kTile / (p.Hq / p.Hkv), nullptr, nullptr};
   if (!plan(line, F::kMinRecords, F::kMinRecords / 2, c, prefix, keys, reinterpret_cast<long long*>(smem), p.positions, p.is_rejected, p.table_keys, p.err))
@@ -139,6 +140,22 @@ __global__ void __launch_bounds__(256, 2) attn_few_kernel(const CachedParams p) 
 #pragma unroll 1
   for (int i = 0; i < F::kStages; ++i) issue();
 
+  // partial results: [slot][row][D] sums, then (maximum, total) [row]
+  auto slot = [&](int part, int i) {
+    return reinterpret_cast<float*>(p.ws + AttnWorkspace::kPartials) + (2LL * part + i) * (16 * (D + 2));
+  };
+  auto part_of = [&](const Reach& at, int part, int row, int d, float(&x)[2]) {
+    const float* from = slot(part, part == at.first);
+    const float2 y = __ldcg(reinterpret_cast<const float2*>(from + row * D + d));
+    x[0] = y.x, x[1] = y.y;
+    return __ldcg(reinterpret_cast<const float2*>(from + 16 * D + 2 * row));
+  };
+  auto finish = [&](const Walk& w, int row, int d, const Running<2>& sum) {
+    const float inv = sum.l > 0.0f ? 1.0f / sum.l : (sum.l == sum.l ? 0.0f : sum.l);
+    *reinterpret_cast<uint32_t*>(
+        p.out + ((long long)(w.first + row / line.G) * p.Hq + w.h * line.G + row % line.G) * D + d) =
+        pack_bf16(sum.o[0] * inv, sum.o[1] * inv);
+  };
   Walk w = c.start;
   while (walk_next(line, w)) {
     const int G = line.G, L = keys[w.b];
@@ -365,10 +382,6 @@ __global__ void __launch_bounds__(256, 2) attn_few_kernel(const CachedParams p) 
     const bool whole = w.t0 == 0 && w.t1 == w.tiles;
     Reach at{0, 0};
     if (!whole) at = reach(w, c);
-    // partial results: [slot][row][D] sums, then (maximum, total) [row]
-    auto slot = [&](int part, int i) {
-      return reinterpret_cast<float*>(p.ws + AttnWorkspace::kPartials) + (2LL * part + i) * (16 * (D + 2));
-    };
     float* mine = slot(blockIdx.x, (int)blockIdx.x == at.first);
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
@@ -425,42 +438,63 @@ __global__ void __launch_bounds__(256, 2) attn_few_kernel(const CachedParams p) 
       }
     }
     if (!whole) {
-      if (threadIdx.x == 0) {
-        unsigned* count = reinterpret_cast<unsigned*>(p.ws) + at.first;
-        const unsigned old = atom_add_acq_rel_u32(count, 1), want = at.last - at.first;
-        if (old > want) atomicOr(p.err, PE_ERR_WORKSPACE);
-        c.last = old == want;
-        if (c.last) *count = 0;
-      }
+      if (threadIdx.x == 0) c.last = arrive_part(p.ws, w, at, p.together, c, p.err);
       __syncthreads();
       if (c.last) {
         for (int i = threadIdx.x; i < nrows * (D / 2); i += 256) {
           const int row = i / (D / 2), d = 2 * (i % (D / 2));
-          // first the maximum, then the sums: the loads of eight parts at a time
-          float top = -INFINITY, total = 0.0f;
-          float2 sum = make_float2(0.0f, 0.0f);
-          auto ml_of = [&](int part) {
-            return __ldcg(reinterpret_cast<const float2*>(slot(part, part == at.first) + 16 * D + 2 * row));
-          };
-#pragma unroll 8
-          for (int part = at.first; part <= at.last; ++part) top = fmaxf(top, ml_of(part).x);
+          Running<2> sum;
 #pragma unroll 8
           for (int part = at.first; part <= at.last; ++part) {
-            const float2 ml = ml_of(part);
-            const float2 y = __ldcg(reinterpret_cast<const float2*>(slot(part, part == at.first) + row * D + d));
-            const bool any = ml.x != -INFINITY;  // the others hold what they like
-            const float f = any ? exp2_approx(ml.x - top) : 0.0f;
-            total += any ? ml.y * f : 0.0f;
-            sum.x += any ? y.x * f : 0.0f, sum.y += any ? y.y * f : 0.0f;
+            float x[2];
+            const float2 ml = part_of(at, part, row, d, x);
+            sum.add(ml.x, ml.y, x);
           }
-          const float inv = total > 0.0f ? 1.0f / total : (total == total ? 0.0f : total);
-          *reinterpret_cast<uint32_t*>(
-              p.out + ((long long)(w.first + row / G) * p.Hq + w.h * G + row % G) * D + d) =
-              pack_bf16(sum.x * inv, sum.y * inv);
+          finish(w, row, d, sum);
         }
       }
       __syncthreads();
     }
+  }
+  if (p.together) {  // a warp for two elements, a lane for every 32nd part: in flight at once
+    const int cuts = c.cuts;
+    unsigned before[2] = {};
+    if (threadIdx.x == 0) {
+      c.last = 1;
+      for (int k = 0; k < cuts; ++k) c.last &= await_parts(p.ws, c.cut[k].at, p.err);
+      for (int k = 0; k < cuts; ++k) before[k & 1] = seen_parts(p.ws, c.cut[k].at);
+    }
+    __syncthreads();
+    int from[2] = {0, 0}, n[2] = {0, 0};  // of each item: pairs of elements
+    for (int k = 0; k < 2; ++k)
+      if (k < cuts && c.last) {
+        const Reach& at = c.cut[k].at;
+        const int parts = at.last - at.first + 1, share = blockIdx.x - at.first;
+        const int all = c.cut[k].w.rows * line.G * (D / 2);
+        from[k] = all * share / parts;
+        n[k] = all * (share + 1) / parts - from[k];
+      }
+#pragma unroll 1
+    for (int x = warp; x < n[0] + n[1]; x += F::kWarps) {
+      const int k = x >= n[0], i = k ? from[1] + x - n[0] : from[0] + x;
+      const int row = i / (D / 2), d = 2 * (i % (D / 2));
+      const Reach at = c.cut[k].at;
+      Running<2> sum;
+#pragma unroll 1
+      for (int part0 = at.first + lane; part0 - lane <= at.last; part0 += 64) {
+        float y[2][2];
+        float2 ml[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) ml[e] = part_of(at, min(part0 + 32 * e, at.last), row, d, y[e]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) sum.add(part0 + 32 * e <= at.last ? ml[e].x : -INFINITY, ml[e].y, y[e]);
+      }
+#pragma unroll 1
+      for (int e = 1; e < 32; e <<= 1) sum.add_lane(e);
+      if (lane == 0) finish(c.cut[k].w, row, d, sum);
+    }
+    if (threadIdx.x == 0)
+      for (int k = 0; k < cuts; ++k) clear_parts(p.ws, c.cut[k].at, before[k & 1]);
   }
   if (c.dead && threadIdx.x == 0) {  // what is still on its way arrives before the CTA leaves
     atomicOr(p.err, PE_ERR_TIMEOUT);

@@ -10,6 +10,8 @@
 #pragma once
 
 #include "pe_attn.cuh"
+#include "pe_tma.cuh"
+#include "pe_umma.cuh"
 
 namespace pe {
 
@@ -22,6 +24,11 @@ __device__ __forceinline__ long long quotient(long long a, long long b) {
 
 // sum_{i=1..k} ceil(i w / 128)
 __device__ __forceinline__ long long sum_tiles(long long k, long long w) {
+  if (k < (1 << 24) && (w & (w - 1)) == 0 && w <= kTile) {  // 1, ..., 1, 2, ..., 2, ...: 128 / w of each
+    const int shift = 31 - __clz(kTile / (int)w);
+    const long long q = k >> shift;
+    return ((q * (q + 1) / 2) << shift) + (k - (q << shift)) * (q + 1);
+  }
   // sum_{i=0..k-1} floor((a i + b) / m), with ceil(x / 128) = floor((x + 127) / 128)
   long long n = k, m = kTile, a = w, b = w + kTile - 1, sum = 0;
   for (;;) {
@@ -206,7 +213,6 @@ __device__ bool plan(Line<kCached, kUnit>& line, int min_units, int most_snap, C
     __syncthreads();
   }
   __syncwarp();
-  __syncwarp();
   if (tid < 2) {  // the part's begin and end
     const long long total = c.total;
     // a part below min_units would spend its time on partial results
@@ -248,5 +254,85 @@ __device__ __forceinline__ Reach reach(const Walk& w, const Control& c) {
   return {(int)quotient((u0 + c.snap + 1) * c.parts + c.total - 1, c.total) - 1,
           (int)quotient((u1 - c.snap) * c.parts - 1, c.total)};
 }
+
+// An item that was cut, and the parts that hold its partial results.
+struct Cut {
+  Walk w;
+  Reach at;
+};
+
+// How the parts of an item become one.  Whichever CTA comes last adds them all;
+// or, when every CTA of the call runs at once and most items are cut (`together`),
+// each CTA adds its share of the rows after its own part: one CTA alone would take
+// 4 us of a call with one token, 10 us of one with a draft.
+// The counter: arrivals in the low half, then CTAs that have taken their share.
+//
+// A partial result is there.  Does this CTA add them up now?  One thread.
+template <class Control>
+__device__ __forceinline__ bool arrive_part(uint8_t* ws, const Walk& w, const Reach& at, bool together, Control& c,
+                                            uint32_t* err) {
+  unsigned* count = reinterpret_cast<unsigned*>(ws) + at.first;
+  const unsigned old = atom_add_acq_rel_u32(count, 1), want = at.last - at.first;
+  if ((old & 0xffffu) > want) atomicOr(err, PE_ERR_WORKSPACE);
+  if (together) {
+    c.cut[c.cuts].w = w;
+    c.cut[c.cuts++].at = at;
+    return false;
+  }
+  if (old == want) *count = 0;
+  return old == want;
+}
+// Together: are all parts there (within the limit of a wait)?  One thread.
+__device__ __forceinline__ bool await_parts(uint8_t* ws, const Reach& at, uint32_t* err) {
+  const unsigned* count = reinterpret_cast<const unsigned*>(ws) + at.first;
+  const unsigned n = at.last - at.first + 1;
+  const unsigned long long t0 = global_ns();
+  for (;;) {
+    unsigned v;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(count) : "memory");
+    if ((v & 0xffffu) >= n) return true;
+    if (global_ns() - t0 > kWaitLimitNs) {
+      atomicOr(err, PE_ERR_TIMEOUT);
+      return false;
+    }
+  }
+}
+// Together: this CTA has seen the counter; the last one that has clears it (in
+// clear_parts, so that nobody waits for the answer meanwhile).  One thread.
+__device__ __forceinline__ unsigned seen_parts(uint8_t* ws, const Reach& at) {
+  unsigned old;
+  asm volatile("atom.relaxed.gpu.global.add.u32 %0, [%1], %2;"
+               : "=r"(old)
+               : "l"(reinterpret_cast<unsigned*>(ws) + at.first), "r"(0x10000u)
+               : "memory");
+  return old >> 16;
+}
+__device__ __forceinline__ void clear_parts(uint8_t* ws, const Reach& at, unsigned before) {
+  if (before == (unsigned)(at.last - at.first)) reinterpret_cast<unsigned*>(ws)[at.first] = 0;
+}
+
+// A running quotient: sums, their maximum and total; and the same of more parts.
+// A factor of zero takes its term out whatever that is.
+template <int N>
+struct Running {
+  float m = -INFINITY, l = 0.0f, o[N] = {};
+  __device__ __forceinline__ void add(float m2, float l2, const float (&o2)[N]) {
+    const float top = fmaxf(m, m2);
+    const float f = m == -INFINITY ? 0.0f : exp2_approx(m - top);
+    const float g = m2 == -INFINITY ? 0.0f : exp2_approx(m2 - top);
+    l = (f != 0.0f ? l * f : 0.0f) + (g != 0.0f ? l2 * g : 0.0f);
+#pragma unroll
+    for (int i = 0; i < N; ++i) o[i] = (f != 0.0f ? o[i] * f : 0.0f) + (g != 0.0f ? o2[i] * g : 0.0f);
+    m = top;
+  }
+  // with the lane `d` away
+  __device__ __forceinline__ void add_lane(int d) {
+    float o2[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) o2[i] = __shfl_xor_sync(0xffffffffu, o[i], d);
+    const float m2 = __shfl_xor_sync(0xffffffffu, m, d), l2 = __shfl_xor_sync(0xffffffffu, l, d);
+    add(m2, l2, o2);
+  }
+};
 
 }  // namespace pe

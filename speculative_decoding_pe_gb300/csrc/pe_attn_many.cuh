@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(kManyThreads, 1) attn_many_kernel(const Cached
     a.Hq = p.Hq, a.table_keys = p.table_keys, a.scale_log2 = p.scale_log2;
     a.positions = p.positions, a.is_rejected = p.is_rejected;
     a.v = nullptr, a.v_row = a.v_head = 0;
-    a.out = p.out, a.ws = p.ws, a.err = p.err;
+    a.out = p.out, a.ws = p.ws, a.err = p.err, a.together = p.together;
     softmax_rows<D, true>(line, c, a, warp >> 2);
   } else if (warp == 8) {
     if (elect_one()) issue_products<D, true>(line, c, smem_addr(smem));
@@ -259,6 +259,14 @@ __global__ void __launch_bounds__(kManyThreads, 1) attn_many_kernel(const Cached
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  if (p.together) {
+    // as many registers as the compiler counts on: the softmax gives back first
+    if (warp < 8)
+      give_registers<96>();
+    else
+      take_registers<96>();
+    if (!c.dead) add_shares<D>(line, c, p);
+  }
   if (c.dead) leave_after_timeout<D, true>(c, p.err);
   if (warp == 8) tmem_dealloc(c.tmem, S::kColumns);
 }

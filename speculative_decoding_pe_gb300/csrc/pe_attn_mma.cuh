@@ -108,7 +108,8 @@ struct AttnControl {
   Walk start;
   long long total, parts, snap;
   uint32_t tmem;
-  int dead, last[2];
+  int dead, last[2], there, cuts;
+  Cut cut[2];
   uint32_t not_finite[8][12];  // values of a masked tile: tokens that hold an infinity or NaN
   int any_not_finite[8];       // of a segment
   float row_scale[4][kTile];   // kCached, by segment: the power of two taken out of a query row
@@ -137,7 +138,7 @@ struct AttnControl {
       }
     }
     mbar_init(&pair, 8);
-    dead = 0;
+    dead = cuts = 0;
     mbar_init_fence();
   }
 };
@@ -227,6 +228,7 @@ struct SoftmaxArgs {
   uint16_t* out;
   uint8_t* ws;
   uint32_t* err;
+  int together;                // kCached
 };
 
 // A partial result in the workspace: fp32 sums as float4 [D/4][256 rows], then
@@ -522,13 +524,7 @@ __device__ void softmax_rows(const Line<kCached>& line, Control& c, const Softma
     // ---- the item is cut: the CTA that comes last adds the parts, in order
     const Reach at = reach(w, c);  // the first part's counter counts
     if (!join_streams(c, joins)) return;
-    if (threadIdx.x == 0) {
-      unsigned* count = reinterpret_cast<unsigned*>(p.ws) + at.first;
-      const unsigned old = atom_add_acq_rel_u32(count, 1), want = at.last - at.first;
-      if (old > want) atomicOr(p.err, PE_ERR_WORKSPACE);
-      c.last[segment & 1] = old == want;
-      if (old == want) *count = 0;
-    }
+    if (threadIdx.x == 0) c.last[segment & 1] = arrive_part(p.ws, w, at, kCached && p.together, c, p.err);
     if (!join_streams(c, joins)) return;
     if (!c.last[segment & 1] || !valid) continue;
     // All threads of both streams add; where these have the same rows, each takes
@@ -564,6 +560,68 @@ __device__ void softmax_rows(const Line<kCached>& line, Control& c, const Softma
       finish(q, o, inverse(l));
     }
   }
+}
+
+// Together (pe_attn_line.cuh), all warps: this CTA's share of the items that it has
+// a part of.  Four lanes take four columns of a row, each every fourth part.  What
+// other CTAs just wrote takes 0.8 us to arrive, so five parts are on their way at a
+// time and every warp takes part.
+template <int D, class Control>
+__device__ void add_shares(const Line<true>& line, Control& c, const CachedParams& p) {
+  constexpr int kAll = kTile * (D / 4), kFlight = 5;
+  const int cuts = c.cuts, sub = (threadIdx.x >> 3) & 3;
+  unsigned before[2] = {};
+  if (threadIdx.x == 0) {
+    c.there = 1;
+    for (int k = 0; k < cuts; ++k) c.there &= await_parts(p.ws, c.cut[k].at, p.err);
+    for (int k = 0; k < cuts; ++k) before[k & 1] = seen_parts(p.ws, c.cut[k].at);
+  }
+  __syncthreads();
+  int from[2] = {0, 0}, n[2] = {0, 0};  // of each item: rows' columns
+  for (int k = 0; k < 2; ++k)
+    if (k < cuts && c.there) {
+      const Reach& at = c.cut[k].at;
+      const int parts = at.last - at.first + 1, share = blockIdx.x - at.first;
+      from[k] = kAll * share / parts;
+      n[k] = kAll * (share + 1) / parts - from[k];
+    }
+#pragma unroll 1
+  for (int x0 = (threadIdx.x >> 5) * 8; x0 < n[0] + n[1]; x0 += blockDim.x / 4) {
+    const int x = x0 + (threadIdx.x & 7);
+    const bool there = x < n[0] + n[1];
+    const int k = there && x >= n[0];  // (an item that this CTA has: the other entry holds nothing)
+    const Cut& cut = c.cut[k];
+    const int i = k ? from[1] + x - n[0] : from[0] + x, r = i & (kTile - 1), d = i / kTile;
+    const int tok = r / line.G, t = cut.w.mt * line.span + tok;
+    const bool mine = there && tok < line.span && t < cut.w.rows;
+    Running<4> sum;
+    const int last = cut.at.last;
+#pragma unroll 1
+    for (int part0 = cut.at.first + sub; mine && part0 <= last; part0 += 4 * kFlight) {
+      float2 ml[kFlight];
+      float4 y[kFlight];
+#pragma unroll
+      for (int e = 0; e < kFlight; ++e) {
+        const int part = min(part0 + 4 * e, last);
+        float4* of = partial<D>(p.ws, part, part == cut.at.first);
+        ml[e] = __ldcg(partial_ml<D>(of, r));
+        y[e] = __ldcg(of + d * 256 + r);
+      }
+#pragma unroll
+      for (int e = 0; e < kFlight; ++e)
+        sum.add(part0 + 4 * e <= last ? ml[e].x : -INFINITY, ml[e].y, {y[e].x, y[e].y, y[e].z, y[e].w});
+    }
+    sum.add_lane(8);
+    sum.add_lane(16);
+    if (mine && sub == 0) {
+      const float inv = sum.l > 0.0f ? 1.0f / sum.l : (sum.l == sum.l ? 0.0f : sum.l);
+      *reinterpret_cast<uint2*>(
+          p.out + ((long long)(cut.w.first + t) * p.Hq + cut.w.h * line.G + (r - tok * line.G)) * D + 4 * d) =
+          make_uint2(pack_bf16(sum.o[0] * inv, sum.o[1] * inv), pack_bf16(sum.o[2] * inv, sum.o[3] * inv));
+    }
+  }
+  if (threadIdx.x == 0)
+    for (int k = 0; k < cuts; ++k) clear_parts(p.ws, c.cut[k].at, before[k & 1]);
 }
 
 // Some wait gave up: every role has left its loop.  What is still on its way
