@@ -4,11 +4,12 @@
 
 namespace {
 
-// Are most items cut into several parts?  (Items: at most those of B requests that
-// fill their last one by a token.)
+// May items have so many parts (of 256 keys at least) that their CTAs add them up
+// together?  A cooperative launch costs 1.3 us.  (Items: at most those of B requests
+// that fill their last one by a token.)
 bool cut_often(const pe::CachedParams& p, int grid) {
   const int64_t span = pe::kTile / (p.Hq / p.Hkv);
-  return 2 * p.Hkv * (p.seg.B + p.seg.T / span) <= grid;
+  return p.table_keys >= pe::kTogether * 256 && 2 * p.Hkv * (p.seg.B + p.seg.T / span) <= grid;
 }
 
 // Together: cooperative, so that every CTA runs at once.  A refusal (other work

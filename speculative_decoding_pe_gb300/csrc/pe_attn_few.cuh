@@ -456,7 +456,7 @@ __global__ void __launch_bounds__(256, 2) attn_few_kernel(const CachedParams p) 
       __syncthreads();
     }
   }
-  if (p.together) {  // a warp for two elements, a lane for every 32nd part: in flight at once
+  if (p.together) {  // (as add_shares of pe_attn_mma.cuh: four parts of two elements in flight)
     const int cuts = c.cuts;
     unsigned before[2] = {};
     if (threadIdx.x == 0) {
@@ -465,33 +465,41 @@ __global__ void __launch_bounds__(256, 2) attn_few_kernel(const CachedParams p) 
       for (int k = 0; k < cuts; ++k) before[k & 1] = seen_parts(p.ws, c.cut[k].at);
     }
     __syncthreads();
-    int from[2] = {0, 0}, n[2] = {0, 0};  // of each item: pairs of elements
+    constexpr int kFlight = 4;
+    int from[2] = {0, 0}, n[2] = {0, 0}, most = 1;  // of each item: pairs of elements; parts
     for (int k = 0; k < 2; ++k)
       if (k < cuts && c.last) {
         const Reach& at = c.cut[k].at;
         const int parts = at.last - at.first + 1, share = blockIdx.x - at.first;
         const int all = c.cut[k].w.rows * line.G * (D / 2);
+        most = max(most, parts);
         from[k] = all * share / parts;
         n[k] = all * (share + 1) / parts - from[k];
       }
+    int width = 32;  // a warp's pairs at a time; 32 / width lanes each
+    while (width > 1 && most * width > 32 * kFlight && (n[0] + n[1]) * (64 / width) <= (int)blockDim.x) width >>= 1;
+    const int sub = lane / width, stride = 32 / width;
 #pragma unroll 1
-    for (int x = warp; x < n[0] + n[1]; x += F::kWarps) {
-      const int k = x >= n[0], i = k ? from[1] + x - n[0] : from[0] + x;
+    for (int x0 = warp * width; x0 < n[0] + n[1]; x0 += F::kWarps * width) {
+      const int x = x0 + (lane & (width - 1));
+      const bool there = x < n[0] + n[1];
+      const int k = there && x >= n[0];  // (an item that this CTA has)
+      const int i = !there ? from[0] : k ? from[1] + x - n[0] : from[0] + x;
       const int row = i / (D / 2), d = 2 * (i % (D / 2));
       const Reach at = c.cut[k].at;
       Running<2> sum;
 #pragma unroll 1
-      for (int part0 = at.first + lane; part0 - lane <= at.last; part0 += 64) {
-        float y[2][2];
-        float2 ml[2];
+      for (int part0 = at.first + sub; there && part0 <= at.last; part0 += stride * kFlight) {
+        float y[kFlight][2];
+        float2 ml[kFlight];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) ml[e] = part_of(at, min(part0 + 32 * e, at.last), row, d, y[e]);
+        for (int e = 0; e < kFlight; ++e) ml[e] = part_of(at, min(part0 + stride * e, at.last), row, d, y[e]);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) sum.add(part0 + 32 * e <= at.last ? ml[e].x : -INFINITY, ml[e].y, y[e]);
+        for (int e = 0; e < kFlight; ++e) sum.add(part0 + stride * e <= at.last ? ml[e].x : -INFINITY, ml[e].y, y[e]);
       }
 #pragma unroll 1
-      for (int e = 1; e < 32; e <<= 1) sum.add_lane(e);
-      if (lane == 0) finish(c.cut[k].w, row, d, sum);
+      for (int e = width; e < 32; e <<= 1) sum.add_lane(e);
+      if (there && sub == 0) finish(c.cut[k].w, row, d, sum);
     }
     if (threadIdx.x == 0)
       for (int k = 0; k < cuts; ++k) clear_parts(p.ws, c.cut[k].at, before[k & 1]);

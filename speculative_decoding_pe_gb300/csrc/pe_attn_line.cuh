@@ -262,9 +262,12 @@ struct Cut {
 };
 
 // How the parts of an item become one.  Whichever CTA comes last adds them all;
-// or, when every CTA of the call runs at once and most items are cut (`together`),
-// each CTA adds its share of the rows after its own part: one CTA alone would take
-// 4 us of a call with one token, 10 us of one with a draft.
+// or, when every CTA of the call runs at once (`together`) and the parts are many,
+// each CTA adds its share of the rows after its own part.  One request over 30000
+// keys, one key head of 128: a token 34 us alone, 15 together; a draft 113 and 25.
+// With few parts the others' wait is longer (4 parts: 10.6 us alone, 12.7 together;
+// 5: 44 and 47; 9: 48.5 and 47.8).
+constexpr int kTogether = 8;
 // The counter: arrivals in the low half, then CTAs that have taken their share.
 //
 // A partial result is there.  Does this CTA add them up now?  One thread.
@@ -274,7 +277,7 @@ __device__ __forceinline__ bool arrive_part(uint8_t* ws, const Walk& w, const Re
   unsigned* count = reinterpret_cast<unsigned*>(ws) + at.first;
   const unsigned old = atom_add_acq_rel_u32(count, 1), want = at.last - at.first;
   if ((old & 0xffffu) > want) atomicOr(err, PE_ERR_WORKSPACE);
-  if (together) {
+  if (together && want + 1 >= kTogether) {
     c.cut[c.cuts].w = w;
     c.cut[c.cuts++].at = at;
     return false;

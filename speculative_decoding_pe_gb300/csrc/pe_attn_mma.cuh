@@ -563,13 +563,13 @@ __device__ void softmax_rows(const Line<kCached>& line, Control& c, const Softma
 }
 
 // Together (pe_attn_line.cuh), all warps: this CTA's share of the items that it has
-// a part of.  Four lanes take four columns of a row, each every fourth part.  What
-// other CTAs just wrote takes 0.8 us to arrive, so five parts are on their way at a
-// time and every warp takes part.
+// a part of.  What other CTAs just wrote takes 0.8 us to arrive, so every warp takes
+// part, and as many lanes share four columns of a row as it takes for a lane to have
+// all its parts (five at most) on their way at once, or as there are.
 template <int D, class Control>
 __device__ void add_shares(const Line<true>& line, Control& c, const CachedParams& p) {
   constexpr int kAll = kTile * (D / 4), kFlight = 5;
-  const int cuts = c.cuts, sub = (threadIdx.x >> 3) & 3;
+  const int cuts = c.cuts;
   unsigned before[2] = {};
   if (threadIdx.x == 0) {
     c.there = 1;
@@ -577,17 +577,21 @@ __device__ void add_shares(const Line<true>& line, Control& c, const CachedParam
     for (int k = 0; k < cuts; ++k) before[k & 1] = seen_parts(p.ws, c.cut[k].at);
   }
   __syncthreads();
-  int from[2] = {0, 0}, n[2] = {0, 0};  // of each item: rows' columns
+  int from[2] = {0, 0}, n[2] = {0, 0}, most = 1;  // of each item: rows' columns; parts
   for (int k = 0; k < 2; ++k)
     if (k < cuts && c.there) {
       const Reach& at = c.cut[k].at;
       const int parts = at.last - at.first + 1, share = blockIdx.x - at.first;
+      most = max(most, parts);
       from[k] = kAll * share / parts;
       n[k] = kAll * (share + 1) / parts - from[k];
     }
+  int width = 32;  // a warp's columns at a time; 32 / width lanes each
+  while (width > 1 && most * width > 32 * kFlight && (n[0] + n[1]) * (64 / width) <= (int)blockDim.x) width >>= 1;
+  const int lane = threadIdx.x & 31, sub = lane / width, stride = 32 / width;
 #pragma unroll 1
-  for (int x0 = (threadIdx.x >> 5) * 8; x0 < n[0] + n[1]; x0 += blockDim.x / 4) {
-    const int x = x0 + (threadIdx.x & 7);
+  for (int x0 = (threadIdx.x >> 5) * width; x0 < n[0] + n[1]; x0 += (blockDim.x >> 5) * width) {
+    const int x = x0 + (lane & (width - 1));
     const bool there = x < n[0] + n[1];
     const int k = there && x >= n[0];  // (an item that this CTA has: the other entry holds nothing)
     const Cut& cut = c.cut[k];
@@ -597,22 +601,22 @@ __device__ void add_shares(const Line<true>& line, Control& c, const CachedParam
     Running<4> sum;
     const int last = cut.at.last;
 #pragma unroll 1
-    for (int part0 = cut.at.first + sub; mine && part0 <= last; part0 += 4 * kFlight) {
+    for (int part0 = cut.at.first + sub; mine && part0 <= last; part0 += stride * kFlight) {
       float2 ml[kFlight];
       float4 y[kFlight];
 #pragma unroll
       for (int e = 0; e < kFlight; ++e) {
-        const int part = min(part0 + 4 * e, last);
+        const int part = min(part0 + stride * e, last);
         float4* of = partial<D>(p.ws, part, part == cut.at.first);
         ml[e] = __ldcg(partial_ml<D>(of, r));
         y[e] = __ldcg(of + d * 256 + r);
       }
 #pragma unroll
       for (int e = 0; e < kFlight; ++e)
-        sum.add(part0 + 4 * e <= last ? ml[e].x : -INFINITY, ml[e].y, {y[e].x, y[e].y, y[e].z, y[e].w});
+        sum.add(part0 + stride * e <= last ? ml[e].x : -INFINITY, ml[e].y, {y[e].x, y[e].y, y[e].z, y[e].w});
     }
-    sum.add_lane(8);
-    sum.add_lane(16);
+#pragma unroll 1
+    for (int e = width; e < 32; e <<= 1) sum.add_lane(e);
     if (mine && sub == 0) {
       const float inv = sum.l > 0.0f ? 1.0f / sum.l : (sum.l == sum.l ? 0.0f : sum.l);
       *reinterpret_cast<uint2*>(
