@@ -434,7 +434,8 @@ int pe_latency_floor(int32_t ctas, int32_t hops, const int32_t* chain, int32_t n
  *  q [T,Hq,D], k, v [T,Hkv,D] with row and head strides in elements (multiples
  *  of 8), q_out [T,Hq,D] and k_out [T,Hkv,D] dense; q_out may be q and k_out
  *  may be k where those are dense.  rope [max_pos, rot_dim] fp32;
- *  rot_dim a multiple of 32, at most D.  T == 0 enqueues nothing. */
+ *  rot_dim a multiple of 32, at most D.  T (Hq + 2 Hkv) below 2^27.  T == 0
+ *  enqueues nothing. */
 typedef struct pe_kv_append_args {
   int32_t T, Hq, Hkv, D, block_size, rot_dim, interleaved, max_pos;
   int64_t num_blocks;
@@ -455,7 +456,7 @@ int pe_kv_append(const pe_kv_append_args* args /* host */, void* stream);
 /* Read cached rows back: k_out[t], v_out[t] [n,Hkv,D] bf16 = the values that
  * the cache holds at slots[t] (exact in bf16); zeros for slot -1, and for a
  * slot outside the cache (PE_ERR_BLOCK_RANGE).  Either output may be NULL.
- * n == 0 enqueues nothing. */
+ * n Hkv below 2^26.  n == 0 enqueues nothing. */
 int pe_kv_read(const void* cache, int64_t num_blocks, int32_t block_size,
                int32_t Hkv, int32_t D, const int64_t* slots, int32_t n,
                void* k_out, void* v_out, uint32_t* err, void* stream);

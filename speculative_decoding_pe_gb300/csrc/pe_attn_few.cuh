@@ -19,7 +19,13 @@
 //
 // Work.  A part of the line is a run of records (16 keys); its CTA's 8 warps
 // share a segment's records and meet at its end.  Each warp brings its records
-// by bulk copies, a step ahead, through segments.
+// by bulk copies, a step ahead, through segments.  A part has 16 records at least
+// (one token over 4000 keys: 8 records 21.7 us, 16: 16.6, 32: 17.0, 64: 18.3).
+//
+// Measured, 8 rows: 256 requests of 32 000 keys on average, 4 heads of 128: 0.92 ms,
+// 5.3 TB/s of the cache, 79 % of a plain copy, with the conversion's instructions
+// next to memory.  One request of 4000 keys, 8 heads of 64: 12.2 us, of which 3 are
+// the plan, 2 the keys, 4 the meetings of the warps and of the parts.
 #pragma once
 
 #include "pe_attn_line.cuh"
@@ -79,7 +85,8 @@ __global__ void __launch_bounds__(256, 2) attn_few_kernel(const CachedParams p) 
   if (threadIdx.x == 0) c.dead = c.cuts = 0;
   mbar_init_fence();
   Line<true, 16> line{p.seg, p.Hkv, p.Hq / p.Hkv, kTile / (p.Hq / p.Hkv), nullptr, nullptr};
-  if (!plan(line, F::kMinRecords, F::kMinRecords / 2, c, prefix, keys, reinterpret_cast<long long*>(smem), p.positions, p.is_rejected, p.table_keys, p.err))
+  if (!plan(line, F::kMinRecords, F::kMinRecords / 2, c, prefix, keys, reinterpret_cast<long long*>(smem),
+            p.positions, p.is_rejected, p.table_keys, p.err))
     return;
   if (c.start.u >= c.start.end) return;
 

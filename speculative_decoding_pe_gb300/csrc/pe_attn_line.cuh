@@ -5,8 +5,9 @@
 // and part c of n is units [c U / n, (c + 1) U / n): equal parts whatever the
 // lengths are, but that an end less than `snap` units from an item's end moves
 // there, because a piece of an item costs a CTA as much as some units do (one
-// token over 4000 keys: 16.4 us against 13.2).  No plan is made on the host, which does not know the lengths:
-// every CTA sums them up for itself.
+// token over 4000 keys: 16.4 us against 13.2).  No plan is made on the host, which
+// does not know the lengths: every CTA sums them up for itself (1 to 3 us of a small
+// call, most of it the first fetch of the instructions).
 #pragma once
 
 #include "pe_attn.cuh"
@@ -144,9 +145,9 @@ __device__ Walk walk_begin(const Line<kCached, kUnit>& line, long long u, long l
 // Every CTA lays the line out for itself (a few loads per request) and finds
 // its part.  False when the offsets are no partition of the rows.
 template <bool kCached, int kUnit, class Control>
-__device__ bool plan(Line<kCached, kUnit>& line, int min_units, int most_snap, Control& c, long long* prefix, int* keys, long long* sums,
-                     const int32_t* positions, const uint8_t* is_rejected, int table_keys,
-                     uint32_t* err) {
+__device__ bool plan(Line<kCached, kUnit>& line, int min_units, int most_snap, Control& c, long long* prefix,
+                     int* keys, long long* sums, const int32_t* positions, const uint8_t* is_rejected,
+                     int table_keys, uint32_t* err) {
   const int tid = threadIdx.x, n = blockDim.x, B = line.seg.B;
   if (line.seg.offsets && !offsets_valid(line.seg.offsets, B, line.seg.T, 0)) {
     if (tid == 0 && blockIdx.x == 0) atomicOr(err, PE_ERR_OFFSETS);

@@ -16,8 +16,8 @@
 // 128 keys.  All units of the call are one line that the CTAs cut into equal
 // parts, whatever the lengths are: a CTA finds its part by itself from the
 // segment lengths.  An item that is cut leaves one partial (O, m, l) per CTA in
-// the workspace, and whichever CTA finishes last adds them in a fixed order, so
-// results do not depend on timing.
+// the workspace; they are added in a fixed order (pe_attn_line.cuh), so results do
+// not depend on timing.
 //
 // CTA.  Two streams of 128 rows, one per softmax warpgroup, alternate on the
 // tensor core: while one takes its exponentials, the other's products run.

@@ -13,8 +13,13 @@
 // its pairs), a warp 1024/D heads of keys and values or twice as many of queries,
 // whose lanes use each table entry for two heads.  The warps go through all keys
 // and values first, then through all queries: with both at once the two codes
-// drove each other out of the instruction cache.  Bound by memory: every element
-// is read and written once.
+// drove each other out of the instruction cache (prefill below: 200 us against 173).
+// Bound by memory: every element is read and written once.
+//
+// Measured (D = 64, 64 + 16 heads, all dimensions rotated): 37 000 prompt rows 160 us,
+// 4.7 TB/s of reads and writes, where the conversion's instructions and the loads
+// wait for each other; two CTAs of 256 threads per SM (three: 173 us).  14 rows
+// 3.8 us, a launch and one trip to memory.
 #include "pe_kv.cuh"
 
 namespace pe {

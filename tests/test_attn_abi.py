@@ -47,7 +47,7 @@ def prompt_args(**over):
 
 @pytest.mark.parametrize("over, rc", [
     (dict(T=-1), EINVAL), (dict(Hq=63), EINVAL), (dict(Hkv=0), EINVAL), (dict(D=96), EINVAL),
-    (dict(block_size=8), EINVAL), (dict(block_size=24), EINVAL), (dict(num_blocks=0), EINVAL),
+    (dict(T=1 << 27), EINVAL), (dict(block_size=8), EINVAL), (dict(block_size=24), EINVAL), (dict(num_blocks=0), EINVAL),
     (dict(num_blocks=1 << 60), EINVAL), (dict(rot_dim=0), EINVAL), (dict(rot_dim=48), EINVAL),
     (dict(rot_dim=96), EINVAL), (dict(max_pos=0), EINVAL), (dict(q=None), EINVAL),
     (dict(k=None), EINVAL), (dict(v=None), EINVAL), (dict(positions=None), EINVAL),
@@ -61,7 +61,7 @@ def test_append_refusals(lib, over, rc):
 
 
 @pytest.mark.parametrize("over, rc", [
-    (dict(n=-1), EINVAL), (dict(D=32), EINVAL), (dict(bs=20), EINVAL), (dict(Hkv=0), EINVAL),
+    (dict(n=-1), EINVAL), (dict(n=1 << 26), EINVAL), (dict(D=32), EINVAL), (dict(bs=20), EINVAL), (dict(Hkv=0), EINVAL),
     (dict(nb=0), EINVAL), (dict(cache=None), EINVAL), (dict(slots=None), EINVAL),
     (dict(err=None), EINVAL), (dict(cache=MIS), EALIGN), (dict(k=MIS), EALIGN),
     (dict(v=MIS), EALIGN), (dict(n=0, cache=None), 0)])
