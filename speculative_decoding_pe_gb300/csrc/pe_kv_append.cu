@@ -16,8 +16,8 @@
 // drove each other out of the instruction cache (prefill below: 200 us against 173).
 // Bound by memory: every element is read and written once.
 //
-// Measured (D = 64, 64 + 16 heads, all dimensions rotated): 37 000 prompt rows 160 us,
-// 4.7 TB/s of reads and writes, where the conversion's instructions and the loads
+// Measured (D = 64, 64 + 16 heads, all dimensions rotated): 38 700 prompt rows 160 us,
+// 4.9 TB/s of reads and writes, where the conversion's instructions and the loads
 // wait for each other; two CTAs of 256 threads per SM (three: 173 us).  14 rows
 // 3.8 us, a launch and one trip to memory.
 #include "pe_kv.cuh"
