@@ -51,6 +51,7 @@ struct FewControl {
   uint64_t full[kWarps][kStages];
   Walk start;
   long long total, parts, snap;
+  int items;
   int dead, last, cuts;
   Cut cut[2];
   float m[kWarps][16], l[kWarps][16];

@@ -107,6 +107,7 @@ struct AttnControl {
   uint64_t s_full[2][4], p_half[2][4], p_full[2][4], o_full[2][4];
   Walk start;
   long long total, parts, snap;
+  int items;
   uint32_t tmem;
   int dead, last[2], there, cuts;
   Cut cut[2];
