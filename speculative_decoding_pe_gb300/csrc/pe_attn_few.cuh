@@ -19,7 +19,7 @@
 //
 // Work.  A part of the line is a run of records (16 keys); its CTA's 8 warps
 // share a segment's records and meet at its end.  Each warp brings its records
-// by bulk copies, a step ahead, through segments.  A part has 16 records at least
+// by bulk copies, a step ahead, through segments.  A cut part has 16 records at least
 // (one token over 4000 keys: 8 records 21.7 us, 16: 16.6, 32: 17.0, 64: 18.3).
 //
 // Measured, 8 rows: 256 requests of 32 000 keys on average, 4 heads of 128: 0.92 ms,
