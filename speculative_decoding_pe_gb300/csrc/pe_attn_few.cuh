@@ -11,10 +11,12 @@
 // both operands agree, so a lane takes 8 or 16 consecutive bytes of a token's
 // keys, and 4 or 8 of its values.
 //
-// Weights.  P is f16 and codes times scales are exact in f16 (6 bits), so V is
-// exact and P keeps 11 bits.  Queries become f16 too after a power of two is
-// taken out of each row (its largest element lies in [1, 2)): elements down to
-// 2^-14 of it keep their 8 bits, and what a smaller one loses is below 2^-25 of
+// Weights.  P V is a tf32 product: a weight keeps 11 bits over fp32's whole range
+// (in f16 those below 2^-31 of the largest would vanish, which shows where the
+// heaviest keys' values are zeros), and codes times scales (6 bits) are exact.
+// K Q is an f16 product: keys are exact, and queries become f16 after a power of
+// two is taken out of each row (its largest element lies in [1, 2)): elements down
+// to 2^-14 of it keep their 8 bits, and what a smaller one loses is below 2^-25 of
 // the largest.
 //
 // Work.  A part of the line is a run of records (16 keys); its CTA's 8 warps
@@ -22,9 +24,9 @@
 // by bulk copies, a step ahead, through segments.  A cut part has 16 records at least
 // (one token over 4000 keys: 8 records 21.7 us, 16: 16.6, 32: 17.0, 64: 18.3).
 //
-// Measured, 8 rows: 256 requests of 32 000 keys on average, 4 heads of 128: 0.92 ms,
-// 5.3 TB/s of the cache, 79 % of a plain copy, with the conversion's instructions
-// next to memory.  One request of 4000 keys, 8 heads of 64: 12.2 us, of which 3 are
+// Measured, 8 rows: 256 requests of 32 000 keys on average, 4 heads of 128: 1.09 ms,
+// 4.4 TB/s of the cache, 66 % of a plain copy: bound by the conversion's instructions
+// (with f16 weights, which are not enough, 0.92 ms).  One request of 4000 keys, 8 heads of 64: 12.2 us, of which 3 are
 // the plan, 2 the keys, 4 the meetings of the warps and of the parts.
 #pragma once
 
@@ -65,10 +67,30 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void mma_tf32(float (&c)[4], float a0, float a1, float a2, float a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(__float_as_uint(a0)), "r"(__float_as_uint(a1)), "r"(__float_as_uint(a2)), "r"(__float_as_uint(a3)),
+        "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t to_tf32(float x) {  // to nearest
+  uint32_t d;
+  asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(d) : "f"(x));
+  return d;
+}
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t y;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
+}
+// Elements 2c, 2c + 1 of row r of an 8 x 8 matrix of words (lane 4 r + c) become
+// rows 2c, 2c + 1 of column r: the halves of the words are turned apart.
+__device__ __forceinline__ void transpose8x8(uint32_t (&x)[2]) {
+  const uint32_t lo = transpose8x8(__byte_perm(x[0], x[1], 0x5410)), hi = transpose8x8(__byte_perm(x[0], x[1], 0x7632));
+  x[0] = __byte_perm(lo, hi, 0x5410), x[1] = __byte_perm(lo, hi, 0x7632);
 }
 template <int D, int NB>
 __global__ void __launch_bounds__(256, 2) attn_few_kernel(const CachedParams p) {
@@ -313,25 +335,25 @@ __global__ void __launch_bounds__(256, 2) attn_few_kernel(const CachedParams p) 
 #pragma unroll
       for (int b = 0; b < NB; ++b)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) shift[b][e] = (m[b][e] == -INFINITY ? 0.0f : -m[b][e]) + 7.0f;
-      // ---- weights; the maximum is held at 2^7, so that an f16 weight keeps
-      // every bit down to 2^-21 of it (before a rescale it reaches 2^15 at most)
+        for (int e = 0; e < 2; ++e) shift[b][e] = m[b][e] == -INFINITY ? 0.0f : -m[b][e];
+      // ---- weights
 #pragma unroll
       for (int x = 0; x < kRec; ++x) {
         if (x >= cnt) break;
         const uint8_t* rec = step + x * R::kBytes;
-        uint32_t pt[NB][2];
+        uint32_t pt[NB][2][2];  // of this lane's row: [half of the record][token 2 cc, 2 cc + 1 of it]
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          float e[4];
+        for (int b = 0; b < NB; ++b)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            e[i] = exp2_approx(fmaf(s[b][x][i], sc[b][i & 1], shift[b][i & 1]));
-            l[b][i & 1] += e[i];
+          for (int i = 0; i < 2; ++i) {
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+              const float e = exp2_approx(fmaf(s[b][x][2 * i + y], sc[b][y], shift[b][y]));
+              l[b][y] += e;
+              pt[b][i][y] = to_tf32(e);
+            }
+            transpose8x8(pt[b][i]);
           }
-          pt[b][0] = transpose8x8(pack_f16(e[0], e[1]));
-          pt[b][1] = transpose8x8(pack_f16(e[2], e[3]));
-        }
         uint32_t vw[4][kGroups], vs[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -347,28 +369,25 @@ __global__ void __launch_bounds__(256, 2) attn_few_kernel(const CachedParams p) 
           // what lies past the request's keys may be anything, a NaN too
           if (masked && ((pos + x) * 16 + tok >= L || !(ok >> x & 1))) vs[i] = 0;
         }
-        // A product wants two tokens' values of one element together, so the codes
-        // of two tokens are interleaved before they are converted.
-        const uint32_t s01 = e4m3x2_f16x2(vs[0] | vs[1] << 8), s23 = e4m3x2_f16x2(vs[2] | vs[3] << 8);
+        // a product: 8 tokens; this lane's two of them, elements 2e and 2e + 1
 #pragma unroll
-        for (int g = 0; g < kGroups; ++g) {
-          uint32_t even[2][4], odd[2][4];  // [tokens][pair of elements]
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t sv[2] = {e4m3_f16x2(vs[2 * i]), e4m3_f16x2(vs[2 * i + 1])};
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint32_t a = vw[2 * i][g], b8 = vw[2 * i + 1][g];
-            e2m1x8_f16((a & 0x0f0f0f0fu) | ((b8 << 4) & 0xf0f0f0f0u), even[i]);
-            e2m1x8_f16(((a >> 4) & 0x0f0f0f0fu) | (b8 & 0xf0f0f0f0u), odd[i]);
+          for (int g = 0; g < kGroups; ++g) {
+            uint32_t va[4], vb[4];
+            e2m1x8_f16(vw[2 * i][g], va);
+            e2m1x8_f16(vw[2 * i + 1][g], vb);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              even[i][e] = hmul2(even[i][e], i ? s23 : s01);
-              odd[i][e] = hmul2(odd[i][e], i ? s23 : s01);
+              float a[4];
+              mul_f16x2_f32(va[e], sv[0], a[0], a[1]);
+              mul_f16x2_f32(vb[e], sv[1], a[2], a[3]);
+#pragma unroll
+              for (int b = 0; b < NB; ++b)
+                mma_tf32(o[b][4 * g + e], a[0], a[1], a[2], a[3], pt[b][i][0], pt[b][i][1]);
             }
           }
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-#pragma unroll
-            for (int b = 0; b < NB; ++b)
-              mma_f16(o[b][4 * g + e], even[0][e], odd[0][e], even[1][e], odd[1][e], pt[b][0], pt[b][1]);
         }
       }
       pos += cnt;
