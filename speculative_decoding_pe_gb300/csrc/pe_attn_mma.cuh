@@ -6,8 +6,8 @@
 // once for all of them) and 128 keys at a time:
 //   S = Q K^T (fp32);  m' = max(m, max S);  P = 2^(S scale log2 e - m');
 //   l = l 2^(m - m') + sum P;  O = O 2^(m - m') + P V;  out = O / l.
-// m need not be the maximum: any m gives the same quotient as long as P stays in
-// range, so it is taken from an item's first tile and then only when a score
+// m need not be the maximum: any m gives the same quotient as long as P and O stay
+// in range, so it is taken from an item's first tile and then only when a score
 // passes it by kSlack; O is rarely rescaled.  S, O, m and l are fp32.  P is
 // rounded to bf16 for the product, each weight by at most 2^-8 of itself however
 // small it is (an f16 would lose the small ones), as the output is.
@@ -272,8 +272,11 @@ template <int D, bool kCached, class Control>
 __device__ void softmax_rows(const Line<kCached>& line, Control& c, const SoftmaxArgs& p, int s) {
   using Sh = AttnShape<D, kCached>;
   // How far (log2) a score may pass the maximum that is held before the row takes
-  // the new one and O is rescaled: weights and sums have fp32's range.
-  constexpr float kSlack = 100.0f;
+  // the new one and O is rescaled.  O must not overflow where the quotient is finite:
+  // for prompts, n keys of magnitude v give up to 2^8 n v.  Over the cache a value is
+  // at most 6 * 448 and keys are below 2^31, so 2^64 leaves room, and tells more tiles
+  // apart by their key scales alone (below; their bound lies some 2^30 over the scores).
+  constexpr float kSlack = kCached ? 64.0f : 8.0f;
   // Columns of S in registers at a time.  Over the cache eight warps that convert
   // codes share the instruction cache with the softmax, and its shorter code is
   // worth more than fewer loads (b64 drafts: 727 us against 468); a prompt's
@@ -381,9 +384,10 @@ __device__ void softmax_rows(const Line<kCached>& line, Control& c, const Softma
             fmaxf(max3(mx[0], mx[1], mx[2]), max3(max3(mx[3], mx[4], mx[5]), mx[6], mx[7])) * scale;
         const bool grew = live && top > m + kSlack;
         if (__any_sync(0xffffffffu, grew)) {
-          const float f = grew ? exp2_approx(m - top) : 1.0f;
+          // in two steps: one is zero below 2^-126, and O may have passed m by kSlack
+          const float f = grew ? exp2_approx(0.5f * (m - top)) : 1.0f;
           if (grew) m = top;
-          l *= f;
+          l = l * f * f;
           if (i > 0) {  // O of the visits before
             if (!wait_warp(&c.o_full[s][(visit - 1) & 3], ((visit - 1) >> 2) & 1, dead)) return;
             tc_fence_after();
@@ -393,7 +397,7 @@ __device__ void softmax_rows(const Line<kCached>& line, Control& c, const Softma
               tmem_ld16(o_addr + q, o);
               tc_wait_ld();
 #pragma unroll
-              for (int r = 0; r < 16; ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) * f);
+              for (int r = 0; r < 16; ++r) o[r] = __float_as_uint(__uint_as_float(o[r]) * f * f);
               tmem_st16(o_addr + q, o);
             }
           }
@@ -434,10 +438,22 @@ __device__ void softmax_rows(const Line<kCached>& line, Control& c, const Softma
     if (!live) m = -INFINITY, l = 0.0f;
     const bool whole = w.t0 == 0 && w.t1 == w.tiles;
     const int slot_row = halves ? row : s * kTile + row;
+    // What meets other results is held for the power of two in its total, because m may
+    // lie kSlack below its largest score: a factor of zero then takes out what is below
+    // 2^-126 of the sum.
+    float unit = 1.0f;
+    if (kCached) {
+      const int e = __float_as_uint(l) >> 23;
+      if (e > 0 && e < 254) unit = __uint_as_float((254 - e) << 23), m += e - 127, l *= unit;
+    }
     auto sums = [&](int q, float(&o)[32]) {
       if (v.count) {
         tmem_ld32(o_addr + q, reinterpret_cast<uint32_t*>(o));
         tc_wait_ld();
+        if (kCached) {
+#pragma unroll
+          for (int r = 0; r < 32; ++r) o[r] *= unit;
+        }
       } else {
 #pragma unroll
         for (int r = 0; r < 32; ++r) o[r] = 0.0f;
