@@ -51,7 +51,7 @@ __device__ __forceinline__ float diff_of_products_odd(float a, float c, float b,
   const float lo = __fadd_rn(__fsub_rn(d, __fsub_rn(hi, tb)), __fsub_rn(t, tb));
   uint32_t u = __float_as_uint(hi);
   if (lo != 0.0f && !(u & 1u)) u += ((__float_as_uint(lo) ^ u) >> 31) ? 0xffffffffu : 1u;
-  return lo == lo ? __uint_as_float(u) : hi;  // an infinity or NaN leaves no remainder
+  return lo == lo ? __uint_as_float(u) : d;  // an infinity has no remainder: all but d is a NaN
 }
 
 // 16 bf16 elements as codes (x, y) and scale (z) of one group.
