@@ -77,7 +77,7 @@ inline int attn_sizes(int T, int B, int Hq, int Hkv, int D, const void* offsets,
       Hq / Hkv > PE_MAX_ATTN_G || (D != 64 && D != 128) || !isfinite(scale) || !(scale > 0.0f))
     return PE_EINVAL;
   if (!offsets && T % B) return PE_EINVAL;
-  if ((int64_t)T * Hq * D > ((int64_t)1 << 40)) return PE_EINVAL;
+  if (T > ((int64_t)1 << 40) / ((int64_t)Hq * D)) return PE_EINVAL;
   return PE_OK;
 }
 

@@ -9,7 +9,7 @@ namespace {
 // that fill their last one by a token.)
 bool cut_often(const pe::CachedParams& p, int grid) {
   const int64_t span = pe::kTile / (p.Hq / p.Hkv);
-  return p.table_keys >= pe::kTogether * 256 && 2 * p.Hkv * (p.seg.B + p.seg.T / span) <= grid;
+  return p.table_keys >= pe::kTogether * 256 && 2 * (int64_t)p.Hkv * (p.seg.B + p.seg.T / span) <= grid;
 }
 
 // Together: cooperative, so that every CTA runs at once.  A refusal (other work
@@ -63,9 +63,8 @@ extern "C" size_t pe_workspace_bytes_attn(int32_t D) {
 extern "C" int pe_attn_cached(const pe_attn_cached_args* a, void* stream) {
   if (!a) return PE_EINVAL;
   if (int rc = pe_host::attn_sizes(a->T, a->B, a->Hq, a->Hkv, a->D, a->offsets, a->scale)) return rc;
-  if (a->block_size < 16 || a->block_size % 16 || a->bt_width < 1 ||
-      (int64_t)a->bt_width * a->block_size > INT32_MAX - 256 || a->num_blocks < 1 ||
-      a->num_blocks > (INT64_MAX >> 8) / ((int64_t)a->Hkv * a->block_size * a->D))
+  if (!pe_host::cache_sizes_ok(a->num_blocks, a->block_size, a->Hkv, a->D) || a->bt_width < 1 ||
+      (int64_t)a->bt_width * a->block_size > INT32_MAX - 256)
     return PE_EINVAL;
   if (a->T == 0) return PE_OK;
   if (!a->q || !a->cache || !a->block_table || !a->positions || !a->out || !a->workspace || !a->err)

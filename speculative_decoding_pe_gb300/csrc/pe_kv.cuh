@@ -110,3 +110,14 @@ __device__ __forceinline__ void f16x2_to_f32(uint32_t w, float& lo, float& hi) {
 }
 
 }  // namespace pe
+
+namespace pe_host {
+
+// The sizes of a cache.  One division after another: the product of the divisors may
+// pass 64 bits, and be zero.
+inline bool cache_sizes_ok(int64_t num_blocks, int32_t block_size, int32_t Hkv, int32_t D) {
+  return Hkv >= 1 && (D == 64 || D == 128) && block_size >= 16 && block_size % 16 == 0 && num_blocks >= 1 &&
+         num_blocks <= (INT64_MAX >> 8) / Hkv / block_size / D;
+}
+
+}  // namespace pe_host

@@ -256,12 +256,9 @@ bool strides_ok(int64_t row, int64_t head) { return row >= 0 && head >= 0 && row
 
 extern "C" int pe_kv_append(const pe_kv_append_args* a, void* stream) {
   if (!a) return PE_EINVAL;
-  if (a->T < 0 || a->Hq < 1 || a->Hkv < 1 || a->Hq % a->Hkv || (a->D != 64 && a->D != 128))
-    return PE_EINVAL;
-  if (a->block_size < 16 || a->block_size % 16 || a->num_blocks < 1 ||
-      a->num_blocks > (INT64_MAX >> 8) / ((int64_t)a->Hkv * a->block_size * a->D))
-    return PE_EINVAL;
-  if ((int64_t)a->T * ((int64_t)a->Hq + 2 * a->Hkv) > INT32_MAX / 16) return PE_EINVAL;
+  if (!pe_host::cache_sizes_ok(a->num_blocks, a->block_size, a->Hkv, a->D)) return PE_EINVAL;
+  if (a->T < 0 || a->Hq < 1 || a->Hq % a->Hkv) return PE_EINVAL;
+  if (a->T > INT32_MAX / 16 / ((int64_t)a->Hq + 2 * (int64_t)a->Hkv)) return PE_EINVAL;
   if (a->rot_dim < 32 || a->rot_dim > a->D || a->rot_dim % 32 || a->max_pos < 1) return PE_EINVAL;
   if (a->T == 0) return PE_OK;
   if (!a->q || !a->k || !a->v || !a->positions || !a->slots || !a->rope || !a->cache || !a->q_out ||
@@ -308,10 +305,8 @@ extern "C" int pe_kv_append(const pe_kv_append_args* a, void* stream) {
 extern "C" int pe_kv_read(const void* cache, int64_t num_blocks, int32_t block_size, int32_t Hkv,
                           int32_t D, const int64_t* slots, int32_t n, void* k_out, void* v_out,
                           uint32_t* err, void* stream) {
-  if (n < 0 || Hkv < 1 || (D != 64 && D != 128) || block_size < 16 || block_size % 16 ||
-      num_blocks < 1 || num_blocks > (INT64_MAX >> 8) / ((int64_t)Hkv * block_size * D) ||
-      (int64_t)n * Hkv > INT32_MAX / 32)
-    return PE_EINVAL;
+  if (!pe_host::cache_sizes_ok(num_blocks, block_size, Hkv, D)) return PE_EINVAL;
+  if (n < 0 || (int64_t)n * Hkv > INT32_MAX / 32) return PE_EINVAL;
   if (n == 0) return PE_OK;
   if (!cache || !slots || !err) return PE_EINVAL;
   if (!pe_host::aligned16(cache) || !pe_host::aligned16(k_out) || !pe_host::aligned16(v_out))
