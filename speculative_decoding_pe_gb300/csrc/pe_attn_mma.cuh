@@ -111,8 +111,11 @@ struct AttnControl {
   uint32_t tmem;
   int dead, last[2], there, cuts;
   Cut cut[2];
-  uint32_t not_finite[8][12];  // values of a masked tile: tokens that hold an infinity or NaN
-  int any_not_finite[8];       // of a segment
+  // prompts, by segment: tokens of masked tiles whose values hold an infinity or NaN,
+  // whether there is one, and that the streams with visits have read so
+  uint32_t not_finite[8][12];
+  int any_not_finite[8];
+  uint64_t notes_read[8];
   float row_scale[4][kTile];   // kCached, by segment: the power of two taken out of a query row
   float row_sum[4][kTile];     // kCached, by segment: the sum of a query's magnitudes
   uint32_t tile_ok[16];        // kCached: records of a tile that lie in the cache
@@ -138,6 +141,7 @@ struct AttnControl {
         mbar_init(&p_full[s][i], 4);
       }
     }
+    for (int i = 0; i < 8; ++i) mbar_init(&notes_read[i], 8);
     mbar_init(&pair, 8);
     dead = cuts = 0;
     mbar_init_fence();
@@ -458,7 +462,7 @@ __device__ void softmax_rows(const Line<kCached>& line, Control& c, const Softma
 #pragma unroll
         for (int r = 0; r < 32; ++r) o[r] = 0.0f;
       }
-      if (!kCached && __builtin_expect(c.any_not_finite[segment & 7], 0)) {
+      if (!kCached && v.count && __builtin_expect(c.any_not_finite[segment & 7], 0)) {
         // values that are not finite were taken out of masked tiles
         // (look_over_values): the rows that see them get them back
         const int first_masked = (2 * w.mt * line.span + 1) / kTile;
@@ -543,6 +547,10 @@ __device__ void softmax_rows(const Line<kCached>& line, Control& c, const Softma
       if (!whole) *partial_ml<D>(mine, slot_row) = make_float2(m, l);
     }
     tc_fence_before();
+    if (!kCached && v.count) {
+      __syncwarp();
+      if ((threadIdx.x & 31) == 0) mbar_arrive(&c.notes_read[segment & 7]);
+    }
     if (whole) continue;
     // ---- the item is cut: the CTA that comes last adds the parts, in order
     const Reach at = reach(w, c);  // the first part's counter counts
