@@ -222,6 +222,7 @@ __device__ bool plan(Line<kCached, kUnit>& line, int min_units, int most_snap, C
   if (used > 32) {
     __syncthreads();
     for (int b = b0; b < b1; ++b) prefix[b + 1] += sums[tid];
+    fence_async_shared();  // the bytes of `sums` are next written by bulk and TMA copies
     __syncthreads();
   }
   __syncwarp();
