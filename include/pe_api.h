@@ -477,8 +477,8 @@ size_t pe_workspace_bytes_attn(int32_t D);
  *   out[t,h] = sum_j softmax_j(scale * q[t,h] . K[j,h/G]) V[j,h/G],  G = Hq/Hkv
  * and zeros when limit is 0.  Key j lies in page block_table[b][j/block_size].
  * The keys of the rows themselves have to be in the cache (pe_kv_append).
- *  q, out [T,Hq,D] bf16, dense.  offsets [B+1] int32: the segments, as
- *  out_offsets; NULL: T/B rows each.  is_rejected [T] or NULL: none.
+ *  q, out [T,Hq,D] bf16, dense; out may be q.  offsets [B+1] int32: the
+ *  segments, as out_offsets; NULL: T/B rows each.  is_rejected [T] or NULL: none.
  *  scale: finite, above 0.  Sums and softmax statistics are fp32.
  *  err: PE_ERR_OFFSETS (offsets no partition of T: nothing is written);
  *  PE_ERR_BLOCK_RANGE (a position below 0 sees nothing, one past the table
@@ -504,8 +504,9 @@ int pe_attn_cached(const pe_attn_cached_args* args /* host */, void* stream);
 /* Causal attention over whole packed prompts: row i of a segment sees the
  * keys 0..i of the same segment.
  *  q [T,Hq,D], k, v [T,Hkv,D] bf16 with row and head strides in elements
- *  (multiples of 8; below 2^31); out [T,Hq,D] dense; offsets [B+1] int32 or
- *  NULL as above (empty segments are allowed).  err as above.
+ *  (multiples of 8; below 2^31; not 0 along an axis of more than one); out
+ *  [T,Hq,D] dense (it may be q where that is); offsets [B+1] int32 or NULL as
+ *  above (empty segments are allowed).  err as above.
  * T == 0 enqueues nothing. */
 typedef struct pe_attn_prompt_args {
   int32_t T, B, Hq, Hkv, D;
