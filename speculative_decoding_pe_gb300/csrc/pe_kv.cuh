@@ -102,6 +102,15 @@ __device__ __forceinline__ void mul_f16x2_f32(uint32_t x, uint32_t y, float& lo,
       : "=f"(lo), "=f"(hi)
       : "r"(x), "r"(y), "f"(0.0f));
 }
+// The same with one half of y for both.
+template <bool kHigh>
+__device__ __forceinline__ void mul_f16x2_f32_by(uint32_t x, uint32_t y, float& lo, float& hi) {
+  asm("{\n\t.reg .f16 a, b, c, d, f;\n\tmov.b32 {a, b}, %2;\n\tmov.b32 {c, d}, %3;\n\t"
+      ".reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\tselp.b16 f, d, c, p;\n\t"
+      "fma.rn.f32.f16 %0, a, f, %4;\n\tfma.rn.f32.f16 %1, b, f, %4;\n\t}"
+      : "=f"(lo), "=f"(hi)
+      : "r"(x), "r"(y), "f"(0.0f), "n"(kHigh));
+}
 
 __device__ __forceinline__ void f16x2_to_f32(uint32_t w, float& lo, float& hi) {
   asm("{\n\t.reg .f16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}"
