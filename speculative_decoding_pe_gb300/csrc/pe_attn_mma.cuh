@@ -98,8 +98,16 @@ struct AttnShape {
   __host__ __device__ static constexpr uint32_t o_col(int s) { return kBuffers * kTile + s * D; }
 };
 
+// Entries for what look_over_values notes of a segment, read when its result is
+// stored.  Every eight segments the streams wait for each other.  Before the notes of
+// segment m are written, the tile five before its first has met its weights (at most
+// four stages), so one stream has come to segment m - 5, and the other has stored all
+// results up to the last meeting: those up to segment m - 13.
+constexpr int kNotes = 16;
+
 template <int kStages>
 struct AttnControl {
+  static_assert(kStages <= 4, "see kNotes");
   uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_ready[kStages], v_empty[kStages];
   uint64_t q_full[2], q_empty[2], pair;
   // by visit of the stream: S runs up to three ahead of the products of P, and so
@@ -112,10 +120,9 @@ struct AttnControl {
   int dead, last[2], there, cuts;
   Cut cut[2];
   // prompts, by segment: tokens of masked tiles whose values hold an infinity or NaN,
-  // whether there is one, and that the streams with visits have read so
-  uint32_t not_finite[8][12];
-  int any_not_finite[8];
-  uint64_t notes_read[8];
+  // and whether there is one
+  uint32_t not_finite[kNotes][12];
+  int any_not_finite[kNotes];
   float row_scale[4][kTile];   // kCached, by segment: the power of two taken out of a query row
   float row_sum[4][kTile];     // kCached, by segment: the sum of a query's magnitudes
   uint32_t tile_ok[16];        // kCached: records of a tile that lie in the cache
@@ -141,7 +148,6 @@ struct AttnControl {
         mbar_init(&p_full[s][i], 4);
       }
     }
-    for (int i = 0; i < 8; ++i) mbar_init(&notes_read[i], 8);
     mbar_init(&pair, 8);
     dead = cuts = 0;
     mbar_init_fence();
@@ -296,6 +302,7 @@ __device__ void softmax_rows(const Line<kCached>& line, Control& c, const Softma
   Walk w = c.start;
   uint32_t kv0 = 0, u0 = 0;  // tiles and visits before the segment
   for (; walk_next(line, w); kv0 += w.t1 - w.t0, ++segment) {
+    if (!kCached && segment % (kNotes / 2) == 0 && segment > 0 && !join_streams(c, joins)) return;
     const Visits v = visits(line, w, s);
     const Order order(s ? visits(line, w, 0) : v, s ? v : visits(line, w, 1));
     const uint32_t base = u0;
@@ -462,13 +469,13 @@ __device__ void softmax_rows(const Line<kCached>& line, Control& c, const Softma
 #pragma unroll
         for (int r = 0; r < 32; ++r) o[r] = 0.0f;
       }
-      if (!kCached && v.count && __builtin_expect(c.any_not_finite[segment & 7], 0)) {
+      if (!kCached && v.count && __builtin_expect(c.any_not_finite[segment % kNotes], 0)) {
         // values that are not finite were taken out of masked tiles
         // (look_over_values): the rows that see them get them back
         const int first_masked = (2 * w.mt * line.span + 1) / kTile;
         for (int j = max(w.t0, first_masked); j < w.t0 + v.count; ++j)
           for (int word = 0; word < 4; ++word) {
-            uint32_t bits = c.not_finite[segment & 7][(j - first_masked) * 4 + word];
+            uint32_t bits = c.not_finite[segment % kNotes][(j - first_masked) * 4 + word];
             for (; bits; bits &= bits - 1) {
               const int key = j * kTile + word * 32 + __ffs(bits) - 1;
               if (!live || key >= limit) continue;
@@ -547,10 +554,6 @@ __device__ void softmax_rows(const Line<kCached>& line, Control& c, const Softma
       if (!whole) *partial_ml<D>(mine, slot_row) = make_float2(m, l);
     }
     tc_fence_before();
-    if (!kCached && v.count) {
-      __syncwarp();
-      if ((threadIdx.x & 31) == 0) mbar_arrive(&c.notes_read[segment & 7]);
-    }
     if (whole) continue;
     // ---- the item is cut: the CTA that comes last adds the parts, in order
     const Reach at = reach(w, c);  // the first part's counter counts

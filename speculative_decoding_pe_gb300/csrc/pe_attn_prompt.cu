@@ -78,12 +78,7 @@ __device__ void look_over_values(const Line<false>& line, Control& c, uint8_t* s
   for (int segment = 0; walk_next(line, w); ++segment) {
     const int least = 2 * w.mt * line.span + 1;  // keys that the item's first row sees
     uint32_t any = 0;
-    // A stream may still be storing the result of eight segments ago while the other
-    // goes through prompts too short for two.  One without visits reads nothing, and
-    // would arrive far ahead: its arrivals come from here.
-    if (!wait_warp(&c.notes_read[segment & 7], ((segment >> 3) & 1) ^ 1, dead)) return;
-    if (lane < 8 && !visits(line, w, lane >> 2).count) mbar_arrive(&c.notes_read[segment & 7]);
-    if (lane == 0) c.any_not_finite[segment & 7] = 0;
+    if (lane == 0) c.any_not_finite[segment % kNotes] = 0;
     for (int j = w.t0; j < w.t1; ++j, ++k) {
       const uint32_t st = k % S::kStages;
       if (!wait_warp(&c.v_full[st], (k / S::kStages) & 1, dead)) return;
@@ -126,8 +121,8 @@ __device__ void look_over_values(const Line<false>& line, Control& c, uint8_t* s
           const uint32_t bits = __ballot_sync(0xffffffffu, found);
           any |= bits;
           if (lane == 0) {
-            c.not_finite[segment & 7][(j - least / kTile) * 4 + word] = bits;
-            c.any_not_finite[segment & 7] = any != 0;
+            c.not_finite[segment % kNotes][(j - least / kTile) * 4 + word] = bits;
+            c.any_not_finite[segment % kNotes] = any != 0;
           }
         }
         fence_async_shared();
