@@ -284,9 +284,10 @@ __device__ void softmax_rows(const Line<kCached>& line, Control& c, const Softma
   // How far (log2) a score may pass the maximum that is held before the row takes
   // the new one and O is rescaled.  O must not overflow where the quotient is finite:
   // for prompts, n keys of magnitude v give up to 2^8 n v.  Over the cache a value is
-  // at most 6 * 448 and keys are below 2^31, so 2^64 leaves room, and tells more tiles
-  // apart by their key scales alone (below; their bound lies some 2^30 over the scores).
-  constexpr float kSlack = kCached ? 64.0f : 8.0f;
+  // at most 6 * 448 and keys are below 2^31, so 2^80 still leaves room; there the room
+  // spares the search for a maximum, whose bound (below) lies some 2^30 to 2^50 over the
+  // scores (256 drafts: 2.16 ms; 2.21 with 2^64, 2.28 with 2^40).
+  constexpr float kSlack = kCached ? 80.0f : 8.0f;
   // Columns of S in registers at a time.  Over the cache eight warps that convert
   // codes share the instruction cache with the softmax, and its shorter code is
   // worth more than fewer loads (b64 drafts: 727 us against 468); a prompt's
