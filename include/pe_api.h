@@ -417,7 +417,11 @@ int pe_latency_floor(int32_t ctas, int32_t hops, const int32_t* chain, int32_t n
  * nearest, ties to even, saturating; s = 0 holds zeros), and stands for code
  * times s.  D is 64 or 128, block_size a multiple of 16, slot =
  * block * block_size + offset as in slot_mapping.  A group with an infinity
- * saturates; the codes of a group with a NaN are unspecified (finite). */
+ * saturates; the codes of a group with a NaN are unspecified (finite).
+ * There is no scale above the groups': one whose largest magnitude is at most
+ * 6 * 2^-10 is held as zeros, and below 6 * 2^-6 its scale has fewer bits (e4m3
+ * is subnormal there).  A layer with values that small scales them up before
+ * the append, and the result of the attention down. */
 
 /* Rotate queries and keys by position and write keys and values to the cache.
  * For row t, head h, pairs (x0, x1) of the first rot_dim elements are turned:
@@ -479,7 +483,11 @@ size_t pe_workspace_bytes_attn(int32_t D);
  * The keys of the rows themselves have to be in the cache (pe_kv_append).
  *  q, out [T,Hq,D] bf16, dense; out may be q.  offsets [B+1] int32: the
  *  segments, as out_offsets; NULL: T/B rows each.  is_rejected [T] or NULL: none.
- *  scale: finite, above 0.  Sums and softmax statistics are fp32.
+ *  scale: finite, above 0.  Scores, sums and softmax statistics are fp32; a
+ *  weight below 2^-100 of its row's largest may count as nothing.  Rounded to
+ *  fewer bits: queries to f16 after a power of two is taken out of each row
+ *  (elements below 2^-14 of its largest lose bits, below 2^-25 all), weights to
+ *  tf32 (up to 16 rows of a request, offsets NULL) or bf16, the result to bf16.
  *  err: PE_ERR_OFFSETS (offsets no partition of T: nothing is written);
  *  PE_ERR_BLOCK_RANGE (a position below 0 sees nothing, one past the table
  *  sees the table's keys; the keys of a page outside the cache are left out);
@@ -502,7 +510,8 @@ typedef struct pe_attn_cached_args {
 int pe_attn_cached(const pe_attn_cached_args* args /* host */, void* stream);
 
 /* Causal attention over whole packed prompts: row i of a segment sees the
- * keys 0..i of the same segment.
+ * keys 0..i of the same segment.  Precision as above, but queries stay bf16;
+ * results are finite where n v is below 2^119 for n values of magnitude v.
  *  q [T,Hq,D], k, v [T,Hkv,D] bf16 with row and head strides in elements
  *  (multiples of 8; below 2^31; not 0 along an axis of more than one); out
  *  [T,Hq,D] dense (it may be q where that is); offsets [B+1] int32 or NULL as

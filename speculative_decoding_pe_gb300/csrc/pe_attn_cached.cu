@@ -89,9 +89,10 @@ extern "C" int pe_attn_cached(const pe_attn_cached_args* a, void* stream) {
   p.err = a->err;
   p.ws = static_cast<uint8_t*>(a->workspace);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  // Rows of a request that are known to be few: 64 requests of 8000 keys, 8 rows 0.105
-  // ms here against 0.217, 16 rows 0.157 against 0.217 (heads of 64), 0.172 against
-  // 0.181 (of 128).
+  // Rows of a request that are known to be few: 64 requests of 8000 keys, in a graph, 8
+  // rows 96 us in the few-row kernel against 190 in the other, 16 rows 145 against 190 (8
+  // heads of 64); 86 against 161 and 150 against 161 (4 heads of 128).  With offsets they
+  // are not known here.
   const int64_t rows = a->offsets ? INT64_MAX : (int64_t)(a->T / a->B) * (a->Hq / a->Hkv);
   if (rows <= 8) return a->D == 64 ? launch_few<64, 1>(p, dev.sm_count, s) : launch_few<128, 1>(p, dev.sm_count, s);
   if (rows <= 16) return a->D == 64 ? launch_few<64, 2>(p, dev.sm_count, s) : launch_few<128, 2>(p, dev.sm_count, s);

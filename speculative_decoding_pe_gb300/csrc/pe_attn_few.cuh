@@ -22,12 +22,17 @@
 // Work.  A part of the line is a run of records (16 keys); its CTA's 8 warps
 // share a segment's records and meet at its end.  Each warp brings its records
 // by bulk copies, a step ahead, through segments.  A cut part has 16 records at least
-// (one token over 4000 keys: 8 records 21.7 us, 16: 16.6, 32: 17.0, 64: 18.3).
+// (one token over 4000 keys, in a graph: 8 records 12.9 us, 16: 12.7, 32: 13.8, 64: 16.6).
 //
-// Measured, 8 rows: 256 requests of 32 000 keys on average, 4 heads of 128: 1.07 ms,
-// 4.5 TB/s of the cache, 68 % of a plain copy: bound by the conversion's instructions
-// (with f16 weights, which are not enough, 0.92 ms).  One request of 4000 keys, 8 heads of 64: 12.2 us, of which 3 are
-// the plan, 2 the keys, 4 the meetings of the warps and of the parts.
+// Measured (in a graph), 8 rows: 256 requests of 32 000 keys on average, 4 heads of
+// 128: 1.06 ms, 4.5 TB/s of the cache, 68 % of a plain copy; issue slots 61 % busy with
+// conversion, waits between dependent instructions and for the alu pipe in between
+// (f16 weights, whose range is not enough, 0.92 ms; bf16 weights and values 1.10 ms;
+// f16 for steps without small weights and tf32 for the others 0.99 and 1.11 ms).  One
+// request of 4000 keys, 8 heads of 64: 12.7 us, of which 3 are the plan, 2 the keys, 4
+// the meetings of the warps and of the parts.  With 9 to 16 rows (NB = 2) some 600
+// bytes a thread (D = 64: 300) spill to local memory; it is still the faster kernel
+// there (pe_attn_cached.cu).
 #pragma once
 
 #include "pe_attn_line.cuh"

@@ -4,10 +4,10 @@
 // kUnit keys.  The units of all items form one line, request after request,
 // and part c of n is units [c U / n, (c + 1) U / n): equal parts whatever the
 // lengths are, but that an end less than `snap` units from an item's end moves
-// there, and any end in a short item, because a piece of an item costs a CTA as much as some units do (one
-// token over 4000 keys: 16.4 us against 13.2).  No plan is made on the host, which
-// does not know the lengths: every CTA sums them up for itself (1 to 3 us of a small
-// call, most of it the first fetch of the instructions).
+// there, and any end in a short item, because a piece of an item costs a CTA as much
+// as some units do (one token over 4000 keys, in a graph: 17.3 us against 12.7).  No
+// plan is made on the host, which does not know the lengths: every CTA sums them up for
+// itself (1 to 3 us of a small call, most of it the first fetch of the instructions).
 #pragma once
 
 #include "pe_attn.cuh"
@@ -30,7 +30,10 @@ __device__ __forceinline__ long long sum_tiles(long long k, long long w) {
     const long long q = k >> shift;
     return ((q * (q + 1) / 2) << shift) + (k - (q << shift)) * (q + 1);
   }
-  // sum_{i=0..k-1} floor((a i + b) / m), with ceil(x / 128) = floor((x + 127) / 128)
+  // sum_{i=0..k-1} floor((a i + b) / m), with ceil(x / 128) = floor((x + 127) / 128),
+  // by the known reduction: whole multiples of m out of a and b, then the points under
+  // the line counted by columns instead of rows, which exchanges a and m as Euclid's
+  // algorithm does
   long long n = k, m = kTile, a = w, b = w + kTile - 1, sum = 0;
   for (;;) {
     if (a >= m) {
@@ -90,7 +93,7 @@ struct Walk {
 template <bool kCached, int kUnit>
 __device__ __forceinline__ bool walk_next(const Line<kCached, kUnit>& line, Walk& w) {
   if (w.u >= w.end) return false;
-  w.t0 += w.t1 - w.t0;  // the tile after the last one
+  w.t0 = w.t1;  // the tile after the last one
   if (w.t1 >= w.tiles) {
     w.t0 = 0;
     if (++w.mt >= line.items(w.rows)) {
@@ -229,8 +232,8 @@ __device__ bool plan(Line<kCached, kUnit>& line, int min_units, int most_snap, C
   if (tid < 2) {  // the part's begin and end
     const long long total = c.total;
     // a part below min_units would spend its time on partial results, unless it is
-    // a whole item (22 requests of 8 to 16 keys, 4 heads: 57 us in parts of 16
-    // records, 10.5 in parts of an item)
+    // a whole item (22 tokens over 8 to 16 keys, 4 heads of 128, in a graph: 77 us in
+    // parts of 16 records, 13 in parts of an item)
     const long long whole = quotient(total, min_units);
     const long long parts = max(1LL, min((long long)gridDim.x, max(whole, (long long)c.items)));
     // half a part, up where the parts are items
@@ -282,10 +285,10 @@ struct Cut {
 
 // How the parts of an item become one.  Whichever CTA comes last adds them all;
 // or, when every CTA of the call runs at once (`together`) and the parts are many,
-// each CTA adds its share of the rows after its own part.  One request over 30000
-// keys, one key head of 128: a token 34 us alone, 15 together; a draft 113 and 25.
-// With few parts the others' wait is longer (4 parts: 10.6 us alone, 12.7 together;
-// 5: 44 and 47; 9: 48.5 and 47.8).
+// each CTA adds its share of the rows after its own part.  In a graph, one request
+// over 30000 keys, one key head of 128: a token 34 us alone, 16 together; a draft 107 and
+// 27.  With few parts nothing is gained (4 parts 12.4 us both ways, 9 parts 54 us alone
+// and 56 together).
 constexpr int kTogether = 8;
 // The counter: arrivals in the low half, then CTAs that have taken their share.
 //

@@ -12,17 +12,19 @@
 // 2^-31 of the largest would vanish, which shows where the heaviest keys' values
 // are zeros.
 //
-// Bound by instructions: codes become operands (K 9, V 17 a word of 8 codes) and
-// scores weights (2.5 each) on the same issue slots, 63 % of which are busy, while
-// the tensor cores are 29 % and memory 24 % busy.  More converter warps, a warp of
-// its own for the largest scales, or converters on two of the four schedulers each
-// change nothing (391 to 411 us): what counts is the number of instructions, and that
-// the loops of the roles fit the instruction cache together.
+// Codes become operands (K 9, V 17 instructions a word of 8 codes) and scores weights
+// (2.5 each) on the same issue slots.  With heads of 64 these bound it: 58 % of the slots
+// are busy, the tensor cores 32 %, memory 25 %.  More converter warps, a warp of its own
+// for the largest scales, or converters on two of the four schedulers each changed
+// nothing: what counts is the number of instructions, and that the loops of the roles
+// fit the instruction cache together.  With heads of 128 nothing is that busy (slots 50
+// %, tensor cores 38 %, memory 30 %): two stages of keys, values and raw records, and
+// two buffers of scores, leave the roles waiting for each other.
 //
-// Measured, 14 rows (drafts) of 8 heads: 64 requests of 16 500 keys, 8 key heads of
-// 64: 0.39 ms (1.6 TB/s of the cache, 0.38 PFLOP/s of rows that are not rejected or
-// padding); 256 of 32 000, 4 heads of 128: 2.18 ms (2.2 TB/s, 0.53 PFLOP/s).  One request of 6000
-// keys: 18.2 us.
+// Measured (in a graph), 14 rows (drafts) of 8 heads: 64 requests of 16 500 keys, 8 key
+// heads of 64: 0.39 ms (1.6 TB/s of the cache, 0.38 PFLOP/s of rows that are not rejected
+// or padding); 256 of 32 000, 4 heads of 128: 2.16 ms (2.3 TB/s, 0.54 PFLOP/s).  One
+// request of 6000 keys: 18.5 us.
 #pragma once
 
 #include "pe_attn_mma.cuh"
@@ -94,8 +96,8 @@ __device__ void bring_records(const Line<true>& line, Control& c, Raw& raw, cons
 // Codes of one token, D elements, into row `row` of an operand tile: as f16 (the
 // keys, next to f16 queries) or as bf16 (the values, next to bf16 weights).
 // Both are exact.  Values rolled, keys two steps at a time: the roles of this
-// kernel share an instruction cache (b64 drafts 391 us; values unrolled too, 401;
-// keys rolled too, 401).
+// kernel share an instruction cache (64 drafts, in a graph: 392 us; values two steps
+// at a time too, 395; keys rolled too, 399).
 template <int D, bool kBf16, int kUnroll = kBf16 ? 1 : 2>
 __device__ __forceinline__ void put_codes(uint8_t* tile, int row, const uint8_t* codes, const uint8_t* scales,
                                           bool valid) {
@@ -250,8 +252,6 @@ __global__ void __launch_bounds__(kManyThreads, 1) attn_many_kernel(const Cached
   // the loads and the converters
   if (warp < 8)
     take_registers<128>();
-  else if (warp < 12)
-    give_registers<72>();
   else
     give_registers<72>();
   if (warp < 8) {

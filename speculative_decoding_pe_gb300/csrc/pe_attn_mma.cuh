@@ -290,8 +290,8 @@ __device__ void softmax_rows(const Line<kCached>& line, Control& c, const Softma
   constexpr float kSlack = kCached ? 80.0f : 8.0f;
   // Columns of S in registers at a time.  Over the cache eight warps that convert
   // codes share the instruction cache with the softmax, and its shorter code is
-  // worth more than fewer loads (b64 drafts: 727 us against 468); a prompt's
-  // softmax is faster unrolled (b8: 2.19 ms against 2.54).
+  // worth more than fewer loads (64 drafts: 808 us in 128 columns, 392 in 64); a
+  // prompt's softmax is faster unrolled (eight prompts: 2.19 ms in 64, 2.06 in 128).
   constexpr int kCols = kCached ? 64 : kTile;
   volatile int* dead = &c.dead;
   const int row = threadIdx.x & (kTile - 1);
@@ -504,8 +504,8 @@ __device__ void softmax_rows(const Line<kCached>& line, Control& c, const Softma
     };
     auto inverse = [](float l) { return l > 0.0f ? 1.0f / l : (l == l ? 0.0f : l); };  // no key: zeros
     float4* half = partial<D>(p.ws, blockIdx.x, 2);
-    // (an item of one tile is stream 0's alone: 256 drafts of up to 60 keys 54 us
-    // against 71 with an exchange of nothing)
+    // (an item of one tile is stream 0's alone: 256 drafts of up to 60 keys, 4 heads of
+    // 128, in a graph 54 us against 72 with an exchange of nothing)
     const bool both = halves && w.t1 - w.t0 > 1;
     const int half_row = (exchanges & 1) * kTile + row;
     exchanges += both;

@@ -9,12 +9,13 @@
 // row masks: rows past the prompt are cleared, and elements that are not finite
 // are taken out and given back at the end to the rows that see them.
 //
-// Measured: two prompts of 18 000 tokens, 32 heads of 128 on 4: 3.47 ms, 1.49
-// PFLOP/s of the causal half, 78 % of a library product's burst rate (3.65 ms in a
-// long run under the power cap, 81 % of its sustained rate): bound by the products.  Eight prompts of 4600 tokens, 64 heads of
-// 64 on 8: 2.02 ms, 0.89 PFLOP/s: bound by the softmax, whose exponentials alone take
-// 0.72 ms and its other instructions about as much.  Sixteen prompts of up to 131
-// tokens: 17.6 us, a chain of a plan, two or three tiles a CTA, and their stores.
+// Measured (in a graph): two prompts of 18 000 tokens, 32 heads of 128 on 4: 3.46 ms,
+// 1.49 PFLOP/s of the causal half, 78 % of a library product's burst rate (3.65 ms in a
+// long run under the power cap, 81 % of its sustained rate): bound by the products.
+// Eight prompts of 4600 tokens, 64 heads of 64 on 8: 2.06 ms, 0.88 PFLOP/s: bound by the
+// softmax, whose exponentials alone take 0.72 ms and its other instructions about as
+// much.  Sixteen prompts of up to 131 tokens: 17.8 us, a chain of a plan, two or three
+// tiles a CTA, and their stores.
 #include "pe_attn_mma.cuh"
 
 namespace pe {
