@@ -105,6 +105,11 @@ typedef enum pe_dtype { PE_F32 = 0, PE_BF16 = 1 } pe_dtype;
 
 #define PE_ERR_POS_RANGE 1024u /* position outside the rotation table: row
                                  taken as not rotated                       */
+#define PE_ERR_PARAM 2048u     /* a request's sampling parameters or given
+                                 number, or its eviction sizes, are not usable:
+                                 the call states what it writes instead     */
+#define PE_ERR_EMPTY_ROW 4096u /* a logits row has no column that weighs
+                                 anything: token -1                         */
 
 /* Limits checked on the host. */
 #define PE_MAX_KP 255 /* previous draft depth K'  */
@@ -205,6 +210,97 @@ int pe_verify_sampled(const void* target_logits, const void* draft_logits,
                       float temperature, uint64_t seed, int32_t* accepted_len,
                       int32_t* bonus_token, void* workspace, uint32_t* err,
                       void* stream);
+
+/* Filtered sampling: what a request asks for.  Each pointer is an array of one
+ * entry per request, or NULL (1, off, off, off).
+ * A row's filter: y = logit / T; columns by y descending, equal ones by column.
+ * Kept are
+ *   the first k;
+ *   of those, the smallest prefix whose weight (of e^y) is at least p times
+ *   theirs, at least one column;
+ *   of those, the columns of at least m times the row's largest weight.
+ * temperature T: 0 keeps the first column alone (greedy); else 2^-30..2^30.
+ * top_k k: <= 0 or >= V is off.  top_p p: >= 1 is off; <= 0 keeps one column.
+ * min_p m: <= 0 is off; >= 1 keeps the columns that equal the largest.
+ * A NaN, or another T, raises PE_ERR_PARAM.
+ * A logit of -infinity (a masked column) or NaN weighs nothing; where a row has
+ * +infinities, these share its weight; a weight below 2^-45 of the row's
+ * largest may count as nothing.  A row without any weight raises
+ * PE_ERR_EMPTY_ROW.
+ * The draw from given u in [0,1): the first column, in column order, whose
+ * running sum of kept weights exceeds u times their sum.  Weights and sums
+ * carry some 32 bits: tokens agree with an exact evaluation except where u
+ * falls within that rounding of a border between two columns, or a prefix's
+ * weight within it of p. */
+typedef struct pe_filter {
+  const float* temperature;
+  const int32_t* top_k;
+  const float* top_p;
+  const float* min_p;
+} pe_filter;
+#define PE_MAX_SAMPLE_V 262144           /* columns of a filtered row   */
+#define PE_MAX_SAMPLE_ROWS (1 << 27)     /* filtered rows of one call   */
+
+/* Drafter readout by sampling (pe_draft_readout's counterpart for callers
+ * that sample their drafts): out_tokens[i] is drawn from the filtered
+ * distribution of logits row sample_idx[i] (row i when NULL) by u[i], under
+ * the parameters of request i / (n / requests).
+ *  logits     [rows, V] of `dtype`, row stride `row_stride` elements.
+ *  out_prob   [n] the drawn token's probability in that distribution; or NULL.
+ *  A row index outside [0, rows) gives -1 (probability 0) and PE_ERR_ROW_RANGE;
+ *  parameters that are not usable, or u outside [0,1), -1 and PE_ERR_PARAM; an
+ *  empty row -1 and PE_ERR_EMPTY_ROW.
+ * n == 0 enqueues nothing.  No workspace. */
+typedef struct pe_draft_sample_args {
+  int32_t n, requests, rows, V, dtype;
+  int64_t row_stride;
+  const void* logits;
+  const int32_t* sample_idx; /* [n] or NULL (then n <= rows) */
+  pe_filter filter;          /* arrays [requests] */
+  const float* u;            /* [n] */
+  int32_t* out_tokens;       /* [n] */
+  float* out_prob;           /* [n] or NULL */
+  uint32_t* err;
+} pe_draft_sample_args;
+int pe_draft_sample(const pe_draft_sample_args* args /* host */, void* stream);
+
+/* Bytes of scratch that pe_verify_filtered needs.  Its content does not matter
+ * before a call and is not kept for the next one; calls that may run
+ * concurrently need separate workspaces. */
+size_t pe_workspace_bytes_filtered(int32_t B, int32_t Kp);
+
+/* Rejection sampling of drafts drawn by pe_draft_sample: pe_verify_sampled's
+ * rule [P3] on filtered distributions.  With p_j and q_j the filtered
+ * distributions of target row b(Kp+1)+j and draft row b*Kp+j under request
+ * b's parameters, and x draft d_{j+1}:
+ *   draft j is accepted when u_accept[b*Kp+j] * q_j(x) < p_j(x); a token
+ *   outside [0,V) is rejected.
+ *   accepted_len[b] = a_b = the first rejected j, or Kp.
+ *   bonus_token[b] = the draw by u_draw[b] from max(0, p_a - q_a) when
+ *   a_b < Kp (from p_a when that is zero everywhere), from p_Kp else.
+ *   accept_prob[b*Kp+j] = min(1, p_j(x) / q_j(x)) of every draft (0 where
+ *   p_j(x) is 0 or the token outside [0,V)); or NULL.
+ *  target_logits, draft_logits, in_tokens, u_accept as pe_verify_sampled.
+ *  A request whose parameters or u_draw are not usable gets accepted_len 0,
+ *  bonus_token -1, accept_prob 0 and PE_ERR_PARAM; an empty target row rejects its
+ *  draft and has bonus token -1, an empty draft row counts as q = 0.
+ * Two launches; B == 0 enqueues nothing. */
+typedef struct pe_verify_filtered_args {
+  int32_t B, Kp, V, dtype;
+  int64_t target_stride, draft_stride;
+  const void* target_logits;
+  const void* draft_logits;
+  const int32_t* in_tokens;
+  const float* u_accept;
+  const float* u_draw; /* [B] */
+  pe_filter filter;    /* arrays [B] */
+  int32_t* accepted_len;
+  int32_t* bonus_token;
+  float* accept_prob; /* [B*Kp] or NULL */
+  void* workspace;
+  uint32_t* err;
+} pe_verify_filtered_args;
+int pe_verify_filtered(const pe_verify_filtered_args* args /* host */, void* stream);
 
 /* Draft-batch rebuild [P2 Fused Triton Kernel; KV Cache and CUDA Graphs].
  * For request b with bonus slot s_b = n_b-1-Kp+a_b and slot k of its output

@@ -33,6 +33,8 @@ ERR_NAN = 128
 ERR_INTERNAL = 256
 ERR_WORKSPACE = 512
 ERR_POS_RANGE = 1024
+ERR_PARAM = 2048
+ERR_EMPTY_ROW = 4096
 MAX_KP, MAX_K = 255, 256
 
 # every function the C header declares
@@ -43,7 +45,8 @@ EXPORTS = ("pe_workspace_bytes", "pe_verify_greedy", "pe_draft_readout",
            "pe_get_tuning",
            "pe_set_tuning", "pe_latency_floor", "pe_status_str",
            "pe_kv_append", "pe_kv_read", "pe_workspace_bytes_attn", "pe_attn_cached",
-           "pe_attn_prompt")
+           "pe_attn_prompt", "pe_draft_sample", "pe_workspace_bytes_filtered",
+           "pe_verify_filtered")
 
 
 class PEError(RuntimeError):
@@ -102,6 +105,22 @@ class AttnPromptArgs(ctypes.Structure):
     _fields_ = ([(n, i32) for n in ("T", "B", "Hq", "Hkv", "D")] + [("scale", ctypes.c_float)] +
                 [(n, i64) for n in ("q_row", "q_head", "k_row", "k_head", "v_row", "v_head")] +
                 [(n, P) for n in ("q", "k", "v", "offsets", "out", "workspace", "err")])
+
+
+class DraftSampleArgs(ctypes.Structure):
+    """Mirror of pe_draft_sample_args (its pe_filter's fields in place)."""
+    _fields_ = ([(n, i32) for n in ("n", "requests", "rows", "V", "dtype")] + [("row_stride", i64)] +
+                [(n, P) for n in ("logits", "sample_idx", "temperature", "top_k", "top_p", "min_p",
+                                  "u", "out_tokens", "out_prob", "err")])
+
+
+class VerifyFilteredArgs(ctypes.Structure):
+    """Mirror of pe_verify_filtered_args (its pe_filter's fields in place)."""
+    _fields_ = ([(n, i32) for n in ("B", "Kp", "V", "dtype")] +
+                [(n, i64) for n in ("target_stride", "draft_stride")] +
+                [(n, P) for n in ("target_logits", "draft_logits", "in_tokens", "u_accept", "u_draw",
+                                  "temperature", "top_k", "top_p", "min_p", "accepted_len",
+                                  "bonus_token", "accept_prob", "workspace", "err")])
 
 
 _lock = threading.Lock()
@@ -168,7 +187,12 @@ def _open(path: str):
     lib.pe_workspace_bytes_attn.restype = ctypes.c_size_t
     lib.pe_attn_cached.argtypes = [ctypes.POINTER(AttnCachedArgs), P]
     lib.pe_attn_prompt.argtypes = [ctypes.POINTER(AttnPromptArgs), P]
-    for f in ("pe_kv_append", "pe_kv_read", "pe_attn_cached", "pe_attn_prompt"):
+    lib.pe_draft_sample.argtypes = [ctypes.POINTER(DraftSampleArgs), P]
+    lib.pe_workspace_bytes_filtered.argtypes = [i32, i32]
+    lib.pe_workspace_bytes_filtered.restype = ctypes.c_size_t
+    lib.pe_verify_filtered.argtypes = [ctypes.POINTER(VerifyFilteredArgs), P]
+    for f in ("pe_kv_append", "pe_kv_read", "pe_attn_cached", "pe_attn_prompt", "pe_draft_sample",
+              "pe_verify_filtered"):
         getattr(lib, f).restype = ctypes.c_int
     lib.pe_status_str.argtypes = [ctypes.c_int]
     lib.pe_status_str.restype = ctypes.c_char_p
@@ -644,6 +668,88 @@ def attn_prompt(q, k, v, offsets, out, workspace, err, scale=None, B=None, strea
                        _vector(offsets, "offsets", torch.int32, B + 1),
                        _dense(out, "out", shape), ws, ep)
     _check(lib, lib.pe_attn_prompt(ctypes.byref(a), _raw_stream(stream, q)), "pe_attn_prompt")
+
+
+# ------------------------------------------------------------ filtered sampling
+
+def _columns(t: torch.Tensor, name: str):
+    """Pointer, element type and row stride of logits rows [rows, V]."""
+    if not t.is_cuda or t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
+        raise ValueError("%s must be a 2-D CUDA tensor with unit column stride" % name)
+    rows, V = t.shape
+    # the stride of one row is never used
+    return t.data_ptr(), _dtype_code(t), t.stride(0) if rows > 1 else -(-V // 8) * 8
+
+
+def _filter(temperature, top_k, top_p, min_p, n: int):
+    """Pointers of the parameter arrays of n requests."""
+    return (_vector(temperature, "temperature", torch.float32, n), _vector(top_k, "top_k", torch.int32, n),
+            _vector(top_p, "top_p", torch.float32, n), _vector(min_p, "min_p", torch.float32, n))
+
+
+def draft_sample(logits, u, out_tokens, err, temperature=None, top_k=None, top_p=None, min_p=None,
+                 out_prob=None, sample_idx=None, stream=None):
+    """Sampled draft tokens: out_tokens[i] is drawn by u[i] from the distribution
+    of logits row sample_idx[i] (row i when None) under temperature, top-k, top-p
+    and min-p: arrays of one entry per request, rows request after request, or
+    None (1, off, off, off).  out_prob takes the tokens' probabilities."""
+    lib = _lib or load()
+    lp, dt, stride = _columns(logits, "logits")
+    rows, V = logits.shape
+    n = u.numel()
+    counts = {t.numel() for t in (temperature, top_k, top_p, min_p) if t is not None} or {1}
+    requests = counts.pop()
+    if counts or n and (not requests or n % requests):
+        raise ValueError("the parameters must have one entry per request, and %d rows share them evenly" % n)
+    a = DraftSampleArgs(n, requests, rows, V, dt, stride, lp, _vector(sample_idx, "sample_idx", torch.int32, n),
+                        *_filter(temperature, top_k, top_p, min_p, requests),
+                        _vector(u, "u", torch.float32, n), _vector(out_tokens, "out_tokens", torch.int32, n),
+                        _vector(out_prob, "out_prob", torch.float32, n), _vector(err, "err", torch.int32, 1))
+    _check(lib, lib.pe_draft_sample(ctypes.byref(a), _raw_stream(stream, logits)), "pe_draft_sample")
+
+
+def workspace_bytes_filtered(B: int, Kp: int) -> int:
+    return int(load().pe_workspace_bytes_filtered(B, Kp))
+
+
+def new_filtered_workspace(B: int, Kp: int, device="cuda") -> torch.Tensor:
+    """Scratch for verify_filtered of up to B requests of depth Kp (reusable)."""
+    return torch.empty(workspace_bytes_filtered(B, Kp), dtype=torch.uint8, device=device)
+
+
+def verify_filtered(target_logits, draft_logits, Kp, in_tokens, u_accept, u_draw, accepted_len, bonus_token,
+                    workspace, err, temperature=None, top_k=None, top_p=None, min_p=None, accept_prob=None,
+                    stream=None):
+    """Rejection sampling of B requests' drafts against the filtered
+    distributions that draft_sample draws from: target rows B*(Kp+1), draft rows
+    B*Kp, accept coins u_accept[B*Kp], u_draw[B] for the bonus tokens; parameters
+    of one entry per request, or None.  accept_prob takes min(1, p/q) of every
+    draft."""
+    lib = _lib or load()
+    tp, dt, t_stride = _columns(target_logits, "target_logits")
+    rows, V = target_logits.shape
+    if Kp < 0 or rows % (Kp + 1):
+        raise ValueError("target_logits rows must be a multiple of Kp+1")
+    B = rows // (Kp + 1)
+    dp, d_stride = None, 0
+    if Kp:
+        dp, ddt, d_stride = _columns(draft_logits, "draft_logits")
+        if ddt != dt or draft_logits.shape != (B * Kp, V):
+            raise ValueError("draft_logits must be [B*Kp, V] of the target's dtype")
+    need = lib.pe_workspace_bytes_filtered(B, Kp)
+    if not workspace.is_cuda or workspace.dtype is not torch.uint8 or not workspace.is_contiguous() or \
+            workspace.numel() < need:
+        raise ValueError("workspace must be what new_filtered_workspace(%d, %d) gives" % (B, Kp))
+    a = VerifyFilteredArgs(B, Kp, V, dt, t_stride, d_stride, tp, dp,
+                           _vector(in_tokens, "in_tokens", torch.int32, rows) if Kp else None,
+                           _vector(u_accept, "u_accept", torch.float32, B * Kp) if Kp else None,
+                           _vector(u_draw, "u_draw", torch.float32, B),
+                           *_filter(temperature, top_k, top_p, min_p, B),
+                           _vector(accepted_len, "accepted_len", torch.int32, B),
+                           _vector(bonus_token, "bonus_token", torch.int32, B),
+                           _vector(accept_prob, "accept_prob", torch.float32, B * Kp),
+                           workspace.data_ptr(), _vector(err, "err", torch.int32, 1))
+    _check(lib, lib.pe_verify_filtered(ctypes.byref(a), _raw_stream(stream, target_logits)), "pe_verify_filtered")
 
 
 def get_tuning() -> dict:

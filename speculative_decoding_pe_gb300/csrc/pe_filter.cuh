@@ -1,0 +1,235 @@
+// Filtered distributions of logits rows: what pe_draft_sample and
+// pe_verify_filtered share.
+//
+// A row's filter under (T, k, p, m): columns ordered by value, equal ones by
+// column; kept are the first k; of those the smallest prefix that holds p of
+// their weight; of those the ones of at least m of the largest weight.  Every
+// step keeps a prefix of the order, so a cut is a value and, among the columns
+// of that value, a last column (Cut below).
+//
+// A row lives in the shared memory of a cluster: one read of global memory,
+// however often the cut's search looks at it.  Weights are
+// w(x) = 2^((x - M) log2(e) / T), M the row's maximum, as a sum of two floats
+// with some 32 bits: the draw falls between running sums of up to V weights, and
+// with 24 bits a draw in a thousand of an unfiltered row would name the
+// neighbour of the right column.  Sums are exact integers or sums of two floats
+// in a fixed order, so a call's results do not depend on timing.
+#pragma once
+
+#include "pe_internal.cuh"
+#include "pe_tma.cuh"
+
+namespace pe {
+
+constexpr int kFT = 512;          // threads of a filter CTA
+constexpr int kFW = kFT / 32;
+constexpr int kListCap = 1024;    // columns of a candidate list
+constexpr int kListK = 256;       // largest top-k that is looked for in a list
+constexpr int kProbe = 128;       // columns that a list is sought for under top-p alone
+constexpr int kMaxCluster = 8;
+
+// ------------------------------------------------------------------ clusters
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+  cluster_arrive();
+  cluster_wait();
+}
+// The same variable in the shared memory of the cluster's CTA `rank`.
+template <class T>
+__device__ __forceinline__ T* at_rank(T* p, uint32_t rank) {
+  T* q;
+  asm("mapa.u64 %0, %1, %2;" : "=l"(q) : "l"(p), "r"(rank));
+  return q;
+}
+
+// ------------------------------------------------------------------- weights
+// 2^(j/32) as the sum of two floats.
+__device__ const float2 kExp2Table[32] = {
+    {0x1.0000000000000p+0f, 0x0.0p+0f}, {0x1.059b0e0000000p+0f, -0x1.9d4f520000000p-25f},
+    {0x1.0b55860000000p+0f, 0x1.9f31220000000p-25f}, {0x1.11301e0000000p+0f, -0x1.fdb4960000000p-25f},
+    {0x1.172b840000000p+0f, -0x1.c157420000000p-27f}, {0x1.1d48740000000p+0f, -0x1.d2e8ca0000000p-25f},
+    {0x1.2387a60000000p+0f, 0x1.ceac480000000p-25f}, {0x1.29e9e00000000p+0f, -0x1.5c04240000000p-25f},
+    {0x1.306fe00000000p+0f, 0x1.4636e20000000p-25f}, {0x1.371a740000000p+0f, -0x1.18aac60000000p-25f},
+    {0x1.3dea640000000p+0f, 0x1.8246840000000p-25f}, {0x1.44e0860000000p+0f, 0x1.8624b40000000p-30f},
+    {0x1.4bfdae0000000p+0f, -0x1.593abc0000000p-25f}, {0x1.5342b60000000p+0f, -0x1.2c56100000000p-25f},
+    {0x1.5ab07e0000000p+0f, -0x1.5bd5ec0000000p-27f}, {0x1.6247ec0000000p+0f, -0x1.f8b5500000000p-25f},
+    {0x1.6a09e60000000p+0f, 0x1.9fcef40000000p-26f}, {0x1.71f75e0000000p+0f, 0x1.1d8bee0000000p-25f},
+    {0x1.7a11480000000p+0f, -0x1.829fd00000000p-25f}, {0x1.82589a0000000p+0f, -0x1.accc7c0000000p-26f},
+    {0x1.8ace540000000p+0f, 0x1.15506e0000000p-27f}, {0x1.93737c0000000p+0f, -0x1.e647440000000p-25f},
+    {0x1.9c49180000000p+0f, 0x1.51f8480000000p-27f}, {0x1.a5503c0000000p+0f, -0x1.b83b540000000p-25f},
+    {0x1.ae89fa0000000p+0f, -0x1.a94b140000000p-26f}, {0x1.b7f7700000000p+0f, -0x1.a094380000000p-25f},
+    {0x1.c199be0000000p+0f, -0x1.3d56b20000000p-27f}, {0x1.cb720e0000000p+0f, -0x1.8837cc0000000p-27f},
+    {0x1.d5818e0000000p+0f, -0x1.822dbc0000000p-27f}, {0x1.dfc9740000000p+0f, -0x1.908c940000000p-25f},
+    {0x1.ea4afa0000000p+0f, 0x1.52486c0000000p-27f}, {0x1.f507660000000p+0f, -0x1.246eb00000000p-26f},
+};
+
+// One row's scale: w(x) = 2^((x - M) c), c = log2(e) / T as two floats.  far: distance
+// from M at which a weight counts as nothing (2^-100).  A row with an infinity
+// shares its weight among those columns.
+struct Scale {
+  float M, ch, cl, far;
+  bool inf;
+};
+
+__device__ __forceinline__ Scale make_scale(float M, float T) {
+  Scale s;
+  const double c = 1.4426950408889634 / (T > 0.f ? (double)T : 1.0);
+  s.M = M;
+  s.inf = M == INFINITY;
+  s.ch = (float)c;
+  s.cl = (float)(c - (double)s.ch);
+  s.far = (float)(100.0 / c);
+  return s;
+}
+
+// w(x) = hi + lo.  y = (x - M) c = n + j/32 + r with |r| <= 1/64;
+// 2^y = 2^n 2^(j/32) (1 + q), q = 2^r - 1 from its Taylor series (the first
+// term left out is below 2^-39).  The difference and the products are carried with
+// their rounding errors; what is left is the rounding of q, 2^-31 at most.
+__device__ __forceinline__ float2 weight(const Scale& s, const float2* table, float x) {
+  if (s.inf) return make_float2(x == INFINITY ? 1.f : 0.f, 0.f);
+  float d = x - s.M;
+  const float bb = d - x;
+  const float dl = (x - (d - bb)) - (s.M + bb);  // exact: d + dl = x - M
+  float e0 = d >= -s.far ? dl : 0.f;
+  d = fmaxf(d, -s.far);  // -inf and NaN too
+  const float p = d * s.ch;
+  const float e = fmaf(d, s.ch, -p) + fmaf(d, s.cl, e0 * s.ch);
+  const float z = p + 393216.f;  // 1.5 * 2^18: the sum's last bit is 1/32
+  const int zi = __float_as_int(z) - 0x48c00000;
+  const float r = (p - (z - 393216.f)) + e;
+  const float2 t = table[zi & 31];
+  const float in = fmaf(r, fmaf(r, fmaf(r, 0x1.3b2ab60000000p-7f, 0x1.c6b08e0000000p-5f), 0x1.ebfbe00000000p-3f), -0x1.05c6100000000p-29f);
+  const float q = fmaf(r, 0x1.62e4300000000p-1f, r * in);
+  const float two_n = __int_as_float((127 + (zi >> 5)) << 23);
+  return make_float2(t.x * two_n, fmaf(t.x, q, t.y) * two_n);
+}
+
+// Sum of weights: a float whose last bit is fixed by a bias larger than anything that
+// is added (so that what an addition drops is exact), and the sum of what was dropped.
+template <int kBias>
+struct WeightSum {
+  float s = (float)kBias, lo = 0.f;
+  __device__ __forceinline__ void add(float h, float l) {
+    const float t = s + h;
+    lo += (h - (t - s)) + l;
+    s = t;
+  }
+  // times 2^bits, as an integer
+  __device__ __forceinline__ unsigned long long fixed(int bits) const {
+    const double v = ((double)(s - (float)kBias) + (double)lo) * (double)(1ull << bits);
+    return v > 0.0 ? (unsigned long long)(v + 0.5) : 0ull;
+  }
+};
+constexpr int kSumBits = 44;   // row sums: up to 2^18 weights of at most 1
+constexpr int kListBits = 52;  // list sums: up to 2^10
+
+// ---------------------------------------------------------------- elements
+template <int DT>
+struct Elt;
+template <>
+struct Elt<PE_BF16> {
+  static constexpr int kN = 8, kSize = 2, kKeyBits = 16;
+  __device__ static __forceinline__ float get(uint4 q, int e) {
+    const uint32_t w = (e >> 1) == 0 ? q.x : (e >> 1) == 1 ? q.y : (e >> 1) == 2 ? q.z : q.w;
+    return (e & 1) ? bf16_hi(w) : bf16_lo(w);
+  }
+  // (a NaN gives way to the other operand)
+  __device__ static __forceinline__ float max_of(uint4 q) {
+    const uint32_t m = bf16x2_max(bf16x2_max(bf16x2_max(q.x, q.y), bf16x2_max(q.z, q.w)), 0xff80ff80u);
+    return fmaxf(bf16_lo(m), bf16_hi(m));
+  }
+  __device__ static __forceinline__ float load(const char* row, int col) {
+    return __uint_as_float((uint32_t)__ldg(reinterpret_cast<const unsigned short*>(row) + col) << 16);
+  }
+};
+template <>
+struct Elt<PE_F32> {
+  static constexpr int kN = 4, kSize = 4, kKeyBits = 32;
+  __device__ static __forceinline__ float get(uint4 q, int e) {
+    return __uint_as_float(e == 0 ? q.x : e == 1 ? q.y : e == 2 ? q.z : q.w);
+  }
+  __device__ static __forceinline__ float max_of(uint4 q) {
+    return fmaxf(fmaxf(fmaxf(__uint_as_float(q.x), __uint_as_float(q.y)),
+                       fmaxf(__uint_as_float(q.z), __uint_as_float(q.w))), -INFINITY);
+  }
+  __device__ static __forceinline__ float load(const char* row, int col) {
+    return __ldg(reinterpret_cast<const float*>(row) + col);
+  }
+};
+
+// Order of values as unsigned integers; NaN as -infinity.
+__device__ __forceinline__ uint32_t value_key(float x) { return ordered_bits(fmaxf(x, -INFINITY)); }
+__device__ __forceinline__ float key_value(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
+}
+
+// ---------------------------------------------------------------------- cuts
+// Kept: x >= floor, and key(x) above `key`, or equal to it with col <= tie.
+struct Cut {
+  uint32_t key;
+  int tie;
+  float floor;
+  __device__ __forceinline__ bool keeps(float x, int col) const {
+    const uint32_t k = value_key(x);
+    return x >= floor && (k > key || (k == key && col <= tie));
+  }
+};
+
+// What is known of a row after its pass (verification).
+struct RowCut {
+  Cut cut;
+  float M;
+  float T;
+  int listed;    // kept columns in the row's list, or -1 (not listed)
+  int token;     // the draw from the row (bonus rows)
+  double W;      // sum of kept weights; 0: nothing to keep; -1: bad parameters
+  double px;     // probability of the row's draft token; -1: not in the vocabulary
+};
+struct Kept {  // a kept column and its weight times 2^kListBits
+  unsigned long long w;
+  int col;
+  int pad;
+};
+constexpr int kKeptCap = 256;  // kept columns that a row's list holds
+
+// Parameters of one request; false: not usable.
+struct Asked {
+  float T, p, m;
+  int k;
+};
+struct AskedArrays {
+  const float* temperature;
+  const int32_t* top_k;
+  const float* top_p;
+  const float* min_p;
+};
+__device__ __forceinline__ bool read_asked(const AskedArrays& a, int i, int V, Asked& o) {
+  o.T = a.temperature ? __ldg(a.temperature + i) : 1.f;
+  o.k = a.top_k ? __ldg(a.top_k + i) : 0;
+  o.p = a.top_p ? __ldg(a.top_p + i) : 1.f;
+  o.m = a.min_p ? __ldg(a.min_p + i) : 0.f;
+  const bool ok = (o.T == 0.f || (o.T >= 0x1p-30f && o.T <= 0x1p30f)) && o.p == o.p && o.m == o.m;
+  if (o.k <= 0 || o.k > V) o.k = V;
+  if (o.T == 0.f) o.k = 1;
+  return ok;
+}
+// Smallest value that min-p keeps (-infinity: all).
+__device__ __forceinline__ float min_p_floor(const Asked& a, float M) {
+  if (!(a.m > 0.f) || a.T == 0.f) return -INFINITY;
+  if (a.m >= 1.f || M == INFINITY) return M;
+  const double t = (double)M + (double)a.T * log((double)a.m);
+  return __double2float_ru(t);  // x >= t exactly when x >= this float
+}
+
+}  // namespace pe

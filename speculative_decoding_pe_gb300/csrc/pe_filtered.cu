@@ -1,0 +1,999 @@
+// Sampling from filtered logits rows (pe_draft_sample) and rejection sampling
+// against filtered distributions (pe_verify_filtered).  Definitions and the
+// row's arithmetic: pe_filter.cuh.
+//
+// filter_kernel: a cluster of C CTAs per row, each with a slice of it in shared
+// memory.
+//  1. Every thread takes the maximum of its columns.
+//  2. List: with a top-k of at most kListK (or top-p alone: kProbe) the k-th
+//     largest of a CTA's thread maxima is a lower bound of the k-th largest
+//     column, so the columns above the largest of the CTAs' bounds are a
+//     superset of the first k, not much larger than k.  CTA 0 gathers them and
+//     finds rank and preceding weight of each by comparing all pairs.
+//  3. Where that does not do (a larger k, more weight than the list holds,
+//     ties), the cut's value is found bit by bit, from counts and weights of the
+//     columns above a trial value, and its last column from counts of equal ones.
+//  4. The draw: the CTAs' kept weights are exchanged, the CTA and then the warp in
+//     whose share the draw falls look for the column.
+// residual_kernel: a cluster per request finds the first rejection and draws
+// from max(0, p - q).
+#include "pe_filter.cuh"
+
+namespace pe {
+
+struct FilterParams {
+  const char* rows_a;  // target rows, or the only ones
+  const char* rows_b;  // draft rows
+  long long a_bytes, b_bytes;
+  int V, nvec, per_cta, seg, n, na, C;
+  int Kp;                     // verification: rows of a request - 1
+  int per;                    // sampling: rows that share parameters
+  int src_rows;
+  const int32_t* sample_idx;  // or NULL
+  AskedArrays asked;
+  const float* u;
+  // sampling
+  int32_t* out_tokens;
+  float* out_prob;
+  // verification
+  const int32_t* tokens;
+  const float* coins;
+  int32_t* accepted;
+  int32_t* bonus;
+  float* chance;
+  RowCut* cuts;  // [n]
+  Kept* kept;    // [na][kKeptCap]
+  uint32_t* err;
+};
+
+struct FilterShared {
+  uint64_t bars[kFW];
+  unsigned long long sums[2][kMaxCluster];  // exchanged by the CTAs, in turns
+  unsigned long long warp_sum[kFW];
+  uint32_t counts[2][kMaxCluster];
+  uint32_t warp_count[kFW];
+  uint32_t bounds[kMaxCluster];
+  uint32_t maxima[kMaxCluster];
+  unsigned long long total;
+  uint32_t listed, own, base, done;
+  int tie, token;
+  float2 table[32];
+  double px;
+};
+struct FilterLists {
+  unsigned long long key[kListCap];
+  unsigned long long w[kListCap];
+};
+
+__device__ __forceinline__ unsigned long long warp_sum_u64(unsigned long long v) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+__device__ __forceinline__ uint32_t key_of(unsigned long long k) { return (uint32_t)(k >> 32); }
+
+// A CTA's view of its row.
+template <int DT>
+struct Slice {
+  const uint4* v;    // the slice in shared memory
+  int n, lo, hi;     // vectors of the slice; of this warp's segment
+  int col0;          // column of the slice's first element
+  int lane, warp, rank, C;
+  FilterShared* sh;
+  int turn;          // exchanges so far
+
+  // Sum over the cluster of one count and one weight (given by every thread of the CTA
+  // as its warp's: lane 0's values count).
+  __device__ __forceinline__ void exchange(uint32_t& count, unsigned long long& sum,
+                                           unsigned long long* before = nullptr, uint32_t* count_before = nullptr) {
+    __syncthreads();  // the arrays' last readers
+    if (lane == 0) {
+      sh->warp_count[warp] = count;
+      sh->warp_sum[warp] = sum;
+    }
+    __syncthreads();
+    const int t = threadIdx.x;
+    const int slot = turn & 1;
+    if (t < C) {
+      uint32_t c = 0;
+      unsigned long long s = 0;
+      for (int w = 0; w < kFW; ++w) {
+        c += sh->warp_count[w];
+        s += sh->warp_sum[w];
+      }
+      *at_rank(&sh->counts[slot][rank], t) = c;
+      *at_rank(&sh->sums[slot][rank], t) = s;
+    }
+    cluster_sync();
+    ++turn;
+    count = 0;
+    sum = 0;
+    for (int r = 0; r < C; ++r) {
+      if (before && r == rank) {
+        *before = sum;
+        *count_before = count;
+      }
+      count += sh->counts[slot][r];
+      sum += sh->sums[slot][r];
+    }
+  }
+
+  // Columns with key >= t: how many, and (kMass) their weight.
+  template <bool kMass>
+  __device__ __forceinline__ void above(const Scale& sc, uint32_t t, uint32_t& count, unsigned long long& sum) {
+    uint32_t c = 0;
+    WeightSum<256> ws;
+    for (int i = lo + lane; i < hi; i += 32) {
+      const uint4 q = v[i];
+#pragma unroll
+      for (int e = 0; e < Elt<DT>::kN; ++e) {
+        const float x = Elt<DT>::get(q, e);
+        if (value_key(x) >= t) {
+          ++c;
+          if (kMass) {
+            const float2 w = weight(sc, sh->table, x);
+            ws.add(w.x, w.y);
+          }
+        }
+      }
+    }
+    count = __reduce_add_sync(0xffffffffu, c);
+    sum = kMass ? warp_sum_u64(ws.fixed(kSumBits)) : 0ull;
+    exchange(count, sum);
+  }
+
+  // The largest value whose columns from it on number at least k (kMass: weigh at least `target`).
+  template <bool kMass>
+  __device__ __forceinline__ uint32_t search(const Scale& sc, uint32_t k, double target) {
+    uint32_t t = 0;
+    for (int bit = 31; bit >= 32 - Elt<DT>::kKeyBits; --bit) {
+      const uint32_t trial = t | (1u << bit);
+      uint32_t c;
+      unsigned long long s;
+      above<kMass>(sc, trial, c, s);
+      if (kMass ? (double)s >= target : c >= k) t = trial;
+    }
+    if (Elt<DT>::kKeyBits == 16 && !(t >> 31)) t |= 0xffffu;  // (a negative bf16's low bits)
+    return t;
+  }
+
+  // Column of the r-th (from 1) of the columns of value `key`.
+  __device__ __forceinline__ int nth_tie(uint32_t key, uint32_t r) {
+    uint32_t c = 0;
+    for (int i = lo + lane; i < hi; i += 32) {
+      const uint4 q = v[i];
+#pragma unroll
+      for (int e = 0; e < Elt<DT>::kN; ++e) c += value_key(Elt<DT>::get(q, e)) == key;
+    }
+    c = __reduce_add_sync(0xffffffffu, c);
+    uint32_t all = c, before = 0;
+    unsigned long long none = 0, none_before;
+    exchange(all, none, &none_before, &before);
+    for (int w = 0; w < warp; ++w) before += sh->warp_count[w];
+    if (before < r && r <= before + c) {  // in this warp's segment
+      uint32_t at = before;
+      for (int i0 = lo; i0 < hi; i0 += 32) {
+        const int i = i0 + lane;
+        uint32_t mine = 0;
+        const uint4 q = v[min(i, hi - 1)];
+        if (i < hi) {
+#pragma unroll
+          for (int e = 0; e < Elt<DT>::kN; ++e) mine += value_key(Elt<DT>::get(q, e)) == key;
+        }
+        uint32_t pre = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const uint32_t x = __shfl_up_sync(0xffffffffu, pre, o);
+          if (lane >= o) pre += x;
+        }
+        if (at + pre - mine < r && r <= at + pre) {
+          uint32_t left = r - (at + pre - mine);
+#pragma unroll
+          for (int e = 0; e < Elt<DT>::kN; ++e)
+            if (value_key(Elt<DT>::get(q, e)) == key && --left == 0) {
+              const int col = col0 + i * Elt<DT>::kN + e;
+              for (int t = 0; t < C; ++t) *at_rank(&sh->tie, t) = col;
+            }
+        }
+        at += __shfl_sync(0xffffffffu, pre, 31);
+      }
+    }
+    cluster_sync();
+    return r > all ? INT32_MAX : sh->tie;
+  }
+};
+
+// The column (relative to the slice) in a warp's segment [lo, hi) of vectors where
+// the running sum passes `target`; get(i, from, to, sum) adds columns from..to-1 of vector
+// i to a sum.  Should roundings leave none, the last column that weighs anything.
+// All lanes return it.
+template <int kN, int kBias, class F>
+__device__ __forceinline__ int find_column(int lo, int hi, int lane, unsigned long long target, int bits, const F& get) {
+  unsigned long long at = 0;
+  int found = -1;
+  for (int i0 = lo; i0 < hi; i0 += 32) {
+    const int i = i0 + lane;
+    unsigned long long mine = 0;
+    if (i < hi) {
+      WeightSum<kBias> ws;
+      get(i, 0, kN, ws);
+      mine = ws.fixed(bits);
+    }
+    unsigned long long pre = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned long long x = __shfl_up_sync(0xffffffffu, pre, o);
+      if (lane >= o) pre += x;
+    }
+    const uint32_t hit = __ballot_sync(0xffffffffu, at + pre > target);
+    const uint32_t some = __ballot_sync(0xffffffffu, mine > 0);
+    const int src = hit ? __ffs(hit) - 1 : some ? 31 - __clz(some) : -1;
+    if (src >= 0) {
+      int col = -1;
+      if (lane == src) {
+        for (int e = 0; e < kN; ++e) {
+          WeightSum<kBias> one, upto;
+          get(i, e, e + 1, one);
+          if (one.fixed(bits) == 0) continue;
+          col = i * kN + e;
+          get(i, 0, e + 1, upto);
+          if (at + (pre - mine) + upto.fixed(bits) > target) break;
+        }
+      }
+      found = __shfl_sync(0xffffffffu, col, src);
+      if (hit) return found;
+    }
+    at += __shfl_sync(0xffffffffu, pre, 31);
+  }
+  return found;
+}
+
+// Largest key prefix (upper 16 bits) that at least k threads of the CTA reach.
+__device__ __forceinline__ uint32_t kth_prefix(uint32_t mine, int k) {
+  uint32_t t = 0;
+  for (int bit = 15; bit >= 0; --bit) {
+    const uint32_t trial = t | (1u << bit);
+    if (__syncthreads_count(mine >= trial) >= k) t = trial;
+  }
+  return t;
+}
+
+template <int DT, bool kVerify>
+__global__ void __launch_bounds__(kFT, 2) filter_kernel(const FilterParams p) {
+  extern __shared__ __align__(128) unsigned char smem[];
+  FilterShared& sh = *reinterpret_cast<FilterShared*>(smem);
+  FilterLists& ls = *reinterpret_cast<FilterLists*>(smem + ((sizeof(FilterShared) + 127) & ~(size_t)127));
+  uint4* data = reinterpret_cast<uint4*>(reinterpret_cast<unsigned char*>(&ls) + sizeof(FilterLists));
+  using E = Elt<DT>;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = (int)cluster_rank();
+  const int row = blockIdx.x / p.C;
+
+  // ---- which row, which parameters (the same in every CTA of the cluster)
+  const char* src;
+  int ask, draft = 0;
+  bool draws = true, ok = true;
+  if (kVerify) {
+    if (row < p.na) {
+      ask = row / (p.Kp + 1);
+      const int j = row - ask * (p.Kp + 1);
+      draws = j == p.Kp;
+      src = p.rows_a + (long long)row * p.a_bytes;
+      if (!draws) draft = __ldg(p.tokens + row + 1);
+    } else {
+      const int r = row - p.na;
+      ask = r / p.Kp;
+      draws = false;
+      src = p.rows_b + (long long)r * p.b_bytes;
+      draft = __ldg(p.tokens + ask * (p.Kp + 1) + (r - ask * p.Kp) + 1);
+    }
+  } else {
+    ask = row / p.per;
+    const int i = p.sample_idx ? __ldg(p.sample_idx + row) : row;
+    ok = i >= 0 && i < p.src_rows;
+    if (!ok && rank == 0 && tid == 0) atomicOr(p.err, PE_ERR_ROW_RANGE);
+    src = p.rows_a + (long long)(ok ? i : 0) * p.a_bytes;
+  }
+  Asked a;
+  if (!read_asked(p.asked, ask, p.V, a)) {
+    ok = false;
+    if (rank == 0 && tid == 0) atomicOr(p.err, PE_ERR_PARAM);
+  }
+  float u = 0.f;
+  if (draws) {
+    u = __ldg(p.u + (kVerify ? ask : row));
+    if (!(u >= 0.f && u < 1.f)) {
+      ok = false;
+      if (rank == 0 && tid == 0) atomicOr(p.err, PE_ERR_PARAM);
+    }
+  }
+  // what a row without an answer gets
+  auto none = [&](double W) {
+    if (rank != 0 || tid != 0) return;
+    if (kVerify) {
+      RowCut& c = p.cuts[row];
+      c.listed = 0;
+      c.token = -1;
+      c.W = W;
+      c.px = 0.0;
+    } else {
+      p.out_tokens[row] = -1;
+      if (p.out_prob) p.out_prob[row] = 0.f;
+    }
+  };
+  if (!ok) {
+    none(-1.0);
+    return;
+  }
+
+  // ---- load
+  Slice<DT> s;
+  s.v = data;
+  s.lane = lane;
+  s.warp = warp;
+  s.rank = rank;
+  s.C = p.C;
+  s.sh = &sh;
+  s.turn = 0;
+  const int v0 = rank * p.per_cta;
+  s.n = max(0, min(p.per_cta, p.nvec - v0));
+  s.lo = min(s.n, warp * p.seg);
+  s.hi = min(s.n, s.lo + p.seg);
+  s.col0 = v0 * E::kN;
+  if (lane == 0) {
+    mbar_init(&sh.bars[warp], 1);
+    mbar_init_fence();
+    const int whole = min(s.hi, p.V / E::kN - v0);  // vectors that lie in the row as a whole
+    const int bytes = max(0, whole - s.lo) * 16;
+    mbar_arrive_expect_tx(&sh.bars[warp], bytes);
+    if (bytes) bulk_load(data + s.lo, src + (long long)(v0 + s.lo) * 16, bytes, &sh.bars[warp]);
+  }
+  if (tid == 0) {
+    sh.listed = 0;
+    sh.own = 0;
+    sh.done = 0;
+  }
+  if (tid < 32) sh.table[tid] = kExp2Table[tid];
+  __syncwarp();
+  __syncthreads();
+  cluster_arrive();
+  // the row's last columns, where they do not fill a vector
+  const int part = p.V % E::kN;
+  if (part && s.hi > s.lo && v0 + s.hi == p.nvec && lane < E::kN) {
+    const int col = (p.nvec - 1) * E::kN + lane;
+    const float x = lane < part ? E::load(src, col) : -INFINITY;
+    if (DT == PE_BF16)
+      reinterpret_cast<unsigned short*>(data + s.hi - 1)[lane] = (unsigned short)(__float_as_uint(x) >> 16);
+    else
+      reinterpret_cast<float*>(data + s.hi - 1)[lane] = x;
+  }
+  if (!mbar_wait(&sh.bars[warp], 0)) {
+    if (lane == 0) atomicOr(p.err, PE_ERR_TIMEOUT);
+    (void)mbar_wait(&sh.bars[warp], 0);
+  }
+  __syncwarp();
+
+  // ---- maxima
+  float tmax = -INFINITY;
+  for (int i = s.lo + lane; i < s.hi; i += 32) tmax = fmaxf(tmax, E::max_of(s.v[i]));
+  const uint32_t mine = ordered_bits(tmax);
+  const uint32_t wmax = __reduce_max_sync(0xffffffffu, mine);
+  if (lane == 0) sh.warp_count[warp] = wmax;
+  const bool small_k = a.k <= kListK && a.k < p.V;
+  const bool nucleus = !small_k && a.k == p.V && a.p < 1.f;
+  uint32_t bound = 0;
+  if (small_k || nucleus) bound = kth_prefix(mine >> 16, small_k ? a.k : kProbe);
+  __syncthreads();
+  cluster_wait();  // every CTA has started
+  if (tid < p.C) {
+    uint32_t m = 0;
+    for (int w = 0; w < kFW; ++w) m = max(m, sh.warp_count[w]);
+    *at_rank(&sh.maxima[rank], tid) = m;
+    *at_rank(&sh.bounds[rank], tid) = bound;
+  }
+  cluster_sync();
+  uint32_t top = 0;
+  for (int r = 0; r < p.C; ++r) {
+    top = max(top, sh.maxima[r]);
+    bound = max(bound, sh.bounds[r]);
+  }
+  const float M = key_value(top);
+  if (M == -INFINITY) {
+    if (rank == 0 && tid == 0) atomicOr(p.err, PE_ERR_EMPTY_ROW);
+    none(0.0);
+    return;
+  }
+  const Scale sc = make_scale(M, a.T);
+  const float floor = min_p_floor(a, M);
+  const double p_mass = a.p > 0.f ? (double)a.p : 0.0;  // at most the whole: >= 1 is off
+
+  auto answer = [&](int token, double w, double W) {  // one thread
+    if (kVerify) {
+      p.cuts[row].token = token;
+    } else {
+      p.out_tokens[row] = token;
+      if (p.out_prob) p.out_prob[row] = (float)(w / W);
+    }
+  };
+
+  // ---- a list of the first columns
+  if (small_k || nucleus) {
+    if ((mine >> 16) >= bound) {
+      for (int i = s.lo + lane; i < s.hi; i += 32) {
+        const uint4 q = s.v[i];
+#pragma unroll
+        for (int e = 0; e < E::kN; ++e) {
+          const uint32_t k = value_key(E::get(q, e));
+          const int col = s.col0 + i * E::kN + e;
+          if ((k >> 16) >= bound && col < p.V) {
+            const uint32_t at = atomicAdd(rank == 0 ? &sh.listed : &sh.own, 1u);
+            if (at < kListCap) ls.key[at] = ((unsigned long long)k << 32) | (0xffffffffu - (uint32_t)col);
+          }
+        }
+      }
+    }
+    __syncthreads();
+    if (rank != 0) {
+      if (tid == 0) sh.base = atomicAdd(at_rank(&sh.listed, 0), sh.own);
+      __syncthreads();
+      for (int i = tid; i < (int)min(sh.own, (uint32_t)kListCap); i += kFT)
+        if (sh.base + i < kListCap) *at_rank(&ls.key[sh.base + i], 0) = ls.key[i];
+    }
+    double Z = 0.0;
+    if (nucleus) {  // the whole row's weight
+      uint32_t c;
+      unsigned long long sum;
+      s.template above<true>(sc, 0u, c, sum);
+      Z = (double)sum * (1.0 / (1ull << kSumBits));
+    } else {
+      cluster_sync();
+    }
+    if (rank == 0) {
+      const int L = (int)sh.listed;
+      bool done = L <= kListCap;
+      if (done) {
+        for (int i = tid; i < L; i += kFT) {
+          const float2 w = weight(sc, sh.table, key_value(key_of(ls.key[i])));
+          ls.w[i] = (unsigned long long)(((double)w.x + (double)w.y) * (double)(1ull << kListBits) + 0.5);
+        }
+        if (tid == 0) sh.total = 0;
+        __syncthreads();
+        // rank and preceding weight of up to two columns a thread
+        uint32_t rk[2] = {0, 0};
+        unsigned long long pre[2] = {0, 0};
+        unsigned long long sum = 0;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int i = tid + h * kFT;
+          if (i < L) {
+            const unsigned long long k = ls.key[i];
+            for (int j = 0; j < L; ++j)
+              if (ls.key[j] > k) {
+                ++rk[h];
+                pre[h] += ls.w[j];
+              }
+            if (small_k && rk[h] < (uint32_t)a.k) sum += ls.w[i];
+            if (nucleus) sum += ls.w[i];
+          }
+        }
+        sum = warp_sum_u64(sum);
+        if (lane == 0) atomicAdd(&sh.total, sum);
+        __syncthreads();
+        const double listed = (double)sh.total * (1.0 / (1ull << kListBits));
+        double target = p_mass * (small_k ? listed : Z);
+        if (a.p >= 1.f) target = 1e300;
+        if (nucleus && listed < target) done = false;
+        __syncthreads();
+        if (done) {
+          bool keep[2];
+          unsigned long long kw = 0, lk = ~0ull;  // kept weight; smallest kept key
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int i = tid + h * kFT;
+            keep[h] = i < L && (small_k ? rk[h] < (uint32_t)a.k : true) &&
+                      (rk[h] == 0 || (double)pre[h] * (1.0 / (1ull << kListBits)) < target) &&
+                      key_value(key_of(ls.key[i < L ? i : 0])) >= floor;
+            if (i < L && !keep[h]) ls.w[i] = 0;
+            if (keep[h]) {
+              kw += ls.w[i];
+              lk = min(lk, ls.key[i]);
+            }
+          }
+          if (tid == 0) sh.total = 0;
+          __syncthreads();
+          kw = warp_sum_u64(kw);
+          for (int o = 16; o; o >>= 1) lk = min(lk, __shfl_xor_sync(0xffffffffu, lk, o));
+          if (lane == 0) {
+            atomicAdd(&sh.total, kw);
+            sh.warp_sum[warp] = lk;
+          }
+          if (tid == 0) sh.own = 0;
+          if (tid == 0) sh.px = draft >= 0 && draft < p.V ? 0.0 : -1.0;
+          __syncthreads();
+          const unsigned long long W = sh.total;
+          if (draws) {
+            const unsigned long long at = (unsigned long long)((double)u * (double)W);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int i = tid + h * kFT;
+              if (i < L && keep[h] && ls.w[i]) {
+                const uint32_t inv = (uint32_t)ls.key[i];  // larger: lower column
+                unsigned long long upto = 0;
+                for (int j = 0; j < L; ++j)
+                  if ((uint32_t)ls.key[j] >= inv) upto += ls.w[j];
+                if (upto > at && upto - ls.w[i] <= at) answer((int)(0xffffffffu - inv), (double)ls.w[i], (double)W);
+              }
+            }
+          }
+          if (kVerify) {
+            const bool store = row < p.na;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int i = tid + h * kFT;
+              if (i < L && keep[h]) {
+                const int col = (int)(0xffffffffu - (uint32_t)ls.key[i]);
+                if (col == draft) sh.px = (double)ls.w[i] / (double)W;
+                if (store) {
+                  const uint32_t at = atomicAdd(&sh.own, 1u);
+                  if (at < kKeptCap) {
+                    Kept& k = p.kept[(long long)row * kKeptCap + at];
+                    k.w = ls.w[i];
+                    k.col = col;
+                  }
+                }
+              }
+            }
+            __syncthreads();
+            if (tid == 0) {
+              unsigned long long k = ~0ull;
+              for (int w = 0; w < kFW; ++w) k = min(k, sh.warp_sum[w]);
+              RowCut& c = p.cuts[row];
+              c.cut.key = key_of(k);
+              c.cut.tie = (int)(0xffffffffu - (uint32_t)k);
+              c.cut.floor = -INFINITY;
+              c.M = M;
+              c.T = a.T;
+              c.listed = store && sh.own <= kKeptCap ? (int)sh.own : -1;
+              c.W = (double)W * (1.0 / (1ull << kListBits));
+              c.px = sh.px;
+            }
+          }
+        }
+      }
+      __syncthreads();
+      if (tid < p.C) *at_rank(&sh.done, tid) = done;
+    }
+    cluster_sync();
+    if (sh.done) return;
+  }
+
+  // ---- the cut, over the whole row
+  Cut cut;
+  cut.key = 0;
+  cut.tie = INT32_MAX;
+  cut.floor = floor;
+  uint32_t ties = 0;  // of the cut's value, that are kept
+  if (a.k < p.V) {
+    cut.key = s.template search<false>(sc, (uint32_t)a.k, 0.0);
+    uint32_t c = 0;
+    unsigned long long sum;
+    if (cut.key != 0xffffffffu) s.template above<false>(sc, cut.key + 1, c, sum);
+    ties = (uint32_t)a.k - c;
+  }
+  if (a.p < 1.f) {
+    uint32_t c = 0;
+    unsigned long long sum = 0;
+    const uint32_t key_k = cut.key;
+    double Z;
+    if (a.k < p.V) {
+      s.template above<true>(sc, key_k + 1, c, sum);
+      const float2 w = weight(sc, sh.table, key_value(key_k));
+      Z = (double)sum + (double)ties * ((double)w.x + (double)w.y) * (double)(1ull << kSumBits);
+    } else {
+      s.template above<true>(sc, 0u, c, sum);
+      Z = (double)sum;
+    }
+    const double target = p_mass * Z;
+    uint32_t key_p = s.template search<true>(sc, 0u, target);
+    if (target <= 0.0) key_p = top;  // the first column alone
+    if (key_p < key_k) key_p = key_k;
+    s.template above<true>(sc, key_p + 1, c, sum);
+    const float2 w = weight(sc, sh.table, key_value(key_p));
+    const double one = ((double)w.x + (double)w.y) * (double)(1ull << kSumBits);
+    double need = ceil((target - (double)sum) / one);
+    if (!(need >= 1.0)) need = 1.0;
+    uint32_t r = need < 4e9 ? (uint32_t)need : 0xffffffffu;
+    if (a.k < p.V && key_p == key_k) r = min(r, ties);
+    cut.key = key_p;
+    ties = r;
+  }
+  if (a.k < p.V || a.p < 1.f) cut.tie = s.nth_tie(cut.key, ties);
+
+  // ---- the kept weight, and the draw
+  uint32_t c = 0;
+  unsigned long long sum, before = 0;
+  uint32_t c_before = 0;
+  auto kept = [&](int i, int from, int to, WeightSum<256>& ws) {
+    const uint4 q = s.v[i];
+#pragma unroll
+    for (int e = 0; e < E::kN; ++e) {
+      const float x = E::get(q, e);
+      if (e >= from && e < to && cut.keeps(x, s.col0 + i * E::kN + e)) {
+        const float2 w = weight(sc, sh.table, x);
+        ws.add(w.x, w.y);
+      }
+    }
+  };
+  WeightSum<256> ws;
+  for (int i = s.lo + lane; i < s.hi; i += 32) kept(i, 0, E::kN, ws);
+  const unsigned long long mine_w = warp_sum_u64(ws.fixed(kSumBits));
+  sum = mine_w;
+  s.exchange(c, sum, &before, &c_before);
+  if (kVerify && rank == 0 && tid == 0) {
+    RowCut& o = p.cuts[row];
+    o.cut = cut;
+    o.M = M;
+    o.T = a.T;
+    o.listed = -1;
+    o.W = (double)sum * (1.0 / (1ull << kSumBits));
+    double px = -1.0;
+    if (draft >= 0 && draft < p.V) {
+      const float x = E::load(src, draft);
+      px = 0.0;
+      if (cut.keeps(x, draft)) {
+        const float2 w = weight(sc, sh.table, x);
+        px = ((double)w.x + (double)w.y) / o.W;
+      }
+    }
+    o.px = px;
+  }
+  if (draws) {
+    unsigned long long at = (unsigned long long)((double)u * (double)sum);
+    at = min(at, sum - 1);
+    for (int w = 0; w < warp; ++w) before += sh.warp_sum[w];
+    if (before <= at && at < before + mine_w) {
+      const int i = find_column<E::kN, 256>(s.lo, s.hi, lane, at - before, kSumBits, kept);
+      if (lane == 0) {
+        const int col = s.col0 + i;
+        const float2 w = weight(sc, sh.table, E::load(src, col));
+        answer(col, ((double)w.x + (double)w.y) * (double)(1ull << kSumBits), (double)sum);
+      }
+    }
+  }
+}
+
+
+// --------------------------------------------------------- the bonus token
+template <int DT>
+__device__ __forceinline__ uint4 row_vector(const char* row, int i, int V) {
+  using E = Elt<DT>;
+  if ((i + 1) * E::kN <= V) return __ldg(reinterpret_cast<const uint4*>(row) + i);
+  uint32_t w[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (DT == PE_BF16) {
+      const int col = i * 8 + 2 * j;
+      const float lo = col < V ? E::load(row, col) : -INFINITY;
+      const float hi = col + 1 < V ? E::load(row, col + 1) : -INFINITY;
+      w[j] = (__float_as_uint(lo) >> 16) | (__float_as_uint(hi) & 0xffff0000u);
+    } else {
+      const int col = i * 4 + j;
+      w[j] = __float_as_uint(col < V ? E::load(row, col) : -INFINITY);
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Request b: the first rejected draft, then a draw from max(0, p - q) of its rows
+// (from p where that is zero everywhere), or the bonus row's own draw.  p's kept
+// columns come from the row's list where it has one: p - q is at most 0 elsewhere.
+// Else both rows are read again, each warp its segment.
+template <int DT>
+__global__ void __launch_bounds__(kFT) residual_kernel(const FilterParams p) {
+  extern __shared__ __align__(128) unsigned char smem[];
+  FilterShared& sh = *reinterpret_cast<FilterShared*>(smem);
+  using E = Elt<DT>;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = (int)cluster_rank();
+  const int b = blockIdx.x / p.C;
+  if (tid < 32) sh.table[tid] = kExp2Table[tid];
+  if (tid == 0) sh.total = 0;
+  __syncthreads();
+  cluster_arrive();
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const RowCut* target = p.cuts + (long long)b * (p.Kp + 1);
+  const RowCut* drafts = p.cuts + p.na + (long long)b * p.Kp;
+  const bool bad = target[p.Kp].W < 0.0;
+  int a = p.Kp;
+  for (int j0 = 0; j0 < p.Kp; j0 += 32) {
+    const int j = j0 + lane;
+    bool no = false;
+    if (j < p.Kp) {
+      const double px = target[j].px, qx = drafts[j].px;
+      no = !((double)__ldg(p.coins + b * p.Kp + j) * qx < px);
+      if (p.chance && rank == 0 && warp == 0)
+        p.chance[b * p.Kp + j] = bad || !(px > 0.0) ? 0.f : px < qx ? (float)(px / qx) : 1.f;
+    }
+    const uint32_t m = __ballot_sync(0xffffffffu, no);
+    if (m && a == p.Kp) a = j0 + __ffs(m) - 1;
+  }
+  const RowCut& t = target[a];
+  const bool stream = !bad && a < p.Kp && t.W > 0.0 && t.listed < 0;
+  if (rank == 0 && tid == 0) {
+    p.accepted[b] = bad ? 0 : a;
+    if (bad || t.W == 0.0) p.bonus[b] = -1;
+    else if (a == p.Kp) p.bonus[b] = t.token;
+  }
+  cluster_wait();
+  if (bad || a == p.Kp || t.W == 0.0) return;
+  const RowCut& d = drafts[a];
+  const char* trow = p.rows_a + ((long long)b * (p.Kp + 1) + a) * p.a_bytes;
+  const char* drow = p.rows_b + ((long long)b * p.Kp + a) * p.b_bytes;
+  const float u = __ldg(p.u + b);
+  const Scale st = make_scale(t.M, t.T);
+  const Scale sd = make_scale(d.W > 0.0 ? d.M : 0.f, t.T);
+  const Cut ct = t.cut, cd = d.cut;
+  const bool has_q = d.W > 0.0;
+  const double it = 1.0 / t.W, id = has_q ? 1.0 / d.W : 0.0;
+  constexpr int kBits = 60;
+
+  if (!stream) {
+    if (rank != 0) return;
+    unsigned long long* w = reinterpret_cast<unsigned long long*>(smem + ((sizeof(FilterShared) + 127) & ~(size_t)127));
+    int* cols = reinterpret_cast<int*>(w + kKeptCap);
+    const Kept* kept = p.kept + ((long long)b * (p.Kp + 1) + a) * kKeptCap;
+    const int L = min(t.listed, kKeptCap);
+    unsigned long long mine = 0, whole = 0;
+    int col = -1;
+    if (tid < L) {
+      col = kept[tid].col;
+      const double pr = (double)kept[tid].w * (1.0 / (1ull << kListBits)) * it;
+      double q = 0.0;
+      if (has_q) {
+        const float x = E::load(drow, col);
+        if (cd.keeps(x, col)) {
+          const float2 f = weight(sd, sh.table, x);
+          q = ((double)f.x + (double)f.y) * id;
+        }
+      }
+      whole = (unsigned long long)(pr * (double)(1ull << kBits) + 0.5);
+      mine = pr > q ? (unsigned long long)((pr - q) * (double)(1ull << kBits) + 0.5) : 0ull;
+    }
+    const unsigned long long part = warp_sum_u64(mine);
+    if (lane == 0 && part) atomicAdd(&sh.total, part);
+    __syncthreads();
+    unsigned long long R = sh.total;
+    __syncthreads();
+    if (R == 0) {
+      mine = whole;
+      const unsigned long long all = warp_sum_u64(mine);
+      if (lane == 0 && all) atomicAdd(&sh.total, all);
+      __syncthreads();
+      R = sh.total;
+    }
+    if (tid < kKeptCap) {
+      w[tid] = mine;
+      cols[tid] = tid < L ? col : INT32_MAX;
+    }
+    __syncthreads();
+    const unsigned long long at = min((unsigned long long)((double)u * (double)R), R - 1);
+    if (mine) {
+      unsigned long long upto = 0;
+      for (int j = 0; j < L; ++j)
+        if (cols[j] <= col) upto += w[j];
+      if (upto > at && upto - mine <= at) p.bonus[b] = col;
+    }
+    return;
+  }
+
+  Slice<DT> s;
+  s.lane = lane;
+  s.warp = warp;
+  s.rank = rank;
+  s.C = p.C;
+  s.sh = &sh;
+  s.turn = 0;
+  const int v0 = rank * p.per_cta, vn = max(0, min(p.per_cta, p.nvec - v0));
+  s.lo = v0 + min(vn, warp * p.seg);
+  s.hi = v0 + min(vn, warp * p.seg + p.seg);
+  const float ith = (float)it, itl = (float)(it - (double)ith);
+  const float idh = (float)id, idl = (float)(id - (double)idh);
+  bool from_p = false;
+  auto rest = [&](int i, int from, int to, WeightSum<2>& ws) {
+    const uint4 x = row_vector<DT>(trow, i, p.V);
+    const uint4 y = row_vector<DT>(drow, i, p.V);
+#pragma unroll
+    for (int e = 0; e < E::kN; ++e) {
+      const float xe = E::get(x, e), ye = E::get(y, e);
+      const int col = i * E::kN + e;
+      if (e >= from && e < to && ct.keeps(xe, col)) {
+        float2 w = weight(st, sh.table, xe);
+        float ph = w.x * ith;
+        float pl = fmaf(w.x, ith, -ph) + fmaf(w.x, itl, w.y * ith);
+        if (!from_p && has_q && cd.keeps(ye, col)) {
+          w = weight(sd, sh.table, ye);
+          const float qh = w.x * idh;
+          const float ql = fmaf(w.x, idh, -qh) + fmaf(w.x, idl, w.y * idh);
+          const float dh = ph - qh, bb = dh - ph;
+          pl = ((ph - (dh - bb)) - (qh + bb)) + (pl - ql);
+          ph = dh;
+        }
+        if (ph + pl > 0.f) ws.add(ph, pl);
+      }
+    }
+  };
+  unsigned long long sum = 0, before = 0, mine = 0;
+  for (int turn = 0; turn < 2; ++turn) {
+    WeightSum<2> ws;
+    for (int i = s.lo + lane; i < s.hi; i += 32) rest(i, 0, E::kN, ws);
+    mine = warp_sum_u64(ws.fixed(kBits));
+    sum = mine;
+    uint32_t c = 0, c_before = 0;
+    s.exchange(c, sum, &before, &c_before);
+    if (sum != 0) break;
+    from_p = true;
+  }
+  if (sum == 0) return;  // (p's weights are not all zero)
+  const unsigned long long at = min((unsigned long long)((double)u * (double)sum), sum - 1);
+  for (int w = 0; w < warp; ++w) before += sh.warp_sum[w];
+  if (before <= at && at < before + mine) {
+    const int col = find_column<E::kN, 2>(s.lo, s.hi, lane, at - before, kBits, rest);
+    if (lane == 0) p.bonus[b] = col;
+  }
+}
+
+}  // namespace pe
+
+// ---------------------------------------------------------------- host side
+namespace {
+
+constexpr size_t kHeader = ((sizeof(pe::FilterShared) + 127) & ~(size_t)127);
+constexpr int kMaxSmem = 200 * 1024;
+constexpr int kRoomySlice = 80 * 1024;  // two CTAs per SM
+
+struct FilteredLayout {
+  size_t kept_off, bytes;
+  FilteredLayout(long long B, long long Kp) {
+    const long long rows = B * (2 * Kp + 1);
+    kept_off = (sizeof(pe::RowCut) * rows + 255) / 256 * 256;
+    bytes = kept_off + sizeof(pe::Kept) * pe::kKeptCap * B * (Kp + 1);
+  }
+};
+
+// CTAs of a row: as few as leave room for two CTAs on an SM, more while the rows
+// do not fill the GPU.
+void split_rows(pe::FilterParams& p, int elt, int sms) {
+  const int epv = 16 / elt;
+  p.nvec = (p.V + epv - 1) / epv;
+  p.C = 1;
+  while (p.C < pe::kMaxCluster &&
+         (p.nvec * 16 / p.C > kRoomySlice || ((long long)p.n * p.C * 2 <= sms && p.nvec / p.C > 512)))
+    p.C *= 2;
+  p.per_cta = (p.nvec + p.C - 1) / p.C;
+  p.seg = (p.per_cta + pe::kFW - 1) / pe::kFW;
+}
+
+template <class K>
+cudaError_t launch(K kernel, int grid, int C, size_t smem, bool dependent, cudaStream_t st, const pe::FilterParams& p) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = C;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(pe::kFT);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = dependent ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+template <int DT, bool kVerify>
+int launch_filter(const pe::FilterParams& p, cudaStream_t st) {
+  static std::atomic<unsigned long long> done{0};
+  if (!pe_host::allow_smem(pe::filter_kernel<DT, kVerify>, kMaxSmem, done)) return PE_ECUDA;
+  const size_t smem = kHeader + sizeof(pe::FilterLists) + (size_t)p.per_cta * 16;
+  return launch(pe::filter_kernel<DT, kVerify>, p.n * p.C, p.C, smem, false, st, p) == cudaSuccess ? PE_OK : PE_ECUDA;
+}
+
+template <int DT>
+int launch_verify(pe::FilterParams p, int B, int elt, int sms, cudaStream_t st) {
+  const int rc = launch_filter<DT, true>(p, st);
+  if (rc != PE_OK) return rc;
+  p.n = B;
+  split_rows(p, elt, sms);
+  const size_t smem = kHeader + 12 * pe::kKeptCap;
+  return launch(pe::residual_kernel<DT>, B * p.C, p.C, smem, true, st, p) == cudaSuccess ? PE_OK : PE_ECUDA;
+}
+
+int rows_ok(const void* rows, int64_t stride, int elt, int V) {
+  if (stride < V || stride > (INT64_MAX >> 8)) return PE_EINVAL;
+  return pe_host::aligned16(rows) && (stride * elt) % 16 == 0 ? PE_OK : PE_EALIGN;
+}
+
+}  // namespace
+
+extern "C" {
+
+int pe_draft_sample(const pe_draft_sample_args* a, void* stream) {
+  if (!a) return PE_EINVAL;
+  const int elt = pe_host::elt_size(a->dtype);
+  if (!elt) return PE_EDTYPE;
+  if (a->n < 0 || a->n > PE_MAX_SAMPLE_ROWS || a->V < 1 || a->V > PE_MAX_SAMPLE_V || a->rows < 0) return PE_EINVAL;
+  if (a->n == 0) return PE_OK;
+  if (a->requests < 1 || a->n % a->requests || (!a->sample_idx && a->n > a->rows)) return PE_EINVAL;
+  if (!a->logits || !a->u || !a->out_tokens || !a->err) return PE_EINVAL;
+  int rc = rows_ok(a->logits, a->row_stride, elt, a->V);
+  if (rc != PE_OK) return rc;
+  pe_host::DeviceInfo dev;
+  if (pe_host::device_info(&dev) != PE_OK) return PE_ECUDA;
+  pe::FilterParams p = {};
+  p.rows_a = static_cast<const char*>(a->logits);
+  p.a_bytes = a->row_stride * elt;
+  p.V = a->V;
+  p.n = a->n;
+  p.per = a->n / a->requests;
+  p.src_rows = a->rows;
+  p.sample_idx = a->sample_idx;
+  p.asked = {a->filter.temperature, a->filter.top_k, a->filter.top_p, a->filter.min_p};
+  p.u = a->u;
+  p.out_tokens = a->out_tokens;
+  p.out_prob = a->out_prob;
+  p.err = a->err;
+  split_rows(p, elt, dev.sm_count);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  rc = a->dtype == PE_BF16 ? launch_filter<PE_BF16, false>(p, st) : launch_filter<PE_F32, false>(p, st);
+  return rc == PE_OK ? pe_host::launch_status() : rc;
+}
+
+size_t pe_workspace_bytes_filtered(int32_t B, int32_t Kp) {
+  if (B < 0 || Kp < 0 || Kp > PE_MAX_KP) return 0;
+  return FilteredLayout(B, Kp).bytes;
+}
+
+int pe_verify_filtered(const pe_verify_filtered_args* a, void* stream) {
+  if (!a) return PE_EINVAL;
+  const int elt = pe_host::elt_size(a->dtype);
+  if (!elt) return PE_EDTYPE;
+  if (a->B < 0 || a->Kp < 0 || a->Kp > PE_MAX_KP || a->V < 1 || a->V > PE_MAX_SAMPLE_V) return PE_EINVAL;
+  if (a->B == 0) return PE_OK;
+  const long long rows = (long long)a->B * (2 * a->Kp + 1);
+  if (rows > PE_MAX_SAMPLE_ROWS) return PE_EINVAL;
+  if (!a->target_logits || !a->u_draw || !a->accepted_len || !a->bonus_token || !a->workspace || !a->err) return PE_EINVAL;
+  if (a->Kp > 0 && (!a->draft_logits || !a->in_tokens || !a->u_accept)) return PE_EINVAL;
+  int rc = rows_ok(a->target_logits, a->target_stride, elt, a->V);
+  if (rc == PE_OK && a->Kp > 0) rc = rows_ok(a->draft_logits, a->draft_stride, elt, a->V);
+  if (rc != PE_OK) return rc;
+  if (!pe_host::aligned16(a->workspace)) return PE_EALIGN;
+  pe_host::DeviceInfo dev;
+  if (pe_host::device_info(&dev) != PE_OK) return PE_ECUDA;
+  pe::FilterParams p = {};
+  p.rows_a = static_cast<const char*>(a->target_logits);
+  p.rows_b = static_cast<const char*>(a->draft_logits);
+  p.a_bytes = a->target_stride * elt;
+  p.b_bytes = a->draft_stride * elt;
+  p.V = a->V;
+  p.n = (int)rows;
+  p.na = a->B * (a->Kp + 1);
+  p.Kp = a->Kp;
+  p.asked = {a->filter.temperature, a->filter.top_k, a->filter.top_p, a->filter.min_p};
+  p.u = a->u_draw;
+  p.tokens = a->in_tokens;
+  p.coins = a->u_accept;
+  p.accepted = a->accepted_len;
+  p.bonus = a->bonus_token;
+  p.chance = a->accept_prob;
+  p.cuts = static_cast<pe::RowCut*>(a->workspace);
+  p.kept = reinterpret_cast<pe::Kept*>(static_cast<char*>(a->workspace) + FilteredLayout(a->B, a->Kp).kept_off);
+  p.err = a->err;
+  split_rows(p, elt, dev.sm_count);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  rc = a->dtype == PE_BF16 ? launch_verify<PE_BF16>(p, a->B, elt, dev.sm_count, st)
+                           : launch_verify<PE_F32>(p, a->B, elt, dev.sm_count, st);
+  return rc == PE_OK ? pe_host::launch_status() : rc;
+}
+
+}  // extern "C"
