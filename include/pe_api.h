@@ -627,6 +627,83 @@ typedef struct pe_attn_prompt_args {
 } pe_attn_prompt_args;
 int pe_attn_prompt(const pe_attn_prompt_args* args /* host */, void* stream);
 
+/* ------------------------------------------------------------------------
+ * A bounded cache.  The drafter's cache grows with the context; these two calls
+ * keep, per request and key head, the keys that attention uses.  Weights lie as the
+ * keys do: mass [num_blocks, Hkv, block_size] fp32, the weight of key j of a
+ * request at its slot.  After an eviction key i of a request is no longer
+ * position i: rows appended later go to slot out_length + i (positions for
+ * kv_append's rotation stay the true ones, positions for pe_attn_cached and
+ * pe_kv_weigh count cached keys). */
+
+/* Bytes of scratch that pe_kv_weigh needs for T rows of Hq heads over a table of
+ * bt_width pages (0 for sizes out of range).  Its content does not matter
+ * before a call and is not kept; calls that may run concurrently need separate
+ * workspaces. */
+size_t pe_workspace_bytes_weigh(int32_t T, int32_t Hq, int32_t bt_width, int32_t block_size);
+
+/* Add the attention weight of a step's rows to every key that they see:
+ *   out[slot(j), g] = old + sum over the request's rows t with j < limit and the
+ *                     heads h of key head g of softmax_j(scale * q[t,h] . K[j,g])
+ * for the keys j below the largest limit of the request's rows; other slots are left as
+ * they are.  Rows, limits, pages, queries and their rounding to f16 as in
+ * pe_attn_cached (the keys' values are exact, sums and exponents fp32).
+ *   old = mass[slot(j), g] for j < fresh[b], else 0 (keys that were appended
+ *   since the last call: their slot's weight is of another key); fresh NULL: for
+ *   every j; mass NULL: 0.
+ *  out may be mass.  No two requests may share a page.  A query that is not
+ *  finite makes the weights of its request and key head NaN.
+ *  err: PE_ERR_OFFSETS (offsets no partition of T: nothing is written);
+ *  PE_ERR_BLOCK_RANGE as in pe_attn_cached.
+ * B Hkv at most 65535.  Three launches; T == 0 enqueues nothing. */
+typedef struct pe_kv_weigh_args {
+  int32_t T, B, Hq, Hkv, D, block_size, bt_width;
+  float scale;
+  int64_t num_blocks;
+  const void* q;              /* [T,Hq,D] bf16, dense */
+  const void* cache;
+  const int32_t* block_table; /* [B, bt_width] */
+  const int32_t* offsets;     /* [B+1] or NULL: T/B rows each */
+  const int32_t* positions;   /* [T] */
+  const uint8_t* is_rejected; /* [T] or NULL */
+  const float* mass;          /* or NULL */
+  float* out;
+  const int32_t* fresh;       /* [B] or NULL */
+  void* workspace;
+  uint32_t* err;
+} pe_kv_weigh_args;
+int pe_kv_weigh(const pe_kv_weigh_args* args /* host */, void* stream);
+
+/* Keep the heaviest keys.  Request b has n = lengths[b] keys in its pages; per key
+ * head, size = min(n, keep[b]) of them stay: the first min(sinks, size), of the rest
+ * the last `recent` (as many as size leaves), and of the others the heaviest (of
+ * equal weights the first; a NaN is lighter than any number).
+ *   kept[b,g,0..size-1]  their indices, ascending; entries from size on are left
+ *   out_lengths[b]       size
+ *   key dst_table[b], i  key kept[b,g,i]: codes, scales and weight, bit for bit, for
+ *                        every g; the pages' other slots are left
+ * dst_table[b] may be block_table[b] (in place), or name pages that no request
+ * reads or writes here; a page at the same place of both counts as in place.  No
+ * two requests may share pages.
+ *  A request whose length or keep is negative or does not fit its table (size:
+ *  dst_table or max_keep) is left as it is with out_lengths -1 and PE_ERR_PARAM;
+ *  one with a page outside the cache likewise, with PE_ERR_BLOCK_RANGE.
+ * B Hkv at most 2^24.  One launch, no workspace; B == 0 enqueues nothing. */
+typedef struct pe_kv_evict_args {
+  int32_t B, Hkv, D, block_size, bt_width, dst_width, max_keep, sinks, recent;
+  int64_t num_blocks;
+  void* cache;
+  float* mass;
+  const int32_t* block_table; /* [B, bt_width] */
+  const int32_t* dst_table;   /* [B, dst_width] */
+  const int32_t* lengths;     /* [B] */
+  const int32_t* keep;        /* [B] */
+  int32_t* kept;              /* [B, Hkv, max_keep] */
+  int32_t* out_lengths;       /* [B] */
+  uint32_t* err;
+} pe_kv_evict_args;
+int pe_kv_evict(const pe_kv_evict_args* args /* host */, void* stream);
+
 /* Human-readable name of a pe_status value. */
 const char* pe_status_str(int status);
 

@@ -8,7 +8,8 @@ assembly run in hand-written CUDA kernels for sm_103a behind the C ABI of
 """
 from ._native import (DraftBatch, PEError, StepArgs, StepOutputs,  # noqa: F401
                       assemble_draft_inputs, attn_cached, attn_prompt, build_draft_batch,
-                      draft_readout, draft_sample, get_tuning, kv_append, kv_read, load, make_step_args,
-                      new_attn_workspace, new_error_word, new_filtered_workspace, new_kv_cache,
-                      new_workspace, rope_table, set_tuning, step, step_packed, verify_filtered,
-                      verify_greedy, workspace_bytes, workspace_bytes_attn, workspace_bytes_filtered)
+                      draft_readout, draft_sample, get_tuning, kv_append, kv_evict, kv_read, kv_weigh,
+                      load, make_step_args, new_attn_workspace, new_error_word, new_filtered_workspace,
+                      new_kv_cache, new_kv_mass, new_weigh_workspace, new_workspace, rope_table,
+                      set_tuning, step, step_packed, verify_filtered, verify_greedy, workspace_bytes,
+                      workspace_bytes_attn, workspace_bytes_filtered, workspace_bytes_weigh)

@@ -8,6 +8,7 @@ rejected, an exception is raised.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -46,7 +47,7 @@ EXPORTS = ("pe_workspace_bytes", "pe_verify_greedy", "pe_draft_readout",
            "pe_set_tuning", "pe_latency_floor", "pe_status_str",
            "pe_kv_append", "pe_kv_read", "pe_workspace_bytes_attn", "pe_attn_cached",
            "pe_attn_prompt", "pe_draft_sample", "pe_workspace_bytes_filtered",
-           "pe_verify_filtered")
+           "pe_verify_filtered", "pe_workspace_bytes_weigh", "pe_kv_weigh", "pe_kv_evict")
 
 
 class PEError(RuntimeError):
@@ -123,6 +124,22 @@ class VerifyFilteredArgs(ctypes.Structure):
                                   "bonus_token", "accept_prob", "workspace", "err")])
 
 
+class KvWeighArgs(ctypes.Structure):
+    """Mirror of pe_kv_weigh_args."""
+    _fields_ = ([(n, i32) for n in ("T", "B", "Hq", "Hkv", "D", "block_size", "bt_width")] +
+                [("scale", ctypes.c_float), ("num_blocks", i64)] +
+                [(n, P) for n in ("q", "cache", "block_table", "offsets", "positions",
+                                  "is_rejected", "mass", "out", "fresh", "workspace", "err")])
+
+
+class KvEvictArgs(ctypes.Structure):
+    """Mirror of pe_kv_evict_args."""
+    _fields_ = ([(n, i32) for n in ("B", "Hkv", "D", "block_size", "bt_width", "dst_width", "max_keep",
+                                    "sinks", "recent")] + [("num_blocks", i64)] +
+                [(n, P) for n in ("cache", "mass", "block_table", "dst_table", "lengths", "keep", "kept",
+                                  "out_lengths", "err")])
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -191,8 +208,12 @@ def _open(path: str):
     lib.pe_workspace_bytes_filtered.argtypes = [i32, i32]
     lib.pe_workspace_bytes_filtered.restype = ctypes.c_size_t
     lib.pe_verify_filtered.argtypes = [ctypes.POINTER(VerifyFilteredArgs), P]
+    lib.pe_workspace_bytes_weigh.argtypes = [i32, i32, i32, i32]
+    lib.pe_workspace_bytes_weigh.restype = ctypes.c_size_t
+    lib.pe_kv_weigh.argtypes = [ctypes.POINTER(KvWeighArgs), P]
+    lib.pe_kv_evict.argtypes = [ctypes.POINTER(KvEvictArgs), P]
     for f in ("pe_kv_append", "pe_kv_read", "pe_attn_cached", "pe_attn_prompt", "pe_draft_sample",
-              "pe_verify_filtered"):
+              "pe_verify_filtered", "pe_kv_weigh", "pe_kv_evict"):
         getattr(lib, f).restype = ctypes.c_int
     lib.pe_status_str.argtypes = [ctypes.c_int]
     lib.pe_status_str.restype = ctypes.c_char_p
@@ -497,6 +518,18 @@ def _raw_stream(stream, t: torch.Tensor) -> int:
     return torch._C._cuda_getCurrentRawStream(t.device.index)
 
 
+_here = contextlib.nullcontext()
+
+
+def _on(t: torch.Tensor, *others):
+    """The device that all the tensors lie on, as the current one during the call."""
+    dev = t.device
+    for x in others:
+        if x is not None and x.device != dev:
+            raise ValueError("all tensors must be on one device, got %s and %s" % (dev, x.device))
+    return _here if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+
+
 def _rows(t: torch.Tensor, name: str, shape):
     """Pointer and strides of bf16 rows [T, heads, D] with dense elements."""
     if t.shape != shape:
@@ -670,6 +703,76 @@ def attn_prompt(q, k, v, offsets, out, workspace, err, scale=None, B=None, strea
     _check(lib, lib.pe_attn_prompt(ctypes.byref(a), _raw_stream(stream, q)), "pe_attn_prompt")
 
 
+# ------------------------------------------------------------- a bounded cache
+
+def new_kv_mass(cache: torch.Tensor) -> torch.Tensor:
+    """Zeroed attention weights [num_blocks, Hkv, block_size] of a cache's keys."""
+    blocks, Hkv, sub, _ = cache.shape
+    return torch.zeros(blocks, Hkv, 16 * sub, dtype=torch.float32, device=cache.device)
+
+
+def workspace_bytes_weigh(T: int, Hq: int, bt_width: int, block_size: int) -> int:
+    return int(load().pe_workspace_bytes_weigh(T, Hq, bt_width, block_size))
+
+
+def new_weigh_workspace(T: int, Hq: int, bt_width: int, block_size: int, device="cuda") -> torch.Tensor:
+    """Scratch for kv_weigh of up to T rows of Hq heads over tables of bt_width pages (reusable)."""
+    return torch.empty(workspace_bytes_weigh(T, Hq, bt_width, block_size), dtype=torch.uint8, device=device)
+
+
+def kv_weigh(q, cache, block_table, offsets, positions, is_rejected, mass, out, workspace, err,
+             fresh=None, scale=None, stream=None):
+    """Add the attention weight that the packed rows give to every cached key they
+    see to ``mass`` (new_kv_mass; None: nothing yet), into ``out`` (it may be
+    mass); keys from fresh[b] on start from nothing.  Rows as in attn_cached."""
+    lib = _lib or load()
+    cp, blocks, bs, Hkv, D = _cache(cache)
+    T, Hq, _ = _heads(q, "q")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B, width]")
+    B, width = block_table.shape
+    n = blocks * Hkv * bs
+    if not workspace.is_cuda or workspace.dtype is not torch.uint8 or not workspace.is_contiguous() or \
+            workspace.numel() < lib.pe_workspace_bytes_weigh(T, Hq, width, bs):
+        raise ValueError("workspace must be what new_weigh_workspace(%d, %d, %d, %d) gives" % (T, Hq, width, bs))
+    a = KvWeighArgs(T, B, Hq, Hkv, D, bs, width, D ** -0.5 if scale is None else scale, blocks,
+                    _dense(q, "q", (T, Hq, D)), cp,
+                    _vector(block_table, "block_table", torch.int32, B * width),
+                    _vector(offsets, "offsets", torch.int32, B + 1),
+                    _vector(positions, "positions", torch.int32, T),
+                    _vector(is_rejected, "is_rejected", torch.uint8, T),
+                    _vector(mass, "mass", torch.float32, n), _vector(out, "out", torch.float32, n),
+                    _vector(fresh, "fresh", torch.int32, B), workspace.data_ptr(),
+                    _vector(err, "err", torch.int32, 1))
+    with _on(q, cache, block_table, offsets, positions, is_rejected, mass, out, workspace, fresh, err):
+        _check(lib, lib.pe_kv_weigh(ctypes.byref(a), _raw_stream(stream, q)), "pe_kv_weigh")
+
+
+def kv_evict(cache, mass, block_table, dst_table, lengths, keep, kept, out_lengths, err, sinks=0, recent=0,
+             stream=None):
+    """Per request and key head, keep the first ``sinks``, the last ``recent`` and
+    the heaviest of the others of the lengths[b] cached keys, keep[b] in all: in
+    ascending order at the front of dst_table's pages (block_table itself: in
+    place), their weights too, their indices in kept [B, Hkv, max_keep], how many
+    in out_lengths."""
+    lib = _lib or load()
+    cp, blocks, bs, Hkv, D = _cache(cache)
+    if block_table.dim() != 2 or dst_table.dim() != 2 or dst_table.shape[0] != block_table.shape[0]:
+        raise ValueError("block_table must be [B, width], dst_table [B, dst_width]")
+    B, width = block_table.shape
+    if kept.dim() != 3 or kept.shape[:2] != (B, Hkv):
+        raise ValueError("kept must be [B, Hkv, max_keep]")
+    a = KvEvictArgs(B, Hkv, D, bs, width, dst_table.shape[1], kept.shape[2], sinks, recent, blocks, cp,
+                    _vector(mass, "mass", torch.float32, blocks * Hkv * bs),
+                    _vector(block_table, "block_table", torch.int32, B * width),
+                    _vector(dst_table, "dst_table", torch.int32, dst_table.numel()),
+                    _vector(lengths, "lengths", torch.int32, B), _vector(keep, "keep", torch.int32, B),
+                    _vector(kept, "kept", torch.int32, kept.numel()),
+                    _vector(out_lengths, "out_lengths", torch.int32, B), _vector(err, "err", torch.int32, 1))
+    with _on(cache, mass, block_table, dst_table, lengths, keep, kept, out_lengths, err):
+        _check(lib, lib.pe_kv_evict(ctypes.byref(a), _raw_stream(stream, cache)), "pe_kv_evict")
+
+
 # ------------------------------------------------------------ filtered sampling
 
 def _columns(t: torch.Tensor, name: str):
@@ -705,7 +808,8 @@ def draft_sample(logits, u, out_tokens, err, temperature=None, top_k=None, top_p
                         *_filter(temperature, top_k, top_p, min_p, requests),
                         _vector(u, "u", torch.float32, n), _vector(out_tokens, "out_tokens", torch.int32, n),
                         _vector(out_prob, "out_prob", torch.float32, n), _vector(err, "err", torch.int32, 1))
-    _check(lib, lib.pe_draft_sample(ctypes.byref(a), _raw_stream(stream, logits)), "pe_draft_sample")
+    with _on(logits, u, out_tokens, err, temperature, top_k, top_p, min_p, out_prob, sample_idx):
+        _check(lib, lib.pe_draft_sample(ctypes.byref(a), _raw_stream(stream, logits)), "pe_draft_sample")
 
 
 def workspace_bytes_filtered(B: int, Kp: int) -> int:
@@ -749,7 +853,9 @@ def verify_filtered(target_logits, draft_logits, Kp, in_tokens, u_accept, u_draw
                            _vector(bonus_token, "bonus_token", torch.int32, B),
                            _vector(accept_prob, "accept_prob", torch.float32, B * Kp),
                            workspace.data_ptr(), _vector(err, "err", torch.int32, 1))
-    _check(lib, lib.pe_verify_filtered(ctypes.byref(a), _raw_stream(stream, target_logits)), "pe_verify_filtered")
+    with _on(target_logits, draft_logits if Kp else None, in_tokens if Kp else None, u_accept if Kp else None, u_draw,
+             accepted_len, bonus_token, workspace, err, temperature, top_k, top_p, min_p, accept_prob):
+        _check(lib, lib.pe_verify_filtered(ctypes.byref(a), _raw_stream(stream, target_logits)), "pe_verify_filtered")
 
 
 def get_tuning() -> dict:

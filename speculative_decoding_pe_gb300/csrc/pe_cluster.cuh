@@ -1,0 +1,58 @@
+// Thread-block clusters: rank, barrier, addresses in another CTA's shared memory.
+#pragma once
+
+#include <stdint.h>
+
+namespace pe {
+
+constexpr int kMaxCluster = 8;
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_sync() {
+  cluster_arrive();
+  cluster_wait();
+}
+// The same variable in the shared memory of the cluster's CTA `rank`.
+template <class T>
+__device__ __forceinline__ T* at_rank(T* p, uint32_t rank) {
+  T* q;
+  asm("mapa.u64 %0, %1, %2;" : "=l"(q) : "l"(p), "r"(rank));
+  return q;
+}
+
+}  // namespace pe
+
+namespace pe_host {
+
+// A launch in clusters of C CTAs; `dependent`: the kernel may start before the one
+// ahead of it on the stream has finished, and waits for it (griddepcontrol.wait).
+template <class K, class P>
+cudaError_t launch_clusters(K kernel, unsigned grid, int threads, int C, size_t smem, bool dependent, cudaStream_t st,
+                            const P& p) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = C;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = dependent ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+}  // namespace pe_host

@@ -16,6 +16,7 @@
 // in a fixed order, so a call's results do not depend on timing.
 #pragma once
 
+#include "pe_cluster.cuh"
 #include "pe_internal.cuh"
 #include "pe_tma.cuh"
 
@@ -26,31 +27,6 @@ constexpr int kFW = kFT / 32;
 constexpr int kListCap = 1024;    // columns of a candidate list
 constexpr int kListK = 256;       // largest top-k that is looked for in a list
 constexpr int kProbe = 128;       // columns that a list is sought for under top-p alone
-constexpr int kMaxCluster = 8;
-
-// ------------------------------------------------------------------ clusters
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_arrive() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait() {
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_sync() {
-  cluster_arrive();
-  cluster_wait();
-}
-// The same variable in the shared memory of the cluster's CTA `rank`.
-template <class T>
-__device__ __forceinline__ T* at_rank(T* p, uint32_t rank) {
-  T* q;
-  asm("mapa.u64 %0, %1, %2;" : "=l"(q) : "l"(p), "r"(rank));
-  return q;
-}
 
 // ------------------------------------------------------------------- weights
 // 2^(j/32) as the sum of two floats.

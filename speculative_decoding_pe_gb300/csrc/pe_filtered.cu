@@ -873,30 +873,12 @@ void split_rows(pe::FilterParams& p, int elt, int sms) {
   p.seg = (p.per_cta + pe::kFW - 1) / pe::kFW;
 }
 
-template <class K>
-cudaError_t launch(K kernel, int grid, int C, size_t smem, bool dependent, cudaStream_t st, const pe::FilterParams& p) {
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = C;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(pe::kFT);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cfg.attrs = attr;
-  cfg.numAttrs = dependent ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p);
-}
-
 template <int DT, bool kVerify>
 int launch_filter(const pe::FilterParams& p, cudaStream_t st) {
   static std::atomic<unsigned long long> done{0};
   if (!pe_host::allow_smem(pe::filter_kernel<DT, kVerify>, kMaxSmem, done)) return PE_ECUDA;
   const size_t smem = kHeader + sizeof(pe::FilterLists) + (size_t)p.per_cta * 16;
-  return launch(pe::filter_kernel<DT, kVerify>, p.n * p.C, p.C, smem, false, st, p) == cudaSuccess ? PE_OK : PE_ECUDA;
+  return pe_host::launch_clusters(pe::filter_kernel<DT, kVerify>, p.n * p.C, pe::kFT, p.C, smem, false, st, p) == cudaSuccess ? PE_OK : PE_ECUDA;
 }
 
 template <int DT>
@@ -906,7 +888,7 @@ int launch_verify(pe::FilterParams p, int B, int elt, int sms, cudaStream_t st) 
   p.n = B;
   split_rows(p, elt, sms);
   const size_t smem = kHeader + 12 * pe::kKeptCap;
-  return launch(pe::residual_kernel<DT>, B * p.C, p.C, smem, true, st, p) == cudaSuccess ? PE_OK : PE_ECUDA;
+  return pe_host::launch_clusters(pe::residual_kernel<DT>, B * p.C, pe::kFT, p.C, smem, true, st, p) == cudaSuccess ? PE_OK : PE_ECUDA;
 }
 
 int rows_ok(const void* rows, int64_t stride, int elt, int V) {
