@@ -50,7 +50,7 @@ __device__ const float2 kExp2Table[32] = {
 };
 
 // One row's scale: w(x) = 2^((x - M) c), c = log2(e) / T as two floats.  far: distance
-// from M at which a weight counts as nothing (2^-100).  A row with an infinity
+// from M from which on a weight is nothing (2^-64).  A row with an infinity
 // shares its weight among those columns.
 struct Scale {
   float M, ch, cl, far;
@@ -64,7 +64,7 @@ __device__ __forceinline__ Scale make_scale(float M, float T) {
   s.inf = M == INFINITY;
   s.ch = (float)c;
   s.cl = (float)(c - (double)s.ch);
-  s.far = (float)(100.0 / c);
+  s.far = (float)(64.0 / c);
   return s;
 }
 
@@ -77,8 +77,9 @@ __device__ __forceinline__ float2 weight(const Scale& s, const float2* table, fl
   float d = x - s.M;
   const float bb = d - x;
   const float dl = (x - (d - bb)) - (s.M + bb);  // exact: d + dl = x - M
-  float e0 = d >= -s.far ? dl : 0.f;
-  d = fmaxf(d, -s.far);  // -inf and NaN too
+  const bool near = d > -s.far;  // not -inf, not NaN
+  const float e0 = near ? dl : 0.f;
+  d = near ? d : 0.f;
   const float p = d * s.ch;
   const float e = fmaf(d, s.ch, -p) + fmaf(d, s.cl, e0 * s.ch);
   const float z = p + 393216.f;  // 1.5 * 2^18: the sum's last bit is 1/32
@@ -87,7 +88,7 @@ __device__ __forceinline__ float2 weight(const Scale& s, const float2* table, fl
   const float2 t = table[zi & 31];
   const float in = fmaf(r, fmaf(r, fmaf(r, 0x1.3b2ab60000000p-7f, 0x1.c6b08e0000000p-5f), 0x1.ebfbe00000000p-3f), -0x1.05c6100000000p-29f);
   const float q = fmaf(r, 0x1.62e4300000000p-1f, r * in);
-  const float two_n = __int_as_float((127 + (zi >> 5)) << 23);
+  const float two_n = near ? __int_as_float((127 + (zi >> 5)) << 23) : 0.f;
   return make_float2(t.x * two_n, fmaf(t.x, q, t.y) * two_n);
 }
 
