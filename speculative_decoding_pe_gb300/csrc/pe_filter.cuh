@@ -26,7 +26,6 @@ constexpr int kFT = 512;          // threads of a filter CTA
 constexpr int kFW = kFT / 32;
 constexpr int kListCap = 1024;    // columns of a candidate list
 constexpr int kListK = 256;       // largest top-k that is looked for in a list
-constexpr int kProbe = 128;       // columns that a list is sought for under top-p alone
 
 // ------------------------------------------------------------------- weights
 // 2^(j/32) as the sum of two floats.
@@ -57,15 +56,24 @@ struct Scale {
   bool inf;
 };
 
-__device__ __forceinline__ Scale make_scale(float M, float T) {
-  Scale s;
-  const double c = 1.4426950408889634 / (T > 0.f ? (double)T : 1.0);
-  s.M = M;
-  s.inf = M == INFINITY;
-  s.ch = (float)c;
-  s.cl = (float)(c - (double)s.ch);
-  s.far = (float)(64.0 / c);
-  return s;
+// The parts of c and of min-p's floor that do not need the row.  64-bit arithmetic is
+// slow on this GPU (a warp's instruction takes some 16 clocks): one thread of a CTA does it, while
+// the row is on its way.
+struct Rates {
+  float ch, cl, far;
+  double log_m;  // T ln(m), where min-p is on
+};
+__device__ __forceinline__ Rates make_rates(float T, float m) {
+  Rates r;
+  const double t = T > 0.f ? (double)T : 1.0, c = 1.4426950408889634 / t;
+  r.ch = (float)c;
+  r.cl = (float)(c - (double)r.ch);
+  r.far = 64.f / r.ch;
+  r.log_m = m > 0.f && m < 1.f ? t * log((double)m) : 0.0;
+  return r;
+}
+__device__ __forceinline__ Scale make_scale(float M, const Rates& r) {
+  return Scale{M, r.ch, r.cl, r.far, M == INFINITY};
 }
 
 // w(x) = hi + lo.  y = (x - M) c = n + j/32 + r with |r| <= 1/64;
@@ -102,12 +110,23 @@ struct WeightSum {
     lo += (h - (t - s)) + l;
     s = t;
   }
-  // times 2^bits, as an integer
+  // times 2^bits, as an integer: s - kBias is a multiple of the bias's last bit
   __device__ __forceinline__ unsigned long long fixed(int bits) const {
-    const double v = ((double)(s - (float)kBias) + (double)lo) * (double)(1ull << bits);
-    return v > 0.0 ? (unsigned long long)(v + 0.5) : 0ull;
+    const long long v = __float2ll_rn((s - (float)kBias) * __int_as_float((127 + bits) << 23)) +
+                        __float2ll_rn(lo * __int_as_float((127 + bits) << 23));
+    return v > 0 ? (unsigned long long)v : 0ull;
   }
 };
+// One weight times 2^bits.
+__device__ __forceinline__ unsigned long long fixed_weight(float2 w, int bits) {
+  const float up = __int_as_float((127 + bits) << 23);
+  const long long v = __float2ll_rn(w.x * up) + __float2ll_rn(w.y * up);
+  return v > 0 ? (unsigned long long)v : 0ull;
+}
+// floor(u W) for u in [0,1)
+__device__ __forceinline__ unsigned long long share_of(float u, unsigned long long W) {
+  return __umul64hi(__float2ull_rz(u * 0x1p64f), W);
+}
 constexpr int kSumBits = 44;   // row sums: up to 2^18 weights of at most 1
 constexpr int kListBits = 52;  // list sums: up to 2^10
 
@@ -202,11 +221,10 @@ __device__ __forceinline__ bool read_asked(const AskedArrays& a, int i, int V, A
   return ok;
 }
 // Smallest value that min-p keeps (-infinity: all).
-__device__ __forceinline__ float min_p_floor(const Asked& a, float M) {
+__device__ __forceinline__ float min_p_floor(const Asked& a, const Rates& r, float M) {
   if (!(a.m > 0.f) || a.T == 0.f) return -INFINITY;
   if (a.m >= 1.f || M == INFINITY) return M;
-  const double t = (double)M + (double)a.T * log((double)a.m);
-  return __double2float_ru(t);  // x >= t exactly when x >= this float
+  return __double2float_ru((double)M + r.log_m);  // x >= t exactly when x >= this float
 }
 
 }  // namespace pe

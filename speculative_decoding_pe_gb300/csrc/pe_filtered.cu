@@ -54,15 +54,35 @@ struct FilterShared {
   uint32_t warp_count[kFW];
   uint32_t bounds[kMaxCluster];
   uint32_t maxima[kMaxCluster];
-  unsigned long long total;
-  uint32_t listed, own, base, done;
-  int tie, token;
+  unsigned long long total, above;
+  uint32_t listed, own, bin, in_bin, stored;
+  int tie;
   float2 table[32];
   double px;
+  Rates rates;
+  float2 inverse[2];
+  float floor;
+  int first;
 };
+constexpr int kListBins = 256;
+constexpr int kSteps = 1024;      // bins of the search for a row's cut by weight
+constexpr int kMaxSegment = 512;  // vectors of a warp's segment, at most
 struct FilterLists {
-  unsigned long long key[kListCap];
-  unsigned long long w[kListCap];
+  unsigned long long key[kListCap];  // (value's key, ~column)
+  union {
+    struct {                         // the columns of one bin
+      unsigned long long key[kListCap];
+      unsigned long long w[kListCap];
+    } sel;
+    unsigned short queue[kFW][kMaxSegment];
+  };
+  union {
+    struct {
+      unsigned long long mass[kListBins];
+      uint32_t count[kListBins];
+    };
+    uint32_t steps[kSteps];
+  };
 };
 
 __device__ __forceinline__ unsigned long long warp_sum_u64(unsigned long long v) {
@@ -116,6 +136,48 @@ struct Slice {
       count += sh->counts[slot][r];
       sum += sh->sums[slot][r];
     }
+  }
+
+  // The warp's share of the row's weight.  Vectors whose largest weight is below 2^-12
+  // go through the hardware's exponential in 24 bits: their errors are of either sign
+  // and some 2^-22 of a small part of the sum.  The others are queued (few, in a row of a
+  // language model: a branch in the loop would be taken by one lane or another nearly every
+  // time) and weighed in full.
+  __device__ __forceinline__ unsigned long long mass(const Scale& sc, unsigned short* queue) {
+    const float big = sc.inf ? -INFINITY : sc.M - 12.f / sc.ch;
+    float small = 0.f;
+    int queued = 0;
+    for (int i0 = lo; i0 < hi; i0 += 32) {
+      const int i = i0 + lane;
+      bool put = false;
+      if (i < hi) {
+        const uint4 q = v[i];
+        put = Elt<DT>::max_of(q) >= big;
+        if (!put) {
+#pragma unroll
+          for (int e = 0; e < Elt<DT>::kN; ++e) {
+            float w;
+            asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w) : "f"((fmaxf(Elt<DT>::get(q, e), -INFINITY) - sc.M) * sc.ch));
+            small += w;
+          }
+        }
+      }
+      const uint32_t m = __ballot_sync(0xffffffffu, put);
+      if (put) queue[queued + __popc(m & ((1u << lane) - 1))] = (unsigned short)(i - lo);
+      queued += __popc(m);
+    }
+    __syncwarp();
+    WeightSum<256> ws;
+    for (int j = lane; j < queued; j += 32) {
+      const uint4 q = v[lo + queue[j]];
+#pragma unroll
+      for (int e = 0; e < Elt<DT>::kN; ++e) {
+        const float2 w = weight(sc, sh->table, Elt<DT>::get(q, e));
+        ws.add(w.x, w.y);
+      }
+    }
+    ws.add(0.f, small);
+    return warp_sum_u64(ws.fixed(kSumBits));
   }
 
   // Columns with key >= t: how many, and (kMass) their weight.
@@ -258,6 +320,229 @@ __device__ __forceinline__ uint32_t kth_prefix(uint32_t mine, int k) {
   return t;
 }
 
+// Bin where the running sum of 256 bins, taken from `bin 0` on, reaches (kCount: of
+// counts) `target`; sh.bin (kListBins: it does not) and the sum before it in sh.above.
+template <bool kCount>
+__device__ __forceinline__ void find_bin(FilterShared& sh, const FilterLists& ls, unsigned long long target) {
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    unsigned long long v[kListBins / 32], mine = 0;
+#pragma unroll
+    for (int i = 0; i < kListBins / 32; ++i) {
+      const int bin = lane * (kListBins / 32) + i;
+      v[i] = kCount ? ls.count[bin] : ls.mass[bin];
+      mine += v[i];
+    }
+    unsigned long long pre = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned long long x = __shfl_up_sync(0xffffffffu, pre, o);
+      if (lane >= o) pre += x;
+    }
+    if (lane == 0) sh.bin = kListBins, sh.in_bin = 0;
+    __syncwarp();
+    pre -= mine;
+#pragma unroll
+    for (int i = 0; i < kListBins / 32; ++i) {
+      if (pre < target && pre + v[i] >= target) {
+        sh.bin = lane * (kListBins / 32) + i;
+        sh.above = pre;
+      }
+      pre += v[i];
+    }
+  }
+  __syncthreads();
+}
+
+// CTA 0 of a row whose kept columns are all among the L listed ones: the cut and the draw
+// in linear time, by bins of the value (from the largest on) and of the column, with all
+// pairs compared within one bin only.  Weights are integers here (2^kListBits for the
+// largest), sums exact.
+//  k: columns kept at most; p: share of the weight (above 1: all); whole: the row's weight,
+//  or -1: that of the first k.
+template <bool kVerify>
+__device__ __forceinline__ void resolve_list(const FilterParams& p, FilterShared& sh, FilterLists& ls, const Scale& sc, int row,
+                                             int L, uint32_t low, uint32_t top, int k, double share, double whole, float floor,
+                                             float T, float u, bool draws, int draft) {
+  constexpr int kPer = kListCap / kFT;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  unsigned long long key[kPer], w[kPer];
+  bool keep[kPer];
+  uint32_t bin[kPer];
+  const float per_bin = (float)kListBins / ((float)(top - low) + 1.f);
+#pragma unroll
+  for (int h = 0; h < kPer; ++h) {
+    const int i = tid + h * kFT;
+    keep[h] = i < L;
+    key[h] = w[h] = bin[h] = 0;
+    if (keep[h]) {
+      key[h] = ls.key[i];
+      w[h] = fixed_weight(weight(sc, sh.table, key_value(key_of(key[h]))), kListBits);
+      bin[h] = min((uint32_t)((float)(top - key_of(key[h])) * per_bin), (uint32_t)kListBins - 1);
+    }
+  }
+  auto clear = [&]() {
+    if (tid < kListBins) ls.mass[tid] = 0, ls.count[tid] = 0;
+    __syncthreads();
+  };
+  auto select = [&](bool in, int h) {
+    if (in) {
+      const uint32_t at = atomicAdd(&sh.in_bin, 1u);
+      ls.sel.key[at] = key[h];
+      ls.sel.w[at] = w[h];
+    }
+  };
+
+  if (L > k) {  // the first k
+    clear();
+#pragma unroll
+    for (int h = 0; h < kPer; ++h)
+      if (keep[h]) atomicAdd(&ls.count[bin[h]], 1u);
+    __syncthreads();
+    find_bin<true>(sh, ls, (unsigned long long)k);
+#pragma unroll
+    for (int h = 0; h < kPer; ++h) select(keep[h] && bin[h] == sh.bin, h);
+    __syncthreads();
+    const int n = (int)sh.in_bin;
+#pragma unroll
+    for (int h = 0; h < kPer; ++h) {
+      if (keep[h] && bin[h] >= sh.bin) {
+        uint32_t r = (uint32_t)sh.above;
+        if (bin[h] == sh.bin)
+          for (int j = 0; j < n; ++j) r += ls.sel.key[j] > key[h];
+        keep[h] = bin[h] == sh.bin && r < (uint32_t)k;
+      }
+    }
+    __syncthreads();
+  }
+  if (share <= 1.0) {  // the smallest prefix that holds its share
+    clear();
+#pragma unroll
+    for (int h = 0; h < kPer; ++h)
+      if (keep[h]) atomicAdd(&ls.mass[bin[h]], w[h]);
+    __syncthreads();
+    if (whole < 0.0) {
+      if (tid < 32) {
+        unsigned long long v = 0;
+#pragma unroll
+        for (int i = 0; i < kListBins / 32; ++i) v += ls.mass[lane + 32 * i];
+        v = warp_sum_u64(v);
+        if (lane == 0) sh.total = v;
+      }
+      __syncthreads();
+      whole = (double)sh.total;
+    }
+    // (a sum is below the real target exactly when it is below the next integer; 1: the first column alone)
+    const unsigned long long target = max((unsigned long long)ceil(share * whole), 1ull);
+    find_bin<false>(sh, ls, target);
+#pragma unroll
+    for (int h = 0; h < kPer; ++h) select(keep[h] && bin[h] == sh.bin, h);
+    __syncthreads();
+    const int n = (int)sh.in_bin;
+#pragma unroll
+    for (int h = 0; h < kPer; ++h) {
+      if (keep[h] && bin[h] >= sh.bin) {
+        unsigned long long before = sh.above;
+        if (bin[h] == sh.bin)
+          for (int j = 0; j < n; ++j)
+            if (ls.sel.key[j] > key[h]) before += ls.sel.w[j];
+        keep[h] = bin[h] == sh.bin && before < target;
+      }
+    }
+    __syncthreads();
+  }
+
+  // what is kept, by bins of the column
+  clear();
+  unsigned long long least = ~0ull;
+  const float per_col = (float)kListBins / (float)p.V;
+#pragma unroll
+  for (int h = 0; h < kPer; ++h) {
+    keep[h] = keep[h] && key_value(key_of(key[h])) >= floor;
+    if (keep[h]) {
+      bin[h] = min((uint32_t)((float)(0xffffffffu - (uint32_t)key[h]) * per_col), (uint32_t)kListBins - 1);
+      atomicAdd(&ls.mass[bin[h]], w[h]);
+      least = min(least, key[h]);
+    }
+  }
+  if (kVerify) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) least = min(least, __shfl_xor_sync(0xffffffffu, least, o));
+    if (lane == 0) sh.warp_sum[warp] = least;
+    if (tid == 0) {
+      sh.stored = 0;
+      sh.px = draft >= 0 && draft < p.V ? 0.0 : -1.0;
+    }
+  }
+  __syncthreads();
+  if (tid < 32) {
+    unsigned long long v = 0;
+#pragma unroll
+    for (int i = 0; i < kListBins / 32; ++i) v += ls.mass[lane + 32 * i];
+    v = warp_sum_u64(v);
+    if (lane == 0) sh.total = v;
+  }
+  __syncthreads();
+  const unsigned long long W = sh.total;
+  if (draws) {
+    const unsigned long long at = share_of(u, W);
+    find_bin<false>(sh, ls, at + 1);
+#pragma unroll
+    for (int h = 0; h < kPer; ++h) select(keep[h] && bin[h] == sh.bin, h);
+    __syncthreads();
+    const int n = (int)sh.in_bin;
+#pragma unroll
+    for (int h = 0; h < kPer; ++h) {
+      if (keep[h] && w[h] && bin[h] == sh.bin) {
+        const uint32_t inv = (uint32_t)key[h];  // larger: a lower column
+        unsigned long long upto = sh.above;
+        for (int j = 0; j < n; ++j)
+          if ((uint32_t)ls.sel.key[j] >= inv) upto += ls.sel.w[j];
+        if (upto > at && upto - w[h] <= at) {
+          const int col = (int)(0xffffffffu - inv);
+          if (kVerify) {
+            p.cuts[row].token = col;
+          } else {
+            p.out_tokens[row] = col;
+            if (p.out_prob) p.out_prob[row] = (float)((double)w[h] / (double)W);
+          }
+        }
+      }
+    }
+  }
+  if (kVerify) {
+    const bool store = row < p.na;
+#pragma unroll
+    for (int h = 0; h < kPer; ++h) {
+      if (keep[h]) {
+        const int col = (int)(0xffffffffu - (uint32_t)key[h]);
+        if (col == draft) sh.px = (double)w[h] / (double)W;
+        if (store) {
+          const uint32_t at = atomicAdd(&sh.stored, 1u);
+          if (at < kKeptCap) {
+            Kept& o = p.kept[(long long)row * kKeptCap + at];
+            o.w = w[h];
+            o.col = col;
+          }
+        }
+      }
+    }
+    __syncthreads();
+    if (tid == 0) {
+      for (int x = 0; x < kFW; ++x) least = min(least, sh.warp_sum[x]);
+      RowCut& c = p.cuts[row];
+      c.cut.key = key_of(least);
+      c.cut.tie = (int)(0xffffffffu - (uint32_t)least);
+      c.cut.floor = -INFINITY;
+      c.M = sc.M;
+      c.T = T;
+      c.listed = store && sh.stored <= kKeptCap ? (int)sh.stored : -1;
+      c.W = (double)W * (1.0 / (1ull << kListBits));
+      c.px = sh.px;
+    }
+  }
+}
+
 template <int DT, bool kVerify>
 __global__ void __launch_bounds__(kFT, 2) filter_kernel(const FilterParams p) {
   extern __shared__ __align__(128) unsigned char smem[];
@@ -351,7 +636,7 @@ __global__ void __launch_bounds__(kFT, 2) filter_kernel(const FilterParams p) {
   if (tid == 0) {
     sh.listed = 0;
     sh.own = 0;
-    sh.done = 0;
+    sh.rates = make_rates(a.T, a.m);
   }
   if (tid < 32) sh.table[tid] = kExp2Table[tid];
   __syncwarp();
@@ -382,7 +667,7 @@ __global__ void __launch_bounds__(kFT, 2) filter_kernel(const FilterParams p) {
   const bool small_k = a.k <= kListK && a.k < p.V;
   const bool nucleus = !small_k && a.k == p.V && a.p < 1.f;
   uint32_t bound = 0;
-  if (small_k || nucleus) bound = kth_prefix(mine >> 16, small_k ? a.k : kProbe);
+  if (small_k) bound = kth_prefix(mine >> 16, a.k);
   __syncthreads();
   cluster_wait();  // every CTA has started
   if (tid < p.C) {
@@ -403,8 +688,13 @@ __global__ void __launch_bounds__(kFT, 2) filter_kernel(const FilterParams p) {
     none(0.0);
     return;
   }
-  const Scale sc = make_scale(M, a.T);
-  const float floor = min_p_floor(a, M);
+  const Scale sc = make_scale(M, sh.rates);
+  float floor = -INFINITY;
+  if (a.m > 0.f) {
+    if (tid == 0) sh.floor = min_p_floor(a, sh.rates, M);
+    __syncthreads();
+    floor = sh.floor;
+  }
   const double p_mass = a.p > 0.f ? (double)a.p : 0.0;  // at most the whole: >= 1 is off
 
   auto answer = [&](int token, double w, double W) {  // one thread
@@ -416,155 +706,74 @@ __global__ void __launch_bounds__(kFT, 2) filter_kernel(const FilterParams p) {
     }
   };
 
-  // ---- a list of the first columns
-  if (small_k || nucleus) {
-    if ((mine >> 16) >= bound) {
+  // ---- candidates: a value that every kept column reaches
+  const bool by_min = a.k == p.V && a.p >= 1.f && floor > -INFINITY;
+  unsigned long long Z = 0;  // the whole row's weight (top-p alone)
+  if (small_k || nucleus || by_min) {
+    uint32_t low = value_key(floor);
+    if (small_k) {
+      low = max(low, bound << 16);
+    } else if (nucleus) {
+      unsigned long long sum = s.mass(sc, ls.queue[warp]);
+      uint32_t c = 0;
+      s.exchange(c, sum);
+      Z = sum;
+      // The last kept column and those after it weigh more than (1 - p) Z and are at most
+      // V, so it weighs more than (1 - p) Z / V: 2^-20 of itself and 2^-20 of M and the distance
+      // less, for this estimate's roundings.
+      const float octaves = log2f((float)(1.0 - p_mass) * ((float)sum * 0x1p-44f) / (float)p.V);
+      const float away = octaves / sc.ch;
+      low = max(low, M == INFINITY ? top : value_key(M + away - 0x1p-20f * (fabsf(M) + fabsf(away)) - 0x1p-18f / sc.ch));
+    }
+    uint32_t mine_n = 0;
+    if (mine >= low) {
+      for (int i = s.lo + lane; i < s.hi; i += 32) {
+        const uint4 q = s.v[i];
+#pragma unroll
+        for (int e = 0; e < E::kN; ++e) mine_n += value_key(E::get(q, e)) >= low && s.col0 + i * E::kN + e < p.V;
+      }
+    }
+    uint32_t pre = mine_n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t x = __shfl_up_sync(0xffffffffu, pre, o);
+      if (lane >= o) pre += x;
+    }
+    const uint32_t warp_n = __shfl_sync(0xffffffffu, pre, 31);
+    uint32_t base = 0;
+    if (warp_n && lane == 0) {
+      atomicAdd(&sh.own, warp_n);
+      base = atomicAdd(at_rank(&sh.listed, 0), warp_n);
+    }
+    base = __shfl_sync(0xffffffffu, base, 0) + pre - mine_n;
+    if (mine_n) {
+      unsigned long long* list = at_rank(ls.key, 0);
       for (int i = s.lo + lane; i < s.hi; i += 32) {
         const uint4 q = s.v[i];
 #pragma unroll
         for (int e = 0; e < E::kN; ++e) {
           const uint32_t k = value_key(E::get(q, e));
           const int col = s.col0 + i * E::kN + e;
-          if ((k >> 16) >= bound && col < p.V) {
-            const uint32_t at = atomicAdd(rank == 0 ? &sh.listed : &sh.own, 1u);
-            if (at < kListCap) ls.key[at] = ((unsigned long long)k << 32) | (0xffffffffu - (uint32_t)col);
+          if (k >= low && col < p.V) {
+            if (base < kListCap) list[base] = ((unsigned long long)k << 32) | (0xffffffffu - (uint32_t)col);
+            ++base;
           }
         }
       }
     }
     __syncthreads();
-    if (rank != 0) {
-      if (tid == 0) sh.base = atomicAdd(at_rank(&sh.listed, 0), sh.own);
-      __syncthreads();
-      for (int i = tid; i < (int)min(sh.own, (uint32_t)kListCap); i += kFT)
-        if (sh.base + i < kListCap) *at_rank(&ls.key[sh.base + i], 0) = ls.key[i];
-    }
-    double Z = 0.0;
-    if (nucleus) {  // the whole row's weight
-      uint32_t c;
-      unsigned long long sum;
-      s.template above<true>(sc, 0u, c, sum);
-      Z = (double)sum * (1.0 / (1ull << kSumBits));
-    } else {
-      cluster_sync();
-    }
-    if (rank == 0) {
-      const int L = (int)sh.listed;
-      bool done = L <= kListCap;
-      if (done) {
-        for (int i = tid; i < L; i += kFT) {
-          const float2 w = weight(sc, sh.table, key_value(key_of(ls.key[i])));
-          ls.w[i] = (unsigned long long)(((double)w.x + (double)w.y) * (double)(1ull << kListBits) + 0.5);
-        }
-        if (tid == 0) sh.total = 0;
-        __syncthreads();
-        // rank and preceding weight of up to two columns a thread
-        uint32_t rk[2] = {0, 0};
-        unsigned long long pre[2] = {0, 0};
-        unsigned long long sum = 0;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int i = tid + h * kFT;
-          if (i < L) {
-            const unsigned long long k = ls.key[i];
-            for (int j = 0; j < L; ++j)
-              if (ls.key[j] > k) {
-                ++rk[h];
-                pre[h] += ls.w[j];
-              }
-            if (small_k && rk[h] < (uint32_t)a.k) sum += ls.w[i];
-            if (nucleus) sum += ls.w[i];
-          }
-        }
-        sum = warp_sum_u64(sum);
-        if (lane == 0) atomicAdd(&sh.total, sum);
-        __syncthreads();
-        const double listed = (double)sh.total * (1.0 / (1ull << kListBits));
-        double target = p_mass * (small_k ? listed : Z);
-        if (a.p >= 1.f) target = 1e300;
-        if (nucleus && listed < target) done = false;
-        __syncthreads();
-        if (done) {
-          bool keep[2];
-          unsigned long long kw = 0, lk = ~0ull;  // kept weight; smallest kept key
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int i = tid + h * kFT;
-            keep[h] = i < L && (small_k ? rk[h] < (uint32_t)a.k : true) &&
-                      (rk[h] == 0 || (double)pre[h] * (1.0 / (1ull << kListBits)) < target) &&
-                      key_value(key_of(ls.key[i < L ? i : 0])) >= floor;
-            if (i < L && !keep[h]) ls.w[i] = 0;
-            if (keep[h]) {
-              kw += ls.w[i];
-              lk = min(lk, ls.key[i]);
-            }
-          }
-          if (tid == 0) sh.total = 0;
-          __syncthreads();
-          kw = warp_sum_u64(kw);
-          for (int o = 16; o; o >>= 1) lk = min(lk, __shfl_xor_sync(0xffffffffu, lk, o));
-          if (lane == 0) {
-            atomicAdd(&sh.total, kw);
-            sh.warp_sum[warp] = lk;
-          }
-          if (tid == 0) sh.own = 0;
-          if (tid == 0) sh.px = draft >= 0 && draft < p.V ? 0.0 : -1.0;
-          __syncthreads();
-          const unsigned long long W = sh.total;
-          if (draws) {
-            const unsigned long long at = (unsigned long long)((double)u * (double)W);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int i = tid + h * kFT;
-              if (i < L && keep[h] && ls.w[i]) {
-                const uint32_t inv = (uint32_t)ls.key[i];  // larger: lower column
-                unsigned long long upto = 0;
-                for (int j = 0; j < L; ++j)
-                  if ((uint32_t)ls.key[j] >= inv) upto += ls.w[j];
-                if (upto > at && upto - ls.w[i] <= at) answer((int)(0xffffffffu - inv), (double)ls.w[i], (double)W);
-              }
-            }
-          }
-          if (kVerify) {
-            const bool store = row < p.na;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int i = tid + h * kFT;
-              if (i < L && keep[h]) {
-                const int col = (int)(0xffffffffu - (uint32_t)ls.key[i]);
-                if (col == draft) sh.px = (double)ls.w[i] / (double)W;
-                if (store) {
-                  const uint32_t at = atomicAdd(&sh.own, 1u);
-                  if (at < kKeptCap) {
-                    Kept& k = p.kept[(long long)row * kKeptCap + at];
-                    k.w = ls.w[i];
-                    k.col = col;
-                  }
-                }
-              }
-            }
-            __syncthreads();
-            if (tid == 0) {
-              unsigned long long k = ~0ull;
-              for (int w = 0; w < kFW; ++w) k = min(k, sh.warp_sum[w]);
-              RowCut& c = p.cuts[row];
-              c.cut.key = key_of(k);
-              c.cut.tie = (int)(0xffffffffu - (uint32_t)k);
-              c.cut.floor = -INFINITY;
-              c.M = M;
-              c.T = a.T;
-              c.listed = store && sh.own <= kKeptCap ? (int)sh.own : -1;
-              c.W = (double)W * (1.0 / (1ull << kListBits));
-              c.px = sh.px;
-            }
-          }
-        }
-      }
-      __syncthreads();
-      if (tid < p.C) *at_rank(&sh.done, tid) = done;
-    }
+    if (tid < p.C) *at_rank(&sh.counts[s.turn & 1][rank], tid) = sh.own;
     cluster_sync();
-    if (sh.done) return;
+    int L = 0;
+    for (int r = 0; r < p.C; ++r) L += (int)min(sh.counts[s.turn & 1][r], 1u << 20);
+    ++s.turn;
+    if (L <= kListCap) {
+      if (rank == 0)
+        resolve_list<kVerify>(p, sh, ls, sc, row, L, low, top, small_k ? a.k : p.V,
+                              a.p < 1.f ? p_mass : 2.0, nucleus ? (double)Z * (1ull << (kListBits - kSumBits)) : -1.0, floor, a.T, u,
+                              draws, draft);
+      return;
+    }
   }
 
   // ---- the cut, over the whole row
@@ -648,8 +857,7 @@ __global__ void __launch_bounds__(kFT, 2) filter_kernel(const FilterParams p) {
     o.px = px;
   }
   if (draws) {
-    unsigned long long at = (unsigned long long)((double)u * (double)sum);
-    at = min(at, sum - 1);
+    const unsigned long long at = share_of(u, sum);
     for (int w = 0; w < warp; ++w) before += sh.warp_sum[w];
     if (before <= at && at < before + mine_w) {
       const int i = find_column<E::kN, 256>(s.lo, s.hi, lane, at - before, kSumBits, kept);
@@ -704,37 +912,44 @@ __global__ void __launch_bounds__(kFT) residual_kernel(const FilterParams p) {
   const RowCut* target = p.cuts + (long long)b * (p.Kp + 1);
   const RowCut* drafts = p.cuts + p.na + (long long)b * p.Kp;
   const bool bad = target[p.Kp].W < 0.0;
-  int a = p.Kp;
-  for (int j0 = 0; j0 < p.Kp; j0 += 32) {
-    const int j = j0 + lane;
-    bool no = false;
-    if (j < p.Kp) {
-      const double px = target[j].px, qx = drafts[j].px;
-      no = !((double)__ldg(p.coins + b * p.Kp + j) * qx < px);
-      if (p.chance && rank == 0 && warp == 0)
-        p.chance[b * p.Kp + j] = bad || !(px > 0.0) ? 0.f : px < qx ? (float)(px / qx) : 1.f;
+  if (warp == 0) {
+    int a = p.Kp;
+    for (int j0 = 0; j0 < p.Kp; j0 += 32) {
+      const int j = j0 + lane;
+      bool no = false;
+      if (j < p.Kp) {
+        const double px = target[j].px, qx = drafts[j].px;
+        no = !((double)__ldg(p.coins + b * p.Kp + j) * qx < px);
+        if (p.chance && rank == 0) p.chance[b * p.Kp + j] = bad || !(px > 0.0) ? 0.f : px < qx ? (float)(px / qx) : 1.f;
+      }
+      const uint32_t m = __ballot_sync(0xffffffffu, no);
+      if (m && a == p.Kp) a = j0 + __ffs(m) - 1;
     }
-    const uint32_t m = __ballot_sync(0xffffffffu, no);
-    if (m && a == p.Kp) a = j0 + __ffs(m) - 1;
+    if (lane == 0) {
+      sh.first = a;
+      const RowCut& t = target[a];
+      if (rank == 0) {
+        p.accepted[b] = bad ? 0 : a;
+        if (bad || t.W == 0.0) p.bonus[b] = -1;
+        else if (a == p.Kp) p.bonus[b] = t.token;
+      }
+      if (!bad && a < p.Kp && t.W > 0.0) sh.rates = make_rates(t.T, 0.f);
+    }
   }
+  __syncthreads();
+  const int a = sh.first;
   const RowCut& t = target[a];
-  const bool stream = !bad && a < p.Kp && t.W > 0.0 && t.listed < 0;
-  if (rank == 0 && tid == 0) {
-    p.accepted[b] = bad ? 0 : a;
-    if (bad || t.W == 0.0) p.bonus[b] = -1;
-    else if (a == p.Kp) p.bonus[b] = t.token;
-  }
+  const bool stream = t.listed < 0;
   cluster_wait();
   if (bad || a == p.Kp || t.W == 0.0) return;
   const RowCut& d = drafts[a];
   const char* trow = p.rows_a + ((long long)b * (p.Kp + 1) + a) * p.a_bytes;
   const char* drow = p.rows_b + ((long long)b * p.Kp + a) * p.b_bytes;
   const float u = __ldg(p.u + b);
-  const Scale st = make_scale(t.M, t.T);
-  const Scale sd = make_scale(d.W > 0.0 ? d.M : 0.f, t.T);
-  const Cut ct = t.cut, cd = d.cut;
   const bool has_q = d.W > 0.0;
-  const double it = 1.0 / t.W, id = has_q ? 1.0 / d.W : 0.0;
+  const Scale st = make_scale(t.M, sh.rates);
+  const Scale sd = make_scale(has_q ? d.M : 0.f, sh.rates);
+  const Cut ct = t.cut, cd = d.cut;
   constexpr int kBits = 60;
 
   if (!stream) {
@@ -747,13 +962,13 @@ __global__ void __launch_bounds__(kFT) residual_kernel(const FilterParams p) {
     int col = -1;
     if (tid < L) {
       col = kept[tid].col;
-      const double pr = (double)kept[tid].w * (1.0 / (1ull << kListBits)) * it;
+      const double pr = (double)kept[tid].w * (1.0 / (1ull << kListBits)) / t.W;
       double q = 0.0;
       if (has_q) {
         const float x = E::load(drow, col);
         if (cd.keeps(x, col)) {
           const float2 f = weight(sd, sh.table, x);
-          q = ((double)f.x + (double)f.y) * id;
+          q = ((double)f.x + (double)f.y) / d.W;
         }
       }
       whole = (unsigned long long)(pr * (double)(1ull << kBits) + 0.5);
@@ -776,7 +991,7 @@ __global__ void __launch_bounds__(kFT) residual_kernel(const FilterParams p) {
       cols[tid] = tid < L ? col : INT32_MAX;
     }
     __syncthreads();
-    const unsigned long long at = min((unsigned long long)((double)u * (double)R), R - 1);
+    const unsigned long long at = share_of(u, R);
     if (mine) {
       unsigned long long upto = 0;
       for (int j = 0; j < L; ++j)
@@ -796,8 +1011,14 @@ __global__ void __launch_bounds__(kFT) residual_kernel(const FilterParams p) {
   const int v0 = rank * p.per_cta, vn = max(0, min(p.per_cta, p.nvec - v0));
   s.lo = v0 + min(vn, warp * p.seg);
   s.hi = v0 + min(vn, warp * p.seg + p.seg);
-  const float ith = (float)it, itl = (float)(it - (double)ith);
-  const float idh = (float)id, idl = (float)(id - (double)idh);
+  if (tid < 2) {  // 1 / W of both rows, as two floats
+    const double i = tid == 0 ? 1.0 / t.W : has_q ? 1.0 / d.W : 0.0;
+    const float hi = (float)i;
+    sh.inverse[tid] = make_float2(hi, (float)(i - (double)hi));
+  }
+  __syncthreads();
+  const float ith = sh.inverse[0].x, itl = sh.inverse[0].y;
+  const float idh = sh.inverse[1].x, idl = sh.inverse[1].y;
   bool from_p = false;
   auto rest = [&](int i, int from, int to, WeightSum<2>& ws) {
     const uint4 x = row_vector<DT>(trow, i, p.V);
@@ -834,7 +1055,7 @@ __global__ void __launch_bounds__(kFT) residual_kernel(const FilterParams p) {
     from_p = true;
   }
   if (sum == 0) return;  // (p's weights are not all zero)
-  const unsigned long long at = min((unsigned long long)((double)u * (double)sum), sum - 1);
+  const unsigned long long at = share_of(u, sum);
   for (int w = 0; w < warp; ++w) before += sh.warp_sum[w];
   if (before <= at && at < before + mine) {
     const int col = find_column<E::kN, 2>(s.lo, s.hi, lane, at - before, kBits, rest);
