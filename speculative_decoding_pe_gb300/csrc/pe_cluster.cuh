@@ -5,19 +5,29 @@
 
 namespace pe {
 
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 16;  // (above 8: kernels that allow a non-portable size)
 
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ void cluster_arrive() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+// Barriers whose lanes arrive one by one (no .aligned).  The forms for whole warps count
+// a warp as soon as some of its lanes come by: in the list's code, where lanes of a warp
+// differ in how many columns they hold from one barrier to the next, the compiled warp
+// reached __syncthreads() in two parts, and the barrier let the others go too early.
+__device__ __forceinline__ void cta_sync() { asm volatile("barrier.cta.sync 0;" ::: "memory"); }
+// The same, and how many threads have `yes`.
+__device__ __forceinline__ int cta_count(bool yes) {
+  int n;
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.popc.u32 %0, 0, p;\n\t}"
+               : "=r"(n)
+               : "r"((uint32_t)yes)
+               : "memory");
+  return n;
 }
-__device__ __forceinline__ void cluster_wait() {
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync() {
   cluster_arrive();
   cluster_wait();

@@ -22,10 +22,10 @@
 
 namespace pe {
 
-constexpr int kFT = 512;          // threads of a filter CTA
+constexpr int kFT = 256;          // threads of a filter CTA: four fit an SM
 constexpr int kFW = kFT / 32;
 constexpr int kListCap = 1024;    // columns of a candidate list
-constexpr int kListK = 256;       // largest top-k that is looked for in a list
+constexpr int kListK = 256;       // largest top-k whose columns the threads' maxima bound (one each)
 
 // ------------------------------------------------------------------- weights
 // 2^(j/32) as the sum of two floats.

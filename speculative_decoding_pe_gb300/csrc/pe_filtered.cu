@@ -46,43 +46,42 @@ struct FilterParams {
   uint32_t* err;
 };
 
+constexpr int kListBins = 256;
+constexpr int kSteps = 4 * kFT;   // bins of the search for a cut over the whole row
+constexpr int kMaxSegment = kListCap * 8 / 2 / kFW;  // vectors of a warp's segment, at most
+
 struct FilterShared {
   uint64_t bars[kFW];
   unsigned long long sums[2][kMaxCluster];  // exchanged by the CTAs, in turns
   unsigned long long warp_sum[kFW];
   uint32_t counts[2][kMaxCluster];
   uint32_t warp_count[kFW];
-  uint32_t bounds[kMaxCluster];
-  uint32_t maxima[kMaxCluster];
+  uint32_t maxima[kMaxCluster], bounds[kMaxCluster], shares[kMaxCluster];
   unsigned long long total, above;
   uint32_t listed, own, bin, in_bin, stored;
-  int tie;
+  uint32_t cut_key;
+  int cut_tie, tie;
   float2 table[32];
   double px;
   Rates rates;
   float2 inverse[2];
   float floor;
   int first;
-};
-constexpr int kListBins = 256;
-constexpr int kSteps = 1024;      // bins of the search for a row's cut by weight
-constexpr int kMaxSegment = 512;  // vectors of a warp's segment, at most
-struct FilterLists {
-  unsigned long long key[kListCap];  // (value's key, ~column)
-  union {
-    struct {                         // the columns of one bin
-      unsigned long long key[kListCap];
-      unsigned long long w[kListCap];
-    } sel;
-    unsigned short queue[kFW][kMaxSegment];
-  };
-  union {
-    struct {
-      unsigned long long mass[kListBins];
-      uint32_t count[kListBins];
-    };
+  uint32_t hist[kFT];
+  union alignas(16) {
+    unsigned long long list[kListCap];         // candidates: (value's key, ~column)
+    unsigned short queue[kFW][kMaxSegment];    // vectors to be weighed in full
     uint32_t steps[kSteps];
   };
+};
+// In the place of CTA 0's slice, once the list holds all that is needed of it.
+struct FilterLists {
+  struct {  // the columns of one bin
+    unsigned long long key[kListCap];
+    unsigned long long w[kListCap];
+  } sel;
+  unsigned long long mass[kListBins];
+  uint32_t count[kListBins];
 };
 
 __device__ __forceinline__ unsigned long long warp_sum_u64(unsigned long long v) {
@@ -106,12 +105,12 @@ struct Slice {
   // as its warp's: lane 0's values count).
   __device__ __forceinline__ void exchange(uint32_t& count, unsigned long long& sum,
                                            unsigned long long* before = nullptr, uint32_t* count_before = nullptr) {
-    __syncthreads();  // the arrays' last readers
+    cta_sync();  // the arrays' last readers
     if (lane == 0) {
       sh->warp_count[warp] = count;
       sh->warp_sum[warp] = sum;
     }
-    __syncthreads();
+    cta_sync();
     const int t = threadIdx.x;
     const int slot = turn & 1;
     if (t < C) {
@@ -180,6 +179,24 @@ struct Slice {
     return warp_sum_u64(ws.fixed(kSumBits));
   }
 
+  // The warp's share of the weight that a cut keeps.
+  __device__ __forceinline__ unsigned long long kept_mass(const Scale& sc, const Cut& cut) {
+    WeightSum<256> ws;
+    for (int i = lo + lane; i < hi; i += 32) {
+      const uint4 q = v[i];
+      if (value_key(Elt<DT>::max_of(q)) < cut.key) continue;
+#pragma unroll
+      for (int e = 0; e < Elt<DT>::kN; ++e) {
+        const float x = Elt<DT>::get(q, e);
+        if (cut.keeps(x, col0 + i * Elt<DT>::kN + e)) {
+          const float2 w = weight(sc, sh->table, x);
+          ws.add(w.x, w.y);
+        }
+      }
+    }
+    return warp_sum_u64(ws.fixed(kSumBits));
+  }
+
   // Columns with key >= t: how many, and (kMass) their weight.
   template <bool kMass>
   __device__ __forceinline__ void above(const Scale& sc, uint32_t t, uint32_t& count, unsigned long long& sum) {
@@ -217,6 +234,81 @@ struct Slice {
     }
     if (Elt<DT>::kKeyBits == 16 && !(t >> 31)) t |= 0xffffu;  // (a negative bf16's low bits)
     return t;
+  }
+
+  // The columns between which a cut lies, by one pass with a histogram: `steps` bins of
+  // x from M down to where weights are 2^-octaves, taken from the columns that `cut` keeps,
+  // of counts or of weights (relative to the bin, in 13 bits: a bin's error is far below the
+  // margins).  Afterwards every kept column of at least `hi` belongs to the wanted prefix, of
+  // `count` columns; none below `lo` does.  False: the range does not reach the target.
+  template <bool kMass>
+  __device__ __forceinline__ bool steer(const Scale& sc, const Cut& cut, float octaves, double target, uint32_t* steps, float& lo_x,
+                                        float& hi_x) {
+    const int tid = threadIdx.x;
+    const float width = octaves / (float)kSteps, range = octaves / sc.ch, per = (float)kSteps / range;
+    for (int i = tid; i < kSteps; i += kFT) steps[i] = 0;
+    cta_sync();
+    for (int i = lo + lane; i < hi; i += 32) {
+      const uint4 q = v[i];
+      if (Elt<DT>::max_of(q) <= sc.M - range) continue;
+#pragma unroll
+      for (int e = 0; e < Elt<DT>::kN; ++e) {
+        const float x = Elt<DT>::get(q, e);
+        const float d = sc.M - x;
+        if (d < range && cut.keeps(x, col0 + i * Elt<DT>::kN + e)) {
+          const int bin = min((int)(d * per), kSteps - 1);
+          uint32_t one = 1;
+          if (kMass) {
+            float w;
+            asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w) : "f"((float)(bin + 1) * width - d * sc.ch));
+            one = (uint32_t)(w * 4096.f);
+          }
+          atomicAdd(&steps[bin], one);
+        }
+      }
+    }
+    cluster_sync();
+    // every CTA adds up all of them: the same answer everywhere
+    double c[4], mine = 0.0;
+    uint32_t sum[4] = {0, 0, 0, 0};
+    for (int r = 0; r < C; ++r) {
+      const uint4 q = *reinterpret_cast<const uint4*>(at_rank(steps, r) + 4 * tid);
+      sum[0] += q.x, sum[1] += q.y, sum[2] += q.z, sum[3] += q.w;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      c[i] = kMass ? (double)sum[i] * (double)exp2f(-(float)(4 * tid + i + 1) * width) * (1.0 / 4096) : (double)sum[i];
+      mine += c[i];
+    }
+    double pre = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const double x = __shfl_up_sync(0xffffffffu, pre, o);
+      if (lane >= o) pre += x;
+    }
+    cta_sync();
+    double* part = reinterpret_cast<double*>(sh->warp_sum);
+    if (lane == 31) part[warp] = pre;
+    if (tid == 0) sh->bin = kSteps, sh->in_bin = kSteps;
+    cta_sync();
+    pre -= mine;
+    for (int w = 0; w < warp; ++w) pre += part[w];
+    const double slack = kMass ? target * 0x1p-11 : 0.0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const double next = pre + c[i];
+      if (pre < target - slack && next >= target - slack) sh->bin = 4 * tid + i;  // the cut lies here at the earliest
+      if (pre < target + slack && next >= target + slack) sh->in_bin = 4 * tid + i;  // or here at the latest
+      pre = next;
+    }
+    cluster_sync();  // (the histograms have been read)
+    const int first = (int)sh->bin, last = (int)sh->in_bin;
+    if (last >= kSteps) return false;
+    // edges of the bins as the conversion above sees them: lowered and raised by its rounding
+    const float eps = 0x1p-21f * (range + fabsf(sc.M));
+    hi_x = first ? sc.M - (float)first / per + eps : INFINITY;
+    lo_x = sc.M - (float)(last + 1) / per - eps;
+    return true;
   }
 
   // Column of the r-th (from 1) of the columns of value `key`.
@@ -310,12 +402,40 @@ __device__ __forceinline__ int find_column(int lo, int hi, int lane, unsigned lo
   return found;
 }
 
-// Largest key prefix (upper 16 bits) that at least k threads of the CTA reach.
-__device__ __forceinline__ uint32_t kth_prefix(uint32_t mine, int k) {
+// Largest key prefix (upper 16 bits) that at least k of the CTA's threads reach: by a
+// histogram of the distance from the largest one, or bit by bit where that is short.
+// hist is zero before and after.
+__device__ __forceinline__ uint32_t kth_prefix(uint32_t* hist, uint32_t mine, uint32_t top, uint32_t k) {
+  const uint32_t d = top - mine;
+  if (d < kFT) atomicAdd(&hist[d], 1u);
+  cta_sync();
+  // every warp adds up all of them
+  const int lane = threadIdx.x & 31;
+  uint32_t c[kFT / 32], sum = 0;
+#pragma unroll
+  for (int i = 0; i < kFT / 32; ++i) sum += c[i] = hist[lane * (kFT / 32) + i];
+  uint32_t pre = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t x = __shfl_up_sync(0xffffffffu, pre, o);
+    if (lane >= o) pre += x;
+  }
+  pre -= sum;
+  uint32_t at = 0xffffffffu;
+#pragma unroll
+  for (int i = 0; i < kFT / 32; ++i) {
+    if (pre < k && pre + c[i] >= k) at = lane * (kFT / 32) + i;
+    pre += c[i];
+  }
+  at = __reduce_min_sync(0xffffffffu, at);
+  cta_sync();
+  hist[threadIdx.x] = 0;
+  cta_sync();
+  if (at != 0xffffffffu) return top - at;
   uint32_t t = 0;
   for (int bit = 15; bit >= 0; --bit) {
     const uint32_t trial = t | (1u << bit);
-    if (__syncthreads_count(mine >= trial) >= k) t = trial;
+    if (cta_count(mine >= trial) >= (int)k) t = trial;
   }
   return t;
 }
@@ -351,19 +471,21 @@ __device__ __forceinline__ void find_bin(FilterShared& sh, const FilterLists& ls
       pre += v[i];
     }
   }
-  __syncthreads();
+  cta_sync();
 }
 
 // CTA 0 of a row whose kept columns are all among the L listed ones: the cut and the draw
 // in linear time, by bins of the value (from the largest on) and of the column, with all
 // pairs compared within one bin only.  Weights are integers here (2^kListBits for the
 // largest), sums exact.
-//  k: columns kept at most; p: share of the weight (above 1: all); whole: the row's weight,
+//  k: columns kept at most; share: of the weight (above 1: all); whole: the row's weight,
 //  or -1: that of the first k.
-template <bool kVerify>
+//  kCutOnly: the listed columns follow others, of weight `above` in all, that are kept; the last
+//  kept column goes to every CTA's sh.cut_key and sh.cut_tie.
+template <bool kVerify, bool kCutOnly>
 __device__ __forceinline__ void resolve_list(const FilterParams& p, FilterShared& sh, FilterLists& ls, const Scale& sc, int row,
                                              int L, uint32_t low, uint32_t top, int k, double share, double whole, float floor,
-                                             float T, float u, bool draws, int draft) {
+                                             float T, float u, bool draws, int draft, int C, unsigned long long above) {
   constexpr int kPer = kListCap / kFT;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   unsigned long long key[kPer], w[kPer];
@@ -376,14 +498,14 @@ __device__ __forceinline__ void resolve_list(const FilterParams& p, FilterShared
     keep[h] = i < L;
     key[h] = w[h] = bin[h] = 0;
     if (keep[h]) {
-      key[h] = ls.key[i];
+      key[h] = sh.list[i];
       w[h] = fixed_weight(weight(sc, sh.table, key_value(key_of(key[h]))), kListBits);
       bin[h] = min((uint32_t)((float)(top - key_of(key[h])) * per_bin), (uint32_t)kListBins - 1);
     }
   }
   auto clear = [&]() {
     if (tid < kListBins) ls.mass[tid] = 0, ls.count[tid] = 0;
-    __syncthreads();
+    cta_sync();
   };
   auto select = [&](bool in, int h) {
     if (in) {
@@ -398,11 +520,11 @@ __device__ __forceinline__ void resolve_list(const FilterParams& p, FilterShared
 #pragma unroll
     for (int h = 0; h < kPer; ++h)
       if (keep[h]) atomicAdd(&ls.count[bin[h]], 1u);
-    __syncthreads();
+    cta_sync();
     find_bin<true>(sh, ls, (unsigned long long)k);
 #pragma unroll
     for (int h = 0; h < kPer; ++h) select(keep[h] && bin[h] == sh.bin, h);
-    __syncthreads();
+    cta_sync();
     const int n = (int)sh.in_bin;
 #pragma unroll
     for (int h = 0; h < kPer; ++h) {
@@ -413,14 +535,14 @@ __device__ __forceinline__ void resolve_list(const FilterParams& p, FilterShared
         keep[h] = bin[h] == sh.bin && r < (uint32_t)k;
       }
     }
-    __syncthreads();
+    cta_sync();
   }
   if (share <= 1.0) {  // the smallest prefix that holds its share
     clear();
 #pragma unroll
     for (int h = 0; h < kPer; ++h)
       if (keep[h]) atomicAdd(&ls.mass[bin[h]], w[h]);
-    __syncthreads();
+    cta_sync();
     if (whole < 0.0) {
       if (tid < 32) {
         unsigned long long v = 0;
@@ -429,15 +551,16 @@ __device__ __forceinline__ void resolve_list(const FilterParams& p, FilterShared
         v = warp_sum_u64(v);
         if (lane == 0) sh.total = v;
       }
-      __syncthreads();
+      cta_sync();
       whole = (double)sh.total;
     }
     // (a sum is below the real target exactly when it is below the next integer; 1: the first column alone)
-    const unsigned long long target = max((unsigned long long)ceil(share * whole), 1ull);
+    unsigned long long target = max((unsigned long long)ceil(share * whole), 1ull);
+    if (kCutOnly) target = max((long long)(target - above), 1ll);
     find_bin<false>(sh, ls, target);
 #pragma unroll
     for (int h = 0; h < kPer; ++h) select(keep[h] && bin[h] == sh.bin, h);
-    __syncthreads();
+    cta_sync();
     const int n = (int)sh.in_bin;
 #pragma unroll
     for (int h = 0; h < kPer; ++h) {
@@ -449,12 +572,28 @@ __device__ __forceinline__ void resolve_list(const FilterParams& p, FilterShared
         keep[h] = bin[h] == sh.bin && before < target;
       }
     }
-    __syncthreads();
+    cta_sync();
+  }
+
+  unsigned long long least = ~0ull;
+  if (kCutOnly) {
+#pragma unroll
+    for (int h = 0; h < kPer; ++h)
+      if (keep[h]) least = min(least, key[h]);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) least = min(least, __shfl_xor_sync(0xffffffffu, least, o));
+    if (lane == 0) sh.warp_sum[warp] = least;
+    cta_sync();
+    if (tid < C) {
+      for (int x = 0; x < kFW; ++x) least = min(least, sh.warp_sum[x]);
+      *at_rank(&sh.cut_key, tid) = key_of(least);
+      *at_rank(&sh.cut_tie, tid) = (int)(0xffffffffu - (uint32_t)least);
+    }
+    return;
   }
 
   // what is kept, by bins of the column
   clear();
-  unsigned long long least = ~0ull;
   const float per_col = (float)kListBins / (float)p.V;
 #pragma unroll
   for (int h = 0; h < kPer; ++h) {
@@ -474,7 +613,7 @@ __device__ __forceinline__ void resolve_list(const FilterParams& p, FilterShared
       sh.px = draft >= 0 && draft < p.V ? 0.0 : -1.0;
     }
   }
-  __syncthreads();
+  cta_sync();
   if (tid < 32) {
     unsigned long long v = 0;
 #pragma unroll
@@ -482,14 +621,14 @@ __device__ __forceinline__ void resolve_list(const FilterParams& p, FilterShared
     v = warp_sum_u64(v);
     if (lane == 0) sh.total = v;
   }
-  __syncthreads();
+  cta_sync();
   const unsigned long long W = sh.total;
   if (draws) {
     const unsigned long long at = share_of(u, W);
     find_bin<false>(sh, ls, at + 1);
 #pragma unroll
     for (int h = 0; h < kPer; ++h) select(keep[h] && bin[h] == sh.bin, h);
-    __syncthreads();
+    cta_sync();
     const int n = (int)sh.in_bin;
 #pragma unroll
     for (int h = 0; h < kPer; ++h) {
@@ -527,7 +666,7 @@ __device__ __forceinline__ void resolve_list(const FilterParams& p, FilterShared
         }
       }
     }
-    __syncthreads();
+    cta_sync();
     if (tid == 0) {
       for (int x = 0; x < kFW; ++x) least = min(least, sh.warp_sum[x]);
       RowCut& c = p.cuts[row];
@@ -544,40 +683,91 @@ __device__ __forceinline__ void resolve_list(const FilterParams& p, FilterShared
 }
 
 template <int DT, bool kVerify>
-__global__ void __launch_bounds__(kFT, 2) filter_kernel(const FilterParams p) {
+__global__ void __launch_bounds__(kFT, 4) filter_kernel(const FilterParams p) {
   extern __shared__ __align__(128) unsigned char smem[];
   FilterShared& sh = *reinterpret_cast<FilterShared*>(smem);
-  FilterLists& ls = *reinterpret_cast<FilterLists*>(smem + ((sizeof(FilterShared) + 127) & ~(size_t)127));
-  uint4* data = reinterpret_cast<uint4*>(reinterpret_cast<unsigned char*>(&ls) + sizeof(FilterLists));
+  unsigned char* room = smem + ((sizeof(FilterShared) + 127) & ~(size_t)127);
+  FilterLists& ls = *reinterpret_cast<FilterLists*>(room);
+  uint4* data = reinterpret_cast<uint4*>(room);
   using E = Elt<DT>;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = (int)cluster_rank();
   const int row = blockIdx.x / p.C;
 
-  // ---- which row, which parameters (the same in every CTA of the cluster)
+  // ---- which row
   const char* src;
   int ask, draft = 0;
   bool draws = true, ok = true;
   if (kVerify) {
     if (row < p.na) {
       ask = row / (p.Kp + 1);
-      const int j = row - ask * (p.Kp + 1);
-      draws = j == p.Kp;
+      draws = row - ask * (p.Kp + 1) == p.Kp;
       src = p.rows_a + (long long)row * p.a_bytes;
-      if (!draws) draft = __ldg(p.tokens + row + 1);
     } else {
       const int r = row - p.na;
       ask = r / p.Kp;
       draws = false;
       src = p.rows_b + (long long)r * p.b_bytes;
-      draft = __ldg(p.tokens + ask * (p.Kp + 1) + (r - ask * p.Kp) + 1);
     }
   } else {
     ask = row / p.per;
     const int i = p.sample_idx ? __ldg(p.sample_idx + row) : row;
     ok = i >= 0 && i < p.src_rows;
-    if (!ok && rank == 0 && tid == 0) atomicOr(p.err, PE_ERR_ROW_RANGE);
     src = p.rows_a + (long long)(ok ? i : 0) * p.a_bytes;
+  }
+
+  // ---- its slice is on the way before anything else is looked at
+  Slice<DT> s;
+  s.v = data;
+  s.lane = lane;
+  s.warp = warp;
+  s.rank = rank;
+  s.C = p.C;
+  s.sh = &sh;
+  s.turn = 0;
+  const int v0 = rank * p.per_cta;
+  s.n = max(0, min(p.per_cta, p.nvec - v0));
+  s.lo = min(s.n, warp * p.seg);
+  s.hi = min(s.n, s.lo + p.seg);
+  s.col0 = v0 * E::kN;
+  uint32_t phase = 0;
+  auto start_load = [&]() {
+    if (lane == 0) {
+      const int whole = min(s.hi, p.V / E::kN - v0);  // vectors that lie in the row as a whole
+      const int bytes = max(0, whole - s.lo) * 16;
+      mbar_arrive_expect_tx(&sh.bars[warp], bytes);
+      if (bytes) bulk_load(data + s.lo, src + (long long)(v0 + s.lo) * 16, bytes, &sh.bars[warp]);
+    }
+  };
+  const int part = p.V % E::kN;
+  auto finish_load = [&]() {
+    // the row's last columns, where they do not fill a vector
+    if (part && s.hi > s.lo && v0 + s.hi == p.nvec && lane < E::kN) {
+      const int col = (p.nvec - 1) * E::kN + lane;
+      const float x = lane < part ? E::load(src, col) : -INFINITY;
+      if (DT == PE_BF16)
+        reinterpret_cast<unsigned short*>(data + s.hi - 1)[lane] = (unsigned short)(__float_as_uint(x) >> 16);
+      else
+        reinterpret_cast<float*>(data + s.hi - 1)[lane] = x;
+    }
+    if (!mbar_wait(&sh.bars[warp], phase)) {
+      if (lane == 0) atomicOr(p.err, PE_ERR_TIMEOUT);
+      (void)mbar_wait(&sh.bars[warp], phase);
+    }
+    phase ^= 1u;
+    __syncwarp();
+  };
+  if (lane == 0) {
+    mbar_init(&sh.bars[warp], 1);
+    mbar_init_fence();
+  }
+  start_load();
+
+  // ---- which parameters (the same in every CTA of the cluster)
+  if (!ok && rank == 0 && tid == 0) atomicOr(p.err, PE_ERR_ROW_RANGE);
+  if (kVerify) {
+    if (row >= p.na) draft = __ldg(p.tokens + ask * (p.Kp + 1) + (row - p.na - ask * p.Kp) + 1);
+    else if (!draws) draft = __ldg(p.tokens + row + 1);
   }
   Asked a;
   if (!read_asked(p.asked, ask, p.V, a)) {
@@ -606,57 +796,21 @@ __global__ void __launch_bounds__(kFT, 2) filter_kernel(const FilterParams p) {
       if (p.out_prob) p.out_prob[row] = 0.f;
     }
   };
-  if (!ok) {
-    none(-1.0);
-    return;
-  }
-
-  // ---- load
-  Slice<DT> s;
-  s.v = data;
-  s.lane = lane;
-  s.warp = warp;
-  s.rank = rank;
-  s.C = p.C;
-  s.sh = &sh;
-  s.turn = 0;
-  const int v0 = rank * p.per_cta;
-  s.n = max(0, min(p.per_cta, p.nvec - v0));
-  s.lo = min(s.n, warp * p.seg);
-  s.hi = min(s.n, s.lo + p.seg);
-  s.col0 = v0 * E::kN;
-  if (lane == 0) {
-    mbar_init(&sh.bars[warp], 1);
-    mbar_init_fence();
-    const int whole = min(s.hi, p.V / E::kN - v0);  // vectors that lie in the row as a whole
-    const int bytes = max(0, whole - s.lo) * 16;
-    mbar_arrive_expect_tx(&sh.bars[warp], bytes);
-    if (bytes) bulk_load(data + s.lo, src + (long long)(v0 + s.lo) * 16, bytes, &sh.bars[warp]);
-  }
   if (tid == 0) {
     sh.listed = 0;
     sh.own = 0;
-    sh.rates = make_rates(a.T, a.m);
   }
   if (tid < 32) sh.table[tid] = kExp2Table[tid];
+  sh.hist[tid] = 0;
+  if (tid == 32) sh.rates = make_rates(a.T, a.m);
   __syncwarp();
-  __syncthreads();
   cluster_arrive();
-  // the row's last columns, where they do not fill a vector
-  const int part = p.V % E::kN;
-  if (part && s.hi > s.lo && v0 + s.hi == p.nvec && lane < E::kN) {
-    const int col = (p.nvec - 1) * E::kN + lane;
-    const float x = lane < part ? E::load(src, col) : -INFINITY;
-    if (DT == PE_BF16)
-      reinterpret_cast<unsigned short*>(data + s.hi - 1)[lane] = (unsigned short)(__float_as_uint(x) >> 16);
-    else
-      reinterpret_cast<float*>(data + s.hi - 1)[lane] = x;
+  finish_load();
+  if (!ok) {  // (not before its copies have landed)
+    cluster_wait();
+    none(-1.0);
+    return;
   }
-  if (!mbar_wait(&sh.bars[warp], 0)) {
-    if (lane == 0) atomicOr(p.err, PE_ERR_TIMEOUT);
-    (void)mbar_wait(&sh.bars[warp], 0);
-  }
-  __syncwarp();
 
   // ---- maxima
   float tmax = -INFINITY;
@@ -664,73 +818,72 @@ __global__ void __launch_bounds__(kFT, 2) filter_kernel(const FilterParams p) {
   const uint32_t mine = ordered_bits(tmax);
   const uint32_t wmax = __reduce_max_sync(0xffffffffu, mine);
   if (lane == 0) sh.warp_count[warp] = wmax;
-  const bool small_k = a.k <= kListK && a.k < p.V;
-  const bool nucleus = !small_k && a.k == p.V && a.p < 1.f;
-  uint32_t bound = 0;
-  if (small_k) bound = kth_prefix(mine >> 16, a.k);
-  __syncthreads();
-  cluster_wait();  // every CTA has started
-  if (tid < p.C) {
-    uint32_t m = 0;
-    for (int w = 0; w < kFW; ++w) m = max(m, sh.warp_count[w]);
-    *at_rank(&sh.maxima[rank], tid) = m;
-    *at_rank(&sh.bounds[rank], tid) = bound;
-  }
-  cluster_sync();
+  cta_sync();
   uint32_t top = 0;
-  for (int r = 0; r < p.C; ++r) {
-    top = max(top, sh.maxima[r]);
-    bound = max(bound, sh.bounds[r]);
+#pragma unroll
+  for (int w = 0; w < kFW; ++w) top = max(top, sh.warp_count[w]);
+  const bool small_k = a.k <= kListK && a.k < p.V;
+  const bool nucleus = a.k == p.V && a.p < 1.f;
+  // every CTA's own first k columns, where that makes a short list
+  bool local = small_k && a.k * p.C <= kListCap / 2;
+  uint32_t bound = 0, fair = 0;
+  if (small_k) {
+    bound = kth_prefix(sh.hist, mine >> 16, top >> 16, (uint32_t)a.k);
+    if (!local) fair = kth_prefix(sh.hist, mine >> 16, top >> 16, (uint32_t)(a.k + p.C - 1) / p.C);
   }
-  const float M = key_value(top);
-  if (M == -INFINITY) {
+  cluster_wait();  // every CTA has started
+  if (!local) {
+    if (tid < p.C) {
+      *at_rank(&sh.maxima[rank], tid) = top;
+      *at_rank(&sh.bounds[rank], tid) = bound;
+      *at_rank(&sh.shares[rank], tid) = fair;
+    }
+    cluster_sync();
+    // k columns lie from the largest of the bounds on, and from the smallest of the CTAs' shares on
+    for (int r = 0; r < p.C; ++r) {
+      top = max(top, sh.maxima[r]);
+      bound = max(bound, sh.bounds[r]);
+      fair = min(fair, sh.shares[r]);
+    }
+    bound = max(bound, fair);
+  }
+  float M = key_value(top);  // local: of this CTA's columns only
+  auto empty = [&]() {
     if (rank == 0 && tid == 0) atomicOr(p.err, PE_ERR_EMPTY_ROW);
     none(0.0);
-    return;
-  }
-  const Scale sc = make_scale(M, sh.rates);
-  float floor = -INFINITY;
-  if (a.m > 0.f) {
-    if (tid == 0) sh.floor = min_p_floor(a, sh.rates, M);
-    __syncthreads();
-    floor = sh.floor;
-  }
-  const double p_mass = a.p > 0.f ? (double)a.p : 0.0;  // at most the whole: >= 1 is off
-
-  auto answer = [&](int token, double w, double W) {  // one thread
-    if (kVerify) {
-      p.cuts[row].token = token;
-    } else {
-      p.out_tokens[row] = token;
-      if (p.out_prob) p.out_prob[row] = (float)(w / W);
-    }
   };
+  if (!local && M == -INFINITY) return empty();
+  const float p_mass = a.p > 0.f ? a.p : 0.f;
 
-  // ---- candidates: a value that every kept column reaches
-  const bool by_min = a.k == p.V && a.p >= 1.f && floor > -INFINITY;
-  unsigned long long Z = 0;  // the whole row's weight (top-p alone)
-  if (small_k || nucleus || by_min) {
-    uint32_t low = value_key(floor);
-    if (small_k) {
-      low = max(low, bound << 16);
-    } else if (nucleus) {
-      unsigned long long sum = s.mass(sc, ls.queue[warp]);
-      uint32_t c = 0;
-      s.exchange(c, sum);
-      Z = sum;
-      // The last kept column and those after it weigh more than (1 - p) Z and are at most
-      // V, so it weighs more than (1 - p) Z / V: 2^-20 of itself and 2^-20 of M and the distance
-      // less, for this estimate's roundings.
-      const float octaves = log2f((float)(1.0 - p_mass) * ((float)sum * 0x1p-44f) / (float)p.V);
-      const float away = octaves / sc.ch;
-      low = max(low, M == INFINITY ? top : value_key(M + away - 0x1p-20f * (fabsf(M) + fabsf(away)) - 0x1p-18f / sc.ch));
-    }
+  // the floor of min-p, once M is the row's
+  auto floor_of = [&]() -> float {
+    if (!(a.m > 0.f)) return -INFINITY;
+    if (tid == 0) sh.floor = min_p_floor(a, sh.rates, M);
+    cta_sync();
+    return sh.floor;
+  };
+  float floor = local ? -INFINITY : floor_of();
+  Scale sc = make_scale(M, sh.rates);
+
+  Cut cut;
+  cut.key = 0;
+  cut.tie = INT32_MAX;
+  cut.floor = -INFINITY;  // (min-p comes last: the others' shares are of columns below its floor too)
+
+  // Gather the columns with keys in [low, high] that the cut so far keeps into CTA 0's
+  // list; their number.
+  auto gather = [&](uint32_t low, uint32_t high) -> int {
     uint32_t mine_n = 0;
     if (mine >= low) {
       for (int i = s.lo + lane; i < s.hi; i += 32) {
         const uint4 q = s.v[i];
+        if (value_key(E::max_of(q)) < low) continue;
 #pragma unroll
-        for (int e = 0; e < E::kN; ++e) mine_n += value_key(E::get(q, e)) >= low && s.col0 + i * E::kN + e < p.V;
+        for (int e = 0; e < E::kN; ++e) {
+          const uint32_t k = value_key(E::get(q, e));
+          const int col = s.col0 + i * E::kN + e;
+          mine_n += k >= low && k <= high && col < p.V && (k != cut.key || col <= cut.tie);
+        }
       }
     }
     uint32_t pre = mine_n;
@@ -740,85 +893,181 @@ __global__ void __launch_bounds__(kFT, 2) filter_kernel(const FilterParams p) {
       if (lane >= o) pre += x;
     }
     const uint32_t warp_n = __shfl_sync(0xffffffffu, pre, 31);
-    uint32_t base = 0;
+    uint32_t base = 0, most = kListCap;
     if (warp_n && lane == 0) {
-      atomicAdd(&sh.own, warp_n);
-      base = atomicAdd(at_rank(&sh.listed, 0), warp_n);
+      base = atomicAdd(&sh.own, warp_n);
+      if (!local) base = atomicAdd(at_rank(&sh.listed, 0), warp_n);
     }
     base = __shfl_sync(0xffffffffu, base, 0) + pre - mine_n;
+    if (local) {  // each CTA has its part of the list
+      most = (uint32_t)(rank + 1) * (kListCap / p.C);
+      base += (uint32_t)rank * (kListCap / p.C);
+    }
     if (mine_n) {
-      unsigned long long* list = at_rank(ls.key, 0);
+      unsigned long long* list = at_rank(sh.list, 0);
       for (int i = s.lo + lane; i < s.hi; i += 32) {
         const uint4 q = s.v[i];
+        if (value_key(E::max_of(q)) < low) continue;
 #pragma unroll
         for (int e = 0; e < E::kN; ++e) {
           const uint32_t k = value_key(E::get(q, e));
           const int col = s.col0 + i * E::kN + e;
-          if (k >= low && col < p.V) {
-            if (base < kListCap) list[base] = ((unsigned long long)k << 32) | (0xffffffffu - (uint32_t)col);
+          if (k >= low && k <= high && col < p.V && (k != cut.key || col <= cut.tie)) {
+            if (base < most) list[base] = ((unsigned long long)k << 32) | (0xffffffffu - (uint32_t)col);
             ++base;
           }
         }
       }
     }
-    __syncthreads();
-    if (tid < p.C) *at_rank(&sh.counts[s.turn & 1][rank], tid) = sh.own;
+    cta_sync();
+    if (tid < p.C) {
+      *at_rank(&sh.counts[s.turn & 1][rank], tid) = sh.own;
+      if (local) *at_rank(&sh.maxima[rank], tid) = top;
+    }
     cluster_sync();
     int L = 0;
-    for (int r = 0; r < p.C; ++r) L += (int)min(sh.counts[s.turn & 1][r], 1u << 20);
+    for (int r = 0; r < p.C; ++r) {
+      const uint32_t n = sh.counts[s.turn & 1][r];
+      L += (int)min(n, 1u << 20);
+      if (local && n > (uint32_t)(kListCap / p.C)) L = 1 << 20;
+    }
     ++s.turn;
+    return min(L, 1 << 20);
+  };
+
+  // ---- rows whose kept columns all reach a known value: a list
+  unsigned long long Z = 0;  // the whole row's weight (top-p alone)
+  float octaves = 0.f;       // how far below M the cut lies at most
+  const bool by_min = a.k == p.V && a.p >= 1.f && floor > -INFINITY;
+  if (small_k || nucleus || by_min) {
+    uint32_t low = small_k ? bound << 16 : value_key(floor);
+    if (nucleus) {
+      Z = s.mass(sc, sh.queue[warp]);
+      uint32_t c = 0;
+      s.exchange(c, Z);
+      // The last kept column and those after it weigh more than (1 - p) Z and are at most
+      // V, so it weighs more than (1 - p) Z / V (and a little less, for this estimate's roundings).
+      octaves = 0x1p-16f - log2f((1.f - p_mass) * ((float)Z * 0x1p-44f) / (float)p.V);
+      const float away = octaves / sc.ch;
+      low = max(low, M == INFINITY ? top : value_key(M - away - 0x1p-20f * (fabsf(M) + away)));
+    }
+    int L = gather(low, 0xffffffffu);
+    if (local) {
+      for (int r = 0; r < p.C; ++r) top = max(top, sh.maxima[r]);
+      M = key_value(top);
+      if (M == -INFINITY) return empty();
+      sc = make_scale(M, sh.rates);
+    }
     if (L <= kListCap) {
-      if (rank == 0)
-        resolve_list<kVerify>(p, sh, ls, sc, row, L, low, top, small_k ? a.k : p.V,
-                              a.p < 1.f ? p_mass : 2.0, nucleus ? (double)Z * (1ull << (kListBits - kSumBits)) : -1.0, floor, a.T, u,
-                              draws, draft);
+      if (rank == 0) {
+        if (local) {
+          floor = floor_of();
+          // (the parts of the list closed up)
+          unsigned long long k[kListCap / kFT];
+          int at[kListCap / kFT];
+          const int region = kListCap / p.C;
+#pragma unroll
+          for (int h = 0; h < kListCap / kFT; ++h) {
+            const int i = tid + h * kFT, r = i / region;
+            at[h] = -1;
+            if (r < p.C && i - r * region < (int)sh.counts[(s.turn - 1) & 1][r]) {
+              at[h] = i - r * region;
+              for (int x = 0; x < r; ++x) at[h] += (int)sh.counts[(s.turn - 1) & 1][x];
+              k[h] = sh.list[i];
+            }
+          }
+          cta_sync();
+#pragma unroll
+          for (int h = 0; h < kListCap / kFT; ++h)
+            if (at[h] >= 0) sh.list[at[h]] = k[h];
+        }
+        cta_sync();
+        resolve_list<kVerify, false>(p, sh, ls, sc, row, L, low, top, small_k ? a.k : p.V, a.p < 1.f ? (double)p_mass : 2.0,
+                                     nucleus ? (double)Z * (1ull << (kListBits - kSumBits)) : -1.0, floor, a.T, u, draws, draft,
+                                     p.C, 0ull);
+      }
       return;
     }
+    if (local) floor = floor_of();
+    local = false;
   }
 
-  // ---- the cut, over the whole row
-  Cut cut;
-  cut.key = 0;
-  cut.tie = INT32_MAX;
-  cut.floor = floor;
-  uint32_t ties = 0;  // of the cut's value, that are kept
-  if (a.k < p.V) {
+  // ---- the cut, over the whole row: a histogram shows between which values it lies, what is
+  // above is added up, and a list of the columns between them decides
+  auto refine = [&](bool by_count, float range, double target, int k, double whole) -> bool {
+    if (M == INFINITY) return false;
+    float lo_x, hi_x;
+    const bool found = by_count ? s.template steer<false>(sc, cut, range, target, sh.steps, lo_x, hi_x)
+                                : s.template steer<true>(sc, cut, range, target, sh.steps, lo_x, hi_x);
+    if (!found) return false;
+    if (tid == 0) {
+      sh.own = 0;
+      if (rank == 0) sh.listed = 0;
+    }
+    uint32_t n = 0;
+    unsigned long long sum = 0;
+    const uint32_t high = hi_x == INFINITY ? 0xffffffffu : value_key(hi_x);
+    if (high != 0xffffffffu) {  // (what the cut so far leaves out is below)
+      if (by_count) s.template above<false>(sc, high, n, sum);
+      else s.template above<true>(sc, high, n, sum);
+    } else {
+      cluster_sync();
+    }
+    const uint32_t low = value_key(lo_x);
+    const int L = gather(low, high - 1);
+    if (L == 0 || L > kListCap) return false;
+    if (rank == 0)
+      resolve_list<kVerify, true>(p, sh, ls, sc, row, L, low, min(high - 1, top), by_count ? k - (int)n : p.V, by_count ? 2.0 : (double)p_mass,
+                                  whole, floor, a.T, u, draws, draft, p.C, sum << (kListBits - kSumBits));
+    cluster_sync();
+    if (rank == 0) {  // its slice again: the list's bins took its place
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      cta_sync();
+      start_load();
+      finish_load();
+    }
+    cut.key = sh.cut_key;
+    cut.tie = sh.cut_tie;
+    return true;
+  };
+  if (a.k < p.V && !refine(true, 63.f, (double)a.k, a.k, -1.0)) {
     cut.key = s.template search<false>(sc, (uint32_t)a.k, 0.0);
     uint32_t c = 0;
     unsigned long long sum;
     if (cut.key != 0xffffffffu) s.template above<false>(sc, cut.key + 1, c, sum);
-    ties = (uint32_t)a.k - c;
+    cut.tie = s.nth_tie(cut.key, (uint32_t)a.k - c);
   }
   if (a.p < 1.f) {
     uint32_t c = 0;
-    unsigned long long sum = 0;
-    const uint32_t key_k = cut.key;
-    double Z;
+    unsigned long long sum = Z;
     if (a.k < p.V) {
-      s.template above<true>(sc, key_k + 1, c, sum);
-      const float2 w = weight(sc, sh.table, key_value(key_k));
-      Z = (double)sum + (double)ties * ((double)w.x + (double)w.y) * (double)(1ull << kSumBits);
-    } else {
-      s.template above<true>(sc, 0u, c, sum);
-      Z = (double)sum;
+      sum = s.kept_mass(sc, cut);
+      s.exchange(c, sum);
+      octaves = 0x1p-16f - log2f((1.f - p_mass) * ((float)sum * 0x1p-44f) / (float)a.k);
     }
-    const double target = p_mass * Z;
-    uint32_t key_p = s.template search<true>(sc, 0u, target);
-    if (target <= 0.0) key_p = top;  // the first column alone
-    if (key_p < key_k) key_p = key_k;
-    s.template above<true>(sc, key_p + 1, c, sum);
-    const float2 w = weight(sc, sh.table, key_value(key_p));
-    const double one = ((double)w.x + (double)w.y) * (double)(1ull << kSumBits);
-    double need = ceil((target - (double)sum) / one);
-    if (!(need >= 1.0)) need = 1.0;
-    uint32_t r = need < 4e9 ? (uint32_t)need : 0xffffffffu;
-    if (a.k < p.V && key_p == key_k) r = min(r, ties);
-    cut.key = key_p;
-    ties = r;
+    const double whole = (double)sum;
+    if (!refine(false, fminf(octaves + 0x1p-8f, 63.f), fmax((double)p_mass * whole * 0x1p-44, 0x1p-40), 0,
+                whole * (1ull << (kListBits - kSumBits)))) {
+      const uint32_t key_k = cut.key;
+      const int tie_k = cut.tie;
+      const double target = (double)p_mass * whole;
+      uint32_t key_p = s.template search<true>(sc, 0u, target);
+      if (target <= 0.0) key_p = top;  // the first column alone
+      if (key_p < key_k) key_p = key_k;
+      s.template above<true>(sc, key_p + 1, c, sum);
+      const float2 w = weight(sc, sh.table, key_value(key_p));
+      const double one = ((double)w.x + (double)w.y) * (double)(1ull << kSumBits);
+      double need = ceil((target - (double)sum) / one);
+      if (!(need >= 1.0)) need = 1.0;
+      cut.key = key_p;
+      cut.tie = s.nth_tie(key_p, need < 4e9 ? (uint32_t)need : 0xffffffffu);
+      if (key_p == key_k) cut.tie = min(cut.tie, tie_k);
+    }
   }
-  if (a.k < p.V || a.p < 1.f) cut.tie = s.nth_tie(cut.key, ties);
+
 
   // ---- the kept weight, and the draw
+  cut.floor = floor;
   uint32_t c = 0;
   unsigned long long sum, before = 0;
   uint32_t c_before = 0;
@@ -833,9 +1082,21 @@ __global__ void __launch_bounds__(kFT, 2) filter_kernel(const FilterParams p) {
       }
     }
   };
-  WeightSum<256> ws;
-  for (int i = s.lo + lane; i < s.hi; i += 32) kept(i, 0, E::kN, ws);
-  const unsigned long long mine_w = warp_sum_u64(ws.fixed(kSumBits));
+  unsigned long long mine_w;
+  if (cut.key == 0 && floor == -INFINITY) {  // every column
+    WeightSum<256> ws;
+    for (int i = s.lo + lane; i < s.hi; i += 32) {
+      const uint4 q = s.v[i];
+#pragma unroll
+      for (int e = 0; e < E::kN; ++e) {
+        const float2 w = weight(sc, sh.table, E::get(q, e));
+        ws.add(w.x, w.y);
+      }
+    }
+    mine_w = warp_sum_u64(ws.fixed(kSumBits));
+  } else {
+    mine_w = s.kept_mass(sc, cut);
+  }
   sum = mine_w;
   s.exchange(c, sum, &before, &c_before);
   if (kVerify && rank == 0 && tid == 0) {
@@ -863,13 +1124,21 @@ __global__ void __launch_bounds__(kFT, 2) filter_kernel(const FilterParams p) {
       const int i = find_column<E::kN, 256>(s.lo, s.hi, lane, at - before, kSumBits, kept);
       if (lane == 0) {
         const int col = s.col0 + i;
-        const float2 w = weight(sc, sh.table, E::load(src, col));
-        answer(col, ((double)w.x + (double)w.y) * (double)(1ull << kSumBits), (double)sum);
+        if (kVerify) {
+          p.cuts[row].token = col;
+        } else {
+          p.out_tokens[row] = col;
+          if (p.out_prob) p.out_prob[row] = (float)((double)fixed_weight(weight(sc, sh.table, E::load(src, col)), kListBits) /
+                                                    ((double)sum * (1ull << (kListBits - kSumBits))));
+        }
       }
     }
   }
 }
 
+}  // namespace pe
+
+namespace pe {
 
 // --------------------------------------------------------- the bonus token
 template <int DT>
@@ -906,7 +1175,7 @@ __global__ void __launch_bounds__(kFT) residual_kernel(const FilterParams p) {
   const int b = blockIdx.x / p.C;
   if (tid < 32) sh.table[tid] = kExp2Table[tid];
   if (tid == 0) sh.total = 0;
-  __syncthreads();
+  cta_sync();
   cluster_arrive();
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const RowCut* target = p.cuts + (long long)b * (p.Kp + 1);
@@ -936,7 +1205,7 @@ __global__ void __launch_bounds__(kFT) residual_kernel(const FilterParams p) {
       if (!bad && a < p.Kp && t.W > 0.0) sh.rates = make_rates(t.T, 0.f);
     }
   }
-  __syncthreads();
+  cta_sync();
   const int a = sh.first;
   const RowCut& t = target[a];
   const bool stream = t.listed < 0;
@@ -976,21 +1245,21 @@ __global__ void __launch_bounds__(kFT) residual_kernel(const FilterParams p) {
     }
     const unsigned long long part = warp_sum_u64(mine);
     if (lane == 0 && part) atomicAdd(&sh.total, part);
-    __syncthreads();
+    cta_sync();
     unsigned long long R = sh.total;
-    __syncthreads();
+    cta_sync();
     if (R == 0) {
       mine = whole;
       const unsigned long long all = warp_sum_u64(mine);
       if (lane == 0 && all) atomicAdd(&sh.total, all);
-      __syncthreads();
+      cta_sync();
       R = sh.total;
     }
     if (tid < kKeptCap) {
       w[tid] = mine;
       cols[tid] = tid < L ? col : INT32_MAX;
     }
-    __syncthreads();
+    cta_sync();
     const unsigned long long at = share_of(u, R);
     if (mine) {
       unsigned long long upto = 0;
@@ -1016,7 +1285,7 @@ __global__ void __launch_bounds__(kFT) residual_kernel(const FilterParams p) {
     const float hi = (float)i;
     sh.inverse[tid] = make_float2(hi, (float)(i - (double)hi));
   }
-  __syncthreads();
+  cta_sync();
   const float ith = sh.inverse[0].x, itl = sh.inverse[0].y;
   const float idh = sh.inverse[1].x, idl = sh.inverse[1].y;
   bool from_p = false;
@@ -1069,8 +1338,8 @@ __global__ void __launch_bounds__(kFT) residual_kernel(const FilterParams p) {
 namespace {
 
 constexpr size_t kHeader = ((sizeof(pe::FilterShared) + 127) & ~(size_t)127);
-constexpr int kMaxSmem = 200 * 1024;
-constexpr int kRoomySlice = 80 * 1024;  // two CTAs per SM
+constexpr int kMaxSmem = (int)kHeader + 64 * 1024;
+constexpr int kRoomySlice = 52 * 1024;  // three CTAs and more on an SM
 
 struct FilteredLayout {
   size_t kept_off, bytes;
@@ -1088,7 +1357,7 @@ void split_rows(pe::FilterParams& p, int elt, int sms) {
   p.nvec = (p.V + epv - 1) / epv;
   p.C = 1;
   while (p.C < pe::kMaxCluster &&
-         (p.nvec * 16 / p.C > kRoomySlice || ((long long)p.n * p.C * 2 <= sms && p.nvec / p.C > 512)))
+         (p.nvec * 16 / p.C > kRoomySlice || ((long long)p.n * p.C * 2 <= sms && p.C < 8 && p.nvec / p.C > 512)))
     p.C *= 2;
   p.per_cta = (p.nvec + p.C - 1) / p.C;
   p.seg = (p.per_cta + pe::kFW - 1) / pe::kFW;
@@ -1097,8 +1366,11 @@ void split_rows(pe::FilterParams& p, int elt, int sms) {
 template <int DT, bool kVerify>
 int launch_filter(const pe::FilterParams& p, cudaStream_t st) {
   static std::atomic<unsigned long long> done{0};
-  if (!pe_host::allow_smem(pe::filter_kernel<DT, kVerify>, kMaxSmem, done)) return PE_ECUDA;
-  const size_t smem = kHeader + sizeof(pe::FilterLists) + (size_t)p.per_cta * 16;
+  auto kernel = pe::filter_kernel<DT, kVerify>;
+  if (p.C > 8 && cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) return PE_ECUDA;
+  if (!pe_host::allow_smem(kernel, kMaxSmem, done)) return PE_ECUDA;
+  const size_t slice = (size_t)p.per_cta * 16;
+  const size_t smem = kHeader + (slice > sizeof(pe::FilterLists) ? slice : sizeof(pe::FilterLists));
   return pe_host::launch_clusters(pe::filter_kernel<DT, kVerify>, p.n * p.C, pe::kFT, p.C, smem, false, st, p) == cudaSuccess ? PE_OK : PE_ECUDA;
 }
 
@@ -1108,6 +1380,11 @@ int launch_verify(pe::FilterParams p, int B, int elt, int sms, cudaStream_t st) 
   if (rc != PE_OK) return rc;
   p.n = B;
   split_rows(p, elt, sms);
+  if (p.C > 8) {
+    p.C = 8;
+    p.per_cta = (p.nvec + 7) / 8;
+    p.seg = (p.per_cta + pe::kFW - 1) / pe::kFW;
+  }
   const size_t smem = kHeader + 12 * pe::kKeptCap;
   return pe_host::launch_clusters(pe::residual_kernel<DT>, B * p.C, pe::kFT, p.C, smem, true, st, p) == cudaSuccess ? PE_OK : PE_ECUDA;
 }

@@ -51,9 +51,9 @@ __device__ __forceinline__ uint32_t block_prefix(uint32_t mine, uint32_t& total,
     const uint32_t x = __shfl_up_sync(0xffffffffu, pre, o);
     if (lane >= o) pre += x;
   }
-  __syncthreads();
+  cta_sync();
   if (lane == 31) sh.warp[warp] = pre;
-  __syncthreads();
+  cta_sync();
   uint32_t before = 0, all = 0;
   for (int w = 0; w < kEW; ++w) {
     const uint32_t x = sh.warp[w];
@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(kET) evict_kernel(const EvictParams p) {
       cluster_sync();  // every CTA has started
       for (int shift = 21, bits = 11;; ) {
         for (int i = tid; i < kBins; i += kET) sh.hist[i] = 0;
-        __syncthreads();
+        cta_sync();
         for (int j = k0 + tid; j < k1; j += kET) {
           const uint32_t k = mass_key(p.mass[slot_of(table, j)]);
           if ((k & mask) == value) atomicAdd(&sh.hist[(k >> shift) & ((1u << bits) - 1)], 1u);
@@ -277,7 +277,7 @@ extern "C" int pe_kv_evict(const pe_kv_evict_args* a, void* stream) {
   p.table = a->block_table, p.dst = a->dst_table, p.lengths = a->lengths, p.keep = a->keep;
   p.kept = a->kept, p.out_lengths = a->out_lengths, p.err = a->err;
   p.C = 1;
-  while (p.C < pe::kMaxCluster && (int64_t)a->B * a->Hkv * p.C * 2 <= 4 * dev.sm_count) p.C *= 2;
+  while (p.C < 8 && (int64_t)a->B * a->Hkv * p.C * 2 <= 4 * dev.sm_count) p.C *= 2;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const unsigned grid = (unsigned)(a->B * a->Hkv * p.C);
   const cudaError_t rc =

@@ -29,7 +29,7 @@ def vec(v, dt=FP):
 
 ASKS = [(1.0, 0, 1.0, 0.0), (0.7, 20, 0.8, 0.0), (0.0, 0, 1.0, 0.0), (0.8, 0, 0.95, 0.0), (1.3, 0, 1.0, 0.05),
         (0.9, 300, 0.9, 0.02), (1.0, 1, 1.0, 0.0), (2.0, 0, 0.999, 0.0), (1.0, 3, 0.0, 0.0), (1.0, 0, 1.0, 1.0),
-        (0.5, 257, 1.0, 0.0), (1.0, 0, 0.3, 0.5), (1e-6, 0, 1.0, 0.0), (1e6, 0, 0.5, 0.0), (1.0, 256, 2.0, -1.0)]
+        (0.5, 257, 1.0, 0.0), (1.0, 0, 0.3, 0.5), (1.4, 30, 0.97, 0.3), (3.0, 250, 0.9, 0.5), (3.0, 600, 0.95, 0.4), (1e-6, 0, 1.0, 0.0), (1e6, 0, 0.5, 0.0), (1.0, 256, 2.0, -1.0)]
 
 
 def asked(rows):
@@ -116,6 +116,20 @@ def test_flat_rows_with_every_column_kept():
     rows = [(1.0, 0, 1.0, 0.0), (1.0, 0, 0.9, 0.0), (1.0, 0, 0.99, 0.01), (1.0, 70000, 0.8, 0.0)] * 3
     tok, prob = sample(x, rows, u)
     assert check(x, rows, u.tolist(), tok, prob) >= n - 1
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_wide_cuts(dtype):
+    # cuts among thousands of columns, and lists longer than the kernel's
+    g = gen(7)
+    rows = [(1.0, 2000, 1.0, 0.0), (3.0, 0, 0.9, 0.0), (3.0, 0, 0.5, 0.2), (2.0, 30000, 0.8, 0.01), (1.0, 1000, 0.95, 0.0),
+            (1.0, 0, 0.9999, 0.0), (1.0, 0, 0.9999999, 0.0), (1.0, 50304, 0.999, 0.0), (50.0, 0, 1e-6, 0.0), (1.0, 1, 0.5, 0.0),
+            (0.01, 0, 0.99, 0.0), (1.0, 256, 0.999, 0.0), (1.0, 255, 1.0, 0.9)]
+    x = f.peaked(len(rows), 50304, g, dtype)
+    x[5, :40000] = 3.0  # a tie of most columns
+    u = torch.rand(len(rows), generator=g, device="cuda")
+    tok, prob = sample(x, rows, u)
+    assert check(x, rows, u.tolist(), tok, prob) >= len(rows) - 1
 
 
 def test_masked_infinite_and_nan_logits():
@@ -271,7 +285,7 @@ def test_verify_wide(V, dtype):
 
 
 def test_verify_the_same_rows_accepts_everything():
-    v = Verify(15, 4, 600, ASKS, 9, noise=0.0)
+    v = Verify(15, 4, 600, ASKS[:15], 9, noise=0.0)
     v.run()
     torch.cuda.synchronize()
     assert v.acc.tolist() == [4] * 15 and bool((v.chance == 1.0).all())
@@ -350,7 +364,7 @@ def test_verify_keeps_the_target_distribution():
 
 # -------------------------------------------------------------- streams, graphs
 def test_another_stream_and_graph_replay():
-    v = Verify(15, 3, 4099, ASKS, 23)
+    v = Verify(15, 3, 4099, ASKS[:15], 23)
     v.run()
     torch.cuda.synchronize()
     want = v.acc.clone(), v.bonus.clone(), v.chance.clone()
@@ -360,7 +374,7 @@ def test_another_stream_and_graph_replay():
     v.run(stream=s)
     s.synchronize()
     assert torch.equal(v.acc, want[0]) and torch.equal(v.bonus, want[1])
-    par, err = asked(ASKS), _native.new_error_word()
+    par, err = asked(ASKS[:15]), _native.new_error_word()
     tok = torch.empty(15 * 3, dtype=torch.int32, device="cuda")
     u = torch.rand(45, generator=gen(1), device="cuda")
     graph = torch.cuda.CUDAGraph()
