@@ -127,6 +127,11 @@ __device__ __forceinline__ unsigned long long fixed_weight(float2 w, int bits) {
 __device__ __forceinline__ unsigned long long share_of(float u, unsigned long long W) {
   return __umul64hi(__float2ull_rz(u * 0x1p64f), W);
 }
+// The smallest whole number that is at least u W, and at least 1
+__device__ __forceinline__ unsigned long long share_from(float u, unsigned long long W) {
+  const unsigned long long f = __float2ull_rz(u * 0x1p64f);
+  return max(__umul64hi(f, W) + (f * W != 0ull), 1ull);
+}
 constexpr int kSumBits = 44;   // row sums: up to 2^18 weights of at most 1
 constexpr int kListBits = 52;  // list sums: up to 2^10
 

@@ -58,7 +58,7 @@ struct FilterShared {
   uint32_t warp_count[kFW];
   uint32_t maxima[kMaxCluster], bounds[kMaxCluster], shares[kMaxCluster];
   unsigned long long total, above;
-  uint32_t listed, own, bin, in_bin, stored;
+  uint32_t own, bin, in_bin, stored;
   uint32_t cut_key;
   int cut_tie, tie;
   float2 table[32];
@@ -75,8 +75,9 @@ struct FilterShared {
   };
 };
 // In the place of CTA 0's slice, once the list holds all that is needed of it.
+constexpr int kPairs = kFT;  // columns of a list that is resolved by comparing all pairs
 struct FilterLists {
-  struct {  // the columns of one bin
+  struct {  // the columns of one bin (pairs: of the list)
     unsigned long long key[kListCap];
     unsigned long long w[kListCap];
   } sel;
@@ -474,18 +475,151 @@ __device__ __forceinline__ void find_bin(FilterShared& sh, const FilterLists& ls
   cta_sync();
 }
 
+// Where column i of a list lies: one after another, or each CTA's in its own part.
+struct ListMap {
+  int C;  // parts, or 0
+  int slot;
+  __device__ __forceinline__ int at(const FilterShared& sh, int i) const {
+    if (!C) return i;
+    int j = i, found = 0;
+    for (int r = 0; r < C; ++r) {
+      const int n = (int)sh.counts[slot][r];
+      if (j >= 0 && j < n) found = r * (kListCap / C) + j;
+      j -= n;
+    }
+    return found;
+  }
+};
+
+// What a row's answer needs of its kept columns, in CTA 0.
+template <bool kVerify>
+__device__ __forceinline__ void answer_draw(const FilterParams& p, int row, int col, unsigned long long w, unsigned long long W) {
+  if (kVerify) {
+    p.cuts[row].token = col;
+  } else {
+    p.out_tokens[row] = col;
+    if (p.out_prob) p.out_prob[row] = (float)((double)w / (double)W);
+  }
+}
+template <bool kVerify, int kPer>
+__device__ __forceinline__ void keep_record(const FilterParams& p, FilterShared& sh, const Scale& sc, int row, float T, int draft,
+                                            unsigned long long W, const bool (&keep)[kPer], const unsigned long long (&key)[kPer],
+                                            const unsigned long long (&w)[kPer]) {
+  const bool store = row < p.na;
+#pragma unroll
+  for (int h = 0; h < kPer; ++h) {
+    if (keep[h]) {
+      const int col = (int)(0xffffffffu - (uint32_t)key[h]);
+      if (col == draft) sh.px = (double)w[h] / (double)W;
+      if (store) {
+        const uint32_t at = atomicAdd(&sh.stored, 1u);
+        if (at < kKeptCap) {
+          Kept& o = p.kept[(long long)row * kKeptCap + at];
+          o.w = w[h];
+          o.col = col;
+        }
+      }
+    }
+  }
+  cta_sync();
+  if (threadIdx.x == 0) {
+    unsigned long long least = ~0ull;
+    for (int x = 0; x < kFW; ++x) least = min(least, sh.warp_sum[x]);
+    RowCut& c = p.cuts[row];
+    c.cut.key = key_of(least);
+    c.cut.tie = (int)(0xffffffffu - (uint32_t)least);
+    c.cut.floor = -INFINITY;
+    c.M = sc.M;
+    c.T = T;
+    c.listed = store && sh.stored <= kKeptCap ? (int)sh.stored : -1;
+    c.W = (double)W * (1.0 / (1ull << kListBits));
+    c.px = sh.px;
+  }
+}
+
+// A short list, one column a thread: ranks, preceding weights and running sums in column
+// order by comparing all pairs.  (Bins, as below, take fewer steps but more barriers, and
+// the row's CTAs wait: for some 170 columns 22,000 clocks against 6,000 here.)
+template <bool kVerify>
+__device__ __forceinline__ void resolve_pairs(const FilterParams& p, FilterShared& sh, FilterLists& ls, const Scale& sc, int row,
+                                              int L, ListMap map, int k, float share, unsigned long long whole, float floor, float T,
+                                              float u, bool draws, int draft) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  ulonglong2* pair = reinterpret_cast<ulonglong2*>(&ls);
+  unsigned long long key[1] = {0}, w[1] = {0};
+  bool keep[1] = {tid < L};
+  const bool on = 32 * warp < L;  // this warp has columns
+  if (on) {
+    if (keep[0]) {
+      key[0] = sh.list[map.at(sh, tid)];
+      w[0] = fixed_weight(weight(sc, sh.table, key_value(key_of(key[0]))), kListBits);
+    }
+    pair[tid] = make_ulonglong2(key[0], w[0]);
+  }
+  if (tid == 0) {
+    sh.above = 0;
+    if (kVerify) {
+      sh.stored = 0;
+      sh.px = draft >= 0 && draft < p.V ? 0.0 : -1.0;
+    }
+  }
+  cta_sync();
+  int rank = 0;
+  unsigned long long pre = 0;
+  if (on) {
+#pragma unroll 4
+    for (int j = 0; j < L; ++j) {
+      const ulonglong2 o = pair[j];
+      const bool first = o.x > key[0];
+      rank += first;
+      pre += first ? o.y : 0ull;
+    }
+    if (keep[0] && rank == min(k, L) - 1) sh.total = pre + w[0];
+  }
+  cta_sync();
+  if (on) {
+    if (keep[0] && share < 1.f)
+      keep[0] = whole ? (pre >> (kListBits - kSumBits)) < share_from(share, whole) : pre < share_from(share, sh.total);
+    keep[0] = keep[0] && rank < k && key_value(key_of(key[0])) >= floor;
+    if (!keep[0]) w[0] = 0;
+    pair[tid].y = w[0];
+    const unsigned long long sum = warp_sum_u64(w[0]);
+    if (lane == 0) atomicAdd(&sh.above, sum);
+  }
+  if (kVerify) {
+    unsigned long long least = keep[0] ? key[0] : ~0ull;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) least = min(least, __shfl_xor_sync(0xffffffffu, least, o));
+    if (lane == 0) sh.warp_sum[warp] = least;
+  }
+  cta_sync();
+  const unsigned long long W = sh.above;
+  if (draws && keep[0] && w[0]) {
+    const unsigned long long at = share_of(u, W);
+    const uint32_t inv = (uint32_t)key[0];  // larger: a lower column
+    unsigned long long upto = 0;
+#pragma unroll 4
+    for (int j = 0; j < L; ++j) {
+      const ulonglong2 o = pair[j];
+      upto += (uint32_t)o.x >= inv ? o.y : 0ull;
+    }
+    if (upto > at && upto - w[0] <= at) answer_draw<kVerify>(p, row, (int)(0xffffffffu - inv), w[0], W);
+  }
+  if (kVerify) keep_record<kVerify, 1>(p, sh, sc, row, T, draft, W, keep, key, w);
+}
+
 // CTA 0 of a row whose kept columns are all among the L listed ones: the cut and the draw
 // in linear time, by bins of the value (from the largest on) and of the column, with all
 // pairs compared within one bin only.  Weights are integers here (2^kListBits for the
 // largest), sums exact.
-//  k: columns kept at most; share: of the weight (above 1: all); whole: the row's weight,
-//  or -1: that of the first k.
-//  kCutOnly: the listed columns follow others, of weight `above` in all, that are kept; the last
+//  k: columns kept at most; share: of the weight (from 1 on: all); whole: the row's weight
+//  times 2^kSumBits, or 0: that of the first k.
+//  kCutOnly: the listed columns follow others, of weight `above` (as whole) in all, that are kept; the last
 //  kept column goes to every CTA's sh.cut_key and sh.cut_tie.
 template <bool kVerify, bool kCutOnly>
 __device__ __forceinline__ void resolve_list(const FilterParams& p, FilterShared& sh, FilterLists& ls, const Scale& sc, int row,
-                                             int L, uint32_t low, uint32_t top, int k, double share, double whole, float floor,
-                                             float T, float u, bool draws, int draft, int C, unsigned long long above) {
+                                             int L, ListMap map, uint32_t low, uint32_t top, int k, float share, unsigned long long whole,
+                                             float floor, float T, float u, bool draws, int draft, int C, unsigned long long above) {
   constexpr int kPer = kListCap / kFT;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   unsigned long long key[kPer], w[kPer];
@@ -498,7 +632,7 @@ __device__ __forceinline__ void resolve_list(const FilterParams& p, FilterShared
     keep[h] = i < L;
     key[h] = w[h] = bin[h] = 0;
     if (keep[h]) {
-      key[h] = sh.list[i];
+      key[h] = sh.list[map.at(sh, i)];
       w[h] = fixed_weight(weight(sc, sh.table, key_value(key_of(key[h]))), kListBits);
       bin[h] = min((uint32_t)((float)(top - key_of(key[h])) * per_bin), (uint32_t)kListBins - 1);
     }
@@ -537,13 +671,13 @@ __device__ __forceinline__ void resolve_list(const FilterParams& p, FilterShared
     }
     cta_sync();
   }
-  if (share <= 1.0) {  // the smallest prefix that holds its share
+  if (share < 1.f) {  // the smallest prefix that holds its share
     clear();
 #pragma unroll
     for (int h = 0; h < kPer; ++h)
       if (keep[h]) atomicAdd(&ls.mass[bin[h]], w[h]);
     cta_sync();
-    if (whole < 0.0) {
+    if (whole == 0) {
       if (tid < 32) {
         unsigned long long v = 0;
 #pragma unroll
@@ -552,11 +686,11 @@ __device__ __forceinline__ void resolve_list(const FilterParams& p, FilterShared
         if (lane == 0) sh.total = v;
       }
       cta_sync();
-      whole = (double)sh.total;
     }
-    // (a sum is below the real target exactly when it is below the next integer; 1: the first column alone)
-    unsigned long long target = max((unsigned long long)ceil(share * whole), 1ull);
-    if (kCutOnly) target = max((long long)(target - above), 1ll);
+    // (a sum of 2^kListBits is below the target exactly when it is below the next whole number)
+    unsigned long long target = share_from(share, whole ? whole : sh.total);
+    if (kCutOnly) target = target > above ? target - above : 1ull;
+    if (whole) target <<= kListBits - kSumBits;
     find_bin<false>(sh, ls, target);
 #pragma unroll
     for (int h = 0; h < kPer; ++h) select(keep[h] && bin[h] == sh.bin, h);
@@ -637,49 +771,11 @@ __device__ __forceinline__ void resolve_list(const FilterParams& p, FilterShared
         unsigned long long upto = sh.above;
         for (int j = 0; j < n; ++j)
           if ((uint32_t)ls.sel.key[j] >= inv) upto += ls.sel.w[j];
-        if (upto > at && upto - w[h] <= at) {
-          const int col = (int)(0xffffffffu - inv);
-          if (kVerify) {
-            p.cuts[row].token = col;
-          } else {
-            p.out_tokens[row] = col;
-            if (p.out_prob) p.out_prob[row] = (float)((double)w[h] / (double)W);
-          }
-        }
+        if (upto > at && upto - w[h] <= at) answer_draw<kVerify>(p, row, (int)(0xffffffffu - inv), w[h], W);
       }
     }
   }
-  if (kVerify) {
-    const bool store = row < p.na;
-#pragma unroll
-    for (int h = 0; h < kPer; ++h) {
-      if (keep[h]) {
-        const int col = (int)(0xffffffffu - (uint32_t)key[h]);
-        if (col == draft) sh.px = (double)w[h] / (double)W;
-        if (store) {
-          const uint32_t at = atomicAdd(&sh.stored, 1u);
-          if (at < kKeptCap) {
-            Kept& o = p.kept[(long long)row * kKeptCap + at];
-            o.w = w[h];
-            o.col = col;
-          }
-        }
-      }
-    }
-    cta_sync();
-    if (tid == 0) {
-      for (int x = 0; x < kFW; ++x) least = min(least, sh.warp_sum[x]);
-      RowCut& c = p.cuts[row];
-      c.cut.key = key_of(least);
-      c.cut.tie = (int)(0xffffffffu - (uint32_t)least);
-      c.cut.floor = -INFINITY;
-      c.M = sc.M;
-      c.T = T;
-      c.listed = store && sh.stored <= kKeptCap ? (int)sh.stored : -1;
-      c.W = (double)W * (1.0 / (1ull << kListBits));
-      c.px = sh.px;
-    }
-  }
+  if (kVerify) keep_record<kVerify, kPer>(p, sh, sc, row, T, draft, W, keep, key, w);
 }
 
 template <int DT, bool kVerify>
@@ -797,7 +893,6 @@ __global__ void __launch_bounds__(kFT, 4) filter_kernel(const FilterParams p) {
     }
   };
   if (tid == 0) {
-    sh.listed = 0;
     sh.own = 0;
   }
   if (tid < 32) sh.table[tid] = kExp2Table[tid];
@@ -828,24 +923,41 @@ __global__ void __launch_bounds__(kFT, 4) filter_kernel(const FilterParams p) {
   bool local = small_k && a.k * p.C <= kListCap / 2;
   uint32_t bound = 0, fair = 0;
   if (small_k) {
-    bound = kth_prefix(sh.hist, mine >> 16, top >> 16, (uint32_t)a.k);
+    bound = a.k == 1 ? top >> 16 : kth_prefix(sh.hist, mine >> 16, top >> 16, (uint32_t)a.k);
     if (!local) fair = kth_prefix(sh.hist, mine >> 16, top >> 16, (uint32_t)(a.k + p.C - 1) / p.C);
   }
+  const float p_mass = a.p > 0.f ? a.p : 0.f;
+  unsigned long long Z = 0;  // the whole row's weight (top-p alone)
+  if (nucleus) Z = s.mass(make_scale(key_value(top), sh.rates), sh.queue[warp]);
   cluster_wait();  // every CTA has started
   if (!local) {
+    const uint32_t own_top = top;
+    if (nucleus) {
+      if (lane == 0) sh.warp_sum[warp] = Z;
+      cta_sync();
+    }
     if (tid < p.C) {
-      *at_rank(&sh.maxima[rank], tid) = top;
-      *at_rank(&sh.bounds[rank], tid) = bound;
-      *at_rank(&sh.shares[rank], tid) = fair;
+      *at_rank(&sh.maxima[rank], tid) = own_top;
+      if (small_k) {
+        *at_rank(&sh.bounds[rank], tid) = bound;
+        *at_rank(&sh.shares[rank], tid) = fair;
+      }
+      if (nucleus) {
+        Z = 0;
+        for (int w = 0; w < kFW; ++w) Z += sh.warp_sum[w];
+        *at_rank(&sh.sums[0][rank], tid) = Z;
+      }
     }
     cluster_sync();
-    // k columns lie from the largest of the bounds on, and from the smallest of the CTAs' shares on
-    for (int r = 0; r < p.C; ++r) {
-      top = max(top, sh.maxima[r]);
-      bound = max(bound, sh.bounds[r]);
-      fair = min(fair, sh.shares[r]);
+    for (int r = 0; r < p.C; ++r) top = max(top, sh.maxima[r]);
+    if (small_k) {
+      // k columns lie from the largest of the bounds on, and from the smallest of the CTAs' shares on
+      for (int r = 0; r < p.C; ++r) {
+        bound = max(bound, sh.bounds[r]);
+        fair = min(fair, sh.shares[r]);
+      }
+      bound = max(bound, fair);
     }
-    bound = max(bound, fair);
   }
   float M = key_value(top);  // local: of this CTA's columns only
   auto empty = [&]() {
@@ -853,7 +965,6 @@ __global__ void __launch_bounds__(kFT, 4) filter_kernel(const FilterParams p) {
     none(0.0);
   };
   if (!local && M == -INFINITY) return empty();
-  const float p_mass = a.p > 0.f ? a.p : 0.f;
 
   // the floor of min-p, once M is the row's
   auto floor_of = [&]() -> float {
@@ -870,41 +981,14 @@ __global__ void __launch_bounds__(kFT, 4) filter_kernel(const FilterParams p) {
   cut.tie = INT32_MAX;
   cut.floor = -INFINITY;  // (min-p comes last: the others' shares are of columns below its floor too)
 
-  // Gather the columns with keys in [low, high] that the cut so far keeps into CTA 0's
-  // list; their number.
-  auto gather = [&](uint32_t low, uint32_t high) -> int {
-    uint32_t mine_n = 0;
-    if (mine >= low) {
-      for (int i = s.lo + lane; i < s.hi; i += 32) {
-        const uint4 q = s.v[i];
-        if (value_key(E::max_of(q)) < low) continue;
-#pragma unroll
-        for (int e = 0; e < E::kN; ++e) {
-          const uint32_t k = value_key(E::get(q, e));
-          const int col = s.col0 + i * E::kN + e;
-          mine_n += k >= low && k <= high && col < p.V && (k != cut.key || col <= cut.tie);
-        }
-      }
-    }
-    uint32_t pre = mine_n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t x = __shfl_up_sync(0xffffffffu, pre, o);
-      if (lane >= o) pre += x;
-    }
-    const uint32_t warp_n = __shfl_sync(0xffffffffu, pre, 31);
-    uint32_t base = 0, most = kListCap;
-    if (warp_n && lane == 0) {
-      base = atomicAdd(&sh.own, warp_n);
-      if (!local) base = atomicAdd(at_rank(&sh.listed, 0), warp_n);
-    }
-    base = __shfl_sync(0xffffffffu, base, 0) + pre - mine_n;
-    if (local) {  // each CTA has its part of the list
-      most = (uint32_t)(rank + 1) * (kListCap / p.C);
-      base += (uint32_t)rank * (kListCap / p.C);
-    }
-    if (mine_n) {
-      unsigned long long* list = at_rank(sh.list, 0);
+  // Gather the columns with keys in [low, high] that the cut so far keeps into CTA 0's list;
+  // their number, and where they lie.
+  const int part_cap = kListCap / p.C;
+  auto gather = [&](uint32_t low, uint32_t high, ListMap& map) -> int {
+    unsigned long long* list = at_rank(sh.list, 0);
+    auto scan = [&](uint32_t first, uint32_t most) {
+      if (mine < low) return;
+#pragma unroll 4
       for (int i = s.lo + lane; i < s.hi; i += 32) {
         const uint4 q = s.v[i];
         if (value_key(E::max_of(q)) < low) continue;
@@ -913,45 +997,61 @@ __global__ void __launch_bounds__(kFT, 4) filter_kernel(const FilterParams p) {
           const uint32_t k = value_key(E::get(q, e));
           const int col = s.col0 + i * E::kN + e;
           if (k >= low && k <= high && col < p.V && (k != cut.key || col <= cut.tie)) {
-            if (base < most) list[base] = ((unsigned long long)k << 32) | (0xffffffffu - (uint32_t)col);
-            ++base;
+            const uint32_t at = atomicAdd(&sh.own, 1u);
+            if (at < most) list[first + at] = ((unsigned long long)k << 32) | (0xffffffffu - (uint32_t)col);
           }
         }
       }
-    }
+    };
+    scan((uint32_t)(rank * part_cap), (uint32_t)part_cap);  // each CTA in its part of the list
     cta_sync();
+    map.C = p.C;
+    map.slot = s.turn & 1;
     if (tid < p.C) {
-      *at_rank(&sh.counts[s.turn & 1][rank], tid) = sh.own;
+      *at_rank(&sh.counts[map.slot][rank], tid) = sh.own;
       if (local) *at_rank(&sh.maxima[rank], tid) = top;
     }
     cluster_sync();
-    int L = 0;
-    for (int r = 0; r < p.C; ++r) {
-      const uint32_t n = sh.counts[s.turn & 1][r];
-      L += (int)min(n, 1u << 20);
-      if (local && n > (uint32_t)(kListCap / p.C)) L = 1 << 20;
-    }
     ++s.turn;
-    return min(L, 1 << 20);
+    uint32_t L = 0, before = 0, most = 0;
+    for (int r = 0; r < p.C; ++r) {
+      const uint32_t n = sh.counts[map.slot][r];
+      if (r == rank) before = L;
+      L += n;
+      most = max(most, n);
+    }
+    if (most > (uint32_t)part_cap && L <= kListCap) {  // some part is too short: one after another
+      if (tid == 0) sh.own = 0;
+      cta_sync();
+      scan(before, kListCap);
+      cluster_sync();
+      map.C = 0;
+    }
+    return (int)L;  // (at most 2^18)
   };
 
   // ---- rows whose kept columns all reach a known value: a list
-  unsigned long long Z = 0;  // the whole row's weight (top-p alone)
-  float octaves = 0.f;       // how far below M the cut lies at most
+  float octaves = 0.f;  // how far below M the cut lies at most
   const bool by_min = a.k == p.V && a.p >= 1.f && floor > -INFINITY;
   if (small_k || nucleus || by_min) {
     uint32_t low = small_k ? bound << 16 : value_key(floor);
     if (nucleus) {
-      Z = s.mass(sc, sh.queue[warp]);
-      uint32_t c = 0;
-      s.exchange(c, Z);
+      // the CTAs' weights, each relative to its own maximum
+      Z = 0;
+      if (lane < p.C) {
+        const float m = key_value(sh.maxima[lane]);
+        const unsigned long long z = sh.sums[0][lane];
+        Z = m == M ? z : __umul64hi(z, fixed_weight(weight(sc, sh.table, m), 62)) << 2;
+      }
+      Z = warp_sum_u64(Z);
       // The last kept column and those after it weigh more than (1 - p) Z and are at most
       // V, so it weighs more than (1 - p) Z / V (and a little less, for this estimate's roundings).
       octaves = 0x1p-16f - log2f((1.f - p_mass) * ((float)Z * 0x1p-44f) / (float)p.V);
       const float away = octaves / sc.ch;
       low = max(low, M == INFINITY ? top : value_key(M - away - 0x1p-20f * (fabsf(M) + away)));
     }
-    int L = gather(low, 0xffffffffu);
+    ListMap map;
+    const int L = gather(low, 0xffffffffu, map);
     if (local) {
       for (int r = 0; r < p.C; ++r) top = max(top, sh.maxima[r]);
       M = key_value(top);
@@ -960,31 +1060,14 @@ __global__ void __launch_bounds__(kFT, 4) filter_kernel(const FilterParams p) {
     }
     if (L <= kListCap) {
       if (rank == 0) {
-        if (local) {
-          floor = floor_of();
-          // (the parts of the list closed up)
-          unsigned long long k[kListCap / kFT];
-          int at[kListCap / kFT];
-          const int region = kListCap / p.C;
-#pragma unroll
-          for (int h = 0; h < kListCap / kFT; ++h) {
-            const int i = tid + h * kFT, r = i / region;
-            at[h] = -1;
-            if (r < p.C && i - r * region < (int)sh.counts[(s.turn - 1) & 1][r]) {
-              at[h] = i - r * region;
-              for (int x = 0; x < r; ++x) at[h] += (int)sh.counts[(s.turn - 1) & 1][x];
-              k[h] = sh.list[i];
-            }
-          }
-          cta_sync();
-#pragma unroll
-          for (int h = 0; h < kListCap / kFT; ++h)
-            if (at[h] >= 0) sh.list[at[h]] = k[h];
-        }
-        cta_sync();
-        resolve_list<kVerify, false>(p, sh, ls, sc, row, L, low, top, small_k ? a.k : p.V, a.p < 1.f ? (double)p_mass : 2.0,
-                                     nucleus ? (double)Z * (1ull << (kListBits - kSumBits)) : -1.0, floor, a.T, u, draws, draft,
-                                     p.C, 0ull);
+        if (local) floor = floor_of();
+        const int k = small_k ? a.k : p.V;
+        const float share = a.p < 1.f ? p_mass : 1.f;
+        const unsigned long long whole = nucleus ? Z : 0ull;
+        if (L <= kPairs)
+          resolve_pairs<kVerify>(p, sh, ls, sc, row, L, map, k, share, whole, floor, a.T, u, draws, draft);
+        else
+          resolve_list<kVerify, false>(p, sh, ls, sc, row, L, map, low, top, k, share, whole, floor, a.T, u, draws, draft, p.C, 0ull);
       }
       return;
     }
@@ -994,16 +1077,13 @@ __global__ void __launch_bounds__(kFT, 4) filter_kernel(const FilterParams p) {
 
   // ---- the cut, over the whole row: a histogram shows between which values it lies, what is
   // above is added up, and a list of the columns between them decides
-  auto refine = [&](bool by_count, float range, double target, int k, double whole) -> bool {
+  auto refine = [&](bool by_count, float range, double target, int k, unsigned long long whole) -> bool {
     if (M == INFINITY) return false;
     float lo_x, hi_x;
     const bool found = by_count ? s.template steer<false>(sc, cut, range, target, sh.steps, lo_x, hi_x)
                                 : s.template steer<true>(sc, cut, range, target, sh.steps, lo_x, hi_x);
     if (!found) return false;
-    if (tid == 0) {
-      sh.own = 0;
-      if (rank == 0) sh.listed = 0;
-    }
+    if (tid == 0) sh.own = 0;
     uint32_t n = 0;
     unsigned long long sum = 0;
     const uint32_t high = hi_x == INFINITY ? 0xffffffffu : value_key(hi_x);
@@ -1014,11 +1094,12 @@ __global__ void __launch_bounds__(kFT, 4) filter_kernel(const FilterParams p) {
       cluster_sync();
     }
     const uint32_t low = value_key(lo_x);
-    const int L = gather(low, high - 1);
+    ListMap map;
+    const int L = gather(low, high - 1, map);
     if (L == 0 || L > kListCap) return false;
     if (rank == 0)
-      resolve_list<kVerify, true>(p, sh, ls, sc, row, L, low, min(high - 1, top), by_count ? k - (int)n : p.V, by_count ? 2.0 : (double)p_mass,
-                                  whole, floor, a.T, u, draws, draft, p.C, sum << (kListBits - kSumBits));
+      resolve_list<kVerify, true>(p, sh, ls, sc, row, L, map, low, min(high - 1, top), by_count ? k - (int)n : p.V,
+                                  by_count ? 1.f : p_mass, whole, floor, a.T, u, draws, draft, p.C, sum);
     cluster_sync();
     if (rank == 0) {  // its slice again: the list's bins took its place
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -1030,7 +1111,7 @@ __global__ void __launch_bounds__(kFT, 4) filter_kernel(const FilterParams p) {
     cut.tie = sh.cut_tie;
     return true;
   };
-  if (a.k < p.V && !refine(true, 63.f, (double)a.k, a.k, -1.0)) {
+  if (a.k < p.V && !refine(true, 63.f, (double)a.k, a.k, 0ull)) {
     cut.key = s.template search<false>(sc, (uint32_t)a.k, 0.0);
     uint32_t c = 0;
     unsigned long long sum;
@@ -1046,8 +1127,7 @@ __global__ void __launch_bounds__(kFT, 4) filter_kernel(const FilterParams p) {
       octaves = 0x1p-16f - log2f((1.f - p_mass) * ((float)sum * 0x1p-44f) / (float)a.k);
     }
     const double whole = (double)sum;
-    if (!refine(false, fminf(octaves + 0x1p-8f, 63.f), fmax((double)p_mass * whole * 0x1p-44, 0x1p-40), 0,
-                whole * (1ull << (kListBits - kSumBits)))) {
+    if (!refine(false, fminf(octaves + 0x1p-8f, 63.f), fmax((double)p_mass * whole * 0x1p-44, 0x1p-40), 0, sum)) {
       const uint32_t key_k = cut.key;
       const int tie_k = cut.tie;
       const double target = (double)p_mass * whole;
