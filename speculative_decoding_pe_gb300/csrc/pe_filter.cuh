@@ -127,6 +127,14 @@ __device__ __forceinline__ unsigned long long fixed_weight(float2 w, int bits) {
 __device__ __forceinline__ unsigned long long share_of(float u, unsigned long long W) {
   return __umul64hi(__float2ull_rz(u * 0x1p64f), W);
 }
+// w / W in fp32 (off by half a step and 2^-40 of itself: the quotient's own rounding is
+// corrected by the remainder).
+__device__ __forceinline__ float ratio(unsigned long long w, unsigned long long W) {
+  const float a = __ull2float_rz(w), b = __ull2float_rz(W);
+  const float al = (float)(w - (unsigned long long)a), bl = (float)(W - (unsigned long long)b);
+  const float q = a / b;
+  return q + (fmaf(-q, b, a) + (al - q * bl)) / b;
+}
 // The smallest whole number that is at least u W, and at least 1
 __device__ __forceinline__ unsigned long long share_from(float u, unsigned long long W) {
   const unsigned long long f = __float2ull_rz(u * 0x1p64f);
@@ -145,6 +153,10 @@ struct Elt<PE_BF16> {
     const uint32_t w = (e >> 1) == 0 ? q.x : (e >> 1) == 1 ? q.y : (e >> 1) == 2 ? q.z : q.w;
     return (e & 1) ? bf16_hi(w) : bf16_lo(w);
   }
+  // element e of vector i in shared memory
+  __device__ static __forceinline__ float element(const uint4* v, int i, int e) {
+    return __uint_as_float((uint32_t) reinterpret_cast<const unsigned short*>(v + i)[e] << 16);
+  }
   // (a NaN gives way to the other operand)
   __device__ static __forceinline__ float max_of(uint4 q) {
     const uint32_t m = bf16x2_max(bf16x2_max(bf16x2_max(q.x, q.y), bf16x2_max(q.z, q.w)), 0xff80ff80u);
@@ -159,6 +171,9 @@ struct Elt<PE_F32> {
   static constexpr int kN = 4, kSize = 4, kKeyBits = 32;
   __device__ static __forceinline__ float get(uint4 q, int e) {
     return __uint_as_float(e == 0 ? q.x : e == 1 ? q.y : e == 2 ? q.z : q.w);
+  }
+  __device__ static __forceinline__ float element(const uint4* v, int i, int e) {
+    return reinterpret_cast<const float*>(v + i)[e];
   }
   __device__ static __forceinline__ float max_of(uint4 q) {
     return fmaxf(fmaxf(fmaxf(__uint_as_float(q.x), __uint_as_float(q.y)),
@@ -195,7 +210,7 @@ struct RowCut {
   int listed;    // kept columns in the row's list, or -1 (not listed)
   int token;     // the draw from the row (bonus rows)
   double W;      // sum of kept weights; 0: nothing to keep; -1: bad parameters
-  double px;     // probability of the row's draft token; -1: not in the vocabulary
+  double wx;     // kept weight of the row's draft token; -1: not in the vocabulary
 };
 struct Kept {  // a kept column and its weight times 2^kListBits
   unsigned long long w;

@@ -53,7 +53,7 @@ constexpr int kMaxSegment = kListCap * 8 / 2 / kFW;  // vectors of a warp's segm
 struct FilterShared {
   uint64_t bars[kFW];
   unsigned long long sums[2][kMaxCluster];  // exchanged by the CTAs, in turns
-  unsigned long long warp_sum[kFW];
+  unsigned long long warp_sum[kFW], warp_large[kFW];
   uint32_t counts[2][kMaxCluster];
   uint32_t warp_count[kFW];
   uint32_t maxima[kMaxCluster], bounds[kMaxCluster], shares[kMaxCluster];
@@ -62,12 +62,13 @@ struct FilterShared {
   uint32_t cut_key;
   int cut_tie, tie;
   float2 table[32];
-  double px;
+  unsigned long long wx;
   Rates rates;
   float2 inverse[2];
   float floor;
   int first;
   uint32_t hist[kFT];
+  unsigned short hits[kFW][64];
   union alignas(16) {
     unsigned long long list[kListCap];         // candidates: (value's key, ~column)
     unsigned short queue[kFW][kMaxSegment];    // vectors to be weighed in full
@@ -138,13 +139,14 @@ struct Slice {
     }
   }
 
-  // The warp's share of the row's weight.  Vectors whose largest weight is below 2^-12
+  // The warp's share of the row's weight.  Vectors whose largest weight is below 2^-20
   // go through the hardware's exponential in 24 bits: their errors are of either sign
   // and some 2^-22 of a small part of the sum.  The others are queued (few, in a row of a
   // language model: a branch in the loop would be taken by one lane or another nearly every
   // time) and weighed in full.
-  __device__ __forceinline__ unsigned long long mass(const Scale& sc, unsigned short* queue) {
-    const float big = sc.inf ? -INFINITY : sc.M - 12.f / sc.ch;
+  // large: the share of the columns of at least 2^-12 of the largest weight.
+  __device__ __forceinline__ unsigned long long mass(const Scale& sc, unsigned short* queue, unsigned long long& large) {
+    const float big = sc.inf ? -INFINITY : sc.M - 20.f / sc.ch, top = sc.inf ? sc.M : sc.M - 12.f / sc.ch;
     float small = 0.f;
     int queued = 0;
     for (int i0 = lo; i0 < hi; i0 += 32) {
@@ -167,17 +169,20 @@ struct Slice {
       queued += __popc(m);
     }
     __syncwarp();
-    WeightSum<256> ws;
+    WeightSum<256> all, most;
     for (int j = lane; j < queued; j += 32) {
       const uint4 q = v[lo + queue[j]];
 #pragma unroll
       for (int e = 0; e < Elt<DT>::kN; ++e) {
-        const float2 w = weight(sc, sh->table, Elt<DT>::get(q, e));
-        ws.add(w.x, w.y);
+        const float x = Elt<DT>::get(q, e);
+        const float2 w = weight(sc, sh->table, x);
+        all.add(w.x, w.y);
+        if (x >= top) most.add(w.x, w.y);
       }
     }
-    ws.add(0.f, small);
-    return warp_sum_u64(ws.fixed(kSumBits));
+    large = warp_sum_u64(most.fixed(kSumBits));
+    all.add(0.f, small);
+    return warp_sum_u64(all.fixed(kSumBits));
   }
 
   // The warp's share of the weight that a cut keeps.
@@ -498,7 +503,7 @@ __device__ __forceinline__ void answer_draw(const FilterParams& p, int row, int 
     p.cuts[row].token = col;
   } else {
     p.out_tokens[row] = col;
-    if (p.out_prob) p.out_prob[row] = (float)((double)w / (double)W);
+    if (p.out_prob) p.out_prob[row] = ratio(w, W);
   }
 }
 template <bool kVerify, int kPer>
@@ -510,7 +515,7 @@ __device__ __forceinline__ void keep_record(const FilterParams& p, FilterShared&
   for (int h = 0; h < kPer; ++h) {
     if (keep[h]) {
       const int col = (int)(0xffffffffu - (uint32_t)key[h]);
-      if (col == draft) sh.px = (double)w[h] / (double)W;
+      if (col == draft) sh.wx = w[h];
       if (store) {
         const uint32_t at = atomicAdd(&sh.stored, 1u);
         if (at < kKeptCap) {
@@ -533,7 +538,7 @@ __device__ __forceinline__ void keep_record(const FilterParams& p, FilterShared&
     c.T = T;
     c.listed = store && sh.stored <= kKeptCap ? (int)sh.stored : -1;
     c.W = (double)W * (1.0 / (1ull << kListBits));
-    c.px = sh.px;
+    c.wx = draft >= 0 && draft < p.V ? (double)sh.wx * (1.0 / (1ull << kListBits)) : -1.0;
   }
 }
 
@@ -547,32 +552,48 @@ __device__ __forceinline__ void resolve_pairs(const FilterParams& p, FilterShare
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   ulonglong2* pair = reinterpret_cast<ulonglong2*>(&ls);
   unsigned long long key[1] = {0}, w[1] = {0};
+  if (tid < L) key[0] = sh.list[map.at(sh, tid)];
+  if (L > k + 8) {  // the CTAs' lists overlap: the first k of them, and a few more
+    const uint32_t mine = tid < L ? key_of(key[0]) >> 16 : 0u;
+    const uint32_t bound = kth_prefix(sh.hist, mine, value_key(sc.M) >> 16, (uint32_t)k);
+    if (tid == 0) sh.own = 0;
+    cta_sync();
+    if (tid < L && mine >= bound) sh.list[atomicAdd(&sh.own, 1u)] = key[0];
+    cta_sync();
+    L = (int)sh.own;
+    if (tid < L) key[0] = sh.list[tid];
+  }
   bool keep[1] = {tid < L};
   const bool on = 32 * warp < L;  // this warp has columns
   if (on) {
-    if (keep[0]) {
-      key[0] = sh.list[map.at(sh, tid)];
-      w[0] = fixed_weight(weight(sc, sh.table, key_value(key_of(key[0]))), kListBits);
-    }
+    if (keep[0]) w[0] = fixed_weight(weight(sc, sh.table, key_value(key_of(key[0]))), kListBits);
     pair[tid] = make_ulonglong2(key[0], w[0]);
   }
   if (tid == 0) {
     sh.above = 0;
     if (kVerify) {
       sh.stored = 0;
-      sh.px = draft >= 0 && draft < p.V ? 0.0 : -1.0;
+      sh.wx = 0;
     }
   }
   cta_sync();
   int rank = 0;
   unsigned long long pre = 0;
   if (on) {
-#pragma unroll 4
-    for (int j = 0; j < L; ++j) {
-      const ulonglong2 o = pair[j];
-      const bool first = o.x > key[0];
-      rank += first;
+    unsigned long long pre2 = 0;
+#pragma unroll 2
+    for (int j = 0; j + 1 < L; j += 2) {
+      const ulonglong2 o = pair[j], o2 = pair[j + 1];
+      const bool first = o.x > key[0], first2 = o2.x > key[0];
+      rank += first + first2;
       pre += first ? o.y : 0ull;
+      pre2 += first2 ? o2.y : 0ull;
+    }
+    pre += pre2;
+    if (L & 1) {
+      const ulonglong2 o = pair[L - 1];
+      rank += o.x > key[0];
+      pre += o.x > key[0] ? o.y : 0ull;
     }
     if (keep[0] && rank == min(k, L) - 1) sh.total = pre + w[0];
   }
@@ -597,12 +618,15 @@ __device__ __forceinline__ void resolve_pairs(const FilterParams& p, FilterShare
   if (draws && keep[0] && w[0]) {
     const unsigned long long at = share_of(u, W);
     const uint32_t inv = (uint32_t)key[0];  // larger: a lower column
-    unsigned long long upto = 0;
-#pragma unroll 4
-    for (int j = 0; j < L; ++j) {
-      const ulonglong2 o = pair[j];
+    unsigned long long upto = 0, upto2 = 0;
+#pragma unroll 2
+    for (int j = 0; j + 1 < L; j += 2) {
+      const ulonglong2 o = pair[j], o2 = pair[j + 1];
       upto += (uint32_t)o.x >= inv ? o.y : 0ull;
+      upto2 += (uint32_t)o2.x >= inv ? o2.y : 0ull;
     }
+    upto += upto2;
+    if ((L & 1) && (uint32_t)pair[L - 1].x >= inv) upto += pair[L - 1].y;
     if (upto > at && upto - w[0] <= at) answer_draw<kVerify>(p, row, (int)(0xffffffffu - inv), w[0], W);
   }
   if (kVerify) keep_record<kVerify, 1>(p, sh, sc, row, T, draft, W, keep, key, w);
@@ -744,7 +768,7 @@ __device__ __forceinline__ void resolve_list(const FilterParams& p, FilterShared
     if (lane == 0) sh.warp_sum[warp] = least;
     if (tid == 0) {
       sh.stored = 0;
-      sh.px = draft >= 0 && draft < p.V ? 0.0 : -1.0;
+      sh.wx = 0;
     }
   }
   cta_sync();
@@ -886,7 +910,7 @@ __global__ void __launch_bounds__(kFT, 4) filter_kernel(const FilterParams p) {
       c.listed = 0;
       c.token = -1;
       c.W = W;
-      c.px = 0.0;
+      c.wx = 0.0;
     } else {
       p.out_tokens[row] = -1;
       if (p.out_prob) p.out_prob[row] = 0.f;
@@ -909,6 +933,7 @@ __global__ void __launch_bounds__(kFT, 4) filter_kernel(const FilterParams p) {
 
   // ---- maxima
   float tmax = -INFINITY;
+#pragma unroll 4
   for (int i = s.lo + lane; i < s.hi; i += 32) tmax = fmaxf(tmax, E::max_of(s.v[i]));
   const uint32_t mine = ordered_bits(tmax);
   const uint32_t wmax = __reduce_max_sync(0xffffffffu, mine);
@@ -928,12 +953,16 @@ __global__ void __launch_bounds__(kFT, 4) filter_kernel(const FilterParams p) {
   }
   const float p_mass = a.p > 0.f ? a.p : 0.f;
   unsigned long long Z = 0;  // the whole row's weight (top-p alone)
-  if (nucleus) Z = s.mass(make_scale(key_value(top), sh.rates), sh.queue[warp]);
+  unsigned long long large = 0;
+  if (nucleus) Z = s.mass(make_scale(key_value(top), sh.rates), sh.queue[warp], large);
   cluster_wait();  // every CTA has started
   if (!local) {
     const uint32_t own_top = top;
     if (nucleus) {
-      if (lane == 0) sh.warp_sum[warp] = Z;
+      if (lane == 0) {
+        sh.warp_sum[warp] = Z;
+        sh.warp_large[warp] = large;
+      }
       cta_sync();
     }
     if (tid < p.C) {
@@ -943,9 +972,13 @@ __global__ void __launch_bounds__(kFT, 4) filter_kernel(const FilterParams p) {
         *at_rank(&sh.shares[rank], tid) = fair;
       }
       if (nucleus) {
-        Z = 0;
-        for (int w = 0; w < kFW; ++w) Z += sh.warp_sum[w];
+        Z = large = 0;
+        for (int w = 0; w < kFW; ++w) {
+          Z += sh.warp_sum[w];
+          large += sh.warp_large[w];
+        }
         *at_rank(&sh.sums[0][rank], tid) = Z;
+        *at_rank(&sh.sums[1][rank], tid) = large;
       }
     }
     cluster_sync();
@@ -986,22 +1019,49 @@ __global__ void __launch_bounds__(kFT, 4) filter_kernel(const FilterParams p) {
   const int part_cap = kListCap / p.C;
   auto gather = [&](uint32_t low, uint32_t high, ListMap& map) -> int {
     unsigned long long* list = at_rank(sh.list, 0);
+    const float low_x = key_value(max(low, 0x007fffffu));  // (below the key of -infinity lie NaNs)
+    // Vectors that hold any go to a queue of the warp; then its lanes take an element each (a
+    // lane with its whole vector, as it comes, takes four times as long: the others wait).
     auto scan = [&](uint32_t first, uint32_t most) {
-      if (mine < low) return;
-#pragma unroll 4
-      for (int i = s.lo + lane; i < s.hi; i += 32) {
-        const uint4 q = s.v[i];
-        if (value_key(E::max_of(q)) < low) continue;
-#pragma unroll
-        for (int e = 0; e < E::kN; ++e) {
-          const uint32_t k = value_key(E::get(q, e));
-          const int col = s.col0 + i * E::kN + e;
-          if (k >= low && k <= high && col < p.V && (k != cut.key || col <= cut.tie)) {
-            const uint32_t at = atomicAdd(&sh.own, 1u);
-            if (at < most) list[first + at] = ((unsigned long long)k << 32) | (0xffffffffu - (uint32_t)col);
+      uint32_t queued = 0;
+      auto take = [&](uint32_t n) {
+        __syncwarp();
+        for (uint32_t j0 = 0; j0 < n; j0 += 32 / E::kN) {
+          const uint32_t j = j0 + lane / E::kN;
+          uint32_t k = 0;
+          int col = 0;
+          bool in = j < n;
+          if (in) {
+            const int i = sh.hits[warp][j], e = lane % E::kN;
+            const float x = E::element(s.v, i, e);
+            k = ordered_bits(x);
+            col = s.col0 + i * E::kN + e;
+            in = x >= low_x && k <= high && col < p.V && (k != cut.key || col <= cut.tie);
+          }
+          const uint32_t m = __ballot_sync(0xffffffffu, in);
+          if (m) {
+            uint32_t at = 0;
+            if (lane == 0) at = atomicAdd(&sh.own, (uint32_t)__popc(m));
+            at = __shfl_sync(0xffffffffu, at, 0) + __popc(m & ((1u << lane) - 1));
+            if (in && at < most) list[first + at] = ((unsigned long long)k << 32) | (0xffffffffu - (uint32_t)col);
           }
         }
+        __syncwarp();
+      };
+#pragma unroll 2
+      for (int i0 = s.lo; i0 < s.hi; i0 += 32) {
+        const int i = i0 + lane;
+        const bool hit = i < s.hi && E::max_of(s.v[i]) >= low_x;
+        const uint32_t m = __ballot_sync(0xffffffffu, hit);
+        if (!m) continue;
+        if (hit) sh.hits[warp][queued + __popc(m & ((1u << lane) - 1))] = (unsigned short)i;
+        queued += __popc(m);
+        if (queued > 32) {  // (room for another 32 is needed)
+          take(queued);
+          queued = 0;
+        }
       }
+      take(queued);
     };
     scan((uint32_t)(rank * part_cap), (uint32_t)part_cap);  // each CTA in its part of the list
     cta_sync();
@@ -1037,18 +1097,32 @@ __global__ void __launch_bounds__(kFT, 4) filter_kernel(const FilterParams p) {
     uint32_t low = small_k ? bound << 16 : value_key(floor);
     if (nucleus) {
       // the CTAs' weights, each relative to its own maximum
-      Z = 0;
+      Z = large = 0;
+      float lowest = INFINITY;  // of the CTAs' maxima
       if (lane < p.C) {
-        const float m = key_value(sh.maxima[lane]);
-        const unsigned long long z = sh.sums[0][lane];
-        Z = m == M ? z : __umul64hi(z, fixed_weight(weight(sc, sh.table, m), 62)) << 2;
+        lowest = key_value(sh.maxima[lane]);
+        Z = sh.sums[0][lane];
+        large = sh.sums[1][lane];
+        if (lowest != M) {
+          const unsigned long long f = fixed_weight(weight(sc, sh.table, lowest), 62);
+          Z = __umul64hi(Z, f) << 2;
+          large = __umul64hi(large, f) << 2;
+        }
       }
       Z = warp_sum_u64(Z);
+      large = warp_sum_u64(large);
+      lowest = key_value(__reduce_min_sync(0xffffffffu, ordered_bits(lowest)));
       // The last kept column and those after it weigh more than (1 - p) Z and are at most
       // V, so it weighs more than (1 - p) Z / V (and a little less, for this estimate's roundings).
       octaves = 0x1p-16f - log2f((1.f - p_mass) * ((float)Z * 0x1p-44f) / (float)p.V);
-      const float away = octaves / sc.ch;
-      low = max(low, M == INFINITY ? top : value_key(M - away - 0x1p-20f * (fabsf(M) + away)));
+      float away = octaves / sc.ch;
+      away += 0x1p-20f * (fabsf(M) + away);
+      // Where what is large holds the share by itself, that is the list.
+      if ((float)large > (p_mass + 0x1p-16f) * (float)Z) {
+        const float reach = (M - lowest) + 12.f / sc.ch;
+        away = fminf(away, reach + 0x1p-20f * (fabsf(M) + fabsf(lowest) + reach));
+      }
+      low = max(low, M == INFINITY ? top : value_key(M - away));
     }
     ListMap map;
     const int L = gather(low, 0xffffffffu, map);
@@ -1186,16 +1260,16 @@ __global__ void __launch_bounds__(kFT, 4) filter_kernel(const FilterParams p) {
     o.T = a.T;
     o.listed = -1;
     o.W = (double)sum * (1.0 / (1ull << kSumBits));
-    double px = -1.0;
+    double wx = -1.0;
     if (draft >= 0 && draft < p.V) {
       const float x = E::load(src, draft);
-      px = 0.0;
+      wx = 0.0;
       if (cut.keeps(x, draft)) {
         const float2 w = weight(sc, sh.table, x);
-        px = ((double)w.x + (double)w.y) / o.W;
+        wx = (double)w.x + (double)w.y;
       }
     }
-    o.px = px;
+    o.wx = wx;
   }
   if (draws) {
     const unsigned long long at = share_of(u, sum);
@@ -1208,8 +1282,11 @@ __global__ void __launch_bounds__(kFT, 4) filter_kernel(const FilterParams p) {
           p.cuts[row].token = col;
         } else {
           p.out_tokens[row] = col;
-          if (p.out_prob) p.out_prob[row] = (float)((double)fixed_weight(weight(sc, sh.table, E::load(src, col)), kListBits) /
-                                                    ((double)sum * (1ull << (kListBits - kSumBits))));
+          if (p.out_prob) {
+            const float2 w = weight(sc, sh.table, E::load(src, col));
+            const float b = __ull2float_rz(sum), bl = (float)(sum - (unsigned long long)b), q = w.x * 0x1p44f / b;
+            p.out_prob[row] = q + (fmaf(-q, b, w.x * 0x1p44f) + (w.y * 0x1p44f - q * bl)) / b;
+          }
         }
       }
     }
@@ -1267,7 +1344,8 @@ __global__ void __launch_bounds__(kFT) residual_kernel(const FilterParams p) {
       const int j = j0 + lane;
       bool no = false;
       if (j < p.Kp) {
-        const double px = target[j].px, qx = drafts[j].px;
+        const double pw = target[j].W, qw = drafts[j].W;
+        const double px = pw > 0.0 ? target[j].wx / pw : 0.0, qx = qw > 0.0 ? drafts[j].wx / qw : 0.0;
         no = !((double)__ldg(p.coins + b * p.Kp + j) * qx < px);
         if (p.chance && rank == 0) p.chance[b * p.Kp + j] = bad || !(px > 0.0) ? 0.f : px < qx ? (float)(px / qx) : 1.f;
       }
