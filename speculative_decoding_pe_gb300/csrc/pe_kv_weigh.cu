@@ -12,6 +12,7 @@
 // mma.sync m16n8k16 and eight columns as its columns: the sum over columns of pass
 // 3 stays in registers, and a record is converted once for all columns.  Each key
 // belongs to one warp: no atomics, the same result every time.
+#include "pe_cluster.cuh"
 #include "pe_kv.cuh"
 
 namespace pe {
@@ -50,6 +51,22 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// Two products, two differences in one instruction each.
+__device__ __forceinline__ void mul2(float& d0, float& d1, float2 f) {
+  asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\tmul.rn.f32x2 a, a, b;\n\t"
+      "mov.b64 {%0, %1}, a;\n\t}"
+      : "+f"(d0), "+f"(d1)
+      : "f"(f.x), "f"(f.y));
+}
+__device__ __forceinline__ float2 add2(float d0, float d1, float2 z) {
+  float2 r;
+  asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tadd.rn.f32x2 a, a, b;\n\t"
+      "mov.b64 {%0, %1}, a;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(d0), "f"(d1), "f"(z.x), "f"(z.y));
+  return r;
+}
+
 // Keys that row t sees.
 __device__ __forceinline__ int row_limit(const WeighParams& p, int t, bool report) {
   if (p.rejected && __ldg(p.rejected + t)) return 0;
@@ -75,11 +92,13 @@ __device__ __forceinline__ void request_rows(const WeighParams& p, int b, int& r
 
 template <int D>
 struct WeighShared {
-  uint2 q[kColBlock / 8][D / 16][32];  // columns as B fragments, eight at a time
+  uint4 q[kColBlock / 8][D / 32][32];  // columns as B fragments, eight at a time, two steps in a word
   float factor[kColBlock];  // scale * log2(e) and the power of two taken out of a column
-  float lse[kColBlock];
+  float lse[kColBlock];     // minus the log2-sum of a column; -infinity: no weight
   int limit[kColBlock];
-  int most, least;          // of the columns' limits
+  float2 sums[kColBlock];   // this CTA's maximum and sum of a column
+  float2 join[kWeighWarps][kColBlock];
+  int least;                // of the columns' limits
   int reach;                // of all the request's rows
 };
 
@@ -126,12 +145,12 @@ struct KeyWords {
   }
 };
 
-// Columns c0.. of request rows [r0, r1), key head h, into shared memory.
+// Columns c0.. of the request's rows from r0 on, key head h, into shared memory.
 template <int D>
-__device__ __forceinline__ void load_columns(const WeighParams& p, WeighShared<D>& sh, int r0, int r1, int h, int c0, int n,
-                                             bool weigh) {
+__device__ __forceinline__ void load_columns(const WeighParams& p, WeighShared<D>& sh, int r0, int h, int c0, int n) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (threadIdx.x == 0) sh.most = 0, sh.least = INT32_MAX;
+  __syncthreads();  // the last sweep's readers
+  if (threadIdx.x == 0) sh.least = INT32_MAX;
   __syncthreads();
   const int padded = (n + 7) & ~7;
   for (int c = warp; c < padded; c += kWeighWarps) {
@@ -150,125 +169,121 @@ __device__ __forceinline__ void load_columns(const WeighParams& p, WeighShared<D
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(lo) : "f"(x[1] * down), "f"(x[0] * down));
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(x[3] * down), "f"(x[2] * down));
     // element 4 lane = t D/4 + 4 s
-    if (4 * lane < D) sh.q[c >> 3][lane % (D / 16)][4 * (c & 7) + lane / (D / 16)] = make_uint2(lo, hi);
+    const int s = lane % (D / 16);
+    if (4 * lane < D)
+      reinterpret_cast<uint2*>(&sh.q[c >> 3][s >> 1][4 * (c & 7) + lane / (D / 16)])[s & 1] = make_uint2(lo, hi);
     if (lane == 0) {
       const int limit = live ? row_limit(p, row, false) : 0;
-      sh.factor[c] = p.scale2 * up;
+      sh.factor[c] = fmaxf(p.scale2 * up, 1.2e-38f);  // (above 0: an infinity times it is one)
       sh.limit[c] = limit;
-      sh.lse[c] = live && weigh ? __ldcg(p.lse + (long long)row * p.Hq + head) : INFINITY;
-      if (live) {
-        atomicMax(&sh.most, limit);
-        atomicMin(&sh.least, limit);
-      }
+      sh.lse[c] = -INFINITY;
+      if (limit) atomicMin(&sh.least, limit);  // (a column that sees nothing gets no weight by its lse)
     }
   }
   __syncthreads();
 }
 
-// The record of keys j0..j0+15 of request b and head h; NULL for a page outside the cache.
-template <int D>
-__device__ __forceinline__ const uint8_t* record_of(const WeighParams& p, int b, int h, int j0, long long& slot) {
-  const int page = j0 / p.block_size, off = j0 - page * p.block_size;
-  const long long block = __ldg(p.table + (long long)b * p.bt_width + page);
-  slot = (block * p.Hkv + h) * p.block_size + off;
-  if (block < 0 || block >= p.num_blocks) return nullptr;
-  return p.cache + ((block * p.Hkv + h) * (p.block_size >> 4) + (off >> 4)) * (long long)Record<D>::kBytes;
-}
+// Running maximum and sum of two columns of each tile, over a lane's rows.
+template <int kTiles>
+struct Stats {
+  float m[kTiles][2], l[kTiles][2];
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < kTiles; ++i) m[i][0] = m[i][1] = -INFINITY, l[i][0] = l[i][1] = 0.f;
+  }
+};
 
-template <int D, bool kWeigh>
-__global__ void __launch_bounds__(kWeighThreads) weigh_kernel(const WeighParams p) {
-  extern __shared__ __align__(16) unsigned char smem[];
-  WeighShared<D>& sh = *reinterpret_cast<WeighShared<D>*>(smem);
+// One look at the records [rec0, rec1) of request b, key head h, by this CTA's warps.  A
+// record's sixteen tokens against all columns: kWeigh: the sum over columns of
+// 2^(score - lse) goes to out; else the columns' statistics.
+template <int D, int kTiles, bool kWeigh>
+__device__ __forceinline__ void sweep(const WeighParams& p, const WeighShared<D>& sh, int b, int h, int rec0, int rec1, int reach,
+                                      int tiles, bool more, Stats<kTiles>& st) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int b = blockIdx.y / p.Hkv, h = blockIdx.y - b * p.Hkv;
-  const int chunk0 = blockIdx.x * p.chunk;
-  int r0, r1;
-  request_rows(p, b, r0, r1);
-  if (r0 == r1) return;
-  if (threadIdx.x == 0) sh.reach = 0;
-  __syncthreads();
-  int most = 0;
-  for (int t = r0 + threadIdx.x; t < r1; t += kWeighThreads)
-    most = max(most, row_limit(p, t, !kWeigh && h == 0 && blockIdx.x == 0));
-  most = __reduce_max_sync(0xffffffffu, most);
-  if (lane == 0) atomicMax(&sh.reach, most);
-  if (kWeigh) asm volatile("griddepcontrol.wait;" ::: "memory");
-  __syncthreads();
-  const int reach = sh.reach;
-  if (kWeigh && p.offsets && __ldcg(p.lse + (long long)p.T * p.Hq) != 0.f) return;  // offsets no partition
-  if (chunk0 >= reach) return;
-  const int chunk1 = min(reach, chunk0 + p.chunk);
-  const int columns = (r1 - r0) * p.G;
   const int g = lane >> 2, t2 = 2 * (lane & 3);
   const int fresh = kWeigh && p.fresh ? __ldg(p.fresh + b) : INT32_MAX;
-
-  for (int c0 = 0; c0 < columns; c0 += kColBlock) {
-    const int n = min(kColBlock, columns - c0), tiles = (n + 7) >> 3;
-    if (c0) __syncthreads();
-    load_columns<D>(p, sh, r0, r1, h, c0, n, kWeigh);
-    float m[kWeigh ? 1 : kColBlock / 8][2], l[kWeigh ? 1 : kColBlock / 8][2];
-    if (!kWeigh) {
+  const int page_recs = p.block_size >> 4;
+  const int32_t* table = p.table + (long long)b * p.bt_width;
+  uint4 q1[D / 32];  // one tile's columns stay in registers
+  if (kTiles == 1) {
 #pragma unroll
-      for (int i = 0; i < (kWeigh ? 1 : kColBlock / 8); ++i) m[i][0] = m[i][1] = -INFINITY, l[i][0] = l[i][1] = 0.f;
-    }
-    long long slot, next_slot = 0;
-    KeyWords<D> words;
-    int j0 = chunk0 + 16 * warp;
-    const uint8_t* rec = nullptr;
-    if (j0 < chunk1) {
-      rec = record_of<D>(p, b, h, j0, next_slot);
-      if (rec) words.load(rec, lane);
-    }
-    for (; j0 < chunk1; j0 += 16 * kWeighWarps) {
-      const uint8_t* cur = rec;
-      slot = next_slot;
-      uint32_t a[D / 16][4];
-      if (cur) words.convert(a);
-      if (j0 + 16 * kWeighWarps < chunk1) {  // the next record's loads ahead of this one's products
-        rec = record_of<D>(p, b, h, j0 + 16 * kWeighWarps, next_slot);
-        if (rec) words.load(rec, lane);
+    for (int s = 0; s < D / 32; ++s) q1[s] = sh.q[0][s][lane];
+  }
+  for (int r0 = rec0 + warp; r0 < rec1; r0 += 32 * kWeighWarps) {
+    // where the warp's next 32 records lie: one division each
+    long long where = -1;
+    {
+      const int r = r0 + kWeighWarps * lane;
+      if (r < rec1) {
+        const int page = r / page_recs;
+        const long long block = __ldg(table + page);
+        if (block >= 0 && block < p.num_blocks) where = (block * p.Hkv + h) * page_recs + (r - page * page_recs);
+        else if (!kWeigh) atomicOr(p.err, PE_ERR_BLOCK_RANGE);
       }
-      if (!cur) {
-        if (!kWeigh && lane == 0) atomicOr(p.err, PE_ERR_BLOCK_RANGE);
-        continue;
+    }
+    const int n = min(32, (rec1 - r0 + kWeighWarps - 1) / kWeighWarps);
+    KeyWords<D> words;
+    long long next = __shfl_sync(0xffffffffu, where, 0);
+    float old0 = 0.f;
+    if (next >= 0) words.load(p.cache + next * Record<D>::kBytes, lane);
+    for (int i = 0; i < n; ++i) {
+      const long long cur = next;
+      const int j0 = 16 * (r0 + kWeighWarps * i);
+      uint32_t a[D / 16][4];
+      if (cur >= 0) words.convert(a);
+      next = __shfl_sync(0xffffffffu, where, min(i + 1, 31));
+      if (i + 1 < n && next >= 0) words.load(p.cache + next * Record<D>::kBytes, lane);  // ahead of the products
+      if (cur < 0) continue;
+      const int row = g + 8 * (lane & 3);  // (lanes with row >= 16 have none to write)
+      if (kWeigh) {
+        old0 = 0.f;
+        if (row < 16 && j0 + row < reach) {
+          if (more) old0 = p.out[cur * 16 + row];
+          else if (p.mass && j0 + row < fresh) old0 = p.mass[cur * 16 + row];
+        }
       }
       const bool edge = j0 + 16 > sh.least;
       float w0 = 0.f, w1 = 0.f;
 #pragma unroll
-      for (int i = 0; i < kColBlock / 8; ++i) {
-        if (i < tiles) {
-          float d[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int i = 0; i < kTiles; ++i) {
+        if (kTiles > 1 && i >= tiles) break;
+        float d[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-          for (int s = 0; s < D / 16; ++s) {
-            const uint2 q = sh.q[i][s][lane];
-            mma_f16(d, a[s], q.x, q.y);
-          }
-          const float2 f = *reinterpret_cast<const float2*>(&sh.factor[8 * i + t2]);
-          d[0] *= f.x, d[1] *= f.y, d[2] *= f.x, d[3] *= f.y;
-          if (edge) {
-            const int2 lim = *reinterpret_cast<const int2*>(&sh.limit[8 * i + t2]);
-            if (j0 + g >= lim.x) d[0] = -INFINITY;
-            if (j0 + g >= lim.y) d[1] = -INFINITY;
-            if (j0 + g + 8 >= lim.x) d[2] = -INFINITY;
-            if (j0 + g + 8 >= lim.y) d[3] = -INFINITY;
-          }
-          if (kWeigh) {
-            const float2 z = *reinterpret_cast<const float2*>(&sh.lse[8 * i + t2]);
-            w0 += exp2_approx(d[0] - z.x) + exp2_approx(d[1] - z.y);
-            w1 += exp2_approx(d[2] - z.x) + exp2_approx(d[3] - z.y);
-          } else {
+        for (int s = 0; s < D / 32; ++s) {
+          const uint4 q = kTiles == 1 ? q1[s] : sh.q[i][s][lane];
+          mma_f16(d, a[2 * s], q.x, q.y);
+          mma_f16(d, a[2 * s + 1], q.z, q.w);
+        }
+        const float2 f = *reinterpret_cast<const float2*>(&sh.factor[8 * i + t2]);
+        // (scores are rounded once, before the differences: from a fused one a large score's
+        // rounding would come back as an exponent)
+        mul2(d[0], d[1], f);
+        mul2(d[2], d[3], f);
+        if (edge) {
+          const int2 lim = *reinterpret_cast<const int2*>(&sh.limit[8 * i + t2]);
+          if (j0 + g >= lim.x) d[0] = -INFINITY;
+          if (j0 + g >= lim.y) d[1] = -INFINITY;
+          if (j0 + g + 8 >= lim.x) d[2] = -INFINITY;
+          if (j0 + g + 8 >= lim.y) d[3] = -INFINITY;
+        }
+        if (kWeigh) {
+          const float2 z = *reinterpret_cast<const float2*>(&sh.lse[8 * i + t2]);  // (negative: -lse)
+          const float2 x = add2(d[0], d[1], z), y = add2(d[2], d[3], z);
+          w0 += exp2_approx(x.x) + exp2_approx(x.y);
+          w1 += exp2_approx(y.x) + exp2_approx(y.y);
+        } else {
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              float& mm = m[kWeigh ? 0 : i][c];
-              float& ll = l[kWeigh ? 0 : i][c];
-              const float hi = fmaxf(d[c], d[c + 2]);
-              if (hi > mm) {
-                ll *= exp2_approx(mm - hi);
-                mm = hi;
-              }
-              if (mm > -INFINITY) ll += exp2_approx(d[c] - mm) + exp2_approx(d[c + 2] - mm);
-              else ll += d[c] + d[c + 2] == -INFINITY ? 0.f : d[c] + d[c + 2];  // a NaN stays one
+          for (int c = 0; c < 2; ++c) {
+            float& mm = st.m[i][c];
+            float& ll = st.l[i][c];
+            const float hi = fmaxf(d[c], d[c + 2]);
+            if (hi > mm) {
+              ll *= exp2_approx(mm - hi);
+              mm = hi;
             }
+            // (nothing seen yet: 2^(-infinity) is 0, and a NaN stays one)
+            const float base = mm > -INFINITY ? mm : 0.f;
+            ll += exp2_approx(d[c] - base) + exp2_approx(d[c + 2] - base);
           }
         }
       }
@@ -277,49 +292,130 @@ __global__ void __launch_bounds__(kWeighThreads) weigh_kernel(const WeighParams 
         w1 += __shfl_xor_sync(0xffffffffu, w1, 1);
         w0 += __shfl_xor_sync(0xffffffffu, w0, 2);
         w1 += __shfl_xor_sync(0xffffffffu, w1, 2);
-        if ((lane & 3) < 2) {
-          const int r = g + 8 * (lane & 3), j = j0 + r;
-          if (j < reach) {
-            // columns past the first block add to what the blocks before them wrote
-            float old = 0.f;
-            if (c0) old = p.out[slot + r];
-            else if (p.mass && j < fresh) old = p.mass[slot + r];
-            p.out[slot + r] = old + ((lane & 3) ? w1 : w0);
-          }
-        }
+        if (row < 16 && j0 + row < reach) p.out[cur * 16 + row] = old0 + ((lane & 3) ? w1 : w0);
       }
     }
+  }
+}
+
+__device__ __forceinline__ float2 merge(float2 a, float2 b) {
+  const float m = fmaxf(a.x, b.x);
+  return make_float2(m, a.y * (a.x == m ? 1.f : exp2_approx(a.x - m)) + b.y * (b.x == m ? 1.f : exp2_approx(b.x - m)));
+}
+
+// The columns' pairs over the CTA's lanes and warps, into sh.sums.
+template <int D, int kTiles>
+__device__ __forceinline__ void join_stats(WeighShared<D>& sh, int tiles, const Stats<kTiles>& st) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int i = 0; i < kTiles; ++i) {
+    if (kTiles > 1 && i >= tiles) break;
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      float2 v = make_float2(st.m[i][c], st.l[i][c]);
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1)
+        v = merge(v, make_float2(__shfl_xor_sync(0xffffffffu, v.x, o), __shfl_xor_sync(0xffffffffu, v.y, o)));
+      if ((lane >> 2) == 0) sh.join[warp][8 * i + 2 * (lane & 3) + c] = v;
+    }
+  }
+  __syncthreads();
+  for (int c = threadIdx.x; c < 8 * tiles; c += kWeighThreads) {
+    float2 v = sh.join[0][c];
+#pragma unroll
+    for (int w = 1; w < kWeighWarps; ++w) v = merge(v, sh.join[w][c]);
+    sh.sums[c] = v;
+  }
+}
+__device__ __forceinline__ float log_sum(float2 v) { return v.y == 0.f ? INFINITY : v.x + log2f(v.y); }
+
+// Rows of the request, and how far they reach (nothing: no keys).
+template <int D>
+__device__ __forceinline__ int request_reach(const WeighParams& p, WeighShared<D>& sh, int b, bool report, int& r0, int& r1) {
+  request_rows(p, b, r0, r1);
+  if (threadIdx.x == 0) sh.reach = 0;
+  __syncthreads();
+  int most = 0;
+  for (int t = r0 + threadIdx.x; t < r1; t += kWeighThreads) most = max(most, row_limit(p, t, report));
+  most = __reduce_max_sync(0xffffffffu, most);
+  if ((threadIdx.x & 31) == 0 && most) atomicMax(&sh.reach, most);
+  __syncthreads();
+  return sh.reach;
+}
+
+// Both looks in one kernel: a cluster per request and key head, the columns' sums
+// exchanged in between; the second look finds the keys in L2 (some 40 clusters at once, of
+// 2.4 MB of keys each at 32,000 keys of 128).
+template <int D, int kTiles>
+__global__ void __launch_bounds__(kWeighThreads, 2) weigh_pair_kernel(const WeighParams p) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  WeighShared<D>& sh = *reinterpret_cast<WeighShared<D>*>(smem);
+  const int C = p.chunks, rank = (int)cluster_rank();
+  const int pair = blockIdx.x / C, b = pair / p.Hkv, h = pair - b * p.Hkv;
+  if (p.offsets && !offsets_valid(p.offsets, p.B, p.T, 0)) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(p.err, PE_ERR_OFFSETS);
+    return;
+  }
+  int r0, r1;
+  const int reach = request_reach(p, sh, b, h == 0 && rank == 0, r0, r1);
+  if (reach == 0) return;
+  const int recs = (reach + 15) >> 4, per = (recs + C - 1) / C;
+  const int rec0 = min(recs, rank * per), rec1 = min(recs, rec0 + per);
+  const int columns = (r1 - r0) * p.G;
+  for (int c0 = 0; c0 < columns; c0 += 8 * kTiles) {
+    const int n = min(8 * kTiles, columns - c0), tiles = (n + 7) >> 3;
+    load_columns(p, sh, r0, h, c0, n);
+    Stats<kTiles> st;
+    st.clear();
+    sweep<D, kTiles, false>(p, sh, b, h, rec0, rec1, reach, tiles, false, st);
+    join_stats<D, kTiles>(sh, tiles, st);
+    __syncwarp();
+    cluster_sync();
+    for (int c = threadIdx.x; c < n; c += kWeighThreads) {
+      float2 v = *at_rank(&sh.sums[c], 0);
+      for (int r = 1; r < C; ++r) v = merge(v, *at_rank(&sh.sums[c], r));
+      sh.lse[c] = sh.limit[c] ? -log_sum(v) : -INFINITY;
+    }
+    cluster_sync();  // (the sums have been read)
+    __syncthreads();
+    sweep<D, kTiles, true>(p, sh, b, h, rec0, rec1, reach, tiles, c0 > 0, st);
+  }
+}
+
+// The two looks as kernels of their own, a CTA per chunk of keys: where there are too few
+// pairs of request and key head for the clusters to fill the GPU.
+template <int D, int kTiles, bool kWeigh>
+__global__ void __launch_bounds__(kWeighThreads, 2) weigh_chunk_kernel(const WeighParams p) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  WeighShared<D>& sh = *reinterpret_cast<WeighShared<D>*>(smem);
+  const int b = blockIdx.y / p.Hkv, h = blockIdx.y - b * p.Hkv;
+  int r0, r1;
+  const int reach = request_reach(p, sh, b, !kWeigh && h == 0 && blockIdx.x == 0, r0, r1);
+  if (kWeigh) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (__ldcg(p.lse + (long long)p.T * p.Hq) != 0.f) return;  // offsets no partition
+  }
+  const int rec0 = blockIdx.x * (p.chunk >> 4), rec1 = min((reach + 15) >> 4, rec0 + (p.chunk >> 4));
+  if (rec0 >= rec1) return;
+  const int columns = (r1 - r0) * p.G;
+  for (int c0 = 0; c0 < columns; c0 += 8 * kTiles) {
+    const int n = min(8 * kTiles, columns - c0), tiles = (n + 7) >> 3;
+    load_columns(p, sh, r0, h, c0, n);
+    Stats<kTiles> st;
     if (!kWeigh) {
-      // a column's pair over the lanes of its quad column, then over the warps
-      float2* join = reinterpret_cast<float2*>(smem + sizeof(WeighShared<D>));  // [warps][kColBlock]
-#pragma unroll
-      for (int i = 0; i < kColBlock / 8; ++i) {
-        if (i < tiles) {
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            float mm = m[kWeigh ? 0 : i][c], ll = l[kWeigh ? 0 : i][c];
-#pragma unroll
-            for (int o = 4; o < 32; o <<= 1) {
-              const float m2 = __shfl_xor_sync(0xffffffffu, mm, o), l2 = __shfl_xor_sync(0xffffffffu, ll, o);
-              const float hi = fmaxf(mm, m2);
-              ll = ll * (mm == hi ? 1.f : exp2_approx(mm - hi)) + l2 * (m2 == hi ? 1.f : exp2_approx(m2 - hi));
-              mm = hi;
-            }
-            if (g == 0) join[warp * kColBlock + 8 * i + t2 + c] = make_float2(mm, ll);
-          }
-        }
-      }
+      st.clear();
+      sweep<D, kTiles, false>(p, sh, b, h, rec0, rec1, reach, tiles, false, st);
+      join_stats<D, kTiles>(sh, tiles, st);
       __syncthreads();
-      for (int c = threadIdx.x; c < n; c += kWeighThreads) {
-        float mm = -INFINITY, ll = 0.f;
-        for (int w = 0; w < kWeighWarps; ++w) mm = fmaxf(mm, join[w * kColBlock + c].x);
-        for (int w = 0; w < kWeighWarps; ++w) {
-          const float2 v = join[w * kColBlock + c];
-          ll += v.y * (v.x == mm ? 1.f : exp2_approx(v.x - mm));
-        }
-        const int row = r0 + (c0 + c) / p.G, head = h * p.G + (c0 + c) % p.G;
-        p.parts[((long long)blockIdx.x * p.T + row) * p.Hq + head] = make_float2(mm, ll);
-      }
+    }
+    for (int c = threadIdx.x; c < n; c += kWeighThreads) {
+      const long long at = (long long)(r0 + (c0 + c) / p.G) * p.Hq + h * p.G + (c0 + c) % p.G;
+      if (kWeigh) sh.lse[c] = -__ldcg(p.lse + at);
+      else p.parts[(long long)blockIdx.x * p.T * p.Hq + at] = sh.sums[c];
+    }
+    if (kWeigh) {
+      __syncthreads();
+      sweep<D, kTiles, true>(p, sh, b, h, rec0, rec1, reach, tiles, c0 > 0, st);
     }
   }
 }
@@ -337,14 +433,9 @@ __global__ void __launch_bounds__(kWeighThreads) weigh_join_kernel(const WeighPa
   if (i >= (long long)p.T * p.Hq) return;
   const int limit = row_limit(p, (int)(i / p.Hq), false);
   const int n = (limit + p.chunk - 1) / p.chunk;
-  float m = -INFINITY, l = 0.f;
-  for (int c = 0; c < n; ++c) {
-    const float2 v = __ldcg(p.parts + (long long)c * p.T * p.Hq + i);
-    const float hi = fmaxf(m, v.x);
-    l = l * (m == hi ? 1.f : exp2_approx(m - hi)) + v.y * (v.x == hi ? 1.f : exp2_approx(v.x - hi));
-    m = hi;
-  }
-  p.lse[i] = l == 0.f ? INFINITY : m + log2f(l);
+  float2 v = make_float2(-INFINITY, 0.f);
+  for (int c = 0; c < n; ++c) v = merge(v, __ldcg(p.parts + (long long)c * p.T * p.Hq + i));
+  p.lse[i] = log_sum(v);
 }
 
 }  // namespace pe
@@ -356,6 +447,32 @@ int weigh_chunk(int B, int Hkv, int64_t keys) {
   int chunk = 2048;
   while (chunk > 128 && (int64_t)B * Hkv * ((keys + chunk - 1) / chunk) < 4096) chunk /= 2;
   return chunk;
+}
+
+template <int D, int kTiles>
+int weigh(pe::WeighParams p, bool pairs, cudaStream_t st) {
+  constexpr int kSmem = (int)sizeof(pe::WeighShared<D>);
+  static std::atomic<unsigned long long> done[3];
+  if (pairs) {
+    // eight CTAs a cluster where the batch is large: its keys at work then fit L2
+    auto kernel = pe::weigh_pair_kernel<D, kTiles>;
+    if (!pe_host::allow_smem(kernel, kSmem, done[0])) return PE_ECUDA;
+    p.chunks = p.B * p.Hkv >= 64 ? 8 : 16;
+    if (p.chunks > 8 && cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+      return PE_ECUDA;
+    const unsigned grid = (unsigned)(p.B * p.Hkv * p.chunks);
+    const cudaError_t rc = pe_host::launch_clusters(kernel, grid, pe::kWeighThreads, p.chunks, kSmem, false, st, p);
+    return rc == cudaSuccess ? pe_host::launch_status() : PE_ECUDA;
+  }
+  auto stats = pe::weigh_chunk_kernel<D, kTiles, false>;
+  auto weigh = pe::weigh_chunk_kernel<D, kTiles, true>;
+  if (!pe_host::allow_smem(stats, kSmem, done[1]) || !pe_host::allow_smem(weigh, kSmem, done[2])) return PE_ECUDA;
+  const dim3 grid(p.chunks, p.B * p.Hkv);
+  stats<<<grid, pe::kWeighThreads, kSmem, st>>>(p);
+  const unsigned cols = (unsigned)(((int64_t)p.T * p.Hq + pe::kWeighThreads - 1) / pe::kWeighThreads);
+  pe::weigh_join_kernel<<<cols, pe::kWeighThreads, 0, st>>>(p);
+  weigh<<<grid, pe::kWeighThreads, kSmem, st>>>(p);
+  return pe_host::launch_status();
 }
 
 }  // namespace
@@ -399,19 +516,14 @@ int pe_kv_weigh(const pe_kv_weigh_args* a, void* stream) {
   p.lse = reinterpret_cast<float*>(p.parts + (size_t)p.chunks * p.T * p.Hq);
   p.err = a->err;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const dim3 grid(p.chunks, p.B * p.Hkv);
-  auto stats = a->D == 64 ? pe::weigh_kernel<64, false> : pe::weigh_kernel<128, false>;
-  auto weigh = a->D == 64 ? pe::weigh_kernel<64, true> : pe::weigh_kernel<128, true>;
-  const int fixed = a->D == 64 ? (int)sizeof(pe::WeighShared<64>) : (int)sizeof(pe::WeighShared<128>);
-  const int join = fixed + (int)sizeof(float2) * pe::kWeighWarps * pe::kColBlock;
-  static std::atomic<unsigned long long> done[4];
-  if (!pe_host::allow_smem(stats, join, done[a->D == 64]) || !pe_host::allow_smem(weigh, fixed, done[2 + (a->D == 64)]))
-    return PE_ECUDA;
-  stats<<<grid, pe::kWeighThreads, join, st>>>(p);
-  const unsigned cols = (unsigned)(((int64_t)p.T * p.Hq + pe::kWeighThreads - 1) / pe::kWeighThreads);
-  pe::weigh_join_kernel<<<cols, pe::kWeighThreads, 0, st>>>(p);
-  weigh<<<grid, pe::kWeighThreads, fixed, st>>>(p);
-  return pe_host::launch_status();
+  pe_host::DeviceInfo dev;
+  if (pe_host::device_info(&dev) != PE_OK) return PE_ECUDA;
+  // columns of a request that has its even share of the rows
+  const int64_t columns = ((int64_t)p.T + p.B - 1) / p.B * p.G;
+  const bool pairs = (int64_t)p.B * p.Hkv * 16 >= dev.sm_count / 2;
+  if (a->D == 64)
+    return columns <= 8 ? weigh<64, 1>(p, pairs, st) : columns <= 32 ? weigh<64, 4>(p, pairs, st) : weigh<64, 16>(p, pairs, st);
+  return columns <= 8 ? weigh<128, 1>(p, pairs, st) : columns <= 32 ? weigh<128, 4>(p, pairs, st) : weigh<128, 16>(p, pairs, st);
 }
 
 }  // extern "C"
