@@ -14,6 +14,7 @@
 // belongs to one warp: no atomics, the same result every time.
 #include "pe_cluster.cuh"
 #include "pe_kv.cuh"
+#include "pe_tma.cuh"
 
 namespace pe {
 
@@ -37,7 +38,7 @@ struct WeighParams {
 
 constexpr int kWeighThreads = 256;
 constexpr int kWeighWarps = kWeighThreads / 32;
-constexpr int kColBlock = 128;  // columns of one sweep over a chunk
+constexpr int kStages = 4;      // records of a warp on their way
 
 __device__ __forceinline__ float exp2_approx(float x) {
   float y;
@@ -90,16 +91,21 @@ __device__ __forceinline__ void request_rows(const WeighParams& p, int b, int& r
   }
 }
 
-template <int D>
+// kTiles: tiles of eight columns that one look takes.
+template <int D, int kTiles>
 struct WeighShared {
-  uint4 q[kColBlock / 8][D / 32][32];  // columns as B fragments, eight at a time, two steps in a word
-  float factor[kColBlock];  // scale * log2(e) and the power of two taken out of a column
-  float lse[kColBlock];     // minus the log2-sum of a column; -infinity: no weight
-  int limit[kColBlock];
-  float2 sums[kColBlock];   // this CTA's maximum and sum of a column
-  float2 join[kWeighWarps][kColBlock];
-  int least;                // of the columns' limits
-  int reach;                // of all the request's rows
+  static constexpr int kCols = 8 * kTiles;
+  static constexpr int kCodes = 16 * Record<D>::kRow, kScales = 16 * Record<D>::kScaleRow;
+  uint8_t ring[kWeighWarps][kStages][kCodes + kScales];  // the keys of records
+  uint4 q[kTiles][D / 32][32];  // columns as B fragments, eight at a time, two steps in a word
+  uint64_t bars[kWeighWarps][kStages];
+  float factor[kCols];  // scale * log2(e) and the power of two taken out of a column
+  float lse[kCols];     // minus the log2-sum of a column; -infinity: no weight
+  int limit[kCols];
+  float2 sums[kCols];   // this CTA's maximum and sum of a column
+  float2 join[kWeighWarps][kCols];
+  int least;            // of the columns' limits
+  int reach;            // of all the request's rows
 };
 
 // One warp's lanes' part of a record's keys: rows g and g + 8, elements t D/4 .. (t+1) D/4
@@ -108,20 +114,20 @@ template <int D>
 struct KeyWords {
   uint4 code[2];
   uint32_t scale[2];
-  __device__ __forceinline__ void load(const uint8_t* rec, int lane) {
+  __device__ __forceinline__ void load(const uint8_t* keys, int lane) {  // codes, then scales
     using R = Record<D>;
     const int g = lane >> 2, t = lane & 3;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const uint8_t* c = rec + R::kK + (g + 8 * i) * R::kRow + t * (D / 8);
-      const uint8_t* s = rec + R::kKs + (g + 8 * i) * R::kScaleRow;
+      const uint8_t* c = keys + (g + 8 * i) * R::kRow + t * (D / 8);
+      const uint8_t* s = keys + 16 * R::kRow + (g + 8 * i) * R::kScaleRow;
       if (D == 128) {
-        code[i] = __ldg(reinterpret_cast<const uint4*>(c));
-        scale[i] = __ldg(reinterpret_cast<const unsigned short*>(s) + t);
+        code[i] = *reinterpret_cast<const uint4*>(c);
+        scale[i] = reinterpret_cast<const unsigned short*>(s)[t];
       } else {
-        const uint2 v = __ldg(reinterpret_cast<const uint2*>(c));
+        const uint2 v = *reinterpret_cast<const uint2*>(c);
         code[i] = make_uint4(v.x, v.y, 0u, 0u);
-        scale[i] = __ldg(s + t);
+        scale[i] = s[t];
       }
     }
   }
@@ -146,8 +152,8 @@ struct KeyWords {
 };
 
 // Columns c0.. of the request's rows from r0 on, key head h, into shared memory.
-template <int D>
-__device__ __forceinline__ void load_columns(const WeighParams& p, WeighShared<D>& sh, int r0, int h, int c0, int n) {
+template <int D, int kTiles>
+__device__ __forceinline__ void load_columns(const WeighParams& p, WeighShared<D, kTiles>& sh, int r0, int h, int c0, int n) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   __syncthreads();  // the last sweep's readers
   if (threadIdx.x == 0) sh.least = INT32_MAX;
@@ -197,8 +203,8 @@ struct Stats {
 // record's sixteen tokens against all columns: kWeigh: the sum over columns of
 // 2^(score - lse) goes to out; else the columns' statistics.
 template <int D, int kTiles, bool kWeigh>
-__device__ __forceinline__ void sweep(const WeighParams& p, const WeighShared<D>& sh, int b, int h, int rec0, int rec1, int reach,
-                                      int tiles, bool more, Stats<kTiles>& st) {
+__device__ __forceinline__ void sweep(const WeighParams& p, WeighShared<D, kTiles>& sh, int b, int h, int rec0, int rec1, int reach,
+                                      int tiles, bool more, uint32_t& turn, Stats<kTiles>& st) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t2 = 2 * (lane & 3);
   const int fresh = kWeigh && p.fresh ? __ldg(p.fresh + b) : INT32_MAX;
@@ -222,26 +228,57 @@ __device__ __forceinline__ void sweep(const WeighParams& p, const WeighShared<D>
       }
     }
     const int n = min(32, (rec1 - r0 + kWeighWarps - 1) / kWeighWarps);
-    KeyWords<D> words;
-    long long next = __shfl_sync(0xffffffffu, where, 0);
-    float old0 = 0.f;
-    if (next >= 0) words.load(p.cache + next * Record<D>::kBytes, lane);
-    for (int i = 0; i < n; ++i) {
-      const long long cur = next;
-      const int j0 = 16 * (r0 + kWeighWarps * i);
-      uint32_t a[D / 16][4];
-      if (cur >= 0) words.convert(a);
-      next = __shfl_sync(0xffffffffu, where, min(i + 1, 31));
-      if (i + 1 < n && next >= 0) words.load(p.cache + next * Record<D>::kBytes, lane);  // ahead of the products
-      if (cur < 0) continue;
-      const int row = g + 8 * (lane & 3);  // (lanes with row >= 16 have none to write)
-      if (kWeigh) {
-        old0 = 0.f;
-        if (row < 16 && j0 + row < reach) {
-          if (more) old0 = p.out[cur * 16 + row];
-          else if (p.mass && j0 + row < fresh) old0 = p.mass[cur * 16 + row];
-        }
+    const uint32_t live = __ballot_sync(0xffffffffu, where >= 0);  // (the first n lanes' at most)
+    // a lane sends for its own record
+    auto send = [&](int i, uint32_t at) {
+      if (lane == i && where >= 0) {
+        using W = WeighShared<D, kTiles>;
+        uint64_t* bar = &sh.bars[warp][at % kStages];
+        uint8_t* to = sh.ring[warp][at % kStages];
+        const uint8_t* rec = p.cache + where * Record<D>::kBytes;
+        mbar_arrive_expect_tx(bar, W::kCodes + W::kScales);
+        bulk_load(to, rec + Record<D>::kK, W::kCodes, bar);
+        bulk_load(to + W::kCodes, rec + Record<D>::kKs, W::kScales, bar);
       }
+    };
+    auto old_of = [&](int i) {  // what this lane's key of record i had
+      const int row = g + 8 * (lane & 3), j = 16 * (r0 + kWeighWarps * i) + row;
+      const long long at = __shfl_sync(0xffffffffu, where, i) * 16 + row;
+      float v = 0.f;
+      if (row < 16 && j < reach && (live >> i & 1)) {
+        if (more) v = p.out[at];
+        else if (p.mass && j < fresh) v = p.mass[at];
+      }
+      return v;
+    };
+    for (int i = 0; i < min(n, kStages - 1); ++i) send(i, turn + i);
+    float old = kWeigh ? old_of(0) : 0.f;
+    for (int i = 0; i < n; ++i) {
+      const uint32_t at = turn + i;
+      __syncwarp();  // (the stage that comes next has been read)
+      if (i + kStages - 1 < n) send(i + kStages - 1, at + kStages - 1);
+      const float old0 = old;
+      if (kWeigh && i + 1 < n) old = old_of(i + 1);
+      if (!(live >> i & 1)) {
+        // (its stage was not used: it counts as done)
+        if (lane == 0) mbar_arrive_expect_tx(&sh.bars[warp][at % kStages], 0);
+        __syncwarp();
+        (void)mbar_wait(&sh.bars[warp][at % kStages], (at / kStages) & 1);
+        continue;
+      }
+      const int j0 = 16 * (r0 + kWeighWarps * i);
+      if (!mbar_wait(&sh.bars[warp][at % kStages], (at / kStages) & 1)) {
+        atomicOr(p.err, PE_ERR_TIMEOUT);
+        (void)mbar_wait(&sh.bars[warp][at % kStages], (at / kStages) & 1);
+      }
+      uint32_t a[D / 16][4];
+      {
+        KeyWords<D> words;
+        words.load(sh.ring[warp][at % kStages], lane);
+        words.convert(a);
+      }
+      const long long cur = kWeigh ? __shfl_sync(0xffffffffu, where, i) : 0;
+      const int row = g + 8 * (lane & 3);  // (lanes with row >= 16 have none to write)
       const bool edge = j0 + 16 > sh.least;
       float w0 = 0.f, w1 = 0.f;
 #pragma unroll
@@ -295,6 +332,8 @@ __device__ __forceinline__ void sweep(const WeighParams& p, const WeighShared<D>
         if (row < 16 && j0 + row < reach) p.out[cur * 16 + row] = old0 + ((lane & 3) ? w1 : w0);
       }
     }
+    turn += n;
+    __syncwarp();
   }
 }
 
@@ -305,7 +344,7 @@ __device__ __forceinline__ float2 merge(float2 a, float2 b) {
 
 // The columns' pairs over the CTA's lanes and warps, into sh.sums.
 template <int D, int kTiles>
-__device__ __forceinline__ void join_stats(WeighShared<D>& sh, int tiles, const Stats<kTiles>& st) {
+__device__ __forceinline__ void join_stats(WeighShared<D, kTiles>& sh, int tiles, const Stats<kTiles>& st) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int i = 0; i < kTiles; ++i) {
@@ -330,10 +369,14 @@ __device__ __forceinline__ void join_stats(WeighShared<D>& sh, int tiles, const 
 __device__ __forceinline__ float log_sum(float2 v) { return v.y == 0.f ? INFINITY : v.x + log2f(v.y); }
 
 // Rows of the request, and how far they reach (nothing: no keys).
-template <int D>
-__device__ __forceinline__ int request_reach(const WeighParams& p, WeighShared<D>& sh, int b, bool report, int& r0, int& r1) {
+template <int D, int kTiles>
+__device__ __forceinline__ int request_reach(const WeighParams& p, WeighShared<D, kTiles>& sh, int b, bool report, int& r0, int& r1) {
   request_rows(p, b, r0, r1);
   if (threadIdx.x == 0) sh.reach = 0;
+  if (threadIdx.x < kWeighWarps * kStages) {
+    mbar_init(&sh.bars[0][0] + threadIdx.x, 1);
+    mbar_init_fence();
+  }
   __syncthreads();
   int most = 0;
   for (int t = r0 + threadIdx.x; t < r1; t += kWeighThreads) most = max(most, row_limit(p, t, report));
@@ -347,9 +390,9 @@ __device__ __forceinline__ int request_reach(const WeighParams& p, WeighShared<D
 // exchanged in between; the second look finds the keys in L2 (some 40 clusters at once, of
 // 2.4 MB of keys each at 32,000 keys of 128).
 template <int D, int kTiles>
-__global__ void __launch_bounds__(kWeighThreads, 2) weigh_pair_kernel(const WeighParams p) {
-  extern __shared__ __align__(16) unsigned char smem[];
-  WeighShared<D>& sh = *reinterpret_cast<WeighShared<D>*>(smem);
+__global__ void __launch_bounds__(kWeighThreads, kTiles == 1 ? 4 : 2) weigh_pair_kernel(const WeighParams p) {
+  extern __shared__ __align__(128) unsigned char smem[];
+  WeighShared<D, kTiles>& sh = *reinterpret_cast<WeighShared<D, kTiles>*>(smem);
   const int C = p.chunks, rank = (int)cluster_rank();
   const int pair = blockIdx.x / C, b = pair / p.Hkv, h = pair - b * p.Hkv;
   if (p.offsets && !offsets_valid(p.offsets, p.B, p.T, 0)) {
@@ -362,12 +405,13 @@ __global__ void __launch_bounds__(kWeighThreads, 2) weigh_pair_kernel(const Weig
   const int recs = (reach + 15) >> 4, per = (recs + C - 1) / C;
   const int rec0 = min(recs, rank * per), rec1 = min(recs, rec0 + per);
   const int columns = (r1 - r0) * p.G;
+  uint32_t turn = 0;  // of the warp's ring
   for (int c0 = 0; c0 < columns; c0 += 8 * kTiles) {
     const int n = min(8 * kTiles, columns - c0), tiles = (n + 7) >> 3;
     load_columns(p, sh, r0, h, c0, n);
     Stats<kTiles> st;
     st.clear();
-    sweep<D, kTiles, false>(p, sh, b, h, rec0, rec1, reach, tiles, false, st);
+    sweep<D, kTiles, false>(p, sh, b, h, rec0, rec1, reach, tiles, false, turn, st);
     join_stats<D, kTiles>(sh, tiles, st);
     __syncwarp();
     cluster_sync();
@@ -378,16 +422,16 @@ __global__ void __launch_bounds__(kWeighThreads, 2) weigh_pair_kernel(const Weig
     }
     cluster_sync();  // (the sums have been read)
     __syncthreads();
-    sweep<D, kTiles, true>(p, sh, b, h, rec0, rec1, reach, tiles, c0 > 0, st);
+    sweep<D, kTiles, true>(p, sh, b, h, rec0, rec1, reach, tiles, c0 > 0, turn, st);
   }
 }
 
 // The two looks as kernels of their own, a CTA per chunk of keys: where there are too few
 // pairs of request and key head for the clusters to fill the GPU.
 template <int D, int kTiles, bool kWeigh>
-__global__ void __launch_bounds__(kWeighThreads, 2) weigh_chunk_kernel(const WeighParams p) {
-  extern __shared__ __align__(16) unsigned char smem[];
-  WeighShared<D>& sh = *reinterpret_cast<WeighShared<D>*>(smem);
+__global__ void __launch_bounds__(kWeighThreads, kTiles == 1 ? 4 : 2) weigh_chunk_kernel(const WeighParams p) {
+  extern __shared__ __align__(128) unsigned char smem[];
+  WeighShared<D, kTiles>& sh = *reinterpret_cast<WeighShared<D, kTiles>*>(smem);
   const int b = blockIdx.y / p.Hkv, h = blockIdx.y - b * p.Hkv;
   int r0, r1;
   const int reach = request_reach(p, sh, b, !kWeigh && h == 0 && blockIdx.x == 0, r0, r1);
@@ -398,13 +442,14 @@ __global__ void __launch_bounds__(kWeighThreads, 2) weigh_chunk_kernel(const Wei
   const int rec0 = blockIdx.x * (p.chunk >> 4), rec1 = min((reach + 15) >> 4, rec0 + (p.chunk >> 4));
   if (rec0 >= rec1) return;
   const int columns = (r1 - r0) * p.G;
+  uint32_t turn = 0;  // of the warp's ring
   for (int c0 = 0; c0 < columns; c0 += 8 * kTiles) {
     const int n = min(8 * kTiles, columns - c0), tiles = (n + 7) >> 3;
     load_columns(p, sh, r0, h, c0, n);
     Stats<kTiles> st;
     if (!kWeigh) {
       st.clear();
-      sweep<D, kTiles, false>(p, sh, b, h, rec0, rec1, reach, tiles, false, st);
+      sweep<D, kTiles, false>(p, sh, b, h, rec0, rec1, reach, tiles, false, turn, st);
       join_stats<D, kTiles>(sh, tiles, st);
       __syncthreads();
     }
@@ -415,7 +460,7 @@ __global__ void __launch_bounds__(kWeighThreads, 2) weigh_chunk_kernel(const Wei
     }
     if (kWeigh) {
       __syncthreads();
-      sweep<D, kTiles, true>(p, sh, b, h, rec0, rec1, reach, tiles, c0 > 0, st);
+      sweep<D, kTiles, true>(p, sh, b, h, rec0, rec1, reach, tiles, c0 > 0, turn, st);
     }
   }
 }
@@ -451,7 +496,7 @@ int weigh_chunk(int B, int Hkv, int64_t keys) {
 
 template <int D, int kTiles>
 int weigh(pe::WeighParams p, bool pairs, cudaStream_t st) {
-  constexpr int kSmem = (int)sizeof(pe::WeighShared<D>);
+  constexpr int kSmem = (int)sizeof(pe::WeighShared<D, kTiles>);
   static std::atomic<unsigned long long> done[3];
   if (pairs) {
     // eight CTAs a cluster where the batch is large: its keys at work then fit L2
