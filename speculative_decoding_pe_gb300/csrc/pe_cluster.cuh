@@ -47,7 +47,7 @@ namespace pe_host {
 // A launch in clusters of C CTAs; `dependent`: the kernel may start before the one
 // ahead of it on the stream has finished, and waits for it (griddepcontrol.wait).
 template <class K, class P>
-cudaError_t launch_clusters(K kernel, unsigned grid, int threads, int C, size_t smem, bool dependent, cudaStream_t st,
+cudaError_t launch_clusters(K kernel, dim3 grid, int threads, int C, size_t smem, bool dependent, cudaStream_t st,
                             const P& p) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
@@ -56,7 +56,7 @@ cudaError_t launch_clusters(K kernel, unsigned grid, int threads, int C, size_t 
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;

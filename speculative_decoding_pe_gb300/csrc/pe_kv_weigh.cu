@@ -136,9 +136,10 @@ struct KeyWords {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const uint32_t w[4] = {code[i].x, code[i].y, code[i].z, code[i].w};
+      const uint32_t both = e4m3x2_f16x2(scale[i]);  // the scales of the lane's two groups (D = 64: one)
 #pragma unroll
       for (int j = 0; j < D / 32; ++j) {
-        const uint32_t f = e4m3_f16x2((scale[i] >> (8 * (j / 2))) & 0xffu);
+        const uint32_t f = __byte_perm(both, 0, j < 2 ? 0x1010 : 0x3232);
         uint32_t v[4];
         e2m1x8_f16(w[j], v);
 #pragma unroll
@@ -189,13 +190,15 @@ __device__ __forceinline__ void load_columns(const WeighParams& p, WeighShared<D
   __syncthreads();
 }
 
+constexpr float kLowest = -3.4e38f;  // below every score (finite: nothing less it is no NaN)
+
 // Running maximum and sum of two columns of each tile, over a lane's rows.
 template <int kTiles>
 struct Stats {
   float m[kTiles][2], l[kTiles][2];
   __device__ __forceinline__ void clear() {
 #pragma unroll
-    for (int i = 0; i < kTiles; ++i) m[i][0] = m[i][1] = -INFINITY, l[i][0] = l[i][1] = 0.f;
+    for (int i = 0; i < kTiles; ++i) m[i][0] = m[i][1] = kLowest, l[i][0] = l[i][1] = 0.f;
   }
 };
 
@@ -229,10 +232,11 @@ __device__ __forceinline__ void sweep(const WeighParams& p, WeighShared<D, kTile
     }
     const int n = min(32, (rec1 - r0 + kWeighWarps - 1) / kWeighWarps);
     const uint32_t live = __ballot_sync(0xffffffffu, where >= 0);  // (the first n lanes' at most)
-    // a lane sends for its own record
-    auto send = [&](int i, uint32_t at) {
-      if (lane == i && where >= 0) {
-        using W = WeighShared<D, kTiles>;
+    using W = WeighShared<D, kTiles>;
+    // lanes send for their own records: of [i, i + 2)
+    auto send = [&](int i, int many) {
+      if (lane >= i && lane < min(i + many, n) && where >= 0) {
+        const uint32_t at = turn + lane;
         uint64_t* bar = &sh.bars[warp][at % kStages];
         uint8_t* to = sh.ring[warp][at % kStages];
         const uint8_t* rec = p.cache + where * Record<D>::kBytes;
@@ -251,12 +255,14 @@ __device__ __forceinline__ void sweep(const WeighParams& p, WeighShared<D, kTile
       }
       return v;
     };
-    for (int i = 0; i < min(n, kStages - 1); ++i) send(i, turn + i);
+    send(0, 2);
     float old = kWeigh ? old_of(0) : 0.f;
     for (int i = 0; i < n; ++i) {
       const uint32_t at = turn + i;
-      __syncwarp();  // (the stage that comes next has been read)
-      if (i + kStages - 1 < n) send(i + kStages - 1, at + kStages - 1);
+      if ((i & 1) == 0) {
+        __syncwarp();  // (the stages that come next have been read)
+        send(i + 2, 2);
+      }
       const float old0 = old;
       if (kWeigh && i + 1 < n) old = old_of(i + 1);
       if (!(live >> i & 1)) {
@@ -309,19 +315,18 @@ __device__ __forceinline__ void sweep(const WeighParams& p, WeighShared<D, kTile
           w0 += exp2_approx(x.x) + exp2_approx(x.y);
           w1 += exp2_approx(y.x) + exp2_approx(y.y);
         } else {
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            float& mm = st.m[i][c];
-            float& ll = st.l[i][c];
-            const float hi = fmaxf(d[c], d[c + 2]);
-            if (hi > mm) {
-              ll *= exp2_approx(mm - hi);
-              mm = hi;
-            }
-            // (nothing seen yet: 2^(-infinity) is 0, and a NaN stays one)
-            const float base = mm > -INFINITY ? mm : 0.f;
-            ll += exp2_approx(d[c] - base) + exp2_approx(d[c + 2] - base);
+          const float hi0 = fmaxf(d[0], d[2]), hi1 = fmaxf(d[1], d[3]);
+          if (hi0 > st.m[i][0] || hi1 > st.m[i][1]) {  // rare after the first records
+            const float m0 = fmaxf(st.m[i][0], hi0), m1 = fmaxf(st.m[i][1], hi1);
+            st.l[i][0] *= exp2_approx(st.m[i][0] - m0);
+            st.l[i][1] *= exp2_approx(st.m[i][1] - m1);
+            st.m[i][0] = m0;
+            st.m[i][1] = m1;
           }
+          const float2 low = make_float2(-st.m[i][0], -st.m[i][1]);
+          const float2 x = add2(d[0], d[1], low), y = add2(d[2], d[3], low);
+          st.l[i][0] += exp2_approx(x.x) + exp2_approx(y.x);
+          st.l[i][1] += exp2_approx(x.y) + exp2_approx(y.y);
         }
       }
       if (kWeigh) {
@@ -390,7 +395,7 @@ __device__ __forceinline__ int request_reach(const WeighParams& p, WeighShared<D
 // exchanged in between; the second look finds the keys in L2 (some 40 clusters at once, of
 // 2.4 MB of keys each at 32,000 keys of 128).
 template <int D, int kTiles>
-__global__ void __launch_bounds__(kWeighThreads, kTiles == 1 ? 4 : 2) weigh_pair_kernel(const WeighParams p) {
+__global__ void __launch_bounds__(kWeighThreads, 2) weigh_pair_kernel(const WeighParams p) {
   extern __shared__ __align__(128) unsigned char smem[];
   WeighShared<D, kTiles>& sh = *reinterpret_cast<WeighShared<D, kTiles>*>(smem);
   const int C = p.chunks, rank = (int)cluster_rank();
@@ -478,7 +483,7 @@ __global__ void __launch_bounds__(kWeighThreads) weigh_join_kernel(const WeighPa
   if (i >= (long long)p.T * p.Hq) return;
   const int limit = row_limit(p, (int)(i / p.Hq), false);
   const int n = (limit + p.chunk - 1) / p.chunk;
-  float2 v = make_float2(-INFINITY, 0.f);
+  float2 v = make_float2(kLowest, 0.f);
   for (int c = 0; c < n; ++c) v = merge(v, __ldcg(p.parts + (long long)c * p.T * p.Hq + i));
   p.lse[i] = log_sum(v);
 }
@@ -489,24 +494,29 @@ namespace {
 
 // Keys of a chunk: as many as keep the GPU in work.
 int weigh_chunk(int B, int Hkv, int64_t keys) {
-  int chunk = 2048;
+  int chunk = 4096;
   while (chunk > 128 && (int64_t)B * Hkv * ((keys + chunk - 1) / chunk) < 4096) chunk /= 2;
   return chunk;
 }
 
+// Little work: pairs, one launch (one token over 4000 keys of 8 heads 14 us; three launches 19).
+// Else one tile of columns: chunks (b256 tokens 1.18 ms; the pair kernel 1.38, at its 128 registers);
+// more: pairs, where these fill the GPU (b64 drafts 1.34 ms; chunks 1.51).
 template <int D, int kTiles>
-int weigh(pe::WeighParams p, bool pairs, cudaStream_t st) {
+int weigh(pe::WeighParams p, int sms, cudaStream_t st) {
   constexpr int kSmem = (int)sizeof(pe::WeighShared<D, kTiles>);
   static std::atomic<unsigned long long> done[3];
-  if (pairs) {
-    // eight CTAs a cluster where the batch is large: its keys at work then fit L2
+  const int64_t keys = (int64_t)p.bt_width * p.block_size, pairs = (int64_t)p.B * p.Hkv;
+  const bool small = pairs * keys <= (int64_t)sms * 2048;
+  if (small || (kTiles > 1 && pairs * 4 >= sms / 2)) {
     auto kernel = pe::weigh_pair_kernel<D, kTiles>;
     if (!pe_host::allow_smem(kernel, kSmem, done[0])) return PE_ECUDA;
-    p.chunks = p.B * p.Hkv >= 64 ? 8 : 16;
+    p.chunks = 4;  // (CTAs of a cluster; eight: 1.46 ms, sixteen: 2.16)
+    while (small && p.chunks < 16 && pairs * p.chunks * 2 <= sms && keys > 256 * p.chunks) p.chunks *= 2;
     if (p.chunks > 8 && cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
       return PE_ECUDA;
-    const unsigned grid = (unsigned)(p.B * p.Hkv * p.chunks);
-    const cudaError_t rc = pe_host::launch_clusters(kernel, grid, pe::kWeighThreads, p.chunks, kSmem, false, st, p);
+    const cudaError_t rc = pe_host::launch_clusters(kernel, dim3((unsigned)(pairs * p.chunks)), pe::kWeighThreads, p.chunks, kSmem,
+                                                    false, st, p);
     return rc == cudaSuccess ? pe_host::launch_status() : PE_ECUDA;
   }
   auto stats = pe::weigh_chunk_kernel<D, kTiles, false>;
@@ -514,10 +524,11 @@ int weigh(pe::WeighParams p, bool pairs, cudaStream_t st) {
   if (!pe_host::allow_smem(stats, kSmem, done[1]) || !pe_host::allow_smem(weigh, kSmem, done[2])) return PE_ECUDA;
   const dim3 grid(p.chunks, p.B * p.Hkv);
   stats<<<grid, pe::kWeighThreads, kSmem, st>>>(p);
+  // the other two may start while the one before drains, and wait in the kernel for it
   const unsigned cols = (unsigned)(((int64_t)p.T * p.Hq + pe::kWeighThreads - 1) / pe::kWeighThreads);
-  pe::weigh_join_kernel<<<cols, pe::kWeighThreads, 0, st>>>(p);
-  weigh<<<grid, pe::kWeighThreads, kSmem, st>>>(p);
-  return pe_host::launch_status();
+  cudaError_t rc = pe_host::launch_clusters(pe::weigh_join_kernel, dim3(cols), pe::kWeighThreads, 1, 0, true, st, p);
+  if (rc == cudaSuccess) rc = pe_host::launch_clusters(weigh, grid, pe::kWeighThreads, 1, kSmem, true, st, p);
+  return rc == cudaSuccess ? pe_host::launch_status() : PE_ECUDA;
 }
 
 }  // namespace
@@ -565,10 +576,9 @@ int pe_kv_weigh(const pe_kv_weigh_args* a, void* stream) {
   if (pe_host::device_info(&dev) != PE_OK) return PE_ECUDA;
   // columns of a request that has its even share of the rows
   const int64_t columns = ((int64_t)p.T + p.B - 1) / p.B * p.G;
-  const bool pairs = (int64_t)p.B * p.Hkv * 16 >= dev.sm_count / 2;
   if (a->D == 64)
-    return columns <= 8 ? weigh<64, 1>(p, pairs, st) : columns <= 32 ? weigh<64, 4>(p, pairs, st) : weigh<64, 16>(p, pairs, st);
-  return columns <= 8 ? weigh<128, 1>(p, pairs, st) : columns <= 32 ? weigh<128, 4>(p, pairs, st) : weigh<128, 16>(p, pairs, st);
+    return columns <= 8 ? weigh<64, 1>(p, dev.sm_count, st) : columns <= 32 ? weigh<64, 4>(p, dev.sm_count, st) : weigh<64, 16>(p, dev.sm_count, st);
+  return columns <= 8 ? weigh<128, 1>(p, dev.sm_count, st) : columns <= 32 ? weigh<128, 4>(p, dev.sm_count, st) : weigh<128, 16>(p, dev.sm_count, st);
 }
 
 }  // extern "C"
