@@ -1,10 +1,12 @@
 // Eviction from the 4-bit cache by accumulated attention weight (pe_kv_evict).
 //
 // A cluster of C CTAs per request and key head:
-//  1. the weight of the lightest kept key, by three passes over the weights with
-//     a histogram of 11, 11 and 10 bits of their ordered form, and how many keys of
-//     exactly that weight are kept (the first ones);
-//  2. the kept keys in ascending order, each CTA its share after the others' counts;
+//  0. the weights' ordered forms, each CTA its share of the keys, into shared memory: one
+//     read, with many loads in flight;
+//  1. the weight of the lightest kept key, by three passes over them with a histogram of
+//     11, 11 and 10 bits, and how many keys of exactly that weight are kept (the first ones);
+//  2. the kept keys in ascending order: each warp counts its share of the keys, and lists
+//     it after the others' counts;
 //  3. the move, in rounds: every lane holds its piece of some keys in registers, a
 //     cluster barrier, then the stores.  A kept key never moves up, so in place
 //     a round's stores overwrite only keys that this round or an earlier one has read.
@@ -16,6 +18,7 @@ namespace pe {
 
 struct EvictParams {
   int B, Hkv, block_size, bt_width, dst_width, max_keep, sinks, recent, C;
+  int room;  // keys of a CTA that its shared memory holds
   long long num_blocks;
   uint8_t* cache;
   float* mass;
@@ -35,40 +38,20 @@ constexpr int kBins = 2048;
 struct EvictShared {
   uint32_t hist[kBins];
   uint32_t counts[2][kMaxCluster];
-  uint32_t warp[kEW + 1];
+  uint32_t heavy[kEW], equal[kEW];
   uint32_t digit, above;
 };
 
 // Order of weights; a NaN is the lightest.
 __device__ __forceinline__ uint32_t mass_key(float x) { return x == x ? ordered_bits(x) : 0u; }
 
-// Sum over the CTA; and this thread's exclusive prefix.
-__device__ __forceinline__ uint32_t block_prefix(uint32_t mine, uint32_t& total, EvictShared& sh) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint32_t pre = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t x = __shfl_up_sync(0xffffffffu, pre, o);
-    if (lane >= o) pre += x;
-  }
-  cta_sync();
-  if (lane == 31) sh.warp[warp] = pre;
-  cta_sync();
-  uint32_t before = 0, all = 0;
-  for (int w = 0; w < kEW; ++w) {
-    const uint32_t x = sh.warp[w];
-    if (w < warp) before += x;
-    all += x;
-  }
-  total = all;
-  return before + pre - mine;
-}
-
 template <int D>
-__global__ void __launch_bounds__(kET) evict_kernel(const EvictParams p) {
+__global__ void __launch_bounds__(kET, 2) evict_kernel(const EvictParams p) {
   using R = Record<D>;
-  __shared__ EvictShared sh;
-  const int tid = threadIdx.x, lane = tid & 31;
+  extern __shared__ __align__(16) unsigned char smem[];
+  EvictShared& sh = *reinterpret_cast<EvictShared*>(smem);
+  uint32_t* held = reinterpret_cast<uint32_t*>(smem + sizeof(EvictShared));
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = (int)cluster_rank();
   const int pair = blockIdx.x / p.C, b = pair / p.Hkv, h = pair - b * p.Hkv;
   const int bs = p.block_size;
@@ -91,7 +74,7 @@ __global__ void __launch_bounds__(kET) evict_kernel(const EvictParams p) {
       bad |= x < 0 || x >= p.num_blocks;
     }
   }
-  bad = __syncthreads_or(bad);
+  bad = cta_count(bad != 0);
   if (!sizes_ok || bad) {
     if (rank == 0 && h == 0 && tid == 0) {
       atomicOr(p.err, sizes_ok ? PE_ERR_BLOCK_RANGE : PE_ERR_PARAM);
@@ -103,7 +86,7 @@ __global__ void __launch_bounds__(kET) evict_kernel(const EvictParams p) {
   if (size == 0) return;
   int32_t* kept = p.kept + ((long long)b * p.Hkv + h) * p.max_keep;
   auto slot_of = [&](const int32_t* tab, int j) {  // index into mass
-    const int page = j / bs;
+    const int page = bs == 16 ? j >> 4 : j / bs;
     return ((long long)__ldg(tab + page) * p.Hkv + h) * bs + (j - page * bs);
   };
 
@@ -115,38 +98,57 @@ __global__ void __launch_bounds__(kET) evict_kernel(const EvictParams p) {
     const int per = ((n + p.C - 1) / p.C + 15) & ~15;
     const int j0 = min(n, rank * per), j1 = min(n, j0 + per);
     const int k0 = max(j0, lo), k1 = min(j1, hi);
-    uint32_t value = 0, mask = 0;
+    // every warp a run of keys, 32 at a time
+    const int run = ((per + kEW - 1) / kEW + 31) & ~31;
+    const int w0 = min(j1, j0 + warp * run), w1 = min(j1, w0 + run);
+    const bool fits = per <= p.room;
+    if (fits) {
+#pragma unroll 8
+      for (int j = j0 + tid; j < j1; j += kET) held[j - j0] = mass_key(p.mass[slot_of(table, j)]);
+    }
+    auto key_of = [&](int j) { return fits ? held[j - j0] : mass_key(p.mass[slot_of(table, j)]); };
+    uint32_t value = 0xffffffffu, mask = 0;
+    cluster_sync();  // every CTA has started; the keys are there
     if (want > 0) {
-      cluster_sync();  // every CTA has started
-      for (int shift = 21, bits = 11;; ) {
+      value = 0;
+      for (int shift = 21, bits = 11;;) {
         for (int i = tid; i < kBins; i += kET) sh.hist[i] = 0;
         cta_sync();
+#pragma unroll 4
         for (int j = k0 + tid; j < k1; j += kET) {
-          const uint32_t k = mass_key(p.mass[slot_of(table, j)]);
+          const uint32_t k = key_of(j);
           if ((k & mask) == value) atomicAdd(&sh.hist[(k >> shift) & ((1u << bits) - 1)], 1u);
         }
-        cluster_sync();
+        if (p.C > 1) cluster_sync();
+        else cta_sync();
         // bins from the heaviest on: thread tid's four
-        uint32_t c[4], mine = 0;
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int bin = kBins - 1 - (4 * tid + x);
-          uint32_t s = 0;
-          for (int r = 0; r < p.C; ++r) s += *at_rank(&sh.hist[bin], r);
-          c[x] = s;
-          mine += s;
+        uint32_t c[4] = {0, 0, 0, 0};
+        const int bin0 = kBins - 4 - 4 * tid;
+        for (int r = 0; r < p.C; ++r) {
+          const uint4 q = *reinterpret_cast<const uint4*>(p.C > 1 ? at_rank(&sh.hist[bin0], r) : &sh.hist[bin0]);
+          c[0] += q.w, c[1] += q.z, c[2] += q.y, c[3] += q.x;
         }
-        uint32_t total;
-        uint32_t pre = block_prefix(mine, total, sh);
+        const uint32_t mine = c[0] + c[1] + c[2] + c[3];
+        uint32_t pre = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const uint32_t x = __shfl_up_sync(0xffffffffu, pre, o);
+          if (lane >= o) pre += x;
+        }
+        if (lane == 31) sh.heavy[warp] = pre;
+        cta_sync();
+        pre -= mine;
+        for (int w = 0; w < warp; ++w) pre += sh.heavy[w];
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
           if (pre < want && want <= pre + c[x]) {
-            sh.digit = kBins - 1 - (4 * tid + x);
+            sh.digit = bin0 + 3 - x;
             sh.above = pre;
           }
           pre += c[x];
         }
-        cluster_sync();  // also: the histograms have been read
+        if (p.C > 1) cluster_sync();  // also: the histograms have been read
+        else cta_sync();
         value |= sh.digit << shift;
         mask |= ((1u << bits) - 1) << shift;
         want -= sh.above;
@@ -154,45 +156,52 @@ __global__ void __launch_bounds__(kET) evict_kernel(const EvictParams p) {
         if (shift == 21) shift = 10, bits = 11;
         else shift = 0, bits = 10;
       }
-    } else {
-      value = 0xffffffffu;  // nothing but the first and the last
     }
     // ---- ascending list: heavier keys, the first `want` of equal weight
     auto state = [&](int j) -> int {  // 2 kept, 1 equal, 0 not
+      if (j >= w1) return 0;
       if (j < lo || j >= hi) return 2;
-      const uint32_t k = mass_key(p.mass[slot_of(table, j)]);
+      const uint32_t k = key_of(j);
       return k > value ? 2 : k == value && want > 0 ? 1 : 0;
     };
     uint32_t heavy = 0, equal = 0;
-    for (int j = j0 + tid; j < j1; j += kET) {
-      const int s = state(j);
-      heavy += s == 2;
-      equal += s == 1;
+    for (int t0 = w0; t0 < w1; t0 += 32) {
+      const int s = state(t0 + lane);
+      heavy += __popc(__ballot_sync(0xffffffffu, s == 2));
+      equal += __popc(__ballot_sync(0xffffffffu, s == 1));
     }
-    uint32_t heavy_all, equal_all;
-    block_prefix(heavy, heavy_all, sh);
-    block_prefix(equal, equal_all, sh);
-    cluster_sync();
-    if (tid < p.C) {
-      *at_rank(&sh.counts[0][rank], tid) = heavy_all;
-      *at_rank(&sh.counts[1][rank], tid) = equal_all;
+    cta_sync();
+    if (lane == 0) {
+      sh.heavy[warp] = heavy;
+      sh.equal[warp] = equal;
     }
-    cluster_sync();
-    uint32_t equal_before = 0, at = 0;
-    for (int r = 0; r < rank; ++r) {
-      at += sh.counts[0][r] + min(sh.counts[1][r], want - min(want, equal_before));
-      equal_before += sh.counts[1][r];
+    cta_sync();
+    uint32_t heavy_all = 0, equal_all = 0, at = 0, before = 0;  // before: equal keys
+    for (int w = 0; w < kEW; ++w) {
+      if (w < warp) at += sh.heavy[w], before += sh.equal[w];
+      heavy_all += sh.heavy[w];
+      equal_all += sh.equal[w];
     }
-    for (int t0 = j0; t0 < j1; t0 += kET) {
-      const int j = t0 + tid;
-      const int s = j < j1 ? state(j) : 0;
-      uint32_t eq, all;
-      const uint32_t e = block_prefix(s == 1, eq, sh);
-      const bool in = s == 2 || (s == 1 && equal_before + e < want);
-      const uint32_t o = block_prefix(in, all, sh);
-      if (in) kept[at + o] = j;
-      at += all;
-      equal_before += eq;
+    if (p.C > 1) {
+      if (tid < p.C) {
+        *at_rank(&sh.counts[0][rank], tid) = heavy_all;
+        *at_rank(&sh.counts[1][rank], tid) = equal_all;
+      }
+      cluster_sync();
+      for (int r = 0; r < rank; ++r) {
+        at += sh.counts[0][r];
+        before += sh.counts[1][r];
+      }
+    }
+    at += min(want, before);
+    for (int t0 = w0; t0 < w1; t0 += 32) {
+      const int s = state(t0 + lane);
+      const uint32_t below = (1u << lane) - 1, eq = __ballot_sync(0xffffffffu, s == 1);
+      const bool in = s == 2 || (s == 1 && before + __popc(eq & below) < want);
+      const uint32_t m = __ballot_sync(0xffffffffu, in);
+      if (in) kept[at + __popc(m & below)] = t0 + lane;
+      at += __popc(m);
+      before += __popc(eq);
     }
   } else {
     for (int j = rank * kET + tid; j < n; j += p.C * kET) kept[j] = j;
@@ -249,10 +258,13 @@ __global__ void __launch_bounds__(kET) evict_kernel(const EvictParams p) {
       }
     }
   }
-  (void)lane;
 }
 
 }  // namespace pe
+
+namespace {
+constexpr int kMostRoom = 48 * 1024;  // keys
+}
 
 extern "C" int pe_kv_evict(const pe_kv_evict_args* a, void* stream) {
   if (!a) return PE_EINVAL;
@@ -276,11 +288,20 @@ extern "C" int pe_kv_evict(const pe_kv_evict_args* a, void* stream) {
   p.mass = a->mass;
   p.table = a->block_table, p.dst = a->dst_table, p.lengths = a->lengths, p.keep = a->keep;
   p.kept = a->kept, p.out_lengths = a->out_lengths, p.err = a->err;
+  // CTAs of a cluster: so many that a share of the table's keys takes at most 64 KB (two CTAs
+  // and more on an SM), and more while the pairs do not fill the GPU
+  const int64_t keys = (int64_t)a->bt_width * a->block_size;
   p.C = 1;
-  while (p.C < 8 && (int64_t)a->B * a->Hkv * p.C * 2 <= 4 * dev.sm_count) p.C *= 2;
+  while (p.C < 16 && (keys > 16384 * p.C || ((int64_t)a->B * a->Hkv * p.C <= dev.sm_count && keys > 512 * p.C))) p.C *= 2;
+  const int64_t share = ((keys + p.C - 1) / p.C + 15) & ~15;
+  p.room = (int)(share < kMostRoom ? share : kMostRoom);  // (a larger share is read from memory each time)
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const unsigned grid = (unsigned)(a->B * a->Hkv * p.C);
+  const dim3 grid((unsigned)(a->B * a->Hkv * p.C));
+  auto kernel = a->D == 64 ? pe::evict_kernel<64> : pe::evict_kernel<128>;
+  static std::atomic<unsigned long long> done[2];
+  if (!pe_host::allow_smem(kernel, (int)sizeof(pe::EvictShared) + 4 * kMostRoom, done[a->D == 64])) return PE_ECUDA;
+  if (p.C > 8 && cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) return PE_ECUDA;
   const cudaError_t rc =
-      pe_host::launch_clusters(a->D == 64 ? pe::evict_kernel<64> : pe::evict_kernel<128>, grid, pe::kET, p.C, 0, false, st, p);
+      pe_host::launch_clusters(kernel, grid, pe::kET, p.C, sizeof(pe::EvictShared) + 4 * (size_t)p.room, false, st, p);
   return rc == cudaSuccess ? pe_host::launch_status() : PE_ECUDA;
 }
