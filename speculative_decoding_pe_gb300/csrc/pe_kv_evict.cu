@@ -8,7 +8,7 @@
 //  2. the kept keys in ascending order: each warp counts its share of the keys, and lists
 //     it after the others' counts;
 //  3. the move, in rounds: every lane holds its piece of some keys in registers, a
-//     cluster barrier, then the stores.  A kept key never moves up, so in place
+//     cluster barrier (where a page stays where it is), then the stores.  A kept key never moves up, so in place
 //     a round's stores overwrite only keys that this round or an earlier one has read.
 // Everything is exact: integers decide, bytes are moved.
 #include "pe_cluster.cuh"
@@ -36,7 +36,7 @@ constexpr int kEW = kET / 32;
 constexpr int kBins = 2048;
 
 struct EvictShared {
-  uint32_t hist[kBins];
+  uint32_t hist[2][kBins];
   uint32_t counts[2][kMaxCluster];
   uint32_t heavy[kEW], equal[kEW];
   uint32_t digit, above;
@@ -55,26 +55,42 @@ __global__ void __launch_bounds__(kET, 2) evict_kernel(const EvictParams p) {
   const int rank = (int)cluster_rank();
   const int pair = blockIdx.x / p.C, b = pair / p.Hkv, h = pair - b * p.Hkv;
   const int bs = p.block_size;
-  const int n = __ldg(p.lengths + b), keep = __ldg(p.keep + b);
   const int32_t* table = p.table + (long long)b * p.bt_width;
   const int32_t* dst = p.dst + (long long)b * p.dst_width;
+  // the tables' first pages along with the sizes that say how many count
+  constexpr int kAhead = 4;
+  int32_t page[kAhead], to_page[kAhead];
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) {
+    page[i] = tid + i * kET < p.bt_width ? __ldg(table + tid + i * kET) : 0;
+    to_page[i] = tid + i * kET < p.dst_width ? __ldg(dst + tid + i * kET) : 0;
+  }
+  const int n = __ldg(p.lengths + b), keep = __ldg(p.keep + b);
 
   // ---- sizes and pages (every CTA of the request comes to the same answer)
   const int size = min(n, keep);
   const bool sizes_ok = n >= 0 && keep >= 0 && n <= (long long)p.bt_width * bs && size <= p.max_keep &&
                         size <= (long long)p.dst_width * bs;
-  int bad = 0;
+  int bad = 0, same = 0;  // a page outside the cache; a page that stays where it is
   if (sizes_ok) {
-    for (int i = tid; i < (n + bs - 1) / bs; i += kET) {
-      const int x = __ldg(table + i);
-      bad |= x < 0 || x >= p.num_blocks;
+    const uint32_t blocks = p.num_blocks > INT32_MAX ? 0x80000000u : (uint32_t)p.num_blocks;
+    const int pages = (n + bs - 1) / bs, dst_pages = (size + bs - 1) / bs;
+#pragma unroll
+    for (int x = 0; x < kAhead; ++x) {
+      const int i = tid + x * kET;
+      bad |= (i < pages) & ((uint32_t)page[x] >= blocks);  // (negative ids too)
+      bad |= (i < dst_pages) & ((uint32_t)to_page[x] >= blocks);
+      same |= (i < dst_pages) & (page[x] == to_page[x]);
     }
-    for (int i = tid; i < (size + bs - 1) / bs; i += kET) {
-      const int x = __ldg(dst + i);
-      bad |= x < 0 || x >= p.num_blocks;
+    for (int i = tid + kAhead * kET; i < pages; i += kET) {
+      const int x = __ldg(table + i), y = i < dst_pages ? __ldg(dst + i) : 0;
+      bad |= (uint32_t)x >= blocks;
+      bad |= (uint32_t)y >= blocks;
+      same |= (i < dst_pages) & (x == y);
     }
   }
   bad = cta_count(bad != 0);
+  const bool in_place = cta_count(same != 0) != 0;
   if (!sizes_ok || bad) {
     if (rank == 0 && h == 0 && tid == 0) {
       atomicOr(p.err, sizes_ok ? PE_ERR_BLOCK_RANGE : PE_ERR_PARAM);
@@ -111,13 +127,15 @@ __global__ void __launch_bounds__(kET, 2) evict_kernel(const EvictParams p) {
     cluster_sync();  // every CTA has started; the keys are there
     if (want > 0) {
       value = 0;
-      for (int shift = 21, bits = 11;;) {
-        for (int i = tid; i < kBins; i += kET) sh.hist[i] = 0;
+      // (two histograms in turns: that of the pass before may still be read by other CTAs)
+      for (int shift = 21, bits = 11, turn = 0;; turn ^= 1) {
+        uint32_t* hist = sh.hist[turn];
+        for (int i = tid; i < kBins; i += kET) hist[i] = 0;
         cta_sync();
 #pragma unroll 4
         for (int j = k0 + tid; j < k1; j += kET) {
           const uint32_t k = key_of(j);
-          if ((k & mask) == value) atomicAdd(&sh.hist[(k >> shift) & ((1u << bits) - 1)], 1u);
+          if ((k & mask) == value) atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1)], 1u);
         }
         if (p.C > 1) cluster_sync();
         else cta_sync();
@@ -125,7 +143,7 @@ __global__ void __launch_bounds__(kET, 2) evict_kernel(const EvictParams p) {
         uint32_t c[4] = {0, 0, 0, 0};
         const int bin0 = kBins - 4 - 4 * tid;
         for (int r = 0; r < p.C; ++r) {
-          const uint4 q = *reinterpret_cast<const uint4*>(p.C > 1 ? at_rank(&sh.hist[bin0], r) : &sh.hist[bin0]);
+          const uint4 q = *reinterpret_cast<const uint4*>(p.C > 1 ? at_rank(&hist[bin0], r) : &hist[bin0]);
           c[0] += q.w, c[1] += q.z, c[2] += q.y, c[3] += q.x;
         }
         const uint32_t mine = c[0] + c[1] + c[2] + c[3];
@@ -147,8 +165,7 @@ __global__ void __launch_bounds__(kET, 2) evict_kernel(const EvictParams p) {
           }
           pre += c[x];
         }
-        if (p.C > 1) cluster_sync();  // also: the histograms have been read
-        else cta_sync();
+        cta_sync();
         value |= sh.digit << shift;
         mask |= ((1u << bits) - 1) << shift;
         want -= sh.above;
@@ -158,17 +175,28 @@ __global__ void __launch_bounds__(kET, 2) evict_kernel(const EvictParams p) {
       }
     }
     // ---- ascending list: heavier keys, the first `want` of equal weight
-    auto state = [&](int j) -> int {  // 2 kept, 1 equal, 0 not
-      if (j >= w1) return 0;
-      if (j < lo || j >= hi) return 2;
-      const uint32_t k = key_of(j);
-      return k > value ? 2 : k == value && want > 0 ? 1 : 0;
+    // (a warp's masks of 32 keys at a time, 32 masks in turn: one in each lane)
+    auto look = [&](int t0, uint2& mine) {
+      for (int i = 0; i < 32 && t0 + 32 * i < w1; ++i) {
+        const int j = t0 + 32 * i + lane;
+        bool heavy = j < w1, equal = false;
+        if (j < w1 && j >= lo && j < hi) {
+          const uint32_t k = key_of(j);
+          heavy = k > value;
+          equal = k == value && want > 0;
+        }
+        const uint32_t a = __ballot_sync(0xffffffffu, heavy), e = __ballot_sync(0xffffffffu, equal);
+        if (lane == i) mine = make_uint2(a, e);
+      }
     };
+    uint2 first_masks = make_uint2(0u, 0u);
     uint32_t heavy = 0, equal = 0;
-    for (int t0 = w0; t0 < w1; t0 += 32) {
-      const int s = state(t0 + lane);
-      heavy += __popc(__ballot_sync(0xffffffffu, s == 2));
-      equal += __popc(__ballot_sync(0xffffffffu, s == 1));
+    for (int t0 = w0; t0 < w1; t0 += 1024) {
+      uint2 m = make_uint2(0u, 0u);
+      look(t0, m);
+      if (t0 == w0) first_masks = m;
+      heavy += __reduce_add_sync(0xffffffffu, __popc(m.x));
+      equal += __reduce_add_sync(0xffffffffu, __popc(m.y));
     }
     cta_sync();
     if (lane == 0) {
@@ -194,14 +222,30 @@ __global__ void __launch_bounds__(kET, 2) evict_kernel(const EvictParams p) {
       }
     }
     at += min(want, before);
-    for (int t0 = w0; t0 < w1; t0 += 32) {
-      const int s = state(t0 + lane);
-      const uint32_t below = (1u << lane) - 1, eq = __ballot_sync(0xffffffffu, s == 1);
-      const bool in = s == 2 || (s == 1 && before + __popc(eq & below) < want);
-      const uint32_t m = __ballot_sync(0xffffffffu, in);
-      if (in) kept[at + __popc(m & below)] = t0 + lane;
-      at += __popc(m);
-      before += __popc(eq);
+    for (int t0 = w0; t0 < w1; t0 += 1024) {
+      uint2 m = first_masks;
+      if (t0 != w0) look(t0, m = make_uint2(0u, 0u));
+      // equal keys of the lanes before, and how many of this lane's are kept
+      uint32_t eq = __popc(m.y), pre = eq;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t x = __shfl_up_sync(0xffffffffu, pre, o);
+        if (lane >= o) pre += x;
+      }
+      const uint32_t all_eq = __shfl_sync(0xffffffffu, pre, 31);
+      uint32_t take = before + pre - eq >= want ? 0u : min(eq, want - (before + pre - eq));
+      before += all_eq;
+      for (uint32_t drop = eq - take; drop; --drop) m.y ^= 0x80000000u >> __clz(m.y);  // its last ones go
+      uint32_t set = m.x | m.y, n_set = __popc(set), off = n_set;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t x = __shfl_up_sync(0xffffffffu, off, o);
+        if (lane >= o) off += x;
+      }
+      const uint32_t all = __shfl_sync(0xffffffffu, off, 31);
+      int32_t* to = kept + at + off - n_set;
+      for (const int j = t0 + 32 * lane; set; set &= set - 1) *to++ = j + __ffs(set) - 1;
+      at += all;
     }
   } else {
     for (int j = rank * kET + tid; j < n; j += p.C * kET) kept[j] = j;
@@ -209,52 +253,61 @@ __global__ void __launch_bounds__(kET, 2) evict_kernel(const EvictParams p) {
   cluster_sync();  // the list is whole (and every CTA has started)
 
   // ---- the move
-  constexpr int kLanes = D / 16;       // of a key: 16 code bytes each
-  constexpr int kU = 4;                // keys of a lane group and round
-  const int part = tid % kLanes, group = tid / kLanes;
-  const int groups = kET / kLanes;
-  const bool is_v = part >= kLanes / 2;
+  constexpr int kLanes = D / 16;        // of a key: 16 code bytes each
+  constexpr int kU = 4;                 // keys of a lane and round
+  constexpr int kKeys = 32 / kLanes;    // keys that a warp moves at once
+  const int part = lane % kLanes, of = lane / kLanes;
+  const bool is_v = part >= kLanes / 2, has_scales = part % (kLanes / 2) == 0;
   const int code = (is_v ? R::kV : R::kK) + (part % (kLanes / 2)) * 16;
-  for (int i0 = 0; i0 < size; i0 += groups * kU * p.C) {
+  const int scale = is_v ? R::kVs : R::kKs;
+  const int round = kKeys * kU;         // keys of a warp and round (a lane looks one up)
+  const int step = round * kEW * p.C;
+  long long from = -1, to = -1;
+  auto look_up = [&](uint32_t i) {
+    from = to = -1;
+    if (lane < round && (uint32_t)i < (uint32_t)size) {
+      from = slot_of(table, __ldcg(kept + i));
+      to = slot_of(dst, (int)i);
+      if (from == to) to = -1;
+    }
+  };
+  const uint32_t i1 = (rank * kEW + warp) * round + lane;
+  look_up(i1);
+  for (uint32_t i0 = 0; i0 < (uint32_t)size; i0 += step) {
     uint4 codes[kU];
     uint2 scales[kU];
     float m[kU];
-    long long to[kU];
+    long long at[kU];
 #pragma unroll
     for (int x = 0; x < kU; ++x) {
-      const int i = i0 + (x * p.C + rank) * groups + group;
-      to[x] = -1;
-      if (i < size) {
-        const int j = __ldcg(kept + i);
-        const long long from = slot_of(table, j);
-        const long long at = slot_of(dst, i);
-        if (from != at) {
-          to[x] = at;
-          const uint8_t* rec = p.cache + (from >> 4) * (long long)R::kBytes;
-          const int r = (int)(from & 15);
-          codes[x] = *reinterpret_cast<const uint4*>(rec + code + r * R::kRow);
-          if (part % (kLanes / 2) == 0) {
-            const uint8_t* s = rec + (is_v ? R::kVs : R::kKs) + r * R::kScaleRow;
-            if (D == 128) scales[x] = *reinterpret_cast<const uint2*>(s);
-            else scales[x].x = *reinterpret_cast<const uint32_t*>(s);
-          }
-          if (part == 0) m[x] = p.mass[from];
+      const long long src = __shfl_sync(0xffffffffu, from, x * kKeys + of);
+      at[x] = __shfl_sync(0xffffffffu, to, x * kKeys + of);
+      if (at[x] >= 0) {
+        const uint8_t* rec = p.cache + (src >> 4) * (long long)R::kBytes;
+        const int r = (int)(src & 15);
+        codes[x] = *reinterpret_cast<const uint4*>(rec + code + r * R::kRow);
+        if (has_scales) {
+          const uint8_t* s = rec + scale + r * R::kScaleRow;
+          if (D == 128) scales[x] = *reinterpret_cast<const uint2*>(s);
+          else scales[x].x = *reinterpret_cast<const uint32_t*>(s);
         }
+        if (part == 0) m[x] = p.mass[src];
       }
     }
-    cluster_sync();
+    look_up(i1 + i0 + step);  // the next round's, while these are on their way
+    if (in_place) cluster_sync();
 #pragma unroll
     for (int x = 0; x < kU; ++x) {
-      if (to[x] >= 0) {
-        uint8_t* rec = p.cache + (to[x] >> 4) * (long long)R::kBytes;
-        const int r = (int)(to[x] & 15);
+      if (at[x] >= 0) {
+        uint8_t* rec = p.cache + (at[x] >> 4) * (long long)R::kBytes;
+        const int r = (int)(at[x] & 15);
         *reinterpret_cast<uint4*>(rec + code + r * R::kRow) = codes[x];
-        if (part % (kLanes / 2) == 0) {
-          uint8_t* s = rec + (is_v ? R::kVs : R::kKs) + r * R::kScaleRow;
+        if (has_scales) {
+          uint8_t* s = rec + scale + r * R::kScaleRow;
           if (D == 128) *reinterpret_cast<uint2*>(s) = scales[x];
           else *reinterpret_cast<uint32_t*>(s) = scales[x].x;
         }
-        if (part == 0) p.mass[to[x]] = m[x];
+        if (part == 0) p.mass[at[x]] = m[x];
       }
     }
   }
