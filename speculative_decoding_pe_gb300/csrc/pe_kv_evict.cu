@@ -35,7 +35,7 @@ constexpr int kET = 512;
 constexpr int kEW = kET / 32;
 constexpr int kBins = 2048;
 
-struct EvictShared {
+struct alignas(16) EvictShared {  // (the keys follow, in vectors)
   uint32_t hist[2][kBins];
   uint32_t counts[2][kMaxCluster];
   uint32_t heavy[kEW], equal[kEW];
@@ -119,8 +119,22 @@ __global__ void __launch_bounds__(kET, 2) evict_kernel(const EvictParams p) {
     const int w0 = min(j1, j0 + warp * run), w1 = min(j1, w0 + run);
     const bool fits = per <= p.room;
     if (fits) {
-#pragma unroll 8
-      for (int j = j0 + tid; j < j1; j += kET) held[j - j0] = mass_key(p.mass[slot_of(table, j)]);
+      // four keys a load, eight loads of a thread at once (the runs of sixteen do not cross pages)
+      for (int v0 = 0; 4 * v0 < j1 - j0; v0 += 8 * kET) {
+        float4 x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int j = j0 + 4 * (v0 + i * kET + tid);
+          if (j < j1) x[i] = *reinterpret_cast<const float4*>(p.mass + slot_of(table, j));
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int v = v0 + i * kET + tid;
+          if (j0 + 4 * v < j1)
+            reinterpret_cast<uint4*>(held)[v] =
+                make_uint4(mass_key(x[i].x), mass_key(x[i].y), mass_key(x[i].z), mass_key(x[i].w));
+        }
+      }
     }
     auto key_of = [&](int j) { return fits ? held[j - j0] : mass_key(p.mass[slot_of(table, j)]); };
     uint32_t value = 0xffffffffu, mask = 0;
