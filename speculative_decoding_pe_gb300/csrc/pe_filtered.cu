@@ -139,31 +139,37 @@ struct Slice {
     }
   }
 
-  // The warp's share of the row's weight.  Vectors whose largest weight is below 2^-20
-  // go through the hardware's exponential in 24 bits: their errors are of either sign
-  // and some 2^-22 of a small part of the sum.  The others are queued (few, in a row of a
-  // language model: a branch in the loop would be taken by one lane or another nearly every
-  // time) and weighed in full.
-  // large: the share of the columns of at least 2^-12 of the largest weight.
+  // The warp's share of the row's weight.  Vectors whose largest weight is below 2^-16
+  // go through the hardware's exponential in 24 bits: its errors are of a part of the sum
+  // that is small where few vectors are large, random but for a mean of -5.1e-8 (measured
+  // over every octave down to 2^-32: -4.9e-8 to -5.2e-8), which is put back.  The others
+  // are queued (a branch in the loop would be taken by one lane or another nearly every time)
+  // and weighed in full.  large: the share of the columns of at least 2^-12 of the largest weight.
   __device__ __forceinline__ unsigned long long mass(const Scale& sc, unsigned short* queue, unsigned long long& large) {
-    const float big = sc.inf ? -INFINITY : sc.M - 20.f / sc.ch, top = sc.inf ? sc.M : sc.M - 12.f / sc.ch;
-    float small = 0.f;
+    const float big = sc.inf ? -INFINITY : sc.M - 16.f / sc.ch, top = sc.inf ? sc.M : sc.M - 12.f / sc.ch;
+    const float2 minus = make_float2(-sc.M, -sc.M), rate = make_float2(sc.ch, sc.ch);
+    auto small_vectors = [&](bool clean) {
+      float2 sum = make_float2(0.f, 0.f);
+#pragma unroll 2
+      for (int i = lo + lane; i < hi; i += 32) {
+        const uint4 q = v[i];
+        if (Elt<DT>::max_of(q) >= big) continue;
+#pragma unroll
+        for (int e = 0; e < Elt<DT>::kN; e += 2) {
+          float2 x = make_float2(Elt<DT>::get(q, e), Elt<DT>::get(q, e + 1));
+          if (clean) x = make_float2(fmaxf(x.x, -INFINITY), fmaxf(x.y, -INFINITY));
+          x = mul2(add2(x, minus), rate);
+          sum = add2(sum, make_float2(exp2_hw(x.x), exp2_hw(x.y)));
+        }
+      }
+      return sum.x + sum.y;
+    };
+    float small = small_vectors(false);
+    if (small != small) small = small_vectors(true);  // NaN columns weigh nothing
     int queued = 0;
     for (int i0 = lo; i0 < hi; i0 += 32) {
       const int i = i0 + lane;
-      bool put = false;
-      if (i < hi) {
-        const uint4 q = v[i];
-        put = Elt<DT>::max_of(q) >= big;
-        if (!put) {
-#pragma unroll
-          for (int e = 0; e < Elt<DT>::kN; ++e) {
-            float w;
-            asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w) : "f"((fmaxf(Elt<DT>::get(q, e), -INFINITY) - sc.M) * sc.ch));
-            small += w;
-          }
-        }
-      }
+      const bool put = i < hi && Elt<DT>::max_of(v[i]) >= big;
       const uint32_t m = __ballot_sync(0xffffffffu, put);
       if (put) queue[queued + __popc(m & ((1u << lane) - 1))] = (unsigned short)(i - lo);
       queued += __popc(m);
@@ -181,8 +187,7 @@ struct Slice {
       }
     }
     large = warp_sum_u64(most.fixed(kSumBits));
-    all.add(0.f, small);
-    return warp_sum_u64(all.fixed(kSumBits));
+    return warp_sum_u64(all.fixed(kSumBits) + fixed_weight(make_float2(small, 5.1e-8f * small), kSumBits));
   }
 
   // The warp's share of the weight that a cut keeps.
@@ -1238,16 +1243,7 @@ __global__ void __launch_bounds__(kFT, 4) filter_kernel(const FilterParams p) {
   };
   unsigned long long mine_w;
   if (cut.key == 0 && floor == -INFINITY) {  // every column
-    WeightSum<256> ws;
-    for (int i = s.lo + lane; i < s.hi; i += 32) {
-      const uint4 q = s.v[i];
-#pragma unroll
-      for (int e = 0; e < E::kN; ++e) {
-        const float2 w = weight(sc, sh.table, E::get(q, e));
-        ws.add(w.x, w.y);
-      }
-    }
-    mine_w = warp_sum_u64(ws.fixed(kSumBits));
+    mine_w = s.mass(sc, sh.queue[warp], large);
   } else {
     mine_w = s.kept_mass(sc, cut);
   }
