@@ -52,7 +52,7 @@ __device__ const float2 kExp2Table[32] = {
 // from M from which on a weight is nothing (2^-64).  A row with an infinity
 // shares its weight among those columns.
 struct Scale {
-  float M, ch, cl, far;
+  float M, ch, cl, far, octave;  // octave: 1 / c
   bool inf;
 };
 
@@ -60,7 +60,7 @@ struct Scale {
 // slow on this GPU (a warp's instruction takes some 16 clocks): one thread of a CTA does it, while
 // the row is on its way.
 struct Rates {
-  float ch, cl, far;
+  float ch, cl, far, octave;
   double log_m;  // T ln(m), where min-p is on
 };
 __device__ __forceinline__ Rates make_rates(float T, float m) {
@@ -68,12 +68,13 @@ __device__ __forceinline__ Rates make_rates(float T, float m) {
   const double t = T > 0.f ? (double)T : 1.0, c = 1.4426950408889634 / t;
   r.ch = (float)c;
   r.cl = (float)(c - (double)r.ch);
-  r.far = 64.f / r.ch;
+  r.octave = (float)(t * 0.6931471805599453);
+  r.far = 64.f * r.octave;
   r.log_m = m > 0.f && m < 1.f ? t * log((double)m) : 0.0;
   return r;
 }
 __device__ __forceinline__ Scale make_scale(float M, const Rates& r) {
-  return Scale{M, r.ch, r.cl, r.far, M == INFINITY};
+  return Scale{M, r.ch, r.cl, r.far, r.octave, M == INFINITY};
 }
 
 // w(x) = hi + lo.  y = (x - M) c = n + j/32 + r with |r| <= 1/64;

@@ -48,7 +48,6 @@ struct FilterParams {
 
 constexpr int kListBins = 256;
 constexpr int kSteps = 4 * kFT;   // bins of the search for a cut over the whole row
-constexpr int kMaxSegment = kListCap * 8 / 2 / kFW;  // vectors of a warp's segment, at most
 
 struct FilterShared {
   uint64_t bars[kFW];
@@ -71,7 +70,6 @@ struct FilterShared {
   unsigned short hits[kFW][64];
   union alignas(16) {
     unsigned long long list[kListCap];         // candidates: (value's key, ~column)
-    unsigned short queue[kFW][kMaxSegment];    // vectors to be weighed in full
     uint32_t steps[kSteps];
   };
 };
@@ -144,48 +142,59 @@ struct Slice {
   // that is small where few vectors are large, random but for a mean of -5.1e-8 (measured
   // over every octave down to 2^-32: -4.9e-8 to -5.2e-8), which is put back.  The others
   // are queued (a branch in the loop would be taken by one lane or another nearly every time)
-  // and weighed in full.  large: the share of the columns of at least 2^-12 of the largest weight.
-  __device__ __forceinline__ unsigned long long mass(const Scale& sc, unsigned short* queue, unsigned long long& large) {
-    const float big = sc.inf ? -INFINITY : sc.M - 16.f / sc.ch, top = sc.inf ? sc.M : sc.M - 12.f / sc.ch;
+  // and weighed in full, an element a lane.  large: the share of the columns of at least 2^-12 of the largest weight.
+  __device__ __forceinline__ unsigned long long mass(const Scale& sc, unsigned long long& large) {
+    const float big = sc.inf ? -INFINITY : sc.M - 16.f * sc.octave, top = sc.inf ? sc.M : sc.M - 12.f * sc.octave;
     const float2 minus = make_float2(-sc.M, -sc.M), rate = make_float2(sc.ch, sc.ch);
-    auto small_vectors = [&](bool clean) {
-      float2 sum = make_float2(0.f, 0.f);
-#pragma unroll 2
-      for (int i = lo + lane; i < hi; i += 32) {
-        const uint4 q = v[i];
-        if (Elt<DT>::max_of(q) >= big) continue;
-#pragma unroll
-        for (int e = 0; e < Elt<DT>::kN; e += 2) {
-          float2 x = make_float2(Elt<DT>::get(q, e), Elt<DT>::get(q, e + 1));
-          if (clean) x = make_float2(fmaxf(x.x, -INFINITY), fmaxf(x.y, -INFINITY));
-          x = mul2(add2(x, minus), rate);
-          sum = add2(sum, make_float2(exp2_hw(x.x), exp2_hw(x.y)));
+    float small = 0.f;
+    WeightSum<256> all, most;
+    uint32_t queued = 0;
+    auto take = [&]() {  // an element a lane: a large vector has one or two large ones
+      __syncwarp();
+      for (uint32_t j0 = 0; j0 < queued; j0 += 32 / Elt<DT>::kN) {
+        const uint32_t j = j0 + lane / Elt<DT>::kN;
+        if (j < queued) {
+          const float x = Elt<DT>::element(v, sh->hits[warp][j], lane % Elt<DT>::kN);
+          const float2 w = weight(sc, sh->table, x);
+          all.add(w.x, w.y);
+          if (x >= top) most.add(w.x, w.y);
         }
       }
-      return sum.x + sum.y;
+      queued = 0;
+      __syncwarp();
     };
-    float small = small_vectors(false);
-    if (small != small) small = small_vectors(true);  // NaN columns weigh nothing
-    int queued = 0;
-    for (int i0 = lo; i0 < hi; i0 += 32) {
-      const int i = i0 + lane;
-      const bool put = i < hi && Elt<DT>::max_of(v[i]) >= big;
-      const uint32_t m = __ballot_sync(0xffffffffu, put);
-      if (put) queue[queued + __popc(m & ((1u << lane) - 1))] = (unsigned short)(i - lo);
-      queued += __popc(m);
-    }
-    __syncwarp();
-    WeightSum<256> all, most;
-    for (int j = lane; j < queued; j += 32) {
-      const uint4 q = v[lo + queue[j]];
+    auto look = [&](bool clean) {
+      float2 sum = make_float2(0.f, 0.f);
+#pragma unroll 2
+      for (int i0 = lo; i0 < hi; i0 += 32) {
+        const int i = i0 + lane;
+        bool put = false;
+        if (i < hi) {
+          const uint4 q = v[i];
+          put = Elt<DT>::max_of(q) >= big;
+          if (!put) {
 #pragma unroll
-      for (int e = 0; e < Elt<DT>::kN; ++e) {
-        const float x = Elt<DT>::get(q, e);
-        const float2 w = weight(sc, sh->table, x);
-        all.add(w.x, w.y);
-        if (x >= top) most.add(w.x, w.y);
+            for (int e = 0; e < Elt<DT>::kN; e += 2) {
+              float2 x = make_float2(Elt<DT>::get(q, e), Elt<DT>::get(q, e + 1));
+              if (clean) x = make_float2(fmaxf(x.x, -INFINITY), fmaxf(x.y, -INFINITY));
+              x = mul2(add2(x, minus), rate);
+              sum = add2(sum, make_float2(exp2_hw(x.x), exp2_hw(x.y)));
+            }
+          }
+        }
+        if (clean) continue;
+        const uint32_t m = __ballot_sync(0xffffffffu, put);
+        if (m) {
+          if (put) sh->hits[warp][queued + __popc(m & ((1u << lane) - 1))] = (unsigned short)i;
+          queued += __popc(m);
+          if (queued > 32) take();  // (room for another 32 is needed)
+        }
       }
-    }
+      small = sum.x + sum.y;
+    };
+    look(false);
+    take();
+    if (__any_sync(0xffffffffu, small != small)) look(true);  // NaN columns weigh nothing
     large = warp_sum_u64(most.fixed(kSumBits));
     return warp_sum_u64(all.fixed(kSumBits) + fixed_weight(make_float2(small, 5.1e-8f * small), kSumBits));
   }
@@ -256,7 +265,7 @@ struct Slice {
   __device__ __forceinline__ bool steer(const Scale& sc, const Cut& cut, float octaves, double target, uint32_t* steps, float& lo_x,
                                         float& hi_x) {
     const int tid = threadIdx.x;
-    const float width = octaves / (float)kSteps, range = octaves / sc.ch, per = (float)kSteps / range;
+    const float width = octaves / (float)kSteps, range = octaves * sc.octave, per = (float)kSteps / range;
     for (int i = tid; i < kSteps; i += kFT) steps[i] = 0;
     cta_sync();
     for (int i = lo + lane; i < hi; i += 32) {
@@ -959,7 +968,7 @@ __global__ void __launch_bounds__(kFT, 4) filter_kernel(const FilterParams p) {
   const float p_mass = a.p > 0.f ? a.p : 0.f;
   unsigned long long Z = 0;  // the whole row's weight (top-p alone)
   unsigned long long large = 0;
-  if (nucleus) Z = s.mass(make_scale(key_value(top), sh.rates), sh.queue[warp], large);
+  if (nucleus) Z = s.mass(make_scale(key_value(top), sh.rates), large);
   cluster_wait();  // every CTA has started
   if (!local) {
     const uint32_t own_top = top;
@@ -1028,6 +1037,7 @@ __global__ void __launch_bounds__(kFT, 4) filter_kernel(const FilterParams p) {
     // Vectors that hold any go to a queue of the warp; then its lanes take an element each (a
     // lane with its whole vector, as it comes, takes four times as long: the others wait).
     auto scan = [&](uint32_t first, uint32_t most) {
+      if (!__any_sync(0xffffffffu, tmax >= low_x)) return;
       uint32_t queued = 0;
       auto take = [&](uint32_t n) {
         __syncwarp();
@@ -1120,11 +1130,11 @@ __global__ void __launch_bounds__(kFT, 4) filter_kernel(const FilterParams p) {
       // The last kept column and those after it weigh more than (1 - p) Z and are at most
       // V, so it weighs more than (1 - p) Z / V (and a little less, for this estimate's roundings).
       octaves = 0x1p-16f - log2f((1.f - p_mass) * ((float)Z * 0x1p-44f) / (float)p.V);
-      float away = octaves / sc.ch;
+      float away = octaves * sc.octave;
       away += 0x1p-20f * (fabsf(M) + away);
       // Where what is large holds the share by itself, that is the list.
       if ((float)large > (p_mass + 0x1p-16f) * (float)Z) {
-        const float reach = (M - lowest) + 12.f / sc.ch;
+        const float reach = (M - lowest) + 12.f * sc.octave;
         away = fminf(away, reach + 0x1p-20f * (fabsf(M) + fabsf(lowest) + reach));
       }
       low = max(low, M == INFINITY ? top : value_key(M - away));
@@ -1243,7 +1253,7 @@ __global__ void __launch_bounds__(kFT, 4) filter_kernel(const FilterParams p) {
   };
   unsigned long long mine_w;
   if (cut.key == 0 && floor == -INFINITY) {  // every column
-    mine_w = s.mass(sc, sh.queue[warp], large);
+    mine_w = s.mass(sc, large);
   } else {
     mine_w = s.kept_mass(sc, cut);
   }
@@ -1269,19 +1279,49 @@ __global__ void __launch_bounds__(kFT, 4) filter_kernel(const FilterParams p) {
   }
   if (draws) {
     const unsigned long long at = share_of(u, sum);
-    for (int w = 0; w < warp; ++w) before += sh.warp_sum[w];
-    if (before <= at && at < before + mine_w) {
-      const int i = find_column<E::kN, 256>(s.lo, s.hi, lane, at - before, kSumBits, kept);
-      if (lane == 0) {
-        const int col = s.col0 + i;
-        if (kVerify) {
-          p.cuts[row].token = col;
-        } else {
-          p.out_tokens[row] = col;
-          if (p.out_prob) {
-            const float2 w = weight(sc, sh.table, E::load(src, col));
-            const float b = __ull2float_rz(sum), bl = (float)(sum - (unsigned long long)b), q = w.x * 0x1p44f / b;
-            p.out_prob[row] = q + (fmaf(-q, b, w.x * 0x1p44f) + (w.y * 0x1p44f - q * bl)) / b;
+    // the CTA and the warp in whose share the draw falls; then all warps take a part of that share
+    int owner = -1;
+    unsigned long long pre = before;
+    for (int w = 0; w < kFW; ++w) {
+      const unsigned long long next = pre + sh.warp_sum[w];
+      if (pre <= at && at < next) {
+        owner = w;
+        before = pre;
+      }
+      pre = next;
+    }
+    if (owner >= 0) {  // (the same in all its threads)
+      const int o_lo = min(s.n, owner * p.seg), o_hi = min(s.n, o_lo + p.seg), sub = (o_hi - o_lo + kFW - 1) / kFW;
+      s.lo = min(o_hi, o_lo + warp * sub);
+      s.hi = min(o_hi, s.lo + sub);
+      mine_w = s.kept_mass(sc, cut);
+      cta_sync();
+      if (lane == 0) sh.warp_sum[warp] = mine_w;
+      cta_sync();
+      int chosen = kFW - 1;  // (roundings may leave the last one)
+      pre = before;
+      for (int w = kFW - 1; w >= 0; --w)
+        if (sh.warp_sum[w] == 0 && chosen == w && w > 0) chosen = w - 1;
+      for (int w = 0; w < chosen; ++w) {
+        if (at < pre + sh.warp_sum[w]) {
+          chosen = w;
+          break;
+        }
+        pre += sh.warp_sum[w];
+      }
+      if (warp == chosen) {
+        const int i = find_column<E::kN, 256>(s.lo, s.hi, lane, at > pre ? at - pre : 0ull, kSumBits, kept);
+        if (lane == 0) {
+          const int col = s.col0 + i;
+          if (kVerify) {
+            p.cuts[row].token = col;
+          } else {
+            p.out_tokens[row] = col;
+            if (p.out_prob) {
+              const float2 w = weight(sc, sh.table, E::load(src, col));
+              const float b = __ull2float_rz(sum), bl = (float)(sum - (unsigned long long)b), q = w.x * 0x1p44f / b;
+              p.out_prob[row] = q + (fmaf(-q, b, w.x * 0x1p44f) + (w.y * 0x1p44f - q * bl)) / b;
+            }
           }
         }
       }
