@@ -52,7 +52,8 @@ constexpr int kSteps = 4 * kFT;   // bins of the search for a cut over the whole
 struct FilterShared {
   uint64_t bars[kFW];
   unsigned long long sums[2][kMaxCluster];  // exchanged by the CTAs, in turns
-  unsigned long long warp_sum[kFW], warp_large[kFW];
+  unsigned long long warp_sum[kFW], warp_large[2][kFW];
+  unsigned long long large[2][kMaxCluster];
   uint32_t counts[2][kMaxCluster];
   uint32_t warp_count[kFW];
   uint32_t maxima[kMaxCluster], bounds[kMaxCluster], shares[kMaxCluster];
@@ -143,11 +144,12 @@ struct Slice {
   // over every octave down to 2^-32: -4.9e-8 to -5.2e-8), which is put back.  The others
   // are queued (a branch in the loop would be taken by one lane or another nearly every time)
   // and weighed in full, an element a lane.  large: the share of the columns of at least 2^-12 of the largest weight.
-  __device__ __forceinline__ unsigned long long mass(const Scale& sc, unsigned long long& large) {
-    const float big = sc.inf ? -INFINITY : sc.M - 16.f * sc.octave, top = sc.inf ? sc.M : sc.M - 12.f * sc.octave;
+  __device__ __forceinline__ unsigned long long mass(const Scale& sc, unsigned long long (&large)[2]) {
+    const float big = sc.inf ? -INFINITY : sc.M - 16.f * sc.octave, top8 = sc.inf ? sc.M : sc.M - 8.f * sc.octave,
+                top12 = sc.inf ? sc.M : sc.M - 12.f * sc.octave;
     const float2 minus = make_float2(-sc.M, -sc.M), rate = make_float2(sc.ch, sc.ch);
     float small = 0.f;
-    WeightSum<256> all, most;
+    WeightSum<256> all, to8, to12;
     uint32_t queued = 0;
     auto take = [&]() {  // an element a lane: a large vector has one or two large ones
       __syncwarp();
@@ -157,7 +159,8 @@ struct Slice {
           const float x = Elt<DT>::element(v, sh->hits[warp][j], lane % Elt<DT>::kN);
           const float2 w = weight(sc, sh->table, x);
           all.add(w.x, w.y);
-          if (x >= top) most.add(w.x, w.y);
+          if (x >= top8) to8.add(w.x, w.y);
+          else if (x >= top12) to12.add(w.x, w.y);
         }
       }
       queued = 0;
@@ -195,7 +198,9 @@ struct Slice {
     look(false);
     take();
     if (__any_sync(0xffffffffu, small != small)) look(true);  // NaN columns weigh nothing
-    large = warp_sum_u64(most.fixed(kSumBits));
+    const unsigned long long at8 = to8.fixed(kSumBits);
+    large[0] = warp_sum_u64(at8);
+    large[1] = warp_sum_u64(at8 + to12.fixed(kSumBits));
     return warp_sum_u64(all.fixed(kSumBits) + fixed_weight(make_float2(small, 5.1e-8f * small), kSumBits));
   }
 
@@ -967,32 +972,14 @@ __global__ void __launch_bounds__(kFT, 4) filter_kernel(const FilterParams p) {
   }
   const float p_mass = a.p > 0.f ? a.p : 0.f;
   unsigned long long Z = 0;  // the whole row's weight (top-p alone)
-  unsigned long long large = 0;
-  if (nucleus) Z = s.mass(make_scale(key_value(top), sh.rates), large);
+  unsigned long long large[2] = {0, 0};
   cluster_wait();  // every CTA has started
   if (!local) {
-    const uint32_t own_top = top;
-    if (nucleus) {
-      if (lane == 0) {
-        sh.warp_sum[warp] = Z;
-        sh.warp_large[warp] = large;
-      }
-      cta_sync();
-    }
     if (tid < p.C) {
-      *at_rank(&sh.maxima[rank], tid) = own_top;
+      *at_rank(&sh.maxima[rank], tid) = top;
       if (small_k) {
         *at_rank(&sh.bounds[rank], tid) = bound;
         *at_rank(&sh.shares[rank], tid) = fair;
-      }
-      if (nucleus) {
-        Z = large = 0;
-        for (int w = 0; w < kFW; ++w) {
-          Z += sh.warp_sum[w];
-          large += sh.warp_large[w];
-        }
-        *at_rank(&sh.sums[0][rank], tid) = Z;
-        *at_rank(&sh.sums[1][rank], tid) = large;
       }
     }
     cluster_sync();
@@ -1111,33 +1098,36 @@ __global__ void __launch_bounds__(kFT, 4) filter_kernel(const FilterParams p) {
   if (small_k || nucleus || by_min) {
     uint32_t low = small_k ? bound << 16 : value_key(floor);
     if (nucleus) {
-      // the CTAs' weights, each relative to its own maximum
-      Z = large = 0;
-      float lowest = INFINITY;  // of the CTAs' maxima
-      if (lane < p.C) {
-        lowest = key_value(sh.maxima[lane]);
-        Z = sh.sums[0][lane];
-        large = sh.sums[1][lane];
-        if (lowest != M) {
-          const unsigned long long f = fixed_weight(weight(sc, sh.table, lowest), 62);
-          Z = __umul64hi(Z, f) << 2;
-          large = __umul64hi(large, f) << 2;
-        }
+      Z = s.mass(sc, large);
+      if (lane == 0) {
+        sh.warp_sum[warp] = Z;
+        sh.warp_large[0][warp] = large[0];
+        sh.warp_large[1][warp] = large[1];
       }
-      Z = warp_sum_u64(Z);
-      large = warp_sum_u64(large);
-      lowest = key_value(__reduce_min_sync(0xffffffffu, ordered_bits(lowest)));
+      cta_sync();
+      if (tid < 3 * p.C) {
+        const unsigned long long* part = tid < p.C ? sh.warp_sum : sh.warp_large[tid / p.C - 1];
+        unsigned long long sum = 0;
+        for (int w = 0; w < kFW; ++w) sum += part[w];
+        *at_rank(tid < p.C ? &sh.sums[0][rank] : &sh.large[tid / p.C - 1][rank], tid % p.C) = sum;
+      }
+      cluster_sync();
+      Z = large[0] = large[1] = 0;
+      for (int r = 0; r < p.C; ++r) {
+        Z += sh.sums[0][r];
+        large[0] += sh.large[0][r];
+        large[1] += sh.large[1][r];
+      }
       // The last kept column and those after it weigh more than (1 - p) Z and are at most
       // V, so it weighs more than (1 - p) Z / V (and a little less, for this estimate's roundings).
       octaves = 0x1p-16f - log2f((1.f - p_mass) * ((float)Z * 0x1p-44f) / (float)p.V);
-      float away = octaves * sc.octave;
-      away += 0x1p-20f * (fabsf(M) + away);
+      float away = octaves;
       // Where what is large holds the share by itself, that is the list.
-      if ((float)large > (p_mass + 0x1p-16f) * (float)Z) {
-        const float reach = (M - lowest) + 12.f * sc.octave;
-        away = fminf(away, reach + 0x1p-20f * (fabsf(M) + fabsf(lowest) + reach));
-      }
-      low = max(low, M == INFINITY ? top : value_key(M - away));
+      const float need = (p_mass + 0x1p-16f) * (float)Z;
+      if ((float)large[0] > need) away = fminf(away, 8.f);
+      else if ((float)large[1] > need) away = fminf(away, 12.f);
+      away *= sc.octave;
+      low = max(low, M == INFINITY ? top : value_key(M - away - 0x1p-20f * (fabsf(M) + away)));
     }
     ListMap map;
     const int L = gather(low, 0xffffffffu, map);
