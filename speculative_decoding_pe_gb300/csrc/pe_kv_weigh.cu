@@ -38,6 +38,7 @@ struct WeighParams {
 
 constexpr int kWeighThreads = 256;
 constexpr int kWeighWarps = kWeighThreads / 32;
+constexpr int kLiveRows = 64;   // (a draft batch's rejected rows are no columns)
 constexpr int kStages = 4;      // records of a warp on their way
 
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -104,6 +105,8 @@ struct WeighShared {
   int limit[kCols];
   float2 sums[kCols];   // this CTA's maximum and sum of a column
   float2 join[kWeighWarps][kCols];
+  int rows[kLiveRows];  // the request's rows that see any key, where it has so few in all
+  int live;
   int least;            // of the columns' limits
   int reach;            // of all the request's rows
 };
@@ -154,7 +157,7 @@ struct KeyWords {
 
 // Columns c0.. of the request's rows from r0 on, key head h, into shared memory.
 template <int D, int kTiles>
-__device__ __forceinline__ void load_columns(const WeighParams& p, WeighShared<D, kTiles>& sh, int r0, int h, int c0, int n) {
+__device__ __forceinline__ void load_columns(const WeighParams& p, WeighShared<D, kTiles>& sh, int r0, bool listed, int h, int c0, int n) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   __syncthreads();  // the last sweep's readers
   if (threadIdx.x == 0) sh.least = INT32_MAX;
@@ -162,7 +165,8 @@ __device__ __forceinline__ void load_columns(const WeighParams& p, WeighShared<D
   const int padded = (n + 7) & ~7;
   for (int c = warp; c < padded; c += kWeighWarps) {
     const bool live = c < n;
-    const int row = r0 + (c0 + c) / p.G, head = h * p.G + (c0 + c) % p.G;
+    const int of = (c0 + c) / p.G, head = h * p.G + (c0 + c) % p.G;
+    const int row = !live ? 0 : listed ? sh.rows[of] : r0 + of;
     uint2 w = make_uint2(0u, 0u);  // four elements, lane * 4 of D (D = 64: the upper half of the warp idles)
     if (live && 4 * lane < D)
       w = __ldg(reinterpret_cast<const uint2*>(p.q + ((long long)row * p.Hq + head) * D) + lane);
@@ -373,9 +377,10 @@ __device__ __forceinline__ void join_stats(WeighShared<D, kTiles>& sh, int tiles
 }
 __device__ __forceinline__ float log_sum(float2 v) { return v.y == 0.f ? INFINITY : v.x + log2f(v.y); }
 
-// Rows of the request, and how far they reach (nothing: no keys).
+// Rows of the request, and how far they reach (nothing: no keys); columns of a key head.
 template <int D, int kTiles>
-__device__ __forceinline__ int request_reach(const WeighParams& p, WeighShared<D, kTiles>& sh, int b, bool report, int& r0, int& r1) {
+__device__ __forceinline__ int request_reach(const WeighParams& p, WeighShared<D, kTiles>& sh, int b, bool report, int& r0, int& columns) {
+  int r1;
   request_rows(p, b, r0, r1);
   if (threadIdx.x == 0) sh.reach = 0;
   if (threadIdx.x < kWeighWarps * kStages) {
@@ -383,10 +388,28 @@ __device__ __forceinline__ int request_reach(const WeighParams& p, WeighShared<D
     mbar_init_fence();
   }
   __syncthreads();
+  const int lane = threadIdx.x & 31;
   int most = 0;
-  for (int t = r0 + threadIdx.x; t < r1; t += kWeighThreads) most = max(most, row_limit(p, t, report));
+  if (r1 - r0 <= kLiveRows) {
+    if (threadIdx.x < 32) {
+      int n = 0;
+      for (int t0 = r0; t0 < r1; t0 += 32) {
+        const int limit = t0 + lane < r1 ? row_limit(p, t0 + lane, report) : 0;
+        const uint32_t m = __ballot_sync(0xffffffffu, limit > 0);
+        if (limit > 0) sh.rows[n + __popc(m & ((1u << lane) - 1))] = t0 + lane;
+        n += __popc(m);
+        most = max(most, limit);
+      }
+      if (lane == 0) sh.live = n;
+    }
+  } else {
+    for (int t = r0 + threadIdx.x; t < r1; t += kWeighThreads) most = max(most, row_limit(p, t, report));
+  }
   most = __reduce_max_sync(0xffffffffu, most);
-  if ((threadIdx.x & 31) == 0 && most) atomicMax(&sh.reach, most);
+  if (lane == 0 && most) atomicMax(&sh.reach, most);
+  __syncthreads();
+  columns = (r1 - r0 <= kLiveRows ? sh.live : r1 - r0) * p.G;
+  if (r1 - r0 > kLiveRows && threadIdx.x == 0) sh.live = 0;  // (all rows)
   __syncthreads();
   return sh.reach;
 }
@@ -404,16 +427,16 @@ __global__ void __launch_bounds__(kWeighThreads, 2) weigh_pair_kernel(const Weig
     if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(p.err, PE_ERR_OFFSETS);
     return;
   }
-  int r0, r1;
-  const int reach = request_reach(p, sh, b, h == 0 && rank == 0, r0, r1);
+  int r0, columns;
+  const int reach = request_reach(p, sh, b, h == 0 && rank == 0, r0, columns);
   if (reach == 0) return;
   const int recs = (reach + 15) >> 4, per = (recs + C - 1) / C;
   const int rec0 = min(recs, rank * per), rec1 = min(recs, rec0 + per);
-  const int columns = (r1 - r0) * p.G;
+  const bool listed = sh.live > 0;
   uint32_t turn = 0;  // of the warp's ring
   for (int c0 = 0; c0 < columns; c0 += 8 * kTiles) {
     const int n = min(8 * kTiles, columns - c0), tiles = (n + 7) >> 3;
-    load_columns(p, sh, r0, h, c0, n);
+    load_columns(p, sh, r0, listed, h, c0, n);
     Stats<kTiles> st;
     st.clear();
     sweep<D, kTiles, false>(p, sh, b, h, rec0, rec1, reach, tiles, false, turn, st);
@@ -438,19 +461,19 @@ __global__ void __launch_bounds__(kWeighThreads, kTiles == 1 ? 4 : 2) weigh_chun
   extern __shared__ __align__(128) unsigned char smem[];
   WeighShared<D, kTiles>& sh = *reinterpret_cast<WeighShared<D, kTiles>*>(smem);
   const int b = blockIdx.y / p.Hkv, h = blockIdx.y - b * p.Hkv;
-  int r0, r1;
-  const int reach = request_reach(p, sh, b, !kWeigh && h == 0 && blockIdx.x == 0, r0, r1);
+  int r0, columns;
+  const int reach = request_reach(p, sh, b, !kWeigh && h == 0 && blockIdx.x == 0, r0, columns);
   if (kWeigh) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (__ldcg(p.lse + (long long)p.T * p.Hq) != 0.f) return;  // offsets no partition
   }
   const int rec0 = blockIdx.x * (p.chunk >> 4), rec1 = min((reach + 15) >> 4, rec0 + (p.chunk >> 4));
   if (rec0 >= rec1) return;
-  const int columns = (r1 - r0) * p.G;
+  const bool listed = sh.live > 0;
   uint32_t turn = 0;  // of the warp's ring
   for (int c0 = 0; c0 < columns; c0 += 8 * kTiles) {
     const int n = min(8 * kTiles, columns - c0), tiles = (n + 7) >> 3;
-    load_columns(p, sh, r0, h, c0, n);
+    load_columns(p, sh, r0, listed, h, c0, n);
     Stats<kTiles> st;
     if (!kWeigh) {
       st.clear();
@@ -459,7 +482,8 @@ __global__ void __launch_bounds__(kWeighThreads, kTiles == 1 ? 4 : 2) weigh_chun
       __syncthreads();
     }
     for (int c = threadIdx.x; c < n; c += kWeighThreads) {
-      const long long at = (long long)(r0 + (c0 + c) / p.G) * p.Hq + h * p.G + (c0 + c) % p.G;
+      const int of = (c0 + c) / p.G;
+      const long long at = (long long)(listed ? sh.rows[of] : r0 + of) * p.Hq + h * p.G + (c0 + c) % p.G;
       if (kWeigh) sh.lse[c] = -__ldcg(p.lse + at);
       else p.parts[(long long)blockIdx.x * p.T * p.Hq + at] = sh.sums[c];
     }
