@@ -12,6 +12,8 @@
 // mma.sync m16n8k16 and eight columns as its columns: the sum over columns of pass
 // 3 stays in registers, and a record is converted once for all columns.  Each key
 // belongs to one warp: no atomics, the same result every time.
+#include <type_traits>
+
 #include "pe_cluster.cuh"
 #include "pe_kv.cuh"
 #include "pe_tma.cuh"
@@ -53,12 +55,14 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Two products, two differences in one instruction each.
-__device__ __forceinline__ void mul2(float& d0, float& d1, float2 f) {
-  asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\tmul.rn.f32x2 a, a, b;\n\t"
-      "mov.b64 {%0, %1}, a;\n\t}"
+// Two products, two sums in one instruction each.  The products as x y + zero with a zero that
+// the compiler does not know: a packed product with a sum directly after it was compiled
+// into one fused operation, although both say .rn.
+__device__ __forceinline__ void mul2(float& d0, float& d1, float2 f, float zero) {
+  asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\tmov.b64 c, {%4, %4};\n\t"
+      "fma.rn.f32x2 a, a, b, c;\n\tmov.b64 {%0, %1}, a;\n\t}"
       : "+f"(d0), "+f"(d1)
-      : "f"(f.x), "f"(f.y));
+      : "f"(f.x), "f"(f.y), "f"(zero));
 }
 __device__ __forceinline__ float2 add2(float d0, float d1, float2 z) {
   float2 r;
@@ -162,7 +166,7 @@ __device__ __forceinline__ void load_columns(const WeighParams& p, WeighShared<D
   __syncthreads();  // the last sweep's readers
   if (threadIdx.x == 0) sh.least = INT32_MAX;
   __syncthreads();
-  const int padded = (n + 7) & ~7;
+  const int padded = kTiles == 1 ? 8 : (n + 15) & ~15;  // (whole pairs of tiles)
   for (int c = warp; c < padded; c += kWeighWarps) {
     const bool live = c < n;
     const int of = (c0 + c) / p.G, head = h * p.G + (c0 + c) % p.G;
@@ -196,7 +200,10 @@ __device__ __forceinline__ void load_columns(const WeighParams& p, WeighShared<D
 
 constexpr float kLowest = -3.4e38f;  // below every score (finite: nothing less it is no NaN)
 
-// Running maximum and sum of two columns of each tile, over a lane's rows.
+// Sum of 2^(score - m) of two columns of each tile, over a lane's rows.  m is the larger
+// score of the lane's first two rows, which any later one may pass: the sum is a float, and only
+// where it grew by more than 2^100 the look is repeated with a running maximum (which takes half
+// as many instructions again).
 template <int kTiles>
 struct Stats {
   float m[kTiles][2], l[kTiles][2];
@@ -211,11 +218,12 @@ struct Stats {
 // 2^(score - lse) goes to out; else the columns' statistics.
 template <int D, int kTiles, bool kWeigh>
 __device__ __forceinline__ void sweep(const WeighParams& p, WeighShared<D, kTiles>& sh, int b, int h, int rec0, int rec1, int reach,
-                                      int tiles, bool more, uint32_t& turn, Stats<kTiles>& st) {
+                                      int tiles, bool more, bool track, uint32_t& turn, Stats<kTiles>& st) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int g = lane >> 2, t2 = 2 * (lane & 3);
   const int fresh = kWeigh && p.fresh ? __ldg(p.fresh + b) : INT32_MAX;
   const int page_recs = p.block_size >> 4;
+  const float zero = __int_as_float((int)(0x80000000u | ((uint32_t)p.T >> 31)));  // -0: T is not negative
   const int32_t* table = p.table + (long long)b * p.bt_width;
   uint4 q1[D / 32];  // one tile's columns stay in registers
   if (kTiles == 1) {
@@ -289,50 +297,64 @@ __device__ __forceinline__ void sweep(const WeighParams& p, WeighShared<D, kTile
       }
       const long long cur = kWeigh ? __shfl_sync(0xffffffffu, where, i) : 0;
       const int row = g + 8 * (lane & 3);  // (lanes with row >= 16 have none to write)
-      const bool edge = j0 + 16 > sh.least;
-      float w0 = 0.f, w1 = 0.f;
-#pragma unroll
-      for (int i = 0; i < kTiles; ++i) {
-        if (kTiles > 1 && i >= tiles) break;
+      const bool first = track || (r0 == rec0 + warp && i == 0);
+      float2 w = make_float2(0.f, 0.f), w2 = w;  // of rows g and g + 8
+      // kSlow: a record at which some column ends, or from which the sums' bases are taken
+      auto tile = [&](int x, float2& sum, auto slow) {
+        constexpr bool kSlow = decltype(slow)::value;
         float d[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int s = 0; s < D / 32; ++s) {
-          const uint4 q = kTiles == 1 ? q1[s] : sh.q[i][s][lane];
+          const uint4 q = kTiles == 1 ? q1[s] : sh.q[x][s][lane];
           mma_f16(d, a[2 * s], q.x, q.y);
           mma_f16(d, a[2 * s + 1], q.z, q.w);
         }
-        const float2 f = *reinterpret_cast<const float2*>(&sh.factor[8 * i + t2]);
+        const float2 f = *reinterpret_cast<const float2*>(&sh.factor[8 * x + t2]);
         // (scores are rounded once, before the differences: from a fused one a large score's
         // rounding would come back as an exponent)
-        mul2(d[0], d[1], f);
-        mul2(d[2], d[3], f);
-        if (edge) {
-          const int2 lim = *reinterpret_cast<const int2*>(&sh.limit[8 * i + t2]);
+        mul2(d[0], d[1], f, zero);
+        mul2(d[2], d[3], f, zero);
+        if (kSlow) {
+          const int2 lim = *reinterpret_cast<const int2*>(&sh.limit[8 * x + t2]);
           if (j0 + g >= lim.x) d[0] = -INFINITY;
           if (j0 + g >= lim.y) d[1] = -INFINITY;
           if (j0 + g + 8 >= lim.x) d[2] = -INFINITY;
           if (j0 + g + 8 >= lim.y) d[3] = -INFINITY;
         }
         if (kWeigh) {
-          const float2 z = *reinterpret_cast<const float2*>(&sh.lse[8 * i + t2]);  // (negative: -lse)
-          const float2 x = add2(d[0], d[1], z), y = add2(d[2], d[3], z);
-          w0 += exp2_approx(x.x) + exp2_approx(x.y);
-          w1 += exp2_approx(y.x) + exp2_approx(y.y);
+          const float2 z = *reinterpret_cast<const float2*>(&sh.lse[8 * x + t2]);  // (negative: -lse)
+          const float2 p0 = add2(d[0], d[1], z), p1 = add2(d[2], d[3], z);
+          sum = add2(sum.x, sum.y, make_float2(exp2_approx(p0.x) + exp2_approx(p0.y), exp2_approx(p1.x) + exp2_approx(p1.y)));
         } else {
-          const float hi0 = fmaxf(d[0], d[2]), hi1 = fmaxf(d[1], d[3]);
-          if (hi0 > st.m[i][0] || hi1 > st.m[i][1]) {  // rare after the first records
-            const float m0 = fmaxf(st.m[i][0], hi0), m1 = fmaxf(st.m[i][1], hi1);
-            st.l[i][0] *= exp2_approx(st.m[i][0] - m0);
-            st.l[i][1] *= exp2_approx(st.m[i][1] - m1);
-            st.m[i][0] = m0;
-            st.m[i][1] = m1;
+          if (kSlow && first) {
+            const float m0 = fmaxf(st.m[x][0], fmaxf(d[0], d[2])), m1 = fmaxf(st.m[x][1], fmaxf(d[1], d[3]));
+            st.l[x][0] *= exp2_approx(st.m[x][0] - m0);
+            st.l[x][1] *= exp2_approx(st.m[x][1] - m1);
+            st.m[x][0] = m0;
+            st.m[x][1] = m1;
           }
-          const float2 low = make_float2(-st.m[i][0], -st.m[i][1]);
-          const float2 x = add2(d[0], d[1], low), y = add2(d[2], d[3], low);
-          st.l[i][0] += exp2_approx(x.x) + exp2_approx(y.x);
-          st.l[i][1] += exp2_approx(x.y) + exp2_approx(y.y);
+          const float2 low = make_float2(-st.m[x][0], -st.m[x][1]);
+          const float2 p0 = add2(d[0], d[1], low), p1 = add2(d[2], d[3], low);
+          st.l[x][0] += exp2_approx(p0.x) + exp2_approx(p1.x);
+          st.l[x][1] += exp2_approx(p0.y) + exp2_approx(p1.y);
         }
-      }
+      };
+      // (two tiles between branches, for their products to overlap)
+      auto all_tiles = [&](auto slow) {
+        if (kTiles == 1) {
+          tile(0, w, slow);
+        } else {
+#pragma unroll
+          for (int x = 0; x < kTiles; x += 2) {
+            if (x >= tiles) break;
+            tile(x, w, slow);
+            tile(x + 1, w2, slow);
+          }
+        }
+      };
+      if (j0 + 16 > sh.least || (!kWeigh && first)) all_tiles(std::true_type());
+      else all_tiles(std::false_type());
+      float w0 = w.x + w2.x, w1 = w.y + w2.y;
       if (kWeigh) {
         w0 += __shfl_xor_sync(0xffffffffu, w0, 1);
         w1 += __shfl_xor_sync(0xffffffffu, w1, 1);
@@ -373,6 +395,20 @@ __device__ __forceinline__ void join_stats(WeighShared<D, kTiles>& sh, int tiles
 #pragma unroll
     for (int w = 1; w < kWeighWarps; ++w) v = merge(v, sh.join[w][c]);
     sh.sums[c] = v;
+  }
+}
+template <int D, int kTiles>
+__device__ __forceinline__ void statistics(const WeighParams& p, WeighShared<D, kTiles>& sh, int b, int h, int rec0, int rec1,
+                                           int reach, int n, uint32_t& turn, Stats<kTiles>& st) {
+  const int tiles = (n + 7) >> 3;
+#pragma unroll 1
+  for (int track = 0; track < 2; ++track) {
+    st.clear();
+    sweep<D, kTiles, false>(p, sh, b, h, rec0, rec1, reach, tiles, false, track, turn, st);
+    join_stats<D, kTiles>(sh, tiles, st);
+    bool large = false;
+    for (int c = threadIdx.x; c < n; c += kWeighThreads) large |= !(sh.sums[c].y <= 0x1p100f);  // (infinite ones may have become NaN)
+    if (!__syncthreads_or(large)) break;
   }
 }
 __device__ __forceinline__ float log_sum(float2 v) { return v.y == 0.f ? INFINITY : v.x + log2f(v.y); }
@@ -438,9 +474,7 @@ __global__ void __launch_bounds__(kWeighThreads, 2) weigh_pair_kernel(const Weig
     const int n = min(8 * kTiles, columns - c0), tiles = (n + 7) >> 3;
     load_columns(p, sh, r0, listed, h, c0, n);
     Stats<kTiles> st;
-    st.clear();
-    sweep<D, kTiles, false>(p, sh, b, h, rec0, rec1, reach, tiles, false, turn, st);
-    join_stats<D, kTiles>(sh, tiles, st);
+    statistics<D, kTiles>(p, sh, b, h, rec0, rec1, reach, n, turn, st);
     __syncwarp();
     cluster_sync();
     for (int c = threadIdx.x; c < n; c += kWeighThreads) {
@@ -450,7 +484,7 @@ __global__ void __launch_bounds__(kWeighThreads, 2) weigh_pair_kernel(const Weig
     }
     cluster_sync();  // (the sums have been read)
     __syncthreads();
-    sweep<D, kTiles, true>(p, sh, b, h, rec0, rec1, reach, tiles, c0 > 0, turn, st);
+    sweep<D, kTiles, true>(p, sh, b, h, rec0, rec1, reach, tiles, c0 > 0, false, turn, st);
   }
 }
 
@@ -476,9 +510,7 @@ __global__ void __launch_bounds__(kWeighThreads, kTiles == 1 ? 4 : 2) weigh_chun
     load_columns(p, sh, r0, listed, h, c0, n);
     Stats<kTiles> st;
     if (!kWeigh) {
-      st.clear();
-      sweep<D, kTiles, false>(p, sh, b, h, rec0, rec1, reach, tiles, false, turn, st);
-      join_stats<D, kTiles>(sh, tiles, st);
+      statistics<D, kTiles>(p, sh, b, h, rec0, rec1, reach, n, turn, st);
       __syncthreads();
     }
     for (int c = threadIdx.x; c < n; c += kWeighThreads) {
@@ -489,7 +521,7 @@ __global__ void __launch_bounds__(kWeighThreads, kTiles == 1 ? 4 : 2) weigh_chun
     }
     if (kWeigh) {
       __syncthreads();
-      sweep<D, kTiles, true>(p, sh, b, h, rec0, rec1, reach, tiles, c0 > 0, turn, st);
+      sweep<D, kTiles, true>(p, sh, b, h, rec0, rec1, reach, tiles, c0 > 0, false, turn, st);
     }
   }
 }
