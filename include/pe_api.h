@@ -239,13 +239,13 @@ typedef struct pe_filter {
   const float* min_p;
 } pe_filter;
 #define PE_MAX_SAMPLE_V 262144           /* columns of a filtered row   */
-#define PE_MAX_SAMPLE_ROWS (1 << 27)     /* filtered rows of one call   */
+#define PE_MAX_SAMPLE_ROWS (1 << 26)     /* filtered rows of one call   */
 
 /* Drafter readout by sampling (pe_draft_readout's counterpart for callers
  * that sample their drafts): out_tokens[i] is drawn from the filtered
  * distribution of logits row sample_idx[i] (row i when NULL) by u[i], under
  * the parameters of request i / (n / requests).
- *  logits     [rows, V] of `dtype`, row stride `row_stride` elements.
+ *  logits     [rows, V] of `dtype`, row stride `row_stride` elements; rows >= 1.
  *  out_prob   [n] the drawn token's probability in that distribution; or NULL.
  *  A row index outside [0, rows) gives -1 (probability 0) and PE_ERR_ROW_RANGE;
  *  parameters that are not usable, or u outside [0,1), -1 and PE_ERR_PARAM; an
@@ -655,7 +655,7 @@ size_t pe_workspace_bytes_weigh(int32_t T, int32_t Hq, int32_t bt_width, int32_t
  *  finite makes the weights of its request and key head NaN.
  *  err: PE_ERR_OFFSETS (offsets no partition of T: nothing is written);
  *  PE_ERR_BLOCK_RANGE as in pe_attn_cached.
- * B Hkv at most 65535.  Three launches; T == 0 enqueues nothing. */
+ * B Hkv at most 65535.  One launch or three; T == 0 enqueues nothing. */
 typedef struct pe_kv_weigh_args {
   int32_t T, B, Hq, Hkv, D, block_size, bt_width;
   float scale;

@@ -1,6 +1,9 @@
 // Thread-block clusters: rank, barrier, addresses in another CTA's shared memory.
 #pragma once
 
+#include <atomic>
+
+#include <cuda_runtime.h>
 #include <stdint.h>
 
 namespace pe {
@@ -43,6 +46,18 @@ __device__ __forceinline__ T* at_rank(T* p, uint32_t rank) {
 }  // namespace pe
 
 namespace pe_host {
+
+// Clusters of more than eight CTAs must be opted into once per kernel and device.
+template <class K>
+bool allow_wide_clusters(K kernel, std::atomic<unsigned long long>& done_mask) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+  const unsigned long long bit = 1ull << dev;
+  if (done_mask.load(std::memory_order_relaxed) & bit) return true;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) return false;
+  done_mask.fetch_or(bit);
+  return true;
+}
 
 // A launch in clusters of C CTAs; `dependent`: the kernel may start before the one
 // ahead of it on the stream has finished, and waits for it (griddepcontrol.wait).

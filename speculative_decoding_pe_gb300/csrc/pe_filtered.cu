@@ -5,16 +5,25 @@
 // filter_kernel: a cluster of C CTAs per row, each with a slice of it in shared
 // memory.
 //  1. Every thread takes the maximum of its columns.
-//  2. List: with a top-k of at most kListK (or top-p alone: kProbe) the k-th
-//     largest of a CTA's thread maxima is a lower bound of the k-th largest
-//     column, so the columns above the largest of the CTAs' bounds are a
-//     superset of the first k, not much larger than k.  CTA 0 gathers them and
-//     finds rank and preceding weight of each by comparing all pairs.
-//  3. Where that does not do (a larger k, more weight than the list holds,
-//     ties), the cut's value is found bit by bit, from counts and weights of the
-//     columns above a trial value, and its last column from counts of equal ones.
-//  4. The draw: the CTAs' kept weights are exchanged, the CTA and then the warp in
-//     whose share the draw falls look for the column.
+//  2. A value that every kept column reaches: under a top-k of at most kListK the k-th
+//     largest of the thread maxima; under top-p, where the columns of at least 2^-8 or 2^-12 of
+//     the largest weight hold the share, that weight, else what the last kept column weighs at
+//     least; under min-p its floor.  The columns from there on go to a list in CTA 0's shared
+//     memory, the other CTAs leave, and CTA 0 finds rank, preceding weight and draw: up to kPairs
+//     columns by comparing all pairs, up to kListCap by bins.
+//  3. Where the list does not do (a larger k, more columns than it holds, ties), a histogram over
+//     the whole row shows between which values the cut lies, the weight above is added up, and the
+//     columns between are listed; failing that (ties), the cut's value is found bit by bit.
+//  4. The draw from many columns: the CTAs' kept weights are exchanged, and the CTA, the warp and
+//     the vector in whose share the draw falls look for the column.
+//
+// 1792 rows of 151936 bf16 columns, read once (81 us at the copy rate): greedy 185 us, top-k 20 217,
+// top-p 0.95 388, unfiltered 354.  What bounds them is the time that a row's slices stay in
+// shared memory: some 3,400 clocks until they have landed, then a chain of barriers and short steps
+// (top-k 20: 14,000 clocks, 21,000 in CTA 0); four CTAs of 256 threads on an SM overlap them.
+// Of that chain: a CTA barrier takes 50 clocks, a cluster barrier with a remote store 1,100.
+// Measured and left: CTAs of 512 threads, two on an SM (top-k 20 465 us at the time, 399 with four of
+// 256); 64-bit arithmetic in every thread (the whole call 841 us, 614 without).
 // residual_kernel: a cluster per request finds the first rejection and draws
 // from max(0, p - q).
 #include "pe_filter.cuh"
@@ -322,8 +331,10 @@ struct Slice {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const double next = pre + c[i];
-      if (pre < target - slack && next >= target - slack) sh->bin = 4 * tid + i;  // the cut lies here at the earliest
-      if (pre < target + slack && next >= target + slack) sh->in_bin = 4 * tid + i;  // or here at the latest
+      // the cut lies here at the earliest, or there at the latest (atomics: two threads' roundings
+      // may both claim it, and every CTA has to take the same)
+      if (pre < target - slack && next >= target - slack) atomicMin(&sh->bin, (uint32_t)(4 * tid + i));
+      if (pre < target + slack && next >= target + slack) atomicMin(&sh->in_bin, (uint32_t)(4 * tid + i));
       pre = next;
     }
     cluster_sync();  // (the histograms have been read)
@@ -1551,7 +1562,8 @@ template <int DT, bool kVerify>
 int launch_filter(const pe::FilterParams& p, cudaStream_t st) {
   static std::atomic<unsigned long long> done{0};
   auto kernel = pe::filter_kernel<DT, kVerify>;
-  if (p.C > 8 && cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) return PE_ECUDA;
+  static std::atomic<unsigned long long> wide{0};
+  if (p.C > 8 && !pe_host::allow_wide_clusters(kernel, wide)) return PE_ECUDA;
   if (!pe_host::allow_smem(kernel, kMaxSmem, done)) return PE_ECUDA;
   const size_t slice = (size_t)p.per_cta * 16;
   const size_t smem = kHeader + (slice > sizeof(pe::FilterLists) ? slice : sizeof(pe::FilterLists));
@@ -1588,7 +1600,7 @@ int pe_draft_sample(const pe_draft_sample_args* a, void* stream) {
   if (!elt) return PE_EDTYPE;
   if (a->n < 0 || a->n > PE_MAX_SAMPLE_ROWS || a->V < 1 || a->V > PE_MAX_SAMPLE_V || a->rows < 0) return PE_EINVAL;
   if (a->n == 0) return PE_OK;
-  if (a->requests < 1 || a->n % a->requests || (!a->sample_idx && a->n > a->rows)) return PE_EINVAL;
+  if (a->rows < 1 || a->requests < 1 || a->n % a->requests || (!a->sample_idx && a->n > a->rows)) return PE_EINVAL;
   if (!a->logits || !a->u || !a->out_tokens || !a->err) return PE_EINVAL;
   int rc = rows_ok(a->logits, a->row_stride, elt, a->V);
   if (rc != PE_OK) return rc;

@@ -367,7 +367,8 @@ extern "C" int pe_kv_evict(const pe_kv_evict_args* a, void* stream) {
   auto kernel = a->D == 64 ? pe::evict_kernel<64> : pe::evict_kernel<128>;
   static std::atomic<unsigned long long> done[2];
   if (!pe_host::allow_smem(kernel, (int)sizeof(pe::EvictShared) + 4 * kMostRoom, done[a->D == 64])) return PE_ECUDA;
-  if (p.C > 8 && cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) return PE_ECUDA;
+  static std::atomic<unsigned long long> wide[2];
+  if (p.C > 8 && !pe_host::allow_wide_clusters(kernel, wide[a->D == 64])) return PE_ECUDA;
   const cudaError_t rc =
       pe_host::launch_clusters(kernel, grid, pe::kET, p.C, sizeof(pe::EvictShared) + 4 * (size_t)p.room, false, st, p);
   return rc == cudaSuccess ? pe_host::launch_status() : PE_ECUDA;

@@ -557,7 +557,7 @@ int weigh_chunk(int B, int Hkv, int64_t keys) {
 
 // Little work: pairs, one launch (one token over 4000 keys of 8 heads 14 us; three launches 19).
 // Else one tile of columns: chunks (b256 tokens 1.18 ms; the pair kernel 1.38, at its 128 registers);
-// more: pairs, where these fill the GPU (b64 drafts 1.34 ms; chunks 1.51).
+// more: pairs, where these fill the GPU (b64 drafts 0.77 ms).
 template <int D, int kTiles>
 int weigh(pe::WeighParams p, int sms, cudaStream_t st) {
   constexpr int kSmem = (int)sizeof(pe::WeighShared<D, kTiles>);
@@ -569,8 +569,8 @@ int weigh(pe::WeighParams p, int sms, cudaStream_t st) {
     if (!pe_host::allow_smem(kernel, kSmem, done[0])) return PE_ECUDA;
     p.chunks = 4;  // (CTAs of a cluster; eight: 1.46 ms, sixteen: 2.16)
     while (small && p.chunks < 16 && pairs * p.chunks * 2 <= sms && keys > 256 * p.chunks) p.chunks *= 2;
-    if (p.chunks > 8 && cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
-      return PE_ECUDA;
+    static std::atomic<unsigned long long> wide{0};
+    if (p.chunks > 8 && !pe_host::allow_wide_clusters(kernel, wide)) return PE_ECUDA;
     const cudaError_t rc = pe_host::launch_clusters(kernel, dim3((unsigned)(pairs * p.chunks)), pe::kWeighThreads, p.chunks, kSmem,
                                                     false, st, p);
     return rc == cudaSuccess ? pe_host::launch_status() : PE_ECUDA;

@@ -35,7 +35,7 @@ EVICT = dict(B=2, Hkv=8, D=64, block_size=16, bt_width=10, dst_width=4, max_keep
 
 @pytest.mark.parametrize("over, rc", [
     (dict(n=-1), EINVAL), (dict(n=7), EINVAL), (dict(requests=0), EINVAL), (dict(requests=4), EINVAL), (dict(V=0), EINVAL),
-    (dict(V=262145, row_stride=262152), EINVAL), (dict(rows=-1), EINVAL), (dict(rows=5, sample_idx=None), EINVAL),
+    (dict(V=262145, row_stride=262152), EINVAL), (dict(rows=-1), EINVAL), (dict(rows=0), EINVAL), (dict(rows=5, sample_idx=None), EINVAL),
     (dict(n=(1 << 27) + 1), EINVAL), (dict(dtype=2), EDTYPE), (dict(row_stride=992), EINVAL), (dict(row_stride=1004), EALIGN),
     (dict(row_stride=1 << 62), EINVAL), (dict(logits=None), EINVAL), (dict(u=None), EINVAL), (dict(out_tokens=None), EINVAL),
     (dict(err=None), EINVAL), (dict(logits=MIS), EALIGN), (dict(n=0, logits=None), 0)])

@@ -142,6 +142,28 @@ def test_weights_over_many_requests():
     w.check()
 
 
+@pytest.mark.parametrize("limits, Hq, Hkv, D, extra", [
+    ([[300, 0, 299, 17]], 8, 8, 128, 2600), ([[40 + i if i % 3 else 0 for i in range(14)]], 64, 8, 64, 2600),
+    ([[500] * 3], 64, 8, 128, 2600), ([[5000], [70]], 8, 4, 64, 2600), ([[7] * 70 + [900] * 5], 4, 4, 64, 5200)])
+def test_few_pairs_over_wide_tables(limits, Hq, Hkv, D, extra):
+    # a table far wider than its requests: chunks of keys as blocks of their own, most without any
+    w = Weigh(limits, Hq, Hkv, D, seed=11, extra=extra)
+    w.check()
+    v = Weigh(limits, Hq, Hkv, D, seed=11, extra=extra)
+    v.offsets[-1] += 1
+    out = torch.full_like(v.mass, -5.0)
+    v.run(out, None)
+    torch.cuda.synchronize()
+    assert int(v.err.item()) == _native.ERR_OFFSETS and bool((out == -5.0).all())
+
+
+@pytest.mark.parametrize("limits, Hq, Hkv, D", [([[60 + 31 * b + i if (b + i) % 4 else 0 for i in range(14)] for b in range(12)], 56, 8, 64),
+                                                ([[9 + b] * 3 for b in range(30)], 24, 4, 128), ([[11] * 80, [400] * 70] * 10, 4, 4, 64)])
+def test_many_pairs_of_many_columns(limits, Hq, Hkv, D):
+    w = Weigh(limits, Hq, Hkv, D, seed=12, extra=1300)
+    w.check()
+
+
 def test_a_row_weighs_one():
     # every kept row's weights sum to one per head: within the tolerance's 2^-20 and the rows' scores
     w = Weigh([[3000, 2999, 0, 17]], 32, 4, 128, seed=3)
@@ -303,6 +325,11 @@ def test_evict(case, Hkv, D, bs):
 def test_evict_many_pairs():
     # more pairs of request and head than CTAs at once
     Evict([50 + b % 77 for b in range(200)], [40] * 200, 16, 64, seed=1, in_place=True, recent=3).check()
+
+
+def test_evict_more_keys_than_shared_memory_holds():
+    for in_place in (False, True):
+        Evict([800000], [3001], 1, 64, bs=64, seed=6, sinks=4, recent=50, in_place=in_place, ties=in_place).check()
 
 
 def test_evict_special_weights():
