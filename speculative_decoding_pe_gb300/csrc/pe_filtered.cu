@@ -421,13 +421,14 @@ __device__ __forceinline__ int find_column(int lo, int hi, int lane, unsigned lo
     if (src >= 0) {
       int col = -1;
       if (lane == src) {
+        WeightSum<kBias> upto;
+        unsigned long long last = 0;
         for (int e = 0; e < kN; ++e) {
-          WeightSum<kBias> one, upto;
-          get(i, e, e + 1, one);
-          if (one.fixed(bits) == 0) continue;
-          col = i * kN + e;
-          get(i, 0, e + 1, upto);
-          if (at + (pre - mine) + upto.fixed(bits) > target) break;
+          get(i, e, e + 1, upto);
+          const unsigned long long now = upto.fixed(bits);
+          if (now > last) col = i * kN + e;
+          last = now;
+          if (at + (pre - mine) + now > target) break;
         }
       }
       found = __shfl_sync(0xffffffffu, col, src);
@@ -436,6 +437,43 @@ __device__ __forceinline__ int find_column(int lo, int hi, int lane, unsigned lo
     at += __shfl_sync(0xffffffffu, pre, 31);
   }
   return found;
+}
+
+// After an exchange of the warps' shares: in the CTA in whose share `at` falls, all warps
+// take a part of the segment of the warp in whose share it falls (`weigh` gives a part's weight);
+// the warp whose part it is, or -1 in the other CTAs.  pre: the weight before that part.
+template <int DT, class F>
+__device__ __forceinline__ int narrow(Slice<DT>& s, FilterShared& sh, int seg, int v_lo, int v_hi, unsigned long long at,
+                                      unsigned long long before, unsigned long long& pre, const F& weigh) {
+  int owner = -1;
+  pre = before;
+  for (int w = 0; w < kFW; ++w) {
+    const unsigned long long next = pre + sh.warp_sum[w];
+    if (pre <= at && at < next) {
+      owner = w;
+      before = pre;
+    }
+    pre = next;
+  }
+  if (owner < 0) return -1;  // (the same in all threads of the CTA)
+  const int o_lo = min(v_hi, v_lo + owner * seg), o_hi = min(v_hi, o_lo + seg), sub = (o_hi - o_lo + kFW - 1) / kFW;
+  s.lo = min(o_hi, o_lo + s.warp * sub);
+  s.hi = min(o_hi, s.lo + sub);
+  const unsigned long long mine = weigh();
+  cta_sync();
+  if (s.lane == 0) sh.warp_sum[s.warp] = mine;
+  cta_sync();
+  int chosen = kFW - 1;  // (roundings may leave the last part that weighs anything)
+  while (chosen > 0 && sh.warp_sum[chosen] == 0) --chosen;
+  pre = before;
+  for (int w = 0; w < chosen; ++w) {
+    if (at < pre + sh.warp_sum[w]) {
+      chosen = w;
+      break;
+    }
+    pre += sh.warp_sum[w];
+  }
+  return chosen;
 }
 
 // Largest key prefix (upper 16 bits) that at least k of the CTA's threads reach: by a
@@ -1280,49 +1318,20 @@ __global__ void __launch_bounds__(kFT, 4) filter_kernel(const FilterParams p) {
   }
   if (draws) {
     const unsigned long long at = share_of(u, sum);
-    // the CTA and the warp in whose share the draw falls; then all warps take a part of that share
-    int owner = -1;
-    unsigned long long pre = before;
-    for (int w = 0; w < kFW; ++w) {
-      const unsigned long long next = pre + sh.warp_sum[w];
-      if (pre <= at && at < next) {
-        owner = w;
-        before = pre;
-      }
-      pre = next;
-    }
-    if (owner >= 0) {  // (the same in all its threads)
-      const int o_lo = min(s.n, owner * p.seg), o_hi = min(s.n, o_lo + p.seg), sub = (o_hi - o_lo + kFW - 1) / kFW;
-      s.lo = min(o_hi, o_lo + warp * sub);
-      s.hi = min(o_hi, s.lo + sub);
-      mine_w = s.kept_mass(sc, cut);
-      cta_sync();
-      if (lane == 0) sh.warp_sum[warp] = mine_w;
-      cta_sync();
-      int chosen = kFW - 1;  // (roundings may leave the last one)
-      pre = before;
-      for (int w = kFW - 1; w >= 0; --w)
-        if (sh.warp_sum[w] == 0 && chosen == w && w > 0) chosen = w - 1;
-      for (int w = 0; w < chosen; ++w) {
-        if (at < pre + sh.warp_sum[w]) {
-          chosen = w;
-          break;
-        }
-        pre += sh.warp_sum[w];
-      }
-      if (warp == chosen) {
-        const int i = find_column<E::kN, 256>(s.lo, s.hi, lane, at > pre ? at - pre : 0ull, kSumBits, kept);
-        if (lane == 0) {
-          const int col = s.col0 + i;
-          if (kVerify) {
-            p.cuts[row].token = col;
-          } else {
-            p.out_tokens[row] = col;
-            if (p.out_prob) {
-              const float2 w = weight(sc, sh.table, E::load(src, col));
-              const float b = __ull2float_rz(sum), bl = (float)(sum - (unsigned long long)b), q = w.x * 0x1p44f / b;
-              p.out_prob[row] = q + (fmaf(-q, b, w.x * 0x1p44f) + (w.y * 0x1p44f - q * bl)) / b;
-            }
+    unsigned long long pre;
+    const int chosen = narrow<DT>(s, sh, p.seg, 0, s.n, at, before, pre, [&]() { return s.kept_mass(sc, cut); });
+    if (warp == chosen) {
+      const int i = find_column<E::kN, 256>(s.lo, s.hi, lane, at > pre ? at - pre : 0ull, kSumBits, kept);
+      if (lane == 0) {
+        const int col = s.col0 + i;
+        if (kVerify) {
+          p.cuts[row].token = col;
+        } else {
+          p.out_tokens[row] = col;
+          if (p.out_prob) {
+            const float2 w = weight(sc, sh.table, E::load(src, col));
+            const float b = __ull2float_rz(sum), bl = (float)(sum - (unsigned long long)b), q = w.x * 0x1p44f / b;
+            p.out_prob[row] = q + (fmaf(-q, b, w.x * 0x1p44f) + (w.y * 0x1p44f - q * bl)) / b;
           }
         }
       }
@@ -1483,47 +1492,104 @@ __global__ void __launch_bounds__(kFT) residual_kernel(const FilterParams p) {
   cta_sync();
   const float ith = sh.inverse[0].x, itl = sh.inverse[0].y;
   const float idh = sh.inverse[1].x, idl = sh.inverse[1].y;
-  bool from_p = false;
+  bool with_q = has_q;
+  // max(0, p - q) of one column, as the sum of two floats
+  auto add_rest = [&](float xe, float ye, int col, WeightSum<2>& ws) {
+    if (!ct.keeps(xe, col)) return;
+    float2 w = weight(st, sh.table, xe);
+    float ph = w.x * ith;
+    float pl = fmaf(w.x, ith, -ph) + fmaf(w.x, itl, w.y * ith);
+    if (with_q && cd.keeps(ye, col)) {
+      w = weight(sd, sh.table, ye);
+      const float qh = w.x * idh;
+      const float ql = fmaf(w.x, idh, -qh) + fmaf(w.x, idl, w.y * idh);
+      const float dh = ph - qh, bb = dh - ph;
+      pl = ((ph - (dh - bb)) - (qh + bb)) + (pl - ql);
+      ph = dh;
+    }
+    if (ph + pl > 0.f) ws.add(ph, pl);
+  };
   auto rest = [&](int i, int from, int to, WeightSum<2>& ws) {
-    const uint4 x = row_vector<DT>(trow, i, p.V);
-    const uint4 y = row_vector<DT>(drow, i, p.V);
-#pragma unroll
-    for (int e = 0; e < E::kN; ++e) {
-      const float xe = E::get(x, e), ye = E::get(y, e);
+    for (int e = from; e < to; ++e) {
       const int col = i * E::kN + e;
-      if (e >= from && e < to && ct.keeps(xe, col)) {
-        float2 w = weight(st, sh.table, xe);
-        float ph = w.x * ith;
-        float pl = fmaf(w.x, ith, -ph) + fmaf(w.x, itl, w.y * ith);
-        if (!from_p && has_q && cd.keeps(ye, col)) {
-          w = weight(sd, sh.table, ye);
-          const float qh = w.x * idh;
-          const float ql = fmaf(w.x, idh, -qh) + fmaf(w.x, idl, w.y * idh);
-          const float dh = ph - qh, bb = dh - ph;
-          pl = ((ph - (dh - bb)) - (qh + bb)) + (pl - ql);
-          ph = dh;
-        }
-        if (ph + pl > 0.f) ws.add(ph, pl);
-      }
+      if (col < p.V) add_rest(E::load(trow, col), E::load(drow, col), col, ws);
     }
   };
-  unsigned long long sum = 0, before = 0, mine = 0;
-  for (int turn = 0; turn < 2; ++turn) {
+  // The warp's share.  Vectors whose weights are below 2^-16 of both rows' largest go through the
+  // hardware's exponential (as in Slice::mass), where no cut asks for more; vectors below the
+  // target's cut have nothing; the others are queued and taken an element a lane.
+  const bool open = ct.key == 0 && ct.floor == -INFINITY && cd.key == 0 && cd.floor == -INFINITY && !st.inf && !(has_q && sd.inf);
+  const float big_t = open ? st.M - 16.f * st.octave : fmaxf(key_value(max(ct.key, 0x007fffffu)), ct.floor);
+  const float big_d = open && has_q ? sd.M - 16.f * sd.octave : INFINITY;
+  auto share = [&]() -> unsigned long long {
     WeightSum<2> ws;
-    for (int i = s.lo + lane; i < s.hi; i += 32) rest(i, 0, E::kN, ws);
-    mine = warp_sum_u64(ws.fixed(kBits));
-    sum = mine;
+    float small = 0.f;
+    uint32_t queued = 0;
+    auto take = [&]() {
+      __syncwarp();
+      for (uint32_t j0 = 0; j0 < queued; j0 += 32 / E::kN) {
+        const uint32_t j = j0 + lane / E::kN;
+        if (j < queued) {
+          const int e = lane % E::kN;
+          rest(sh.hits[warp][j], e, e + 1, ws);
+        }
+      }
+      queued = 0;
+      __syncwarp();
+    };
+    uint4 x = make_uint4(0u, 0u, 0u, 0u), y = x;
+    if (s.lo + lane < s.hi) {
+      x = row_vector<DT>(trow, s.lo + lane, p.V);
+      y = row_vector<DT>(drow, s.lo + lane, p.V);
+    }
+    for (int i0 = s.lo; i0 < s.hi; i0 += 32) {
+      const int i = i0 + lane;
+      const uint4 cx = x, cy = y;
+      if (i + 32 < s.hi) {  // the next ones ahead
+        x = row_vector<DT>(trow, i + 32, p.V);
+        y = row_vector<DT>(drow, i + 32, p.V);
+      }
+      bool put = false;
+      if (i < s.hi) {
+        put = E::max_of(cx) >= big_t || E::max_of(cy) >= big_d;
+        if (!put && open) {
+#pragma unroll
+          for (int e = 0; e < E::kN; ++e) {
+            const float wt = exp2_hw((fmaxf(E::get(cx, e), -INFINITY) - st.M) * st.ch);
+            const float wd = with_q ? exp2_hw((fmaxf(E::get(cy, e), -INFINITY) - sd.M) * sd.ch) : 0.f;
+            small += fmaxf(fmaf(wt, itl, wt * ith) - fmaf(wd, idl, wd * idh), 0.f);
+          }
+        }
+      }
+      const uint32_t m = __ballot_sync(0xffffffffu, put);
+      if (m) {
+        if (put) sh.hits[warp][queued + __popc(m & ((1u << lane) - 1))] = (unsigned short)i;
+        queued += __popc(m);
+        if (queued > 32) take();  // (room for another 32 is needed)
+      }
+    }
+    take();
+    return warp_sum_u64(ws.fixed(kBits) + fixed_weight(make_float2(small, 5.1e-8f * small), kBits));
+  };
+  unsigned long long sum = 0, before = 0;
+  for (int turn = 0; turn < 2; ++turn) {
+    sum = share();
     uint32_t c = 0, c_before = 0;
     s.exchange(c, sum, &before, &c_before);
     if (sum != 0) break;
-    from_p = true;
+    with_q = false;
   }
   if (sum == 0) return;  // (p's weights are not all zero)
   const unsigned long long at = share_of(u, sum);
-  for (int w = 0; w < warp; ++w) before += sh.warp_sum[w];
-  if (before <= at && at < before + mine) {
-    const int col = find_column<E::kN, 2>(s.lo, s.hi, lane, at - before, kBits, rest);
-    if (lane == 0) p.bonus[b] = col;
+  unsigned long long pre;
+  const int chosen = narrow<DT>(s, sh, p.seg, v0, v0 + vn, at, before, pre, [&]() {
+    WeightSum<2> ws;
+    for (int i = s.lo + lane; i < s.hi; i += 32) rest(i, 0, E::kN, ws);
+    return warp_sum_u64(ws.fixed(kBits));
+  });
+  if (warp == chosen) {
+    const int col = find_column<E::kN, 2>(s.lo, s.hi, lane, at > pre ? at - pre : 0ull, kBits, rest);
+    if (lane == 0 && col >= 0) p.bonus[b] = col;
   }
 }
 
