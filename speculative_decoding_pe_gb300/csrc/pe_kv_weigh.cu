@@ -548,10 +548,11 @@ __global__ void __launch_bounds__(kWeighThreads) weigh_join_kernel(const WeighPa
 
 namespace {
 
-// Keys of a chunk: as many as keep the GPU in work.
-int weigh_chunk(int B, int Hkv, int64_t keys) {
+// Keys of a chunk: as many as keep the GPU in work with `want` chunks.  With one tile of columns a
+// chunk costs little to begin with; with more it loads and converts all of them.
+int weigh_chunk(int B, int Hkv, int64_t keys, int want) {
   int chunk = 4096;
-  while (chunk > 128 && (int64_t)B * Hkv * ((keys + chunk - 1) / chunk) < 4096) chunk /= 2;
+  while (chunk > 128 && (int64_t)B * Hkv * ((keys + chunk - 1) / chunk) < want) chunk /= 2;
   return chunk;
 }
 
@@ -567,7 +568,8 @@ int weigh(pe::WeighParams p, int sms, cudaStream_t st) {
   if (small || (kTiles > 1 && pairs * 4 >= sms / 2)) {
     auto kernel = pe::weigh_pair_kernel<D, kTiles>;
     if (!pe_host::allow_smem(kernel, kSmem, done[0])) return PE_ECUDA;
-    p.chunks = 4;  // (CTAs of a cluster; eight: 1.46 ms, sixteen: 2.16)
+    p.chunks = 1;  // CTAs of a cluster: up to four (b64 drafts 1.46 ms with eight, 1.35 with four at the time)
+    while (p.chunks < 4 && keys > 1024 * p.chunks) p.chunks *= 2;
     while (small && p.chunks < 16 && pairs * p.chunks * 2 <= sms && keys > 256 * p.chunks) p.chunks *= 2;
     static std::atomic<unsigned long long> wide{0};
     if (p.chunks > 8 && !pe_host::allow_wide_clusters(kernel, wide)) return PE_ECUDA;
@@ -616,7 +618,9 @@ int pe_kv_weigh(const pe_kv_weigh_args* a, void* stream) {
   p.T = a->T, p.B = a->B, p.Hq = a->Hq, p.Hkv = a->Hkv, p.G = a->Hq / a->Hkv;
   p.block_size = a->block_size, p.bt_width = a->bt_width;
   const int64_t keys = (int64_t)a->bt_width * a->block_size;
-  p.chunk = weigh_chunk(a->B, a->Hkv, keys);
+  // columns of a request that has its even share of the rows
+  const int64_t columns = ((int64_t)a->T + a->B - 1) / a->B * p.G;
+  p.chunk = weigh_chunk(a->B, a->Hkv, keys, columns <= 8 ? 4096 : 256);
   p.chunks = (int)((keys + p.chunk - 1) / p.chunk);
   p.scale2 = (float)((double)a->scale * 1.4426950408889634);
   p.num_blocks = a->num_blocks;
@@ -630,8 +634,6 @@ int pe_kv_weigh(const pe_kv_weigh_args* a, void* stream) {
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   pe_host::DeviceInfo dev;
   if (pe_host::device_info(&dev) != PE_OK) return PE_ECUDA;
-  // columns of a request that has its even share of the rows
-  const int64_t columns = ((int64_t)p.T + p.B - 1) / p.B * p.G;
   if (a->D == 64)
     return columns <= 8 ? weigh<64, 1>(p, dev.sm_count, st) : columns <= 32 ? weigh<64, 4>(p, dev.sm_count, st) : weigh<64, 16>(p, dev.sm_count, st);
   return columns <= 8 ? weigh<128, 1>(p, dev.sm_count, st) : columns <= 32 ? weigh<128, 4>(p, dev.sm_count, st) : weigh<128, 16>(p, dev.sm_count, st);
