@@ -17,13 +17,15 @@
 //  4. The draw from many columns: the CTAs' kept weights are exchanged, and the CTA, the warp and
 //     the vector in whose share the draw falls look for the column.
 //
-// 1792 rows of 151936 bf16 columns, read once (81 us at the copy rate): greedy 185 us, top-k 20 217,
-// top-p 0.95 388, unfiltered 354.  What bounds them is the time that a row's slices stay in
-// shared memory: some 3,400 clocks until they have landed, then a chain of barriers and short steps
+// 1792 rows of 151936 bf16 columns, read once (81 us at the copy rate): greedy 184 us, top-k 20 218,
+// top-p 0.95 385, unfiltered 331.  What bounds them is the time that a row's slices stay in
+// shared memory: some 3,500 clocks until they have landed, then a chain of barriers and short steps
 // (top-k 20: 14,000 clocks, 21,000 in CTA 0); four CTAs of 256 threads on an SM overlap them.
 // Of that chain: a CTA barrier takes 50 clocks, a cluster barrier with a remote store 1,100.
-// Measured and left: CTAs of 512 threads, two on an SM (top-k 20 465 us at the time, 399 with four of
-// 256); 64-bit arithmetic in every thread (the whole call 841 us, 614 without).
+// Measured and left: CTAs of 512 threads, two on an SM (top-k 20 465 us; the step to
+// four of 256, with wider clusters and the histogram, 399); 64-bit arithmetic in every thread (1792 mixed
+// rows 841 us, 614 by the end of the step that took it out).
+// Verification of 256 such requests: 616 us, of which this kernel 572.
 // residual_kernel: a cluster per request finds the first rejection and draws
 // from max(0, p - q).
 #include "pe_filter.cuh"

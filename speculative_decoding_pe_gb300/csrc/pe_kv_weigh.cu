@@ -12,6 +12,11 @@
 // mma.sync m16n8k16 and eight columns as its columns: the sum over columns of pass
 // 3 stays in registers, and a record is converted once for all columns.  Each key
 // belongs to one warp: no atomics, the same result every time.
+//
+// One token, 256 requests of up to 65,535 keys, 4 heads of 128: 1.21 ms, 66 % of two reads at the copy
+// rate; issue slots (75 % busy) bound it, of which converting codes takes the most.  64 drafts of 14 rows,
+// up to 32,767 keys, 8 heads of 64: 0.77 ms, 7 % of the bytes' floor; products and exponentials wait
+// for each other at 16 warps an SM (mma.sync 36 % busy, ex2 19 %).
 #include <type_traits>
 
 #include "pe_cluster.cuh"
