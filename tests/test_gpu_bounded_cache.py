@@ -475,3 +475,20 @@ def test_another_stream():
     x.run(r)
     torch.cuda.synchronize()
     assert torch.equal(e.kept, f.kept) and torch.equal(e.cache, f.cache) and torch.equal(o, r)
+
+
+def test_two_calls_at_once():
+    # (many columns in one launch beside a single token's chunks, each with a workspace of its own)
+    both = [Weigh([[3000 + 7 * i, 2999] for i in range(9)], 16, 2, 64, seed=41),
+            Weigh([[9000 + 13 * i] for i in range(50)], 8, 4, 128, seed=42)]
+    want = [torch.zeros_like(w.mass) for w in both]
+    got = [torch.zeros_like(w.mass) for w in both]
+    for w, o in zip(both, want):
+        w.run(o)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in both]
+    for _ in range(8):
+        for w, o, s in zip(both, got, streams):
+            w.run(o, stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, got))

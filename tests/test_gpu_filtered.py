@@ -402,3 +402,27 @@ def test_the_same_result_every_time():
     first = sample(x, rows, u)
     for _ in range(5):
         assert sample(x, rows, u) == first
+
+
+def test_two_calls_at_once():
+    both = [Verify(40, 5, 20011, [ASKS[(i + at) % len(ASKS)] for i in range(40)], 31 + at) for at in range(2)]
+    want = []
+    for v in both:
+        v.run()
+        torch.cuda.synchronize()
+        want.append([t.clone() for t in (v.acc, v.bonus, v.chance)])
+    streams = [torch.cuda.Stream() for _ in both]
+    for v in both:
+        v.acc.fill_(-7), v.bonus.fill_(-7), v.chance.fill_(-7)
+    torch.cuda.synchronize()
+    # The parameters' arrays live until both streams are done: dropped earlier, their memory would go
+    # to the other call's parameters, made on the current stream, while a kernel still reads it.
+    held = [asked(v.rows) for v in both]
+    torch.cuda.synchronize()
+    for _ in range(8):  # each has a workspace of its own
+        for v, s, par in zip(both, streams, held):
+            _native.verify_filtered(v.target, v.draft, v.Kp, v.tokens, v.coins, v.u, v.acc, v.bonus, v.ws, v.err,
+                                    accept_prob=v.chance, stream=s, **par)
+    torch.cuda.synchronize()
+    for v, w in zip(both, want):
+        assert all(torch.equal(a, b) for a, b in zip((v.acc, v.bonus, v.chance), w))
