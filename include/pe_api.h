@@ -87,7 +87,9 @@ typedef enum pe_dtype { PE_F32 = 0, PE_BF16 = 1 } pe_dtype;
                                  NaN; the outputs are then undefined        */
 #define PE_ERR_INTERNAL 256u  /* an internal index invariant of the fused
                                  step failed; the access was skipped (never
-                                 expected: a library bug)                  */
+                                 expected: a library bug).  By every build:
+                                 a filtered draw found no column: token -1
+                                 (never expected either)                   */
 /* Raised by every build. */
 #define PE_ERR_WORKSPACE 512u /* a workspace counter or hand-off word held a
                                  value outside its legal range: the

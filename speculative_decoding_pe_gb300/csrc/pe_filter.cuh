@@ -111,6 +111,7 @@ struct WeightSum {
     lo += (h - (t - s)) + l;
     s = t;
   }
+  __device__ __forceinline__ bool positive() const { return (s - (float)kBias) + lo > 0.f; }
   // times 2^bits, as an integer: s - kBias is a multiple of the bias's last bit
   __device__ __forceinline__ unsigned long long fixed(int bits) const {
     const long long v = __float2ll_rn((s - (float)kBias) * __int_as_float((127 + bits) << 23)) +

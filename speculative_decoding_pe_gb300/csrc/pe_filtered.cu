@@ -397,8 +397,9 @@ struct Slice {
 
 // The column (relative to the slice) in a warp's segment [lo, hi) of vectors where
 // the running sum passes `target`; get(i, from, to, sum) adds columns from..to-1 of vector
-// i to a sum.  Should roundings leave none, the last column that weighs anything.
-// All lanes return it.
+// i to a sum.  Should roundings leave none, the last column that weighs anything; where every
+// vector by itself rounds to nothing (a warp's share adds up what its vectors' roundings drop),
+// the first column of any weight.  -1: there is none.  All lanes return it.
 template <int kN, int kBias, class F>
 __device__ __forceinline__ int find_column(int lo, int hi, int lane, unsigned long long target, int bits, const F& get) {
   unsigned long long at = 0;
@@ -438,12 +439,25 @@ __device__ __forceinline__ int find_column(int lo, int hi, int lane, unsigned lo
     }
     at += __shfl_sync(0xffffffffu, pre, 31);
   }
-  return found;
+  if (found >= 0) return found;
+  for (int i0 = lo; i0 < hi; i0 += 32) {
+    const int i = i0 + lane;
+    int first = -1;
+    for (int e = kN - 1; e >= 0 && i < hi; --e) {
+      WeightSum<kBias> one;
+      get(i, e, e + 1, one);
+      if (one.positive()) first = i * kN + e;
+    }
+    const uint32_t some = __ballot_sync(0xffffffffu, first >= 0);
+    if (some) return __shfl_sync(0xffffffffu, first, __ffs(some) - 1);
+  }
+  return -1;
 }
 
 // After an exchange of the warps' shares: in the CTA in whose share `at` falls, all warps
 // take a part of the segment of the warp in whose share it falls (`weigh` gives a part's weight);
-// the warp whose part it is, or -1 in the other CTAs.  pre: the weight before that part.
+// the warp whose part it is, or -1 in the other CTAs.  pre: the weight before that part.  Parts are
+// rounded by themselves: where all of them round to nothing, one warp takes the whole segment.
 template <int DT, class F>
 __device__ __forceinline__ int narrow(Slice<DT>& s, FilterShared& sh, int seg, int v_lo, int v_hi, unsigned long long at,
                                       unsigned long long before, unsigned long long& pre, const F& weigh) {
@@ -466,8 +480,13 @@ __device__ __forceinline__ int narrow(Slice<DT>& s, FilterShared& sh, int seg, i
   if (s.lane == 0) sh.warp_sum[s.warp] = mine;
   cta_sync();
   int chosen = kFW - 1;  // (roundings may leave the last part that weighs anything)
-  while (chosen > 0 && sh.warp_sum[chosen] == 0) --chosen;
+  while (chosen >= 0 && sh.warp_sum[chosen] == 0) --chosen;
   pre = before;
+  if (chosen < 0) {
+    s.lo = o_lo;
+    s.hi = o_hi;
+    return 0;
+  }
   for (int w = 0; w < chosen; ++w) {
     if (at < pre + sh.warp_sum[w]) {
       chosen = w;
@@ -1325,9 +1344,13 @@ __global__ void __launch_bounds__(kFT, 4) filter_kernel(const FilterParams p) {
     if (warp == chosen) {
       const int i = find_column<E::kN, 256>(s.lo, s.hi, lane, at > pre ? at - pre : 0ull, kSumBits, kept);
       if (lane == 0) {
-        const int col = s.col0 + i;
+        const int col = i < 0 ? -1 : s.col0 + i;
+        if (i < 0) atomicOr(p.err, PE_ERR_INTERNAL);  // (a share that is not zero has a column of some weight)
         if (kVerify) {
           p.cuts[row].token = col;
+        } else if (i < 0) {
+          p.out_tokens[row] = -1;
+          if (p.out_prob) p.out_prob[row] = 0.f;
         } else {
           p.out_tokens[row] = col;
           if (p.out_prob) {
@@ -1517,6 +1540,12 @@ __global__ void __launch_bounds__(kFT) residual_kernel(const FilterParams p) {
       if (col < p.V) add_rest(E::load(trow, col), E::load(drow, col), col, ws);
     }
   };
+  // the same of two small weights
+  auto small_rest = [&](float xe, float ye) -> float {
+    const float wt = exp2_hw((fmaxf(xe, -INFINITY) - st.M) * st.ch);
+    const float wd = with_q ? exp2_hw((fmaxf(ye, -INFINITY) - sd.M) * sd.ch) : 0.f;
+    return fmaxf(fmaf(wt, itl, wt * ith) - fmaf(wd, idl, wd * idh), 0.f);
+  };
   // The warp's share.  Vectors whose weights are below 2^-16 of both rows' largest go through the
   // hardware's exponential (as in Slice::mass), where no cut asks for more; vectors below the
   // target's cut have nothing; the others are queued and taken an element a lane.
@@ -1556,11 +1585,7 @@ __global__ void __launch_bounds__(kFT) residual_kernel(const FilterParams p) {
         put = E::max_of(cx) >= big_t || E::max_of(cy) >= big_d;
         if (!put && open) {
 #pragma unroll
-          for (int e = 0; e < E::kN; ++e) {
-            const float wt = exp2_hw((fmaxf(E::get(cx, e), -INFINITY) - st.M) * st.ch);
-            const float wd = with_q ? exp2_hw((fmaxf(E::get(cy, e), -INFINITY) - sd.M) * sd.ch) : 0.f;
-            small += fmaxf(fmaf(wt, itl, wt * ith) - fmaf(wd, idl, wd * idh), 0.f);
-          }
+          for (int e = 0; e < E::kN; ++e) small += small_rest(E::get(cx, e), E::get(cy, e));
         }
       }
       const uint32_t m = __ballot_sync(0xffffffffu, put);
@@ -1581,17 +1606,41 @@ __global__ void __launch_bounds__(kFT) residual_kernel(const FilterParams p) {
     if (sum != 0) break;
     with_q = false;
   }
-  if (sum == 0) return;  // (p's weights are not all zero)
+  auto no_column = [&]() {
+    atomicOr(p.err, PE_ERR_INTERNAL);
+    p.bonus[b] = -1;
+  };
+  if (sum == 0) {  // (p's weights are not all zero)
+    if (rank == 0 && tid == 0) no_column();
+    return;
+  }
+  // Vector by vector in the share's arithmetic: where p and q nearly agree, the other one may find
+  // no column above zero in a share that is.
+  auto alike = [&](int i, int from, int to, WeightSum<2>& ws) {
+    if (open) {
+      const uint4 x = row_vector<DT>(trow, i, p.V), y = row_vector<DT>(drow, i, p.V);
+      if (!(E::max_of(x) >= big_t || E::max_of(y) >= big_d)) {
+#pragma unroll
+        for (int e = 0; e < E::kN; ++e)
+          if (e >= from && e < to) ws.add(small_rest(E::get(x, e), E::get(y, e)), 0.f);
+        return;
+      }
+    }
+    rest(i, from, to, ws);
+  };
   const unsigned long long at = share_of(u, sum);
   unsigned long long pre;
   const int chosen = narrow<DT>(s, sh, p.seg, v0, v0 + vn, at, before, pre, [&]() {
     WeightSum<2> ws;
-    for (int i = s.lo + lane; i < s.hi; i += 32) rest(i, 0, E::kN, ws);
+    for (int i = s.lo + lane; i < s.hi; i += 32) alike(i, 0, E::kN, ws);
     return warp_sum_u64(ws.fixed(kBits));
   });
   if (warp == chosen) {
-    const int col = find_column<E::kN, 2>(s.lo, s.hi, lane, at > pre ? at - pre : 0ull, kBits, rest);
-    if (lane == 0 && col >= 0) p.bonus[b] = col;
+    const int col = find_column<E::kN, 2>(s.lo, s.hi, lane, at > pre ? at - pre : 0ull, kBits, alike);
+    if (lane == 0) {
+      if (col >= 0) p.bonus[b] = col;
+      else no_column();
+    }
   }
 }
 

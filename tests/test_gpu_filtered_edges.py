@@ -1,0 +1,70 @@
+"""Filtered sampling where roundings decide: rows whose tail holds much of the weight or next to none of
+it, tokens that no row can give, rows alike, and what an earlier call left in a workspace.
+
+Tolerances as in test_gpu_filtered.py unless a test derives its own."""
+import math
+
+import pytest
+import torch
+
+import filter_util as f
+from speculative_decoding_pe_gb300 import _native
+from test_gpu_filtered import BF, FP, NEAR, Verify, asked, gen, sample, vec
+
+pytestmark = pytest.mark.gpu
+LN2 = math.log(2.0)
+
+
+# ------------------------------------------------- shares that round to nothing
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("octaves", [44, 46, 47, 48, 49, 50, 51, 52, 60])
+def test_a_peak_over_a_bulk_next_to_nothing(octaves, dtype):
+    # A lane's columns add up to some units of the sums' last bit, a vector's or a part's to none of them.
+    V = 151936
+    x = torch.full((4, V), 1.0 - octaves * LN2, device="cuda").to(dtype)
+    for i, c in enumerate((140003, 5, 75000, V - 1)):
+        x[i, c] = 1.0
+    u = [0.0, 2.0 ** -40, 2.0 ** -33, 0.5]
+    for k in (0, 100000):  # every column; a cut
+        for v in u:
+            tok, prob = sample(x, [(1.0, k, 1.0, 0.0)] * 4, vec([v] * 4))
+            for i, c in enumerate(tok):
+                z = torch.exp((x[i].double() - 1.0))
+                if k:
+                    z[torch.argsort(-z, stable=True)[k:]] = 0.0
+                z /= z.sum()
+                run = z.cumsum(0)
+                assert 0 <= c < V and float(z[c]) > 0
+                assert float(run[c] - z[c]) <= v + NEAR and float(run[c]) >= v - NEAR
+                assert abs(prob[i] - float(z[c])) <= (2.0 ** -24 + 2.0 ** -29) * float(z[c])
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("octaves", [20, 40, 50, 56, 58, 60, 62])
+def test_a_rest_next_to_nothing(octaves, dtype):
+    # The target's rows have a bulk that the draft's lack, and the rest p - q is that bulk alone: equal weights,
+    # whose roundings are alike too (2^-20 of u covers the sums'; from 2^-50 on units of 2^-60 decide).
+    V, B, peak = 50000, 8, 40001
+    v = Verify(B, 1, V, [(1.0, 0, 1.0, 0.0)] * B, 3, dtype)
+    v.target[:] = 1.0 - octaves * LN2
+    v.target[:, peak] = 1.0
+    v.draft[:] = float("-inf")
+    v.draft[:, peak] = 1.0
+    v.draft[0::2, 7] = 1.0 - (octaves - 3) * LN2  # eight times what the target gives: rejected
+    v.tokens[0::2, 1] = 7
+    v.tokens[1::2, 1] = peak                      # accepted: the bonus row's own draw
+    v.coins.fill_(0.5)
+    v.u.copy_(vec([0.0, 0.0, 2.0 ** -45, 2.0 ** -45, 0.75, 0.75, 1.0 - 2.0 ** -24, 1.0 - 2.0 ** -24]))
+    v.run()
+    torch.cuda.synchronize()
+    assert int(v.err.item()) == 0 and v.acc.tolist() == [0, 1] * 4
+    for b in range(B):
+        c, u = int(v.bonus[b]), float(v.u[b])
+        z = torch.exp(v.target[2 * b + b % 2].double() - 1.0)
+        if b % 2 == 0:
+            z[peak] = z[7] = 0.0
+        run = z.cumsum(0) / z.sum()
+        assert 0 <= c < V and float(z[c]) > 0
+        if b % 2 or octaves <= 50:
+            near = NEAR if b % 2 else 2.0 ** -20
+            assert float(run[c] - z[c] / z.sum()) <= u + near and float(run[c]) >= u - near
