@@ -235,7 +235,7 @@ struct RowCut {
   int listed;    // kept columns in the row's list, or -1 (not listed)
   int token;     // the draw from the row (bonus rows)
   double W;      // sum of kept weights; 0: nothing to keep; -1: bad parameters
-  double wx;     // kept weight of the row's draft token; -1: not in the vocabulary
+  double wx;     // kept weight of the row's draft token; 0: not kept, or not in the vocabulary
 };
 struct Kept {  // a kept column and its weight times 2^kListBits
   unsigned long long w;

@@ -627,7 +627,7 @@ __device__ __forceinline__ void keep_record(const FilterParams& p, FilterShared&
     c.T = T;
     c.listed = store && sh.stored <= kKeptCap ? (int)sh.stored : -1;
     c.W = (double)W * (1.0 / (1ull << kListBits));
-    c.wx = draft >= 0 && draft < p.V ? (double)sh.wx * (1.0 / (1ull << kListBits)) : -1.0;
+    c.wx = (double)sh.wx * (1.0 / (1ull << kListBits));  // (a token outside [0,V) is no listed column)
   }
 }
 
@@ -1326,10 +1326,9 @@ __global__ void __launch_bounds__(kFT, 4) filter_kernel(const FilterParams p) {
     o.T = a.T;
     o.listed = -1;
     o.W = (double)sum * (1.0 / (1ull << kSumBits));
-    double wx = -1.0;
+    double wx = 0.0;
     if (draft >= 0 && draft < p.V) {
       const float x = E::load(src, draft);
-      wx = 0.0;
       if (cut.keeps(x, draft)) {
         const float2 w = weight(sc, sh.table, x);
         wx = (double)w.x + (double)w.y;
@@ -1416,6 +1415,7 @@ __global__ void __launch_bounds__(kFT) residual_kernel(const FilterParams p) {
       bool no = false;
       if (j < p.Kp) {
         const double pw = target[j].W, qw = drafts[j].W;
+        // (a token outside [0,V): 0 and 0, rejected under any coin)
         const double px = pw > 0.0 ? target[j].wx / pw : 0.0, qx = qw > 0.0 ? drafts[j].wx / qw : 0.0;
         no = !((double)__ldg(p.coins + b * p.Kp + j) * qx < px);
         if (p.chance && rank == 0) p.chance[b * p.Kp + j] = bad || !(px > 0.0) ? 0.f : px < qx ? (float)(px / qx) : 1.f;

@@ -68,3 +68,40 @@ def test_a_rest_next_to_nothing(octaves, dtype):
         if b % 2 or octaves <= 50:
             near = NEAR if b % 2 else 2.0 ** -20
             assert float(run[c] - z[c] / z.sum()) <= u + near and float(run[c]) >= u - near
+
+
+# ------------------------------------------------- tokens that no row can give
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("flat_target", [True, False])
+@pytest.mark.parametrize("ask", [(2.0, 0, 1.0, 0.0), (2.0, 20, 1.0, 0.0), (2.0, 0, 0.9, 0.0), (2.0, 600, 1.0, 0.0), (1.0, 0, 1.0, 1e-3)])
+def test_tokens_outside_the_vocabulary_are_rejected(ask, flat_target, dtype):
+    # whatever the coins and the two rows' sums of weights
+    B, Kp, V = 12, 3, 1000
+    v = Verify(B, Kp, V, [ask] * B, 41, dtype)
+    v.target.mul_(0.3 if flat_target else 2.0)
+    v.draft.mul_(2.0 if flat_target else 0.3)
+    bad = torch.tensor([-1, V, 2 ** 31 - 1, -2 ** 31, V + 8, -2], dtype=torch.int32, device="cuda")
+    at = torch.arange(B, device="cuda") % Kp
+    v.tokens[torch.arange(B, device="cuda"), 1 + at] = bad[torch.arange(B, device="cuda") % 6]
+    for coins in (0.0, 0.5, 1.0 - 2.0 ** -24, None):
+        if coins is None:
+            v.coins.copy_(torch.rand(B * Kp, generator=gen(42), device="cuda"))
+        else:
+            v.coins.fill_(coins)
+        v.check()
+        assert bool((v.acc <= at).all())
+        assert not bool(v.chance.view(B, Kp).gather(1, at[:, None]).any())
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_a_draft_that_could_not_be_drawn_is_rejected(dtype):
+    # draft_sample writes -1 where its number is not usable; the draft's row itself is sound
+    B, V = 16, 900
+    v = Verify(B, 1, V, [(1.5, 0, 1.0, 0.0)] * B, 43, dtype)
+    v.target.mul_(0.2)
+    tok, _ = sample(v.draft, v.rows, vec([float("nan")] * B), want_err=_native.ERR_PARAM)
+    assert tok == [-1] * B
+    v.tokens[:, 1] = -1
+    v.coins.fill_(0.99)
+    compared, rejected = v.check()
+    assert rejected == B and compared >= B - 2
