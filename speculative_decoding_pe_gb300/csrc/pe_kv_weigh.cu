@@ -176,8 +176,11 @@ __device__ __forceinline__ void load_columns(const WeighParams& p, WeighShared<D
     const bool live = c < n;
     const int of = (c0 + c) / p.G, head = h * p.G + (c0 + c) % p.G;
     const int row = !live ? 0 : listed ? sh.rows[of] : r0 + of;
-    uint2 w = make_uint2(0u, 0u);  // four elements, lane * 4 of D (D = 64: the upper half of the warp idles)
-    if (live && 4 * lane < D)
+    const int limit = live ? row_limit(p, row, false) : 0;
+    // four elements, lane * 4 of D (D = 64: the upper half of the warp idles); a row that sees nothing
+    // is a column of zeros: what its query holds, a NaN too, reaches no key
+    uint2 w = make_uint2(0u, 0u);
+    if (limit && 4 * lane < D)
       w = __ldg(reinterpret_cast<const uint2*>(p.q + ((long long)row * p.Hq + head) * D) + lane);
     float x[4] = {bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y)};
     float m = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
@@ -193,7 +196,6 @@ __device__ __forceinline__ void load_columns(const WeighParams& p, WeighShared<D
     if (4 * lane < D)
       reinterpret_cast<uint2*>(&sh.q[c >> 3][s >> 1][4 * (c & 7) + lane / (D / 16)])[s & 1] = make_uint2(lo, hi);
     if (lane == 0) {
-      const int limit = live ? row_limit(p, row, false) : 0;
       sh.factor[c] = fmaxf(p.scale2 * up, 1.2e-38f);  // (above 0: an infinity times it is one)
       sh.limit[c] = limit;
       sh.lse[c] = -INFINITY;
