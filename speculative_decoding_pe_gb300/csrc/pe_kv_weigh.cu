@@ -185,6 +185,9 @@ __device__ __forceinline__ void load_columns(const WeighParams& p, WeighShared<D
     float x[4] = {bf16_lo(w.x), bf16_hi(w.x), bf16_lo(w.y), bf16_hi(w.y)};
     float m = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
     m = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
+    // Not finite: NaN as a whole.  (An infinity alone may give -infinity with every key, which
+    // would count as a row that sees nothing.)
+    if (m == INFINITY) x[0] = x[1] = x[2] = x[3] = NAN;
     // the power of two below the largest: 2^e <= m < 2^(e + 1)
     const int e = m > 0.f ? max((int)(__float_as_uint(m) >> 23) - 127, -100) : 0;
     const float down = __int_as_float((127 - min(e, 126)) << 23), up = __int_as_float((127 + min(e, 126)) << 23);

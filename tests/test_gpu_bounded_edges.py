@@ -33,3 +33,22 @@ def test_rows_out_of_the_table_that_are_not_finite_give_nothing(D, many):
     torch.cuda.synchronize()
     assert int(w.err.item()) == _native.ERR_BLOCK_RANGE
     au.within(out, *w.want(None))
+
+
+@pytest.mark.parametrize("limits", [[[1], [2]], [[1] * 12, [3]], [[1] * 80, [3] * 80], [[20], [1]]])
+@pytest.mark.parametrize("Hq, Hkv, D", [(8, 2, 64), (4, 4, 128)])
+def test_a_query_with_an_infinity(limits, Hq, Hkv, D):
+    # whichever sign, and wherever the keys' signs make every score -infinity
+    G = Hq // Hkv
+    for at in range(0, D, 5):
+        for sign in (1.0, -1.0):
+            w = Weigh(limits, Hq, Hkv, D, seed=23)
+            w.q[0, G, at] = sign * float("inf")  # request 0, key head 1
+            out = torch.zeros_like(w.mass)
+            w.run(out, None)
+            torch.cuda.synchronize()
+            a, b = w.slots
+            assert int(w.err.item()) == 0
+            assert bool(out[a // 16, 1, a % 16].isnan().all()) and bool(out[b // 16, :, b % 16].isfinite().all())
+            rest = [h for h in range(Hkv) if h != 1]
+            assert bool(out[a // 16][:, rest][torch.arange(len(a)), :, a % 16].isfinite().all())
