@@ -995,7 +995,13 @@ __global__ void __launch_bounds__(kFT, 4) filter_kernel(const FilterParams p) {
   auto none = [&](double W) {
     if (rank != 0 || tid != 0) return;
     if (kVerify) {
+      // (all of it: the residual pass chooses its arithmetic by the cuts of both rows)
       RowCut& c = p.cuts[row];
+      c.cut.key = 0;
+      c.cut.tie = INT32_MAX;
+      c.cut.floor = -INFINITY;
+      c.M = 0.f;
+      c.T = a.T;
       c.listed = 0;
       c.token = -1;
       c.W = W;

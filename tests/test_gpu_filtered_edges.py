@@ -105,3 +105,29 @@ def test_a_draft_that_could_not_be_drawn_is_rejected(dtype):
     v.coins.fill_(0.99)
     compared, rejected = v.check()
     assert rejected == B and compared >= B - 2
+
+
+# ------------------------------------------------- what the workspace held
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_an_empty_draft_row_hides_what_the_workspace_held(dtype):
+    B, V = 96, 100000
+    v = Verify(B, 1, V, [(1.0, 0, 1.0, 0.0)] * B, 47, dtype)
+    v.target[:] = (-0.7 * torch.arange(B * 2, device="cuda")[:, None] / B - 12.0 +
+                   0.5 * torch.randn(B * 2, V, generator=gen(48), device="cuda")).to(dtype)
+    v.target[:, 50000], v.target[:, 9] = 1.0, float("-inf")
+    v.draft[:] = float("nan")
+    v.tokens[:, 1] = 9
+    for b in range(B):  # numbers next to borders of the weights below 2^-16
+        run = torch.exp(v.target[2 * b].double() - 1.0).cumsum(0)
+        v.u[b] = (run[30 + 1000 * b] / run[-1]).float()
+    got = []
+    for words in ([-1] * 12, [0] * 12, [0, 2 ** 31 - 1, -8388608] + [0] * 9, [-2, 5, 0x7f800000] + [1065353216] * 9):
+        held = torch.tensor(words, dtype=torch.int32, device="cuda")
+        n = v.ws.numel() // 48
+        v.ws[:48 * n].view(torch.int32).view(n, 12).copy_(held.expand(n, 12))
+        v.bonus.fill_(-7)
+        v.run()
+        torch.cuda.synchronize()
+        assert int(v.err.item()) == _native.ERR_EMPTY_ROW and not bool(v.acc.any())
+        got.append(v.bonus.tolist())
+    assert got[1:] == got[:1] * 3
