@@ -1471,8 +1471,8 @@ __global__ void __launch_bounds__(kFT) residual_kernel(const FilterParams p) {
       if (has_q) {
         const float x = E::load(drow, col);
         if (cd.keeps(x, col)) {
-          const float2 f = weight(sd, sh.table, x);
-          q = ((double)f.x + (double)f.y) / d.W;
+          // (rounded as the list's weights are: rows alike have to leave exactly nothing)
+          q = (double)fixed_weight(weight(sd, sh.table, x), kListBits) * (1.0 / (1ull << kListBits)) / d.W;
         }
       }
       whole = (unsigned long long)(pr * (double)(1ull << kBits) + 0.5);

@@ -107,6 +107,23 @@ def test_a_draft_that_could_not_be_drawn_is_rejected(dtype):
     assert rejected == B and compared >= B - 2
 
 
+# ------------------------------------------------- rows alike
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("ask", [(1.0, 20, 1.0, 0.0), (0.7, 30, 0.9999, 0.0), (1.0, 0, 1.0, 1e-12), (1.0, 300, 1.0, 0.0), (1.0, 0, 1.0, 0.0)])
+def test_rows_alike_leave_no_rest(ask, dtype):
+    # p - q is zero everywhere, for weights of every size: the bonus token comes from p
+    B, V = 10, 700
+    v = Verify(B, 1, V, [ask] * B, 44, dtype)
+    rows = -0.75 * torch.arange(V, device="cuda").float() + 0.1 * torch.randn(B, V, generator=gen(45), device="cuda")
+    rows = rows[:, torch.randperm(V, generator=gen(46), device="cuda")]
+    rows[:, 3] = float("-inf")
+    v.target[0::2], v.target[1::2], v.draft[:] = rows.to(dtype), 0.0, rows.to(dtype)
+    v.tokens[:, 1] = 3  # neither gives it
+    v.u.copy_((torch.arange(B, device="cuda") + 0.5) / B)
+    compared, rejected = v.check()
+    assert rejected == B and compared >= B - 1
+
+
 # ------------------------------------------------- what the workspace held
 @pytest.mark.parametrize("dtype", [BF, FP])
 def test_an_empty_draft_row_hides_what_the_workspace_held(dtype):
