@@ -690,6 +690,7 @@ int pe_kv_weigh(const pe_kv_weigh_args* args /* host */, void* stream);
  *  A request whose length or keep is negative or does not fit its table (size:
  *  dst_table or max_keep) is left as it is with out_lengths -1 and PE_ERR_PARAM;
  *  one with a page outside the cache likewise, with PE_ERR_BLOCK_RANGE.
+ * kept and out_lengths must not overlap lengths, keep or the tables (PE_EINVAL).
  * B Hkv at most 2^24.  One launch, no workspace; B == 0 enqueues nothing. */
 typedef struct pe_kv_evict_args {
   int32_t B, Hkv, D, block_size, bt_width, dst_width, max_keep, sinks, recent;

@@ -200,6 +200,11 @@ struct Tuning {
 Tuning tuning();
 
 inline bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+// Do two ranges of bytes share any?
+inline bool overlap(const void* p, int64_t n, const void* q, int64_t m) {
+  const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;
+  return p && q && n > 0 && m > 0 && (a < b ? b - a < (uint64_t)n : a - b < (uint64_t)m);
+}
 inline int elt_size(int dtype) { return dtype == PE_F32 ? 4 : dtype == PE_BF16 ? 2 : 0; }
 inline int launch_status() {
   return cudaGetLastError() == cudaSuccess ? PE_OK : PE_ECUDA;

@@ -349,6 +349,16 @@ extern "C" int pe_kv_evict(const pe_kv_evict_args* a, void* stream) {
       !a->err)
     return PE_EINVAL;
   if (!pe_host::aligned16(a->cache) || !pe_host::aligned16(a->mass)) return PE_EALIGN;
+  // A request's sizes and pages are read by the CTAs of all its key heads, at any time up to the last one's
+  // start, and the first one writes: they would not agree on what there is to keep, nor on their barriers.
+  const int64_t B = a->B;
+  const void* out[2] = {a->out_lengths, a->kept};
+  const int64_t out_bytes[2] = {4 * B, 4 * B * a->Hkv * a->max_keep};
+  const void* in[4] = {a->lengths, a->keep, a->block_table, a->dst_table};
+  const int64_t in_bytes[4] = {4 * B, 4 * B, 4 * B * a->bt_width, 4 * B * a->dst_width};
+  for (int o = 0; o < 2; ++o)
+    for (int i = 0; i < 4; ++i)
+      if (pe_host::overlap(out[o], out_bytes[o], in[i], in_bytes[i])) return PE_EINVAL;
   pe_host::DeviceInfo dev;
   if (pe_host::device_info(&dev) != PE_OK) return PE_ECUDA;
   pe::EvictParams p = {};

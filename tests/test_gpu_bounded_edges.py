@@ -1,10 +1,11 @@
-"""Attention weights of cached keys where queries are not finite; tolerances as in test_gpu_bounded_cache.py."""
+"""Attention weights of cached keys where queries are not finite (tolerances as in test_gpu_bounded_cache.py), and
+outputs of an eviction that lie over its inputs."""
 import pytest
 import torch
 
 import attn_util as au
 from speculative_decoding_pe_gb300 import _native
-from test_gpu_bounded_cache import Weigh
+from test_gpu_bounded_cache import Evict, Weigh
 
 pytestmark = pytest.mark.gpu
 
@@ -52,3 +53,16 @@ def test_a_query_with_an_infinity(limits, Hq, Hkv, D):
             assert bool(out[a // 16, 1, a % 16].isnan().all()) and bool(out[b // 16, :, b % 16].isfinite().all())
             rest = [h for h in range(Hkv) if h != 1]
             assert bool(out[a // 16][:, rest][torch.arange(len(a)), :, a % 16].isfinite().all())
+
+
+def test_evict_refuses_outputs_over_its_sizes():
+    # (refused on the host, before any launch)
+    n, out = torch.full((4,), 40, dtype=torch.int32, device="cuda"), torch.empty(2, dtype=torch.int32, device="cuda")
+    e = Evict([40, 40], [20, 20], 2, 64, seed=24)
+    for lengths, keep, size in ((n[:2], n[2:], n[:2]), (n[:2], n[2:], n[2:]), (n[:2], n[2:], n[1:3])):
+        with pytest.raises(_native.PEError):
+            _native.kv_evict(e.cache, e.mass, e.table, e.dst, lengths, keep, e.kept, size, e.err)
+    both = torch.tensor([40, 40, -1, -1, 20, 20], dtype=torch.int32, device="cuda")  # next to each other
+    _native.kv_evict(e.cache, e.mass, e.table, e.dst, both[:2], both[4:], e.kept, both[2:4], e.err)
+    _native.kv_evict(e.cache, e.mass, e.table, e.dst, both[:2], both[4:], e.kept, out, e.err)
+    assert int(e.err.item()) == 0 and both.tolist() == [40, 40, 20, 20, 20, 20] and out.tolist() == [20, 20]
