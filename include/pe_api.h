@@ -286,6 +286,7 @@ size_t pe_workspace_bytes_filtered(int32_t B, int32_t Kp);
  *  A request whose parameters or u_draw are not usable gets accepted_len 0,
  *  bonus_token -1, accept_prob 0 and PE_ERR_PARAM; an empty target row rejects its
  *  draft and has bonus token -1, an empty draft row counts as q = 0.
+ *  The outputs must not overlap u_accept or u_draw (PE_EINVAL).
  * Two launches; B == 0 enqueues nothing. */
 typedef struct pe_verify_filtered_args {
   int32_t B, Kp, V, dtype;

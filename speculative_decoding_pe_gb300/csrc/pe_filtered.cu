@@ -1767,6 +1767,14 @@ int pe_verify_filtered(const pe_verify_filtered_args* a, void* stream) {
   if (rc == PE_OK && a->Kp > 0) rc = rows_ok(a->draft_logits, a->draft_stride, elt, a->V);
   if (rc != PE_OK) return rc;
   if (!pe_host::aligned16(a->workspace)) return PE_EALIGN;
+  // All CTAs of a request read its coins and its number while the first one writes: over them, they would
+  // not agree on the first rejection, nor on their barriers.
+  const int64_t B = a->B, n = B * a->Kp;
+  const void* out[3] = {a->accepted_len, a->bonus_token, a->accept_prob};
+  const int64_t out_bytes[3] = {4 * B, 4 * B, 4 * n};
+  for (int o = 0; o < 3; ++o)
+    if (pe_host::overlap(out[o], out_bytes[o], a->u_accept, 4 * n) || pe_host::overlap(out[o], out_bytes[o], a->u_draw, 4 * B))
+      return PE_EINVAL;
   pe_host::DeviceInfo dev;
   if (pe_host::device_info(&dev) != PE_OK) return PE_ECUDA;
   pe::FilterParams p = {};

@@ -3,7 +3,7 @@ one's start.  Every call here is refused before CUDA is touched; fake pointers a
 import pytest
 
 from speculative_decoding_pe_gb300 import _native
-from test_bounded_abi import EINVAL, EVICT, fill, lib  # noqa: F401
+from test_bounded_abi import EINVAL, EVICT, VERIFY, fill, lib  # noqa: F401
 
 FAR = 0x10000
 
@@ -23,3 +23,13 @@ def apart(struct, at):
 def test_evict(lib, at):  # noqa: F811
     a = fill(_native.KvEvictArgs(), **EVICT, **apart(_native.KvEvictArgs, at))
     assert lib.pe_kv_evict(a, None) == EINVAL
+
+
+@pytest.mark.parametrize("at", [
+    # (two requests of three drafts each)
+    dict(accept_prob=FAR, u_accept=FAR), dict(accept_prob=FAR + 20, u_accept=FAR), dict(accept_prob=FAR, u_accept=FAR + 20),
+    dict(accept_prob=FAR, u_draw=FAR + 20), dict(accept_prob=FAR + 4, u_draw=FAR), dict(accepted_len=FAR, u_draw=FAR),
+    dict(bonus_token=FAR, u_draw=FAR + 4), dict(accepted_len=FAR + 20, u_accept=FAR), dict(bonus_token=FAR, u_accept=FAR)])
+def test_verify(lib, at):  # noqa: F811
+    a = fill(_native.VerifyFilteredArgs(), **VERIFY, **apart(_native.VerifyFilteredArgs, at))
+    assert lib.pe_verify_filtered(a, None) == EINVAL

@@ -148,3 +148,23 @@ def test_an_empty_draft_row_hides_what_the_workspace_held(dtype):
         assert int(v.err.item()) == _native.ERR_EMPTY_ROW and not bool(v.acc.any())
         got.append(v.bonus.tolist())
     assert got[1:] == got[:1] * 3
+
+
+# ------------------------------------------------- outputs over inputs
+def test_verify_refuses_outputs_over_its_numbers():
+    # (refused on the host, before any launch)
+    v = Verify(4, 3, 200, [(1.0, 0, 1.0, 0.0)] * 4, 49)
+    v.run()
+    torch.cuda.synchronize()
+    want = v.chance.clone()
+    room = torch.rand(28, device="cuda")
+    room[:12], room[12:16] = v.coins, v.u
+    coins, u, chance = v.coins, v.u, v.chance
+    for at in (0, 11, 12, 15):
+        v.coins, v.u, v.chance = room[:12], room[12:16], room[at:at + 12]
+        with pytest.raises(_native.PEError):
+            v.run()
+    v.chance = room[16:28]  # next to them
+    v.run()
+    torch.cuda.synchronize()
+    assert int(v.err.item()) == 0 and torch.equal(room[16:28], want) and torch.equal(room[:12], coins) and torch.equal(room[12:16], u)
