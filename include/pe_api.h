@@ -231,9 +231,12 @@ int pe_verify_sampled(const void* target_logits, const void* draft_logits,
  * PE_ERR_EMPTY_ROW.
  * The draw from given u in [0,1): the first column, in column order, whose
  * running sum of kept weights exceeds u times their sum.  Weights and sums
- * carry some 32 bits: tokens agree with an exact evaluation except where u
- * falls within that rounding of a border between two columns, or a prefix's
- * weight within it of p. */
+ * carry some 32 bits, but for weights below 2^-16 of the row's largest where
+ * every column counts (in rows without a filter, and in the whole that top-p
+ * takes its share of): each of those is within 2^-19 of itself, and the sum of
+ * a row's, where they are of many values, within 2^-25.  Tokens agree with an
+ * exact evaluation except where u falls within that rounding of a border
+ * between two columns, or a prefix's weight within it of p. */
 typedef struct pe_filter {
   const float* temperature;
   const int32_t* top_k;

@@ -12,7 +12,8 @@
 // w(x) = 2^((x - M) log2(e) / T), M the row's maximum, as a sum of two floats
 // with some 32 bits: the draw falls between running sums of up to V weights, and
 // with 24 bits a draw in a thousand of an unfiltered row would name the
-// neighbour of the right column.  Sums are exact integers or sums of two floats
+// neighbour of the right column.  Where all columns count, the smallest weights, which hold little,
+// are taken in fewer bits (small weights below).  Sums are exact integers or sums of two floats
 // in a fixed order, so a call's results do not depend on timing.
 #pragma once
 
@@ -66,8 +67,8 @@ struct Rates {
 __device__ __forceinline__ Rates make_rates(float T, float m) {
   Rates r;
   const double t = T > 0.f ? (double)T : 1.0, c = 1.4426950408889634 / t;
-  r.ch = (float)c;
-  r.cl = (float)(c - (double)r.ch);
+  r.ch = __double2float_rz(c);
+  r.cl = fmaxf((float)(c - (double)r.ch), 0x1p-120f);  // (above zero: -infinity times it is one)
   r.octave = (float)(t * 0.6931471805599453);
   r.far = 64.f * r.octave;
   r.log_m = m > 0.f && m < 1.f ? t * log((double)m) : 0.0;
@@ -109,6 +110,11 @@ struct WeightSum {
   __device__ __forceinline__ void add(float h, float l) {
     const float t = s + h;
     lo += (h - (t - s)) + l;
+    s = t;
+  }
+  __device__ __forceinline__ void add(float h) {
+    const float t = s + h;
+    lo += h - (t - s);
     s = t;
   }
   __device__ __forceinline__ bool positive() const { return (s - (float)kBias) + lo > 0.f; }
@@ -162,10 +168,60 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return r;
 }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{\n\t.reg .b64 a, b, c;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 a, a, b, c;\n\tmov.b64 {%0, %1}, a;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
 __device__ __forceinline__ float exp2_hw(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// Small weights: those of a vector whose largest is below 2^-16 of the row's, by the hardware's
+// exponential of the exponent (x - M) c in 24 bits.  The part of c that 24 bits leave out would put all
+// weights of a row off alike (5e-7 at T = 1.3) and is put in: c is split so that it is above zero, and a
+// masked column's exponent stays -infinity.  fp32 rows also carry what the product's rounding drops, r:
+// 2^(y + r) = 2^y (1 + r ln 2); a row's values may lie so close that the roundings go one way (2.7e-7 of the
+// sum).  In bf16 rows they differ from value to value; carrying r there makes sums hardly better and takes
+// 7 % longer (64 verifications under top-p).
+// What is left of one weight: the difference's or the exponent's rounding and the exponential's own error
+// (1.4e-7 at most), 2^-19 of itself in all (2^-18 below 2^-32).  Of a row's sum: the exponential's mean error,
+// which is put back: -5.0e-8 to -5.4e-8 over fp32 values that fill an octave, -3.2e-8 to -7.9e-8 over the hundred
+// different values of a bf16 row there (T from 0.3 to 2).
+constexpr float kSmallMean = 5.1e-8f;  // of a small weight, to be added
+constexpr float kNothing = -256.f;     // octaves, below what the exponential gives anything for
+
+// Two of them, added to sum, and what their exponents lack, to rest (times ln 2).  clean: NaN may be there.
+template <int DT>
+__device__ __forceinline__ void add_small(const Scale& s, float2 x, bool clean, float2& sum, float2& rest) {
+  const float2 rate = make_float2(s.ch, s.ch), rate_lo = make_float2(s.cl, s.cl);
+  if (DT == PE_BF16 && clean) x = make_float2(fmaxf(x.x, -INFINITY), fmaxf(x.y, -INFINITY));
+  float2 d = add2(x, make_float2(-s.M, -s.M));
+  if (DT == PE_BF16) {
+    const float2 y = fma2(d, rate, mul2(d, rate_lo));
+    sum = add2(sum, make_float2(exp2_hw(y.x), exp2_hw(y.y)));
+  } else {
+    const float least = kNothing * s.octave;
+    d = make_float2(fmaxf(d.x, least), fmaxf(d.y, least));  // (-infinity and NaN too)
+    const float2 y = mul2(d, make_float2(-s.ch, -s.ch));    // (of the other sign)
+    const float2 w = make_float2(exp2_hw(-y.x), exp2_hw(-y.y));
+    sum = add2(sum, w);
+    rest = fma2(w, fma2(d, rate_lo, fma2(d, rate, y)), rest);
+  }
+}
+// One of them.
+template <int DT>
+__device__ __forceinline__ float small_weight(const Scale& s, float x) {
+  float d = fmaxf(x, -INFINITY) - s.M;
+  if (DT == PE_BF16) return exp2_hw(fmaf(d, s.ch, d * s.cl));
+  d = fmaxf(d, kNothing * s.octave);
+  const float y = d * s.ch, w = exp2_hw(y);
+  return fmaf(w * 0.693147181f, fmaf(d, s.cl, fmaf(d, s.ch, -y)), w);
 }
 
 // ---------------------------------------------------------------- elements

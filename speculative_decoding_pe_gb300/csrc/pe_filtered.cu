@@ -149,17 +149,14 @@ struct Slice {
     }
   }
 
-  // The warp's share of the row's weight.  Vectors whose largest weight is below 2^-16
-  // go through the hardware's exponential in 24 bits: its errors are of a part of the sum
-  // that is small where few vectors are large, random but for a mean of -5.1e-8 (measured
-  // over every octave down to 2^-32: -4.9e-8 to -5.2e-8), which is put back.  The others
+  // The warp's share of the row's weight.  Vectors of small weights (pe_filter.cuh) are added up as
+  // they come, a vector at a time: a sum whose last bit is 2^-23, and what that drops.  The others
   // are queued (a branch in the loop would be taken by one lane or another nearly every time)
   // and weighed in full, an element a lane.  large: the share of the columns of at least 2^-12 of the largest weight.
   __device__ __forceinline__ unsigned long long mass(const Scale& sc, unsigned long long (&large)[2]) {
     const float big = sc.inf ? -INFINITY : sc.M - 16.f * sc.octave, top8 = sc.inf ? sc.M : sc.M - 8.f * sc.octave,
                 top12 = sc.inf ? sc.M : sc.M - 12.f * sc.octave;
-    const float2 minus = make_float2(-sc.M, -sc.M), rate = make_float2(sc.ch, sc.ch);
-    float small = 0.f;
+    WeightSum<1> small;
     WeightSum<256> all, to8, to12;
     uint32_t queued = 0;
     auto take = [&]() {  // an element a lane: a large vector has one or two large ones
@@ -178,7 +175,7 @@ struct Slice {
       __syncwarp();
     };
     auto look = [&](bool clean) {
-      float2 sum = make_float2(0.f, 0.f);
+      small = WeightSum<1>();
 #pragma unroll 2
       for (int i0 = lo; i0 < hi; i0 += 32) {
         const int i = i0 + lane;
@@ -187,13 +184,12 @@ struct Slice {
           const uint4 q = v[i];
           put = Elt<DT>::max_of(q) >= big;
           if (!put) {
+            float2 sum = make_float2(0.f, 0.f), rest = sum;
 #pragma unroll
-            for (int e = 0; e < Elt<DT>::kN; e += 2) {
-              float2 x = make_float2(Elt<DT>::get(q, e), Elt<DT>::get(q, e + 1));
-              if (clean) x = make_float2(fmaxf(x.x, -INFINITY), fmaxf(x.y, -INFINITY));
-              x = mul2(add2(x, minus), rate);
-              sum = add2(sum, make_float2(exp2_hw(x.x), exp2_hw(x.y)));
-            }
+            for (int e = 0; e < Elt<DT>::kN; e += 2)
+              add_small<DT>(sc, make_float2(Elt<DT>::get(q, e), Elt<DT>::get(q, e + 1)), clean, sum, rest);
+            if (DT == PE_F32) sum = fma2(rest, make_float2(0.693147181f, 0.693147181f), sum);
+            small.add(sum.x + sum.y);
           }
         }
         if (clean) continue;
@@ -204,15 +200,15 @@ struct Slice {
           if (queued > 32) take();  // (room for another 32 is needed)
         }
       }
-      small = sum.x + sum.y;
     };
     look(false);
     take();
-    if (__any_sync(0xffffffffu, small != small)) look(true);  // NaN columns weigh nothing
+    if (DT == PE_BF16 && __any_sync(0xffffffffu, small.lo != small.lo)) look(true);
     const unsigned long long at8 = to8.fixed(kSumBits);
     large[0] = warp_sum_u64(at8);
     large[1] = warp_sum_u64(at8 + to12.fixed(kSumBits));
-    return warp_sum_u64(all.fixed(kSumBits) + fixed_weight(make_float2(small, 5.1e-8f * small), kSumBits));
+    small.lo = fmaf(kSmallMean, (small.s - 1.f) + small.lo, small.lo);
+    return warp_sum_u64(all.fixed(kSumBits) + small.fixed(kSumBits));
   }
 
   // The warp's share of the weight that a cut keeps.
@@ -1399,7 +1395,7 @@ __device__ __forceinline__ uint4 row_vector(const char* row, int i, int V) {
 // columns come from the row's list where it has one: p - q is at most 0 elsewhere.
 // Else both rows are read again, each warp its segment.
 template <int DT>
-__global__ void __launch_bounds__(kFT) residual_kernel(const FilterParams p) {
+__global__ void __launch_bounds__(kFT, 4) residual_kernel(const FilterParams p) {
   extern __shared__ __align__(128) unsigned char smem[];
   FilterShared& sh = *reinterpret_cast<FilterShared*>(smem);
   using E = Elt<DT>;
@@ -1548,19 +1544,17 @@ __global__ void __launch_bounds__(kFT) residual_kernel(const FilterParams p) {
   };
   // the same of two small weights
   auto small_rest = [&](float xe, float ye) -> float {
-    const float wt = exp2_hw((fmaxf(xe, -INFINITY) - st.M) * st.ch);
-    const float wd = with_q ? exp2_hw((fmaxf(ye, -INFINITY) - sd.M) * sd.ch) : 0.f;
+    const float wt = small_weight<DT>(st, xe), wd = with_q ? small_weight<DT>(sd, ye) : 0.f;
     return fmaxf(fmaf(wt, itl, wt * ith) - fmaf(wd, idl, wd * idh), 0.f);
   };
-  // The warp's share.  Vectors whose weights are below 2^-16 of both rows' largest go through the
-  // hardware's exponential (as in Slice::mass), where no cut asks for more; vectors below the
+  // The warp's share.  Vectors of small weights in both rows are added up as they come (as in
+  // Slice::mass), where no cut asks for more; vectors below the
   // target's cut have nothing; the others are queued and taken an element a lane.
   const bool open = ct.key == 0 && ct.floor == -INFINITY && cd.key == 0 && cd.floor == -INFINITY && !st.inf && !(has_q && sd.inf);
   const float big_t = open ? st.M - 16.f * st.octave : fmaxf(key_value(max(ct.key, 0x007fffffu)), ct.floor);
   const float big_d = open && has_q ? sd.M - 16.f * sd.octave : INFINITY;
   auto share = [&]() -> unsigned long long {
     WeightSum<2> ws;
-    float small = 0.f;
     uint32_t queued = 0;
     auto take = [&]() {
       __syncwarp();
@@ -1590,8 +1584,10 @@ __global__ void __launch_bounds__(kFT) residual_kernel(const FilterParams p) {
       if (i < s.hi) {
         put = E::max_of(cx) >= big_t || E::max_of(cy) >= big_d;
         if (!put && open) {
+          float small = 0.f;
 #pragma unroll
           for (int e = 0; e < E::kN; ++e) small += small_rest(E::get(cx, e), E::get(cy, e));
+          ws.add(small, kSmallMean * small);
         }
       }
       const uint32_t m = __ballot_sync(0xffffffffu, put);
@@ -1602,7 +1598,7 @@ __global__ void __launch_bounds__(kFT) residual_kernel(const FilterParams p) {
       }
     }
     take();
-    return warp_sum_u64(ws.fixed(kBits) + fixed_weight(make_float2(small, 5.1e-8f * small), kBits));
+    return warp_sum_u64(ws.fixed(kBits));
   };
   unsigned long long sum = 0, before = 0;
   for (int turn = 0; turn < 2; ++turn) {
@@ -1628,7 +1624,10 @@ __global__ void __launch_bounds__(kFT) residual_kernel(const FilterParams p) {
       if (!(E::max_of(x) >= big_t || E::max_of(y) >= big_d)) {
 #pragma unroll
         for (int e = 0; e < E::kN; ++e)
-          if (e >= from && e < to) ws.add(small_rest(E::get(x, e), E::get(y, e)), 0.f);
+          if (e >= from && e < to) {
+            const float w = small_rest(E::get(x, e), E::get(y, e));
+            ws.add(w, kSmallMean * w);
+          }
         return;
       }
     }

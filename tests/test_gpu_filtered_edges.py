@@ -168,3 +168,135 @@ def test_verify_refuses_outputs_over_its_numbers():
     v.run()
     torch.cuda.synchronize()
     assert int(v.err.item()) == 0 and torch.equal(room[16:28], want) and torch.equal(room[:12], coins) and torch.equal(room[12:16], u)
+
+
+# ------------------------------------------------- tails of small weights
+# Weights below 2^-16 of the largest go through the hardware's exponential, which is off by 1.4e-7 at most after its mean
+# of -5.1e-8 has been put back.  For one value, 2^-19: bf16 rows round the exponent (half of its last bit, 2^-19 from
+# 16 to 32: 6.6e-7 of the weight), fp32 rows the difference (2^-24 of it: 2^-24 * 32 * ln 2 = 1.3e-6).  Over the values
+# of a row: measured for T from 0.3 to 2 at -5.0e-8 to -5.4e-8 in fp32, within 2^-27 of the weight after the correction,
+# and at -3.2e-8 to -7.9e-8 over bf16's some hundred values, within 2^-25.  A border moves by that times the tail's
+# share at most.
+ANY = 2.0 ** -19
+MEAN = {FP: 2.0 ** -27, BF: 2.0 ** -25}
+
+
+def tail_row(V, T, dtype, seed, least=16.5, most=19.5, at=4.0):
+    """One column of weight 1, the others of 2^-least to 2^-most: a third of the sum for 100,000 columns."""
+    x = at - T * LN2 * (least + (most - least) * torch.rand(1, V, generator=gen(seed), device="cuda"))
+    x[0, V // 3] = at
+    return x.to(dtype)
+
+
+def borders(x, T, keep=None):
+    """64-bit running sums and the whole, the tail's share."""
+    T = float(torch.tensor(T, dtype=FP))
+    w = torch.exp((x[0].double() - x[0].double().max()) / T).nan_to_num(0.0)
+    small = float(w[w < 2.0 ** -16].sum() / w.sum())
+    return w.cumsum(0), float(w.sum()), small
+
+
+def compare_draws(tok, u, run, whole, near, least):
+    u = u.double() * whole
+    want = torch.searchsorted(run, u, right=True)
+    before = torch.cat((run.new_zeros(1), run))[want]
+    clear = (torch.minimum(u - before, run[want] - u) > near * whole) | ((want == 0) & (run[want] - u > near * whole))
+    assert int(clear.sum()) >= least * u.numel()
+    wrong = clear & (tok.long() != want)
+    assert int(wrong.sum()) == 0, "%d of %d draws" % (int(wrong.sum()), int(clear.sum()))
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("T", [0.8, 1.0, 1.1, 1.3])
+@pytest.mark.parametrize("V", [100000, 30000])
+def test_draws_from_a_tail(T, V, dtype):
+    x = f.pitched(tail_row(V, T, dtype, 61))
+    n = 100000 if V > 50000 else 30000
+    u = torch.rand(n, generator=gen(62), device="cuda")
+    tok, prob, err = torch.empty(n, dtype=torch.int32, device="cuda"), torch.empty(n, device="cuda"), _native.new_error_word()
+    idx = torch.zeros(n, dtype=torch.int32, device="cuda")
+    _native.draft_sample(x, u, tok, err, temperature=vec([T]), out_prob=prob, sample_idx=idx)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    run, whole, share = borders(x, T)
+    assert share > 0.1
+    compare_draws(tok, u, run, whole, MEAN[dtype] * share + NEAR, 0.95)
+    z = torch.diff(run, prepend=run.new_zeros(1))[tok.long()] / whole
+    assert bool(((prob.double() - z).abs() <= z * (2.0 ** -24 + 2.0 ** -29 + MEAN[dtype] * share)).all())
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("T", [0.7, 1.0, 1.3])
+@pytest.mark.parametrize("octaves", [16.3, 17.1, 18.9])
+def test_draws_from_equal_small_weights(octaves, T, dtype):
+    # one value only
+    V, n = 60000, 4096
+    x = torch.full((1, V), 3.0 - T * LN2 * octaves, device="cuda").to(dtype)
+    x[0, 20000] = 3.0
+    u = torch.rand(n, generator=gen(63), device="cuda")
+    tok, err = torch.empty(n, dtype=torch.int32, device="cuda"), _native.new_error_word()
+    _native.draft_sample(x, u, tok, err, temperature=vec([T]), sample_idx=torch.zeros(n, dtype=torch.int32, device="cuda"))
+    torch.cuda.synchronize()
+    run, whole, share = borders(x, T)
+    compare_draws(tok, u, run, whole, ANY * share + NEAR, 0.8)
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("T", [0.8, 1.0, 1.3])
+def test_a_rest_of_a_tail(T, dtype):
+    # The target has a tail and a second large column at the end, the draft neither: the rest is both.
+    V, B = 100000, 600
+    v = Verify(B, 1, V, [(T, 0, 1.0, 0.0)] * B, 64, dtype)
+    row = tail_row(V, T, dtype, 65)
+    row[0, V - 1] = 4.0 - T
+    v.target[0::2], v.target[1::2] = row, 0.0
+    v.draft[:] = float("-inf")
+    v.draft[:, V // 3] = 4.0
+    v.draft[:, 7] = 4.0 - 12.0 * T
+    v.tokens[:, 1] = 7  # some 1 of 6 times what the target gives it, to be rejected by its coin
+    v.coins.fill_(0.999)
+    v.u.copy_(torch.rand(B, generator=gen(66), device="cuda"))
+    p = torch.exp((row[0].double() - 4.0) / float(torch.tensor(T, dtype=FP)))
+    q = torch.exp((v.draft[0].double() - 4.0) / float(torch.tensor(T, dtype=FP)))
+    p, q = p / p.sum(), q / q.sum()
+    if float(p[7]) >= 0.999 * float(q[7]):  # (a bf16 value may be the larger one)
+        v.draft[:, 7] = 4.0 - 10.0 * T
+        q = torch.exp((v.draft[0].double() - 4.0) / float(torch.tensor(T, dtype=FP)))
+        q = q / q.sum()
+    v.run()
+    torch.cuda.synchronize()
+    assert int(v.err.item()) == 0 and not bool(v.acc.any())
+    rest = (p - q).clamp(min=0)
+    # the tail's weights over the rest's whole
+    near = MEAN[dtype] * float(rest[rest < 2.0 ** -16].sum() / rest.sum()) + NEAR / float(rest.sum())
+    compare_draws(v.bonus, v.u, rest.cumsum(0), float(rest.sum()), near, 0.9)
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_masked_columns_in_a_tail(dtype):
+    # NaN and -infinity among small weights, alone in a vector or all of it; largest logits of any size
+    inf, nan = float("inf"), float("nan")
+    V, n = 40000, 20000
+    x = tail_row(V, 1.0, dtype, 67)
+    x[0, 100:9000], x[0, 20001::7], x[0, 5::11], x[0, 30000:30064] = -inf, nan, -inf, nan
+    x[0, V // 3] = 4.0
+    u = torch.rand(n, generator=gen(68), device="cuda")
+    idx = torch.zeros(n, dtype=torch.int32, device="cuda")
+    tok, err = torch.empty(n, dtype=torch.int32, device="cuda"), _native.new_error_word()
+    _native.draft_sample(x, u, tok, err, sample_idx=idx)
+    run, whole, share = borders(torch.where(x.isnan(), -inf, x.float()), 1.0)
+    compare_draws(tok, u, run, whole, MEAN[dtype] * share + NEAR, 0.95)
+    low = torch.finfo(dtype).min
+    for T in (2.0 ** -30, 1e-3, 1.0, 100.0, 2.0 ** 30):
+        for top, rest in ((low, -inf), (-3.0e38, low), (3.0e38, low), (3.0e38, -inf), (1e-30, -inf), (-17.0, low), (0.0, nan)):
+            y = torch.full((1, 5000), rest, device="cuda").to(dtype)
+            y[0, 17::1000] = top
+            m = 512
+            u = (torch.arange(m, device="cuda") + 0.5) / m
+            tok = torch.empty(m, dtype=torch.int32, device="cuda")
+            prob = torch.empty(m, device="cuda")
+            _native.draft_sample(y, u, tok, err, temperature=vec([T]), sample_idx=idx[:m], out_prob=prob)
+            torch.cuda.synchronize()
+            assert tok.tolist() == [17 + 1000 * int(5 * (i + 0.5) / m) for i in range(m)], (T, top, rest)
+            assert bool((prob - 0.2).abs().max() <= 2.0 ** -26)
+    assert int(err.item()) == 0
