@@ -13,8 +13,8 @@
 // with some 32 bits: the draw falls between running sums of up to V weights, and
 // with 24 bits a draw in a thousand of an unfiltered row would name the
 // neighbour of the right column.  Where all columns count, the smallest weights, which hold little,
-// are taken in fewer bits (small weights below).  Sums are exact integers or sums of two floats
-// in a fixed order, so a call's results do not depend on timing.
+// are taken in fewer bits (small weights below).  Sums are exact integers or floats with
+// what they drop, in a fixed order, so a call's results do not depend on timing.
 #pragma once
 
 #include "pe_cluster.cuh"
@@ -105,23 +105,38 @@ __device__ __forceinline__ float2 weight(const Scale& s, const float2* table, fl
 // Sum of weights: a float whose last bit is fixed by a bias larger than anything that
 // is added (so that what an addition drops is exact), and the sum of what was dropped.
 template <int kBias>
-struct WeightSum {
+struct ShortSum {
   float s = (float)kBias, lo = 0.f;
-  __device__ __forceinline__ void add(float h, float l) {
-    const float t = s + h;
-    lo += (h - (t - s)) + l;
-    s = t;
-  }
   __device__ __forceinline__ void add(float h) {
     const float t = s + h;
     lo += h - (t - s);
     s = t;
   }
-  __device__ __forceinline__ bool positive() const { return (s - (float)kBias) + lo > 0.f; }
   // times 2^bits, as an integer: s - kBias is a multiple of the bias's last bit
   __device__ __forceinline__ unsigned long long fixed(int bits) const {
     const long long v = __float2ll_rn((s - (float)kBias) * __int_as_float((127 + bits) << 23)) +
                         __float2ll_rn(lo * __int_as_float((127 + bits) << 23));
+    return v > 0 ? (unsigned long long)v : 0ull;
+  }
+};
+// The same of weights as two floats, of any size and alike: what the first float drops goes to a
+// second one with a bias of its own, of some 2^10 such pieces.  (In a plain sum, roundings of equal
+// weights below half of the first one's last bit go one way: 1e-7 of them.)
+template <int kBias>
+struct WeightSum {
+  static constexpr float kMid = (float)kBias / (1 << 13);
+  float s = (float)kBias, mid = kMid, lo = 0.f;
+  __device__ __forceinline__ void add(float h, float l) {
+    const float w = h + l;  // (l may be a 64th of h: table value and rest)
+    const float t = s + w, r = w - (t - s), u = mid + r;
+    lo += (r - (u - mid)) + (l - (w - h));
+    s = t;
+    mid = u;
+  }
+  __device__ __forceinline__ bool positive() const { return (s - (float)kBias) + ((mid - kMid) + lo) > 0.f; }
+  __device__ __forceinline__ unsigned long long fixed(int bits) const {
+    const float up = __int_as_float((127 + bits) << 23);
+    const long long v = __float2ll_rn((s - (float)kBias) * up) + __float2ll_rn((mid - kMid) * up) + __float2ll_rn(lo * up);
     return v > 0 ? (unsigned long long)v : 0ull;
   }
 };

@@ -156,8 +156,9 @@ struct Slice {
   __device__ __forceinline__ unsigned long long mass(const Scale& sc, unsigned long long (&large)[2]) {
     const float big = sc.inf ? -INFINITY : sc.M - 16.f * sc.octave, top8 = sc.inf ? sc.M : sc.M - 8.f * sc.octave,
                 top12 = sc.inf ? sc.M : sc.M - 12.f * sc.octave;
-    WeightSum<1> small;
-    WeightSum<256> all, to8, to12;
+    ShortSum<1> small;
+    ShortSum<256> to8, to12;  // (for a choice with a margin)
+    WeightSum<256> all;
     uint32_t queued = 0;
     auto take = [&]() {  // an element a lane: a large vector has one or two large ones
       __syncwarp();
@@ -167,15 +168,15 @@ struct Slice {
           const float x = Elt<DT>::element(v, sh->hits[warp][j], lane % Elt<DT>::kN);
           const float2 w = weight(sc, sh->table, x);
           all.add(w.x, w.y);
-          if (x >= top8) to8.add(w.x, w.y);
-          else if (x >= top12) to12.add(w.x, w.y);
+          if (x >= top8) to8.add(w.x + w.y);
+          else if (x >= top12) to12.add(w.x + w.y);
         }
       }
       queued = 0;
       __syncwarp();
     };
     auto look = [&](bool clean) {
-      small = WeightSum<1>();
+      small = ShortSum<1>();
 #pragma unroll 2
       for (int i0 = lo; i0 < hi; i0 += 32) {
         const int i = i0 + lane;

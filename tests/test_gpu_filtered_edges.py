@@ -300,3 +300,72 @@ def test_masked_columns_in_a_tail(dtype):
             assert tok.tolist() == [17 + 1000 * int(5 * (i + 0.5) / m) for i in range(m)], (T, top, rest)
             assert bool((prob - 0.2).abs().max() <= 2.0 ** -26)
     assert int(err.item()) == 0
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("p", [0.7, 0.9, 0.9999])
+def test_a_share_of_a_tail(p, dtype):
+    # top-p ends within the tail: its whole weight decides where
+    V, n, T = 100000, 20000, 1.1
+    x = tail_row(V, T, dtype, 69)
+    u = torch.rand(n, generator=gen(70), device="cuda")
+    tok, err = torch.empty(n, dtype=torch.int32, device="cuda"), _native.new_error_word()
+    _native.draft_sample(x, u, tok, err, temperature=vec([T]), top_p=vec([p]), sample_idx=torch.zeros(n, dtype=torch.int32, device="cuda"))
+    torch.cuda.synchronize()
+    run, whole, share = borders(x, T)
+    w = torch.diff(run, prepend=run.new_zeros(1))
+    order = torch.argsort(x[0].float(), descending=True, stable=True)
+    sums = w[order].cumsum(0)
+    p = float(torch.tensor(p, dtype=FP))
+    kept = int((sums - w[order] < p * whole).sum())
+    gap = min(abs(float(sums[kept - 1]) / whole - p), abs(float(sums[kept - 1] - w[order[kept - 1]]) / whole - p))
+    off = MEAN[dtype] * share + NEAR
+    w[order[kept:]] = 0.0
+    run = w.cumsum(0)
+    # one column more or less in the prefix, where the share falls next to a border, moves borders by its weight
+    compare_draws(tok, u, run, float(run[-1]), off + (0.0 if gap > off else 2.0 ** -16), 0.9 if gap > off else 0.0)
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("ask", [(1.1, 90000, 1.0, 0.0), (0.9, 60000, 1.0, 0.0), (1.1, 0, 1.0, 1e-6)])
+@pytest.mark.parametrize("values", [1, 5])
+def test_sums_of_equal_weights(values, ask, dtype):
+    # Behind a cut every weight is taken in full: sums of equal ones, whose roundings go one way, hold to NEAR too.
+    V, n, (T, k, _, m) = 100000, 60000, ask
+    x = torch.full((1, V), 4.0, device="cuda") - T * (11.5 + (torch.arange(V, device="cuda") % values) * 0.25)
+    x[0, V // 3] = 4.0
+    x = x.to(dtype)
+    u = torch.rand(n, generator=gen(71), device="cuda")
+    tok, err = torch.empty(n, dtype=torch.int32, device="cuda"), _native.new_error_word()
+    _native.draft_sample(x, u, tok, err, sample_idx=torch.zeros(n, dtype=torch.int32, device="cuda"), **asked([ask]))
+    torch.cuda.synchronize()
+    run, whole, share = borders(x, T)
+    w = torch.diff(run, prepend=run.new_zeros(1))
+    order = torch.argsort(x[0].float(), descending=True, stable=True)
+    if k:
+        w[order[k:]] = 0.0
+    if m:
+        w[w < float(torch.tensor(m, dtype=FP))] = 0.0
+    run = w.cumsum(0)
+    compare_draws(tok, u, run, float(run[-1]), NEAR, 0.9)
+
+
+def test_a_rest_of_equal_weights():
+    # p - q of a row without a draft's tail, behind a cut: as above, in units of p
+    V, B, T = 100000, 3000, 1.0
+    v = Verify(B, 1, 64, [(T, 0, 1.0, 0.0)] * B, 72, FP)
+    v.V, v.rows = V, [(T, 99999, 1.0, 0.0)] * B
+    row = torch.full((V,), 4.0 - 11.5, device="cuda")
+    row[V // 3], row[V - 2], row[V - 1] = 4.0, 3.0, -90.0
+    v.target = row.to(BF).expand(2 * B, V).contiguous()
+    v.draft = torch.full((B, V), float("-inf"), dtype=BF, device="cuda")
+    v.draft[:, V // 3], v.draft[:, 7] = 4.0, 0.0
+    v.tokens[:, 1] = 7
+    v.coins.fill_(0.5)
+    v.run()
+    torch.cuda.synchronize()
+    assert int(v.err.item()) == 0 and not bool(v.acc.any())
+    p, q = (torch.exp(r.double() - 4.0) for r in (v.target[0], v.draft[0]))
+    p[V - 1] = 0.0
+    rest = (p / p.sum() - q / q.sum()).clamp(min=0)
+    compare_draws(v.bonus, v.u, rest.cumsum(0), float(rest.sum()), 2.0 ** -28 / float(rest.sum()), 0.9)
