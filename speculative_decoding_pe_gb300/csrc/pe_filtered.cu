@@ -800,7 +800,9 @@ __device__ __forceinline__ void resolve_list(const FilterParams& p, FilterShared
     // (a sum of 2^kListBits is below the target exactly when it is below the next whole number)
     unsigned long long target = share_from(share, whole ? whole : sh.total);
     if (kCutOnly) target = target > above ? target - above : 1ull;
-    if (whole) target <<= kListBits - kSumBits;
+    // (a flat row's share may be more than 2^64 in the list's units: more than any list holds, where min-p left
+    // out what the share would have kept)
+    if (whole) target = min(target, ~0ull >> (kListBits - kSumBits)) << (kListBits - kSumBits);
     find_bin<false>(sh, ls, target);
 #pragma unroll
     for (int h = 0; h < kPer; ++h) select(keep[h] && bin[h] == sh.bin, h);

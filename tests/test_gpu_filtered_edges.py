@@ -369,3 +369,34 @@ def test_a_rest_of_equal_weights():
     p[V - 1] = 0.0
     rest = (p / p.sum() - q / q.sum()).clamp(min=0)
     compare_draws(v.bonus, v.u, rest.cumsum(0), float(rest.sum()), 2.0 ** -28 / float(rest.sum()), 0.9)
+
+
+# ------------------------------------------------- a share that a list cannot hold
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("V", [40003, 90000, 151936])
+def test_min_p_leaves_less_than_the_share(V, dtype):
+    # Flat rows of a weight of thousands of their largest, of which min-p leaves some hundreds of columns: top-p keeps
+    # tens of thousands, so that min-p alone decides.  Shares just above whole multiples of 2^12 of the largest weight.
+    n = 24
+    x = -3.0 * torch.rand(n, V, generator=gen(80), device="cuda")
+    x[:, torch.randperm(V, generator=gen(81), device="cuda")[:3000]] += 0.9
+    x = f.pitched(x.to(dtype))
+    w = torch.exp(x.double() - x.double().max(1, keepdim=True)[0])
+    whole = w.sum(1).tolist()
+    asks = [(1.0, 0, (4096 * (1 + i % int(whole[i] / 4096)) + 100) / whole[i], 0.55) for i in range(n)]
+    u = torch.rand(n, generator=gen(82), device="cuda")
+    tok, prob = sample(x, asks, u)
+    counted = 0
+    for i, c in enumerate(tok):
+        floor = float(x[i].double().max()) + math.log(float(torch.tensor(0.55, dtype=FP)))
+        kept = x[i].double() >= floor
+        assert 200 < int(kept.sum()) < asks[i][2] * V / 10
+        z = torch.where(kept, w[i], 0.0)
+        z /= z.sum()
+        run = z.cumsum(0)
+        want = int((run <= float(u[i])).sum())
+        if min(abs(float(run[want]) - float(u[i])), abs(float(u[i] - (run[want] - z[want])))) < NEAR:
+            continue
+        counted += 1
+        assert c == want and abs(prob[i] - float(z[c])) <= (2.0 ** -24 + 2.0 ** -29) * float(z[c])
+    assert counted >= n - 2
