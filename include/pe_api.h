@@ -284,7 +284,9 @@ size_t pe_workspace_bytes_filtered(int32_t B, int32_t Kp);
  *   bonus_token[b] = the draw by u_draw[b] from max(0, p_a - q_a) when
  *   a_b < Kp (from p_a when that is zero everywhere), from p_Kp else.
  *   accept_prob[b*Kp+j] = min(1, p_j(x) / q_j(x)) of every draft (0 where
- *   p_j(x) is 0 or the token outside [0,V)); or NULL.
+ *   p_j(x) is 0 or the token outside [0,V)); or NULL.  Weights of rows
+ *   with some hundreds of kept columns at most are held in units of 2^-52 of the
+ *   largest: chances of next to nothing have as many bits less.
  *  target_logits, draft_logits, in_tokens, u_accept as pe_verify_sampled.
  *  A request whose parameters or u_draw are not usable gets accepted_len 0,
  *  bonus_token -1, accept_prob 0 and PE_ERR_PARAM; an empty target row rejects its
@@ -640,10 +642,12 @@ int pe_attn_prompt(const pe_attn_prompt_args* args /* host */, void* stream);
  * request at its slot.  After an eviction key i of a request is no longer
  * position i: rows appended later go to slot out_length + i (positions for
  * kv_append's rotation stay the true ones, positions for pe_attn_cached and
- * pe_kv_weigh count cached keys). */
+ * pe_kv_weigh count cached keys).  The step's slot_mapping goes by position: for
+ * such a request the caller maps the slots. */
 
 /* Bytes of scratch that pe_kv_weigh needs for T rows of Hq heads over a table of
- * bt_width pages (0 for sizes out of range).  Its content does not matter
+ * bt_width pages (0 for sizes out of range): T Hq bt_width block_size / 16 and
+ * some.  Its content does not matter
  * before a call and is not kept; calls that may run concurrently need separate
  * workspaces. */
 size_t pe_workspace_bytes_weigh(int32_t T, int32_t Hq, int32_t bt_width, int32_t block_size);
@@ -656,9 +660,11 @@ size_t pe_workspace_bytes_weigh(int32_t T, int32_t Hq, int32_t bt_width, int32_t
  * pe_attn_cached (the keys' values are exact, sums and exponents fp32).
  *   old = mass[slot(j), g] for j < fresh[b], else 0 (keys that were appended
  *   since the last call: their slot's weight is of another key); fresh NULL: for
- *   every j; mass NULL: 0.
+ *   every j; mass NULL: 0.  Each 8, 32 or 128 pairs of row
+ *   and head (by the mean number of rows) are added to it with one rounding.
  *  out may be mass.  No two requests may share a page.  A query that is not
- *  finite makes the weights of its request and key head NaN.
+ *  finite, of a row that sees keys, makes the weights of its request and key
+ *  head NaN; so may a finite one whose scores pass fp32's range.
  *  err: PE_ERR_OFFSETS (offsets no partition of T: nothing is written);
  *  PE_ERR_BLOCK_RANGE as in pe_attn_cached.
  * B Hkv at most 65535.  One launch or three; T == 0 enqueues nothing. */

@@ -17,15 +17,15 @@
 //  4. The draw from many columns: the CTAs' kept weights are exchanged, and the CTA, the warp and
 //     the vector in whose share the draw falls look for the column.
 //
-// 1792 rows of 151936 bf16 columns, read once (81 us at the copy rate): greedy 184 us, top-k 20 218,
-// top-p 0.95 385, unfiltered 331.  What bounds them is the time that a row's slices stay in
+// 1792 rows of 151936 bf16 columns, read once (81 us at the copy rate): greedy 182 us, top-k 20 216,
+// top-p 0.95 395, unfiltered 349.  What bounds them is the time that a row's slices stay in
 // shared memory: some 3,500 clocks until they have landed, then a chain of barriers and short steps
 // (top-k 20: 14,000 clocks, 21,000 in CTA 0); four CTAs of 256 threads on an SM overlap them.
 // Of that chain: a CTA barrier takes 50 clocks, a cluster barrier with a remote store 1,100.
 // Measured and left: CTAs of 512 threads, two on an SM (top-k 20 465 us; the step to
 // four of 256, with wider clusters and the histogram, 399); 64-bit arithmetic in every thread (1792 mixed
 // rows 841 us, 614 by the end of the step that took it out).
-// Verification of 256 such requests: 616 us, of which this kernel 572.
+// Verification of 256 such requests: 618 us, of which this kernel 570.
 // residual_kernel: a cluster per request finds the first rejection and draws
 // from max(0, p - q).
 #include "pe_filter.cuh"
@@ -629,8 +629,7 @@ __device__ __forceinline__ void keep_record(const FilterParams& p, FilterShared&
 }
 
 // A short list, one column a thread: ranks, preceding weights and running sums in column
-// order by comparing all pairs.  (Bins, as below, take fewer steps but more barriers, and
-// the row's CTAs wait: for some 170 columns 22,000 clocks against 6,000 here.)
+// order by comparing all pairs.  (Bins, as below, take fewer steps but more barriers.)
 template <bool kVerify>
 __device__ __forceinline__ void resolve_pairs(const FilterParams& p, FilterShared& sh, FilterLists& ls, const Scale& sc, int row,
                                               int L, ListMap map, int k, float share, unsigned long long whole, float floor, float T,
