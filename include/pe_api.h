@@ -284,9 +284,7 @@ size_t pe_workspace_bytes_filtered(int32_t B, int32_t Kp);
  *   bonus_token[b] = the draw by u_draw[b] from max(0, p_a - q_a) when
  *   a_b < Kp (from p_a when that is zero everywhere), from p_Kp else.
  *   accept_prob[b*Kp+j] = min(1, p_j(x) / q_j(x)) of every draft (0 where
- *   p_j(x) is 0 or the token outside [0,V)); or NULL.  Weights of rows
- *   with some hundreds of kept columns at most are held in units of 2^-52 of the
- *   largest: chances of next to nothing have as many bits less.
+ *   p_j(x) is 0 or the token outside [0,V)); or NULL.
  *  target_logits, draft_logits, in_tokens, u_accept as pe_verify_sampled.
  *  A request whose parameters or u_draw are not usable gets accepted_len 0,
  *  bonus_token -1, accept_prob 0 and PE_ERR_PARAM; an empty target row rejects its

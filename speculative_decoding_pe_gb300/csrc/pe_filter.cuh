@@ -150,13 +150,13 @@ __device__ __forceinline__ unsigned long long fixed_weight(float2 w, int bits) {
 __device__ __forceinline__ unsigned long long share_of(float u, unsigned long long W) {
   return __umul64hi(__float2ull_rz(u * 0x1p64f), W);
 }
-// w / W in fp32 (off by half a step and 2^-40 of itself: the quotient's own rounding is
+// w / W in fp32, W times 2^bits (off by half a step and 2^-31 of itself: the quotient's own rounding is
 // corrected by the remainder).
-__device__ __forceinline__ float ratio(unsigned long long w, unsigned long long W) {
-  const float a = __ull2float_rz(w), b = __ull2float_rz(W);
-  const float al = (float)(w - (unsigned long long)a), bl = (float)(W - (unsigned long long)b);
+__device__ __forceinline__ float ratio(float2 w, unsigned long long W, int bits) {
+  const float up = __int_as_float((127 + bits) << 23);
+  const float a = w.x * up, b = __ull2float_rz(W), bl = (float)(W - (unsigned long long)b);
   const float q = a / b;
-  return q + (fmaf(-q, b, a) + (al - q * bl)) / b;
+  return q + (fmaf(-q, b, a) + (w.y * up - q * bl)) / b;
 }
 // The smallest whole number that is at least u W, and at least 1
 __device__ __forceinline__ unsigned long long share_from(float u, unsigned long long W) {

@@ -73,7 +73,7 @@ struct FilterShared {
   uint32_t cut_key;
   int cut_tie, tie;
   float2 table[32];
-  unsigned long long wx;
+  double wx;
   Rates rates;
   float2 inverse[2];
   float floor;
@@ -583,13 +583,16 @@ struct ListMap {
 };
 
 // What a row's answer needs of its kept columns, in CTA 0.
+// (A probability is of the weight itself: of one of next to nothing the list's units hold few bits.)
 template <bool kVerify>
-__device__ __forceinline__ void answer_draw(const FilterParams& p, int row, int col, unsigned long long w, unsigned long long W) {
+__device__ __forceinline__ void answer_draw(const FilterParams& p, const FilterShared& sh, const Scale& sc, int row,
+                                            unsigned long long key, unsigned long long W) {
+  const int col = (int)(0xffffffffu - (uint32_t)key);
   if (kVerify) {
     p.cuts[row].token = col;
   } else {
     p.out_tokens[row] = col;
-    if (p.out_prob) p.out_prob[row] = ratio(w, W);
+    if (p.out_prob) p.out_prob[row] = ratio(weight(sc, sh.table, key_value(key_of(key))), W, kListBits);
   }
 }
 template <bool kVerify, int kPer>
@@ -601,7 +604,10 @@ __device__ __forceinline__ void keep_record(const FilterParams& p, FilterShared&
   for (int h = 0; h < kPer; ++h) {
     if (keep[h]) {
       const int col = (int)(0xffffffffu - (uint32_t)key[h]);
-      if (col == draft) sh.wx = w[h];
+      if (col == draft) {
+        const float2 f = weight(sc, sh.table, key_value(key_of(key[h])));
+        sh.wx = (double)f.x + (double)f.y;
+      }
       if (store) {
         const uint32_t at = atomicAdd(&sh.stored, 1u);
         if (at < kKeptCap) {
@@ -624,7 +630,7 @@ __device__ __forceinline__ void keep_record(const FilterParams& p, FilterShared&
     c.T = T;
     c.listed = store && sh.stored <= kKeptCap ? (int)sh.stored : -1;
     c.W = (double)W * (1.0 / (1ull << kListBits));
-    c.wx = (double)sh.wx * (1.0 / (1ull << kListBits));  // (a token outside [0,V) is no listed column)
+    c.wx = sh.wx;  // (a token outside [0,V) is no listed column)
   }
 }
 
@@ -658,7 +664,7 @@ __device__ __forceinline__ void resolve_pairs(const FilterParams& p, FilterShare
     sh.above = 0;
     if (kVerify) {
       sh.stored = 0;
-      sh.wx = 0;
+      sh.wx = 0.0;
     }
   }
   cta_sync();
@@ -712,7 +718,7 @@ __device__ __forceinline__ void resolve_pairs(const FilterParams& p, FilterShare
     }
     upto += upto2;
     if ((L & 1) && (uint32_t)pair[L - 1].x >= inv) upto += pair[L - 1].y;
-    if (upto > at && upto - w[0] <= at) answer_draw<kVerify>(p, row, (int)(0xffffffffu - inv), w[0], W);
+    if (upto > at && upto - w[0] <= at) answer_draw<kVerify>(p, sh, sc, row, key[0], W);
   }
   if (kVerify) keep_record<kVerify, 1>(p, sh, sc, row, T, draft, W, keep, key, w);
 }
@@ -855,7 +861,7 @@ __device__ __forceinline__ void resolve_list(const FilterParams& p, FilterShared
     if (lane == 0) sh.warp_sum[warp] = least;
     if (tid == 0) {
       sh.stored = 0;
-      sh.wx = 0;
+      sh.wx = 0.0;
     }
   }
   cta_sync();
@@ -882,7 +888,7 @@ __device__ __forceinline__ void resolve_list(const FilterParams& p, FilterShared
         unsigned long long upto = sh.above;
         for (int j = 0; j < n; ++j)
           if ((uint32_t)ls.sel.key[j] >= inv) upto += ls.sel.w[j];
-        if (upto > at && upto - w[h] <= at) answer_draw<kVerify>(p, row, (int)(0xffffffffu - inv), w[h], W);
+        if (upto > at && upto - w[h] <= at) answer_draw<kVerify>(p, sh, sc, row, key[h], W);
       }
     }
   }
@@ -1356,11 +1362,7 @@ __global__ void __launch_bounds__(kFT, 4) filter_kernel(const FilterParams p) {
           if (p.out_prob) p.out_prob[row] = 0.f;
         } else {
           p.out_tokens[row] = col;
-          if (p.out_prob) {
-            const float2 w = weight(sc, sh.table, E::load(src, col));
-            const float b = __ull2float_rz(sum), bl = (float)(sum - (unsigned long long)b), q = w.x * 0x1p44f / b;
-            p.out_prob[row] = q + (fmaf(-q, b, w.x * 0x1p44f) + (w.y * 0x1p44f - q * bl)) / b;
-          }
+          if (p.out_prob) p.out_prob[row] = ratio(weight(sc, sh.table, E::load(src, col)), sum, kSumBits);
         }
       }
     }

@@ -400,3 +400,30 @@ def test_min_p_leaves_less_than_the_share(V, dtype):
         counted += 1
         assert c == want and abs(prob[i] - float(z[c])) <= (2.0 ** -24 + 2.0 ** -29) * float(z[c])
     assert counted >= n - 2
+
+
+# ------------------------------------------------- probabilities of next to nothing
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("k, V", [(40, 300), (600, 4000), (0, 4000)])
+def test_probabilities_of_tiny_weights(k, V, dtype):
+    # columns of 2^-1 to 2^-44 of the largest, kept in a short list, a long one, or without any
+    B = 40
+    v = Verify(B, 1, V, [(1.0, k, 1.0, 0.0)] * B, 90, dtype)
+    fall = torch.arange(40, device="cuda").float() * (44 * LN2 / 40)
+    for i, rows in enumerate((v.target, v.draft)):
+        rows[:] = -60.0
+        x = 8.0 - fall - 0.3 * torch.rand(rows.shape[0], 40, generator=gen(91 + i), device="cuda")
+        rows[:, 17:17 + 40 * 5:5] = x.flip(1).to(dtype)  # the lightest first
+    v.tokens[:, 1] = 17 + 5 * torch.arange(B, device="cuda") % 200
+    v.run()
+    # u = 0 draws the first kept column that weighs anything; here it may be any of the lightest
+    tok, prob = sample(v.target, [v.rows[0]] * (2 * B), vec([0.0] * (2 * B)))
+    torch.cuda.synchronize()
+    assert int(v.err.item()) == 0
+    for b in range(B):
+        p, q = (f.probabilities(r[b], 1.0, k) for r in (v.target[0::2], v.draft))
+        x = int(v.tokens[b, 1])
+        want = min(1.0, float(p[x]) / float(q[x]))
+        assert abs(float(v.chance[b]) - want) <= (2.0 ** -24 + 2.0 ** -28) * want, b
+        c = tok[2 * b]
+        assert 0 <= c <= 17 + 200 and float(p[c]) > 0 and abs(prob[2 * b] - float(p[c])) <= (2.0 ** -24 + 2.0 ** -29) * float(p[c])
