@@ -4,6 +4,7 @@ import pytest
 import torch
 
 import attn_util as au
+import speculative_decoding_pe_gb300 as pe
 from speculative_decoding_pe_gb300 import _native
 from test_gpu_bounded_cache import Evict, Weigh
 
@@ -66,3 +67,65 @@ def test_evict_refuses_outputs_over_its_sizes():
     _native.kv_evict(e.cache, e.mass, e.table, e.dst, both[:2], both[4:], e.kept, both[2:4], e.err)
     _native.kv_evict(e.cache, e.mass, e.table, e.dst, both[:2], both[4:], e.kept, out, e.err)
     assert int(e.err.item()) == 0 and both.tolist() == [40, 40, 20, 20, 20, 20] and out.tolist() == [20, 20]
+
+
+@pytest.mark.parametrize("Hq, Hkv, D, bs", [(16, 2, 64, 16), (8, 4, 128, 32)])
+def test_a_draft_batch_after_an_eviction(Hq, Hkv, D, bs):
+    # Verified rows (some rejected) and MASK rows of a step, appended behind what an eviction left: rotation by the true
+    # positions, slots, limits and weights by the cached ones.
+    g = torch.Generator(device="cuda")
+    g.manual_seed(25)
+    B, n, keep, Kp, K, width = 4, 300, [96, 97, 111, 300], 7, 5, 24
+    m, G = Kp + K, Hq // Hkv
+    accepted = [0, 3, 7, 5]
+    cache = au.random_cache(B * width, Hkv, bs, D, g)
+    mass = torch.rand(B * width, Hkv, bs, generator=g, device="cuda")
+    table = torch.randperm(B * width, generator=g, device="cuda").to(torch.int32).view(B, width)
+    err, i32 = pe.new_error_word(), torch.int32
+    dev = lambda x, dt=i32: torch.tensor(x, dtype=dt, device="cuda")  # noqa: E731
+    kept, size = torch.full((B, Hkv, 300), -1, dtype=i32, device="cuda"), torch.empty(B, dtype=i32, device="cuda")
+    before = [au.held(cache, D, table[b].long()[torch.arange(n, device="cuda") // bs] * bs + torch.arange(n, device="cuda") % bs)
+              for b in range(B)]
+    old = [mass[table[b].long()[torch.arange(n, device="cuda") // bs], :, torch.arange(n, device="cuda") % bs] for b in range(B)]
+    pe.kv_evict(cache, mass, table, table, dev([n] * B), dev(keep), kept, size, err, sinks=2, recent=20)
+    assert size.tolist() == keep
+    step = [[(k, k <= a) for k in range(Kp + 1)] + [(a + i, True) for i in range(1, K)] for a in accepted]
+    rel, live = dev([[p for p, _ in r] for r in step]), dev([[k for _, k in r] for r in step], torch.bool)
+    cached = size[:, None] + rel
+    slots = torch.where(live, table.gather(1, (cached // bs).long()).long() * bs + cached % bs, -1)
+    rope = pe.rope_table(n + 32, D)
+    q, k, v = (torch.randn(B * m, h, D, generator=g, device="cuda").to(torch.bfloat16) for h in (Hq, Hkv, Hkv))
+    qr, out = torch.empty_like(q), torch.empty_like(q)
+    k[~live.flatten()] = float("nan")
+    rejected = (~live).flatten().to(torch.uint8)
+    pe.kv_append(q, k, v, (n + rel).flatten(), slots.flatten(), rope, cache, qr, err)
+    qr[~live.flatten()] = float("nan")
+    pe.attn_cached(qr, cache, table, None, cached.flatten(), rejected, out, pe.new_attn_workspace(D), err)
+    ws = pe.new_weigh_workspace(B * m, Hq, width, bs)
+    pe.kv_weigh(qr, cache, table, None, cached.flatten(), rejected, mass, mass, ws, err, fresh=size)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    key = au.quantised(au.to_bf16(au.rotated(k, rope, (n + rel).flatten(), False)[0]))
+    for b in range(B):
+        L = keep[b] + accepted[b] + K
+        j = torch.arange(L, device="cuda")
+        hk, hv = au.held(cache, D, table[b].long()[j // bs] * bs + j % bs)
+        rows = slice(b * m, (b + 1) * m)
+        limit = torch.where(live[b], cached[b] + 1, 0).long()
+        for h in range(Hkv):  # what was kept, and the step's rows behind it
+            at = kept[b, h, :keep[b]].long()
+            assert torch.equal(hk[:keep[b], h], before[b][0][at, h]) and torch.equal(hv[:keep[b], h], before[b][1][at, h])
+            assert torch.equal(hk[cached[b][live[b]].long(), h], key[rows][live[b]][:, h])
+            qq = qr[rows][live[b]][:, h * G:(h + 1) * G].double()
+            hidden = j >= limit[live[b]][:, None, None]
+            s = (torch.einsum("mgd,ld->mgl", qq, hk[:, h]) * D ** -0.5).masked_fill(hidden, -float("inf"))
+            mag = (torch.einsum("mgd,ld->mgl", qq.abs(), hk[:, h].abs()) * D ** -0.5).masked_fill(hidden, 0.0)
+            p = torch.softmax(s, -1)
+            # (as in the weights' own tests)
+            off = (D + 8) * 2.0 ** -24 * (mag + mag.amax(-1, keepdim=True)) + 2.0 ** -20
+            want = p.sum((0, 1))
+            want[:keep[b]] += old[b][at, h].double()
+            got = mass[table[b].long()[j // bs], h, j % bs]
+            au.within(got, want, (p * off).sum((0, 1)) + 2.0 ** -23 * want)
+        w, tol = au.attention(qr[rows].nan_to_num(0.0), hk, hv, limit, D ** -0.5)
+        au.within(out[rows], w, tol)
